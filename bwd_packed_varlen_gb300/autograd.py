@@ -99,6 +99,135 @@ class SBHDAttentionFunction(torch.autograd.Function):
         return dq, dk, dv, None, None, None, None
 
 
+class RotaryFunction(torch.autograd.Function):
+    """``(q', k') = rotary positions of (q, k)``; the backward turns by the negative angle.
+    ``cu_pad`` None: the sequence-major layout ``[S, B, h, d]``, else packed ``[T, h, d]``."""
+
+    @staticmethod
+    def forward(ctx, q, k, inv_freq, cu, cu_pad, start, interleaved, mscale):
+        ctx.save_for_backward(inv_freq, cu, cu_pad, start)
+        ctx.args = (interleaved, mscale)
+        return RotaryFunction._turn(q, k, inv_freq, cu, cu_pad, start, interleaved, mscale, False)
+
+    @staticmethod
+    def _turn(q, k, inv_freq, cu, cu_pad, start, *args):
+        if cu_pad is None:
+            return _b.rope_sbhd(q, k, inv_freq, cu, start, *args)
+        return _b.rope(q, k, inv_freq, cu, cu_pad, start, *args)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        tables = ctx.saved_tensors
+        # e.g. the expanded ones of .sum().backward(): elements of a head must be adjacent,
+        # and sequence-major rows evenly spaced
+        dq, dk = (g if g is None or (g.stride(-1) == 1 and tables[2] is not None) else g.contiguous()
+                  for g in (dq, dk))
+        dq, dk = RotaryFunction._turn(dq, dk, *tables, *ctx.args, True)
+        return (dq, dk) + (None,) * 6
+
+
+class PrefixAttentionFunction(torch.autograd.Function):
+    """``out = attention(q, [k_prefix; k], [v_prefix; v])`` over packed sequences that share
+    the prefix; returns ``(out, lse)``. The backward returns the gradients of all five, the
+    prefix's summed over the sequences."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, kp, vp, cu_q, cu_kv, cu_q_pad, cu_kv_pad, scale, mask, prefix_len):
+        out, lse = _b.prefix_fwd(q, k, v, kp, vp, cu_q, cu_kv, cu_q_pad, cu_kv_pad, scale, mask, prefix_len)
+        ctx.save_for_backward(q, k, v, kp, vp, out, lse, cu_q, cu_kv, cu_q_pad, cu_kv_pad, prefix_len)
+        ctx.args = (scale, mask)
+        ctx.mark_non_differentiable(lse)
+        return out, lse
+
+    @staticmethod
+    def backward(ctx, dout, _dlse):
+        q, k, v, kp, vp, out, lse, cu_q, cu_kv, cu_q_pad, cu_kv_pad, prefix_len = ctx.saved_tensors
+        scale, mask = ctx.args
+        grads = _b.prefix_bwd(q, k, v, kp, vp, out, dout.contiguous(), lse, cu_q, cu_kv, cu_q_pad, cu_kv_pad,
+                              scale, mask, prefix_len)
+        return tuple(grads) + (None,) * 7
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_length=4096,
+                     beta_fast=32.0, beta_slow=1.0, device="cuda"):
+    """Angles per position of ``rot_dim / 2`` pairs, ``base ** (-2c / rot_dim)`` in float64, and
+    the factor on cos and sin: ``(inv_freq, mscale)`` for :func:`rope` and
+    :func:`rotary_positions`. ``scaling`` stretches a model trained on ``original_length``
+    positions to ``factor`` times as many: ``"linear"`` divides every angle by ``factor``;
+    ``"ntk"`` raises the base so that the slowest pair is stretched by ``factor`` and the
+    fastest not at all; ``"yarn"`` divides the pairs that make less than ``beta_slow`` turns
+    over ``original_length``, keeps those that make more than ``beta_fast`` and blends
+    between, with ``mscale = 0.1 ln(factor) + 1``."""
+    rot_dim = int(rot_dim)
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and positive")
+    if not (base > 0 and factor >= 1):
+        raise ValueError("base must be positive and factor at least 1")
+    c = torch.arange(rot_dim // 2, dtype=torch.float64)
+    mscale = 1.0
+    if scaling == "ntk" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    w = float(base) ** (-2.0 * c / rot_dim)
+    if scaling == "linear":
+        w = w / factor
+    elif scaling == "yarn":
+        turns = original_length * w / (2 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        w = w * keep + w / factor * (1.0 - keep)
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}: None, 'linear', 'ntk' or 'yarn'")
+    return w.to(device), mscale
+
+
+def rotary_positions(q, k, inv_freq, cu_seqlens=None, cu_seqlens_padded=None, start_positions=None,
+                     interleaved=False, mscale=1.0, qkv_format="thd"):
+    """Differentiable rotary positions; returns ``(q', k')`` (``k`` may be None). Layouts and
+    real lengths as in :func:`dot_product_attention`; token i of sequence b is at position
+    ``start_positions[b] + i`` (int32 ``[B]``, default 0: the length of what is cached or
+    shared before it)."""
+    shape_q, shape_k = q.shape, None if k is None else k.shape
+    if qkv_format == "thd":
+        if cu_seqlens is None:
+            raise ValueError("thd needs cu_seqlens")
+        pad = cu_seqlens if cu_seqlens_padded is None else cu_seqlens_padded
+    elif qkv_format in ("bshd", "sbhd"):
+        if q.dim() != 4 or (k is not None and k.dim() != 4):
+            raise ValueError(f"{qkv_format} tensors must have four dimensions")
+        if cu_seqlens_padded is not None:
+            raise ValueError(f"{qkv_format} takes no padded cu_seqlens")
+        pad = None
+        S, B = (shape_q[1], shape_q[0]) if qkv_format == "bshd" else shape_q[:2]
+        full = _full_lengths(B, S, q.device)
+        cu_seqlens = full if cu_seqlens is None else cu_seqlens
+        if qkv_format == "bshd":
+            q, pad = q.flatten(0, 1), full
+            k = None if k is None else k.flatten(0, 1)
+    else:
+        raise NotImplementedError(f"qkv_format {qkv_format!r}: 'thd', 'bshd' or 'sbhd'")
+    q, k = RotaryFunction.apply(q, k, inv_freq, cu_seqlens, pad, start_positions, bool(interleaved), float(mscale))
+    return q.view(shape_q), None if k is None else k.view(shape_k)
+
+
+def shared_prefix_attention(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv,
+                            cu_seqlens_q_padded=None, cu_seqlens_kv_padded=None,
+                            attn_mask_type="padding_causal", softmax_scale=None, prefix_len=None,
+                            return_lse=False):
+    """Differentiable attention over packed sequences that all see the same prefix first:
+    ``q [T_q, hq, d]``, ``k, v [T_kv, hkv, d]``, ``k_prefix, v_prefix [P, hkv, d]``; lengths,
+    mask names and the shape of the result as in :func:`dot_product_attention`. The prefix is
+    read once for the batch. ``prefix_len`` (one int32 on the device) gives its real length.
+    For a decoding step pass the caches as ``k, v`` with ``"padding_causal_bottom_right"``."""
+    scale = 1.0 / math.sqrt(q.shape[-1]) if softmax_scale is None else float(softmax_scale)
+    out, lse = PrefixAttentionFunction.apply(
+        q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv,
+        cu_seqlens_q if cu_seqlens_q_padded is None else cu_seqlens_q_padded,
+        cu_seqlens_kv if cu_seqlens_kv_padded is None else cu_seqlens_kv_padded, scale,
+        _mask_name(attn_mask_type), prefix_len)
+    out = out.view(q.shape[0], q.shape[1] * q.shape[2])
+    return (out, lse) if return_lse else out
+
+
 def _full_lengths(B, S, device):
     return torch.arange(0, (B + 1) * S, S, dtype=torch.int32, device=device)
 

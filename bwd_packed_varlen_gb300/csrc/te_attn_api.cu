@@ -20,6 +20,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/te_attn.h"
+#include "api_internal.h"
 #include "common.cuh"
 #include "launch.h"
 
@@ -226,6 +227,37 @@ cudaError_t timed(int kernel, cudaStream_t st, F&& launch) {
 namespace teattn {
 // Lets other entry points of the library report through te_attn_last_error().
 void set_last_error(const std::string& msg) { g_last_error = msg; }
+
+int api_fail(int code, const char* msg) noexcept {
+  try {
+    return fail(code, msg);
+  } catch (...) {  // no memory for the message: the code still reaches the caller
+    return code;
+  }
+}
+
+int api_ok() noexcept { return ok_status(); }
+
+int api_cuda_fail(cudaError_t e, const char* where) noexcept {
+  try {
+    return cuda_fail(e, where);
+  } catch (...) {
+    return TE_ERR_CUDA;
+  }
+}
+
+int api_num_sms() { return num_sms_of_current_device(); }
+
+int api_check_common(int batch, int total_q, int total_kv, int hq, int hkv, int d, float attn_scale,
+                     int mask_type, int dtype, const int32_t* cu_q, const int32_t* cu_kv,
+                     const int32_t* cu_q_pad, const int32_t* cu_kv_pad) {
+  return check_common(batch, total_q, total_kv, hq, hkv, d, attn_scale, mask_type, dtype, cu_q, cu_kv,
+                      cu_q_pad, cu_kv_pad);
+}
+
+cudaError_t api_timed(int kernel, cudaStream_t st, cudaError_t (*launch)(void*), void* ctx) {
+  return timed(kernel, st, [&] { return launch(ctx); });
+}
 }  // namespace teattn
 
 extern "C" {

@@ -267,6 +267,93 @@ int te_attn_fwd_thd_e4m3(const void* q, const void* k, const void* v, void* out,
                          void* stream);
 
 /*
+ * Rotary positions (no counterpart in the pages; attention itself takes q and k as they
+ * are). Each head's first rot = 2 * n_freq elements are n_freq pairs; pair c of token i
+ * of sequence b is turned by the angle a = (start_positions[b] + i) * inv_freq[c]:
+ *   y1 = mscale * (x1 cos a - x2 sin a),  y2 = mscale * (x2 cos a + x1 sin a),
+ * the other d - rot elements are copied. interleaved = 0: pair c is elements (c, c + rot/2);
+ * interleaved = 1: elements (2c, 2c + 1). inverse = 1 turns by -a, which is the backward
+ * pass (dq, dk in place of q, k). Rows that are no token (pad slots, tails, sequences
+ * whose lengths are inconsistent) are written as exact zeros, whatever they hold.
+ *   q [total, hq, d], k [total, hkv, d] 16-bit with any non-negative strides (elements,
+ *   at most 2^31) between tokens and between heads, elements of a head adjacent: slices
+ *   of a fused projection need no copy. q_out [total, hq, d] and k_out [total, hkv, d]
+ *   contiguous; an output may be its own input (same pointer, contiguous) but not
+ *   otherwise overlap an input. hkv = 0: no keys (k and k_out are not read).
+ *   inv_freq: double [n_freq] on the device, finite, radians per position, already scaled
+ *   for long contexts where wanted; angles are reduced exactly (a 64-bit fraction of a
+ *   turn), so far positions lose nothing. start_positions: int32 [batch] or NULL (zeros).
+ * d as for attention, 1 <= n_freq <= d / 2. Fastest when pointers are 16-byte aligned and
+ * strides (and rot / 2, with interleaved = 0, or rot) are multiples of 8 elements.
+ * No workspace; deterministic; capturable. The sbhd form takes row i * batch + b for
+ * token i of sequence b, strides between those rows.
+ */
+int te_attn_rope_thd(const void* q, const void* k, void* q_out, void* k_out,
+                     const double* inv_freq, int n_freq, const int32_t* cu_seqlens,
+                     const int32_t* cu_seqlens_padded, const int32_t* start_positions, int batch,
+                     int total, int hq, int hkv, int d, int64_t q_stride_t, int64_t q_stride_h,
+                     int64_t k_stride_t, int64_t k_stride_h, int interleaved, float mscale,
+                     int inverse, int dtype, void* stream);
+
+int te_attn_rope_sbhd(const void* q, const void* k, void* q_out, void* k_out,
+                      const double* inv_freq, int n_freq, const int32_t* cu_seqlens,
+                      const int32_t* start_positions, int batch, int seq, int hq, int hkv, int d,
+                      int64_t q_stride_t, int64_t q_stride_h, int64_t k_stride_t,
+                      int64_t k_stride_h, int interleaved, float mscale, int inverse, int dtype,
+                      void* stream);
+
+/*
+ * Attention of a packed batch whose sequences share a prefix (no counterpart in the
+ * pages): every real query sees every real key of the prefix, then the keys of its own
+ * sequence that `mask_type` leaves:
+ *   S = attn_scale [Q_b K_prefix^T | Q_b K_b^T + mask],  P = softmax(S),
+ *   O = P [V_prefix; V_b],  LSE as above, over both parts.
+ * The prefix is read once for the whole batch, not once per sequence: the rows of short
+ * sequences (one token each while decoding) are packed together against it, with all
+ * heads of a kv head's group. Long key axes are split over the GPU and joined in fp32.
+ *   k_prefix, v_prefix, dk_prefix, dv_prefix: [prefix_rows, hkv, d], contiguous, q's
+ *   dtype; prefix_rows may be 0. prefix_len: NULL (all rows are real) or one int32 on the
+ *   device, the real rows; the rows behind it may hold any finite values, and get exact
+ *   zeros in dk_prefix/dv_prefix.
+ * q, k, v, cu_seqlens_*, masks, head dims, dtypes, zero rows, alignment, determinism and
+ * errors are te_attn_fwd_thd's; k, v of one decoding step are the sequences' caches in
+ * their padded slots, with TE_MASK_PADDING_CAUSAL_BOTTOM_RIGHT. Masks place queries and
+ * own keys of one sequence against each other; the prefix lies before both. A real query
+ * that sees no key at all gets out = 0, lse = -inf, dq = 0. total_q * hq < 2^31.
+ * An inconsistent prefix_len counts as 0 and raises TE_STATUS_BAD_SEQLENS.
+ * The workspaces' sizes are the *_workspace_size functions'; te_attn_read_status() works
+ * on them.
+ */
+size_t te_attn_prefix_fwd_workspace_size(int batch, int total_q, int total_kv, int prefix_rows,
+                                         int hq, int hkv, int d);
+size_t te_attn_prefix_bwd_workspace_size(int batch, int total_q, int total_kv, int prefix_rows,
+                                         int hq, int hkv, int d);
+
+int te_attn_prefix_fwd_thd(const void* q, const void* k, const void* v, const void* k_prefix,
+                           const void* v_prefix, void* out, float* lse,
+                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                           const int32_t* cu_seqlens_q_padded,
+                           const int32_t* cu_seqlens_kv_padded, const int32_t* prefix_len,
+                           int batch, int total_q, int total_kv, int prefix_rows, int hq, int hkv,
+                           int d, float attn_scale, int mask_type, int dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward pass: dq, dk, dv as te_attn_bwd_thd gives them and dk_prefix, dv_prefix,
+ * summed over all sequences and the group's heads in a fixed order, from out, lse (of
+ * te_attn_prefix_fwd_thd) and dout.
+ */
+int te_attn_prefix_bwd_thd(const void* q, const void* k, const void* v, const void* k_prefix,
+                           const void* v_prefix, const void* out, const void* dout,
+                           const float* lse, void* dq, void* dk, void* dv, void* dk_prefix,
+                           void* dv_prefix, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_kv, const int32_t* cu_seqlens_q_padded,
+                           const int32_t* cu_seqlens_kv_padded, const int32_t* prefix_len,
+                           int batch, int total_q, int total_kv, int prefix_rows, int hq, int hkv,
+                           int d, float attn_scale, int mask_type, int dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then copies the device status word of the last call that
  * used `workspace` into *status (0 = clean, else TE_STATUS_* bits). Returns TE_OK or
  * TE_ERR_CUDA. Intended for tests and debugging; it blocks the host.
@@ -299,7 +386,9 @@ int te_attn_selftest_wait_timeout(void* workspace, size_t workspace_bytes,
  * k = TE_KERNEL_* (arrays of at least TE_NUM_KERNELS entries), and clears the
  * record. Disabled by default; while enabled, each launch costs two event
  * records. Returns TE_OK or TE_ERR_CUDA. The record is process-wide (guarded by a
- * mutex): calls from several threads land in the same totals.
+ * mutex): calls from several threads land in the same totals. Shared-prefix calls count
+ * under the kernels they correspond to (joining split keys under TE_KERNEL_FWD, summing
+ * split queries under TE_KERNEL_DKDV); rotary calls are one launch and are not recorded.
  */
 #define TE_KERNEL_SCHEDULE 0
 #define TE_KERNEL_FWD 1
