@@ -1,6 +1,5 @@
-// Shared-prefix attention, forward and backward, one warp per row.
+// Shared-prefix attention, backward, one warp per row.
 //
-//   S = scale [q Kp^T | q K_b^T + mask],  O = softmax(S) [Vp; V_b],  LSE = log sum exp S
 //   P = exp(S - LSE),  dS = P (dO V^T - rowsum(dO O)),  dQ = scale dS K,
 //   dK = scale dS^T Q and dV = P^T dO, summed over the group's heads and, for the
 //   prefix, over every sequence.
@@ -60,40 +59,6 @@ __device__ __forceinline__ bool query_of_row(const PrefixParams& p, int r, SeqIn
   if (b < 0) return false;
   *s = load_seq(p, b);
   return *i < s->len_q;
-}
-
-template <bool kBF16>
-__global__ void prefix_fwd_rows(PrefixParams p) {
-  const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (w >= static_cast<long long>(p.total_q) * p.hq) return;
-  const int r = static_cast<int>(w / p.hq), h = static_cast<int>(w % p.hq), g = h / p.group;
-  SeqInfo s;
-  int i;
-  float o[kMaxPer] = {};
-  if (!query_of_row(p, r, &s, &i)) {
-    store_row<kBF16>(p.out, w, p.d, o);
-    if ((threadIdx.x & 31) == 0) p.lse[w] = 0.f;
-    return;
-  }
-  float q[kMaxPer], k[kMaxPer], v[kMaxPer];
-  load_row<kBF16>(p.q, w, p.d, q);
-  const int np = prefix_keys(p), n = np + row_keys(s, i, p.causal != 0);
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < n; ++j) {
-    const size_t row = j < np ? j : k_row(p, s, j - np);
-    load_row<kBF16>(j < np ? p.kp : p.k, row * p.hkv + g, p.d, k);
-    load_row<kBF16>(j < np ? p.vp : p.v, row * p.hkv + g, p.d, v);
-    const float x = dot_row(q, k) * p.scale;
-    const float mn = fmaxf(m, x), a = expf(m - mn), e = expf(x - mn);
-    l = l * a + e;
-    m = mn;
-#pragma unroll
-    for (int c = 0; c < kMaxPer; ++c) o[c] = o[c] * a + e * v[c];
-  }
-#pragma unroll
-  for (int c = 0; c < kMaxPer; ++c) o[c] = l > 0.f ? o[c] / l : 0.f;
-  store_row<kBF16>(p.out, w, p.d, o);
-  if ((threadIdx.x & 31) == 0) p.lse[w] = l > 0.f ? m + logf(l) : -INFINITY;
 }
 
 template <bool kBF16>
@@ -185,15 +150,6 @@ __global__ void prefix_status(PrefixParams p) {
 }
 
 static unsigned blocks_for(long long warps) { return static_cast<unsigned>((warps + 3) / 4); }
-
-cudaError_t launch_prefix_fwd(const PrefixParams& p, bool bf16, int num_sms, cudaStream_t st) {
-  const long long rows = static_cast<long long>(p.total_q) * p.hq;
-  prefix_status<<<1, 256, 0, st>>>(p);
-  if (rows == 0) return cudaGetLastError();
-  if (bf16) prefix_fwd_rows<true><<<blocks_for(rows), 128, 0, st>>>(p);
-  else prefix_fwd_rows<false><<<blocks_for(rows), 128, 0, st>>>(p);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_prefix_bwd(const PrefixParams& p, bool bf16, int num_sms, cudaStream_t st) {
   const long long rows = static_cast<long long>(p.total_q) * p.hq;

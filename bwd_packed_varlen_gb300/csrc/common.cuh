@@ -25,6 +25,8 @@ enum HeaderWord : int {
   kHdrNumFPairs = 6, // number of (sequence, 256-row query tile pair) items
   kHdrNextFused = 7, // work counter of the fused backward kernel
   kHdrSelftest = 8,  // words 8..11: results of te_attn_selftest_wait_timeout
+  kHdrPrefixEntries = 12, // shared-prefix forward: (group, chunk) entries
+  kHdrPrefixFirst = 13,   // shared-prefix forward: first prefix group (-1: none, -2: no result)
   kHdrWords = 64     // header size in int32 words (256 bytes, keeps alignment)
 };
 

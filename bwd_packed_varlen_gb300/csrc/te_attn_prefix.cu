@@ -64,6 +64,47 @@ PrefixParams base_params(const void* q, const void* k, const void* v, const void
   return p;
 }
 
+// Forward workspace, 256-byte aligned sections: header, per-sequence records, compact
+// tokens, groups, entries, partial rows (maximum and sum; d fp32 columns). The capacities
+// follow from sum_b Lq_b <= total_q: with T chunks aimed at and row tiles of R packed rows,
+//   groups   <= 2 (total_q G / R + batch + 1)        entries <= T + groups
+//   partial rows of a kv head <= 2 R T + 2 min(total_q G, 128 batch):
+// a group of n key tiles has at most n / len + 1 chunks, sum n / len <= T, rows of short
+// sequences (at most 128 each) are in two groups, and a long group leaves partial rows
+// only with two chunks or more, when n / len + 1 <= 2 n / len.
+struct FwdLayout {
+  size_t seqs, short_tok, groups, entries, part_ml, part_o, total;
+  int parts_target;
+  long long cap_groups, cap_entries, cap_rows;
+};
+
+bool fwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, int hkv, int d, FwdLayout* L) {
+  if (batch < 1 || total_q < 0 || total_kv < 0 || prefix_rows < 0 || hq < 1 || hkv < 1 || hq % hkv != 0 ||
+      d < 8 || d > 256 || d % 8 != 0 || static_cast<long long>(total_q) * hq > INT32_MAX)
+    return false;
+  const long long rows = static_cast<long long>(total_q) * (hq / hkv), rt = prefix_row_tile(d);
+  L->parts_target = (kPartsTarget + hkv - 1) / hkv;
+  L->cap_groups = 2 * (rows / rt + batch + 1);
+  L->cap_entries = L->parts_target + L->cap_groups;
+  const long long few = static_cast<long long>(kShortRows) * batch;
+  L->cap_rows = hkv * (2 * rt * L->parts_target + 2 * (rows < few ? rows : few));
+  if (L->cap_rows > INT32_MAX || L->cap_entries * hkv > INT32_MAX) return false;
+  size_t off = kHdrWords * sizeof(int);
+  auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return at;
+  };
+  L->seqs = take(static_cast<size_t>(batch) * sizeof(int4));
+  L->short_tok = take(static_cast<size_t>(total_q) * sizeof(int));
+  L->groups = take(static_cast<size_t>(L->cap_groups) * 2 * sizeof(int4));
+  L->entries = take(static_cast<size_t>(L->cap_entries) * sizeof(int2));
+  L->part_ml = take(static_cast<size_t>(L->cap_rows) * sizeof(float2));
+  L->part_o = take(static_cast<size_t>(L->cap_rows) * d * sizeof(float));
+  L->total = off;
+  return true;
+}
+
 }  // namespace
 }  // namespace teattn
 
@@ -73,15 +114,14 @@ extern "C" {
 
 size_t te_attn_prefix_fwd_workspace_size(int batch, int total_q, int total_kv, int prefix_rows,
                                          int hq, int hkv, int d) {
-  if (batch < 1 || total_q < 0 || total_kv < 0 || prefix_rows < 0 || hq < 1 || hkv < 1 || hq % hkv != 0 ||
-      d < 8 || d > 256)
-    return 0;
-  return kHdrWords * sizeof(int);
+  FwdLayout L;
+  return fwd_layout(batch, total_q, total_kv, prefix_rows, hq, hkv, d, &L) ? L.total : 0;
 }
 
 size_t te_attn_prefix_bwd_workspace_size(int batch, int total_q, int total_kv, int prefix_rows,
                                          int hq, int hkv, int d) {
-  return te_attn_prefix_fwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d);
+  FwdLayout L;
+  return fwd_layout(batch, total_q, total_kv, prefix_rows, hq, hkv, d, &L) ? kHdrWords * sizeof(int) : 0;
 }
 
 int te_attn_prefix_fwd_thd(const void* q, const void* k, const void* v, const void* k_prefix,
@@ -102,7 +142,10 @@ int te_attn_prefix_fwd_thd(const void* q, const void* k, const void* v, const vo
   if (total_kv > 0 && (!k || !v)) return api_fail(TE_ERR_INVALID_ARG, "k and v must not be NULL");
   if (prefix_rows > 0 && (!k_prefix || !v_prefix))
     return api_fail(TE_ERR_INVALID_ARG, "k_prefix and v_prefix must not be NULL");
-  if (workspace_bytes < te_attn_prefix_fwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d))
+  FwdLayout L;
+  if (!fwd_layout(batch, total_q, total_kv, prefix_rows, hq, hkv, d, &L))
+    return api_fail(TE_ERR_UNSUPPORTED, "problem too large for its work lists");
+  if (workspace_bytes < L.total)
     return api_fail(TE_ERR_WORKSPACE_TOO_SMALL, "workspace smaller than te_attn_prefix_fwd_workspace_size()");
   const int sms = api_num_sms();
   if (sms <= 0) return api_fail(TE_ERR_CUDA, "no CUDA device");
@@ -111,11 +154,29 @@ int te_attn_prefix_fwd_thd(const void* q, const void* k, const void* v, const vo
                                total_kv, prefix_rows, hq, hkv, d, attn_scale, mask_type);
   p.out = out;
   p.lse = lse;
+  char* ws = static_cast<char*>(workspace);
   p.header = static_cast<int*>(workspace);
+  p.seqs = reinterpret_cast<int4*>(ws + L.seqs);
+  p.short_tok = reinterpret_cast<int*>(ws + L.short_tok);
+  p.groups = reinterpret_cast<int4*>(ws + L.groups);
+  p.entries = reinterpret_cast<int2*>(ws + L.entries);
+  p.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
+  p.part_o = reinterpret_cast<float*>(ws + L.part_o);
+  p.parts_target = L.parts_target;
+  p.cap_groups = static_cast<int>(L.cap_groups);
+  p.cap_entries = static_cast<int>(L.cap_entries);
+  p.cap_rows = static_cast<int>(L.cap_rows);
+  const bool bf16 = dtype == TE_DTYPE_BF16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      api_timed(TE_KERNEL_FWD, st, [&] { return launch_prefix_fwd(p, dtype == TE_DTYPE_BF16, sms, st); });
-  return e == cudaSuccess ? api_ok() : api_cuda_fail(e, "shared-prefix forward");
+  cudaError_t e = api_timed(TE_KERNEL_SCHEDULE, st, [&] { return launch_prefix_schedule(p, st); });
+  if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix schedule");
+  if (total_q == 0) return api_ok();
+  if (total_kv > 0 || prefix_rows > 0) {
+    e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_prefix_fwd(p, bf16, sms, st); });
+    if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix forward");
+  }
+  e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_prefix_join(p, bf16, st); });
+  return e == cudaSuccess ? api_ok() : api_cuda_fail(e, "shared-prefix join");
 }
 
 int te_attn_prefix_bwd_thd(const void* q, const void* k, const void* v, const void* k_prefix,
