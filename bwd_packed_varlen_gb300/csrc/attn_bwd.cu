@@ -35,6 +35,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "attn_prefix.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "row_store.cuh"
@@ -102,9 +103,9 @@ struct DkdvShape {
   static_assert(kStages >= 1, "shared memory budget");
 };
 
-template <int kD, bool kBF16>
+template <int kD, bool kBF16, class P = AttnParams>
 __global__ void __launch_bounds__(kBwdThreads, 1)
-    attn_bwd_dkdv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap tmQ,
+    attn_bwd_dkdv_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmDO, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV) {
   using S = DkdvShape<kD>;
@@ -129,8 +130,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   int* status = p.header + kHdrStatus;
   const int per_pair = p.hkv * S::kSplit;
   const int n_pairs = p.header[kHdrNumKPairs];
-  const int n_items = n_pairs * per_pair;
+  // Items of the prefix come first: they are the longest.
+  constexpr bool kPrefix = is_prefix<P>;
+  const int pre_keys = prefix_keys_of(p);
+  int n_pre = 0;
+  if constexpr (kPrefix) n_pre = (pre_keys + kBlockN - 1) / kBlockN * per_pair * p.splits;
+  const int n_items = n_pre + n_pairs * per_pair;
   const bool causal = p.causal != 0;
+  const int sh = pack_shift(p), vgroup = virtual_group(p);
 
   if (tid == 0) {
     mbar_init(&bar_kv_full, 1);
@@ -161,9 +168,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   struct Item {
     SeqInfo s;
     int b, kt, g, split, qt0, nq, steps;
+    bool pre;  // prefix keys; the steps are [t0, t0 + steps) of the sweep over all rows
+    int t0, part;
   };
   auto decode = [&](int item) {
     Item it;
+    it.pre = false;
+    it.t0 = it.part = 0;
+    if constexpr (kPrefix) {
+      if (item < n_pre) {
+        // parts of one key tile and head side by side: they share its K and V
+        it.part = item % p.splits;
+        const int r = item / p.splits;
+        it.g = r % per_pair / S::kSplit;
+        it.split = r % S::kSplit;
+        it.kt = r / per_pair;
+        it.b = -1;
+        it.pre = true;
+        it.s = SeqInfo{0, p.total_q, 0, pre_keys, 0, 0, true};
+        it.qt0 = 0;
+        it.nq = static_cast<int>(p.rows_lin / kBM);
+        const long long all = static_cast<long long>(vgroup) * it.nq;
+        it.t0 = static_cast<int>(all * it.part / p.splits);
+        it.steps = static_cast<int>(all * (it.part + 1) / p.splits) - it.t0;
+        return it;
+      }
+      item -= n_pre;
+    }
     const PairHead ph = item_pair_head_banded(item, n_pairs, per_pair);
     const int2 pr = p.k_pairs[ph.pair];
     it.g = ph.head / S::kSplit;
@@ -171,9 +202,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     it.kt = pr.y;
     it.b = pr.x;
     it.s = load_seq(p, pr.x);
-    it.qt0 = first_query(it.s, it.kt * kBlockN, causal) / kBM;
-    it.nq = (it.s.len_q + kBM - 1) / kBM;
-    it.steps = p.group * (it.nq - it.qt0);
+    it.qt0 = (first_query(it.s, it.kt * kBlockN, causal) << sh) / kBM;
+    it.nq = ((it.s.len_q << sh) + kBM - 1) / kBM;
+    it.steps = vgroup * (it.nq - it.qt0);
     return it;
   };
 
@@ -200,28 +231,47 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         nxt = next_item(p.header + kHdrNextDkdv);  // used at the next hand-over
         if (ii > 0 && !(ok = mbar_wait(&bar_kv_empty, (ii - 1) & 1, status))) break;
         mbar_arrive_expect_tx(&bar_kv_full, 2 * S::kKVBytes);
+        const CUtensorMap *mk = &tmK, *mv = &tmV;
+        if constexpr (kPrefix) {
+          if (I.pre) {
+            mk = &p.tm_kp;
+            mv = &p.tm_vp;
+          }
+        }
         for (int c = 0; c < S::kChunks; ++c) {
-          tma_load_4d(sK + c * 16384, &tmK, &bar_kv_full, c * 64, I.g, I.s.tb, I.s.off_k + I.kt * kBlockN);
-          tma_load_4d(sV + c * 16384, &tmV, &bar_kv_full, c * 64, I.g, I.s.tb, I.s.off_k + I.kt * kBlockN);
+          tma_load_4d(sK + c * 16384, mk, &bar_kv_full, c * 64, I.g, I.s.tb, I.s.off_k + I.kt * kBlockN);
+          tma_load_4d(sV + c * 16384, mv, &bar_kv_full, c * 64, I.g, I.s.tb, I.s.off_k + I.kt * kBlockN);
         }
         const int nqt = I.nq - I.qt0;
         for (int t = 0; t < I.steps; ++t, ++it) {
-          const int h = I.g * p.group + t / nqt;
-          const int qt = I.qt0 + t % nqt;
+          const int h = I.g * vgroup + (I.t0 + t) / nqt;
+          const int qt = I.qt0 + (I.t0 + t) % nqt;
           const int st = it % NS;
           if (it >= NS && !(ok = mbar_wait(&bar_q_empty[st], ((it / NS) - 1) & 1, status))) break;
           mbar_arrive_expect_tx(&bar_q_full[st], 2 * S::kQBytes + 2 * kBM * 4);
           for (int c = 0; c < S::kChunks; ++c) {
-            tma_load_4d(sQ + st * S::kQBytes + c * kBM * 128, &tmQ, &bar_q_full[st], c * 64, h, I.s.tb,
-                        I.s.off_q + qt * kBM);
-            tma_load_4d(sDO + st * S::kQBytes + c * kBM * 128, &tmDO, &bar_q_full[st], c * 64, h, I.s.tb,
-                        I.s.off_q + qt * kBM);
+            tma_load_4d(sQ + st * S::kQBytes + c * kBM * 128, &tmQ, &bar_q_full[st], c * 64, h << sh, I.s.tb,
+                        I.s.off_q + (qt * kBM >> sh));
+            tma_load_4d(sDO + st * S::kQBytes + c * kBM * 128, &tmDO, &bar_q_full[st], c * 64, h << sh, I.s.tb,
+                        I.s.off_q + (qt * kBM >> sh));
           }
-          size_t ti = tiled_index(p, I.b, qt * kBM, h);
+          const float *lse_src = p.lse_t, *delta_src = p.delta_t;
+          size_t ti, ti_cap = static_cast<size_t>(p.pair_cap_q) * virtual_heads(p) * kBlockM;
+          bool lin = false;
+          if constexpr (kPrefix) {
+            if (I.pre) {
+              lin = true;
+              lse_src = p.lse_lin;
+              delta_src = p.delta_lin;
+              ti = static_cast<size_t>(h) * p.rows_lin + static_cast<size_t>(qt) * kBM;
+              ti_cap = static_cast<size_t>(p.vheads) * p.rows_lin;
+            }
+          }
+          if (!lin) ti = packed_index(p, I.b, qt * kBM, h);
           // a bad offset still completes the barrier's byte count, from row 0
-          if (!bounds_ok(ti + kBM <= static_cast<size_t>(p.pair_cap_q) * p.hq * kBlockM, status)) ti = 0;
-          bulk_load(sLse + st * kBM, p.lse_t + ti, kBM * 4, &bar_q_full[st]);
-          bulk_load(sDelta + st * kBM, p.delta_t + ti, kBM * 4, &bar_q_full[st]);
+          if (!bounds_ok(ti + kBM <= ti_cap, status)) ti = 0;
+          bulk_load(sLse + st * kBM, lse_src + ti, kBM * 4, &bar_q_full[st]);
+          bulk_load(sDelta + st * kBM, delta_src + ti, kBM * 4, &bar_q_full[st]);
         }
       }
     }
@@ -329,17 +379,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // tensor row of key token 0: the loop carries one value for the epilogue
       const int kv_row0 = I.s.off_k * p.rs + I.s.tb;
       for (int t = 0; t < I.steps; ++t, ++it) {
-        const int qt = I.qt0 + t % nqt;
+        const int qt = I.qt0 + (I.t0 + t) % nqt;
         const int st = it % NS;
         ok = __all_sync(0xffffffffu, mbar_wait(&bar_q_full[st], (it / NS) & 1, status));
         if (!ok) break;
         // query columns i of this warp with a nonzero P^T for this key row: [lo, hi)
         const int q_base = qt * kBM + col0;
-        const int hi = kv_valid ? min(kG, I.s.len_q - q_base) : 0;
-        const int lo = causal ? max(0, kv_row - I.s.diag - q_base) : 0;
+        int hi = kv_valid ? min(kG, (I.s.len_q << sh) - q_base) : 0;
+        int lo = causal ? max(0, (kv_row - I.s.diag) * (1 << sh) - q_base) : 0;
+        uint32_t tokens = 0xffffffffu;  // columns that are tokens (prefix items: among all rows)
+        if constexpr (kPrefix) {
+          if (I.pre) {
+            lo = 0;
+            hi = kv_valid ? kG : 0;
+            tokens = __ballot_sync(0xffffffffu, lane >= kG || sLse[st * kBM + col0 + lane % kG] != -INFINITY);
+          }
+        }
         // Warp-uniform: only tiles on the causal diagonal or a length boundary pay
         // for per-element masking.
-        const bool full = __all_sync(0xffffffffu, lo == 0 && hi >= kG);
+        const bool full = __all_sync(0xffffffffu, lo == 0 && hi >= kG && (!kPrefix || tokens == 0xffffffffu));
+        auto keep = [&](int i) {
+          if constexpr (kPrefix) return i >= lo && i < hi && ((tokens >> i) & 1u);
+          else return i >= lo && i < hi;
+        };
         const float4* lse4 = reinterpret_cast<const float4*>(sLse + st * kBM + col0);
         const float4* dlt4 = reinterpret_cast<const float4*>(sDelta + st * kBM + col0);
         // ---- phase A: P^T = exp2(S^T * scale * log2e - lse2), masked entries 0
@@ -376,7 +438,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               for (int e = 0; e < 4; ++e) {
                 const int i = 4 * k + e;
                 const float x = ex2b(fmaf(__uint_as_float(sv[i]), sl2, l[e]));
-                pv[i] = (i >= lo && i < hi) ? x : 0.f;
+                pv[i] = keep(i) ? x : 0.f;
               }
             }
           }
@@ -418,7 +480,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
           if (!full) {
 #pragma unroll
-            for (int i = 0; i < kG; ++i) r[i] = (i >= lo && i < hi) ? r[i] : 0.f;
+            for (int i = 0; i < kG; ++i) r[i] = keep(i) ? r[i] : 0.f;
           }
           uint32_t dk[kG / 2];
 #pragma unroll
@@ -437,13 +499,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const size_t kv_tok = static_cast<size_t>(kv_row0) + static_cast<size_t>(kv_row) * p.rs;
-      const bool store = kv_row < seen_keys(I.s, causal) &&
-                         bounds_ok(kv_tok < static_cast<size_t>(p.total_kv), status);
+      size_t kv_rows = static_cast<size_t>(p.total_kv);
+      void *dk_out = p.dk, *dv_out = p.dv;
+      if constexpr (kPrefix) {
+        if (I.pre) {
+          kv_rows = static_cast<size_t>(p.prefix_rows);
+          dk_out = p.dkp;
+          dv_out = p.dvp;
+        }
+      }
+      const bool store = kv_row < (kPrefix && I.pre ? I.s.len_k : seen_keys(I.s, causal)) &&
+                         bounds_ok(kv_tok < kv_rows, status);
       const size_t kv_off = (kv_tok * p.hkv + I.g) * p.d;
-      const auto dk_rows = make_row_pair(static_cast<elem_t<kBF16>*>(p.dk) + kv_off, store);
-      const auto dv_rows = make_row_pair(static_cast<elem_t<kBF16>*>(p.dv) + kv_off, store);
       const int col_out = I.split * S::kDo;
       constexpr int kOutCols = S::kDo / kColGroups;
+      if constexpr (kPrefix) {
+        if (I.pre && p.splits > 1) {
+          // fp32 partial sums (dK not scaled yet); the reduction rounds once
+          const size_t at = static_cast<size_t>(I.part) * p.prefix_rows * p.hkv * p.d + kv_off;
+#pragma unroll
+          for (int c = 0; c < kOutCols; c += 16) {
+            const int c0 = grp * kOutCols + c;
+            uint32_t a[16], b[16];
+            tmem_ld16(tmem + S::kColDK + lane_base + c0, a);
+            tmem_ld16(tmem + S::kColDV + lane_base + c0, b);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              if (!store || col_out + c0 + e >= p.d) continue;
+              *reinterpret_cast<uint4*>(p.part_dk + at + col_out + c0 + e) = make_uint4(a[e], a[e + 1], a[e + 2], a[e + 3]);
+              *reinterpret_cast<uint4*>(p.part_dv + at + col_out + c0 + e) = make_uint4(b[e], b[e + 1], b[e + 2], b[e + 3]);
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(&bar_acc_empty);
+          continue;
+        }
+      }
+      const auto dk_rows = make_row_pair(static_cast<elem_t<kBF16>*>(dk_out) + kv_off, store);
+      const auto dv_rows = make_row_pair(static_cast<elem_t<kBF16>*>(dv_out) + kv_off, store);
 #pragma unroll
       for (int c = 0; c < kOutCols; c += 16) {
         const int c0 = grp * kOutCols + c;
@@ -503,9 +597,9 @@ struct DqShape {
   static_assert(kKStages >= 2 && kVStages >= 1, "shared memory budget");
 };
 
-template <int kD, bool kBF16>
+template <int kD, bool kBF16, class P = AttnParams>
 __global__ void __launch_bounds__(kBwdThreads, 1)
-    attn_bwd_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap tmQ,
+    attn_bwd_dq_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmDO, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV) {
   using S = DqShape<kD>;
@@ -532,8 +626,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* status = p.header + kHdrStatus;
   const int n_pairs = p.header[kHdrNumQPairs];
-  const int n_items = n_pairs * p.hq;
+  const int n_items = n_pairs * virtual_heads(p);
   const bool causal = p.causal != 0;
+  constexpr bool kPrefix = is_prefix<P>;
+  const int sh = pack_shift(p), vgroup = virtual_group(p);
+  const int pre_keys = prefix_keys_of(p);
+  const int np = (pre_keys + kBN - 1) / kBN;  // prefix key tiles, ahead of the own ones
 
   if (tid == 0) {
     mbar_init(&bar_q_full, 1);
@@ -582,10 +680,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // are left to the zero fill and never reach the ring.
         PairHead ph{0, 0};
         while (item >= 0) {
-          ph = item_pair_head(item, n_pairs, p.group);
+          ph = item_pair_head(item, n_pairs, vgroup);
           pr = p.q_pairs[ph.pair];
           s = load_seq(p, pr.x);
-          n = (visible_keys(s, pr.y, causal) + kBN - 1) / kBN;
+          n = np + (tile_keys(p, s, pr.y, causal) + kBN - 1) / kBN;
           if (n > 0) break;
           nxt = next_item(p.header + kHdrNextDq);
           item = nxt < n_items ? nxt : -1;
@@ -594,28 +692,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           ok = ring_put(ring, ii, -1, status);
           break;
         }
-        const int h = ph.head, g = h / p.group;
+        const int h = ph.head, g = h / vgroup;
         // the step count travels with the item: the MMA thread then needs no global loads
         if (!(ok = ring_put(ring, ii, item, status, n))) break;
         nxt = next_item(p.header + kHdrNextDq);  // used at the next hand-over
         if (ii > 0 && !(ok = mbar_wait(&bar_q_empty, (ii - 1) & 1, status))) break;
         mbar_arrive_expect_tx(&bar_q_full, 2 * S::kQBytes);
         for (int c = 0; c < S::kChunks; ++c) {
-          tma_load_4d(sQ + c * 16384, &tmQ, &bar_q_full, c * 64, h, s.tb, s.off_q + pr.y * kBlockM);
-          tma_load_4d(sDO + c * 16384, &tmDO, &bar_q_full, c * 64, h, s.tb, s.off_q + pr.y * kBlockM);
+          tma_load_4d(sQ + c * 16384, &tmQ, &bar_q_full, c * 64, h << sh, s.tb, s.off_q + (pr.y * kBlockM >> sh));
+          tma_load_4d(sDO + c * 16384, &tmDO, &bar_q_full, c * 64, h << sh, s.tb, s.off_q + (pr.y * kBlockM >> sh));
         }
         for (int j = 0; j < n; ++j, ++it) {
           const int sk = it % KS, sv = it % VS;
+          const CUtensorMap *mk = &tmK, *mv = &tmV;
+          int key = s.off_k + (j - np) * kBN;
+          if constexpr (kPrefix) {
+            if (j < np) {
+              mk = &p.tm_kp;
+              mv = &p.tm_vp;
+              key = j * kBN;
+            }
+          }
           if (it >= KS && !(ok = mbar_wait(&bar_k_empty[sk], ((it / KS) - 1) & 1, status))) break;
           mbar_arrive_expect_tx(&bar_k_full[sk], S::kKVBytes);
           for (int c = 0; c < S::kChunks; ++c)
-            tma_load_4d(sK + sk * S::kKVBytes + c * kBN * 128, &tmK, &bar_k_full[sk], c * 64, g, s.tb,
-                        s.off_k + j * kBN);
+            tma_load_4d(sK + sk * S::kKVBytes + c * kBN * 128, mk, &bar_k_full[sk], c * 64, g, s.tb, key);
           if (it >= VS && !(ok = mbar_wait(&bar_v_empty[sv], ((it / VS) - 1) & 1, status))) break;
           mbar_arrive_expect_tx(&bar_v_full[sv], S::kKVBytes);
           for (int c = 0; c < S::kChunks; ++c)
-            tma_load_4d(sV + sv * S::kKVBytes + c * kBN * 128, &tmV, &bar_v_full[sv], c * 64, g, s.tb,
-                        s.off_k + j * kBN);
+            tma_load_4d(sV + sv * S::kKVBytes + c * kBN * 128, mv, &bar_v_full[sv], c * 64, g, s.tb, key);
         }
       }
     }
@@ -715,23 +820,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bool row_valid;
       size_t gi;
       float nlse2, ndlt;  // -lse * log2(e) and -D of this row
+      int pre;  // prefix keys the row sees
     };
     auto decode = [&](int item) {
-      RowItem r{item, 0, 0, false, 0, 0.f, 0.f};
+      RowItem r{item, 0, 0, false, 0, 0.f, 0.f, 0};
       if (item < 0) return r;
-      const PairHead ph = item_pair_head(item, n_pairs, p.group);
+      const PairHead ph = item_pair_head(item, n_pairs, vgroup);
       const int2 pr = p.q_pairs[ph.pair];
       const int h = ph.head;
       const SeqInfo s = load_seq(p, pr.x);
-      r.n = (visible_keys(s, pr.y, causal) + kBN - 1) / kBN;
+      r.n = np + (tile_keys(p, s, pr.y, causal) + kBN - 1) / kBN;
       const int row = pr.y * kBlockM + quarter * 32 + lane;
+      const int tok = row >> sh;
       // rows that see no key (before a lower-right triangle) are the zero fill's
-      r.lim = row < s.len_q ? row_keys(s, row, causal) : 0;
-      r.gi = q_row(p, s, row) * p.hq + h;
-      const size_t ti = tiled_index(p, pr.x, row, h);
-      r.row_valid = r.lim > 0 &&
+      r.lim = tok < s.len_q ? row_keys(s, tok, causal) : 0;
+      r.pre = tok < s.len_q ? pre_keys : 0;
+      r.gi = q_row(p, s, tok) * p.hq + (h << sh) + (row & ((1 << sh) - 1));
+      const size_t ti = packed_index(p, pr.x, row, h);
+      r.row_valid = r.lim + r.pre > 0 &&
                     bounds_ok(r.gi < static_cast<size_t>(p.total_q) * p.hq &&
-                                  ti < static_cast<size_t>(p.pair_cap_q) * p.hq * kBlockM,
+                                  ti < static_cast<size_t>(p.pair_cap_q) * virtual_heads(p) * kBlockM,
                               status);
       r.nlse2 = r.row_valid ? p.lse_t[ti] : 0.f;
       r.ndlt = r.row_valid ? p.delta_t[ti] : 0.f;
@@ -744,7 +852,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int n = cur.n, lim = cur.lim;
       const float nlse2 = cur.nlse2, ndlt = cur.ndlt;
       for (int j = 0; j < n; ++j, ++it) {
-        const int nvalid = lim - (j * kBN + col0);
+        int nvalid = lim - ((j - np) * kBN + col0);
+        if constexpr (kPrefix)
+          if (j < np) nvalid = cur.pre - (j * kBN + col0);
         // ---- phase A: P = exp2(S * scale * log2e - nlse2) into registers, then free S
         ok = __all_sync(0xffffffffu, mbar_wait(&bar_s_full, it & 1, status));
         if (!ok) break;
@@ -803,6 +913,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const float2 r = f2_unpack(fmul2(f2_pack(pv[2 * k], pv[2 * k + 1]),
                                              fadd2(f2_pack(__uint_as_float(dv[2 * k]), __uint_as_float(dv[2 * k + 1])), nd2)));
             dd[k] = pack2<kBF16>(r.x, r.y);
+          }
+          if constexpr (kPrefix) {
+            // masked entries are 0 whatever dP came to (pad rows of V may overflow it)
+            if (!__all_sync(0xffffffffu, nvalid >= kG)) {
+#pragma unroll
+              for (int k = 0; k < kG / 2; ++k)
+                dd[k] = 2 * k + 1 < nvalid ? dd[k] : 2 * k < nvalid ? dd[k] & 0xffffu : 0u;
+            }
           }
           const uint32_t ds_col = S::kColDS + (it & 1) * S::kDsCols + grp * (kG / 2);
           if constexpr (kG == 32) tmem_st16(tmem + ds_col + lane_base, dd);
@@ -889,6 +1007,76 @@ static cudaError_t launch_dq_impl(const AttnParams& p, int num_sms, cudaStream_t
   const int grid = static_cast<int>(max_items < num_sms ? (max_items > 0 ? max_items : 1) : num_sms);
   kern<<<grid, kBwdThreads, S::kSmemBytes, st>>>(p, tq, tdo, tk, tv);
   return cudaGetLastError();
+}
+
+// The prefix's maps and the packed ones of q and dout.
+template <bool kBF16>
+static bool prefix_maps(PrefixBwd* p, CUtensorMap* tq, CUtensorMap* tdo, CUtensorMap* tk, CUtensorMap* tv,
+                        int q_rows, int k_rows) {
+  const int pack = 1 << p->pack_shift;
+  // an absent tensor's map is never used: any valid address will do
+  const bool own = p->total_kv > 0, pre = p->prefix_rows > 0;
+  const void* any = own ? p->k : p->kp;
+  return make_tmap_tokens(tq, p->q, p->total_q, 1, p->hq, p->d, kBF16, q_rows, pack) &&
+         make_tmap_tokens(tdo, p->dout, p->total_q, 1, p->hq, p->d, kBF16, q_rows, pack) &&
+         make_tmap_tokens(tk, own ? p->k : any, own ? p->total_kv : 1, 1, p->hkv, p->d, kBF16, k_rows) &&
+         make_tmap_tokens(tv, own ? p->v : any, own ? p->total_kv : 1, 1, p->hkv, p->d, kBF16, k_rows) &&
+         make_tmap_tokens(&p->tm_kp, pre ? p->kp : any, pre ? p->prefix_rows : 1, 1, p->hkv, p->d, kBF16, k_rows) &&
+         make_tmap_tokens(&p->tm_vp, pre ? p->vp : any, pre ? p->prefix_rows : 1, 1, p->hkv, p->d, kBF16, k_rows);
+}
+
+template <int kD, bool kBF16>
+static cudaError_t launch_prefix_dkdv_impl(PrefixBwd p, int num_sms, cudaStream_t st) {
+  using S = DkdvShape<kD>;
+  CUtensorMap tq, tdo, tk, tv;
+  if (!prefix_maps<kBF16>(&p, &tq, &tdo, &tk, &tv, S::kBM, 128)) return cudaErrorInvalidValue;
+  auto kern = attn_bwd_dkdv_kernel<kD, kBF16, PrefixBwd>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const long long max_items =
+      (static_cast<long long>(p.pair_cap_k) + static_cast<long long>(p.prefix_rows / kBlockN + 1) * p.splits) *
+      p.hkv * S::kSplit;
+  kern<<<static_cast<int>(max_items < num_sms ? max_items : num_sms), kBwdThreads, S::kSmemBytes, st>>>(p, tq, tdo, tk,
+                                                                                                  tv);
+  return cudaGetLastError();
+}
+
+template <int kD, bool kBF16>
+static cudaError_t launch_prefix_dq_impl(PrefixBwd p, int num_sms, cudaStream_t st) {
+  using S = DqShape<kD>;
+  CUtensorMap tq, tdo, tk, tv;
+  if (!prefix_maps<kBF16>(&p, &tq, &tdo, &tk, &tv, 128, S::kBN)) return cudaErrorInvalidValue;
+  auto kern = attn_bwd_dq_kernel<kD, kBF16, PrefixBwd>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const long long max_items = static_cast<long long>(p.pair_cap_q) * p.vheads;
+  kern<<<static_cast<int>(max_items < num_sms ? max_items : num_sms), kBwdThreads, S::kSmemBytes, st>>>(p, tq, tdo, tk,
+                                                                                                  tv);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prefix_bwd_dkdv(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st) {
+  const int d = p.d;
+  if (bf16) {
+    if (d <= 64) return launch_prefix_dkdv_impl<64, true>(p, num_sms, st);
+    if (d <= 128) return launch_prefix_dkdv_impl<128, true>(p, num_sms, st);
+    return launch_prefix_dkdv_impl<256, true>(p, num_sms, st);
+  }
+  if (d <= 64) return launch_prefix_dkdv_impl<64, false>(p, num_sms, st);
+  if (d <= 128) return launch_prefix_dkdv_impl<128, false>(p, num_sms, st);
+  return launch_prefix_dkdv_impl<256, false>(p, num_sms, st);
+}
+
+cudaError_t launch_prefix_bwd_dq(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st) {
+  const int d = p.d;
+  if (bf16) {
+    if (d <= 64) return launch_prefix_dq_impl<64, true>(p, num_sms, st);
+    if (d <= 128) return launch_prefix_dq_impl<128, true>(p, num_sms, st);
+    return launch_prefix_dq_impl<256, true>(p, num_sms, st);
+  }
+  if (d <= 64) return launch_prefix_dq_impl<64, false>(p, num_sms, st);
+  if (d <= 128) return launch_prefix_dq_impl<128, false>(p, num_sms, st);
+  return launch_prefix_dq_impl<256, false>(p, num_sms, st);
 }
 
 cudaError_t launch_attn_bwd_dkdv(const AttnParams& p, bool bf16, int num_sms, cudaStream_t st) {

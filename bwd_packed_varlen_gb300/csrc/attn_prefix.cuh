@@ -1,6 +1,10 @@
 // Shared-prefix attention: launch parameters and work lists of its kernels.
 #pragma once
 
+#include <cuda.h>
+
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace teattn {
@@ -77,9 +81,88 @@ __device__ __forceinline__ size_t partial_row(const PrefixParams& p, const Prefi
   return static_cast<size_t>(g.slot) + (static_cast<size_t>(c) * p.hkv + h) * g.rows + r;
 }
 
+// ---------------------------------------------------------------------------
+// Backward: the dQ and dK/dV kernels of the packed problem, with the prefix's keys as
+// further key tiles. `pack` = 2^pack_shift heads of a group (the largest power of two that
+// divides the group, at most 128) go token by token into one row tile: packed row r of a
+// sequence is (token r >> pack_shift, head vh * pack + r % pack) of virtual head vh. A tile
+// then covers 128 / pack tokens, so short sequences waste little of it and the heads of a
+// group share the key tiles' loads; one TMA box still fetches it.
+// The prefix's dK/dV items sweep the rows of the whole tensor, pad rows among them (their
+// lse is taken as infinite, so P is 0); with few key tiles the sweep is split, each part
+// leaving fp32 partial sums that a reduction adds in order.
+// ---------------------------------------------------------------------------
+constexpr int kBwdItemsTarget = 3 * 152;  // prefix items of the dK/dV kernel, about
+
+struct PrefixBwd : PrefixParams {
+  CUtensorMap tm_kp, tm_vp;
+  int pack_shift;
+  int vheads;        // hq >> pack_shift
+  int vgroup;        // group >> pack_shift
+  long long rows_lin;  // total_q << pack_shift, rounded up to a row tile
+  float* lse_lin;    // [vheads][rows_lin]: -lse log2(e); -infinity on rows that are no token
+  float* delta_lin;  // [vheads][rows_lin]: -rowsum(dO O)
+  float* part_dk;    // [splits][prefix_rows][hkv][d] (splits > 1)
+  float* part_dv;
+  int splits;
+};
+
+template <class P>
+constexpr bool is_prefix = std::is_same_v<P, PrefixBwd>;
+
+// Compile-time 0 for problems without a prefix: their kernels stay as they are.
+template <class P>
+__device__ __forceinline__ int pack_shift(const P& p) {
+  if constexpr (is_prefix<P>) return p.pack_shift;
+  else return 0;
+}
+template <class P>
+__device__ __forceinline__ int virtual_heads(const P& p) {
+  if constexpr (is_prefix<P>) return p.vheads;
+  else return p.hq;
+}
+template <class P>
+__device__ __forceinline__ int virtual_group(const P& p) {
+  if constexpr (is_prefix<P>) return p.vgroup;
+  else return p.group;
+}
+// Prefix keys (0 without a prefix).
+template <class P>
+__device__ __forceinline__ int prefix_keys_of(const P& p) {
+  if constexpr (is_prefix<P>) return prefix_keys(p);
+  else return 0;
+}
+// Own keys that the packed row tile t sees.
+template <class P>
+__device__ __forceinline__ int tile_keys(const P& p, const SeqInfo& s, int t, bool causal) {
+  if constexpr (is_prefix<P>) {
+    if (!causal) return s.len_k;
+    const int last = min((t + 1) * kBlockM >> p.pack_shift, s.len_q);
+    return min(s.len_k, max(0, last + s.diag));
+  } else {
+    return visible_keys(s, t, causal);
+  }
+}
+// tiled_index() of packed row r and virtual head vh.
+template <class P>
+__device__ __forceinline__ size_t packed_index(const P& p, int b, int r, int vh) {
+  if constexpr (is_prefix<P>) {
+    const int pair = p.pref_q[b] + r / kBlockM;
+    return (static_cast<size_t>(pair) * p.vheads + vh) * kBlockM + (r % kBlockM);
+  } else {
+    return tiled_index(p, b, r, vh);
+  }
+}
+
+cudaError_t launch_prefix_bwd_schedule(const PrefixBwd& p, int* pref_q, int* pref_k, int* pref_f, cudaStream_t st);
+cudaError_t launch_prefix_bwd_zero_fill(const PrefixBwd& p, int num_sms, cudaStream_t st);
+cudaError_t launch_prefix_delta(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st);
+cudaError_t launch_prefix_bwd_dq(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st);
+cudaError_t launch_prefix_bwd_dkdv(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st);
+cudaError_t launch_prefix_sum(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st);
+
 cudaError_t launch_prefix_schedule(const PrefixParams& p, cudaStream_t st);
 cudaError_t launch_prefix_fwd(const PrefixParams& p, bool bf16, int num_sms, cudaStream_t st);
 cudaError_t launch_prefix_join(const PrefixParams& p, bool bf16, cudaStream_t st);
-cudaError_t launch_prefix_bwd(const PrefixParams& p, bool bf16, int num_sms, cudaStream_t st);
 
 }  // namespace teattn

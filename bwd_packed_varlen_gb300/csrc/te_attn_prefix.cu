@@ -105,6 +105,60 @@ bool fwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, i
   return true;
 }
 
+// Backward workspace, 256-byte aligned sections: header, prefix sums and sorted lists of
+// row and key tiles (as te_attn_bwd_thd's, of packed rows), lse and D of those tiles and of
+// the whole tensor's rows, and with splits > 1 the parts of the prefix's gradients.
+struct BwdLayout {
+  size_t pref_q, pref_k, pref_f, q_pairs, k_pairs, lse_t, delta_t, lse_lin, delta_lin, part_dk, part_dv, total;
+  int pack_shift, splits;
+  long long cap_q, cap_k, rows_lin;
+};
+
+bool bwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, int hkv, int d, BwdLayout* L) {
+  if (batch < 1 || total_q < 0 || total_kv < 0 || prefix_rows < 0 || hq < 1 || hkv < 1 || hq % hkv != 0 ||
+      d < 8 || d > 256 || d % 8 != 0 || static_cast<long long>(total_q) * hq > INT32_MAX)
+    return false;
+  const int group = hq / hkv;
+  int sh = 0;  // a 64-row tile holds whole tokens
+  while (sh < 6 && group % (2 << sh) == 0) ++sh;
+  L->pack_shift = sh;
+  const long long rows = static_cast<long long>(total_q) << sh;
+  L->cap_q = rows / kBlockM + batch + 1;
+  L->cap_k = total_kv / kBlockN + static_cast<long long>(batch) + 1;
+  L->rows_lin = (rows + kBlockM - 1) / kBlockM * kBlockM;
+  const int halves = d > 128 ? 2 : 1;
+  const long long steps = (group >> sh) * (L->rows_lin / (d > 128 ? 64 : 128));
+  const long long items = (static_cast<long long>(prefix_rows) + kBlockN - 1) / kBlockN * hkv * halves;
+  // about three items per SM, and 16 steps of a sweep at least to pay for storing its sums
+  long long want = items > 0 ? (kBwdItemsTarget + items - 1) / items : 1;
+  const long long most = steps / 16 > 1 ? steps / 16 : 1;
+  L->splits = static_cast<int>(want < most ? want : most);
+  if (steps / L->splits >= (1 << 24) - 1 || L->cap_q * hq > INT32_MAX || L->cap_k * hkv * halves > INT32_MAX) return false;
+  size_t off = kHdrWords * sizeof(int);
+  auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t sums = (static_cast<size_t>(batch) + 1) * sizeof(int);
+  L->pref_q = take(sums);
+  L->pref_k = take(sums);
+  L->pref_f = take(sums);
+  L->q_pairs = take(static_cast<size_t>(L->cap_q) * sizeof(int2));
+  L->k_pairs = take(static_cast<size_t>(L->cap_k) * sizeof(int2));
+  const size_t tiled = static_cast<size_t>(L->cap_q) * (hq >> sh) * kBlockM * sizeof(float);
+  L->lse_t = take(tiled);
+  L->delta_t = take(tiled);
+  const size_t lin = static_cast<size_t>(L->rows_lin) * (hq >> sh) * sizeof(float);
+  L->lse_lin = take(lin);
+  L->delta_lin = take(lin);
+  const size_t part = L->splits > 1 ? static_cast<size_t>(L->splits) * prefix_rows * hkv * d * sizeof(float) : 0;
+  L->part_dk = take(part);
+  L->part_dv = take(part);
+  L->total = off;
+  return true;
+}
+
 }  // namespace
 }  // namespace teattn
 
@@ -120,8 +174,8 @@ size_t te_attn_prefix_fwd_workspace_size(int batch, int total_q, int total_kv, i
 
 size_t te_attn_prefix_bwd_workspace_size(int batch, int total_q, int total_kv, int prefix_rows,
                                          int hq, int hkv, int d) {
-  FwdLayout L;
-  return fwd_layout(batch, total_q, total_kv, prefix_rows, hq, hkv, d, &L) ? kHdrWords * sizeof(int) : 0;
+  BwdLayout L;
+  return bwd_layout(batch, total_q, total_kv, prefix_rows, hq, hkv, d, &L) ? L.total : 0;
 }
 
 int te_attn_prefix_fwd_thd(const void* q, const void* k, const void* v, const void* k_prefix,
@@ -199,13 +253,17 @@ int te_attn_prefix_bwd_thd(const void* q, const void* k, const void* v, const vo
     return api_fail(TE_ERR_INVALID_ARG, "k, v, dk and dv must not be NULL");
   if (prefix_rows > 0 && (!k_prefix || !v_prefix || !dk_prefix || !dv_prefix))
     return api_fail(TE_ERR_INVALID_ARG, "k_prefix, v_prefix, dk_prefix and dv_prefix must not be NULL");
-  if (workspace_bytes < te_attn_prefix_bwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d))
+  BwdLayout L;
+  if (!bwd_layout(batch, total_q, total_kv, prefix_rows, hq, hkv, d, &L))
+    return api_fail(TE_ERR_UNSUPPORTED, "problem too large for its work lists");
+  if (workspace_bytes < L.total)
     return api_fail(TE_ERR_WORKSPACE_TOO_SMALL, "workspace smaller than te_attn_prefix_bwd_workspace_size()");
   const int sms = api_num_sms();
   if (sms <= 0) return api_fail(TE_ERR_CUDA, "no CUDA device");
-  PrefixParams p = base_params(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv,
-                               cu_seqlens_q_padded, cu_seqlens_kv_padded, prefix_len, batch, total_q,
-                               total_kv, prefix_rows, hq, hkv, d, attn_scale, mask_type);
+  PrefixBwd p{};
+  static_cast<PrefixParams&>(p) =
+      base_params(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded,
+                  prefix_len, batch, total_q, total_kv, prefix_rows, hq, hkv, d, attn_scale, mask_type);
   p.out_in = out;
   p.dout = dout;
   p.lse_in = lse;
@@ -214,11 +272,48 @@ int te_attn_prefix_bwd_thd(const void* q, const void* k, const void* v, const vo
   p.dv = dv;
   p.dkp = dk_prefix;
   p.dvp = dv_prefix;
+  char* ws = static_cast<char*>(workspace);
   p.header = static_cast<int*>(workspace);
+  int* pref_q = reinterpret_cast<int*>(ws + L.pref_q);
+  int* pref_k = reinterpret_cast<int*>(ws + L.pref_k);
+  int* pref_f = reinterpret_cast<int*>(ws + L.pref_f);
+  p.pref_q = pref_q;
+  p.q_pairs = reinterpret_cast<int2*>(ws + L.q_pairs);
+  p.k_pairs = reinterpret_cast<int2*>(ws + L.k_pairs);
+  p.pair_cap_q = static_cast<int>(L.cap_q);
+  p.pair_cap_k = static_cast<int>(L.cap_k);
+  p.pair_cap_f = INT32_MAX;  // that list is not built
+  p.sched_lists = kListQ | kListK;
+  p.lse_t = reinterpret_cast<float*>(ws + L.lse_t);
+  p.delta_t = reinterpret_cast<float*>(ws + L.delta_t);
+  p.lse_lin = reinterpret_cast<float*>(ws + L.lse_lin);
+  p.delta_lin = reinterpret_cast<float*>(ws + L.delta_lin);
+  p.part_dk = reinterpret_cast<float*>(ws + L.part_dk);
+  p.part_dv = reinterpret_cast<float*>(ws + L.part_dv);
+  p.pack_shift = L.pack_shift;
+  p.vheads = hq >> L.pack_shift;
+  p.vgroup = p.group >> L.pack_shift;
+  p.rows_lin = L.rows_lin;
+  p.splits = L.splits;
+  const bool bf16 = dtype == TE_DTYPE_BF16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      api_timed(TE_KERNEL_DKDV, st, [&] { return launch_prefix_bwd(p, dtype == TE_DTYPE_BF16, sms, st); });
-  return e == cudaSuccess ? api_ok() : api_cuda_fail(e, "shared-prefix backward");
+  cudaError_t e = api_timed(TE_KERNEL_SCHEDULE, st, [&] { return launch_prefix_bwd_schedule(p, pref_q, pref_k, pref_f, st); });
+  if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix schedule");
+  e = api_timed(TE_KERNEL_ZERO_FILL, st, [&] { return launch_prefix_bwd_zero_fill(p, sms, st); });
+  if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix zero fill");
+  if (total_q > 0 && (total_kv > 0 || prefix_rows > 0)) {
+    e = api_timed(TE_KERNEL_DELTA, st, [&] { return launch_prefix_delta(p, bf16, sms, st); });
+    if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix delta");
+    e = api_timed(TE_KERNEL_DQ, st, [&] { return launch_prefix_bwd_dq(p, bf16, sms, st); });
+    if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix dQ");
+    e = api_timed(TE_KERNEL_DKDV, st, [&] { return launch_prefix_bwd_dkdv(p, bf16, sms, st); });
+    if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix dK/dV");
+  }
+  if (prefix_rows > 0) {
+    e = api_timed(TE_KERNEL_DKDV, st, [&] { return launch_prefix_sum(p, bf16, sms, st); });
+    if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix gradient sum");
+  }
+  return api_ok();
 }
 
 }  // extern "C"
