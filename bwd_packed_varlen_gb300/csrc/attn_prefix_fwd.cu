@@ -9,7 +9,13 @@
 // them. Roles as in the two-tile forward:
 //   warps 0-3   softmax of row tile A (one thread per row / TMEM lane),
 //   warps 4-7   softmax of row tile B (head_dim <= 128 only),
-//   then        one producer warp (gathers the Q rows, TMA for K and V) and one MMA warp.
+//   then        an item warp (decodes items and gathers their Q rows, an item ahead), a
+//               K/V warp (TMA) and an MMA warp.
+// An item of one row tile that leaves partial results is taken in turns: tile j of its keys
+// goes to softmax group j % 2, each with its own O, so the chain S -> P -> O of one tile
+// overlaps the other's (a decoding step's rows fill a few lanes only; the chain's latency,
+// not its work, is what counts). Its Q rows use one half of the Q buffer, and the next
+// such item's the other.
 // S = Q K^T into TMEM, P = exp2(S scale log2e - m) over it as 16-bit values, O += P V in
 // TMEM. The offset m is raised only when a row's maximum exceeds it by more than 2^8.
 // P is rounded to 16 bits for the tensor cores (relative to the row's largest value, half a
@@ -34,202 +40,249 @@
 namespace teattn {
 
 // ---------------------------------------------------------------------------
-// Scheduler: one block; from the lengths to groups, chunks and partial rows. It is a few
-// passes over the sequences with block-wide scans; the result depends on lengths only.
+// Scheduler: one block; from the lengths to entries and partial rows, with a thread per
+// sequence and block-wide scans. It is on every call's critical path and latency-bound, so
+// each phase loads what it needs at once and costs two barriers. The result depends on the
+// lengths only.
 // ---------------------------------------------------------------------------
-constexpr int kPrefixSchedThreads = 512;
+constexpr int kPrefixSchedThreads = 1024;
 
-// Exclusive scan of two counters at once over the block; totals in *tx, *ty.
-__device__ __forceinline__ int2 block_scan2(int x, int y, unsigned long long* warp_sums, int* tx, int* ty) {
+struct Scan3 {
+  int x, y, z;     // exclusive sums before this thread
+  int tx, ty, tz;  // totals
+};
+
+// Exclusive scan of three counters over the block. `buf`: 3 x 32 ints.
+__device__ __forceinline__ Scan3 block_scan3(int x, int y, int z, int (*buf)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const unsigned long long own = static_cast<unsigned long long>(static_cast<unsigned>(x)) |
-                                 (static_cast<unsigned long long>(static_cast<unsigned>(y)) << 32);
-  unsigned long long v = own;
+  int ix = x, iy = y, iz = z;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+    const int ux = __shfl_up_sync(0xffffffffu, ix, o), uy = __shfl_up_sync(0xffffffffu, iy, o);
+    const int uz = __shfl_up_sync(0xffffffffu, iz, o);
+    if (lane >= o) {
+      ix += ux;
+      iy += uy;
+      iz += uz;
+    }
   }
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  unsigned long long before = 0, total = 0;
-  for (int w = 0; w < nw; ++w) {
-    const unsigned long long s = warp_sums[w];
-    if (w < warp) before += s;
-    total += s;
+  if (lane == 31) {
+    buf[0][warp] = ix;
+    buf[1][warp] = iy;
+    buf[2][warp] = iz;
   }
   __syncthreads();
-  v += before - own;
-  *tx = static_cast<int>(total & 0xffffffffu);
-  *ty = static_cast<int>(total >> 32);
-  return make_int2(static_cast<int>(v & 0xffffffffu), static_cast<int>(v >> 32));
+  // every warp sums the warps' totals itself: lane w holds warp w's
+  int wx = lane < nw ? buf[0][lane] : 0, wy = lane < nw ? buf[1][lane] : 0, wz = lane < nw ? buf[2][lane] : 0;
+  __syncthreads();
+  const int bx = lane < warp ? wx : 0, by = lane < warp ? wy : 0, bz = lane < warp ? wz : 0;
+  Scan3 r;
+  r.tx = __reduce_add_sync(0xffffffffu, wx);
+  r.ty = __reduce_add_sync(0xffffffffu, wy);
+  r.tz = __reduce_add_sync(0xffffffffu, wz);
+  r.x = __reduce_add_sync(0xffffffffu, bx) + ix - x;
+  r.y = __reduce_add_sync(0xffffffffu, by) + iy - y;
+  r.z = __reduce_add_sync(0xffffffffu, bz) + iz - z;
+  return r;
 }
 
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
-// Own key tiles that the rows [row0, row0 + rows) of sequence s see.
-__device__ __forceinline__ int own_tiles(const PrefixParams& p, const SeqInfo& s, int row0, int rows, int bn) {
-  const int last = (row0 + rows - 1) / p.group;
-  return div_up(row_keys(s, last, p.causal != 0), bn);
+// Keys that token i of a sequence sees.
+__device__ __forceinline__ int keys_seen(int causal, int len_k, int diag, int i) {
+  return causal ? min(len_k, max(0, i + 1 + diag)) : len_k;
+}
+// Own key tiles that the packed rows [row0, row0 + rows) see.
+__device__ __forceinline__ int own_tiles(const PrefixParams& p, int len_k, int diag, int row0, int rows, int bn) {
+  return div_up(keys_seen(p.causal, len_k, diag, (row0 + rows - 1) / p.group), bn);
 }
 
 __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(const __grid_constant__ PrefixParams p) {
-  __shared__ unsigned long long warp_sums[32];
+  __shared__ int buf[3][32];
   __shared__ int bad;
   __shared__ unsigned long long work, tokens;
-  const int rt = prefix_row_tile(p.d), bn = prefix_key_tile(p.d), tid = threadIdx.x;
-  const int np_keys = prefix_keys(p), np = div_up(np_keys, bn);
+  const int rt = prefix_row_tile(p.d), bn = prefix_key_tile(p.d), tid = threadIdx.x, lane = tid & 31;
+  const int most_ways = rt / 128;
   if (tid == 0) {
     bad = p.prefix_len && (*p.prefix_len < 0 || *p.prefix_len > p.prefix_rows) ? 1 : 0;
     work = tokens = 0;
   }
+  const int np_keys = prefix_keys(p), np = div_up(np_keys, bn);
   __syncthreads();
-  // sequences: compact tokens, own groups, long groups; an upper bound of the key tiles
-  int n_tok = 0, n_long = 0;
+  // sequences: compact tokens, long row tiles; an upper bound of the key tiles. With at
+  // most a thread per sequence, `s` stays for the later phases.
+  SeqInfo s{};
+  int n_tok = 0, n_long = 0, first_tok = 0, first_long = 0;
   for (int base = 0; base < p.batch; base += blockDim.x) {
     const int b = base + tid;
     int tok = 0, nl = 0;
+    unsigned long long w = 0, q = 0;
+    s = SeqInfo{};
     if (b < p.batch) {
-      const SeqInfo s = load_seq(p, b);
+      s = load_seq(p, b);
       if (!s.ok) bad = 1;
       const int tiles = div_up(s.len_k, bn);
       const long long rows = static_cast<long long>(s.len_q) * p.group;
-      atomicAdd(&tokens, static_cast<unsigned long long>(s.len_q));
+      q = s.len_q;
       if (rows > kShortRows) {
         nl = static_cast<int>((rows + rt - 1) / rt);
-        atomicAdd(&work, static_cast<unsigned long long>(nl) * (np + tiles));
+        w = static_cast<unsigned long long>(nl) * (np + tiles);
       } else if (rows > 0) {
         tok = s.len_q;
-        atomicAdd(&work, static_cast<unsigned long long>(tiles));
+        w = tiles;
       }
     }
-    int t0, t1;
-    const int2 at = block_scan2(tok, nl, warp_sums, &t0, &t1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      w += __shfl_xor_sync(0xffffffffu, w, o);
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+    }
+    if (lane == 0) {
+      atomicAdd(&work, w);
+      atomicAdd(&tokens, q);
+    }
+    const Scan3 at = block_scan3(tok, nl, 0, buf);
+    first_tok = tok > 0 ? n_tok + at.x : -1;
+    first_long = n_long + at.y;
     if (b < p.batch) {
-      p.seqs[b] = make_int4(tok > 0 ? n_tok + at.x : -1, -1, nl > 0 ? n_long + at.y : -1, n_long + at.y);
-      if (tok > 0) {
-        const int row = p.cu_q_pad[b];
-        for (int i = 0; i < tok; ++i)
-          if (n_tok + at.x + i < p.total_q) p.short_tok[n_tok + at.x + i] = row + i;
-      }
+      p.seqs[b] = make_int4(first_tok, -1, 0, first_long);
+      for (int i = 0; i < tok; ++i)
+        if (first_tok + i < p.total_q) p.short_tok[first_tok + i] = s.off_q + i;
     }
-    n_tok += t0;
-    n_long += t1;
+    n_tok += at.tx;
+    n_long += at.ty;
   }
-  __syncthreads();
+  // (the scans' barriers order the sums and the records above before what follows)
   if (tokens > static_cast<unsigned long long>(p.total_q)) {
     // sequences overlap: more tokens than rows, for which the lists have no room
     if (tid == 0) {
       p.header[kHdrStatus] = kStatusBadSeqlens;
       p.header[kHdrPrefixEntries] = 0;
-      p.header[kHdrPrefixFirst] = -2;
+      p.header[kHdrPrefixChunks] = -1;
       p.header[kHdrNextFwd] = 0;
     }
     return;
   }
-  const int short_rows = n_tok * p.group;  // at most 128 per sequence
+  const int short_rows = n_tok * p.group;
   const int n_pre = np > 0 ? div_up(short_rows, rt) : 0;
   const unsigned long long all = work + static_cast<unsigned long long>(n_pre) * np;
   // chunk length in key tiles: all heads' chunks together about parts_target * hkv
   const int len = static_cast<int>(max(1ull, (all + p.parts_target - 1) / p.parts_target));
-  int n_groups = 0, n_entries = 0, n_rows = 0;  // running totals
-  // long groups
+  int n_entries = 0, n_rows = 0;  // running totals
+  // Chunk c of a row tile with n key tiles in `chunks` chunks (they differ by one tile at
+  // most), as entry `at`; e.slot: the row tile's first partial row.
+  auto put_chunk = [&](PrefixEntry e, int n, int chunks, int c, int at) {
+    const int q = n / chunks, r = n - q * chunks;
+    e.t0 = c * q + min(c, r);
+    e.t1 = e.t0 + q + (c < r ? 1 : 0);
+    if (e.slot >= 0) e.slot += c * e.ways * p.hkv * e.rows;
+    if (at < p.cap_entries) store_entry(p, at, e);
+  };
+  // long row tiles
   for (int base = 0; base < n_long; base += blockDim.x) {
-    const int e = base + tid;
-    PrefixGroup g{};
-    int ch = 0, slots = 0;
-    if (e < n_long) {
-      int lo = 0, hi = p.batch - 1;  // last sequence whose first long group is at most e
+    const int g = base + tid;
+    PrefixEntry e{};
+    int n = 0, ch = 0, slots = 0;
+    if (g < n_long) {
+      int lo = 0, hi = p.batch - 1;  // last sequence whose first row tile is at most g
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.seqs[mid].w <= e) lo = mid; else hi = mid - 1;
+        if (p.seqs[mid].w <= g) lo = mid; else hi = mid - 1;
       }
-      const SeqInfo s = load_seq(p, lo);
-      const int u = e - p.seqs[lo].w;
-      g.seq = lo;
-      g.row0 = u * rt;
-      g.rows = min(rt, s.len_q * p.group - g.row0);
-      g.np = np;
-      g.no = own_tiles(p, s, g.row0, g.rows, bn);
-      g.chunks = ch = div_up(g.np + g.no, len);
-      g.is_long = 1;
-      slots = ch > 1 ? ch * p.hkv * g.rows : 0;
+      const SeqInfo q = load_seq(p, lo);
+      e.seq = lo;
+      e.row0 = (g - p.seqs[lo].w) * rt;
+      e.rows = min(rt, q.len_q * p.group - e.row0);
+      e.np = np;
+      e.off_q = q.off_q;
+      e.off_k = q.off_k;
+      e.len_k = q.len_k;
+      e.diag = q.diag;
+      n = np + own_tiles(p, q.len_k, q.diag, e.row0, e.rows, bn);
+      ch = div_up(n, len);
+      e.ways = ch > 1 && e.rows <= rt / 2 ? most_ways : 1;
+      slots = ch > 1 ? ch * e.ways * p.hkv * e.rows : 0;
     }
-    int t0, t1;
-    const int2 at = block_scan2(ch, slots, warp_sums, &t0, &t1);
-    if (e < n_long && n_groups + tid < p.cap_groups) {
-      g.slot = slots > 0 ? n_rows + at.y : -1;
-      store_group(p, e, g);
-      for (int c = 0; c < ch; ++c)
-        if (n_entries + at.x + c < p.cap_entries) p.entries[n_entries + at.x + c] = make_int2(e, c);
+    const Scan3 at = block_scan3(ch, slots, 0, buf);
+    if (g < n_long && g < p.cap_longs) {
+      e.slot = slots > 0 ? n_rows + at.y : -1;
+      p.longs[g] = make_int4(e.slot, ch * e.ways, e.rows, 0);
+      for (int c = 0; c < ch; ++c) put_chunk(e, n, ch, c, n_entries + at.x + c);
     }
-    n_groups += min(static_cast<int>(blockDim.x), n_long - base);
-    n_entries += t0;
-    n_rows += t1;
+    n_entries += at.tx;
+    n_rows += at.ty;
   }
-  // prefix groups, chunk-major: row tiles that read the same keys are taken side by side
+  // the compact rows against the prefix, chunk-major: row tiles that read the same keys
+  // are taken side by side
   const int pre_chunks = n_pre > 0 ? div_up(np, len) : 0;
-  for (int u = tid; u < n_pre; u += blockDim.x) {
-    PrefixGroup g{};
-    g.seq = -1;
-    g.row0 = u * rt;
-    g.rows = min(rt, short_rows - g.row0);
-    g.np = np;
-    g.chunks = pre_chunks;
-    g.slot = n_rows + u * rt * pre_chunks * p.hkv;
-    if (n_groups + u < p.cap_groups) store_group(p, n_groups + u, g);
-    for (int c = 0; c < pre_chunks; ++c) {
-      const int at = n_entries + c * n_pre + u;
-      if (at < p.cap_entries) p.entries[at] = make_int2(n_groups + u, c);
-    }
+  const int pre_slot = n_rows;
+  for (int k = tid; k < n_pre * pre_chunks; k += blockDim.x) {
+    const int c = k / n_pre, u = k - c * n_pre;
+    PrefixEntry e{};
+    e.seq = -1;
+    e.row0 = u * rt;
+    e.rows = min(rt, short_rows - e.row0);
+    e.np = np;
+    e.ways = e.rows <= rt / 2 ? most_ways : 1;
+    e.slot = pre_slot + u * rt * pre_chunks * p.hkv;
+    put_chunk(e, np, pre_chunks, c, n_entries + k);
   }
-  const int first_pre = n_groups;
-  n_groups += n_pre;
   n_entries += n_pre * pre_chunks;
-  n_rows += short_rows * pre_chunks * p.hkv;
-  // own groups of short sequences
+  if (n_pre > 0) {
+    const int last = short_rows - (n_pre - 1) * rt;
+    n_rows += ((n_pre - 1) * rt + last * (last <= rt / 2 ? most_ways : 1)) * pre_chunks * p.hkv;
+  }
+  // short sequences against their own keys
   for (int base = 0; base < p.batch; base += blockDim.x) {
     const int b = base + tid;
-    PrefixGroup g{};
-    int ch = 0, slots = 0, has = 0;
-    if (b < p.batch && p.seqs[b].x >= 0) {
-      const SeqInfo s = load_seq(p, b);
-      g.seq = b;
-      g.rows = s.len_q * p.group;
-      g.no = own_tiles(p, s, 0, g.rows, bn);
-      g.chunks = ch = div_up(g.no, len);
-      has = ch > 0 ? 1 : 0;
-      // without a prefix a single chunk is the whole result
-      slots = ch > 1 || n_pre > 0 ? ch * p.hkv * g.rows : 0;
+    if (p.batch > blockDim.x) {  // otherwise this thread's sequence is still at hand
+      s = SeqInfo{};
+      first_tok = -1;
+      if (b < p.batch) {
+        s = load_seq(p, b);
+        first_tok = p.seqs[b].x;
+      }
     }
-    int t0, t1, t2, t3;
-    const int2 at = block_scan2(ch, slots, warp_sums, &t0, &t1);
-    const int2 ag = block_scan2(has, 0, warp_sums, &t2, &t3);
-    if (has && n_groups + ag.x < p.cap_groups) {
-      const int e = n_groups + ag.x;
-      g.slot = slots > 0 ? n_rows + at.y : -1;
-      store_group(p, e, g);
-      p.seqs[b].y = e;
-      for (int c = 0; c < ch; ++c)
-        if (n_entries + at.x + c < p.cap_entries) p.entries[n_entries + at.x + c] = make_int2(e, c);
+    PrefixEntry e{};
+    int n = 0, ch = 0, slots = 0;
+    if (b < p.batch && first_tok >= 0) {
+      e.seq = b;
+      e.rows = s.len_q * p.group;
+      e.off_q = s.off_q;
+      e.off_k = s.off_k;
+      e.len_k = s.len_k;
+      e.diag = s.diag;
+      n = own_tiles(p, s.len_k, s.diag, 0, e.rows, bn);
+      ch = div_up(n, len);
+      // without a prefix a single tile is the whole result
+      const bool direct = n == 1 && n_pre == 0;
+      e.ways = direct ? 1 : most_ways;
+      slots = direct ? 0 : ch * e.ways * p.hkv * e.rows;
     }
-    n_groups += t2;
-    n_entries += t0;
-    n_rows += t1;
+    const Scan3 at = block_scan3(ch, slots, 0, buf);
+    if (ch > 0) {
+      e.slot = slots > 0 ? n_rows + at.y : -1;
+      p.seqs[b] = make_int4(first_tok, e.slot, slots > 0 ? ch * e.ways : -1, 0);
+      for (int c = 0; c < ch; ++c) put_chunk(e, n, ch, c, n_entries + at.x + c);
+    }
+    n_entries += at.tx;
+    n_rows += at.ty;
   }
-  __syncthreads();
   if (tid == 0) {
     // the capacities hold for every set of lengths; if they did not, nothing is computed
-    const bool over = n_groups > p.cap_groups || n_entries > p.cap_entries || n_rows > p.cap_rows;
+    const bool over = n_long > p.cap_longs || n_entries > p.cap_entries || n_rows > p.cap_rows;
     p.header[kHdrStatus] = (bad ? kStatusBadSeqlens : 0) | (over ? kStatusInternal : 0);
     p.header[kHdrPrefixEntries] = over ? 0 : n_entries;
-    p.header[kHdrPrefixFirst] = over ? -2 : n_pre > 0 ? first_pre : -1;
+    p.header[kHdrPrefixChunks] = over ? -1 : pre_chunks;
+    p.header[kHdrPrefixSlot] = pre_slot;
+    p.header[kHdrPrefixRows] = short_rows;
     p.header[kHdrNextFwd] = 0;
   }
 }
 
 cudaError_t launch_prefix_schedule(const PrefixParams& p, cudaStream_t st) {
-  prefix_schedule_kernel<<<1, kPrefixSchedThreads, 0, st>>>(p);
+  const int threads = p.batch >= kPrefixSchedThreads ? kPrefixSchedThreads : (p.batch + 31) / 32 * 32;
+  prefix_schedule_kernel<<<1, threads < 128 ? 128 : threads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -245,7 +298,7 @@ struct PrefixShape {
   static constexpr int kKVBytes = kChunks * kBN * 128;     // one K or V tile
   static constexpr int kStages = kD == 64 ? 4 : 2;
   static constexpr int kSmemBytes = kNT * kQBytes + 2 * kStages * kKVBytes + 1024;
-  static constexpr int kThreads = kNT * 128 + 64;
+  static constexpr int kThreads = kNT * 128 + 96;
   // TMEM columns of O and S of row tile x: O_0 O_1 S_0 S_1
   __device__ static constexpr uint32_t col_o(int x) { return static_cast<uint32_t>(x) * 128u; }
   __device__ static constexpr uint32_t col_s(int x) { return 256u + static_cast<uint32_t>(x) * 128u; }
@@ -267,15 +320,19 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 
 // What the producer hands over with an item (two of them, in turn).
 struct PrefixItem {
-  int n[2];         // key tiles that row tile A / B visits (0: none)
-  int np;           // the first np of them are prefix tiles
+  int n[2];         // key tiles that softmax group 0 / 1 visits (0: none)
+  int turns;        // 1: group x takes the key tiles x, x + 2, .. of one row tile
+                    // 0: group x takes every key tile for row tile x
+  int half;         // half of the Q buffer that holds the rows; -1: both
+  int np;           // the first np key tiles are the prefix's
+  int p_key, o_key; // tensor rows of the first prefix key and the first own key
   int p_left;       // prefix keys from the item's first prefix tile on
   int o_left;       // own real keys from the item's first own tile on
   int direct;       // rows are written to out / lse, not to partial rows
   int head;         // kv head
+  int part[2];      // partial row of the group's first row
   int row[256];     // per row: token * hq + head; -1: no row
   int lim[256];     // per row: own keys it sees from the item's first own tile on
-  int part;         // partial row of row 0
 };
 
 template <int kD, bool kBF16>
@@ -285,7 +342,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
                            const __grid_constant__ CUtensorMap tmVp) {
   using S = PrefixShape<kD>;
   constexpr int NT = S::kNT, NS = S::kStages, BN = S::kBN;
-  constexpr int kWarpProducer = NT * 4, kWarpMma = NT * 4 + 1;
+  constexpr int kWarpItem = NT * 4, kWarpKv = NT * 4 + 1, kWarpMma = NT * 4 + 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -293,7 +350,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
   uint8_t* sK = sQ + NT * S::kQBytes;
   uint8_t* sV = sK + NS * S::kKVBytes;
 
-  __shared__ uint64_t bar_q_full, bar_q_empty;
+  __shared__ uint64_t bar_q_full[NT], bar_q_empty[NT];  // per 128-row half of the Q buffer
   __shared__ uint64_t bar_k_full[NS], bar_k_empty[NS], bar_v_full[NS], bar_v_empty[NS];
   __shared__ uint64_t bar_s_full[NT], bar_p_ready[NT], bar_o_full[NT], bar_o_empty[NT];
   __shared__ WorkRing ring;
@@ -304,8 +361,6 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
   int* status = p.header + kHdrStatus;
 
   if (tid == 0) {
-    mbar_init(&bar_q_full, 32);
-    mbar_init(&bar_q_empty, 1);
     for (int i = 0; i < NS; ++i) {
       mbar_init(&bar_k_full[i], 1);
       mbar_init(&bar_k_empty[i], 1);
@@ -313,12 +368,14 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       mbar_init(&bar_v_empty[i], 1);
     }
     for (int x = 0; x < NT; ++x) {
+      mbar_init(&bar_q_full[x], 32);
+      mbar_init(&bar_q_empty[x], 1);
       mbar_init(&bar_s_full[x], 1);
       mbar_init(&bar_p_ready[x], 128);
       mbar_init(&bar_o_full[x], 1);
       mbar_init(&bar_o_empty[x], 128);
     }
-    ring_init(ring, 32 + NT * 128);
+    ring_init(ring, 1 + 32 + NT * 128);
     fence_barrier_init();
   }
   if (warp == kWarpMma) {
@@ -330,21 +387,22 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  if (warp == kWarpProducer) {
-    // ------------------------------------------------------------- producer
+  if (warp == kWarpItem) {
+    // ------------------------------------------------------------- items and Q rows
     const int n_items = p.header[kHdrPrefixEntries] * p.hkv;
     const int np_keys = prefix_keys(p);
-    if (lane == 0) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-      tma_prefetch_desc(&tmKp);
-      tma_prefetch_desc(&tmVp);
-    }
-    int it = 0;
     bool ok = true;
     int nxt = blockIdx.x;
+    int uses[2] = {0, 0};  // items so far in each half of the Q buffer
+    int half = 0;
     for (int ii = 0; ok; ++ii) {
       const int item = nxt < n_items ? nxt : -1;
+      PrefixEntry e{};
+      if (item >= 0) {
+        if (lane == 0) nxt = next_item(p.header + kHdrNextFwd);
+        e = load_entry(p, item / p.hkv);
+        nxt = __shfl_sync(0xffffffffu, nxt, 0);
+      }
       // the slot's last readers are done with it
       if (ii >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&ring.empty[ii & 1], ((ii >> 1) - 1) & 1, status));
       if (!ok) break;
@@ -355,25 +413,18 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         }
         break;
       }
-      if (lane == 0) nxt = next_item(p.header + kHdrNextFwd);
-      nxt = __shfl_sync(0xffffffffu, nxt, 0);
-      const int2 en = p.entries[item / p.hkv];
       const int h = item % p.hkv;
-      const PrefixGroup g = load_group(p, en.x);
-      const int2 ct = chunk_tiles(g, en.y);
-      SeqInfo s{};
-      if (g.seq >= 0) s = load_seq(p, g.seq);
-      const int p0 = ct.x, np = max(0, min(ct.y, g.np) - ct.x);  // prefix tiles of the chunk
-      const int o0 = max(0, ct.x - g.np);                        // first own tile
+      const int np = max(0, min(e.t1, e.np) - e.t0);  // prefix tiles of the chunk
+      const int o0 = max(0, e.t0 - e.np);             // first own tile
       PrefixItem& I = items[ii & 1];
       // rows
       for (int r = lane; r < NT * 128; r += 32) {
         int row = -1, lim = 0;
-        if (r < g.rows) {
-          const int rr = g.row0 + r, i = rr / p.group, j = rr - i * p.group;
-          const int tok = g.seq < 0 ? p.short_tok[i] : s.off_q + i;
+        if (r < e.rows) {
+          const int rr = e.row0 + r, i = rr / p.group, j = rr - i * p.group;
+          const int tok = e.seq < 0 ? p.short_tok[i] : e.off_q + i;
           row = tok * p.hq + h * p.group + j;
-          if (g.seq >= 0) lim = max(0, row_keys(s, i, p.causal != 0) - o0 * BN);
+          if (e.seq >= 0) lim = max(0, keys_seen(p.causal, e.len_k, e.diag, i) - o0 * BN);
           if (!bounds_ok(tok >= 0 && tok < p.total_q, status)) row = -1;
         }
         I.row[r] = row;
@@ -381,71 +432,100 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       }
       // own tiles end at the last one that a row of the tile sees
       int n[2] = {0, 0};
+      const bool turns = e.ways == 2;
 #pragma unroll
       for (int x = 0; x < NT; ++x) {
-        const int rows = min(128, g.rows - x * 128);
+        const int rows = min(128, e.rows - x * 128);
         if (rows > 0) {
-          const int no = g.seq >= 0 ? own_tiles(p, s, g.row0 + x * 128, rows, BN) : 0;
-          n[x] = max(0, min(ct.y, g.np + no) - ct.x);
+          const int no = e.seq >= 0 ? own_tiles(p, e.len_k, e.diag, e.row0 + x * 128, rows, BN) : 0;
+          n[x] = max(0, min(e.t1, e.np + no) - e.t0);
         }
       }
-      const int nmax = max(n[0], n[1]);
+      if (turns) {
+        n[1] = n[0] / 2;
+        n[0] -= n[1];
+      }
+      const bool both = e.rows > 128;
+      if (NT == 1) half = 0;
       if (lane == 0) {
         I.n[0] = n[0];
         I.n[1] = n[1];
+        I.turns = turns ? 1 : 0;
+        I.half = both ? -1 : half;
         I.np = np;
-        I.p_left = np_keys - p0 * BN;
-        I.o_left = s.len_k - o0 * BN;
-        I.direct = g.slot < 0 ? 1 : 0;
+        I.p_key = e.t0 * BN;
+        I.o_key = e.off_k + o0 * BN;
+        I.p_left = np_keys - e.t0 * BN;
+        I.o_left = e.len_k - o0 * BN;
+        I.direct = e.slot < 0 ? 1 : 0;
         I.head = h;
-        I.part = g.slot < 0 ? 0 : static_cast<int>(partial_row(p, g, en.y, h, 0));
+        for (int x = 0; x < 2; ++x)
+          I.part[x] = e.slot < 0 ? 0
+                                 : e.slot + static_cast<int>(partial_offset(p, e.rows, turns ? x : 0, h)) +
+                                       (turns ? 0 : x * 128);
         *reinterpret_cast<volatile int*>(&ring.item[ii & 1]) = item;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.full[ii & 1]);
-      if (ii > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar_q_empty, (ii - 1) & 1, status));
-      if (!ok) break;
       // Q rows, 16 bytes per lane and step, in the 128-byte swizzle the MMAs read;
       // columns from d on are filled with zeros. Rows past the last stay as they are:
       // they meet no other row.
+      const int h0 = both ? 0 : half, h1 = both ? NT - 1 : half;
+      for (int x = h0; x <= h1 && ok; ++x)
+        if (uses[x] > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar_q_empty[x], (uses[x] - 1) & 1, status));
+      if (!ok) break;
       constexpr int kPieces = kD / 8;
-      const int pieces = g.rows * kPieces;
+      const int pieces = e.rows * kPieces;
       for (int t = lane; t < pieces; t += 32) {
         const int r = t / kPieces, c = t % kPieces;
         const int row = I.row[r];
         const bool in = row >= 0 && c * 8 < p.d;
         const char* src = static_cast<const char*>(p.q) +
                           (in ? (static_cast<size_t>(row) * p.d + c * 8) * 2 : static_cast<size_t>(0));
-        uint8_t* dst = sQ + (r >> 7) * S::kQBytes + (c >> 3) * 16384 + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
+        uint8_t* dst = sQ + (h0 + (r >> 7)) * S::kQBytes + (c >> 3) * 16384 + (r & 127) * 128 +
+                       (((c & 7) ^ (r & 7)) << 4);
         cp_async16(dst, src, in ? 16 : 0);
       }
-      for (int j = 0; j < nmax; ++j, ++it) {
-        const int st = it % NS;
-        if (lane == 0) {
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      for (int x = h0; x <= h1; ++x) {
+        mbar_arrive(&bar_q_full[x]);
+        ++uses[x];
+      }
+      if (!both) half ^= 1;
+    }
+  } else if (warp == kWarpKv) {
+    // ------------------------------------------------------------- K and V tiles
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      tma_prefetch_desc(&tmKp);
+      tma_prefetch_desc(&tmVp);
+      int it = 0;
+      bool ok = true;
+      for (int ii = 0; ok; ++ii) {
+        const int sl = ii & 1;
+        if (!(ok = mbar_wait(&ring.full[sl], (ii >> 1) & 1, status))) break;
+        const int item = *reinterpret_cast<volatile int*>(&ring.item[sl]);
+        const PrefixItem& I = items[sl];
+        const int n = I.turns ? I.n[0] + I.n[1] : max(I.n[0], I.n[1]);
+        const int np = I.np, p_key = I.p_key, o_key = I.o_key, h = I.head;
+        mbar_arrive(&ring.empty[sl]);
+        if (item < 0) break;
+        for (int j = 0; j < n; ++j, ++it) {
+          const int st = it % NS;
           const bool pre = j < np;
           const CUtensorMap* mk = pre ? &tmKp : &tmK;
           const CUtensorMap* mv = pre ? &tmVp : &tmV;
-          const int key = pre ? (p0 + j) * BN : s.off_k + (o0 + j - np) * BN;
-          if (it >= NS) ok = mbar_wait(&bar_k_empty[st], ((it / NS) - 1) & 1, status);
-          if (ok) {
-            mbar_arrive_expect_tx(&bar_k_full[st], S::kKVBytes);
-            for (int c = 0; c < S::kChunks; ++c)
-              tma_load_4d(sK + st * S::kKVBytes + c * BN * 128, mk, &bar_k_full[st], c * 64, h, 0, key);
-            if (it >= NS) ok = mbar_wait(&bar_v_empty[st], ((it / NS) - 1) & 1, status);
-          }
-          if (ok) {
-            mbar_arrive_expect_tx(&bar_v_full[st], S::kKVBytes);
-            for (int c = 0; c < S::kChunks; ++c)
-              tma_load_4d(sV + st * S::kKVBytes + c * BN * 128, mv, &bar_v_full[st], c * 64, h, 0, key);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-        if (j == 0) {
-          // the first K and V tiles are on their way: now the Q rows
-          cp_async_wait_all();
-          fence_proxy_async_smem();
-          mbar_arrive(&bar_q_full);
+          const int key = pre ? p_key + j * BN : o_key + (j - np) * BN;
+          if (it >= NS && !(ok = mbar_wait(&bar_k_empty[st], ((it / NS) - 1) & 1, status))) break;
+          mbar_arrive_expect_tx(&bar_k_full[st], S::kKVBytes);
+          for (int c = 0; c < S::kChunks; ++c)
+            tma_load_4d(sK + st * S::kKVBytes + c * BN * 128, mk, &bar_k_full[st], c * 64, h, 0, key);
+          if (it >= NS && !(ok = mbar_wait(&bar_v_empty[st], ((it / NS) - 1) & 1, status))) break;
+          mbar_arrive_expect_tx(&bar_v_full[st], S::kKVBytes);
+          for (int c = 0; c < S::kChunks; ++c)
+            tma_load_4d(sV + st * S::kKVBytes + c * BN * 128, mv, &bar_v_full[st], c * 64, h, 0, key);
         }
       }
     }
@@ -457,85 +537,110 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
     const SmemDesc dk = smem_desc(smem_u32(sK), 16, 1024, kLayoutSW128);
     const SmemDesc dv = smem_desc(smem_u32(sV), BN * 128, 1024, kLayoutSW128);
     int it = 0;
-    int np[2] = {0, 0};  // P hand-overs consumed per tile
-    int no[2] = {0, 0};  // items in which the tile was present
+    int np[2] = {0, 0};    // P hand-overs consumed per softmax group
+    int no[2] = {0, 0};    // items in which the group was present
+    int uses[2] = {0, 0};  // items so far in each half of the Q buffer
     bool ok = true;
-    auto issue_s = [&](int x, int st) {
-      const SmemDesc qx{dq.lo + ((x * S::kQBytes) >> 4), dq.hi};
-      const SmemDesc kst{dk.lo + ((st * S::kKVBytes) >> 4), dk.hi};
-      __syncwarp();  // elect.sync in the MMA wrappers needs a converged warp
-#pragma unroll
-      for (int s = 0; s < kD / 16; ++s)
-        mma_ss(tmem + S::col_s(x), qx, (s >> 2) * 16384 + (s & 3) * 32, kst, (s >> 2) * (BN * 128) + (s & 3) * 32,
-               idS, s > 0 ? 1u : 0u);
-      mma_commit(&bar_s_full[x]);
-    };
     for (int ii = 0; ok; ++ii) {
       const int sl = ii & 1;
       ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[sl], (ii >> 1) & 1, status));
       if (!ok) break;
       const int item = *reinterpret_cast<volatile int*>(&ring.item[sl]);
       const int n[2] = {items[sl].n[0], items[sl].n[1]};
+      const bool turns = items[sl].turns != 0;
+      const int half = items[sl].half;
       const int n_pre = items[sl].np, p_left = items[sl].p_left, o_left = items[sl].o_left;
       mbar_arrive(&ring.empty[sl]);
       if (item < 0) break;
-      const int nmax = max(n[0], n[1]);
-      if (!(ok = mbar_wait_warp(&bar_q_full, ii & 1, status))) break;
-      if (!(ok = mbar_wait_warp(&bar_k_full[it % NS], (it / NS) & 1, status))) break;
-      tc_fence_after();
-      for (int x = 0; x < NT; ++x)
-        if (n[x] > 0) issue_s(x, it % NS);
-      mma_commit(&bar_k_empty[it % NS]);
-      if (nmax == 1) mma_commit(&bar_q_empty);
-      for (int j = 0; j < nmax && ok; ++j) {
-        const int cur = it + j, st = cur % NS;
-        bool v_ready = false, k_ready = false;
-        for (int x = 0; x < NT && ok; ++x) {
-          if (j >= n[x]) continue;
-          if (!(ok = mbar_wait_warp(&bar_p_ready[x], np[x] & 1, status))) break;
-          ++np[x];
-          if (j == 0 && no[x] > 0 && !(ok = mbar_wait_warp(&bar_o_empty[x], (no[x] - 1) & 1, status))) break;
-          if (!v_ready) {
-            if (!(ok = mbar_wait_warp(&bar_v_full[st], (cur / NS) & 1, status))) break;
-            v_ready = true;
-            // V rows that are no real key: zeros (P is 0 there, but 0 times NaN is not)
-            const int real = j < n_pre ? p_left - j * BN : o_left - (j - n_pre) * BN;
-            if (real < BN) {
-              for (int t = real * 8 + lane; t < BN * 8; t += 32)
-                for (int c = 0; c < S::kChunks; ++c)
-                  st_shared_v4(sV + st * S::kKVBytes + c * BN * 128 + t * 16, 0, 0, 0, 0);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-          }
-          tc_fence_after();
-          const SmemDesc vst{dv.lo + ((st * S::kKVBytes) >> 4), dv.hi};
-          const uint32_t acc0 = j > 0 ? 1u : 0u;
-          __syncwarp();
+      const int h0 = half < 0 ? 0 : half, h1 = half < 0 ? NT - 1 : half;
+      for (int x = h0; x <= h1 && ok; ++x) ok = mbar_wait_warp(&bar_q_full[x], uses[x]++ & 1, status);
+      if (!ok) break;
+      auto run_item = [&](auto turns_tag) -> bool {
+        constexpr bool kTurns = decltype(turns_tag)::value;
+        int s_left = n[0] + n[1];  // scores still to be issued: then the Q rows are free
+        // S_x = Q_x K^T for the item's key tile t
+        auto issue_s = [&](int x, int t) {
+          const int st = (it + t) % NS;
+          const SmemDesc qx{dq.lo + (((half < 0 ? x : half) * S::kQBytes) >> 4), dq.hi};
+          const SmemDesc kst{dk.lo + ((st * S::kKVBytes) >> 4), dk.hi};
+          __syncwarp();  // elect.sync in the MMA wrappers needs a converged warp
 #pragma unroll
-          for (int s = 0; s < BN / 16; ++s)
-            mma_ts(tmem + S::col_o(x), tmem + S::col_s(x) + s * 8, vst, s * 2048, idPV, s > 0 ? 1u : acc0);
-          if (j + 1 < n[x]) {
-            const int nx = cur + 1;
-            if (!k_ready) {
-              if (!(ok = mbar_wait_warp(&bar_k_full[nx % NS], (nx / NS) & 1, status))) break;
-              k_ready = true;
+          for (int s = 0; s < kD / 16; ++s)
+            mma_ss(tmem + S::col_s(x), qx, (s >> 2) * 16384 + (s & 3) * 32, kst, (s >> 2) * (BN * 128) + (s & 3) * 32,
+                   idS, s > 0 ? 1u : 0u);
+          mma_commit(&bar_s_full[x]);
+          if (kTurns) mma_commit(&bar_k_empty[st]);
+          if (--s_left == 0)
+            for (int y = h0; y <= h1; ++y) mma_commit(&bar_q_empty[y]);
+        };
+        auto wait_k = [&](int t) {
+          const int cur = it + t;
+          return mbar_wait_warp(&bar_k_full[cur % NS], (cur / NS) & 1, status);
+        };
+        const int rounds = max(n[0], n[1]);
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          if (n[x] == 0) continue;
+          const int t = kTurns ? x : 0;
+          if (!wait_k(t)) return false;
+          tc_fence_after();
+          issue_s(x, t);
+        }
+        if (!kTurns) mma_commit(&bar_k_empty[it % NS]);
+        for (int j = 0; j < rounds; ++j) {
+          bool v_ready = false, k_ready = false;
+#pragma unroll
+          for (int x = 0; x < NT; ++x) {
+            if (j >= n[x]) continue;
+            const int t = kTurns ? 2 * j + x : j, cur = it + t, st = cur % NS;
+            if (!mbar_wait_warp(&bar_p_ready[x], np[x] & 1, status)) return false;
+            ++np[x];
+            if (j == 0 && no[x] > 0 && !mbar_wait_warp(&bar_o_empty[x], (no[x] - 1) & 1, status)) return false;
+            if (kTurns || !v_ready) {
+              if (!mbar_wait_warp(&bar_v_full[st], (cur / NS) & 1, status)) return false;
+              v_ready = true;
+              // V rows that are no real key: zeros (P is 0 there, but 0 times NaN is not)
+              const int real = t < n_pre ? p_left - t * BN : o_left - (t - n_pre) * BN;
+              if (real < BN) {
+                for (int z = real * 8 + lane; z < BN * 8; z += 32)
+                  for (int c = 0; c < S::kChunks; ++c)
+                    st_shared_v4(sV + st * S::kKVBytes + c * BN * 128 + z * 16, 0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
             }
             tc_fence_after();
-            issue_s(x, nx % NS);
-          } else {
-            mma_commit(&bar_o_full[x]);
+            const SmemDesc vst{dv.lo + ((st * S::kKVBytes) >> 4), dv.hi};
+            const uint32_t acc0 = j > 0 ? 1u : 0u;
+            __syncwarp();
+#pragma unroll
+            for (int s = 0; s < BN / 16; ++s)
+              mma_ts(tmem + S::col_o(x), tmem + S::col_s(x) + s * 8, vst, s * 2048, idPV, s > 0 ? 1u : acc0);
+            if (kTurns) mma_commit(&bar_v_empty[st]);
+            if (j + 1 < n[x]) {
+              const int tn = kTurns ? t + 2 : t + 1;
+              if (kTurns || !k_ready) {
+                if (!wait_k(tn)) return false;
+                k_ready = true;
+              }
+              tc_fence_after();
+              issue_s(x, tn);
+            } else {
+              mma_commit(&bar_o_full[x]);
+            }
+          }
+          if (!kTurns) {
+            mma_commit(&bar_v_empty[(it + j) % NS]);
+            if (j + 1 < rounds) mma_commit(&bar_k_empty[(it + j + 1) % NS]);
           }
         }
-        if (!ok) break;
-        mma_commit(&bar_v_empty[st]);
-        if (j + 1 < nmax) mma_commit(&bar_k_empty[(cur + 1) % NS]);
-        if (j + 2 == nmax) mma_commit(&bar_q_empty);
-      }
+        it += kTurns ? n[0] + n[1] : rounds;
+        return true;
+      };
+      ok = NT == 2 && turns ? run_item(std::true_type{}) : run_item(std::false_type{});
       if (!ok) break;
       for (int x = 0; x < NT; ++x)
         if (n[x] > 0) ++no[x];
-      it += nmax;
     }
   } else {
     // ------------------------------------------------------------- softmax
@@ -544,7 +649,6 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
     const uint32_t t_s = tmem + S::col_s(x) + lane_base;
     const uint32_t t_o = tmem + S::col_o(x) + lane_base;
     using T = typename std::conditional<kBF16, __nv_bfloat16, __half>::type;
-    const int r = x * 128 + quarter * 32 + lane;  // row of the item
     const float sl2 = p.scale_log2;
     int ns = 0, no = 0;  // S hand-overs and items of this tile so far
     bool ok = true;
@@ -554,9 +658,12 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       if (!ok) break;
       const int item = *reinterpret_cast<volatile int*>(&ring.item[sl]);
       const int n = items[sl].n[x], n_pre = items[sl].np, p_left = items[sl].p_left;
+      const int turns = items[sl].turns;
+      // row of the item: with turns both groups hold the same rows
+      const int r = (turns ? 0 : x * 128) + quarter * 32 + lane;
       const int row = items[sl].row[r], own = items[sl].lim[r];
       const bool direct = items[sl].direct != 0;
-      const size_t part = static_cast<size_t>(items[sl].part) + r;
+      const size_t part = static_cast<size_t>(items[sl].part[x]) + quarter * 32 + lane;
       mbar_arrive(&ring.empty[sl]);
       if (item < 0) break;
       const bool live = row >= 0;
@@ -571,7 +678,8 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           continue;
         }
         tc_fence_after();
-        const int left = j < n_pre ? p_left - j * BN : own - (j - n_pre) * BN;
+        const int t = turns ? 2 * j + x : j;
+        const int left = t < n_pre ? p_left - t * BN : own - (t - n_pre) * BN;
         const int nvalid = live ? min(max(left, 0), BN) : 0;
         const bool full = __all_sync(0xffffffffu, nvalid >= BN);
         // Row max of this tile's visible scores (log2 domain), from S in TMEM.
@@ -753,100 +861,150 @@ cudaError_t launch_prefix_fwd(const PrefixParams& p, bool bf16, int num_sms, cud
 }
 
 // ---------------------------------------------------------------------------
-// Join: rows that left partial results, and the rows that hold no token. One warp per
-// (token, some heads); of a row's n partial rows, O = sum_c 2^(m_c - M) O_c / L with
-// M = max m_c and L = sum_c 2^(m_c - M) l_c, all in fp32, rounded once.
+// Join: rows that left partial results, and the rows that hold no token. Of a row's n
+// partial rows, O = sum_k 2^(m_k - M) O_k / L with M = max m_k and L = sum_k 2^(m_k - M)
+// l_k, in fp32 and in the order of k (per warp), rounded once. Latency-bound with few rows:
+// then kWarps warps share a row's parts, four loads in flight each, and add up in shared
+// memory; with many, one warp takes a row alone, or several heads of a token.
 // ---------------------------------------------------------------------------
-template <bool kBF16>
+template <bool kBF16, int kWarps>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ PrefixParams p, int slices) {
-  const int lane = threadIdx.x & 31;
-  const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (w >= static_cast<long long>(p.total_q) * slices) return;
-  const int t = static_cast<int>(w / slices), slice = static_cast<int>(w % slices);
-  const int h0 = static_cast<int>(static_cast<long long>(p.hq) * slice / slices);
-  const int h1 = static_cast<int>(static_cast<long long>(p.hq) * (slice + 1) / slices);
   using T = typename std::conditional<kBF16, __nv_bfloat16, __half>::type;
-  int i = 0;
-  const int b = locate_row(p, p.cu_q_pad, t, &i);
+  __shared__ float s_acc[kWarps > 1 ? 8 : 1][kWarps > 1 ? 256 : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = warp % kWarps;  // this warp's share of a row's parts
+  const long long w = static_cast<long long>(blockIdx.x) * (8 / kWarps) + warp / kWarps;
+  const bool any = w < static_cast<long long>(p.total_q) * slices;
+  const int t = any ? static_cast<int>(w / slices) : 0, slice = any ? static_cast<int>(w % slices) : 0;
+  const int h0 = static_cast<int>(static_cast<long long>(p.hq) * slice / slices);
+  const int h1 = any ? static_cast<int>(static_cast<long long>(p.hq) * (slice + 1) / slices) : h0;
+  // the token's sequence: a search among offsets in shared memory, where they fit (each
+  // step of it would otherwise be a trip to L2)
+  constexpr int kCached = 2047;
+  __shared__ int s_pad[kCached + 1];
+  const int rt = prefix_row_tile(p.d);
+  const int pre_chunks = p.header[kHdrPrefixChunks], pre_slot = p.header[kHdrPrefixSlot];
+  const int pre_rows = p.header[kHdrPrefixRows];
+  int i = 0, b;
+  if (p.batch <= kCached) {
+    for (int k = threadIdx.x; k <= p.batch; k += 256) s_pad[k] = p.cu_q_pad[k];
+    __syncthreads();
+    b = locate_row(p, s_pad, t, &i);
+  } else {
+    b = locate_row(p, p.cu_q_pad, t, &i);
+  }
   SeqInfo s{};
-  if (b >= 0) s = load_seq(p, b);
-  const int rt = prefix_row_tile(p.d), first_pre = p.header[kHdrPrefixFirst];
-  // -2: the lengths allow no result
-  const bool real = b >= 0 && i < s.len_q && first_pre != -2;
-  const int4 info = real ? p.seqs[b] : make_int4(-1, -1, -1, 0);
-  for (int h = h0; h < h1; ++h) {
+  int4 info = make_int4(-1, -1, 0, 0);
+  if (b >= 0) {
+    s = load_seq(p, b);
+    info = p.seqs[b];
+  }
+  // -1 chunks: the lengths allow no result
+  const bool real = b >= 0 && i < s.len_q && pre_chunks >= 0;
+  if (kWarps == 1 && real && info.x < 0) {
+    // a long sequence's token whose row tiles the main kernel wrote whole: nothing to do
+    const int4 first = p.longs[info.w + i * p.group / rt], last = p.longs[info.w + (i * p.group + p.group - 1) / rt];
+    if (p.group <= rt && first.x < 0 && first.y == 1 && last.x < 0 && last.y == 1) return;
+  }
+  // several warps per row: slices == hq, one head each, so the loop runs once for all
+  for (int h = h0; h < (kWarps > 1 ? h0 + 1 : h1); ++h) {
     const size_t row = static_cast<size_t>(t) * p.hq + h;
     const int g = h / p.group, j = h - g * p.group;
-    // up to two groups hold this row
-    PrefixGroup ga{}, gb{};
-    int ra = 0, rb = 0, na = 0, nb = 0;
-    if (info.z >= 0) {
+    // the row's parts: na of row tile a (partial rows a0 + k astep), then nb of its own keys
+    bool write = h < h1;
+    int na = 0, nb = 0;
+    size_t a0 = 0, astep = 0, b0 = 0, bstep = 0;
+    if (real && info.x < 0) {
       const int rr = i * p.group + j;
-      ga = load_group(p, info.z + rr / rt);
-      if (ga.chunks == 1) continue;  // written by the main kernel
-      ra = rr % rt;
-      na = ga.chunks;
-    } else if (info.x >= 0) {
-      if (first_pre >= 0) {
-        const int rr = (info.x + i) * p.group + j;
-        ga = load_group(p, first_pre + rr / rt);
-        ra = rr % rt;
-        na = ga.chunks;
+      const int4 tile = p.longs[info.w + rr / rt];
+      write = write && (tile.x >= 0 || tile.y == 0);  // else the main kernel wrote it
+      na = tile.y;
+      a0 = static_cast<size_t>(tile.x) + partial_offset(p, tile.z, 0, g) + rr % rt;
+      astep = partial_offset(p, tile.z, 1, 0);
+    } else if (real) {
+      if (pre_chunks > 0) {
+        const int rr = (info.x + i) * p.group + j, u = rr / rt;
+        const int rows = min(rt, pre_rows - u * rt);
+        na = pre_chunks * (rows <= rt / 2 ? rt / 128 : 1);
+        a0 = static_cast<size_t>(pre_slot) + static_cast<size_t>(u) * rt * pre_chunks * p.hkv +
+             partial_offset(p, rows, 0, g) + rr % rt;
+        astep = partial_offset(p, rows, 1, 0);
       }
-      if (info.y >= 0) {
-        gb = load_group(p, info.y);
-        if (gb.slot < 0) continue;  // written by the main kernel
-        rb = i * p.group + j;
-        nb = gb.chunks;
-      }
+      write = write && info.z >= 0;
+      nb = max(info.z, 0);
+      const int rows = s.len_q * p.group;
+      b0 = static_cast<size_t>(info.y) + partial_offset(p, rows, 0, g) + i * p.group + j;
+      bstep = partial_offset(p, rows, 1, 0);
     }
-    const int n = na + nb;
-    auto at = [&](int c) { return c < na ? partial_row(p, ga, c, g, ra) : partial_row(p, gb, c - na, g, rb); };
+    const int n = write ? na + nb : 0;
+    auto at = [&](int k) { return k < na ? a0 + k * astep : b0 + (k - na) * bstep; };
     float M = -INFINITY;
-    for (int c = lane; c < n; c += 32) {
-      const float2 ml = p.part_ml[at(c)];
+    for (int k = lane; k < n; k += 32) {
+      const float2 ml = p.part_ml[at(k)];
       if (ml.y > 0.f) M = fmaxf(M, ml.x);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float L = 0.f;
     float acc[8] = {};
-    for (int c0 = 0; c0 < n; c0 += 32) {
+    for (int k0 = 0; k0 < n; k0 += 32) {
       float wgt = 0.f;
-      if (c0 + lane < n) {
-        const float2 ml = p.part_ml[at(c0 + lane)];
-        // a chunk without a visible key left no output
+      if (k0 + lane < n) {
+        const float2 ml = p.part_ml[at(k0 + lane)];
+        // a part without a visible key left no output
         wgt = ml.y > 0.f ? ex2p(ml.x - M) : 0.f;
         L += wgt * ml.y;
       }
-      const int nc = min(32, n - c0);
-      for (int c = 0; c < nc; ++c) {
-        const float wc = __shfl_sync(0xffffffffu, wgt, c);
-        if (wc == 0.f) continue;
-        const float* src = p.part_o + at(c0 + c) * p.d;
+      uint32_t todo = __ballot_sync(0xffffffffu, wgt != 0.f && (k0 + lane) % kWarps == sub);
+      while (todo) {
+        float wk[4];
+        float4 v[4][2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int col = 128 * k + 4 * lane;
-          if (col < p.d) {
-            const float4 v = *reinterpret_cast<const float4*>(src + col);
-            acc[4 * k] = fmaf(wc, v.x, acc[4 * k]);
-            acc[4 * k + 1] = fmaf(wc, v.y, acc[4 * k + 1]);
-            acc[4 * k + 2] = fmaf(wc, v.z, acc[4 * k + 2]);
-            acc[4 * k + 3] = fmaf(wc, v.w, acc[4 * k + 3]);
+        for (int u = 0; u < 4; ++u) {
+          const int k = todo ? __ffs(todo) - 1 : 0;
+          const float ww = __shfl_sync(0xffffffffu, wgt, k);
+          wk[u] = todo ? ww : 0.f;
+          const float* src = p.part_o + at(k0 + k) * p.d;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col = 128 * c + 4 * lane;
+            v[u][c] = todo && col < p.d ? *reinterpret_cast<const float4*>(src + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          todo &= todo - 1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            acc[4 * c] = fmaf(wk[u], v[u][c].x, acc[4 * c]);
+            acc[4 * c + 1] = fmaf(wk[u], v[u][c].y, acc[4 * c + 1]);
+            acc[4 * c + 2] = fmaf(wk[u], v[u][c].z, acc[4 * c + 2]);
+            acc[4 * c + 3] = fmaf(wk[u], v[u][c].w, acc[4 * c + 3]);
           }
         }
       }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if constexpr (kWarps > 1) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s_acc[warp][(c >> 2) * 128 + 4 * lane + (c & 3)] = acc[c];
+      __syncthreads();
+      if (sub != 0) return;
+#pragma unroll
+      for (int o = 1; o < kWarps; ++o)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] += s_acc[warp + o][(c >> 2) * 128 + 4 * lane + (c & 3)];
+    }
+    if (!write) continue;
     const float inv = L > 0.f ? 1.0f / L : 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int col = 128 * k + 4 * lane;
+    for (int c = 0; c < 2; ++c) {
+      const int col = 128 * c + 4 * lane;
       if (col < p.d) {
         uint2 v;
-        v.x = pack2<kBF16>(acc[4 * k] * inv, acc[4 * k + 1] * inv);
-        v.y = pack2<kBF16>(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv);
+        v.x = pack2<kBF16>(acc[4 * c] * inv, acc[4 * c + 1] * inv);
+        v.y = pack2<kBF16>(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv);
         *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * p.d + col) = v;
       }
     }
@@ -854,14 +1012,25 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
   }
 }
 
-cudaError_t launch_prefix_join(const PrefixParams& p, bool bf16, cudaStream_t st) {
-  // enough warps to fill the GPU with few tokens, whole tokens with many
-  const int slices = p.total_q >= 4096 ? 1 : (4096 + p.total_q - 1) / p.total_q < p.hq ? (4096 + p.total_q - 1) / p.total_q : p.hq;
-  const long long warps = static_cast<long long>(p.total_q) * slices;
-  const unsigned blocks = static_cast<unsigned>((warps + 7) / 8);
-  if (bf16) prefix_join_kernel<true><<<blocks, 256, 0, st>>>(p, slices);
-  else prefix_join_kernel<false><<<blocks, 256, 0, st>>>(p, slices);
+template <bool kBF16>
+static cudaError_t launch_join_impl(const PrefixParams& p, int num_sms, cudaStream_t st) {
+  const long long rows = static_cast<long long>(p.total_q) * p.hq, few = static_cast<long long>(num_sms) * 16;
+  auto blocks = [](long long warps) { return static_cast<unsigned>((warps + 7) / 8); };
+  if (rows * 4 <= few) {
+    prefix_join_kernel<kBF16, 8><<<blocks(rows * 8), 256, 0, st>>>(p, p.hq);
+  } else if (rows <= few) {
+    prefix_join_kernel<kBF16, 4><<<blocks(rows * 4), 256, 0, st>>>(p, p.hq);
+  } else {
+    // one warp per row while that fills the GPU about twice over, several heads beyond it
+    const long long want = (4 * few + p.total_q - 1) / p.total_q;
+    const int slices = static_cast<int>(want < p.hq ? want : p.hq);
+    prefix_join_kernel<kBF16, 1><<<blocks(static_cast<long long>(p.total_q) * slices), 256, 0, st>>>(p, slices);
+  }
   return cudaGetLastError();
+}
+
+cudaError_t launch_prefix_join(const PrefixParams& p, bool bf16, int num_sms, cudaStream_t st) {
+  return bf16 ? launch_join_impl<true>(p, num_sms, st) : launch_join_impl<false>(p, num_sms, st);
 }
 
 }  // namespace teattn

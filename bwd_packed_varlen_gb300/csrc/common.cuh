@@ -25,8 +25,10 @@ enum HeaderWord : int {
   kHdrNumFPairs = 6, // number of (sequence, 256-row query tile pair) items
   kHdrNextFused = 7, // work counter of the fused backward kernel
   kHdrSelftest = 8,  // words 8..11: results of te_attn_selftest_wait_timeout
-  kHdrPrefixEntries = 12, // shared-prefix forward: (group, chunk) entries
-  kHdrPrefixFirst = 13,   // shared-prefix forward: first prefix group (-1: none, -2: no result)
+  kHdrPrefixEntries = 12, // shared-prefix forward: entries; of the compact rows against the
+  kHdrPrefixChunks = 13,  // prefix: chunks (0: none, -1: no row has a result), first partial
+  kHdrPrefixSlot = 14,    // row, rows
+  kHdrPrefixRows = 15,
   kHdrWords = 64     // header size in int32 words (256 bytes, keeps alignment)
 };
 

@@ -65,17 +65,19 @@ PrefixParams base_params(const void* q, const void* k, const void* v, const void
 }
 
 // Forward workspace, 256-byte aligned sections: header, per-sequence records, compact
-// tokens, groups, entries, partial rows (maximum and sum; d fp32 columns). The capacities
-// follow from sum_b Lq_b <= total_q: with T chunks aimed at and row tiles of R packed rows,
-//   groups   <= 2 (total_q G / R + batch + 1)        entries <= T + groups
-//   partial rows of a kv head <= 2 R T + 2 min(total_q G, 128 batch):
-// a group of n key tiles has at most n / len + 1 chunks, sum n / len <= T, rows of short
-// sequences (at most 128 each) are in two groups, and a long group leaves partial rows
-// only with two chunks or more, when n / len + 1 <= 2 n / len.
+// tokens, long row tiles, entries, partial rows (maximum and sum; d fp32 columns). The
+// capacities follow from sum_b Lq_b <= total_q: with T chunks aimed at and row tiles of R rows,
+//   long row tiles <= total_q G / R + batch,   entries <= T + 2 (total_q G / R + batch + 1)
+//   partial rows of a kv head <= 2 R T + 3 min(total_q G, 128 batch) + 128:
+// a group of n key tiles has at most n / len + 1 chunks, sum n / len <= T, a chunk leaves
+// at most R partial rows (two parts only of at most R / 2 rows), rows of short sequences
+// (at most 128 each) are in a prefix group, of which only the last leaves two parts, and in
+// an own one, and a long group leaves partial rows only with two chunks or more, when
+// n / len + 1 <= 2 n / len.
 struct FwdLayout {
-  size_t seqs, short_tok, groups, entries, part_ml, part_o, total;
+  size_t seqs, short_tok, longs, entries, part_ml, part_o, total;
   int parts_target;
-  long long cap_groups, cap_entries, cap_rows;
+  long long cap_longs, cap_entries, cap_rows;
 };
 
 bool fwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, int hkv, int d, FwdLayout* L) {
@@ -84,10 +86,10 @@ bool fwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, i
     return false;
   const long long rows = static_cast<long long>(total_q) * (hq / hkv), rt = prefix_row_tile(d);
   L->parts_target = (kPartsTarget + hkv - 1) / hkv;
-  L->cap_groups = 2 * (rows / rt + batch + 1);
-  L->cap_entries = L->parts_target + L->cap_groups;
+  L->cap_longs = rows / rt + batch;
+  L->cap_entries = L->parts_target + 2 * (L->cap_longs + 1);
   const long long few = static_cast<long long>(kShortRows) * batch;
-  L->cap_rows = hkv * (2 * rt * L->parts_target + 2 * (rows < few ? rows : few));
+  L->cap_rows = hkv * (2 * rt * L->parts_target + 3 * (rows < few ? rows : few) + 128);
   if (L->cap_rows > INT32_MAX || L->cap_entries * hkv > INT32_MAX) return false;
   size_t off = kHdrWords * sizeof(int);
   auto take = [&off](size_t bytes) {
@@ -97,8 +99,8 @@ bool fwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, i
   };
   L->seqs = take(static_cast<size_t>(batch) * sizeof(int4));
   L->short_tok = take(static_cast<size_t>(total_q) * sizeof(int));
-  L->groups = take(static_cast<size_t>(L->cap_groups) * 2 * sizeof(int4));
-  L->entries = take(static_cast<size_t>(L->cap_entries) * sizeof(int2));
+  L->longs = take(static_cast<size_t>(L->cap_longs) * sizeof(int4));
+  L->entries = take(static_cast<size_t>(L->cap_entries) * 3 * sizeof(int4));
   L->part_ml = take(static_cast<size_t>(L->cap_rows) * sizeof(float2));
   L->part_o = take(static_cast<size_t>(L->cap_rows) * d * sizeof(float));
   L->total = off;
@@ -212,12 +214,12 @@ int te_attn_prefix_fwd_thd(const void* q, const void* k, const void* v, const vo
   p.header = static_cast<int*>(workspace);
   p.seqs = reinterpret_cast<int4*>(ws + L.seqs);
   p.short_tok = reinterpret_cast<int*>(ws + L.short_tok);
-  p.groups = reinterpret_cast<int4*>(ws + L.groups);
-  p.entries = reinterpret_cast<int2*>(ws + L.entries);
+  p.longs = reinterpret_cast<int4*>(ws + L.longs);
+  p.entries = reinterpret_cast<int4*>(ws + L.entries);
   p.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   p.part_o = reinterpret_cast<float*>(ws + L.part_o);
   p.parts_target = L.parts_target;
-  p.cap_groups = static_cast<int>(L.cap_groups);
+  p.cap_longs = static_cast<int>(L.cap_longs);
   p.cap_entries = static_cast<int>(L.cap_entries);
   p.cap_rows = static_cast<int>(L.cap_rows);
   const bool bf16 = dtype == TE_DTYPE_BF16;
@@ -229,7 +231,7 @@ int te_attn_prefix_fwd_thd(const void* q, const void* k, const void* v, const vo
     e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_prefix_fwd(p, bf16, sms, st); });
     if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix forward");
   }
-  e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_prefix_join(p, bf16, st); });
+  e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_prefix_join(p, bf16, sms, st); });
   return e == cudaSuccess ? api_ok() : api_cuda_fail(e, "shared-prefix join");
 }
 
