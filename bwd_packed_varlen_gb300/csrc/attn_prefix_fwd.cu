@@ -323,6 +323,7 @@ struct PrefixItem {
   int n[2];         // key tiles that softmax group 0 / 1 visits (0: none)
   int turns;        // 1: group x takes the key tiles x, x + 2, .. of one row tile
                     // 0: group x takes every key tile for row tile x
+  int rows;         // rows of the item; the arrays below hold them rounded up to 32
   int half;         // half of the Q buffer that holds the rows; -1: both
   int np;           // the first np key tiles are the prefix's
   int p_key, o_key; // tensor rows of the first prefix key and the first own key
@@ -389,6 +390,9 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
 
   if (warp == kWarpItem) {
     // ------------------------------------------------------------- items and Q rows
+    // the first entry is read along with the number of entries (the grid is no larger than
+    // the entries' capacity)
+    PrefixEntry first = load_entry(p, blockIdx.x / p.hkv);
     const int n_items = p.header[kHdrPrefixEntries] * p.hkv;
     const int np_keys = prefix_keys(p);
     bool ok = true;
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       PrefixEntry e{};
       if (item >= 0) {
         if (lane == 0) nxt = next_item(p.header + kHdrNextFwd);
-        e = load_entry(p, item / p.hkv);
+        e = ii == 0 ? first : load_entry(p, item / p.hkv);
         nxt = __shfl_sync(0xffffffffu, nxt, 0);
       }
       // the slot's last readers are done with it
@@ -417,18 +421,22 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       const int np = max(0, min(e.t1, e.np) - e.t0);  // prefix tiles of the chunk
       const int o0 = max(0, e.t0 - e.np);             // first own tile
       PrefixItem& I = items[ii & 1];
-      // rows
-      for (int r = lane; r < NT * 128; r += 32) {
-        int row = -1, lim = 0;
-        if (r < e.rows) {
-          const int rr = e.row0 + r, i = rr / p.group, j = rr - i * p.group;
-          const int tok = e.seq < 0 ? p.short_tok[i] : e.off_q + i;
-          row = tok * p.hq + h * p.group + j;
-          if (e.seq >= 0) lim = max(0, keys_seen(p.causal, e.len_k, e.diag, i) - o0 * BN);
-          if (!bounds_ok(tok >= 0 && tok < p.total_q, status)) row = -1;
-        }
-        I.row[r] = row;
-        I.lim[r] = lim;
+      // rows: where they lie and what they see (all loads of a batch in flight at once)
+      constexpr int kPer = NT * 4;  // rows per lane
+      int tok[kPer];
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const int r = u * 32 + lane, i = (e.row0 + r) / p.group;
+        tok[u] = r >= e.rows ? -1 : e.seq < 0 ? p.short_tok[i] : e.off_q + i;
+      }
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const int r = u * 32 + lane;
+        if (u * 32 >= e.rows) break;
+        const int rr = e.row0 + r, i = rr / p.group, j = rr - i * p.group;
+        const bool in = r < e.rows && bounds_ok(tok[u] >= 0 && tok[u] < p.total_q, status);
+        I.row[r] = in ? tok[u] * p.hq + h * p.group + j : -1;
+        I.lim[r] = in && e.seq >= 0 ? max(0, keys_seen(p.causal, e.len_k, e.diag, i) - o0 * BN) : 0;
       }
       // own tiles end at the last one that a row of the tile sees
       int n[2] = {0, 0};
@@ -450,6 +458,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       if (lane == 0) {
         I.n[0] = n[0];
         I.n[1] = n[1];
+        I.rows = e.rows;
         I.turns = turns ? 1 : 0;
         I.half = both ? -1 : half;
         I.np = np;
@@ -474,17 +483,28 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       for (int x = h0; x <= h1 && ok; ++x)
         if (uses[x] > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar_q_empty[x], (uses[x] - 1) & 1, status));
       if (!ok) break;
-      constexpr int kPieces = kD / 8;
-      const int pieces = e.rows * kPieces;
-      for (int t = lane; t < pieces; t += 32) {
-        const int r = t / kPieces, c = t % kPieces;
-        const int row = I.row[r];
-        const bool in = row >= 0 && c * 8 < p.d;
-        const char* src = static_cast<const char*>(p.q) +
-                          (in ? (static_cast<size_t>(row) * p.d + c * 8) * 2 : static_cast<size_t>(0));
-        uint8_t* dst = sQ + (h0 + (r >> 7)) * S::kQBytes + (c >> 3) * 16384 + (r & 127) * 128 +
-                       (((c & 7) ^ (r & 7)) << 4);
-        cp_async16(dst, src, in ? 16 : 0);
+      // (A lane keeps its column; addresses of eight rows are worked out before the copies,
+      // which then issue back to back: one by one each took 130 cycles of this warp.)
+      constexpr int kPieces = kD / 8, kRowsPer = 32 / (kPieces < 32 ? kPieces : 32);  // rows per step
+      const int c = lane % kPieces, r_in = lane / kPieces;
+      const bool col = c * 8 < p.d;
+      const char* q_col = static_cast<const char*>(p.q) + c * 16;
+      uint8_t* s_col = sQ + h0 * S::kQBytes + (c >> 3) * 16384;
+      for (int r0 = 0; r0 < e.rows; r0 += 8 * kRowsPer) {
+        const char* src[8];
+        uint8_t* dst[8];
+        int bytes[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int r = r0 + u * kRowsPer + r_in;
+          const int row = r < e.rows ? I.row[r] : -1;
+          bytes[u] = row >= 0 && col ? 16 : 0;
+          src[u] = bytes[u] ? q_col + static_cast<size_t>(row) * (p.d * 2) : static_cast<const char*>(p.q);
+          dst[u] = s_col + (r >> 7) * S::kQBytes + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (r0 + u * kRowsPer + r_in < e.rows) cp_async16(dst[u], src[u], bytes[u]);
       }
       cp_async_wait_all();
       fence_proxy_async_smem();
@@ -649,7 +669,10 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
     const uint32_t t_s = tmem + S::col_s(x) + lane_base;
     const uint32_t t_o = tmem + S::col_o(x) + lane_base;
     using T = typename std::conditional<kBF16, __nv_bfloat16, __half>::type;
-    const float sl2 = p.scale_log2;
+    // A scale of 0 becomes the smallest positive one, which gives the same P (2^(S 1e-38) =
+    // 1), so that the infinity put on a masked score below stays one.
+    const float sl2 = p.scale_log2 == 0.f ? 1.17549435e-38f : p.scale_log2;
+    const float masked = sl2 > 0.f ? -INFINITY : INFINITY;
     int ns = 0, no = 0;  // S hand-overs and items of this tile so far
     bool ok = true;
     for (int ii = 0; ok; ++ii) {
@@ -661,7 +684,8 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       const int turns = items[sl].turns;
       // row of the item: with turns both groups hold the same rows
       const int r = (turns ? 0 : x * 128) + quarter * 32 + lane;
-      const int row = items[sl].row[r], own = items[sl].lim[r];
+      const bool in = r < items[sl].rows;
+      const int row = in ? items[sl].row[r] : -1, own = in ? items[sl].lim[r] : 0;
       const bool direct = items[sl].direct != 0;
       const size_t part = static_cast<size_t>(items[sl].part[x]) + quarter * 32 + lane;
       mbar_arrive(&ring.empty[sl]);
@@ -681,35 +705,52 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         const int t = turns ? 2 * j + x : j;
         const int left = t < n_pre ? p_left - t * BN : own - (t - n_pre) * BN;
         const int nvalid = live ? min(max(left, 0), BN) : 0;
-        const bool full = __all_sync(0xffffffffu, nvalid >= BN);
-        // Row max of this tile's visible scores (log2 domain), from S in TMEM.
-        auto tile_max = [&]() -> float {
-          float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int k = 0; k < BN / 32; ++k) {
+        // Tiles that some row does not see whole: its masked scores become -infinity (once
+        // scaled) in TMEM, 32 columns at a time, and the rest of the code knows no masks.
+        // These rare steps are rolled loops: unrolled, with a masked copy of the pass below,
+        // the code outgrew the instruction cache and a block's first tile took 5000 cycles.
+        if (!__all_sync(0xffffffffu, nvalid >= BN)) {
+#pragma unroll 1
+          for (int k = 0; k < BN; k += 32) {
+            if (__all_sync(0xffffffffu, nvalid >= k + 32)) continue;
             uint32_t sv[32];
-            tmem_ld32(t_s + 32 * k, sv);
+            tmem_ld32(t_s + k, sv);
             tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float a = __uint_as_float(sv[2 * c]) * sl2, b = __uint_as_float(sv[2 * c + 1]) * sl2;
-              mp[c & 3] = max3(mp[c & 3], 32 * k + 2 * c < nvalid ? a : -INFINITY,
-                               32 * k + 2 * c + 1 < nvalid ? b : -INFINITY);
-            }
+            for (int c = 0; c < 32; ++c) sv[c] = k + c < nvalid ? sv[c] : __float_as_uint(masked);
+            tmem_st16(t_s + k, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
+            tmem_st16(t_s + k + 16, *reinterpret_cast<uint32_t(*)[16]>(&sv[16]));
+          }
+          tmem_st_wait();
+        }
+        // Row max of the first `cols` columns (log2 domain), from S in TMEM.
+        auto max_of = [&](int cols) -> float {
+          float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int k = 0; k < cols; k += 32) {
+            uint32_t sv[32];
+            tmem_ld32(t_s + k, sv);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              mp[c & 3] = max3(mp[c & 3], __uint_as_float(sv[2 * c]) * sl2, __uint_as_float(sv[2 * c + 1]) * sl2);
           }
           return fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]);
         };
-        // A row's first tile with a visible key: its max, to start the offset m.
+        // A row's first tile with a visible key: the max of its first 32 scores starts the
+        // offset m; should a later one exceed it by 2^8, the raise below catches it.
         if (__any_sync(0xffffffffu, m == -INFINITY && nvalid > 0)) {
-          const float mxs = tile_max();
+          const float mxs = max_of(32);
           if (m == -INFINITY && nvalid > 0) m = mxs;
         }
         float alpha = 1.f;
         uint64_t sp[4];
         uint32_t pk[BN / 32][16];
-        auto pass = [&](auto full_tag) {
-          constexpr bool kFull = decltype(full_tag)::value;
-          const uint64_t sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(-m, -m);
+        // a row that has seen no key yet: any finite offset makes its P zeros
+        const float off = m == -INFINITY ? 0.f : m;
+        float neg = -off;
+        for (;;) {
+          const uint64_t sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(neg, neg);
 #pragma unroll
           for (int k = 0; k < 4; ++k) sp[k] = f2_pack(0.f, 0.f);
 #pragma unroll
@@ -721,35 +762,27 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
             for (int c = 0; c < 16; ++c) {
               const float2 xx = f2_unpack(ffma2(f2_pack(__uint_as_float(sv[2 * c]), __uint_as_float(sv[2 * c + 1])),
                                                 sl2x2, negm2));
-              float p0 = ex2p(xx.x), p1 = ex2p(xx.y);
-              if constexpr (!kFull) {
-                p0 = 32 * k + 2 * c < nvalid ? p0 : 0.f;
-                p1 = 32 * k + 2 * c + 1 < nvalid ? p1 : 0.f;
-              }
+              const float p0 = ex2p(xx.x), p1 = ex2p(xx.y);
               sp[c & 3] = fadd2(sp[c & 3], f2_pack(p0, p1));
               pk[k][c] = pack2<kBF16>(p0, p1);
             }
           }
-        };
-        for (;;) {
-          if (full)
-            pass(std::true_type{});
-          else
-            pass(std::false_type{});
           // a row whose P sums to at most 2^8 has no entry above 2^8: nothing to raise
           const float2 s01 = f2_unpack(fadd2(fadd2(sp[0], sp[1]), fadd2(sp[2], sp[3])));
           if (!__any_sync(0xffffffffu, s01.x + s01.y > 256.0f)) break;
-          const float mxs = tile_max();
+          const float mxs = max_of(BN);
           const bool raise = nvalid > 0 && mxs > m + 8.0f;
           if (!__any_sync(0xffffffffu, raise)) break;
           if (raise) {
-            alpha = ex2p(m - mxs);
+            // a row without an earlier key has nothing to scale (and l is 0)
+            alpha = m == -INFINITY ? 0.f : ex2p(m - mxs);
             m = mxs;
+            neg = -mxs;
           }
           // S(j) was issued after P V(j-1): O is final for the tiles before this one. At the
           // item's first tile there is nothing to scale: the product will overwrite it.
           if (j > 0) {
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < kD; c0 += 32) {
               uint32_t o[32];
               tmem_ld32(t_o + c0, o);
