@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -344,53 +345,98 @@ def bwd_sbhd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, attn_scale,
     return dq, dk, dv
 
 
-def _same_device(q, *ts):
+# The rotary and shared-prefix entry points serve single decoding steps, where the kernels
+# take less time than the checks used to: these helpers keep a call's host side short.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device_index(q, ts):
+    """Index of q's CUDA device, which all of ``ts`` (None allowed) must share."""
+    i = q.get_device()
     for t in ts:
-        if t is not None and t.device != q.device:
-            raise ValueError("all tensors must be on one device")
+        if t is not None and t.get_device() != i:
+            raise ValueError("all tensors must be CUDA tensors on one device (there is no CPU path)")
+    if i < 0:
+        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
+    return i
 
 
-def _stream(t, stream):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream)
+def _call(fn, index, stream, args):
+    """fn(*args, stream) with device ``index`` current, on its current stream by default."""
+    if stream is None:
+        stream = _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, stream)
+    if rc != 0:
+        _check(rc)
 
 
-def _rope_outputs(q, k, q_out, k_out):
-    """Outputs of a rotation: new contiguous tensors, or the caller's after a check."""
-    outs = []
-    for x, y in ((q, q_out), (k, k_out)):
-        if x is None:
-            if y is not None:
-                raise ValueError("k_out without k")
-            outs.append(None)
-            continue
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        elif y.shape != x.shape or y.dtype != x.dtype or not y.is_contiguous():
-            raise ValueError("outputs must be contiguous, with the shape and dtype of their input")
-        outs.append(y)
-    return outs
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
-def _rope_check(q, k, inv_freq, ints, outs, dims):
-    for t in (q, k, inv_freq, *ints, *outs):
-        if t is not None and not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
-    _same_device(q, k, inv_freq, *ints, *outs)
-    if q.dtype not in _DTYPES or (k is not None and k.dtype != q.dtype):
+def _ints(ts, n):
+    for t in ts:
+        if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"cu_seqlens must be contiguous int32 vectors of batch + 1 = {n} values")
+
+
+def _rope_output(x, y):
+    """Output of a rotation: a new contiguous tensor, or the caller's after a check."""
+    if y is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if y.shape != x.shape or y.dtype != x.dtype or not y.is_contiguous():
+        raise ValueError("outputs must be contiguous, with the shape and dtype of their input")
+    return y
+
+
+def _rope(q, k, inv_freq, cu, cu_pad, start, interleaved, mscale, inverse, q_out, k_out, stream):
+    """Both layouts: ``cu_pad`` None is the sequence-major one."""
+    L = library()
+    index = _device_index(q, (k, inv_freq, cu, cu_pad, start, q_out, k_out))
+    code = _DTYPES.get(q.dtype)
+    if code is None or (k is not None and k.dtype != q.dtype):
         raise ValueError("q and k must share one dtype, float16 or bfloat16")
+    dims = 4 if cu_pad is None else 3
     for x in (q, k):
-        if x is not None and x.numel() and (x.dim() != dims or x.stride(-1) != 1):
-            raise ValueError("q and k must keep the elements of a head adjacent")
+        if x is not None and (x.dim() != dims or (x.stride(-1) != 1 and x.numel())):
+            raise ValueError(f"q and k must have {dims} dimensions and adjacent elements in a head")
     if k is not None and (k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]):
         raise ValueError("q and k must share tokens and head dim")
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 vector")
-    for t in ints:
-        if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()):
-            raise ValueError("cu_seqlens and start_positions must be contiguous int32 vectors")
-    cu, start = ints[0], ints[-1]
-    if cu.numel() < 2 or (start is not None and start.numel() != cu.numel() - 1):
-        raise ValueError("cu_seqlens must hold batch + 1 values, start_positions batch")
+    n = cu.numel()
+    if n < 2:
+        raise ValueError("cu_seqlens must hold batch + 1 values")
+    _ints((cu,) if cu_pad is None else (cu, cu_pad), n)
+    if start is not None:
+        _ints((start,), n - 1)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    y = _rope_output(q, q_out)
+    z = None if k is None else _rope_output(k, k_out)
+    qs = q.stride()
+    ks = qs if k is None else k.stride()
+    tail = (qs[-3], qs[-2], ks[-3], ks[-2], 1 if interleaved else 0, float(mscale), 1 if inverse else 0, code)
+    if cu_pad is None:
+        S, B, hq, d = q.shape
+        if B != n - 1:
+            raise ValueError("cu_seqlens must hold batch + 1 values")
+        for x in (q, k):
+            if x is not None and S > 1 and x.stride(0) != B * x.stride(1):
+                raise ValueError("rows i * batch + b must be evenly spaced")
+        _call(L.te_attn_rope_sbhd, index, stream,
+              (q.data_ptr(), _at(k), y.data_ptr(), _at(z), inv_freq.data_ptr(), inv_freq.numel(), cu.data_ptr(),
+               _at(start), B, S, hq, 0 if k is None else k.shape[2], d) + tail)
+    else:
+        T, hq, d = q.shape
+        _call(L.te_attn_rope_thd, index, stream,
+              (q.data_ptr(), _at(k), y.data_ptr(), _at(z), inv_freq.data_ptr(), inv_freq.numel(), cu.data_ptr(),
+               cu_pad.data_ptr(), _at(start), n - 1, T, hq, 0 if k is None else k.shape[1], d) + tail)
+    return y, z
 
 
 def rope(q, k, inv_freq, cu_seqlens, cu_seqlens_padded, start_positions=None, interleaved=False,
@@ -399,69 +445,59 @@ def rope(q, k, inv_freq, cu_seqlens, cu_seqlens_padded, start_positions=None, in
     (or ``k=None``); returns ``(q_out, k_out)``, contiguous. Inputs may be strided slices of a
     fused projection. ``inv_freq`` float64 ``[rot / 2]`` (see :func:`rope_frequencies`);
     ``inverse=True`` is the backward pass."""
-    L = library()
-    outs = _rope_outputs(q, k, q_out, k_out)
-    _rope_check(q, k, inv_freq, (cu_seqlens, cu_seqlens_padded, start_positions), outs, 3)
-    if cu_seqlens_padded.numel() != cu_seqlens.numel():
-        raise ValueError("cu_seqlens and cu_seqlens_padded must have one length")
-    T, hq, d = q.shape
-    hkv = 0 if k is None else k.shape[1]
-    ks = (0, 0) if k is None else (k.stride(0), k.stride(1))
-    with _on(q):
-        _check(L.te_attn_rope_thd(
-            _ptr(q), _ptr(k), _ptr(outs[0]), _ptr(outs[1]), _ptr(inv_freq), inv_freq.numel(),
-            _ptr(cu_seqlens), _ptr(cu_seqlens_padded), _ptr(start_positions), cu_seqlens.numel() - 1, T,
-            hq, hkv, d, q.stride(0), q.stride(1), ks[0], ks[1], 1 if interleaved else 0, float(mscale),
-            1 if inverse else 0, _DTYPES[q.dtype], _stream(q, stream)))
-    return outs[0], outs[1]
+    return _rope(q, k, inv_freq, cu_seqlens, cu_seqlens_padded, start_positions, interleaved, mscale, inverse,
+                 q_out, k_out, stream)
 
 
 def rope_sbhd(q, k, inv_freq, cu_seqlens, start_positions=None, interleaved=False, mscale=1.0,
               inverse=False, q_out=None, k_out=None, stream=None):
     """``te_attn_rope_sbhd``: the same on ``q [S, B, hq, d]`` and ``k [S, B, hkv, d]``, real
     lengths from ``cu_seqlens``."""
-    L = library()
-    outs = _rope_outputs(q, k, q_out, k_out)
-    _rope_check(q, k, inv_freq, (cu_seqlens, start_positions), outs, 4)
-    S, B, hq, d = q.shape
-    if cu_seqlens.numel() != B + 1:
-        raise ValueError("cu_seqlens must hold batch + 1 values")
-    hkv = 0 if k is None else k.shape[2]
-    for x in (q, k):
-        if x is not None and S > 1 and x.stride(0) != B * x.stride(1):
-            raise ValueError("rows i * batch + b must be evenly spaced")
-    ks = (0, 0) if k is None else (k.stride(1), k.stride(2))
-    with _on(q):
-        _check(L.te_attn_rope_sbhd(
-            _ptr(q), _ptr(k), _ptr(outs[0]), _ptr(outs[1]), _ptr(inv_freq), inv_freq.numel(),
-            _ptr(cu_seqlens), _ptr(start_positions), B, S, hq, hkv, d, q.stride(1), q.stride(2), ks[0],
-            ks[1], 1 if interleaved else 0, float(mscale), 1 if inverse else 0, _DTYPES[q.dtype],
-            _stream(q, stream)))
-    return outs[0], outs[1]
+    return _rope(q, k, inv_freq, cu_seqlens, None, start_positions, interleaved, mscale, inverse, q_out, k_out,
+                 stream)
 
 
+@functools.lru_cache(maxsize=512)
 def prefix_fwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d) -> int:
     return int(library().te_attn_prefix_fwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d))
 
 
+@functools.lru_cache(maxsize=512)
 def prefix_bwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d) -> int:
     return int(library().te_attn_prefix_bwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d))
 
 
-def _prefix_check(q, k, v, kp, vp, cus, prefix_len, others):
-    _need_cuda(q, k, v, kp, vp, *cus, prefix_len, *others)
-    _same_device(q, k, v, kp, vp, *cus, prefix_len, *others)
-    _cu(*cus)
-    if q.dtype not in _DTYPES or any(t.dtype != q.dtype for t in (k, v, kp, vp)):
+def _prefix_sizes(q, k, v, kp, vp, cus, prefix_len, out, lse, others):
+    """Checks what a forward and a backward share; returns (device index, dtype code, sizes)."""
+    given = (k, v, kp, vp, *cus, prefix_len, out, lse, *others)
+    index = _device_index(q, given)
+    for t in (q, *given):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous")
+    dtype = q.dtype
+    code = _DTYPES.get(dtype)
+    if code is None or k.dtype != dtype or v.dtype != dtype or kp.dtype != dtype or vp.dtype != dtype:
         raise ValueError("q, k, v, k_prefix, v_prefix must share one dtype, float16 or bfloat16")
     if q.dim() != 3 or k.dim() != 3 or kp.dim() != 3:
         raise ValueError("q, k, v, k_prefix, v_prefix must be [rows, heads, d]")
-    if v.shape != k.shape or vp.shape != kp.shape or k.shape[1:] != kp.shape[1:] or k.shape[2] != q.shape[2]:
+    tq, hq, d = q.shape
+    tk, hkv, dk = k.shape
+    rows, hp, dp = kp.shape
+    if v.shape != k.shape or vp.shape != kp.shape or hp != hkv or dk != d or dp != d:
         raise ValueError("k, v and k_prefix, v_prefix must share heads and head dim, and d with q")
-    if any(c.numel() != cus[0].numel() or c.dim() != 1 for c in cus):
-        raise ValueError("cu_seqlens tensors must all hold batch + 1 values")
+    n = cus[0].numel()
+    _ints(cus, n)
     if prefix_len is not None and (prefix_len.dtype != torch.int32 or prefix_len.numel() != 1):
         raise ValueError("prefix_len must be one int32")
+    if out is not None and (out.shape != q.shape or out.dtype != dtype):
+        raise ValueError("out must have the shape and dtype of q")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2]):
+        raise ValueError("lse must be float32 [T_q, hq]")
+    return index, code, (n - 1, tq, tk, rows, hq, hkv, d)
+
+
+def _workspace(given, size, device):
+    return torch.empty(max(size, 1), dtype=torch.uint8, device=device) if given is None else given
 
 
 def _like(x, y, name):
@@ -478,23 +514,18 @@ def prefix_fwd(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seql
     """``te_attn_prefix_fwd_thd``: attention over a prefix ``k_prefix, v_prefix [P, hkv, d]``
     that every sequence shares, then each sequence's own keys; returns ``(out [T_q, hq, d],
     lse [T_q, hq])``."""
-    L = library()
     cus = (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded)
-    _prefix_check(q, k, v, k_prefix, v_prefix, cus, prefix_len, (out, lse, workspace))
-    out = _like(q, out, "out")
+    index, code, sizes = _prefix_sizes(q, k, v, k_prefix, v_prefix, cus, prefix_len, out, lse, (workspace,))
+    if out is None:
+        out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or lse.shape != q.shape[:2]:
-        raise ValueError("lse must be float32 [T_q, hq]")
-    sizes = (cu_seqlens_q.numel() - 1, q.shape[0], k.shape[0], k_prefix.shape[0], q.shape[1], k.shape[1],
-             q.shape[2])
-    if workspace is None:
-        workspace = torch.empty(max(prefix_fwd_workspace_size(*sizes), 1), dtype=torch.uint8, device=q.device)
-    with _on(q):
-        _check(L.te_attn_prefix_fwd_thd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(k_prefix), _ptr(v_prefix), _ptr(out), _ptr(lse),
-            *(_ptr(c) for c in cus), _ptr(prefix_len), *sizes, float(attn_scale), _mask(mask_type),
-            _DTYPES[q.dtype], _ptr(workspace), workspace.numel(), _stream(q, stream)))
+        lse = torch.empty(sizes[1], sizes[4], dtype=torch.float32, device=q.device)
+    ws = _workspace(workspace, prefix_fwd_workspace_size(*sizes), q.device)
+    _call(library().te_attn_prefix_fwd_thd, index, stream,
+          (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), out.data_ptr(),
+           lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(), cu_seqlens_q_padded.data_ptr(),
+           cu_seqlens_kv_padded.data_ptr(), _at(prefix_len), *sizes, float(attn_scale), _mask(mask_type), code,
+           ws.data_ptr(), ws.numel()))
     return out, lse
 
 
@@ -503,25 +534,18 @@ def prefix_bwd(q, k, v, k_prefix, v_prefix, out, dout, lse, cu_seqlens_q, cu_seq
                mask_type="padding_causal_bottom_right", prefix_len=None, dq=None, dk=None, dv=None,
                dk_prefix=None, dv_prefix=None, workspace=None, stream=None):
     """``te_attn_prefix_bwd_thd``: returns ``(dq, dk, dv, dk_prefix, dv_prefix)``."""
-    L = library()
     cus = (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded)
-    _prefix_check(q, k, v, k_prefix, v_prefix, cus, prefix_len,
-                  (out, dout, lse, dq, dk, dv, dk_prefix, dv_prefix, workspace))
-    for t, name in ((out, "out"), (dout, "dout")):
-        _like(q, t, name)
-    if lse.dtype != torch.float32 or lse.shape != q.shape[:2]:
-        raise ValueError("lse must be float32 [T_q, hq]")
+    index, code, sizes = _prefix_sizes(q, k, v, k_prefix, v_prefix, cus, prefix_len, out, lse,
+                                       (dout, dq, dk, dv, dk_prefix, dv_prefix, workspace))
+    _like(q, dout, "dout")
     grads = (_like(q, dq, "dq"), _like(k, dk, "dk"), _like(v, dv, "dv"), _like(k_prefix, dk_prefix, "dk_prefix"),
              _like(v_prefix, dv_prefix, "dv_prefix"))
-    sizes = (cu_seqlens_q.numel() - 1, q.shape[0], k.shape[0], k_prefix.shape[0], q.shape[1], k.shape[1],
-             q.shape[2])
-    if workspace is None:
-        workspace = torch.empty(max(prefix_bwd_workspace_size(*sizes), 1), dtype=torch.uint8, device=q.device)
-    with _on(q):
-        _check(L.te_attn_prefix_bwd_thd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(k_prefix), _ptr(v_prefix), _ptr(out), _ptr(dout), _ptr(lse),
-            *(_ptr(g) for g in grads), *(_ptr(c) for c in cus), _ptr(prefix_len), *sizes, float(attn_scale),
-            _mask(mask_type), _DTYPES[q.dtype], _ptr(workspace), workspace.numel(), _stream(q, stream)))
+    ws = _workspace(workspace, prefix_bwd_workspace_size(*sizes), q.device)
+    _call(library().te_attn_prefix_bwd_thd, index, stream,
+          (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), out.data_ptr(),
+           dout.data_ptr(), lse.data_ptr(), *(g.data_ptr() for g in grads), cu_seqlens_q.data_ptr(),
+           cu_seqlens_kv.data_ptr(), cu_seqlens_q_padded.data_ptr(), cu_seqlens_kv_padded.data_ptr(),
+           _at(prefix_len), *sizes, float(attn_scale), _mask(mask_type), code, ws.data_ptr(), ws.numel()))
     return grads
 
 

@@ -38,6 +38,7 @@
 #include "attn_prefix.cuh"
 #include "common.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 #include "row_store.cuh"
 #include "sm103_ptx.cuh"
 #include "tmap.h"
@@ -129,6 +130,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* status = p.header + kHdrStatus;
   const int per_pair = p.hkv * S::kSplit;
+  // With a prefix this kernel is launched once every dQ block runs, i.e. has seen the lists
+  // and rows complete: it needs nothing of dQ, and takes SMs as dQ's blocks leave them.
+  if constexpr (is_prefix<P>) pdl_trigger();
   const int n_pairs = p.header[kHdrNumKPairs];
   // Items of the prefix come first: they are the longest.
   constexpr bool kPrefix = is_prefix<P>;
@@ -560,6 +564,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if constexpr (kPrefix) pdl_wait();  // complete only after dQ, for what follows in the stream
 }
 
 // ===========================================================================
@@ -625,6 +630,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* status = p.header + kHdrStatus;
+  if constexpr (is_prefix<P>) {
+    pdl_wait();
+    pdl_trigger();
+  }
   const int n_pairs = p.header[kHdrNumQPairs];
   const int n_items = n_pairs * virtual_heads(p);
   const bool causal = p.causal != 0;
@@ -1036,9 +1045,8 @@ static cudaError_t launch_prefix_dkdv_impl(PrefixBwd p, int num_sms, cudaStream_
   const long long max_items =
       (static_cast<long long>(p.pair_cap_k) + static_cast<long long>(p.prefix_rows / kBlockN + 1) * p.splits) *
       p.hkv * S::kSplit;
-  kern<<<static_cast<int>(max_items < num_sms ? max_items : num_sms), kBwdThreads, S::kSmemBytes, st>>>(p, tq, tdo, tk,
-                                                                                                  tv);
-  return cudaGetLastError();
+  return launch_dependent(kern, static_cast<unsigned>(max_items < num_sms ? max_items : num_sms), kBwdThreads,
+                          S::kSmemBytes, st, p, tq, tdo, tk, tv);
 }
 
 template <int kD, bool kBF16>
@@ -1050,9 +1058,8 @@ static cudaError_t launch_prefix_dq_impl(PrefixBwd p, int num_sms, cudaStream_t 
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const long long max_items = static_cast<long long>(p.pair_cap_q) * p.vheads;
-  kern<<<static_cast<int>(max_items < num_sms ? max_items : num_sms), kBwdThreads, S::kSmemBytes, st>>>(p, tq, tdo, tk,
-                                                                                                  tv);
-  return cudaGetLastError();
+  return launch_dependent(kern, static_cast<unsigned>(max_items < num_sms ? max_items : num_sms), kBwdThreads,
+                          S::kSmemBytes, st, p, tq, tdo, tk, tv);
 }
 
 cudaError_t launch_prefix_bwd_dkdv(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st) {

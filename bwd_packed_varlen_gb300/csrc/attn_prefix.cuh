@@ -31,6 +31,54 @@ struct PrefixParams : AttnParams {
   int cap_longs, cap_entries, cap_rows;
 };
 
+struct Scan3 {
+  int x, y, z;     // exclusive sums before this thread
+  int tx, ty, tz;  // totals
+};
+
+// Exclusive scan of three counters over the block (two barriers). `buf`: 3 x 32 ints.
+__device__ __forceinline__ Scan3 block_scan3(int x, int y, int z, int (*buf)[32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int ix = x, iy = y, iz = z;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int ux = __shfl_up_sync(0xffffffffu, ix, o), uy = __shfl_up_sync(0xffffffffu, iy, o);
+    const int uz = __shfl_up_sync(0xffffffffu, iz, o);
+    if (lane >= o) {
+      ix += ux;
+      iy += uy;
+      iz += uz;
+    }
+  }
+  if (lane == 31) {
+    buf[0][warp] = ix;
+    buf[1][warp] = iy;
+    buf[2][warp] = iz;
+  }
+  __syncthreads();
+  // every warp sums the warps' totals itself: lane w holds warp w's
+  const int wx = lane < nw ? buf[0][lane] : 0, wy = lane < nw ? buf[1][lane] : 0, wz = lane < nw ? buf[2][lane] : 0;
+  __syncthreads();
+  Scan3 r;
+  r.tx = __reduce_add_sync(0xffffffffu, wx);
+  r.ty = __reduce_add_sync(0xffffffffu, wy);
+  r.tz = __reduce_add_sync(0xffffffffu, wz);
+  r.x = __reduce_add_sync(0xffffffffu, lane < warp ? wx : 0) + ix - x;
+  r.y = __reduce_add_sync(0xffffffffu, lane < warp ? wy : 0) + iy - y;
+  r.z = __reduce_add_sync(0xffffffffu, lane < warp ? wz : 0) + iz - z;
+  return r;
+}
+
+// locate_row() among offsets copied to shared memory, where they fit: each step of the
+// search would otherwise be a trip to L2. Every thread of the block calls cache_offsets().
+constexpr int kCachedOffsets = 2048;
+__device__ __forceinline__ const int* cache_offsets(const int* cu_pad, int batch, int* shared) {
+  if (batch >= kCachedOffsets) return cu_pad;
+  for (int k = threadIdx.x; k <= batch; k += blockDim.x) shared[k] = cu_pad[k];
+  __syncthreads();
+  return shared;
+}
+
 // Real prefix keys; a length outside [0, prefix_rows] counts as 0 (and is reported).
 __device__ __forceinline__ int prefix_keys(const PrefixParams& p) {
   if (!p.prefix_len) return p.prefix_rows;
@@ -124,7 +172,7 @@ __device__ __forceinline__ int virtual_group(const P& p) {
   if constexpr (is_prefix<P>) return p.vgroup;
   else return p.group;
 }
-// Prefix keys (0 without a prefix).
+// Prefix keys (0 for problems without a prefix).
 template <class P>
 __device__ __forceinline__ int prefix_keys_of(const P& p) {
   if constexpr (is_prefix<P>) return prefix_keys(p);
@@ -152,9 +200,8 @@ __device__ __forceinline__ size_t packed_index(const P& p, int b, int r, int vh)
   }
 }
 
-cudaError_t launch_prefix_bwd_schedule(const PrefixBwd& p, int* pref_q, int* pref_k, int* pref_f, cudaStream_t st);
-cudaError_t launch_prefix_bwd_zero_fill(const PrefixBwd& p, int num_sms, cudaStream_t st);
-cudaError_t launch_prefix_delta(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st);
+cudaError_t launch_prefix_bwd_schedule(const PrefixBwd& p, int* pref_q, cudaStream_t st);
+cudaError_t launch_prefix_prep(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st);
 cudaError_t launch_prefix_bwd_dq(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st);
 cudaError_t launch_prefix_bwd_dkdv(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st);
 cudaError_t launch_prefix_sum(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st);

@@ -1,11 +1,193 @@
-// Shared-prefix attention, backward: the sum of the prefix gradients' parts. The dQ and
-// dK/dV kernels are the packed problem's, with the prefix as further key tiles.
+// Shared-prefix attention, backward: the lists of row and key tiles, what the tiles need
+// of every row (and the rows no tile writes), and the sum of the prefix gradients' parts.
+// The dQ and dK/dV kernels between them are the packed problem's, with the prefix as
+// further key tiles.
 #include <cuda_runtime.h>
 
 #include "attn_prefix.cuh"
+#include "pdl.cuh"
 #include "sm103_ptx.cuh"
 
 namespace teattn {
+
+// ---------------------------------------------------------------------------
+// Lists of (sequence, row tile) and (sequence, key tile) in natural order. With a prefix
+// every row tile costs about the same, and the prefix's own dK/dV items, the longest, go
+// first by themselves, so the packed problem's sort by cost would only delay the start.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(1024) prefix_bwd_schedule_kernel(const __grid_constant__ PrefixBwd p, int* pref_q) {
+  pdl_trigger();
+  __shared__ int buf[3][32];
+  __shared__ int bad;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) bad = p.prefix_len && (*p.prefix_len < 0 || *p.prefix_len > p.prefix_rows) ? 1 : 0;
+  const bool prefix = prefix_keys(p) > 0;
+  __syncthreads();
+  int n_q = 0, n_k = 0;
+  for (int base = 0; base < p.batch; base += blockDim.x) {
+    const int b = base + threadIdx.x;
+    int cq = 0, ck = 0;
+    if (b < p.batch) {
+      const SeqInfo s = load_seq(p, b);
+      if (!s.ok) bad = 1;
+      if (s.len_q > 0) {
+        if (prefix || s.len_k > 0) cq = ((s.len_q << p.pack_shift) + kBlockM - 1) / kBlockM;
+        ck = (seen_keys(s, p.causal != 0) + kBlockN - 1) / kBlockN;
+      }
+    }
+    const Scan3 at = block_scan3(cq, ck, 0, buf);
+    if (b < p.batch) pref_q[b] = n_q + at.x;
+    // a warp writes its 32 sequences' tiles together
+    for (int l = 0; l < 32; ++l) {
+      const int seq = __shfl_sync(0xffffffffu, b, l);
+      const int q0 = n_q + __shfl_sync(0xffffffffu, at.x, l), nq = __shfl_sync(0xffffffffu, cq, l);
+      const int k0 = n_k + __shfl_sync(0xffffffffu, at.y, l), nk = __shfl_sync(0xffffffffu, ck, l);
+      for (int t = lane; t < nq; t += 32)
+        if (q0 + t < p.pair_cap_q) p.q_pairs[q0 + t] = make_int2(seq, t);
+      for (int t = lane; t < nk; t += 32)
+        if (k0 + t < p.pair_cap_k) p.k_pairs[k0 + t] = make_int2(seq, t);
+    }
+    n_q += at.tx;
+    n_k += at.ty;
+  }
+  if (threadIdx.x == 0) {
+    // overlapping sequences can have more tiles than the lists hold: none is computed
+    const bool over = n_q > p.pair_cap_q || n_k > p.pair_cap_k;
+    pref_q[p.batch] = n_q;
+    p.header[kHdrStatus] = bad || over ? kStatusBadSeqlens : 0;
+    p.header[kHdrNumQPairs] = over ? 0 : n_q;
+    p.header[kHdrNumKPairs] = over ? 0 : n_k;
+    p.header[kHdrNextDkdv] = 0;
+    p.header[kHdrNextDq] = 0;
+  }
+}
+
+cudaError_t launch_prefix_bwd_schedule(const PrefixBwd& p, int* pref_q, cudaStream_t st) {
+  const int threads = p.batch >= 1024 ? 1024 : (p.batch + 31) / 32 * 32;
+  prefix_bwd_schedule_kernel<<<1, threads, 0, st>>>(p, pref_q);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Every query row: -lse log2(e) and -D = -rowsum(dO O) for the tiles that read it, both by
+// (sequence, row tile) and by tensor row (rows that are no token: -infinity, which makes
+// their P zero); dq of rows no tile writes. Every own key row that no query sees: zeros.
+// One warp per row, 16-byte loads, four groups in flight; memory-bound.
+// ---------------------------------------------------------------------------
+template <bool kBF16>
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = unpack2<kBF16>(x[i]), v = unpack2<kBF16>(y[i]);
+    s = fmaf(u.x, v.x, s);
+    s = fmaf(u.y, v.y, s);
+  }
+  return s;
+}
+
+__device__ __forceinline__ void zero_rows(void* base, size_t row, int bytes) {
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<char*>(base) + row * bytes);
+  for (int i = threadIdx.x & 31; i < bytes / 16; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+}
+
+template <bool kBF16>
+__global__ void __launch_bounds__(256) prefix_prep_kernel(const __grid_constant__ PrefixBwd p) {
+  __shared__ int s_q[kCachedOffsets], s_k[kCachedOffsets];
+  const int* q_pad = cache_offsets(p.cu_q_pad, p.batch, s_q);
+  const int* k_pad = cache_offsets(p.cu_kv_pad, p.batch, s_k);
+  const long long warps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+  const long long gw = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31, sh = p.pack_shift, mask = (1 << sh) - 1;
+  const bool causal = p.causal != 0, prefix = prefix_keys(p) > 0;
+  constexpr float kLog2e = 1.4426950408889634f;
+  const int cpr = p.d / 8;  // 16-byte chunks per head
+  const int chunks = p.hq * cpr;
+  pdl_trigger();
+  pdl_wait();  // pref_q and the header
+  // more tiles than the lists hold (overlapping sequences): no row is a token
+  const bool none = p.header[kHdrNumQPairs] != p.pref_q[p.batch];
+  // linear rows past the tensor's last one
+  const long long first = static_cast<long long>(p.total_q) << sh, pad = p.rows_lin - first;
+  for (long long z = gw * 32 + lane; z < pad * p.vheads; z += warps * 32) {
+    const size_t at = static_cast<size_t>(z / pad) * p.rows_lin + first + z % pad;
+    p.lse_lin[at] = -INFINITY;
+    p.delta_lin[at] = 0.f;
+  }
+  for (long long r = gw; r < p.total_q; r += warps) {
+    int i = 0;
+    const int b = none ? -1 : locate_row(p, q_pad, static_cast<int>(r), &i);
+    SeqInfo s{};
+    if (b >= 0) s = load_seq(p, b);
+    const size_t row = static_cast<size_t>(r);
+    auto linear = [&](int h) { return static_cast<size_t>(h >> sh) * p.rows_lin + (row << sh) + (h & mask); };
+    const bool real = b >= 0 && i < s.len_q;
+    // rows that see no key: their tiles leave dq to this kernel
+    if (!real || (!prefix && row_keys(s, i, causal) == 0)) zero_rows(p.dq, row, p.hq * p.d * 2);
+    if (!real || (!prefix && s.len_k == 0)) {
+      for (int h = lane; h < p.hq; h += 32) {
+        p.lse_lin[linear(h)] = -INFINITY;
+        p.delta_lin[linear(h)] = 0.f;
+      }
+      continue;
+    }
+    // index of head h in the tiles
+    const size_t t0 = packed_index(p, b, i << sh, 0);
+    auto tiled = [&](int h) { return t0 + static_cast<size_t>(h >> sh) * kBlockM + (h & mask); };
+    if (!bounds_ok(tiled(p.hq - 1) < static_cast<size_t>(p.pair_cap_q) * p.vheads * kBlockM, p.header + kHdrStatus))
+      continue;
+    auto put = [&](int h, float v) { p.delta_t[tiled(h)] = p.delta_lin[linear(h)] = v; };
+    for (int h = lane; h < p.hq; h += 32)
+      p.lse_t[tiled(h)] = p.lse_lin[linear(h)] = -(p.lse_in[row * p.hq + h] * kLog2e);
+    const uint4* o = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.out_in) + row * p.hq * p.d);
+    const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dout) + row * p.hq * p.d);
+    if (32 % cpr == 0) {
+      // the lanes of a head are neighbours and add up by shuffles
+      for (int c0 = 0; c0 < chunks; c0 += 128) {
+        uint4 oa[4], ga[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int c = c0 + 32 * u + lane;
+          if (c < chunks) {
+            oa[u] = o[c];
+            ga[u] = g[c];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int c = c0 + 32 * u + lane;
+          float v = c < chunks ? dot8<kBF16>(oa[u], ga[u]) : 0.f;
+          for (int w = cpr >> 1; w > 0; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
+          if (c < chunks && (c % cpr) == 0) put(c / cpr, -v);
+        }
+      }
+    } else {
+      for (int h = lane; h < p.hq; h += 32) {
+        float v = 0.f;
+        for (int c = 0; c < cpr; ++c) v += dot8<kBF16>(o[h * cpr + c], g[h * cpr + c]);
+        put(h, -v);
+      }
+    }
+  }
+  for (long long r = gw; r < p.total_kv; r += warps) {
+    int j = 0;
+    const int b = none ? -1 : locate_row(p, k_pad, static_cast<int>(r), &j);
+    SeqInfo s{};
+    if (b >= 0) s = load_seq(p, b);
+    if (b >= 0 && j < seen_keys(s, causal)) continue;  // its tile writes it
+    zero_rows(p.dk, static_cast<size_t>(r), p.hkv * p.d * 2);
+    zero_rows(p.dv, static_cast<size_t>(r), p.hkv * p.d * 2);
+  }
+}
+
+cudaError_t launch_prefix_prep(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st) {
+  const long long rows = static_cast<long long>(p.total_q) > p.total_kv ? p.total_q : p.total_kv;
+  const long long want = (rows + 7) / 8;
+  if (want == 0) return cudaSuccess;
+  const unsigned grid = static_cast<unsigned>(want < num_sms * 8 ? want : num_sms * 8);
+  return launch_dependent(bf16 ? prefix_prep_kernel<true> : prefix_prep_kernel<false>, grid, 256, 0, st, p);
+}
 
 // dK_prefix = scale sum_s part_dk[s], dV_prefix = sum_s part_dv[s] in the order of s, in
 // fp32, rounded once; rows that no query sees (behind the real length, or without any
@@ -13,6 +195,7 @@ namespace teattn {
 // bound: every fp32 part is read once, 32 bytes per thread and part.
 template <bool kBF16>
 __global__ void __launch_bounds__(256) prefix_sum_kernel(const __grid_constant__ PrefixBwd p) {
+  pdl_wait();
   const int seen = p.total_q > 0 ? prefix_keys(p) : 0;
   const size_t row_elems = static_cast<size_t>(p.hkv) * p.d;
   const size_t n = static_cast<size_t>(p.prefix_rows) * row_elems;
@@ -46,9 +229,8 @@ cudaError_t launch_prefix_sum(const PrefixBwd& p, bool bf16, int num_sms, cudaSt
   const long long blocks = (static_cast<long long>(p.prefix_rows) * p.hkv * p.d / 8 + 255) / 256;
   if (blocks == 0) return cudaSuccess;
   const int grid = static_cast<int>(blocks < num_sms * 8 ? blocks : num_sms * 8);
-  if (bf16) prefix_sum_kernel<true><<<grid, 256, 0, st>>>(p);
-  else prefix_sum_kernel<false><<<grid, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(bf16 ? prefix_sum_kernel<true> : prefix_sum_kernel<false>, static_cast<unsigned>(grid), 256,
+                          0, st, p);
 }
 
 }  // namespace teattn

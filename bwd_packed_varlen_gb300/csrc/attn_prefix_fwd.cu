@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "attn_prefix.cuh"
+#include "pdl.cuh"
 #include "row_store.cuh"
 #include "sm103_ptx.cuh"
 #include "tmap.h"
@@ -46,45 +47,6 @@ namespace teattn {
 // lengths only.
 // ---------------------------------------------------------------------------
 constexpr int kPrefixSchedThreads = 1024;
-
-struct Scan3 {
-  int x, y, z;     // exclusive sums before this thread
-  int tx, ty, tz;  // totals
-};
-
-// Exclusive scan of three counters over the block. `buf`: 3 x 32 ints.
-__device__ __forceinline__ Scan3 block_scan3(int x, int y, int z, int (*buf)[32]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int ix = x, iy = y, iz = z;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int ux = __shfl_up_sync(0xffffffffu, ix, o), uy = __shfl_up_sync(0xffffffffu, iy, o);
-    const int uz = __shfl_up_sync(0xffffffffu, iz, o);
-    if (lane >= o) {
-      ix += ux;
-      iy += uy;
-      iz += uz;
-    }
-  }
-  if (lane == 31) {
-    buf[0][warp] = ix;
-    buf[1][warp] = iy;
-    buf[2][warp] = iz;
-  }
-  __syncthreads();
-  // every warp sums the warps' totals itself: lane w holds warp w's
-  int wx = lane < nw ? buf[0][lane] : 0, wy = lane < nw ? buf[1][lane] : 0, wz = lane < nw ? buf[2][lane] : 0;
-  __syncthreads();
-  const int bx = lane < warp ? wx : 0, by = lane < warp ? wy : 0, bz = lane < warp ? wz : 0;
-  Scan3 r;
-  r.tx = __reduce_add_sync(0xffffffffu, wx);
-  r.ty = __reduce_add_sync(0xffffffffu, wy);
-  r.tz = __reduce_add_sync(0xffffffffu, wz);
-  r.x = __reduce_add_sync(0xffffffffu, bx) + ix - x;
-  r.y = __reduce_add_sync(0xffffffffu, by) + iy - y;
-  r.z = __reduce_add_sync(0xffffffffu, bz) + iz - z;
-  return r;
-}
 
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
@@ -101,6 +63,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
   __shared__ int buf[3][32];
   __shared__ int bad;
   __shared__ unsigned long long work, tokens;
+  pdl_trigger();
   const int rt = prefix_row_tile(p.d), bn = prefix_key_tile(p.d), tid = threadIdx.x, lane = tid & 31;
   const int most_ways = rt / 128;
   if (tid == 0) {
@@ -387,6 +350,8 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  pdl_trigger();
+  pdl_wait();  // the scheduler's lists
 
   if (warp == kWarpItem) {
     // ------------------------------------------------------------- items and Q rows
@@ -878,8 +843,8 @@ static cudaError_t launch_fwd_impl(const PrefixParams& p, int num_sms, cudaStrea
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const long long most = static_cast<long long>(p.cap_entries) * p.hkv;
-  kern<<<static_cast<int>(most < num_sms ? most : num_sms), S::kThreads, S::kSmemBytes, st>>>(p, tk, tv, tkp, tvp);
-  return cudaGetLastError();
+  return launch_dependent(kern, static_cast<unsigned>(most < num_sms ? most : num_sms), S::kThreads, S::kSmemBytes, st,
+                          p, tk, tv, tkp, tvp);
 }
 
 cudaError_t launch_prefix_fwd(const PrefixParams& p, bool bf16, int num_sms, cudaStream_t st) {
@@ -911,27 +876,17 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
   const int t = any ? static_cast<int>(w / slices) : 0, slice = any ? static_cast<int>(w % slices) : 0;
   const int h0 = static_cast<int>(static_cast<long long>(p.hq) * slice / slices);
   const int h1 = any ? static_cast<int>(static_cast<long long>(p.hq) * (slice + 1) / slices) : h0;
-  // the token's sequence: a search among offsets in shared memory, where they fit (each
-  // step of it would otherwise be a trip to L2)
-  constexpr int kCached = 2047;
-  __shared__ int s_pad[kCached + 1];
+  __shared__ int s_pad[kCachedOffsets];
   const int rt = prefix_row_tile(p.d);
+  int i = 0;
+  const int b = locate_row(p, cache_offsets(p.cu_q_pad, p.batch, s_pad), t, &i);
+  SeqInfo s{};
+  if (b >= 0) s = load_seq(p, b);
+  pdl_wait();  // the main kernel's results, and the scheduler's
   const int pre_chunks = p.header[kHdrPrefixChunks], pre_slot = p.header[kHdrPrefixSlot];
   const int pre_rows = p.header[kHdrPrefixRows];
-  int i = 0, b;
-  if (p.batch <= kCached) {
-    for (int k = threadIdx.x; k <= p.batch; k += 256) s_pad[k] = p.cu_q_pad[k];
-    __syncthreads();
-    b = locate_row(p, s_pad, t, &i);
-  } else {
-    b = locate_row(p, p.cu_q_pad, t, &i);
-  }
-  SeqInfo s{};
   int4 info = make_int4(-1, -1, 0, 0);
-  if (b >= 0) {
-    s = load_seq(p, b);
-    info = p.seqs[b];
-  }
+  if (b >= 0) info = p.seqs[b];
   // -1 chunks: the lengths allow no result
   const bool real = b >= 0 && i < s.len_q && pre_chunks >= 0;
   if (kWarps == 1 && real && info.x < 0) {
@@ -1050,16 +1005,16 @@ static cudaError_t launch_join_impl(const PrefixParams& p, int num_sms, cudaStre
   const long long rows = static_cast<long long>(p.total_q) * p.hq, few = static_cast<long long>(num_sms) * 16;
   auto blocks = [](long long warps) { return static_cast<unsigned>((warps + 7) / 8); };
   if (rows * 4 <= few) {
-    prefix_join_kernel<kBF16, 8><<<blocks(rows * 8), 256, 0, st>>>(p, p.hq);
+    return launch_dependent(prefix_join_kernel<kBF16, 8>, blocks(rows * 8), 256, 0, st, p, p.hq);
   } else if (rows <= few) {
-    prefix_join_kernel<kBF16, 4><<<blocks(rows * 4), 256, 0, st>>>(p, p.hq);
+    return launch_dependent(prefix_join_kernel<kBF16, 4>, blocks(rows * 4), 256, 0, st, p, p.hq);
   } else {
     // one warp per row while that fills the GPU about twice over, several heads beyond it
     const long long want = (4 * few + p.total_q - 1) / p.total_q;
     const int slices = static_cast<int>(want < p.hq ? want : p.hq);
-    prefix_join_kernel<kBF16, 1><<<blocks(static_cast<long long>(p.total_q) * slices), 256, 0, st>>>(p, slices);
+    return launch_dependent(prefix_join_kernel<kBF16, 1>, blocks(static_cast<long long>(p.total_q) * slices), 256, 0,
+                            st, p, slices);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_prefix_join(const PrefixParams& p, bool bf16, int num_sms, cudaStream_t st) {

@@ -9,7 +9,6 @@
 #include <algorithm>
 #include <cmath>
 
-#include "attn_prefix.cuh"
 #include "common.cuh"
 #include "launch.h"
 
@@ -76,17 +75,15 @@ __device__ __forceinline__ int find_seq(const int* pref, int B, int i) {
   return lo;
 }
 
-template <class P>
-__device__ int q_pair_cost(const P& p, int b, int t) {
+__device__ int q_pair_cost(const AttnParams& p, int b, int t) {
   SeqInfo s = load_seq(p, b);
-  return (tile_keys(p, s, t, p.causal) + kBlockN - 1) / kBlockN;
+  return (visible_keys(s, t, p.causal) + kBlockN - 1) / kBlockN;
 }
 
-template <class P>
-__device__ int k_pair_cost(const P& p, int b, int t) {
+__device__ int k_pair_cost(const AttnParams& p, int b, int t) {
   SeqInfo s = load_seq(p, b);
-  int nq = ((s.len_q << pack_shift(p)) + kBlockM - 1) / kBlockM;
-  return nq - (first_query(s, t * kBlockN, p.causal) << pack_shift(p)) / kBlockM;
+  int nq = (s.len_q + kBlockM - 1) / kBlockM;
+  return nq - first_query(s, t * kBlockN, p.causal) / kBlockM;
 }
 
 // Forward item of two query tiles: both tiles' key tiles (the second sees most).
@@ -151,8 +148,8 @@ __device__ void build_chain_list(const AttnParams& p, const int* pref, int n, in
 // a list of n <= kSortCap pairs runs in three phases, each over the threads
 // [t, t + nt): the keys (cost descending, then list position) padded to a power of
 // two m, the bitonic stages (k, j), and the sorted pairs written out.
-template <int kKind, class P>
-__device__ void list_keys(const P& p, const int* pref, int n, int m, uint64_t* keys, int t,
+template <int kKind>
+__device__ void list_keys(const AttnParams& p, const int* pref, int n, int m, uint64_t* keys, int t,
                           int nt) {
   for (int i = t; i < m; i += nt) {
     uint64_t key = ~0ull;
@@ -197,8 +194,8 @@ __device__ __forceinline__ int pow2_at_least(int n) {
   return m;
 }
 
-template <int kKind, class P>
-__device__ void build_list(const P& p, const int* pref, int n, int2* out,
+template <int kKind>
+__device__ void build_list(const AttnParams& p, const int* pref, int n, int2* out,
                            uint64_t* keys) {
   if (n <= kSortCap) {
     const int m = pow2_at_least(n);
@@ -223,8 +220,7 @@ __device__ void build_list(const P& p, const int* pref, int n, int2* out,
 // The backward's query-tile and key-tile lists, sorted side by side: half of the
 // threads each, one block-wide barrier per stage of the longer list (the shorter
 // list's stages are a prefix of it), so the two sorts cost about one.
-template <class P>
-__device__ void build_q_k_lists(const P& p, const int* pref_q, int nq, const int* pref_k, int nk,
+__device__ void build_q_k_lists(const AttnParams& p, const int* pref_q, int nq, const int* pref_k, int nk,
                                 uint64_t* keys) {
   const int half = blockDim.x / 2;
   const bool first = threadIdx.x < half;
@@ -255,19 +251,12 @@ __device__ void build_q_k_lists(const P& p, const int* pref_q, int nq, const int
   __syncthreads();
 }
 
-template <class P>
-__global__ void __launch_bounds__(kSchedThreads) schedule_kernel(const __grid_constant__ P p, int* pref_q,
+__global__ void __launch_bounds__(kSchedThreads) schedule_kernel(AttnParams p, int* pref_q,
                                                                   int* pref_k, int* pref_f) {
   extern __shared__ uint64_t sort_keys[];
   __shared__ int warp_sums[32];
   __shared__ int bad;
-  // with a prefix every query sees a key, whatever its own sequence holds
-  const bool prefix = prefix_keys_of(p) > 0;
-  if (threadIdx.x == 0) {
-    bad = 0;
-    if constexpr (is_prefix<P>)
-      if (p.prefix_len && (*p.prefix_len < 0 || *p.prefix_len > p.prefix_rows)) bad = 1;
-  }
+  if (threadIdx.x == 0) bad = 0;
   __syncthreads();
   int carry_q = 0, carry_k = 0, carry_f = 0;
   for (int base = 0; base < p.batch; base += blockDim.x) {
@@ -276,8 +265,8 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(const __grid_co
     if (b < p.batch) {
       SeqInfo s = load_seq(p, b);
       if (!s.ok) bad = 1;
-      if (s.len_q > 0 && (s.len_k > 0 || prefix)) {
-        cq = ((s.len_q << pack_shift(p)) + kBlockM - 1) / kBlockM;
+      if (s.len_q > 0 && s.len_k > 0) {
+        cq = (s.len_q + kBlockM - 1) / kBlockM;
         ck = (seen_keys(s, p.causal) + kBlockN - 1) / kBlockN;
         cf = (s.len_q + kBlockF - 1) / kBlockF;
       }
@@ -349,21 +338,11 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(const __grid_co
 cudaError_t launch_schedule(const AttnParams& p, int* pref_q, int* pref_k, int* pref_f,
                             cudaStream_t st) {
   const size_t smem = 2 * kSortCap * sizeof(uint64_t);  // two lists sorted side by side
-  cudaError_t e = cudaFuncSetAttribute(schedule_kernel<AttnParams>,
+  cudaError_t e = cudaFuncSetAttribute(schedule_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  schedule_kernel<AttnParams><<<1, kSchedThreads, smem, st>>>(p, pref_q, pref_k, pref_f);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_prefix_bwd_schedule(const PrefixBwd& p, int* pref_q, int* pref_k, int* pref_f,
-                                       cudaStream_t st) {
-  const size_t smem = 2 * kSortCap * sizeof(uint64_t);
-  cudaError_t e = cudaFuncSetAttribute(schedule_kernel<PrefixBwd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  schedule_kernel<PrefixBwd><<<1, kSchedThreads, smem, st>>>(p, pref_q, pref_k, pref_f);
+  schedule_kernel<<<1, kSchedThreads, smem, st>>>(p, pref_q, pref_k, pref_f);
   return cudaGetLastError();
 }
 
@@ -384,8 +363,7 @@ __device__ __forceinline__ void zero_row(void* base, long long r, int row_bytes)
 }
 
 // mode 0: forward (out, lse); mode 1: backward (dq, dk, dv)
-template <class P>
-__global__ void __launch_bounds__(256) zero_fill_kernel(const __grid_constant__ P p, int mode) {
+__global__ void __launch_bounds__(256) zero_fill_kernel(AttnParams p, int mode) {
   const int b = blockIdx.x;
   const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
   const int w0 = blockIdx.y * nw + (threadIdx.x >> 5), wstep = nw * gridDim.y;
@@ -412,9 +390,7 @@ __global__ void __launch_bounds__(256) zero_fill_kernel(const __grid_constant__ 
     const long long qbase = p.sbhd ? b : p.cu_q_pad[b];
     const int qn = min(max(p.sbhd ? p.total_q / p.batch : p.cu_q_pad[b + 1] - p.cu_q_pad[b], 0), p.total_q);
     const int stride = p.sbhd ? p.batch : 1;
-    const int dead = prefix_keys_of(p) > 0 ? 0
-                     : s.len_k == 0 ? s.len_q
-                                    : (causal ? min(s.len_q, max(0, -s.diag)) : 0);
+    const int dead = s.len_k == 0 ? s.len_q : (causal ? min(s.len_q, max(0, -s.diag)) : 0);
     const int nq = dead + max(0, qn - s.len_q);
     for (int z = w0; z < nq; z += wstep) {
       const int i = z < dead ? z : s.len_q + (z - dead);
@@ -451,14 +427,7 @@ cudaError_t launch_zero_fill(const AttnParams& p, int mode, int num_sms, cudaStr
   // so that about four blocks per SM share the rows of few long sequences
   const int nb = p.batch + 1;
   const int y = std::max(1, std::min(65535, (num_sms * 4 + nb - 1) / nb));
-  zero_fill_kernel<AttnParams><<<dim3(nb, y), 256, 0, st>>>(p, mode);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_prefix_bwd_zero_fill(const PrefixBwd& p, int num_sms, cudaStream_t st) {
-  const int nb = p.batch + 1;
-  const int y = std::max(1, std::min(65535, (num_sms * 4 + nb - 1) / nb));
-  zero_fill_kernel<PrefixBwd><<<dim3(nb, y), 256, 0, st>>>(p, 1);
+  zero_fill_kernel<<<dim3(nb, y), 256, 0, st>>>(p, mode);
   return cudaGetLastError();
 }
 
@@ -481,67 +450,28 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   return s;
 }
 
-template <typename T, class P>
-__global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ P p) {
+template <typename T>
+__global__ void __launch_bounds__(256) delta_kernel(AttnParams p) {
   const int warps = (gridDim.x * blockDim.x) >> 5;
   const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const int cpr = p.d / 8;  // 16-byte chunks per head
   const int chunks = p.hq * cpr;
   constexpr float kLog2e = 1.4426950408889634f;
-  const int sh = pack_shift(p);
-  if constexpr (is_prefix<P>) {
-    // the linear rows past the tensor's last one are no tokens either
-    const long long first = static_cast<long long>(p.total_q) << sh, pad = p.rows_lin - first;
-    for (long long z = gw * 32ll + lane; z < pad * p.vheads; z += warps * 32ll) {
-      const size_t at = static_cast<size_t>(z / pad) * p.rows_lin + first + z % pad;
-      p.lse_lin[at] = -INFINITY;
-      p.delta_lin[at] = 0.f;
-    }
-  }
   for (int r = gw; r < p.total_q; r += warps) {
     int i = 0;
     const int b = locate_row(p, p.cu_q_pad, r, &i);
-    SeqInfo s{};
-    if (b >= 0) s = load_seq(p, b);
+    if (b < 0) continue;
+    const SeqInfo s = load_seq(p, b);
+    if (i >= s.len_q || s.len_k == 0) continue;  // no tile reads this row
     const size_t row = static_cast<size_t>(r);
-    // where head h's values go in the linear rows
-    auto linear = [&](int h) {
-      if constexpr (is_prefix<P>)
-        return static_cast<size_t>(h >> sh) * p.rows_lin + (row << sh) + (h & ((1 << sh) - 1));
-      else
-        return static_cast<size_t>(0);
-    };
-    if constexpr (is_prefix<P>) {
-      if (b < 0 || i >= s.len_q || (s.len_k == 0 && prefix_keys(p) == 0)) {
-        for (int h = lane; h < p.hq; h += 32) {
-          p.lse_lin[linear(h)] = -INFINITY;
-          p.delta_lin[linear(h)] = 0.f;
-        }
-        continue;
-      }
-    } else {
-      if (b < 0) continue;
-      if (i >= s.len_q || s.len_k == 0) continue;  // no tile reads this row
-    }
-    // index of head h in the tiles: without packing t0 + h * 128
-    const size_t t0 = packed_index(p, b, i << sh, 0);
-    auto tiled = [&](int h) {
-      if constexpr (is_prefix<P>) return t0 + static_cast<size_t>(h >> sh) * kBlockM + (h & ((1 << sh) - 1));
-      else return t0 + static_cast<size_t>(h) * kBlockM;
-    };
-    if (!bounds_ok(tiled(p.hq - 1) < static_cast<size_t>(p.pair_cap_q) * virtual_heads(p) * kBlockM,
+    const size_t t0 = tiled_index(p, b, i, 0);   // + h * 128 for head h
+    if (!bounds_ok(t0 + static_cast<size_t>(p.hq - 1) * kBlockM <
+                       static_cast<size_t>(p.pair_cap_q) * p.hq * kBlockM,
                    p.header + kHdrStatus))
       continue;
-    auto put_delta = [&](int h, float v) {
-      p.delta_t[tiled(h)] = v;
-      if constexpr (is_prefix<P>) p.delta_lin[linear(h)] = v;
-    };
-    for (int h = lane; h < p.hq; h += 32) {
-      const float v = -(p.lse_in[row * p.hq + h] * kLog2e);
-      p.lse_t[tiled(h)] = v;
-      if constexpr (is_prefix<P>) p.lse_lin[linear(h)] = v;
-    }
+    for (int h = lane; h < p.hq; h += 32)
+      p.lse_t[t0 + static_cast<size_t>(h) * kBlockM] = -(p.lse_in[row * p.hq + h] * kLog2e);
     const uint4* o = reinterpret_cast<const uint4*>(static_cast<const T*>(p.out_in) +
                                                     row * p.hq * p.d);
     const uint4* g = reinterpret_cast<const uint4*>(static_cast<const T*>(p.dout) +
@@ -563,14 +493,15 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ P p)
           const int c = c0 + 32 * u + lane;
           float v = c < chunks ? dot8<T>(oa[u], ga[u]) : 0.f;
           for (int w = cpr >> 1; w > 0; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
-          if (c < chunks && (c % cpr) == 0) put_delta(c / cpr, -v);
+          if (c < chunks && (c % cpr) == 0)
+            p.delta_t[t0 + static_cast<size_t>(c / cpr) * kBlockM] = -v;
         }
       }
     } else {
       for (int h = lane; h < p.hq; h += 32) {
         float v = 0.f;
         for (int c = 0; c < cpr; ++c) v += dot8<T>(o[h * cpr + c], g[h * cpr + c]);
-        put_delta(h, -v);
+        p.delta_t[t0 + static_cast<size_t>(h) * kBlockM] = -v;
       }
     }
   }
@@ -578,17 +509,9 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ P p)
 
 cudaError_t launch_delta(const AttnParams& p, bool bf16, int num_sms, cudaStream_t st) {
   if (bf16)
-    delta_kernel<__nv_bfloat16, AttnParams><<<num_sms * 8, 256, 0, st>>>(p);
+    delta_kernel<__nv_bfloat16><<<num_sms * 8, 256, 0, st>>>(p);
   else
-    delta_kernel<__half, AttnParams><<<num_sms * 8, 256, 0, st>>>(p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_prefix_delta(const PrefixBwd& p, bool bf16, int num_sms, cudaStream_t st) {
-  if (bf16)
-    delta_kernel<__nv_bfloat16, PrefixBwd><<<num_sms * 8, 256, 0, st>>>(p);
-  else
-    delta_kernel<__half, PrefixBwd><<<num_sms * 8, 256, 0, st>>>(p);
+    delta_kernel<__half><<<num_sms * 8, 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -107,11 +107,11 @@ bool fwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, i
   return true;
 }
 
-// Backward workspace, 256-byte aligned sections: header, prefix sums and sorted lists of
-// row and key tiles (as te_attn_bwd_thd's, of packed rows), lse and D of those tiles and of
+// Backward workspace, 256-byte aligned sections: header, prefix sums of row tiles, lists of
+// row and key tiles (of packed rows), lse and D of those tiles and of
 // the whole tensor's rows, and with splits > 1 the parts of the prefix's gradients.
 struct BwdLayout {
-  size_t pref_q, pref_k, pref_f, q_pairs, k_pairs, lse_t, delta_t, lse_lin, delta_lin, part_dk, part_dv, total;
+  size_t pref_q, q_pairs, k_pairs, lse_t, delta_t, lse_lin, delta_lin, part_dk, part_dv, total;
   int pack_shift, splits;
   long long cap_q, cap_k, rows_lin;
 };
@@ -131,10 +131,13 @@ bool bwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, i
   const int halves = d > 128 ? 2 : 1;
   const long long steps = (group >> sh) * (L->rows_lin / (d > 128 ? 64 : 128));
   const long long items = (static_cast<long long>(prefix_rows) + kBlockN - 1) / kBlockN * hkv * halves;
-  // about three items per SM, and 16 steps of a sweep at least to pay for storing its sums
-  long long want = items > 0 ? (kBwdItemsTarget + items - 1) / items : 1;
-  const long long most = steps / 16 > 1 ? steps / 16 : 1;
-  L->splits = static_cast<int>(want < most ? want : most);
+  // about three items per SM, with 16 steps of a sweep at least to pay for storing its sums
+  const long long want = items > 0 ? (kBwdItemsTarget + items - 1) / items : 1;
+  // down to 4 steps where that is needed to give every SM an item
+  const long long fill = items > 0 ? (152 + items - 1) / items : 1;
+  const long long few = fill < steps / 4 ? fill : steps / 4, many = want < steps / 16 ? want : steps / 16;
+  const long long best = few > many ? few : many;
+  L->splits = static_cast<int>(best > 1 ? best : 1);
   if (steps / L->splits >= (1 << 24) - 1 || L->cap_q * hq > INT32_MAX || L->cap_k * hkv * halves > INT32_MAX) return false;
   size_t off = kHdrWords * sizeof(int);
   auto take = [&off](size_t bytes) {
@@ -142,10 +145,7 @@ bool bwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, i
     off = (off + bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t sums = (static_cast<size_t>(batch) + 1) * sizeof(int);
-  L->pref_q = take(sums);
-  L->pref_k = take(sums);
-  L->pref_f = take(sums);
+  L->pref_q = take((static_cast<size_t>(batch) + 1) * sizeof(int));
   L->q_pairs = take(static_cast<size_t>(L->cap_q) * sizeof(int2));
   L->k_pairs = take(static_cast<size_t>(L->cap_k) * sizeof(int2));
   const size_t tiled = static_cast<size_t>(L->cap_q) * (hq >> sh) * kBlockM * sizeof(float);
@@ -277,15 +277,11 @@ int te_attn_prefix_bwd_thd(const void* q, const void* k, const void* v, const vo
   char* ws = static_cast<char*>(workspace);
   p.header = static_cast<int*>(workspace);
   int* pref_q = reinterpret_cast<int*>(ws + L.pref_q);
-  int* pref_k = reinterpret_cast<int*>(ws + L.pref_k);
-  int* pref_f = reinterpret_cast<int*>(ws + L.pref_f);
   p.pref_q = pref_q;
   p.q_pairs = reinterpret_cast<int2*>(ws + L.q_pairs);
   p.k_pairs = reinterpret_cast<int2*>(ws + L.k_pairs);
   p.pair_cap_q = static_cast<int>(L.cap_q);
   p.pair_cap_k = static_cast<int>(L.cap_k);
-  p.pair_cap_f = INT32_MAX;  // that list is not built
-  p.sched_lists = kListQ | kListK;
   p.lse_t = reinterpret_cast<float*>(ws + L.lse_t);
   p.delta_t = reinterpret_cast<float*>(ws + L.delta_t);
   p.lse_lin = reinterpret_cast<float*>(ws + L.lse_lin);
@@ -299,19 +295,18 @@ int te_attn_prefix_bwd_thd(const void* q, const void* k, const void* v, const vo
   p.splits = L.splits;
   const bool bf16 = dtype == TE_DTYPE_BF16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = api_timed(TE_KERNEL_SCHEDULE, st, [&] { return launch_prefix_bwd_schedule(p, pref_q, pref_k, pref_f, st); });
+  cudaError_t e = api_timed(TE_KERNEL_SCHEDULE, st, [&] { return launch_prefix_bwd_schedule(p, pref_q, st); });
   if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix schedule");
-  e = api_timed(TE_KERNEL_ZERO_FILL, st, [&] { return launch_prefix_bwd_zero_fill(p, sms, st); });
-  if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix zero fill");
+  e = api_timed(TE_KERNEL_DELTA, st, [&] { return launch_prefix_prep(p, bf16, sms, st); });
+  if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix rows");
   if (total_q > 0 && (total_kv > 0 || prefix_rows > 0)) {
-    e = api_timed(TE_KERNEL_DELTA, st, [&] { return launch_prefix_delta(p, bf16, sms, st); });
-    if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix delta");
     e = api_timed(TE_KERNEL_DQ, st, [&] { return launch_prefix_bwd_dq(p, bf16, sms, st); });
     if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix dQ");
     e = api_timed(TE_KERNEL_DKDV, st, [&] { return launch_prefix_bwd_dkdv(p, bf16, sms, st); });
     if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix dK/dV");
   }
-  if (prefix_rows > 0) {
+  // with one part and every row seen, the dK/dV kernel wrote all of it
+  if (prefix_rows > 0 && (p.splits > 1 || prefix_len || total_q == 0)) {
     e = api_timed(TE_KERNEL_DKDV, st, [&] { return launch_prefix_sum(p, bf16, sms, st); });
     if (e != cudaSuccess) return api_cuda_fail(e, "shared-prefix gradient sum");
   }
