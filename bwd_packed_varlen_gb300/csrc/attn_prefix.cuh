@@ -93,10 +93,7 @@ __device__ __forceinline__ int prefix_keys(const PrefixParams& p) {
 // against the prefix (row tiles of the compact token list) and stand alone against its own
 // keys. A longer sequence has row tiles of its own, each over the prefix and then its own
 // keys. A row tile's key tiles are cut into chunks; rows whose only chunk is the whole are
-// written directly, the others leave partial results that the join kernel merges. A row
-// tile of at most 128 rows that leaves partial results leaves two per chunk ("ways"): the
-// two softmax groups of a block then take its key tiles in turn, so one's exponentials
-// overlap the other's products.
+// written directly, the others leave partial results that the join kernel merges.
 // ---------------------------------------------------------------------------
 constexpr int kShortRows = 128;
 constexpr int kPartsTarget = 2 * 152;  // chunks over all kv heads, about: two per SM
@@ -108,23 +105,22 @@ __host__ __device__ constexpr int prefix_key_tile(int d) { return d <= 128 ? 128
 struct PrefixEntry {
   int row0, rows;    // packed rows [row0, row0 + rows) of the list
   int seq;           // -1: the compact tokens
-  int ways;
   int t0, t1, np;    // key tiles [t0, t1), of which tiles below np are the prefix's
-  int slot;          // partial row of (way 0, kv head 0, row 0); -1: written directly
+  int slot;          // partial row of (kv head 0, row 0); -1: written directly
   int off_q, off_k, len_k, diag;  // of the sequence (SeqInfo)
 };
 __device__ __forceinline__ PrefixEntry load_entry(const PrefixParams& p, int e) {
   const int4 a = p.entries[3 * e], b = p.entries[3 * e + 1], c = p.entries[3 * e + 2];
-  return PrefixEntry{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+  return PrefixEntry{a.x, a.y, a.z, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
 }
 __device__ __forceinline__ void store_entry(const PrefixParams& p, int e, const PrefixEntry& v) {
-  p.entries[3 * e] = make_int4(v.row0, v.rows, v.seq, v.ways);
+  p.entries[3 * e] = make_int4(v.row0, v.rows, v.seq, 0);
   p.entries[3 * e + 1] = make_int4(v.t0, v.t1, v.np, v.slot);
   p.entries[3 * e + 2] = make_int4(v.off_q, v.off_k, v.len_k, v.diag);
 }
-// Partial row of way x and kv head h, counted from the chunk's first one.
-__device__ __forceinline__ size_t partial_offset(const PrefixParams& p, int rows, int x, int h) {
-  return (static_cast<size_t>(x) * p.hkv + h) * rows;
+// Partial rows before those of chunk c and kv head h, of a row tile's.
+__device__ __forceinline__ size_t partial_offset(const PrefixParams& p, int rows, int c, int h) {
+  return (static_cast<size_t>(c) * p.hkv + h) * rows;
 }
 
 // ---------------------------------------------------------------------------

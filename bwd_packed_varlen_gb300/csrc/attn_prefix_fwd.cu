@@ -2,20 +2,19 @@
 //
 //   S = scale [q Kp^T | q K_b^T + mask],  O = softmax(S) [Vp; V_b],  LSE = log sum exp S
 //
-// One persistent kernel takes items (group of rows, chunk of its key tiles, kv head); see
-// attn_prefix.cuh for the groups. The rows of an item are the queries of one kv head's
-// group packed token by token, so a decoding step of many sequences fills the 128-row
-// tiles of the tensor cores against the prefix, and K/V tiles are read once for all of
-// them. Roles as in the two-tile forward:
-//   warps 0-3   softmax of row tile A (one thread per row / TMEM lane),
-//   warps 4-7   softmax of row tile B (head_dim <= 128 only),
-//   then        an item warp (decodes items and gathers their Q rows, an item ahead), a
+// One persistent kernel takes items (rows, chunk of their key tiles, kv head); see
+// attn_prefix.cuh. The rows of an item are the queries of one kv head's group packed token
+// by token, so a decoding step of many sequences fills the 128-row tiles of the tensor
+// cores against the prefix, and K/V tiles are read once for all of them. Roles:
+//   warps 0-3   softmax of stream 0 (one thread per row / TMEM lane),
+//   warps 4-7   softmax of stream 1 (head_dim <= 128 only),
+//   then        an item warp (decodes items ahead and starts the loads of their Q rows), a
 //               K/V warp (TMA) and an MMA warp.
-// An item of one row tile that leaves partial results is taken in turns: tile j of its keys
-// goes to softmax group j % 2, each with its own O, so the chain S -> P -> O of one tile
-// overlaps the other's (a decoding step's rows fill a few lanes only; the chain's latency,
-// not its work, is what counts). Its Q rows use one half of the Q buffer, and the next
-// such item's the other.
+// An item of at most 128 rows runs on one stream; the streams work on different items and
+// their key tiles alternate in the shared K/V ring, so one item's exponentials, first
+// scores and stores overlap the other's products (a decoding step's items are a few tiles
+// long, and the chain S -> P -> O of a tile is about 2700 cycles against 1000 of tensor
+// work). An item of more rows takes both streams, row tile A and B, over the same key tiles.
 // S = Q K^T into TMEM, P = exp2(S scale log2e - m) over it as 16-bit values, O += P V in
 // TMEM. The offset m is raised only when a row's maximum exceeds it by more than 2^8.
 // P is rounded to 16 bits for the tensor cores (relative to the row's largest value, half a
@@ -65,7 +64,6 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
   __shared__ unsigned long long work, tokens;
   pdl_trigger();
   const int rt = prefix_row_tile(p.d), bn = prefix_key_tile(p.d), tid = threadIdx.x, lane = tid & 31;
-  const int most_ways = rt / 128;
   if (tid == 0) {
     bad = p.prefix_len && (*p.prefix_len < 0 || *p.prefix_len > p.prefix_rows) ? 1 : 0;
     work = tokens = 0;
@@ -138,7 +136,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
     const int q = n / chunks, r = n - q * chunks;
     e.t0 = c * q + min(c, r);
     e.t1 = e.t0 + q + (c < r ? 1 : 0);
-    if (e.slot >= 0) e.slot += c * e.ways * p.hkv * e.rows;
+    if (e.slot >= 0) e.slot += c * p.hkv * e.rows;
     if (at < p.cap_entries) store_entry(p, at, e);
   };
   // long row tiles
@@ -163,13 +161,12 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
       e.diag = q.diag;
       n = np + own_tiles(p, q.len_k, q.diag, e.row0, e.rows, bn);
       ch = div_up(n, len);
-      e.ways = ch > 1 && e.rows <= rt / 2 ? most_ways : 1;
-      slots = ch > 1 ? ch * e.ways * p.hkv * e.rows : 0;
+      slots = ch > 1 ? ch * p.hkv * e.rows : 0;
     }
     const Scan3 at = block_scan3(ch, slots, 0, buf);
     if (g < n_long && g < p.cap_longs) {
       e.slot = slots > 0 ? n_rows + at.y : -1;
-      p.longs[g] = make_int4(e.slot, ch * e.ways, e.rows, 0);
+      p.longs[g] = make_int4(e.slot, ch, e.rows, 0);
       for (int c = 0; c < ch; ++c) put_chunk(e, n, ch, c, n_entries + at.x + c);
     }
     n_entries += at.tx;
@@ -186,15 +183,11 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
     e.row0 = u * rt;
     e.rows = min(rt, short_rows - e.row0);
     e.np = np;
-    e.ways = e.rows <= rt / 2 ? most_ways : 1;
     e.slot = pre_slot + u * rt * pre_chunks * p.hkv;
     put_chunk(e, np, pre_chunks, c, n_entries + k);
   }
   n_entries += n_pre * pre_chunks;
-  if (n_pre > 0) {
-    const int last = short_rows - (n_pre - 1) * rt;
-    n_rows += ((n_pre - 1) * rt + last * (last <= rt / 2 ? most_ways : 1)) * pre_chunks * p.hkv;
-  }
+  n_rows += short_rows * pre_chunks * p.hkv;
   // short sequences against their own keys
   for (int base = 0; base < p.batch; base += blockDim.x) {
     const int b = base + tid;
@@ -217,15 +210,13 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
       e.diag = s.diag;
       n = own_tiles(p, s.len_k, s.diag, 0, e.rows, bn);
       ch = div_up(n, len);
-      // without a prefix a single tile is the whole result
-      const bool direct = n == 1 && n_pre == 0;
-      e.ways = direct ? 1 : most_ways;
-      slots = direct ? 0 : ch * e.ways * p.hkv * e.rows;
+      // without a prefix a single chunk is the whole result
+      slots = ch > 1 || n_pre > 0 ? ch * p.hkv * e.rows : 0;
     }
     const Scan3 at = block_scan3(ch, slots, 0, buf);
     if (ch > 0) {
       e.slot = slots > 0 ? n_rows + at.y : -1;
-      p.seqs[b] = make_int4(first_tok, e.slot, slots > 0 ? ch * e.ways : -1, 0);
+      p.seqs[b] = make_int4(first_tok, e.slot, slots > 0 ? ch : -1, 0);
       for (int c = 0; c < ch; ++c) put_chunk(e, n, ch, c, n_entries + at.x + c);
     }
     n_entries += at.tx;
@@ -252,17 +243,25 @@ cudaError_t launch_prefix_schedule(const PrefixParams& p, cudaStream_t st) {
 // ---------------------------------------------------------------------------
 // Main kernel
 // ---------------------------------------------------------------------------
+// Tensor maps of one call.
+struct PrefixMaps {
+  CUtensorMap k, v, kp, vp;
+  CUtensorMap q_tile, q_token, q_row;  // boxes of 128 rows (whole tokens), one token's group, one row
+  int q_tokens;                        // tokens of q_tile's box; 0: a tile does not hold whole ones
+};
+
 template <int kD>
 struct PrefixShape {
-  static constexpr int kNT = prefix_row_tile(kD) / 128;   // row tiles of an item
+  static constexpr int kNT = prefix_row_tile(kD) / 128;   // streams
   static constexpr int kBN = prefix_key_tile(kD);          // keys per tile
   static constexpr int kChunks = kD / 64;                  // 64-column chunks of a row
   static constexpr int kQBytes = kChunks * 16384;          // one 128-row Q tile
   static constexpr int kKVBytes = kChunks * kBN * 128;     // one K or V tile
   static constexpr int kStages = kD == 64 ? 4 : 2;
-  static constexpr int kSmemBytes = kNT * kQBytes + 2 * kStages * kKVBytes + 1024;
+  static constexpr int kStageBytes = kNT * 4 * 2048;       // per softmax warp, for its stores
+  static constexpr int kSmemBytes = kNT * kQBytes + 2 * kStages * kKVBytes + kStageBytes + 1024;
   static constexpr int kThreads = kNT * 128 + 96;
-  // TMEM columns of O and S of row tile x: O_0 O_1 S_0 S_1
+  // TMEM columns of O and S of stream x: O_0 O_1 S_0 S_1
   __device__ static constexpr uint32_t col_o(int x) { return static_cast<uint32_t>(x) * 128u; }
   __device__ static constexpr uint32_t col_s(int x) { return 256u + static_cast<uint32_t>(x) * 128u; }
   static_assert(kSmemBytes <= 220 * 1024, "shared memory budget");
@@ -274,51 +273,63 @@ __device__ __forceinline__ float ex2p(float x) {
   return y;
 }
 
-// 16-byte global -> shared copy; `bytes` 0 fills with zeros without reading.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// What the producer hands over with an item (two of them, in turn).
+// What the item warp hands to a stream, the K/V warp and the MMA warp (two slots in turn).
 struct PrefixItem {
-  int n[2];         // key tiles that softmax group 0 / 1 visits (0: none)
-  int turns;        // 1: group x takes the key tiles x, x + 2, .. of one row tile
-                    // 0: group x takes every key tile for row tile x
-  int rows;         // rows of the item; the arrays below hold them rounded up to 32
-  int half;         // half of the Q buffer that holds the rows; -1: both
+  int n;            // key tiles the stream visits; -1: no more items
+  int pair;         // the item takes both streams (n may then be 0 for the first)
   int np;           // the first np key tiles are the prefix's
   int p_key, o_key; // tensor rows of the first prefix key and the first own key
   int p_left;       // prefix keys from the item's first prefix tile on
   int o_left;       // own real keys from the item's first own tile on
   int direct;       // rows are written to out / lse, not to partial rows
   int head;         // kv head
-  int part[2];      // partial row of the group's first row
-  int row[256];     // per row: token * hq + head; -1: no row
-  int lim[256];     // per row: own keys it sees from the item's first own tile on
+  int part;         // partial row of the stream's first row
+  int rows;         // rows of the stream; the arrays hold them rounded up to 32
+  int row[128];     // per row: token * hq + head; -1: no row
+  int lim[128];     // per row: own keys it sees from the item's first own tile on
+};
+struct ItemRing {
+  PrefixItem item[2];
+  uint64_t full[2], empty[2];
+};
+
+// The order of key tiles over the streams, in which the K/V warp loads and the MMA warp
+// issues them: streams that have tiles left alternate, a stream that runs out takes the
+// next item at once, and an item for both waits until both have run out. The item warp
+// follows the same counts to know which stream that is.
+struct TileOrder {
+  int left0 = 0, left1 = 0;  // key tiles that each stream has left (scalars: no local memory)
+  int last = 1;
+  __device__ __forceinline__ int left(int x) const { return x ? left1 : left0; }
+  __device__ __forceinline__ void set(int x, int n) {
+    if (x) left1 = n;
+    else left0 = n;
+  }
+  __device__ __forceinline__ void take(int x) {
+    set(x, left(x) - 1);
+    last = x;
+  }
+  __device__ __forceinline__ int next() const { return left(1 - last) > 0 ? 1 - last : last; }
 };
 
 template <int kD, bool kBF16>
 __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
-    attn_prefix_fwd_kernel(const __grid_constant__ PrefixParams p, const __grid_constant__ CUtensorMap tmK,
-                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKp,
-                           const __grid_constant__ CUtensorMap tmVp) {
+    attn_prefix_fwd_kernel(const __grid_constant__ PrefixParams p, const __grid_constant__ PrefixMaps tm) {
   using S = PrefixShape<kD>;
   constexpr int NT = S::kNT, NS = S::kStages, BN = S::kBN;
   constexpr int kWarpItem = NT * 4, kWarpKv = NT * 4 + 1, kWarpMma = NT * 4 + 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* sQ = smem;
+  uint8_t* sQ = smem;                        // one tile per stream
   uint8_t* sK = sQ + NT * S::kQBytes;
   uint8_t* sV = sK + NS * S::kKVBytes;
+  uint8_t* sStage = sV + NS * S::kKVBytes;
 
-  __shared__ uint64_t bar_q_full[NT], bar_q_empty[NT];  // per 128-row half of the Q buffer
+  __shared__ uint64_t bar_q_full[NT], bar_q_empty[NT];
   __shared__ uint64_t bar_k_full[NS], bar_k_empty[NS], bar_v_full[NS], bar_v_empty[NS];
   __shared__ uint64_t bar_s_full[NT], bar_p_ready[NT], bar_o_full[NT], bar_o_empty[NT];
-  __shared__ WorkRing ring;
-  __shared__ PrefixItem items[2];
+  __shared__ ItemRing rings[NT];
   __shared__ uint32_t tmem_slot;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -332,14 +343,17 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       mbar_init(&bar_v_empty[i], 1);
     }
     for (int x = 0; x < NT; ++x) {
-      mbar_init(&bar_q_full[x], 32);
+      mbar_init(&bar_q_full[x], 1);
       mbar_init(&bar_q_empty[x], 1);
       mbar_init(&bar_s_full[x], 1);
       mbar_init(&bar_p_ready[x], 128);
       mbar_init(&bar_o_full[x], 1);
       mbar_init(&bar_o_empty[x], 128);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&rings[x].full[i], 1);
+        mbar_init(&rings[x].empty[i], 1 + 32 + 128);  // K/V warp's lane 0, MMA warp, softmax
+      }
     }
-    ring_init(ring, 1 + 32 + NT * 128);
     fence_barrier_init();
   }
   if (warp == kWarpMma) {
@@ -350,6 +364,10 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  if (warp == kWarpKv && lane == 0) {
+    const CUtensorMap* maps[] = {&tm.k, &tm.v, &tm.kp, &tm.vp, &tm.q_tile, &tm.q_token, &tm.q_row};
+    for (const CUtensorMap* m : maps) tma_prefetch_desc(m);
+  }
   pdl_trigger();
   pdl_wait();  // the scheduler's lists
 
@@ -357,160 +375,203 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
     // ------------------------------------------------------------- items and Q rows
     // the first entry is read along with the number of entries (the grid is no larger than
     // the entries' capacity)
-    PrefixEntry first = load_entry(p, blockIdx.x / p.hkv);
+    const PrefixEntry first = load_entry(p, blockIdx.x / p.hkv);
     const int n_items = p.header[kHdrPrefixEntries] * p.hkv;
     const int np_keys = prefix_keys(p);
-    bool ok = true;
     int nxt = blockIdx.x;
-    int uses[2] = {0, 0};  // items so far in each half of the Q buffer
-    int half = 0;
-    for (int ii = 0; ok; ++ii) {
+    int puts0 = 0, puts1 = 0;  // hand-overs so far, per stream: each also uses its Q tile once
+    auto puts = [&](int x) { return x ? puts1 : puts0; };
+    TileOrder order;
+    bool ok = true;
+    auto wait_slot = [&](int x) {
+      const int n = puts(x);
+      return n < 2 || __all_sync(0xffffffffu, mbar_wait(&rings[x].empty[n & 1], ((n >> 1) - 1) & 1, status));
+    };
+    for (int ii = 0;; ++ii) {
       const int item = nxt < n_items ? nxt : -1;
-      PrefixEntry e{};
-      if (item >= 0) {
-        if (lane == 0) nxt = next_item(p.header + kHdrNextFwd);
-        e = ii == 0 ? first : load_entry(p, item / p.hkv);
-        nxt = __shfl_sync(0xffffffffu, nxt, 0);
-      }
-      // the slot's last readers are done with it
-      if (ii >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&ring.empty[ii & 1], ((ii >> 1) - 1) & 1, status));
-      if (!ok) break;
-      if (item < 0) {
-        if (lane == 0) {
-          *reinterpret_cast<volatile int*>(&ring.item[ii & 1]) = -1;
-          mbar_arrive(&ring.full[ii & 1]);
-        }
-        break;
-      }
+      if (item < 0) break;
+      if (lane == 0) nxt = next_item(p.header + kHdrNextFwd);
+      const PrefixEntry e = ii == 0 ? first : load_entry(p, item / p.hkv);
+      nxt = __shfl_sync(0xffffffffu, nxt, 0);
       const int h = item % p.hkv;
       const int np = max(0, min(e.t1, e.np) - e.t0);  // prefix tiles of the chunk
       const int o0 = max(0, e.t0 - e.np);             // first own tile
-      PrefixItem& I = items[ii & 1];
-      // rows: where they lie and what they see (all loads of a batch in flight at once)
-      constexpr int kPer = NT * 4;  // rows per lane
-      int tok[kPer];
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const int r = u * 32 + lane, i = (e.row0 + r) / p.group;
-        tok[u] = r >= e.rows ? -1 : e.seq < 0 ? p.short_tok[i] : e.off_q + i;
-      }
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const int r = u * 32 + lane;
-        if (u * 32 >= e.rows) break;
-        const int rr = e.row0 + r, i = rr / p.group, j = rr - i * p.group;
-        const bool in = r < e.rows && bounds_ok(tok[u] >= 0 && tok[u] < p.total_q, status);
-        I.row[r] = in ? tok[u] * p.hq + h * p.group + j : -1;
-        I.lim[r] = in && e.seq >= 0 ? max(0, keys_seen(p.causal, e.len_k, e.diag, i) - o0 * BN) : 0;
-      }
+      const bool pair = e.rows > 128;
       // own tiles end at the last one that a row of the tile sees
-      int n[2] = {0, 0};
-      const bool turns = e.ways == 2;
-#pragma unroll
-      for (int x = 0; x < NT; ++x) {
+      auto tiles = [&](int x) {
         const int rows = min(128, e.rows - x * 128);
-        if (rows > 0) {
-          const int no = e.seq >= 0 ? own_tiles(p, e.len_k, e.diag, e.row0 + x * 128, rows, BN) : 0;
-          n[x] = max(0, min(e.t1, e.np + no) - e.t0);
+        const int no = e.seq >= 0 ? own_tiles(p, e.len_k, e.diag, e.row0 + x * 128, rows, BN) : 0;
+        return max(0, min(e.t1, e.np + no) - e.t0);
+      };
+      int x0 = 0, x1 = NT - 1;
+      if (pair) {
+        order = TileOrder();
+      } else {
+        while (order.left0 > 0 && order.left1 > 0) order.take(order.next());
+        x0 = x1 = NT == 1 || order.left0 == 0 ? 0 : 1;
+        order.set(x0, tiles(0));
+      }
+      // rows: where they lie and what they see (all loads in flight at once)
+      int tok[NT][4];
+#pragma unroll
+      for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = k * 128 + u * 32 + lane, i = (e.row0 + r) / p.group;
+          tok[k][u] = r >= e.rows ? -1 : e.seq < 0 ? p.short_tok[i] : e.off_q + i;
         }
+      // Both streams' hand-overs of an item come before any wait for a Q tile: the MMA warp
+      // may need the second one to go on with the item that still uses that tile.
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        const int x = x0 + k, r0 = k * 128;  // row tile k of the item goes to stream x
+        if (x > x1 || !ok) continue;
+        const int rows = min(128, e.rows - r0);
+        // the slot's last readers are done with it
+        if (!(ok = wait_slot(x))) break;
+        PrefixItem& I = rings[x].item[puts(x) & 1];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = u * 32 + lane;
+          if (u * 32 >= rows) break;
+          const int rr = e.row0 + r0 + r, i = rr / p.group, j = rr - i * p.group;
+          const bool in = r < rows && bounds_ok(tok[k][u] >= 0 && tok[k][u] < p.total_q, status);
+          I.row[r] = in ? tok[k][u] * p.hq + h * p.group + j : -1;
+          I.lim[r] = in && e.seq >= 0 ? max(0, keys_seen(p.causal, e.len_k, e.diag, i) - o0 * BN) : 0;
+        }
+        if (lane == 0) {
+          I.n = tiles(k);
+          I.pair = pair ? 1 : 0;
+          I.np = np;
+          I.p_key = e.t0 * BN;
+          I.o_key = e.off_k + o0 * BN;
+          I.p_left = np_keys - e.t0 * BN;
+          I.o_left = e.len_k - o0 * BN;
+          I.direct = e.slot < 0 ? 1 : 0;
+          I.head = h;
+          I.part = e.slot < 0 ? 0 : e.slot + static_cast<int>(partial_offset(p, e.rows, 0, h)) + r0;
+          I.rows = rows;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rings[x].full[puts(x) & 1]);
       }
-      if (turns) {
-        n[1] = n[0] / 2;
-        n[0] -= n[1];
+      // Q rows by TMA: whole tiles where tokens lie side by side and a tile holds whole
+      // ones, else token by token (all heads of the group in one box, one lane each), and
+      // row by row where a token's heads do not all lie in this tile. A box may start at
+      // any 128-byte row of the tile: the swizzle goes by shared-memory address.
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        const int x = x0 + k, r0 = k * 128;
+        if (x > x1 || !ok) continue;
+        const int rows = min(128, e.rows - r0);
+        if (puts(x) > 0 &&
+            !(ok = __all_sync(0xffffffffu, mbar_wait(&bar_q_empty[x], (puts(x) - 1) & 1, status))))
+          break;
+        if (x) ++puts1;
+        else ++puts0;
+        uint8_t* q_tile = sQ + x * S::kQBytes;
+        const int rr0 = e.row0 + r0, i0 = rr0 / p.group, i1 = (rr0 + rows - 1) / p.group;
+        const int first_tok = __shfl_sync(0xffffffffu, tok[k][0], 0);
+        int last_tok = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (u == (rows - 1) >> 5) last_tok = __shfl_sync(0xffffffffu, tok[k][u], (rows - 1) & 31);
+        const bool whole = tm.q_tokens > 0 && last_tok - first_tok == i1 - i0 && rr0 % p.group == 0;
+        if (lane == 0) mbar_arrive_expect_tx(&bar_q_full[x], (whole ? 128 : rows) * 128 * S::kChunks);
+        __syncwarp();
+        if (whole) {
+          if (lane < S::kChunks)
+            tma_load_4d(q_tile + lane * 16384, &tm.q_tile, &bar_q_full[x], lane * 64, h * p.group, 0, first_tok);
+        } else {
+          for (int i = i0 + lane; i <= i1; i += 32) {
+            const int t = e.seq < 0 ? p.short_tok[i] : e.off_q + i;
+            const int ra = i * p.group - rr0;  // the token's first row here
+            if (p.group <= 128 && ra >= 0 && ra + p.group <= rows) {
+              for (int c = 0; c < S::kChunks; ++c)
+                tma_load_4d(q_tile + c * 16384 + ra * 128, &tm.q_token, &bar_q_full[x], c * 64, h * p.group, 0, t);
+            } else {
+              for (int r = max(ra, 0); r < min(ra + p.group, rows); ++r)
+                for (int c = 0; c < S::kChunks; ++c)
+                  tma_load_4d(q_tile + c * 16384 + r * 128, &tm.q_row, &bar_q_full[x], c * 64,
+                              h * p.group + r - ra, 0, t);
+            }
+          }
+        }
+        __syncwarp();
       }
-      const bool both = e.rows > 128;
-      if (NT == 1) half = 0;
-      if (lane == 0) {
-        I.n[0] = n[0];
-        I.n[1] = n[1];
-        I.rows = e.rows;
-        I.turns = turns ? 1 : 0;
-        I.half = both ? -1 : half;
-        I.np = np;
-        I.p_key = e.t0 * BN;
-        I.o_key = e.off_k + o0 * BN;
-        I.p_left = np_keys - e.t0 * BN;
-        I.o_left = e.len_k - o0 * BN;
-        I.direct = e.slot < 0 ? 1 : 0;
-        I.head = h;
-        for (int x = 0; x < 2; ++x)
-          I.part[x] = e.slot < 0 ? 0
-                                 : e.slot + static_cast<int>(partial_offset(p, e.rows, turns ? x : 0, h)) +
-                                       (turns ? 0 : x * 128);
-        *reinterpret_cast<volatile int*>(&ring.item[ii & 1]) = item;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ring.full[ii & 1]);
-      // Q rows, 16 bytes per lane and step, in the 128-byte swizzle the MMAs read;
-      // columns from d on are filled with zeros. Rows past the last stay as they are:
-      // they meet no other row.
-      const int h0 = both ? 0 : half, h1 = both ? NT - 1 : half;
-      for (int x = h0; x <= h1 && ok; ++x)
-        if (uses[x] > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bar_q_empty[x], (uses[x] - 1) & 1, status));
       if (!ok) break;
-      // (A lane keeps its column; addresses of eight rows are worked out before the copies,
-      // which then issue back to back: one by one each took 130 cycles of this warp.)
-      constexpr int kPieces = kD / 8, kRowsPer = 32 / (kPieces < 32 ? kPieces : 32);  // rows per step
-      const int c = lane % kPieces, r_in = lane / kPieces;
-      const bool col = c * 8 < p.d;
-      const char* q_col = static_cast<const char*>(p.q) + c * 16;
-      uint8_t* s_col = sQ + h0 * S::kQBytes + (c >> 3) * 16384;
-      for (int r0 = 0; r0 < e.rows; r0 += 8 * kRowsPer) {
-        const char* src[8];
-        uint8_t* dst[8];
-        int bytes[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int r = r0 + u * kRowsPer + r_in;
-          const int row = r < e.rows ? I.row[r] : -1;
-          bytes[u] = row >= 0 && col ? 16 : 0;
-          src[u] = bytes[u] ? q_col + static_cast<size_t>(row) * (p.d * 2) : static_cast<const char*>(p.q);
-          dst[u] = s_col + (r >> 7) * S::kQBytes + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (r0 + u * kRowsPer + r_in < e.rows) cp_async16(dst[u], src[u], bytes[u]);
+    }
+    // no more items, on every stream
+    for (int x = 0; x < NT && ok; ++x) {
+      if (!(ok = wait_slot(x))) break;
+      if (lane == 0) {
+        rings[x].item[puts(x) & 1].n = -1;
+        mbar_arrive(&rings[x].full[puts(x) & 1]);
       }
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      for (int x = h0; x <= h1; ++x) {
-        mbar_arrive(&bar_q_full[x]);
-        ++uses[x];
-      }
-      if (!both) half ^= 1;
     }
   } else if (warp == kWarpKv) {
     // ------------------------------------------------------------- K and V tiles
     if (lane == 0) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-      tma_prefetch_desc(&tmKp);
-      tma_prefetch_desc(&tmVp);
       int it = 0;
       bool ok = true;
-      for (int ii = 0; ok; ++ii) {
-        const int sl = ii & 1;
-        if (!(ok = mbar_wait(&ring.full[sl], (ii >> 1) & 1, status))) break;
-        const int item = *reinterpret_cast<volatile int*>(&ring.item[sl]);
-        const PrefixItem& I = items[sl];
-        const int n = I.turns ? I.n[0] + I.n[1] : max(I.n[0], I.n[1]);
-        const int np = I.np, p_key = I.p_key, o_key = I.o_key, h = I.head;
-        mbar_arrive(&ring.empty[sl]);
-        if (item < 0) break;
-        for (int j = 0; j < n; ++j, ++it) {
-          const int st = it % NS;
-          const bool pre = j < np;
-          const CUtensorMap* mk = pre ? &tmKp : &tmK;
-          const CUtensorMap* mv = pre ? &tmVp : &tmV;
-          const int key = pre ? p_key + j * BN : o_key + (j - np) * BN;
-          if (it >= NS && !(ok = mbar_wait(&bar_k_empty[st], ((it / NS) - 1) & 1, status))) break;
-          mbar_arrive_expect_tx(&bar_k_full[st], S::kKVBytes);
-          for (int c = 0; c < S::kChunks; ++c)
-            tma_load_4d(sK + st * S::kKVBytes + c * BN * 128, mk, &bar_k_full[st], c * 64, h, 0, key);
-          if (it >= NS && !(ok = mbar_wait(&bar_v_empty[st], ((it / NS) - 1) & 1, status))) break;
-          mbar_arrive_expect_tx(&bar_v_full[st], S::kKVBytes);
-          for (int c = 0; c < S::kChunks; ++c)
-            tma_load_4d(sV + st * S::kKVBytes + c * BN * 128, mv, &bar_v_full[st], c * 64, h, 0, key);
+      struct Tiles {
+        int np, p_key, o_key, h, j;
+      };
+      Tiles cur[2] = {};
+      int gets[2] = {0, 0};
+      bool held[2] = {false, false}, ended[2] = {false, NT == 1};
+      int pair_n[2] = {0, 0};
+      TileOrder order;
+      auto load_tile = [&](Tiles& c) -> bool {
+        const int st = it % NS;
+        const bool pre = c.j < c.np;
+        const CUtensorMap* mk = pre ? &tm.kp : &tm.k;
+        const CUtensorMap* mv = pre ? &tm.vp : &tm.v;
+        const int key = pre ? c.p_key + c.j * BN : c.o_key + (c.j - c.np) * BN;
+        if (it >= NS && !mbar_wait(&bar_k_empty[st], ((it / NS) - 1) & 1, status)) return false;
+        mbar_arrive_expect_tx(&bar_k_full[st], S::kKVBytes);
+        for (int k = 0; k < S::kChunks; ++k)
+          tma_load_4d(sK + st * S::kKVBytes + k * BN * 128, mk, &bar_k_full[st], k * 64, c.h, 0, key);
+        if (it >= NS && !mbar_wait(&bar_v_empty[st], ((it / NS) - 1) & 1, status)) return false;
+        mbar_arrive_expect_tx(&bar_v_full[st], S::kKVBytes);
+        for (int k = 0; k < S::kChunks; ++k)
+          tma_load_4d(sV + st * S::kKVBytes + k * BN * 128, mv, &bar_v_full[st], k * 64, c.h, 0, key);
+        ++c.j;
+        ++it;
+        return true;
+      };
+      while (ok) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          if (!ok || order.left(x) > 0 || held[x] || ended[x]) continue;
+          const int sl = gets[x] & 1;
+          if (!(ok = mbar_wait(&rings[x].full[sl], (gets[x] >> 1) & 1, status))) break;
+          ++gets[x];
+          const PrefixItem& I = rings[x].item[sl];
+          const int n = I.n;
+          cur[x] = {I.np, I.p_key, I.o_key, I.head, 0};
+          const bool pair = I.pair != 0;
+          mbar_arrive(&rings[x].empty[sl]);
+          if (n < 0) {
+            ended[x] = true;
+          } else if (pair) {
+            held[x] = true;
+            pair_n[x] = n;
+          } else {
+            order.set(x, n);
+          }
+        }
+        if (!ok) break;
+        if (order.left0 > 0 || order.left1 > 0) {
+          const int x = order.next();
+          order.take(x);
+          ok = x ? load_tile(cur[1]) : load_tile(cur[0]);
+        } else if (held[0]) {
+          for (int j = max(pair_n[0], pair_n[1]); j > 0 && ok; --j) ok = load_tile(cur[0]);
+          held[0] = held[1] = false;
+          order = TileOrder();
+        } else {
+          break;
         }
       }
     }
@@ -521,111 +582,192 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
     const SmemDesc dq = smem_desc(smem_u32(sQ), 16, 1024, kLayoutSW128);
     const SmemDesc dk = smem_desc(smem_u32(sK), 16, 1024, kLayoutSW128);
     const SmemDesc dv = smem_desc(smem_u32(sV), BN * 128, 1024, kLayoutSW128);
-    int it = 0;
-    int np[2] = {0, 0};    // P hand-overs consumed per softmax group
-    int no[2] = {0, 0};    // items in which the group was present
-    int uses[2] = {0, 0};  // items so far in each half of the Q buffer
+    int it = 0;             // key tiles issued: tile `it` is in stage it % NS
+    int np[2] = {0, 0};     // P hand-overs consumed per stream
+    int no[2] = {0, 0};     // items whose O a stream has accumulated
+    int gets[2] = {0, 0};   // items taken per stream (each used its Q tile once)
+    bool held[2] = {false, false}, ended[2] = {false, NT == 1};
     bool ok = true;
-    for (int ii = 0; ok; ++ii) {
-      const int sl = ii & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[sl], (ii >> 1) & 1, status));
-      if (!ok) break;
-      const int item = *reinterpret_cast<volatile int*>(&ring.item[sl]);
-      const int n[2] = {items[sl].n[0], items[sl].n[1]};
-      const bool turns = items[sl].turns != 0;
-      const int half = items[sl].half;
-      const int n_pre = items[sl].np, p_left = items[sl].p_left, o_left = items[sl].o_left;
-      mbar_arrive(&ring.empty[sl]);
-      if (item < 0) break;
-      const int h0 = half < 0 ? 0 : half, h1 = half < 0 ? NT - 1 : half;
-      for (int x = h0; x <= h1 && ok; ++x) ok = mbar_wait_warp(&bar_q_full[x], uses[x]++ & 1, status);
-      if (!ok) break;
-      auto run_item = [&](auto turns_tag) -> bool {
-        constexpr bool kTurns = decltype(turns_tag)::value;
-        int s_left = n[0] + n[1];  // scores still to be issued: then the Q rows are free
-        // S_x = Q_x K^T for the item's key tile t
-        auto issue_s = [&](int x, int t) {
-          const int st = (it + t) % NS;
-          const SmemDesc qx{dq.lo + (((half < 0 ? x : half) * S::kQBytes) >> 4), dq.hi};
-          const SmemDesc kst{dk.lo + ((st * S::kKVBytes) >> 4), dk.hi};
-          __syncwarp();  // elect.sync in the MMA wrappers needs a converged warp
+    struct Running {
+      int n, j;                     // key tiles, and those whose scores are issued
+      int n_pre, p_left, o_left;
+      int pend;                     // tile whose scores are issued, product not: its number `it`; -1
+    };
+    Running cur[2] = {{0, 0, 0, 0, 0, -1}, {0, 0, 0, 0, 0, -1}};
+    TileOrder order;
+    auto issue_s = [&](int x, int tile) {
+      const int st = tile % NS;
+      const SmemDesc qx{dq.lo + ((x * S::kQBytes) >> 4), dq.hi};
+      const SmemDesc kst{dk.lo + ((st * S::kKVBytes) >> 4), dk.hi};
+      __syncwarp();  // elect.sync in the MMA wrappers needs a converged warp
 #pragma unroll
-          for (int s = 0; s < kD / 16; ++s)
-            mma_ss(tmem + S::col_s(x), qx, (s >> 2) * 16384 + (s & 3) * 32, kst, (s >> 2) * (BN * 128) + (s & 3) * 32,
-                   idS, s > 0 ? 1u : 0u);
-          mma_commit(&bar_s_full[x]);
-          if (kTurns) mma_commit(&bar_k_empty[st]);
-          if (--s_left == 0)
-            for (int y = h0; y <= h1; ++y) mma_commit(&bar_q_empty[y]);
-        };
-        auto wait_k = [&](int t) {
-          const int cur = it + t;
-          return mbar_wait_warp(&bar_k_full[cur % NS], (cur / NS) & 1, status);
-        };
-        const int rounds = max(n[0], n[1]);
+      for (int s = 0; s < kD / 16; ++s)
+        mma_ss(tmem + S::col_s(x), qx, (s >> 2) * 16384 + (s & 3) * 32, kst, (s >> 2) * (BN * 128) + (s & 3) * 32,
+               idS, s > 0 ? 1u : 0u);
+      mma_commit(&bar_s_full[x]);
+    };
+    auto issue_pv = [&](int x, int tile, bool first) {
+      const int st = tile % NS;
+      const SmemDesc vst{dv.lo + ((st * S::kKVBytes) >> 4), dv.hi};
+      const uint32_t acc0 = first ? 0u : 1u;
+      __syncwarp();
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-          if (n[x] == 0) continue;
-          const int t = kTurns ? x : 0;
-          if (!wait_k(t)) return false;
-          tc_fence_after();
-          issue_s(x, t);
+      for (int s = 0; s < BN / 16; ++s)
+        mma_ts(tmem + S::col_o(x), tmem + S::col_s(x) + s * 8, vst, s * 2048, idPV, s > 0 ? 1u : acc0);
+    };
+    auto wait_k = [&](int tile) { return mbar_wait_warp(&bar_k_full[tile % NS], (tile / NS) & 1, status); };
+    // V of a tile: rows that are no real key become zeros (P is 0 there, but 0 times NaN is
+    // not). j: the tile's number in its item.
+    auto wait_v = [&](int x, int tile, int j) -> bool {
+      const int st = tile % NS;
+      if (!mbar_wait_warp(&bar_v_full[st], (tile / NS) & 1, status)) return false;
+      const int real = j < cur[x].n_pre ? cur[x].p_left - j * BN : cur[x].o_left - (j - cur[x].n_pre) * BN;
+      if (real < BN) {
+        for (int z = real * 8 + lane; z < BN * 8; z += 32)
+          for (int c = 0; c < S::kChunks; ++c)
+            st_shared_v4(sV + st * S::kKVBytes + c * BN * 128 + z * 16, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      return true;
+    };
+    // P of stream x is ready, and for an item's first product the last item's O is read
+    auto wait_p = [&](int x, bool first) -> bool {
+      if (!mbar_wait_warp(&bar_p_ready[x], np[x] & 1, status)) return false;
+      ++np[x];
+      return !(first && no[x] > 0) || mbar_wait_warp(&bar_o_empty[x], (no[x] - 1) & 1, status);
+    };
+    // One step of stream x: the product of its last tile, then the scores of its next one.
+    auto step = [&](auto x_tag) -> bool {
+      constexpr int x = decltype(x_tag)::value;
+      auto& c = cur[x];
+      if (c.pend >= 0) {
+        const bool first_tile = c.j == 1, last_tile = c.j == c.n;
+        if (!wait_p(x, first_tile) || !wait_v(x, c.pend, c.j - 1)) return false;
+        tc_fence_after();
+        issue_pv(x, c.pend, first_tile);
+        mma_commit(&bar_v_empty[c.pend % NS]);
+        c.pend = -1;
+        if (last_tile) {
+          mma_commit(&bar_o_full[x]);
+          ++no[x];
         }
-        if (!kTurns) mma_commit(&bar_k_empty[it % NS]);
-        for (int j = 0; j < rounds; ++j) {
-          bool v_ready = false, k_ready = false;
-#pragma unroll
-          for (int x = 0; x < NT; ++x) {
-            if (j >= n[x]) continue;
-            const int t = kTurns ? 2 * j + x : j, cur = it + t, st = cur % NS;
-            if (!mbar_wait_warp(&bar_p_ready[x], np[x] & 1, status)) return false;
-            ++np[x];
-            if (j == 0 && no[x] > 0 && !mbar_wait_warp(&bar_o_empty[x], (no[x] - 1) & 1, status)) return false;
-            if (kTurns || !v_ready) {
-              if (!mbar_wait_warp(&bar_v_full[st], (cur / NS) & 1, status)) return false;
-              v_ready = true;
-              // V rows that are no real key: zeros (P is 0 there, but 0 times NaN is not)
-              const int real = t < n_pre ? p_left - t * BN : o_left - (t - n_pre) * BN;
-              if (real < BN) {
-                for (int z = real * 8 + lane; z < BN * 8; z += 32)
-                  for (int c = 0; c < S::kChunks; ++c)
-                    st_shared_v4(sV + st * S::kKVBytes + c * BN * 128 + z * 16, 0, 0, 0, 0);
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
-            }
-            tc_fence_after();
-            const SmemDesc vst{dv.lo + ((st * S::kKVBytes) >> 4), dv.hi};
-            const uint32_t acc0 = j > 0 ? 1u : 0u;
-            __syncwarp();
-#pragma unroll
-            for (int s = 0; s < BN / 16; ++s)
-              mma_ts(tmem + S::col_o(x), tmem + S::col_s(x) + s * 8, vst, s * 2048, idPV, s > 0 ? 1u : acc0);
-            if (kTurns) mma_commit(&bar_v_empty[st]);
-            if (j + 1 < n[x]) {
-              const int tn = kTurns ? t + 2 : t + 1;
-              if (kTurns || !k_ready) {
-                if (!wait_k(tn)) return false;
-                k_ready = true;
-              }
-              tc_fence_after();
-              issue_s(x, tn);
-            } else {
-              mma_commit(&bar_o_full[x]);
-            }
-          }
-          if (!kTurns) {
-            mma_commit(&bar_v_empty[(it + j) % NS]);
-            if (j + 1 < rounds) mma_commit(&bar_k_empty[(it + j + 1) % NS]);
-          }
-        }
-        it += kTurns ? n[0] + n[1] : rounds;
-        return true;
+      }
+      return true;
+    };
+    auto start = [&](auto x_tag) -> bool {
+      constexpr int x = decltype(x_tag)::value;
+      auto& c = cur[x];
+      if (c.j == 0 && !mbar_wait_warp(&bar_q_full[x], (gets[x] - 1) & 1, status)) return false;
+      if (!wait_k(it)) return false;
+      tc_fence_after();
+      issue_s(x, it);
+      mma_commit(&bar_k_empty[it % NS]);
+      if (++c.j == c.n) mma_commit(&bar_q_empty[x]);
+      c.pend = it++;
+      return true;
+    };
+    // An item's next hand-over to stream x (its fields wait in `next` until the stream's
+    // last product is issued).
+    struct Next {
+      int n, n_pre, p_left, o_left;
+    };
+    Next next[2] = {};
+    auto run_pair = [&]() -> bool {
+      const int n[2] = {next[0].n, next[NT - 1].n};
+      for (int x = 0; x < NT; ++x) {
+        cur[x].n_pre = next[x].n_pre;
+        cur[x].p_left = next[x].p_left;
+        cur[x].o_left = next[x].o_left;
+        if (!mbar_wait_warp(&bar_q_full[x], (gets[x] - 1) & 1, status)) return false;
+      }
+      int s_left[2] = {n[0], n[1]};
+      auto scores = [&](auto x_tag, int tile) {
+        constexpr int x = decltype(x_tag)::value;
+        issue_s(x, tile);
+        if (--s_left[x] == 0) mma_commit(&bar_q_empty[x]);
       };
-      ok = NT == 2 && turns ? run_item(std::true_type{}) : run_item(std::false_type{});
-      if (!ok) break;
+      const int rounds = max(n[0], n[1]);
+      if (!wait_k(it)) return false;
+      tc_fence_after();
       for (int x = 0; x < NT; ++x)
-        if (n[x] > 0) ++no[x];
+        if (n[x] == 0) mma_commit(&bar_q_empty[x]);
+      if (n[0] > 0) scores(std::integral_constant<int, 0>{}, it);
+      if (n[1] > 0) scores(std::integral_constant<int, NT - 1>{}, it);
+      mma_commit(&bar_k_empty[it % NS]);
+      for (int j = 0; j < rounds; ++j) {
+        bool v_ready = false, k_ready = false;
+        auto turn = [&](auto x_tag) -> bool {
+          constexpr int x = decltype(x_tag)::value;
+          if (j >= n[x]) return true;
+          if (!wait_p(x, j == 0)) return false;
+          if (!v_ready && !wait_v(x, it + j, j)) return false;
+          v_ready = true;
+          tc_fence_after();
+          issue_pv(x, it + j, j == 0);
+          if (j + 1 < n[x]) {
+            if (!k_ready && !wait_k(it + j + 1)) return false;
+            k_ready = true;
+            tc_fence_after();
+            scores(x_tag, it + j + 1);
+          } else {
+            mma_commit(&bar_o_full[x]);
+            ++no[x];
+          }
+          return true;
+        };
+        if (!turn(std::integral_constant<int, 0>{})) return false;
+        if (NT == 2 && !turn(std::integral_constant<int, NT - 1>{})) return false;
+        mma_commit(&bar_v_empty[(it + j) % NS]);
+        if (j + 1 < rounds) mma_commit(&bar_k_empty[(it + j + 1) % NS]);
+      }
+      it += rounds;
+      return true;
+    };
+    while (ok) {
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        if (!ok || order.left(x) > 0 || held[x] || ended[x]) continue;
+        const int sl = gets[x] & 1;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&rings[x].full[sl], (gets[x] >> 1) & 1, status)))) break;
+        ++gets[x];
+        const PrefixItem& I = rings[x].item[sl];
+        next[x] = {I.n, I.np, I.p_left, I.o_left};
+        const bool pair = I.pair != 0;
+        __syncwarp();
+        mbar_arrive(&rings[x].empty[sl]);
+        if (next[x].n < 0) ended[x] = true;
+        else if (pair) held[x] = true;
+        else order.set(x, next[x].n);
+      }
+      if (!ok) break;
+      // a stream acts while it has tiles to start or a product to finish
+      const bool act0 = order.left0 > 0 || cur[0].pend >= 0, act1 = order.left1 > 0 || cur[1].pend >= 0;
+      if (act0 || act1) {
+        const int x = (order.last == 1 ? act0 : act1) ? 1 - order.last : order.last;
+        order.last = x;
+        auto act_on = [&](auto x_tag) -> bool {
+          constexpr int y = decltype(x_tag)::value;
+          if (!step(x_tag)) return false;
+          if (order.left(y) == 0) return true;
+          if (order.left(y) == next[y].n) {  // a new item
+            cur[y].n = next[y].n;
+            cur[y].j = 0;
+            cur[y].n_pre = next[y].n_pre;
+            cur[y].p_left = next[y].p_left;
+            cur[y].o_left = next[y].o_left;
+          }
+          order.set(y, order.left(y) - 1);
+          return start(x_tag);
+        };
+        ok = x == 0 ? act_on(std::integral_constant<int, 0>{}) : act_on(std::integral_constant<int, NT - 1>{});
+      } else if (held[0]) {
+        ok = run_pair();
+        held[0] = held[1] = false;
+        order = TileOrder();
+      } else {
+        break;
+      }
     }
   } else {
     // ------------------------------------------------------------- softmax
@@ -638,23 +780,22 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
     // 1), so that the infinity put on a masked score below stays one.
     const float sl2 = p.scale_log2 == 0.f ? 1.17549435e-38f : p.scale_log2;
     const float masked = sl2 > 0.f ? -INFINITY : INFINITY;
-    int ns = 0, no = 0;  // S hand-overs and items of this tile so far
+    uint8_t* stage = sStage + warp * 2048;
+    int ns = 0, no = 0;  // S hand-overs of this stream, and items with an output, so far
     bool ok = true;
     for (int ii = 0; ok; ++ii) {
       const int sl = ii & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[sl], (ii >> 1) & 1, status));
+      ok = __all_sync(0xffffffffu, mbar_wait(&rings[x].full[sl], (ii >> 1) & 1, status));
       if (!ok) break;
-      const int item = *reinterpret_cast<volatile int*>(&ring.item[sl]);
-      const int n = items[sl].n[x], n_pre = items[sl].np, p_left = items[sl].p_left;
-      const int turns = items[sl].turns;
-      // row of the item: with turns both groups hold the same rows
-      const int r = (turns ? 0 : x * 128) + quarter * 32 + lane;
-      const bool in = r < items[sl].rows;
-      const int row = in ? items[sl].row[r] : -1, own = in ? items[sl].lim[r] : 0;
-      const bool direct = items[sl].direct != 0;
-      const size_t part = static_cast<size_t>(items[sl].part[x]) + quarter * 32 + lane;
-      mbar_arrive(&ring.empty[sl]);
-      if (item < 0) break;
+      const PrefixItem& I = rings[x].item[sl];
+      const int n = I.n, n_pre = I.np, p_left = I.p_left;
+      const int r = quarter * 32 + lane;
+      const bool in = n >= 0 && r < I.rows;
+      const int row = in ? I.row[r] : -1, own = in ? I.lim[r] : 0;
+      const bool direct = I.direct != 0;
+      const size_t part = static_cast<size_t>(I.part) + quarter * 32;  // of the warp's first row
+      mbar_arrive(&rings[x].empty[sl]);
+      if (n < 0) break;
       const bool live = row >= 0;
       const bool alive = __any_sync(0xffffffffu, live);  // no row of this warp: only hand-overs
       float m = -INFINITY, l = 0.f;
@@ -667,8 +808,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           continue;
         }
         tc_fence_after();
-        const int t = turns ? 2 * j + x : j;
-        const int left = t < n_pre ? p_left - t * BN : own - (t - n_pre) * BN;
+        const int left = j < n_pre ? p_left - j * BN : own - (j - n_pre) * BN;
         const int nvalid = live ? min(max(left, 0), BN) : 0;
         // Tiles that some row does not see whole: its masked scores become -infinity (once
         // scaled) in TMEM, 32 columns at a time, and the rest of the code knows no masks.
@@ -774,39 +914,65 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         ++no;
         tc_fence_after();
       }
-      if (alive && direct) {
-        const float inv = l > 0.f ? 1.0f / l : 0.f;
-        const size_t row_at = static_cast<size_t>(live ? row : 0);
-        const auto rows = make_row_pair(static_cast<T*>(p.out) + row_at * p.d, live);
+      if (alive) {
+        const uint32_t rows = __ballot_sync(0xffffffffu, live);
+        // 64 bytes of every row at a time go through shared memory, so that a store
+        // instruction writes eight rows' 64 bytes rather than 32 rows' 16: a 16-byte piece
+        // of row r is kept at piece ^ (r / 2 % 4), which spreads both sides over all banks.
+        auto store64 = [&](const uint32_t (&w)[16], auto&& put) {
 #pragma unroll
-        for (int c0 = 0; c0 < kD; c0 += 16) {
-          uint32_t o[16];
-          if (n > 0) {
-            tmem_ld16(t_o + c0, o);
-            tmem_ld_wait();
+          for (int c = 0; c < 4; ++c)
+            st_shared_v4(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2],
+                         w[4 * c + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (((rows >> (8 * k)) & 0xffu) == 0) continue;
+            const int rr = 8 * k + (lane >> 2), c = lane & 3;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+            put(rr, c, v);
           }
-          // a row without a key: zeros, whatever TMEM holds
+          __syncwarp();
+        };
+        if (direct) {
+          const float inv = l > 0.f ? 1.0f / l : 0.f;
+#pragma unroll 1
+          for (int c0 = 0; c0 < p.d; c0 += 32) {
+            uint32_t o[32], w[16];
+            if (n > 0) {
+              tmem_ld32(t_o + c0, o);
+              tmem_ld_wait();
+            }
+            // a row without a key: zeros, whatever TMEM holds
 #pragma unroll
-          for (int c = 0; c < 16; ++c) o[c] = n > 0 && l > 0.f ? o[c] : 0u;
-          store_pair16<kBF16>(rows, c0, p.d, o, inv);
-        }
-        if (live) p.lse[row_at] = l > 0.f ? m * 0.69314718055994531f + logf(l) : -INFINITY;
-      } else if (alive) {
-        if (live && bounds_ok(part < static_cast<size_t>(p.cap_rows), status)) {
-          p.part_ml[part] = make_float2(m, l);
-        }
-        if (n > 0) {
-          float* dst = p.part_o + part * p.d;
+            for (int c = 0; c < 16; ++c)
+              w[c] = n > 0 && l > 0.f
+                         ? pack2<kBF16>(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv)
+                         : 0u;
+            store64(w, [&](int rr, int c, const uint4& v) {
+              const int at = __shfl_sync(0xffffffffu, row, rr);
+              if (at >= 0 && c0 + 8 * c < p.d)
+                *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + static_cast<size_t>(at) * p.d + c0 + 8 * c) = v;
+            });
+          }
+          if (live) p.lse[row] = l > 0.f ? m * 0.69314718055994531f + logf(l) : -INFINITY;
+        } else {
+          if (live && bounds_ok(part + lane < static_cast<size_t>(p.cap_rows), status))
+            p.part_ml[part + lane] = make_float2(m, l);
+          if (n > 0) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < p.d; c0 += 32) {
+              uint32_t o[2][16];
+              tmem_ld16(t_o + c0, o[0]);
+              tmem_ld16(t_o + c0 + 16, o[1]);
+              tmem_ld_wait();
 #pragma unroll
-          for (int c0 = 0; c0 < kD; c0 += 16) {
-            uint32_t o[16];
-            tmem_ld16(t_o + c0, o);
-            tmem_ld_wait();
-            if (live && bounds_ok(part < static_cast<size_t>(p.cap_rows), status)) {
-#pragma unroll
-              for (int c = 0; c < 16; c += 4)
-                if (c0 + c < p.d)
-                  *reinterpret_cast<uint4*>(dst + c0 + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+              for (int u = 0; u < 2; ++u)
+                store64(o[u], [&](int rr, int c, const uint4& v) {
+                  const int col = c0 + 16 * u + 4 * c;
+                  if (((rows >> rr) & 1u) && col < p.d && bounds_ok(part + rr < static_cast<size_t>(p.cap_rows), status))
+                    *reinterpret_cast<uint4*>(p.part_o + (part + rr) * p.d + col) = v;
+                });
             }
           }
         }
@@ -830,21 +996,26 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
 template <int kD, bool kBF16>
 static cudaError_t launch_fwd_impl(const PrefixParams& p, int num_sms, cudaStream_t st) {
   using S = PrefixShape<kD>;
-  CUtensorMap tk, tv, tkp, tvp;
+  PrefixMaps tm;
   // an absent tensor's map is never used: any valid address will do
   const void* any = p.total_kv > 0 ? p.k : p.kp;
   const bool own = p.total_kv > 0, pre = p.prefix_rows > 0;
-  if (!make_tmap_tokens(&tk, own ? p.k : any, own ? p.total_kv : 1, 1, p.hkv, p.d, kBF16, S::kBN) ||
-      !make_tmap_tokens(&tv, own ? p.v : any, own ? p.total_kv : 1, 1, p.hkv, p.d, kBF16, S::kBN) ||
-      !make_tmap_tokens(&tkp, pre ? p.kp : any, pre ? p.prefix_rows : 1, 1, p.hkv, p.d, kBF16, S::kBN) ||
-      !make_tmap_tokens(&tvp, pre ? p.vp : any, pre ? p.prefix_rows : 1, 1, p.hkv, p.d, kBF16, S::kBN))
+  tm.q_tokens = 128 % p.group == 0 ? 128 / p.group : 0;
+  const int whole = tm.q_tokens > 0 ? p.group : 1, token = p.group <= 128 ? p.group : 1;
+  if (!make_tmap_tokens(&tm.k, own ? p.k : any, own ? p.total_kv : 1, 1, p.hkv, p.d, kBF16, S::kBN) ||
+      !make_tmap_tokens(&tm.v, own ? p.v : any, own ? p.total_kv : 1, 1, p.hkv, p.d, kBF16, S::kBN) ||
+      !make_tmap_tokens(&tm.kp, pre ? p.kp : any, pre ? p.prefix_rows : 1, 1, p.hkv, p.d, kBF16, S::kBN) ||
+      !make_tmap_tokens(&tm.vp, pre ? p.vp : any, pre ? p.prefix_rows : 1, 1, p.hkv, p.d, kBF16, S::kBN) ||
+      !make_tmap_tokens(&tm.q_tile, p.q, p.total_q, 1, p.hq, p.d, kBF16, 128, whole) ||
+      !make_tmap_tokens(&tm.q_token, p.q, p.total_q, 1, p.hq, p.d, kBF16, token, token) ||
+      !make_tmap_tokens(&tm.q_row, p.q, p.total_q, 1, p.hq, p.d, kBF16, 1, 1))
     return cudaErrorInvalidValue;
   auto kern = attn_prefix_fwd_kernel<kD, kBF16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const long long most = static_cast<long long>(p.cap_entries) * p.hkv;
   return launch_dependent(kern, static_cast<unsigned>(most < num_sms ? most : num_sms), S::kThreads, S::kSmemBytes, st,
-                          p, tk, tv, tkp, tvp);
+                          p, tm);
 }
 
 cudaError_t launch_prefix_fwd(const PrefixParams& p, bool bf16, int num_sms, cudaStream_t st) {
@@ -913,7 +1084,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
       if (pre_chunks > 0) {
         const int rr = (info.x + i) * p.group + j, u = rr / rt;
         const int rows = min(rt, pre_rows - u * rt);
-        na = pre_chunks * (rows <= rt / 2 ? rt / 128 : 1);
+        na = pre_chunks;
         a0 = static_cast<size_t>(pre_slot) + static_cast<size_t>(u) * rt * pre_chunks * p.hkv +
              partial_offset(p, rows, 0, g) + rr % rt;
         astep = partial_offset(p, rows, 1, 0);

@@ -68,12 +68,11 @@ PrefixParams base_params(const void* q, const void* k, const void* v, const void
 // tokens, long row tiles, entries, partial rows (maximum and sum; d fp32 columns). The
 // capacities follow from sum_b Lq_b <= total_q: with T chunks aimed at and row tiles of R rows,
 //   long row tiles <= total_q G / R + batch,   entries <= T + 2 (total_q G / R + batch + 1)
-//   partial rows of a kv head <= 2 R T + 3 min(total_q G, 128 batch) + 128:
-// a group of n key tiles has at most n / len + 1 chunks, sum n / len <= T, a chunk leaves
-// at most R partial rows (two parts only of at most R / 2 rows), rows of short sequences
-// (at most 128 each) are in a prefix group, of which only the last leaves two parts, and in
-// an own one, and a long group leaves partial rows only with two chunks or more, when
-// n / len + 1 <= 2 n / len.
+//   partial rows of a kv head <= 2 R T + 2 min(total_q G, 128 batch):
+// a row tile of n key tiles has at most n / len + 1 chunks, sum n / len <= T, a chunk leaves
+// at most R partial rows, rows of short sequences (at most 128 each) are in a compact row
+// tile and in one of their own, and a long row tile leaves partial rows only with two chunks
+// or more, when n / len + 1 <= 2 n / len.
 struct FwdLayout {
   size_t seqs, short_tok, longs, entries, part_ml, part_o, total;
   int parts_target;
@@ -89,7 +88,7 @@ bool fwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, i
   L->cap_longs = rows / rt + batch;
   L->cap_entries = L->parts_target + 2 * (L->cap_longs + 1);
   const long long few = static_cast<long long>(kShortRows) * batch;
-  L->cap_rows = hkv * (2 * rt * L->parts_target + 3 * (rows < few ? rows : few) + 128);
+  L->cap_rows = hkv * (2 * rt * L->parts_target + 2 * (rows < few ? rows : few));
   if (L->cap_rows > INT32_MAX || L->cap_entries * hkv > INT32_MAX) return false;
   size_t off = kHdrWords * sizeof(int);
   auto take = [&off](size_t bytes) {
