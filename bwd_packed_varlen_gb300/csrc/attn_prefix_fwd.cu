@@ -290,7 +290,8 @@ struct PrefixItem {
 };
 struct ItemRing {
   PrefixItem item[2];
-  uint64_t full[2], empty[2];
+  // kv: all but the rows is there (the K/V warp starts on that); full: the rows too
+  uint64_t kv[2], full[2], empty[2];
 };
 
 // The order of key tiles over the streams, in which the K/V warp loads and the MMA warp
@@ -350,6 +351,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       mbar_init(&bar_o_full[x], 1);
       mbar_init(&bar_o_empty[x], 128);
       for (int i = 0; i < 2; ++i) {
+        mbar_init(&rings[x].kv[i], 1);
         mbar_init(&rings[x].full[i], 1);
         mbar_init(&rings[x].empty[i], 1 + 32 + 128);  // K/V warp's lane 0, MMA warp, softmax
       }
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         x0 = x1 = NT == 1 || order.left0 == 0 ? 0 : 1;
         order.set(x0, tiles(0));
       }
-      // rows: where they lie and what they see (all loads in flight at once)
+      // rows: where they lie (all loads in flight at once)
       int tok[NT][4];
 #pragma unroll
       for (int k = 0; k < NT; ++k)
@@ -426,20 +428,10 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       for (int k = 0; k < NT; ++k) {
         const int x = x0 + k, r0 = k * 128;  // row tile k of the item goes to stream x
         if (x > x1 || !ok) continue;
-        const int rows = min(128, e.rows - r0);
         // the slot's last readers are done with it
         if (!(ok = wait_slot(x))) break;
-        PrefixItem& I = rings[x].item[puts(x) & 1];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = u * 32 + lane;
-          if (u * 32 >= rows) break;
-          const int rr = e.row0 + r0 + r, i = rr / p.group, j = rr - i * p.group;
-          const bool in = r < rows && bounds_ok(tok[k][u] >= 0 && tok[k][u] < p.total_q, status);
-          I.row[r] = in ? tok[k][u] * p.hq + h * p.group + j : -1;
-          I.lim[r] = in && e.seq >= 0 ? max(0, keys_seen(p.causal, e.len_k, e.diag, i) - o0 * BN) : 0;
-        }
         if (lane == 0) {
+          PrefixItem& I = rings[x].item[puts(x) & 1];
           I.n = tiles(k);
           I.pair = pair ? 1 : 0;
           I.np = np;
@@ -450,7 +442,25 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           I.direct = e.slot < 0 ? 1 : 0;
           I.head = h;
           I.part = e.slot < 0 ? 0 : e.slot + static_cast<int>(partial_offset(p, e.rows, 0, h)) + r0;
-          I.rows = rows;
+          I.rows = min(128, e.rows - r0);
+          mbar_arrive(&rings[x].kv[puts(x) & 1]);
+        }
+      }
+      // the rows' places and what they see
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        const int x = x0 + k, r0 = k * 128;
+        if (x > x1 || !ok) continue;
+        const int rows = min(128, e.rows - r0);
+        PrefixItem& I = rings[x].item[puts(x) & 1];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = u * 32 + lane;
+          if (u * 32 >= rows) break;
+          const int rr = e.row0 + r0 + r, i = rr / p.group, j = rr - i * p.group;
+          const bool in = r < rows && bounds_ok(tok[k][u] >= 0 && tok[k][u] < p.total_q, status);
+          I.row[r] = in ? tok[k][u] * p.hq + h * p.group + j : -1;
+          I.lim[r] = in && e.seq >= 0 ? max(0, keys_seen(p.causal, e.len_k, e.diag, i) - o0 * BN) : 0;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&rings[x].full[puts(x) & 1]);
@@ -506,6 +516,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       if (!(ok = wait_slot(x))) break;
       if (lane == 0) {
         rings[x].item[puts(x) & 1].n = -1;
+        mbar_arrive(&rings[x].kv[puts(x) & 1]);
         mbar_arrive(&rings[x].full[puts(x) & 1]);
       }
     }
@@ -545,7 +556,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         for (int x = 0; x < NT; ++x) {
           if (!ok || order.left(x) > 0 || held[x] || ended[x]) continue;
           const int sl = gets[x] & 1;
-          if (!(ok = mbar_wait(&rings[x].full[sl], (gets[x] >> 1) & 1, status))) break;
+          if (!(ok = mbar_wait(&rings[x].kv[sl], (gets[x] >> 1) & 1, status))) break;
           ++gets[x];
           const PrefixItem& I = rings[x].item[sl];
           const int n = I.n;
@@ -809,7 +820,8 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         }
         tc_fence_after();
         const int left = j < n_pre ? p_left - j * BN : own - (j - n_pre) * BN;
-        const int nvalid = live ? min(max(left, 0), BN) : 0;
+        // (a lane without a row masks nothing: an offset of infinity keeps its P at zero)
+        const int nvalid = live ? min(max(left, 0), BN) : BN;
         // Tiles that some row does not see whole: its masked scores become -infinity (once
         // scaled) in TMEM, 32 columns at a time, and the rest of the code knows no masks.
         // These rare steps are rolled loops: unrolled, with a masked copy of the pass below,
@@ -844,16 +856,15 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         };
         // A row's first tile with a visible key: the max of its first 32 scores starts the
         // offset m; should a later one exceed it by 2^8, the raise below catches it.
-        if (__any_sync(0xffffffffu, m == -INFINITY && nvalid > 0)) {
+        if (__any_sync(0xffffffffu, live && m == -INFINITY && nvalid > 0)) {
           const float mxs = max_of(32);
-          if (m == -INFINITY && nvalid > 0) m = mxs;
+          if (live && m == -INFINITY && nvalid > 0) m = mxs;
         }
         float alpha = 1.f;
         uint64_t sp[4];
         uint32_t pk[BN / 32][16];
         // a row that has seen no key yet: any finite offset makes its P zeros
-        const float off = m == -INFINITY ? 0.f : m;
-        float neg = -off;
+        float neg = !live ? -INFINITY : m == -INFINITY ? 0.f : -m;
         for (;;) {
           const uint64_t sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(neg, neg);
 #pragma unroll
@@ -876,7 +887,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           const float2 s01 = f2_unpack(fadd2(fadd2(sp[0], sp[1]), fadd2(sp[2], sp[3])));
           if (!__any_sync(0xffffffffu, s01.x + s01.y > 256.0f)) break;
           const float mxs = max_of(BN);
-          const bool raise = nvalid > 0 && mxs > m + 8.0f;
+          const bool raise = live && nvalid > 0 && mxs > m + 8.0f;
           if (!__any_sync(0xffffffffu, raise)) break;
           if (raise) {
             // a row without an earlier key has nothing to scale (and l is 0)
