@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
   __shared__ int buf[3][32];
   __shared__ int bad;
   __shared__ unsigned long long work, tokens;
+  __shared__ int s_tiles[kPrefixSchedThreads], s_order[kPrefixSchedThreads];
   pdl_trigger();
   const int rt = prefix_row_tile(p.d), bn = prefix_key_tile(p.d), tid = threadIdx.x, lane = tid & 31;
   if (tid == 0) {
@@ -70,8 +71,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
   }
   const int np_keys = prefix_keys(p), np = div_up(np_keys, bn);
   __syncthreads();
-  // sequences: compact tokens, long row tiles; an upper bound of the key tiles. With at
-  // most a thread per sequence, `s` stays for the later phases.
+  // sequences: compact tokens, long row tiles; an upper bound of the key tiles
   SeqInfo s{};
   int n_tok = 0, n_long = 0, first_tok = 0, first_long = 0;
   for (int base = 0; base < p.batch; base += blockDim.x) {
@@ -188,27 +188,41 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
   }
   n_entries += n_pre * pre_chunks;
   n_rows += short_rows * pre_chunks * p.hkv;
-  // short sequences against their own keys
+  // Short sequences against their own keys, the longest first (with at most a thread per
+  // sequence): the blocks then run out of work together. A sequence's place is the number of
+  // sequences that go before it.
+  const bool sorted = p.batch <= blockDim.x;
+  if (sorted) {
+    const int n = first_tok >= 0 ? own_tiles(p, s.len_k, s.diag, 0, s.len_q * p.group, bn) : -1;
+    s_tiles[tid] = n;
+    __syncthreads();
+    int place = 0;
+    for (int j = 0; j < p.batch; ++j) {
+      const int o = s_tiles[j];
+      place += o > n || (o == n && j < tid) ? 1 : 0;
+    }
+    if (tid < p.batch) s_order[place] = tid;
+    __syncthreads();
+  }
   for (int base = 0; base < p.batch; base += blockDim.x) {
-    const int b = base + tid;
-    if (p.batch > blockDim.x) {  // otherwise this thread's sequence is still at hand
-      s = SeqInfo{};
-      first_tok = -1;
-      if (b < p.batch) {
-        s = load_seq(p, b);
-        first_tok = p.seqs[b].x;
-      }
+    const int at_b = base + tid;
+    const int b = at_b < p.batch ? (sorted ? s_order[tid] : at_b) : p.batch;
+    SeqInfo q{};
+    int first = -1;
+    if (b < p.batch) {
+      q = load_seq(p, b);
+      first = p.seqs[b].x;
     }
     PrefixEntry e{};
     int n = 0, ch = 0, slots = 0;
-    if (b < p.batch && first_tok >= 0) {
+    if (first >= 0) {
       e.seq = b;
-      e.rows = s.len_q * p.group;
-      e.off_q = s.off_q;
-      e.off_k = s.off_k;
-      e.len_k = s.len_k;
-      e.diag = s.diag;
-      n = own_tiles(p, s.len_k, s.diag, 0, e.rows, bn);
+      e.rows = q.len_q * p.group;
+      e.off_q = q.off_q;
+      e.off_k = q.off_k;
+      e.len_k = q.len_k;
+      e.diag = q.diag;
+      n = own_tiles(p, q.len_k, q.diag, 0, e.rows, bn);
       ch = div_up(n, len);
       // without a prefix a single chunk is the whole result
       slots = ch > 1 || n_pre > 0 ? ch * p.hkv * e.rows : 0;
@@ -216,7 +230,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
     const Scan3 at = block_scan3(ch, slots, 0, buf);
     if (ch > 0) {
       e.slot = slots > 0 ? n_rows + at.y : -1;
-      p.seqs[b] = make_int4(first_tok, e.slot, slots > 0 ? ch : -1, 0);
+      p.seqs[b] = make_int4(first, e.slot, slots > 0 ? ch : -1, 0);
       for (int c = 0; c < ch; ++c) put_chunk(e, n, ch, c, n_entries + at.x + c);
     }
     n_entries += at.tx;
@@ -295,9 +309,11 @@ struct ItemRing {
 };
 
 // The order of key tiles over the streams, in which the K/V warp loads and the MMA warp
-// issues them: streams that have tiles left alternate, a stream that runs out takes the
-// next item at once, and an item for both waits until both have run out. The item warp
-// follows the same counts to know which stream that is.
+// issues them, one tile a step: before a step one stream without tiles, if there is one,
+// takes the next item (the one whose turn it is before the other), then the streams with
+// tiles alternate. An item for both streams waits until both have run out. The item warp
+// follows the same counts to know which stream takes an item. (One item a step: the first
+// item's loads do not wait for the second one to be decoded.)
 struct TileOrder {
   int left0 = 0, left1 = 0;  // key tiles that each stream has left (scalars: no local memory)
   int last = 1;
@@ -311,6 +327,11 @@ struct TileOrder {
     last = x;
   }
   __device__ __forceinline__ int next() const { return left(1 - last) > 0 ? 1 - last : last; }
+  // Stream that takes the next item before this step; -1: none.
+  __device__ __forceinline__ int wants(bool able0, bool able1) const {
+    const bool w0 = left0 == 0 && able0, w1 = left1 == 0 && able1;
+    return last == 1 ? (w0 ? 0 : w1 ? 1 : -1) : (w1 ? 1 : w0 ? 0 : -1);
+  }
 };
 
 template <int kD, bool kBF16>
@@ -409,9 +430,10 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       if (pair) {
         order = TileOrder();
       } else {
-        while (order.left0 > 0 && order.left1 > 0) order.take(order.next());
-        x0 = x1 = NT == 1 || order.left0 == 0 ? 0 : 1;
+        while (NT == 2 && order.wants(true, true) < 0) order.take(order.next());
+        x0 = x1 = NT == 2 ? order.wants(true, true) : 0;
         order.set(x0, tiles(0));
+        order.take(order.next());
       }
       // rows: where they lie (all loads in flight at once)
       int tok[NT][4];
@@ -552,9 +574,10 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         return true;
       };
       while (ok) {
+        const int w = order.wants(!held[0] && !ended[0], !held[1] && !ended[1]);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-          if (!ok || order.left(x) > 0 || held[x] || ended[x]) continue;
+          if (x != w) continue;
           const int sl = gets[x] & 1;
           if (!(ok = mbar_wait(&rings[x].kv[sl], (gets[x] >> 1) & 1, status))) break;
           ++gets[x];
@@ -577,11 +600,11 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           const int x = order.next();
           order.take(x);
           ok = x ? load_tile(cur[1]) : load_tile(cur[0]);
-        } else if (held[0]) {
+        } else if (held[0] && held[1]) {
           for (int j = max(pair_n[0], pair_n[1]); j > 0 && ok; --j) ok = load_tile(cur[0]);
           held[0] = held[1] = false;
           order = TileOrder();
-        } else {
+        } else if (w < 0) {
           break;
         }
       }
@@ -736,9 +759,10 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       return true;
     };
     while (ok) {
+      const int w = order.wants(!held[0] && !ended[0], !held[1] && !ended[1]);
 #pragma unroll
       for (int x = 0; x < NT; ++x) {
-        if (!ok || order.left(x) > 0 || held[x] || ended[x]) continue;
+        if (x != w) continue;
         const int sl = gets[x] & 1;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&rings[x].full[sl], (gets[x] >> 1) & 1, status)))) break;
         ++gets[x];
@@ -772,11 +796,11 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           return start(x_tag);
         };
         ok = x == 0 ? act_on(std::integral_constant<int, 0>{}) : act_on(std::integral_constant<int, NT - 1>{});
-      } else if (held[0]) {
+      } else if (held[0] && held[1]) {
         ok = run_pair();
         held[0] = held[1] = false;
         order = TileOrder();
-      } else {
+      } else if (w < 0) {
         break;
       }
     }
