@@ -127,8 +127,10 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
   const int short_rows = n_tok * p.group;
   const int n_pre = np > 0 ? div_up(short_rows, rt) : 0;
   const unsigned long long all = work + static_cast<unsigned long long>(n_pre) * np;
-  // chunk length in key tiles: all heads' chunks together about parts_target * hkv
-  const int len = static_cast<int>(max(1ull, (all + p.parts_target - 1) / p.parts_target));
+  // Chunk length in key tiles: all heads' chunks together about one per SM when there is
+  // little to do (an item costs about four tiles before its first), two when there is much.
+  const int parts = all >= 8ull * p.parts_target ? p.parts_target : (p.parts_target + 1) / 2;
+  const int len = static_cast<int>(max(1ull, (all + parts - 1) / parts));
   int n_entries = 0, n_rows = 0;  // running totals
   // Chunk c of a row tile with n key tiles in `chunks` chunks (they differ by one tile at
   // most), as entry `at`; e.slot: the row tile's first partial row.
@@ -352,12 +354,14 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
   __shared__ uint64_t bar_k_full[NS], bar_k_empty[NS], bar_v_full[NS], bar_v_empty[NS];
   __shared__ uint64_t bar_s_full[NT], bar_p_ready[NT], bar_o_full[NT], bar_o_empty[NT];
   __shared__ ItemRing rings[NT];
+  __shared__ int tiles_loaded;  // by the K/V warp, for the item warp to keep pace with
   __shared__ uint32_t tmem_slot;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* status = p.header + kHdrStatus;
 
   if (tid == 0) {
+    tiles_loaded = 0;
     for (int i = 0; i < NS; ++i) {
       mbar_init(&bar_k_full[i], 1);
       mbar_init(&bar_k_empty[i], 1);
@@ -410,12 +414,40 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       const int n = puts(x);
       return n < 2 || __all_sync(0xffffffffu, mbar_wait(&rings[x].empty[n & 1], ((n >> 1) - 1) & 1, status));
     };
+    // An item is taken from the common list only when the tiles before it are loaded but for
+    // kAhead: enough to hide its decoding, and no more, since a block that takes items early
+    // may sit on them while others have run out.
+    constexpr int kAhead = 4;
+    int emitted = 0;  // tiles in the order so far
+    auto keep_pace = [&]() -> bool {
+      const volatile int* loaded = &tiles_loaded;
+      if (emitted - *loaded <= kAhead) return true;
+      const unsigned long long t0 = global_ns();
+      for (uint32_t it = 1;; ++it) {
+        __nanosleep(100);
+        if (emitted - *loaded <= kAhead) return true;
+        if ((it & 63u) == 0) {
+          if (*reinterpret_cast<volatile int*>(status) & kErrTimeout) return false;
+          if (global_ns() - t0 > kWaitLimitNs) {
+            atomicOr(status, kErrTimeout);
+            return false;
+          }
+        }
+      }
+    };
     for (int ii = 0;; ++ii) {
+      while (NT == 2 && order.wants(true, true) < 0) {
+        order.take(order.next());
+        ++emitted;
+      }
+      if (ii > 0) {
+        if (!(ok = __all_sync(0xffffffffu, keep_pace()))) break;
+        if (lane == 0) nxt = next_item(p.header + kHdrNextFwd);
+        nxt = __shfl_sync(0xffffffffu, nxt, 0);
+      }
       const int item = nxt < n_items ? nxt : -1;
       if (item < 0) break;
-      if (lane == 0) nxt = next_item(p.header + kHdrNextFwd);
       const PrefixEntry e = ii == 0 ? first : load_entry(p, item / p.hkv);
-      nxt = __shfl_sync(0xffffffffu, nxt, 0);
       const int h = item % p.hkv;
       const int np = max(0, min(e.t1, e.np) - e.t0);  // prefix tiles of the chunk
       const int o0 = max(0, e.t0 - e.np);             // first own tile
@@ -428,12 +460,15 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       };
       int x0 = 0, x1 = NT - 1;
       if (pair) {
+        emitted += order.left0 + order.left1 + max(tiles(0), tiles(1));
         order = TileOrder();
-      } else {
-        while (NT == 2 && order.wants(true, true) < 0) order.take(order.next());
-        x0 = x1 = NT == 2 ? order.wants(true, true) : 0;
+      } else if (NT == 2) {
+        x0 = x1 = order.wants(true, true);
         order.set(x0, tiles(0));
         order.take(order.next());
+        ++emitted;
+      } else {
+        emitted += tiles(0);
       }
       // rows: where they lie (all loads in flight at once)
       int tok[NT][4];
@@ -515,18 +550,26 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           if (lane < S::kChunks)
             tma_load_4d(q_tile + lane * 16384, &tm.q_tile, &bar_q_full[x], lane * 64, h * p.group, 0, first_tok);
         } else {
-          for (int i = i0 + lane; i <= i1; i += 32) {
-            const int t = e.seq < 0 ? p.short_tok[i] : e.off_q + i;
-            const int ra = i * p.group - rr0;  // the token's first row here
-            if (p.group <= 128 && ra >= 0 && ra + p.group <= rows) {
+          // this lane's tokens, whole ones, then the rows of the first and last one if cut
+          const int lead = i0 * p.group < rr0 ? (i0 + 1) * p.group - rr0 : 0;
+          const int tail = (i1 + 1) * p.group > rr0 + rows ? rr0 + rows - max(i1 * p.group, rr0 + lead) : 0;
+          const bool boxes = p.group <= 128;
+          const int w0 = i0 + (lead > 0 ? 1 : 0), w1 = i1 - (tail > 0 ? 1 : 0);
+          if (boxes) {
+            for (int i = w0 + lane; i <= w1; i += 32) {
+              const int t = e.seq < 0 ? p.short_tok[i] : e.off_q + i;
               for (int c = 0; c < S::kChunks; ++c)
-                tma_load_4d(q_tile + c * 16384 + ra * 128, &tm.q_token, &bar_q_full[x], c * 64, h * p.group, 0, t);
-            } else {
-              for (int r = max(ra, 0); r < min(ra + p.group, rows); ++r)
-                for (int c = 0; c < S::kChunks; ++c)
-                  tma_load_4d(q_tile + c * 16384 + r * 128, &tm.q_row, &bar_q_full[x], c * 64,
-                              h * p.group + r - ra, 0, t);
+                tma_load_4d(q_tile + c * 16384 + (i * p.group - rr0) * 128, &tm.q_token, &bar_q_full[x], c * 64,
+                            h * p.group, 0, t);
             }
+          }
+          const int whole_rows = boxes ? max(0, w1 - w0 + 1) * p.group : 0;
+          for (int z = lane; z < rows - whole_rows; z += 32) {
+            const int r = !boxes || z < lead ? z : z + whole_rows;
+            const int i = (rr0 + r) / p.group, t = e.seq < 0 ? p.short_tok[i] : e.off_q + i;
+            for (int c = 0; c < S::kChunks; ++c)
+              tma_load_4d(q_tile + c * 16384 + r * 128, &tm.q_row, &bar_q_full[x], c * 64, rr0 + r - i * p.group + h * p.group,
+                          0, t);
           }
         }
         __syncwarp();
@@ -570,7 +613,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         for (int k = 0; k < S::kChunks; ++k)
           tma_load_4d(sV + st * S::kKVBytes + k * BN * 128, mv, &bar_v_full[st], k * 64, c.h, 0, key);
         ++c.j;
-        ++it;
+        *const_cast<volatile int*>(&tiles_loaded) = ++it;
         return true;
       };
       while (ok) {
