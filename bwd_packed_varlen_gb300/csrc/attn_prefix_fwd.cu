@@ -424,9 +424,9 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       if (emitted - *loaded <= kAhead) return true;
       const unsigned long long t0 = global_ns();
       for (uint32_t it = 1;; ++it) {
-        __nanosleep(100);
+        __nanosleep(400);
         if (emitted - *loaded <= kAhead) return true;
-        if ((it & 63u) == 0) {
+        if ((it & 15u) == 0) {
           if (*reinterpret_cast<volatile int*>(status) & kErrTimeout) return false;
           if (global_ns() - t0 > kWaitLimitNs) {
             atomicOr(status, kErrTimeout);
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         ++emitted;
       }
       if (ii > 0) {
-        if (!(ok = __all_sync(0xffffffffu, keep_pace()))) break;
+        if (!(ok = __all_sync(0xffffffffu, lane > 0 || keep_pace()))) break;
         if (lane == 0) nxt = next_item(p.header + kHdrNextFwd);
         nxt = __shfl_sync(0xffffffffu, nxt, 0);
       }
