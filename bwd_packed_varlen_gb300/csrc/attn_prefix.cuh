@@ -96,7 +96,8 @@ __device__ __forceinline__ int prefix_keys(const PrefixParams& p) {
 // written directly, the others leave partial results that the join kernel merges.
 // ---------------------------------------------------------------------------
 constexpr int kShortRows = 128;
-constexpr int kPartsTarget = 2 * 152;  // chunks over all kv heads, about: two per SM
+constexpr int kSMs = 152;             // of the GPU that work is cut for
+constexpr int kPartsTarget = 2 * kSMs;  // chunks over all kv heads, about: two per SM
 
 __host__ __device__ constexpr int prefix_row_tile(int d) { return d <= 128 ? 256 : 128; }
 __host__ __device__ constexpr int prefix_key_tile(int d) { return d <= 128 ? 128 : 64; }
@@ -134,8 +135,6 @@ __device__ __forceinline__ size_t partial_offset(const PrefixParams& p, int rows
 // lse is taken as infinite, so P is 0); with few key tiles the sweep is split, each part
 // leaving fp32 partial sums that a reduction adds in order.
 // ---------------------------------------------------------------------------
-constexpr int kBwdItemsTarget = 3 * 152;  // prefix items of the dK/dV kernel, about
-
 struct PrefixBwd : PrefixParams {
   CUtensorMap tm_kp, tm_vp;
   int pack_shift;

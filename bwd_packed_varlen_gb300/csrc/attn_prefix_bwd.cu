@@ -92,85 +92,104 @@ __device__ __forceinline__ void zero_rows(void* base, size_t row, int bytes) {
   for (int i = threadIdx.x & 31; i < bytes / 16; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
 }
 
+constexpr int kPrepRows = 8, kPrepHeads = 128;  // rows of a block at a time, heads of a pass
+
 template <bool kBF16>
 __global__ void __launch_bounds__(256) prefix_prep_kernel(const __grid_constant__ PrefixBwd p) {
   __shared__ int s_q[kCachedOffsets], s_k[kCachedOffsets];
+  __shared__ float s_lse[kPrepHeads][kPrepRows + 1], s_delta[kPrepHeads][kPrepRows + 1];
+  __shared__ long long s_tile[kPrepRows];  // index of a row's head 0 in the tiles; -1: in none
   const int* q_pad = cache_offsets(p.cu_q_pad, p.batch, s_q);
   const int* k_pad = cache_offsets(p.cu_kv_pad, p.batch, s_k);
-  const long long warps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
-  const long long gw = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31, sh = p.pack_shift, mask = (1 << sh) - 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sh = p.pack_shift;
   const bool causal = p.causal != 0, prefix = prefix_keys(p) > 0;
   constexpr float kLog2e = 1.4426950408889634f;
   const int cpr = p.d / 8;  // 16-byte chunks per head
-  const int chunks = p.hq * cpr;
   pdl_trigger();
   pdl_wait();  // pref_q and the header
   // more tiles than the lists hold (overlapping sequences): no row is a token
   const bool none = p.header[kHdrNumQPairs] != p.pref_q[p.batch];
-  // linear rows past the tensor's last one
-  const long long first = static_cast<long long>(p.total_q) << sh, pad = p.rows_lin - first;
-  for (long long z = gw * 32 + lane; z < pad * p.vheads; z += warps * 32) {
-    const size_t at = static_cast<size_t>(z / pad) * p.rows_lin + first + z % pad;
-    p.lse_lin[at] = -INFINITY;
-    p.delta_lin[at] = 0.f;
-  }
-  for (long long r = gw; r < p.total_q; r += warps) {
+  // blocks of rows, up to the linear rows past the tensor's last one
+  const long long rows_end = p.rows_lin >> sh;
+  for (long long r0 = static_cast<long long>(blockIdx.x) * kPrepRows; r0 < rows_end;
+       r0 += static_cast<long long>(gridDim.x) * kPrepRows) {
+    const long long r = r0 + warp;
+    const size_t row = static_cast<size_t>(r);
     int i = 0;
-    const int b = none ? -1 : locate_row(p, q_pad, static_cast<int>(r), &i);
+    const int b = none || r >= p.total_q ? -1 : locate_row(p, q_pad, static_cast<int>(r), &i);
     SeqInfo s{};
     if (b >= 0) s = load_seq(p, b);
-    const size_t row = static_cast<size_t>(r);
-    auto linear = [&](int h) { return static_cast<size_t>(h >> sh) * p.rows_lin + (row << sh) + (h & mask); };
     const bool real = b >= 0 && i < s.len_q;
     // rows that see no key: their tiles leave dq to this kernel
-    if (!real || (!prefix && row_keys(s, i, causal) == 0)) zero_rows(p.dq, row, p.hq * p.d * 2);
-    if (!real || (!prefix && s.len_k == 0)) {
-      for (int h = lane; h < p.hq; h += 32) {
-        p.lse_lin[linear(h)] = -INFINITY;
-        p.delta_lin[linear(h)] = 0.f;
+    if (r < p.total_q && (!real || (!prefix && row_keys(s, i, causal) == 0))) zero_rows(p.dq, row, p.hq * p.d * 2);
+    const bool read = real && (prefix || s.len_k > 0);  // some tile reads this row
+    if (lane == 0) s_tile[warp] = read ? static_cast<long long>(packed_index(p, b, i << sh, 0)) : -1;
+    for (int h0 = 0; h0 < p.hq; h0 += kPrepHeads) {
+      const int nh = min(kPrepHeads, p.hq - h0);
+      for (int h = lane; h < nh; h += 32) {
+        s_lse[h][warp] = read ? -(p.lse_in[row * p.hq + h0 + h] * kLog2e) : -INFINITY;
+        s_delta[h][warp] = 0.f;
       }
-      continue;
-    }
-    // index of head h in the tiles
-    const size_t t0 = packed_index(p, b, i << sh, 0);
-    auto tiled = [&](int h) { return t0 + static_cast<size_t>(h >> sh) * kBlockM + (h & mask); };
-    if (!bounds_ok(tiled(p.hq - 1) < static_cast<size_t>(p.pair_cap_q) * p.vheads * kBlockM, p.header + kHdrStatus))
-      continue;
-    auto put = [&](int h, float v) { p.delta_t[tiled(h)] = p.delta_lin[linear(h)] = v; };
-    for (int h = lane; h < p.hq; h += 32)
-      p.lse_t[tiled(h)] = p.lse_lin[linear(h)] = -(p.lse_in[row * p.hq + h] * kLog2e);
-    const uint4* o = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.out_in) + row * p.hq * p.d);
-    const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dout) + row * p.hq * p.d);
-    if (32 % cpr == 0) {
-      // the lanes of a head are neighbours and add up by shuffles
-      for (int c0 = 0; c0 < chunks; c0 += 128) {
-        uint4 oa[4], ga[4];
+      __syncwarp();
+      if (read) {
+        const size_t at = (row * p.hq + h0) * p.d;
+        const uint4* o = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.out_in) + at);
+        const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.dout) + at);
+        const int chunks = nh * cpr;
+        if (32 % cpr == 0) {
+          // the lanes of a head are neighbours and add up by shuffles
+          for (int c0 = 0; c0 < chunks; c0 += 128) {
+            uint4 oa[4], ga[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int c = c0 + 32 * u + lane;
-          if (c < chunks) {
-            oa[u] = o[c];
-            ga[u] = g[c];
+            for (int u = 0; u < 4; ++u) {
+              const int c = c0 + 32 * u + lane;
+              if (c < chunks) {
+                oa[u] = o[c];
+                ga[u] = g[c];
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int c = c0 + 32 * u + lane;
+              float v = c < chunks ? dot8<kBF16>(oa[u], ga[u]) : 0.f;
+              for (int w = cpr >> 1; w > 0; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
+              if (c < chunks && (c % cpr) == 0) s_delta[c / cpr][warp] = -v;
+            }
+          }
+        } else {
+          for (int h = lane; h < nh; h += 32) {
+            float v = 0.f;
+            for (int c = 0; c < cpr; ++c) v += dot8<kBF16>(o[h * cpr + c], g[h * cpr + c]);
+            s_delta[h][warp] = -v;
           }
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int c = c0 + 32 * u + lane;
-          float v = c < chunks ? dot8<kBF16>(oa[u], ga[u]) : 0.f;
-          for (int w = cpr >> 1; w > 0; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
-          if (c < chunks && (c % cpr) == 0) put(c / cpr, -v);
+      }
+      __syncthreads();
+      // The rows' values leave in runs: of a virtual head, eight rows times its packed heads
+      // lie side by side by tensor row, and a row's packed heads by tile.
+      for (int z = threadIdx.x; z < nh * kPrepRows; z += 256) {
+        const int w = (z >> sh) % kPrepRows, vh = (z >> sh) / kPrepRows, j = z & ((1 << sh) - 1);
+        const int h = (vh << sh) + j;
+        const float lse = s_lse[h][w], delta = s_delta[h][w];
+        const size_t vhead = static_cast<size_t>((h0 >> sh) + vh);
+        if (r0 + w < rows_end) {
+          const size_t lin = vhead * p.rows_lin + (static_cast<size_t>(r0 + w) << sh) + j;
+          p.lse_lin[lin] = lse;
+          p.delta_lin[lin] = delta;
+        }
+        if (s_tile[w] >= 0) {
+          const size_t t = static_cast<size_t>(s_tile[w]) + vhead * kBlockM + j;
+          if (bounds_ok(t < static_cast<size_t>(p.pair_cap_q) * p.vheads * kBlockM, p.header + kHdrStatus)) {
+            p.lse_t[t] = lse;
+            p.delta_t[t] = delta;
+          }
         }
       }
-    } else {
-      for (int h = lane; h < p.hq; h += 32) {
-        float v = 0.f;
-        for (int c = 0; c < cpr; ++c) v += dot8<kBF16>(o[h * cpr + c], g[h * cpr + c]);
-        put(h, -v);
-      }
+      __syncthreads();
     }
   }
-  for (long long r = gw; r < p.total_kv; r += warps) {
+  const long long warps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+  for (long long r = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < p.total_kv; r += warps) {
     int j = 0;
     const int b = none ? -1 : locate_row(p, k_pad, static_cast<int>(r), &j);
     SeqInfo s{};

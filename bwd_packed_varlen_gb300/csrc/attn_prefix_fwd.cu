@@ -141,55 +141,71 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
     if (e.slot >= 0) e.slot += c * p.hkv * e.rows;
     if (at < p.cap_entries) store_entry(p, at, e);
   };
-  // long row tiles
-  for (int base = 0; base < n_long; base += blockDim.x) {
-    const int g = base + tid;
-    PrefixEntry e{};
-    int n = 0, ch = 0, slots = 0;
-    if (g < n_long) {
-      int lo = 0, hi = p.batch - 1;  // last sequence whose first row tile is at most g
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.seqs[mid].w <= g) lo = mid; else hi = mid - 1;
+  // Entries of more than 128 rows, which take both streams of a block, come first: one that
+  // came after an entry of fewer would keep a stream idle until the other is through.
+  const int pre_chunks = n_pre > 0 ? div_up(np, len) : 0;
+  const int last_pre = n_pre > 0 ? short_rows - (n_pre - 1) * rt : 0;
+  const int wide_pre = n_pre > 0 ? n_pre - (last_pre > 128 ? 0 : 1) : 0;  // compact row tiles of both streams
+  // Long row tiles in two rounds, the wide ones and then the others.
+  auto long_tiles = [&](bool wide) {
+    for (int base = 0; base < n_long; base += blockDim.x) {
+      const int g = base + tid;
+      PrefixEntry e{};
+      int n = 0, ch = 0, slots = 0;
+      if (g < n_long) {
+        int lo = 0, hi = p.batch - 1;  // last sequence whose first row tile is at most g
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (p.seqs[mid].w <= g) lo = mid; else hi = mid - 1;
+        }
+        const SeqInfo q = load_seq(p, lo);
+        e.seq = lo;
+        e.row0 = (g - p.seqs[lo].w) * rt;
+        e.rows = min(rt, q.len_q * p.group - e.row0);
+        if ((e.rows > 128) == wide) {
+          e.np = np;
+          e.off_q = q.off_q;
+          e.off_k = q.off_k;
+          e.len_k = q.len_k;
+          e.diag = q.diag;
+          n = np + own_tiles(p, q.len_k, q.diag, e.row0, e.rows, bn);
+          ch = div_up(n, len);
+          slots = ch > 1 ? ch * p.hkv * e.rows : 0;
+        } else {
+          e.rows = 0;
+        }
       }
-      const SeqInfo q = load_seq(p, lo);
-      e.seq = lo;
-      e.row0 = (g - p.seqs[lo].w) * rt;
-      e.rows = min(rt, q.len_q * p.group - e.row0);
-      e.np = np;
-      e.off_q = q.off_q;
-      e.off_k = q.off_k;
-      e.len_k = q.len_k;
-      e.diag = q.diag;
-      n = np + own_tiles(p, q.len_k, q.diag, e.row0, e.rows, bn);
-      ch = div_up(n, len);
-      slots = ch > 1 ? ch * p.hkv * e.rows : 0;
+      const Scan3 at = block_scan3(ch, slots, 0, buf);
+      if (e.rows > 0 && g < p.cap_longs) {
+        e.slot = slots > 0 ? n_rows + at.y : -1;
+        p.longs[g] = make_int4(e.slot, ch, e.rows, 0);
+        for (int c = 0; c < ch; ++c) put_chunk(e, n, ch, c, n_entries + at.x + c);
+      }
+      n_entries += at.tx;
+      n_rows += at.ty;
     }
-    const Scan3 at = block_scan3(ch, slots, 0, buf);
-    if (g < n_long && g < p.cap_longs) {
-      e.slot = slots > 0 ? n_rows + at.y : -1;
-      p.longs[g] = make_int4(e.slot, ch, e.rows, 0);
-      for (int c = 0; c < ch; ++c) put_chunk(e, n, ch, c, n_entries + at.x + c);
-    }
-    n_entries += at.tx;
-    n_rows += at.ty;
-  }
+  };
+  if (rt > 128) long_tiles(true);
   // the compact rows against the prefix, chunk-major: row tiles that read the same keys
   // are taken side by side
-  const int pre_chunks = n_pre > 0 ? div_up(np, len) : 0;
   const int pre_slot = n_rows;
-  for (int k = tid; k < n_pre * pre_chunks; k += blockDim.x) {
-    const int c = k / n_pre, u = k - c * n_pre;
-    PrefixEntry e{};
-    e.seq = -1;
-    e.row0 = u * rt;
-    e.rows = min(rt, short_rows - e.row0);
-    e.np = np;
-    e.slot = pre_slot + u * rt * pre_chunks * p.hkv;
-    put_chunk(e, np, pre_chunks, c, n_entries + k);
-  }
-  n_entries += n_pre * pre_chunks;
+  auto compact_tiles = [&](int u0, int u1) {
+    for (int k = tid; k < (u1 - u0) * pre_chunks; k += blockDim.x) {
+      const int c = k / (u1 - u0), u = u0 + k - c * (u1 - u0);
+      PrefixEntry e{};
+      e.seq = -1;
+      e.row0 = u * rt;
+      e.rows = min(rt, short_rows - e.row0);
+      e.np = np;
+      e.slot = pre_slot + u * rt * pre_chunks * p.hkv;
+      put_chunk(e, np, pre_chunks, c, n_entries + k);
+    }
+    n_entries += (u1 - u0) * pre_chunks;
+  };
+  if (rt > 128) compact_tiles(0, wide_pre);
   n_rows += short_rows * pre_chunks * p.hkv;
+  long_tiles(false);
+  compact_tiles(rt > 128 ? wide_pre : 0, n_pre);
   // Short sequences against their own keys, the longest first (with at most a thread per
   // sequence): the blocks then run out of work together. A sequence's place is the number of
   // sequences that go before it.

@@ -130,13 +130,17 @@ bool bwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, i
   const int halves = d > 128 ? 2 : 1;
   const long long steps = (group >> sh) * (L->rows_lin / (d > 128 ? 64 : 128));
   const long long items = (static_cast<long long>(prefix_rows) + kBlockN - 1) / kBlockN * hkv * halves;
-  // about three items per SM, with 16 steps of a sweep at least to pay for storing its sums
-  const long long want = items > 0 ? (kBwdItemsTarget + items - 1) / items : 1;
-  // down to 4 steps where that is needed to give every SM an item
-  const long long fill = items > 0 ? (152 + items - 1) / items : 1;
-  const long long few = fill < steps / 4 ? fill : steps / 4, many = want < steps / 16 ? want : steps / 16;
-  const long long best = few > many ? few : many;
-  L->splits = static_cast<int>(best > 1 ? best : 1);
+  // parts of a sweep: as many as give the shortest run of whole rounds over the SMs, a part
+  // costing about three steps more than its sweep (starting it, storing its fp32 sums)
+  long long best = 0;
+  L->splits = 1;
+  for (long long n = 1; items > 0 && n <= 64 && n <= (steps / 4 > 1 ? steps / 4 : 1); ++n) {
+    const long long cost = (items * n + kSMs - 1) / kSMs * ((steps + n - 1) / n + (n > 1 ? 3 : 1));
+    if (best == 0 || cost < best) {
+      best = cost;
+      L->splits = static_cast<int>(n);
+    }
+  }
   if (steps / L->splits >= (1 << 24) - 1 || L->cap_q * hq > INT32_MAX || L->cap_k * hkv * halves > INT32_MAX) return false;
   size_t off = kHdrWords * sizeof(int);
   auto take = [&off](size_t bytes) {
