@@ -62,7 +62,10 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
   __shared__ int buf[3][32];
   __shared__ int bad;
   __shared__ unsigned long long work, tokens;
-  __shared__ int s_tiles[kPrefixSchedThreads], s_order[kPrefixSchedThreads];
+  // with at most a thread per sequence: their own key tiles, order by those, and spans
+  __shared__ __align__(16) int s_tiles[kPrefixSchedThreads];
+  __shared__ int s_order[kPrefixSchedThreads], s_first[kPrefixSchedThreads];
+  __shared__ int4 s_seq[kPrefixSchedThreads];
   pdl_trigger();
   const int rt = prefix_row_tile(p.d), bn = prefix_key_tile(p.d), tid = threadIdx.x, lane = tid & 31;
   if (tid == 0) {
@@ -146,8 +149,12 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
   const int pre_chunks = n_pre > 0 ? div_up(np, len) : 0;
   const int last_pre = n_pre > 0 ? short_rows - (n_pre - 1) * rt : 0;
   const int wide_pre = n_pre > 0 ? n_pre - (last_pre > 128 ? 0 : 1) : 0;  // compact row tiles of both streams
-  // Long row tiles in two rounds, the wide ones and then the others.
-  auto long_tiles = [&](bool wide) {
+  int pre_slot = 0;
+#pragma unroll 1
+  for (int round = rt > 128 ? 0 : 1; round < 2; ++round) {  // the wide entries, then the others
+    const bool wide = round == 0;
+    // long row tiles
+#pragma unroll 1
     for (int base = 0; base < n_long; base += blockDim.x) {
       const int g = base + tid;
       PrefixEntry e{};
@@ -184,12 +191,13 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
       n_entries += at.tx;
       n_rows += at.ty;
     }
-  };
-  if (rt > 128) long_tiles(true);
-  // the compact rows against the prefix, chunk-major: row tiles that read the same keys
-  // are taken side by side
-  const int pre_slot = n_rows;
-  auto compact_tiles = [&](int u0, int u1) {
+    // the compact rows against the prefix, chunk-major: row tiles that read the same keys
+    // are taken side by side
+    if (wide || rt == 128) {
+      pre_slot = n_rows;
+      n_rows += short_rows * pre_chunks * p.hkv;
+    }
+    const int u0 = wide || rt == 128 ? 0 : wide_pre, u1 = wide ? wide_pre : n_pre;
     for (int k = tid; k < (u1 - u0) * pre_chunks; k += blockDim.x) {
       const int c = k / (u1 - u0), u = u0 + k - c * (u1 - u0);
       PrefixEntry e{};
@@ -201,11 +209,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
       put_chunk(e, np, pre_chunks, c, n_entries + k);
     }
     n_entries += (u1 - u0) * pre_chunks;
-  };
-  if (rt > 128) compact_tiles(0, wide_pre);
-  n_rows += short_rows * pre_chunks * p.hkv;
-  long_tiles(false);
-  compact_tiles(rt > 128 ? wide_pre : 0, n_pre);
+  }
   // Short sequences against their own keys, the longest first (with at most a thread per
   // sequence): the blocks then run out of work together. A sequence's place is the number of
   // sequences that go before it.
@@ -213,13 +217,18 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
   if (sorted) {
     const int n = first_tok >= 0 ? own_tiles(p, s.len_k, s.diag, 0, s.len_q * p.group, bn) : -1;
     s_tiles[tid] = n;
+    s_first[tid] = first_tok;
+    s_seq[tid] = make_int4(s.off_q, s.len_q, s.off_k, s.len_k);
     __syncthreads();
+    // (threads past the batch hold -1 and come after every sequence)
     int place = 0;
-    for (int j = 0; j < p.batch; ++j) {
-      const int o = s_tiles[j];
-      place += o > n || (o == n && j < tid) ? 1 : 0;
+#pragma unroll 4
+    for (int j = 0; j < p.batch; j += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(&s_tiles[j]);
+      place += (o.x > n || (o.x == n && j < tid)) + (o.y > n || (o.y == n && j + 1 < tid)) +
+               (o.z > n || (o.z == n && j + 2 < tid)) + (o.w > n || (o.w == n && j + 3 < tid));
     }
-    if (tid < p.batch) s_order[place] = tid;
+    s_order[place] = tid;
     __syncthreads();
   }
   for (int base = 0; base < p.batch; base += blockDim.x) {
@@ -227,7 +236,15 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
     const int b = at_b < p.batch ? (sorted ? s_order[tid] : at_b) : p.batch;
     SeqInfo q{};
     int first = -1;
-    if (b < p.batch) {
+    if (sorted && b < p.batch) {
+      first = s_first[b];
+      const int4 v = s_seq[b];
+      q.off_q = v.x;
+      q.len_q = v.y;
+      q.off_k = v.z;
+      q.len_k = v.w;
+      q.diag = p.causal == 2 ? v.w - v.y : 0;
+    } else if (b < p.batch) {
       q = load_seq(p, b);
       first = p.seqs[b].x;
     }
@@ -430,18 +447,19 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       const int n = puts(x);
       return n < 2 || __all_sync(0xffffffffu, mbar_wait(&rings[x].empty[n & 1], ((n >> 1) - 1) & 1, status));
     };
-    // An item is taken from the common list only when the tiles before it are loaded but for
-    // kAhead: enough to hide its decoding, and no more, since a block that takes items early
-    // may sit on them while others have run out.
-    constexpr int kAhead = 4;
+    // With few items per block an item is taken from the common list only when the tiles
+    // before it are loaded but for four: enough to hide its decoding, and no more, since a
+    // block that takes items early may sit on them while others have run out (decoding steps:
+    // 10 % slower). With many the hand-over slots alone bound it: there taking late cost 4 %.
+    const int ahead = n_items > 4 * static_cast<int>(gridDim.x) ? INT32_MAX : 4;
     int emitted = 0;  // tiles in the order so far
     auto keep_pace = [&]() -> bool {
       const volatile int* loaded = &tiles_loaded;
-      if (emitted - *loaded <= kAhead) return true;
+      if (emitted - *loaded <= ahead) return true;
       const unsigned long long t0 = global_ns();
       for (uint32_t it = 1;; ++it) {
         __nanosleep(400);
-        if (emitted - *loaded <= kAhead) return true;
+        if (emitted - *loaded <= ahead) return true;
         if ((it & 15u) == 0) {
           if (*reinterpret_cast<volatile int*>(status) & kErrTimeout) return false;
           if (global_ns() - t0 > kWaitLimitNs) {
