@@ -346,19 +346,20 @@ def bwd_sbhd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, attn_scale,
 
 
 # The rotary and shared-prefix entry points serve single decoding steps, where the kernels
-# take less time than the checks used to: these helpers keep a call's host side short.
+# take less time than the checks used to: these helpers, and the straight lines of conditions
+# below, keep a call's host side short.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
 
 
-def _device_index(q, ts):
-    """Index of q's CUDA device, which all of ``ts`` (None allowed) must share."""
-    i = q.get_device()
-    for t in ts:
-        if t is not None and t.get_device() != i:
-            raise ValueError("all tensors must be CUDA tensors on one device (there is no CPU path)")
-    if i < 0:
-        raise ValueError("all tensors must be CUDA tensors (there is no CPU path)")
-    return i
+def _lib():
+    return _libs.get(_use_debug) or library()
+
+
+def _one_device(index):
+    if index < 0:
+        return "all tensors must be CUDA tensors (there is no CPU path)"
+    return "all tensors must be CUDA tensors on one device (there is no CPU path)"
 
 
 def _call(fn, index, stream, args):
@@ -374,68 +375,70 @@ def _call(fn, index, stream, args):
         _check(rc)
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _cu_vector(t, n, index):
+    """t's address, as an int32 vector of n values on the device."""
+    if t.dtype != _I32 or t.dim() != 1 or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"cu_seqlens and start_positions must be contiguous int32 vectors on q's device, of "
+                         f"batch + 1 and batch values (here {n})")
+    return t.data_ptr()
 
 
-def _ints(ts, n):
-    for t in ts:
-        if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"cu_seqlens must be contiguous int32 vectors of batch + 1 = {n} values")
-
-
-def _rope_output(x, y):
+def _rope_output(x, y, index):
     """Output of a rotation: a new contiguous tensor, or the caller's after a check."""
     if y is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if y.shape != x.shape or y.dtype != x.dtype or not y.is_contiguous():
-        raise ValueError("outputs must be contiguous, with the shape and dtype of their input")
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    if y.shape != x.shape or y.dtype != x.dtype or y.get_device() != index or not y.is_contiguous():
+        raise ValueError("outputs must be contiguous, with the shape, dtype and device of their input")
     return y
 
 
 def _rope(q, k, inv_freq, cu, cu_pad, start, interleaved, mscale, inverse, q_out, k_out, stream):
     """Both layouts: ``cu_pad`` None is the sequence-major one."""
-    L = library()
-    index = _device_index(q, (k, inv_freq, cu, cu_pad, start, q_out, k_out))
-    code = _DTYPES.get(q.dtype)
-    if code is None or (k is not None and k.dtype != q.dtype):
+    index = q.get_device()
+    if index < 0 or inv_freq.get_device() != index or (k is not None and k.get_device() != index):
+        raise ValueError(_one_device(index))
+    dtype, q_shape, qs = q.dtype, q.shape, q.stride()
+    code = _DTYPES.get(dtype)
+    if code is None or (k is not None and k.dtype != dtype):
         raise ValueError("q and k must share one dtype, float16 or bfloat16")
     dims = 4 if cu_pad is None else 3
-    for x in (q, k):
-        if x is not None and (x.dim() != dims or (x.stride(-1) != 1 and x.numel())):
-            raise ValueError(f"q and k must have {dims} dimensions and adjacent elements in a head")
-    if k is not None and (k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]):
-        raise ValueError("q and k must share tokens and head dim")
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if len(q_shape) != dims or (qs[-1] != 1 and q.numel()):
+        raise ValueError(f"q and k must have {dims} dimensions and adjacent elements in a head")
+    if inv_freq.dtype != _F64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous float64 vector")
     n = cu.numel()
     if n < 2:
         raise ValueError("cu_seqlens must hold batch + 1 values")
-    _ints((cu,) if cu_pad is None else (cu, cu_pad), n)
-    if start is not None:
-        _ints((start,), n - 1)
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
-    y = _rope_output(q, q_out)
-    z = None if k is None else _rope_output(k, k_out)
-    qs = q.stride()
-    ks = qs if k is None else k.stride()
+    at_cu = _cu_vector(cu, n, index)
+    at_start = None if start is None else _cu_vector(start, n - 1, index)
+    y = _rope_output(q, q_out, index)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        z, hkv, ks, at_k, at_z = None, 0, qs, None, None
+    else:
+        k_shape, ks = k.shape, k.stride()
+        if len(k_shape) != dims or (ks[-1] != 1 and k.numel()):
+            raise ValueError(f"q and k must have {dims} dimensions and adjacent elements in a head")
+        if k_shape[0] != q_shape[0] or k_shape[-1] != q_shape[-1] or (dims == 4 and k_shape[1] != q_shape[1]):
+            raise ValueError("q and k must share tokens and head dim")
+        z = _rope_output(k, k_out, index)
+        hkv, at_k, at_z = k_shape[-2], k.data_ptr(), z.data_ptr()
     tail = (qs[-3], qs[-2], ks[-3], ks[-2], 1 if interleaved else 0, float(mscale), 1 if inverse else 0, code)
     if cu_pad is None:
-        S, B, hq, d = q.shape
+        S, B, hq, d = q_shape
         if B != n - 1:
             raise ValueError("cu_seqlens must hold batch + 1 values")
-        for x in (q, k):
-            if x is not None and S > 1 and x.stride(0) != B * x.stride(1):
-                raise ValueError("rows i * batch + b must be evenly spaced")
-        _call(L.te_attn_rope_sbhd, index, stream,
-              (q.data_ptr(), _at(k), y.data_ptr(), _at(z), inv_freq.data_ptr(), inv_freq.numel(), cu.data_ptr(),
-               _at(start), B, S, hq, 0 if k is None else k.shape[2], d) + tail)
+        if S > 1 and (qs[0] != B * qs[1] or ks[0] != B * ks[1]):
+            raise ValueError("rows i * batch + b must be evenly spaced")
+        _call(_lib().te_attn_rope_sbhd, index, stream,
+              (q.data_ptr(), at_k, y.data_ptr(), at_z, inv_freq.data_ptr(), inv_freq.numel(), at_cu, at_start, B, S,
+               hq, hkv, d) + tail)
     else:
-        T, hq, d = q.shape
-        _call(L.te_attn_rope_thd, index, stream,
-              (q.data_ptr(), _at(k), y.data_ptr(), _at(z), inv_freq.data_ptr(), inv_freq.numel(), cu.data_ptr(),
-               cu_pad.data_ptr(), _at(start), n - 1, T, hq, 0 if k is None else k.shape[1], d) + tail)
+        T, hq, d = q_shape
+        _call(_lib().te_attn_rope_thd, index, stream,
+              (q.data_ptr(), at_k, y.data_ptr(), at_z, inv_freq.data_ptr(), inv_freq.numel(), at_cu,
+               _cu_vector(cu_pad, n, index), at_start, n - 1, T, hq, hkv, d) + tail)
     return y, z
 
 
@@ -467,45 +470,57 @@ def prefix_bwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d)
     return int(library().te_attn_prefix_bwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d))
 
 
-def _prefix_sizes(q, k, v, kp, vp, cus, prefix_len, out, lse, others):
-    """Checks what a forward and a backward share; returns (device index, dtype code, sizes)."""
-    given = (k, v, kp, vp, *cus, prefix_len, out, lse, *others)
-    index = _device_index(q, given)
-    for t in (q, *given):
-        if t is not None and not t.is_contiguous():
-            raise ValueError("all tensors must be contiguous")
-    dtype = q.dtype
+def _prefix_args(q, k, v, kp, vp, cu_q, cu_kv, cu_q_pad, cu_kv_pad, prefix_len):
+    """Checks what forward and backward share: (device index, dtype code, sizes, the lengths'
+    addresses)."""
+    index, dtype = q.get_device(), q.dtype
+    if (index < 0 or k.get_device() != index or v.get_device() != index or kp.get_device() != index
+            or vp.get_device() != index):
+        raise ValueError(_one_device(index))
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and kp.is_contiguous()
+            and vp.is_contiguous()):
+        raise ValueError("all tensors must be contiguous")
     code = _DTYPES.get(dtype)
     if code is None or k.dtype != dtype or v.dtype != dtype or kp.dtype != dtype or vp.dtype != dtype:
         raise ValueError("q, k, v, k_prefix, v_prefix must share one dtype, float16 or bfloat16")
-    if q.dim() != 3 or k.dim() != 3 or kp.dim() != 3:
+    q_shape, k_shape, p_shape = q.shape, k.shape, kp.shape
+    if len(q_shape) != 3 or len(k_shape) != 3 or len(p_shape) != 3:
         raise ValueError("q, k, v, k_prefix, v_prefix must be [rows, heads, d]")
-    tq, hq, d = q.shape
-    tk, hkv, dk = k.shape
-    rows, hp, dp = kp.shape
-    if v.shape != k.shape or vp.shape != kp.shape or hp != hkv or dk != d or dp != d:
+    tq, hq, d = q_shape
+    tk, hkv, dk = k_shape
+    rows, hp, dp = p_shape
+    if v.shape != k_shape or vp.shape != p_shape or hp != hkv or dk != d or dp != d:
         raise ValueError("k, v and k_prefix, v_prefix must share heads and head dim, and d with q")
-    n = cus[0].numel()
-    _ints(cus, n)
-    if prefix_len is not None and (prefix_len.dtype != torch.int32 or prefix_len.numel() != 1):
-        raise ValueError("prefix_len must be one int32")
-    if out is not None and (out.shape != q.shape or out.dtype != dtype):
-        raise ValueError("out must have the shape and dtype of q")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2]):
-        raise ValueError("lse must be float32 [T_q, hq]")
-    return index, code, (n - 1, tq, tk, rows, hq, hkv, d)
-
-
-def _workspace(given, size, device):
-    return torch.empty(max(size, 1), dtype=torch.uint8, device=device) if given is None else given
+    n = cu_q.numel()
+    lens = (_cu_vector(cu_q, n, index), _cu_vector(cu_kv, n, index), _cu_vector(cu_q_pad, n, index),
+            _cu_vector(cu_kv_pad, n, index), None if prefix_len is None else _cu_vector(prefix_len, 1, index))
+    return index, code, (n - 1, tq, tk, rows, hq, hkv, d), lens
 
 
 def _like(x, y, name):
+    """A new tensor like x, or the caller's after a check."""
     if y is None:
         return torch.empty_like(x)
-    if y.shape != x.shape or y.dtype != x.dtype:
-        raise ValueError(f"{name} must have the shape and dtype of its counterpart")
+    if y.shape != x.shape or y.dtype != x.dtype or y.get_device() != x.get_device() or not y.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, with the shape, dtype and device of its counterpart")
     return y
+
+
+def _prefix_lse(q, lse):
+    """A new lse [T_q, hq], or the caller's after a check."""
+    if lse is None:
+        return torch.empty(q.shape[:2], dtype=_F32, device=q.device)
+    if lse.dtype != _F32 or lse.shape != q.shape[:2] or lse.get_device() != q.get_device() or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [T_q, hq] on q's device")
+    return lse
+
+
+def _prefix_workspace(q, ws, size):
+    if ws is None:
+        return torch.empty(size if size > 0 else 1, dtype=torch.uint8, device=q.device)
+    if ws.get_device() != q.get_device() or not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous, on q's device")
+    return ws
 
 
 def prefix_fwd(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
@@ -514,18 +529,14 @@ def prefix_fwd(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seql
     """``te_attn_prefix_fwd_thd``: attention over a prefix ``k_prefix, v_prefix [P, hkv, d]``
     that every sequence shares, then each sequence's own keys; returns ``(out [T_q, hq, d],
     lse [T_q, hq])``."""
-    cus = (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded)
-    index, code, sizes = _prefix_sizes(q, k, v, k_prefix, v_prefix, cus, prefix_len, out, lse, (workspace,))
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty(sizes[1], sizes[4], dtype=torch.float32, device=q.device)
-    ws = _workspace(workspace, prefix_fwd_workspace_size(*sizes), q.device)
-    _call(library().te_attn_prefix_fwd_thd, index, stream,
+    index, code, sizes, lens = _prefix_args(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv,
+                                            cu_seqlens_q_padded, cu_seqlens_kv_padded, prefix_len)
+    out = _like(q, out, "out")
+    lse = _prefix_lse(q, lse)
+    ws = _prefix_workspace(q, workspace, prefix_fwd_workspace_size(*sizes))
+    _call(_lib().te_attn_prefix_fwd_thd, index, stream,
           (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), out.data_ptr(),
-           lse.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(), cu_seqlens_q_padded.data_ptr(),
-           cu_seqlens_kv_padded.data_ptr(), _at(prefix_len), *sizes, float(attn_scale), _mask(mask_type), code,
-           ws.data_ptr(), ws.numel()))
+           lse.data_ptr(), *lens, *sizes, float(attn_scale), _mask(mask_type), code, ws.data_ptr(), ws.numel()))
     return out, lse
 
 
@@ -534,19 +545,21 @@ def prefix_bwd(q, k, v, k_prefix, v_prefix, out, dout, lse, cu_seqlens_q, cu_seq
                mask_type="padding_causal_bottom_right", prefix_len=None, dq=None, dk=None, dv=None,
                dk_prefix=None, dv_prefix=None, workspace=None, stream=None):
     """``te_attn_prefix_bwd_thd``: returns ``(dq, dk, dv, dk_prefix, dv_prefix)``."""
-    cus = (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded)
-    index, code, sizes = _prefix_sizes(q, k, v, k_prefix, v_prefix, cus, prefix_len, out, lse,
-                                       (dout, dq, dk, dv, dk_prefix, dv_prefix, workspace))
+    index, code, sizes, lens = _prefix_args(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv,
+                                            cu_seqlens_q_padded, cu_seqlens_kv_padded, prefix_len)
+    if out is None or dout is None or lse is None:
+        raise ValueError("the backward needs out, dout and lse")
+    _like(q, out, "out")
     _like(q, dout, "dout")
-    grads = (_like(q, dq, "dq"), _like(k, dk, "dk"), _like(v, dv, "dv"), _like(k_prefix, dk_prefix, "dk_prefix"),
-             _like(v_prefix, dv_prefix, "dv_prefix"))
-    ws = _workspace(workspace, prefix_bwd_workspace_size(*sizes), q.device)
-    _call(library().te_attn_prefix_bwd_thd, index, stream,
+    _prefix_lse(q, lse)
+    dq, dk, dv = _like(q, dq, "dq"), _like(k, dk, "dk"), _like(v, dv, "dv")
+    dkp, dvp = _like(k_prefix, dk_prefix, "dk_prefix"), _like(v_prefix, dv_prefix, "dv_prefix")
+    ws = _prefix_workspace(q, workspace, prefix_bwd_workspace_size(*sizes))
+    _call(_lib().te_attn_prefix_bwd_thd, index, stream,
           (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), out.data_ptr(),
-           dout.data_ptr(), lse.data_ptr(), *(g.data_ptr() for g in grads), cu_seqlens_q.data_ptr(),
-           cu_seqlens_kv.data_ptr(), cu_seqlens_q_padded.data_ptr(), cu_seqlens_kv_padded.data_ptr(),
-           _at(prefix_len), *sizes, float(attn_scale), _mask(mask_type), code, ws.data_ptr(), ws.numel()))
-    return grads
+           dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dkp.data_ptr(),
+           dvp.data_ptr(), *lens, *sizes, float(attn_scale), _mask(mask_type), code, ws.data_ptr(), ws.numel()))
+    return dq, dk, dv, dkp, dvp
 
 
 def read_status(workspace, stream=None) -> int:

@@ -12,8 +12,14 @@
 // few fp64 operations are per block and pair, not per element.
 //
 // Memory-bound: each element is read once and written once, 16 bytes per access where
-// sizes and alignment allow it. A block takes kTokens tokens, computes their angles into
-// shared memory once and applies them to every query and key head.
+// sizes and alignment allow it. A block takes a few tokens (and, with few tokens, a part of
+// the heads), issues its first loads, works out the tokens' angles into shared memory while
+// they are on their way, and applies them to every query and key head. What it took:
+// bytes in flight from many small blocks (a thread keeps one access in 32-40 registers;
+// unrolled, or with a warp on its own, it was slower), few instructions per access (one
+// loop over rotated and copied units took 43 us where two take 34), and angles laid out so
+// that neighbouring lanes read neighbouring words. 34656 tokens of 40 heads of 128, all of
+// each head rotated: 113 us, 6.3 TB/s; a token each of 48 sequences: 6 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -37,25 +43,34 @@ struct RopeParams {
   int batch, total, d, rot;
   int sbhd;              // rows i * batch + b instead of cu_pad[b] + i
   float mscale, sign;    // sign -1: the inverse rotation
+  int tokens, heads_per; // tokens and heads (of q, then k) of a block
+  int units[2];          // of a head: rotated, copied
+  uint32_t units_inv[2], heads_inv;  // ceil(2^32 / n) of those
 };
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256, kRopeTokens = 4;
+constexpr int kRopeSMs = 152;  // of the GPU that work is cut for
 
-// Position of row r, or *real = false for a row that holds no token.
+// n / d with inv = ceil(2^32 / d), exact for n d < 2^32.
+__device__ __forceinline__ int div_by(int n, uint32_t inv, int d) {
+  return d == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), inv));
+}
+
+// Position of row r, or *real = false for a row that holds no token. A whole warp works on
+// one row: the lanes count the sequences that start at or before it, one trip to memory
+// instead of a search's several.
 __device__ __forceinline__ long long rope_position(const RopeParams& p, int r, bool* real) {
-  int b = 0, i;
+  int b, i;
   *real = false;
   if (p.sbhd) {
     b = r % p.batch;
     i = r / p.batch;
+    if (p.cu[b + 1] - p.cu[b] > p.total / p.batch) return 0;
   } else {
-    if (r < p.cu_pad[0] || r >= p.cu_pad[p.batch]) return 0;
-    int lo = 0, hi = p.batch - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.cu_pad[mid] <= r) lo = mid; else hi = mid - 1;
-    }
-    b = lo;
+    int before = 0;
+    for (int k = threadIdx.x & 31; k < p.batch; k += 32) before += p.cu_pad[k] <= r ? 1 : 0;
+    b = __reduce_add_sync(0xffffffffu, before) - 1;
+    if (b < 0) return 0;
     i = r - p.cu_pad[b];
     // a sequence whose real length does not fit its slot, or whose slot does not fit
     // the tensor, is treated as empty
@@ -64,7 +79,6 @@ __device__ __forceinline__ long long rope_position(const RopeParams& p, int r, b
       return 0;
   }
   if (i < 0 || i >= p.cu[b + 1] - p.cu[b]) return 0;
-  if (p.sbhd && p.cu[b + 1] - p.cu[b] > p.total / p.batch) return 0;
   *real = true;
   return static_cast<long long>(p.start ? p.start[b] : 0) + i;
 }
@@ -82,150 +96,167 @@ template <>
 struct Vec<1> { using type = uint16_t; };
 
 template <int V, bool kBF16>
-__device__ __forceinline__ void load_vec(const uint16_t* src, float (&f)[V]) {
-  using T = typename Vec<V>::type;
-  union {
-    T v;
-    uint16_t h[V];
-  } u;
-  u.v = *reinterpret_cast<const T*>(src);
+__device__ __forceinline__ void widen(typename Vec<V>::type v, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = kBF16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if constexpr (kBF16)
-      f[i] = __uint_as_float(static_cast<uint32_t>(u.h[i]) << 16);
-    else
-      f[i] = __half2float(__ushort_as_half(u.h[i]));
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 x = unpack2<kBF16>(w[i]);
+      f[2 * i] = x.x;
+      f[2 * i + 1] = x.y;
+    }
   }
 }
 
 template <int V, bool kBF16>
-__device__ __forceinline__ void store_vec(uint16_t* dst, const float (&f)[V]) {
-  using T = typename Vec<V>::type;
-  union {
-    T v;
-    uint16_t h[V];
-  } u;
+__device__ __forceinline__ typename Vec<V>::type narrow(const float (&f)[V]) {
+  typename Vec<V>::type v;
+  if constexpr (V == 1) {
+    v = kBF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f[0])) : __half_as_ushort(__float2half_rn(f[0]));
+  } else {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if constexpr (kBF16)
-      u.h[i] = __bfloat16_as_ushort(__float2bfloat16_rn(f[i]));
-    else
-      u.h[i] = __half_as_ushort(__float2half_rn(f[i]));
+    for (int i = 0; i < V / 2; ++i) w[i] = pack2<kBF16>(f[2 * i], f[2 * i + 1]);
   }
-  *reinterpret_cast<T*>(dst) = u.v;
+  return v;
 }
 
-// kHalf: pairs (c, c + rot/2), a unit is V pairs; otherwise pairs (2c, 2c + 1), a unit
-// is V elements. The units of a head are its rotated ones, then V-element pieces of the
-// rest. V = 1 with interleaved pairs takes one pair per unit.
+// kHalf: pairs (c, c + rot/2), a rotated unit is V pairs in two accesses; otherwise pairs
+// (2c, 2c + 1), a unit is V elements in one (V = 1: one pair in two). A copied unit is V
+// elements of the rest of the head. The two kinds are loops of their own, so that no warp
+// goes through both.
 template <int V, bool kHalf, bool kBF16>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p,
-                                                            int tokens_per_block) {
-  extern __shared__ float2 s_cs[];  // [tokens][rot / 2]
-  __shared__ long long s_pos[16];
-  __shared__ bool s_real[16];
-  const int tid = threadIdx.x;
-  const int r0 = blockIdx.x * tokens_per_block;
-  const int nt = min(tokens_per_block, p.total - r0);
-  const int half = p.rot / 2;
-  if (tid < nt) {
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  // (cos, sin) of pair i of rotated unit u at [token][i][u]: neighbouring lanes hold
+  // neighbouring units, and read neighbouring words
+  extern __shared__ float2 s_cs[];
+  __shared__ long long s_pos[kRopeTokens];
+  __shared__ bool s_real[kRopeTokens];
+  using T = typename Vec<V>::type;
+  constexpr bool kTwo = kHalf || V == 1;                // two accesses per rotated unit
+  constexpr int kPair = kHalf ? V : (V == 1 ? 2 : V);  // elements from one unit to the next
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int r0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.total - r0);
+  const int half = p.rot / 2, units = p.units[0], second = kHalf ? half : 1;
+  const int h0 = blockIdx.y * p.heads_per, nh = min(p.heads_per, p.heads[0] + p.heads[1] - h0);
+  // unit n of one kind: (token, head, unit) = (n / (heads_per units), .., n % units); its
+  // elements' places in the input and output, or false past the block's last one
+  auto locate = [&](int n, int kind, const uint16_t** x, uint16_t** y, int* t, int* u) {
+    const int th = div_by(n, p.units_inv[kind], p.units[kind]);
+    *u = n - th * p.units[kind];
+    *t = div_by(th, p.heads_inv, p.heads_per);
+    const int k = th - *t * p.heads_per;
+    if (*t >= nt || k >= nh) return false;
+    const int head = h0 + k, which = head >= p.heads[0] ? 1 : 0, h = which ? head - p.heads[0] : head;
+    const long long r = r0 + *t;
+    const int e = kind ? p.rot + *u * V : *u * kPair;
+    *x = static_cast<const uint16_t*>(p.x[which]) + r * p.stride_t[which] + h * p.stride_h[which] + e;
+    *y = static_cast<uint16_t*>(p.y[which]) + (r * p.heads[which] + h) * p.d + e;
+    return true;
+  };
+  struct Unit {
+    T a, b;
+    uint16_t* y;
+    int t, u;
+    bool in;
+  };
+  auto load = [&](int n, int kind, Unit& w) {
+    const uint16_t* x;
+    w.in = locate(n, kind, &x, &w.y, &w.t, &w.u);
+    if (!w.in) return;
+    w.a = *reinterpret_cast<const T*>(x);
+    if (kTwo && kind == 0) w.b = *reinterpret_cast<const T*>(x + second);
+  };
+  const int n_rot = nt * p.heads_per * units, n_copy = nt * p.heads_per * p.units[1];
+  Unit w;
+  load(tid, 0, w);
+
+  if (warp < nt) {
     bool real;
-    s_pos[tid] = rope_position(p, r0 + tid, &real);
-    s_real[tid] = real;
+    const long long pos = rope_position(p, r0 + warp, &real);
+    s_pos[warp] = pos;
+    s_real[warp] = real;
   }
   __syncthreads();
+  const int per = half / units;  // pairs of a unit
   for (int c = tid; c < half; c += kRopeThreads) {
     const double turns = p.inv_freq[c] * 0.15915494309189535;  // 1 / (2 pi)
     const unsigned long long step =
         static_cast<unsigned long long>((turns - floor(turns)) * 18446744073709551616.0);
+    const int u = c / per, at = (c - u * per) * units + u;
     for (int t = 0; t < nt; ++t) {
       const long long frac = static_cast<long long>(static_cast<unsigned long long>(s_pos[t]) * step);
       float sn, cs;
       sincospif(static_cast<float>(frac) * 1.0842021724855044e-19f, &sn, &cs);  // 2^-63: half turns
-      s_cs[t * half + c] = make_float2(cs * p.mscale, sn * p.mscale * p.sign);
+      s_cs[t * half + at] = make_float2(cs * p.mscale, sn * p.mscale * p.sign);
     }
   }
   __syncthreads();
 
-  constexpr int kPairElems = kHalf ? V : (V == 1 ? 2 : V);  // elements a rotated unit reads at once
-  const int rot_units = kHalf ? half / V : p.rot / kPairElems;
-  const int units = rot_units + (p.d - p.rot) / V;
-  const int heads = p.heads[0] + p.heads[1];
-  const int per_token = heads * units;
-  for (int w = tid; w < nt * per_token; w += kRopeThreads) {
-    const int t = w / per_token, rem = w - t * per_token;
-    const int hh = rem / units, u = rem - hh * units;
-    const int which = hh >= p.heads[0] ? 1 : 0;
-    const int h = which ? hh - p.heads[0] : hh;
-    const long long r = r0 + t;
-    const uint16_t* x = static_cast<const uint16_t*>(p.x[which]) + r * p.stride_t[which] + h * p.stride_h[which];
-    uint16_t* y = static_cast<uint16_t*>(p.y[which]) + (r * p.heads[which] + h) * p.d;
-    const bool real = s_real[t];
-    if (u >= rot_units) {
-      const int c = p.rot + (u - rot_units) * V;
-      float f[V];
-      load_vec<V, kBF16>(x + c, f);
-      if (!real) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = 0.f;
-      }
-      store_vec<V, kBF16>(y + c, f);
-      continue;
-    }
-    const float2* cs = s_cs + t * half;
-    if constexpr (kHalf) {
-      const int c = u * V;
-      float a[V], b[V];
-      load_vec<V, kBF16>(x + c, a);
-      load_vec<V, kBF16>(x + half + c, b);
+  for (int n = tid; n < n_rot; n += kRopeThreads) {
+    if (n != tid) load(n, 0, w);
+    if (!w.in) continue;
+    const bool real = s_real[w.t];
+    const float2* cs = s_cs + w.t * half + w.u;
+    float f[V];
+    widen<V, kBF16>(w.a, f);
+    if constexpr (kTwo) {
+      float g[V];
+      widen<V, kBF16>(w.b, g);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float2 w2 = cs[c + i];
-        const float y1 = a[i] * w2.x - b[i] * w2.y, y2 = b[i] * w2.x + a[i] * w2.y;
-        a[i] = real ? y1 : 0.f;
-        b[i] = real ? y2 : 0.f;
+        const float2 z = cs[i * units];
+        const float y1 = f[i] * z.x - g[i] * z.y, y2 = g[i] * z.x + f[i] * z.y;
+        f[i] = y1;
+        g[i] = y2;
       }
-      store_vec<V, kBF16>(y + c, a);
-      store_vec<V, kBF16>(y + half + c, b);
+      *reinterpret_cast<T*>(w.y + second) = real ? narrow<V, kBF16>(g) : T{};
     } else {
-      const int c = u * kPairElems;
-      float f[kPairElems];
-      if constexpr (V == 1) {
-        float a[1], b[1];
-        load_vec<1, kBF16>(x + c, a);
-        load_vec<1, kBF16>(x + c + 1, b);
-        f[0] = a[0];
-        f[1] = b[0];
-      } else {
-        load_vec<V, kBF16>(x + c, f);
-      }
 #pragma unroll
-      for (int i = 0; i < kPairElems; i += 2) {
-        const float2 w2 = cs[c / 2 + i / 2];
-        const float y1 = f[i] * w2.x - f[i + 1] * w2.y, y2 = f[i + 1] * w2.x + f[i] * w2.y;
-        f[i] = real ? y1 : 0.f;
-        f[i + 1] = real ? y2 : 0.f;
-      }
-      if constexpr (V == 1) {
-        const float a[1] = {f[0]}, b[1] = {f[1]};
-        store_vec<1, kBF16>(y + c, a);
-        store_vec<1, kBF16>(y + c + 1, b);
-      } else {
-        store_vec<V, kBF16>(y + c, f);
+      for (int i = 0; i < V; i += 2) {
+        const float2 z = cs[i / 2 * units];
+        const float y1 = f[i] * z.x - f[i + 1] * z.y, y2 = f[i + 1] * z.x + f[i] * z.y;
+        f[i] = y1;
+        f[i + 1] = y2;
       }
     }
+    *reinterpret_cast<T*>(w.y) = real ? narrow<V, kBF16>(f) : T{};
+  }
+  for (int n = tid; n < n_copy; n += kRopeThreads) {
+    load(n, 1, w);
+    if (w.in) *reinterpret_cast<T*>(w.y) = s_real[w.t] ? w.a : T{};
   }
 }
 
 template <int V, bool kHalf>
-static cudaError_t launch_rope_v(const RopeParams& p, bool bf16, cudaStream_t st) {
-  const int tokens = 4;
-  const int grid = (p.total + tokens - 1) / tokens;
-  const size_t smem = static_cast<size_t>(tokens) * (p.rot / 2) * sizeof(float2);
+static cudaError_t launch_rope_v(RopeParams p, bool bf16, cudaStream_t st) {
+  p.units[0] = kHalf ? p.rot / 2 / V : p.rot / (V == 1 ? 2 : V);
+  p.units[1] = (p.d - p.rot) / V;
+  const int heads = p.heads[0] + p.heads[1], all = heads * (p.units[0] + p.units[1]);
+  // A block takes up to four tokens, which share the work on the frequencies, while that is
+  // no more than five passes of its threads: many small blocks overlap one's angles with
+  // another's copies. With few tokens a block takes a part of a token's heads, half a pass at
+  // least, to fill the SMs; and never more units than the divisions allow.
+  const int share = 5 * kRopeThreads / all;
+  p.tokens = p.total < 16 * kRopeSMs || share < 1 ? 1 : share < kRopeTokens ? share : kRopeTokens;
+  const int blocks = (p.total + p.tokens - 1) / p.tokens;
+  const int want = blocks < 2 * kRopeSMs ? (2 * kRopeSMs + blocks - 1) / blocks : 1;
+  const int most = (all + kRopeThreads / 2 - 1) / (kRopeThreads / 2), least = (all + 8191) / 8192;
+  int parts = want > most ? most : want > least ? want : least;
+  parts = parts < heads ? parts : heads;
+  p.heads_per = (heads + parts - 1) / parts;
+  auto inverse = [](int n) { return n > 0 ? static_cast<uint32_t>(((1ull << 32) + n - 1) / n) : 0u; };
+  p.units_inv[0] = inverse(p.units[0]);
+  p.units_inv[1] = inverse(p.units[1]);
+  p.heads_inv = inverse(p.heads_per);
+  const size_t smem = static_cast<size_t>(p.tokens) * (p.rot / 2) * sizeof(float2);
+  const dim3 grid(blocks, (heads + p.heads_per - 1) / p.heads_per);
   if (bf16)
-    rope_kernel<V, kHalf, true><<<grid, kRopeThreads, smem, st>>>(p, tokens);
+    rope_kernel<V, kHalf, true><<<grid, kRopeThreads, smem, st>>>(p);
   else
-    rope_kernel<V, kHalf, false><<<grid, kRopeThreads, smem, st>>>(p, tokens);
+    rope_kernel<V, kHalf, false><<<grid, kRopeThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -268,7 +299,7 @@ static int rope_impl(const void* q, const void* k, void* q_out, void* k_out, con
   if (batch < 1) return api_fail(TE_ERR_INVALID_ARG, "batch must be >= 1");
   if (rows < 0 || rows > INT32_MAX) return api_fail(TE_ERR_INVALID_ARG, "rows must lie in [0, 2^31)");
   if (hq < 1 || hkv < 0) return api_fail(TE_ERR_INVALID_ARG, "hq must be >= 1 and hkv >= 0");
-  if (hq > 65535 || hkv > 65535) return api_fail(TE_ERR_UNSUPPORTED, "at most 65535 heads");
+  if (hq > 4096 || hkv > 4096) return api_fail(TE_ERR_UNSUPPORTED, "at most 4096 heads");
   if (d < 8 || d > 256 || d % 8 != 0)
     return api_fail(TE_ERR_UNSUPPORTED, "head dim must be a multiple of 8 in [8, 256]");
   if (n_freq < 1 || 2 * n_freq > d)
