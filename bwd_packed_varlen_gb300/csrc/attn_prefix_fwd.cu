@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         }
       }
     };
+#pragma unroll 1
     for (int ii = 0;; ++ii) {
       while (NT == 2 && order.wants(true, true) < 0) {
         order.take(order.next());
@@ -488,43 +489,43 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       const int o0 = max(0, e.t0 - e.np);             // first own tile
       const bool pair = e.rows > 128;
       // own tiles end at the last one that a row of the tile sees
-      auto tiles = [&](int x) {
-        const int rows = min(128, e.rows - x * 128);
-        const int no = e.seq >= 0 ? own_tiles(p, e.len_k, e.diag, e.row0 + x * 128, rows, BN) : 0;
+      auto tiles = [&](int k) {
+        const int rows = min(128, e.rows - k * 128);
+        const int no = e.seq >= 0 ? own_tiles(p, e.len_k, e.diag, e.row0 + k * 128, rows, BN) : 0;
         return max(0, min(e.t1, e.np + no) - e.t0);
       };
-      int x0 = 0, x1 = NT - 1;
+      const int n0 = tiles(0), n1 = pair ? tiles(1) : 0;
+      int x0 = 0;
       if (pair) {
-        emitted += order.left0 + order.left1 + max(tiles(0), tiles(1));
+        emitted += order.left0 + order.left1 + max(n0, n1);
         order = TileOrder();
       } else if (NT == 2) {
-        x0 = x1 = order.wants(true, true);
-        order.set(x0, tiles(0));
+        x0 = order.wants(true, true);
+        order.set(x0, n0);
         order.take(order.next());
         ++emitted;
       } else {
-        emitted += tiles(0);
+        emitted += n0;
       }
-      // rows: where they lie (all loads in flight at once)
-      int tok[NT][4];
-#pragma unroll
-      for (int k = 0; k < NT; ++k)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = k * 128 + u * 32 + lane, i = (e.row0 + r) / p.group;
-          tok[k][u] = r >= e.rows ? -1 : e.seq < 0 ? p.short_tok[i] : e.off_q + i;
-        }
+      const int parts = pair ? 2 : 1;  // row tile k of the item goes to stream x0 + k
       // Both streams' hand-overs of an item come before any wait for a Q tile: the MMA warp
       // may need the second one to go on with the item that still uses that tile.
+#pragma unroll 1
+      for (int k = 0; k < parts; ++k) {
+        const int x = x0 + k, r0 = k * 128, rows = min(128, e.rows - r0);
+        // rows: where they lie (all loads in flight at once)
+        int tok[4];
 #pragma unroll
-      for (int k = 0; k < NT; ++k) {
-        const int x = x0 + k, r0 = k * 128;  // row tile k of the item goes to stream x
-        if (x > x1 || !ok) continue;
+        for (int u = 0; u < 4; ++u) {
+          const int r = u * 32 + lane, i = (e.row0 + r0 + r) / p.group;
+          tok[u] = r >= rows ? -1 : e.seq < 0 ? p.short_tok[i] : e.off_q + i;
+        }
         // the slot's last readers are done with it
         if (!(ok = wait_slot(x))) break;
+        const int sl = puts(x) & 1;
+        PrefixItem& I = rings[x].item[sl];
         if (lane == 0) {
-          PrefixItem& I = rings[x].item[puts(x) & 1];
-          I.n = tiles(k);
+          I.n = k ? n1 : n0;
           I.pair = pair ? 1 : 0;
           I.np = np;
           I.p_key = e.t0 * BN;
@@ -534,84 +535,60 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           I.direct = e.slot < 0 ? 1 : 0;
           I.head = h;
           I.part = e.slot < 0 ? 0 : e.slot + static_cast<int>(partial_offset(p, e.rows, 0, h)) + r0;
-          I.rows = min(128, e.rows - r0);
-          mbar_arrive(&rings[x].kv[puts(x) & 1]);
+          I.rows = rows;
+          mbar_arrive(&rings[x].kv[sl]);
         }
-      }
-      // the rows' places and what they see
-#pragma unroll
-      for (int k = 0; k < NT; ++k) {
-        const int x = x0 + k, r0 = k * 128;
-        if (x > x1 || !ok) continue;
-        const int rows = min(128, e.rows - r0);
-        PrefixItem& I = rings[x].item[puts(x) & 1];
+        // the rows' places and what they see
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int r = u * 32 + lane;
           if (u * 32 >= rows) break;
           const int rr = e.row0 + r0 + r, i = rr / p.group, j = rr - i * p.group;
-          const bool in = r < rows && bounds_ok(tok[k][u] >= 0 && tok[k][u] < p.total_q, status);
-          I.row[r] = in ? tok[k][u] * p.hq + h * p.group + j : -1;
+          const bool in = r < rows && bounds_ok(tok[u] >= 0 && tok[u] < p.total_q, status);
+          I.row[r] = in ? tok[u] * p.hq + h * p.group + j : -1;
           I.lim[r] = in && e.seq >= 0 ? max(0, keys_seen(p.causal, e.len_k, e.diag, i) - o0 * BN) : 0;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&rings[x].full[puts(x) & 1]);
+        if (lane == 0) mbar_arrive(&rings[x].full[sl]);
       }
-      // Q rows by TMA: whole tiles where tokens lie side by side and a tile holds whole
-      // ones, else token by token (all heads of the group in one box, one lane each), and
-      // row by row where a token's heads do not all lie in this tile. A box may start at
+      if (!ok) break;
+      // Q rows by TMA: one box of 128 rows where tokens lie side by side and a tile holds
+      // whole ones, else token by token (all heads of the group in one box, one lane each),
+      // and row by row where a token's heads do not all lie in this tile. A box may start at
       // any 128-byte row of the tile: the swizzle goes by shared-memory address.
-#pragma unroll
-      for (int k = 0; k < NT; ++k) {
-        const int x = x0 + k, r0 = k * 128;
-        if (x > x1 || !ok) continue;
-        const int rows = min(128, e.rows - r0);
-        if (puts(x) > 0 &&
-            !(ok = __all_sync(0xffffffffu, mbar_wait(&bar_q_empty[x], (puts(x) - 1) & 1, status))))
-          break;
-        if (x) ++puts1;
-        else ++puts0;
+#pragma unroll 1
+      for (int k = 0; k < parts; ++k) {
+        const int x = x0 + k, n = puts(x);
+        if (n > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bar_q_empty[x], (n - 1) & 1, status)))) break;
         uint8_t* q_tile = sQ + x * S::kQBytes;
-        const int rr0 = e.row0 + r0, i0 = rr0 / p.group, i1 = (rr0 + rows - 1) / p.group;
-        const int first_tok = __shfl_sync(0xffffffffu, tok[k][0], 0);
-        int last_tok = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (u == (rows - 1) >> 5) last_tok = __shfl_sync(0xffffffffu, tok[k][u], (rows - 1) & 31);
-        const bool whole = tm.q_tokens > 0 && last_tok - first_tok == i1 - i0 && rr0 % p.group == 0;
+        const PrefixItem& I = rings[x].item[n & 1];
+        const int rows = min(128, e.rows - k * 128), h0 = h * p.group;
+        const int row_a = I.row[0], row_z = I.row[rows - 1];
+        const int tok_a = row_a / p.hq, tok_z = row_z / p.hq;
+        const bool whole = tm.q_tokens > 0 && min(row_a, row_z) >= 0 && row_a - tok_a * p.hq == h0 &&
+                           (tok_z - tok_a) * p.group + row_z - tok_z * p.hq - h0 == rows - 1;
         if (lane == 0) mbar_arrive_expect_tx(&bar_q_full[x], (whole ? 128 : rows) * 128 * S::kChunks);
         __syncwarp();
-        if (whole) {
-          if (lane < S::kChunks)
-            tma_load_4d(q_tile + lane * 16384, &tm.q_tile, &bar_q_full[x], lane * 64, h * p.group, 0, first_tok);
-        } else {
-          // this lane's tokens, whole ones, then the rows of the first and last one if cut
-          const int lead = i0 * p.group < rr0 ? (i0 + 1) * p.group - rr0 : 0;
-          const int tail = (i1 + 1) * p.group > rr0 + rows ? rr0 + rows - max(i1 * p.group, rr0 + lead) : 0;
-          const bool boxes = p.group <= 128;
-          const int w0 = i0 + (lead > 0 ? 1 : 0), w1 = i1 - (tail > 0 ? 1 : 0);
-          if (boxes) {
-            for (int i = w0 + lane; i <= w1; i += 32) {
-              const int t = e.seq < 0 ? p.short_tok[i] : e.off_q + i;
-              for (int c = 0; c < S::kChunks; ++c)
-                tma_load_4d(q_tile + c * 16384 + (i * p.group - rr0) * 128, &tm.q_token, &bar_q_full[x], c * 64,
-                            h * p.group, 0, t);
-            }
-          }
-          const int whole_rows = boxes ? max(0, w1 - w0 + 1) * p.group : 0;
-          for (int z = lane; z < rows - whole_rows; z += 32) {
-            const int r = !boxes || z < lead ? z : z + whole_rows;
-            const int i = (rr0 + r) / p.group, t = e.seq < 0 ? p.short_tok[i] : e.off_q + i;
-            for (int c = 0; c < S::kChunks; ++c)
-              tma_load_4d(q_tile + c * 16384 + r * 128, &tm.q_row, &bar_q_full[x], c * 64, rr0 + r - i * p.group + h * p.group,
-                          0, t);
-          }
+#pragma unroll 1
+        for (int r = lane; r < rows; r += 32) {
+          // (a row without a place, after an error: zeros, from behind the last token)
+          const int row = I.row[r], t = row < 0 ? p.total_q : row / p.hq, head = row < 0 ? h0 : row - t * p.hq;
+          const int j = head - h0;  // the token's rows in the tile: from r - j on
+          const bool box = row >= 0 && p.group <= 128 && r >= j && r - j + p.group <= rows;
+          if (whole ? r > 0 : box && j > 0) continue;
+          const CUtensorMap* map = whole ? &tm.q_tile : box ? &tm.q_token : &tm.q_row;
+#pragma unroll 1
+          for (int c = 0; c < S::kChunks; ++c)
+            tma_load_4d(q_tile + c * 16384 + r * 128, map, &bar_q_full[x], c * 64, head, 0, t);
         }
         __syncwarp();
+        if (x) ++puts1;
+        else ++puts0;
       }
       if (!ok) break;
     }
     // no more items, on every stream
+#pragma unroll 1
     for (int x = 0; x < NT && ok; ++x) {
       if (!(ok = wait_slot(x))) break;
       if (lane == 0) {
@@ -623,85 +600,99 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
   } else if (warp == kWarpKv) {
     // ------------------------------------------------------------- K and V tiles
     if (lane == 0) {
-      int it = 0;
-      bool ok = true;
       struct Tiles {
         int np, p_key, o_key, h, j;
       };
-      Tiles cur[2] = {};
-      int gets[2] = {0, 0};
-      bool held[2] = {false, false}, ended[2] = {false, NT == 1};
-      int pair_n[2] = {0, 0};
+      int it = 0;
+      Tiles cur0{}, cur1{};
+      int gets0 = 0, gets1 = 0;
+      bool held0 = false, held1 = false, ended0 = false, ended1 = NT == 1;
+      int pair_left = 0;  // tiles that the item on both streams has left
+      int pair_n = 0;
       TileOrder order;
       // K of a tile goes before V of the tile before it: that is the order in which their
       // stages come free, as a stream's next scores do not wait for the other's product (6 %
       // of a step over many long caches; with V beside its K, 1 % less for wide items).
       const CUtensorMap* v_map = nullptr;  // the V tile that is still to be loaded
       int v_key = 0, v_head = 0;
-      auto load_v = [&]() -> bool {
-        if (!v_map) return true;
-        const int st = (it - 1) % NS;
-        if (it > NS && !mbar_wait(&bar_v_empty[st], (((it - 1) / NS) - 1) & 1, status)) return false;
-        mbar_arrive_expect_tx(&bar_v_full[st], S::kKVBytes);
+      auto load = [&](uint8_t* base, uint64_t* full, uint64_t* empty, const CUtensorMap* map, int head, int key,
+                      int tile) -> bool {
+        const int st = tile % NS;
+        if (tile >= NS && !mbar_wait(&empty[st], ((tile / NS) - 1) & 1, status)) return false;
+        mbar_arrive_expect_tx(&full[st], S::kKVBytes);
+#pragma unroll 1
         for (int k = 0; k < S::kChunks; ++k)
-          tma_load_4d(sV + st * S::kKVBytes + k * BN * 128, v_map, &bar_v_full[st], k * 64, v_head, 0, v_key);
-        v_map = nullptr;
+          tma_load_4d(base + st * S::kKVBytes + k * BN * 128, map, &full[st], k * 64, head, 0, key);
         return true;
       };
-      auto load_tile = [&](Tiles& c) -> bool {
-        const int st = it % NS;
+      for (;;) {
+        bool flush = false;  // no tile to load before a wait or the end: V of the last one
+        const int w = pair_left > 0 ? -1 : order.wants(!held0 && !ended0, !held1 && !ended1);
+        if (w >= 0) {
+          const int gets = w ? gets1 : gets0, sl = gets & 1;
+          uint64_t* bar = &rings[w].kv[sl];
+          if (!mbar_try_wait(bar, (gets >> 1) & 1)) {
+            flush = v_map != nullptr;
+            if (!flush && !mbar_wait(bar, (gets >> 1) & 1, status)) break;
+          }
+          if (!flush) {
+            const PrefixItem& I = rings[w].item[sl];
+            const int n = I.n;
+            const Tiles c{I.np, I.p_key, I.o_key, I.head, 0};
+            const bool pair = I.pair != 0;
+            mbar_arrive(&rings[w].empty[sl]);
+            if (w) {
+              ++gets1;
+              cur1 = c;
+              if (n < 0) ended1 = true;
+              else if (pair) held1 = true;
+            } else {
+              ++gets0;
+              cur0 = c;
+              if (n < 0) ended0 = true;
+              else if (pair) held0 = true;
+            }
+            if (n >= 0 && pair) pair_n = max(pair_n, n);
+            if (n >= 0 && !pair) order.set(w, n);
+          }
+        }
+        int x = -1;  // stream whose tile is next
+        if (pair_left > 0) {
+          x = 0;
+          --pair_left;
+        } else if (!flush && (order.left0 > 0 || order.left1 > 0)) {
+          x = order.next();
+          order.take(x);
+        } else if (!flush && held0 && held1) {
+          pair_left = pair_n;
+          pair_n = 0;
+          held0 = held1 = false;
+          order = TileOrder();
+          continue;
+        } else if (!flush && w < 0) {
+          if (!v_map) break;
+          flush = true;
+        }
+        if (x < 0 && !flush) continue;
+        const Tiles c = x == 1 ? cur1 : cur0;
         const bool pre = c.j < c.np;
-        const CUtensorMap* mk = pre ? &tm.kp : &tm.k;
         const int key = pre ? c.p_key + c.j * BN : c.o_key + (c.j - c.np) * BN;
-        if (it >= NS && !mbar_wait(&bar_k_empty[st], ((it / NS) - 1) & 1, status)) return false;
-        mbar_arrive_expect_tx(&bar_k_full[st], S::kKVBytes);
-        for (int k = 0; k < S::kChunks; ++k)
-          tma_load_4d(sK + st * S::kKVBytes + k * BN * 128, mk, &bar_k_full[st], k * 64, c.h, 0, key);
-        if (!load_v()) return false;
+        bool ok = true;
+#pragma unroll 1
+        for (int kv = 0; kv < 2 && ok; ++kv) {  // K of this tile, V of the one before
+          if (kv == 0 ? x < 0 : v_map == nullptr) continue;
+          ok = load(kv ? sV : sK, kv ? bar_v_full : bar_k_full, kv ? bar_v_empty : bar_k_empty,
+                    kv ? v_map : pre ? &tm.kp : &tm.k, kv ? v_head : c.h, kv ? v_key : key, kv ? it - 1 : it);
+        }
+        if (!ok) break;
+        v_map = nullptr;
+        if (x < 0) continue;
         v_map = pre ? &tm.vp : &tm.v;
         v_key = key;
         v_head = c.h;
-        ++c.j;
+        if (x) ++cur1.j;
+        else ++cur0.j;
         *const_cast<volatile int*>(&tiles_loaded) = ++it;
-        return true;
-      };
-      while (ok) {
-        const int w = order.wants(!held[0] && !ended[0], !held[1] && !ended[1]);
-#pragma unroll
-        for (int x = 0; x < NT; ++x) {
-          if (x != w) continue;
-          const int sl = gets[x] & 1;
-          if (!mbar_try_wait(&rings[x].kv[sl], (gets[x] >> 1) & 1) &&
-              !(ok = load_v() && mbar_wait(&rings[x].kv[sl], (gets[x] >> 1) & 1, status)))
-            break;
-          ++gets[x];
-          const PrefixItem& I = rings[x].item[sl];
-          const int n = I.n;
-          cur[x] = {I.np, I.p_key, I.o_key, I.head, 0};
-          const bool pair = I.pair != 0;
-          mbar_arrive(&rings[x].empty[sl]);
-          if (n < 0) {
-            ended[x] = true;
-          } else if (pair) {
-            held[x] = true;
-            pair_n[x] = n;
-          } else {
-            order.set(x, n);
-          }
-        }
-        if (!ok) break;
-        if (order.left0 > 0 || order.left1 > 0) {
-          const int x = order.next();
-          order.take(x);
-          ok = x ? load_tile(cur[1]) : load_tile(cur[0]);
-        } else if (held[0] && held[1]) {
-          for (int j = max(pair_n[0], pair_n[1]); j > 0 && ok; --j) ok = load_tile(cur[0]);
-          held[0] = held[1] = false;
-          order = TileOrder();
-        } else if (w < 0) {
-          load_v();
-          break;
-        }
       }
     }
   } else if (warp == kWarpMma) {
@@ -711,193 +702,178 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
     const SmemDesc dq = smem_desc(smem_u32(sQ), 16, 1024, kLayoutSW128);
     const SmemDesc dk = smem_desc(smem_u32(sK), 16, 1024, kLayoutSW128);
     const SmemDesc dv = smem_desc(smem_u32(sV), BN * 128, 1024, kLayoutSW128);
-    int it = 0;             // key tiles issued: tile `it` is in stage it % NS
-    int np[2] = {0, 0};     // P hand-overs consumed per stream
-    int no[2] = {0, 0};     // items whose O a stream has accumulated
-    int gets[2] = {0, 0};   // items taken per stream (each used its Q tile once)
-    bool held[2] = {false, false}, ended[2] = {false, NT == 1};
-    bool ok = true;
-    struct Running {
-      int n, j;                     // key tiles, and those whose scores are issued
-      int n_pre, p_left, o_left;
-      int pend;                     // tile whose scores are issued, product not: its number `it`; -1
+    // Items on one stream: one copy of the code serves both streams; a turn of stream x issues
+    // the product of its last tile and the scores of its next one. Such items are short, so
+    // each passes through all of the code, and its length counts: with a copy per stream and
+    // use the kernel was 163 KB long and every role ran at a third of its speed. Items on
+    // both streams are long; their loop has a copy per stream (8 % faster).
+    struct Stream {
+      int n, j;                   // the item's key tiles, and those whose scores are issued
+      int n_pre, p_left, o_left;  // as in PrefixItem
+      int pend;                   // tile whose scores are issued, product not: its number; -1
+      int real;                   // real keys of that tile
+      bool first, last;           // it is its item's first or last one
+      int np, no;                 // P hand-overs consumed; items whose O is accumulated
+      int gets;                   // hand-overs taken (each used its Q tile once)
     };
-    Running cur[2] = {{0, 0, 0, 0, 0, -1}, {0, 0, 0, 0, 0, -1}};
+    Stream s0{}, s1{};
+    s0.pend = s1.pend = -1;
+    bool held0 = false, held1 = false, ended0 = false, ended1 = NT == 1;
+    int it = 0;  // key tiles so far: tile `it` is in stage it % NS
     TileOrder order;
-    auto issue_s = [&](int x, int tile) {
-      const int st = tile % NS;
-      const SmemDesc qx{dq.lo + ((x * S::kQBytes) >> 4), dq.hi};
-      const SmemDesc kst{dk.lo + ((st * S::kKVBytes) >> 4), dk.hi};
-      __syncwarp();  // elect.sync in the MMA wrappers needs a converged warp
-#pragma unroll
-      for (int s = 0; s < kD / 16; ++s)
-        mma_ss(tmem + S::col_s(x), qx, (s >> 2) * 16384 + (s & 3) * 32, kst, (s >> 2) * (BN * 128) + (s & 3) * 32,
-               idS, s > 0 ? 1u : 0u);
-      mma_commit(&bar_s_full[x]);
+    auto wait_k = [&](int tile) { return mbar_wait_warp(&bar_k_full[tile % NS], (tile / NS) & 1, status); };
+    auto wait_v = [&](int tile) { return mbar_wait_warp(&bar_v_full[tile % NS], (tile / NS) & 1, status); };
+    // P is there, and for an item's first product the last item's O is read
+    auto wait_p = [&](int x, Stream& c, bool first) {
+      if (!mbar_wait_warp(&bar_p_ready[x], c.np & 1, status)) return false;
+      ++c.np;
+      return !first || c.no == 0 || mbar_wait_warp(&bar_o_empty[x], (c.no - 1) & 1, status);
+    };
+    // V rows that are no real key become zeros (P is 0 there, but 0 times NaN is not)
+    auto zero_v = [&](int tile, int real) {
+#pragma unroll 1
+      for (int z = real * 8 + lane; z < BN * 8; z += 32)
+#pragma unroll 1
+        for (int k = 0; k < S::kChunks; ++k)
+          st_shared_v4(sV + (tile % NS) * S::kKVBytes + k * BN * 128 + z * 16, 0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    auto real_keys = [&](const Stream& c, int j) {
+      return j < c.n_pre ? c.p_left - j * BN : c.o_left - (j - c.n_pre) * BN;
     };
     auto issue_pv = [&](int x, int tile, bool first) {
-      const int st = tile % NS;
-      const SmemDesc vst{dv.lo + ((st * S::kKVBytes) >> 4), dv.hi};
-      const uint32_t acc0 = first ? 0u : 1u;
-      __syncwarp();
+      const SmemDesc vst{dv.lo + (((tile % NS) * S::kKVBytes) >> 4), dv.hi};
+      const uint32_t t_o = tmem + S::col_o(x), t_p = tmem + S::col_s(x), acc0 = first ? 0u : 1u;
+      __syncwarp();  // elect.sync in the MMA wrappers needs a converged warp
+      if (elect_one())
 #pragma unroll
-      for (int s = 0; s < BN / 16; ++s)
-        mma_ts(tmem + S::col_o(x), tmem + S::col_s(x) + s * 8, vst, s * 2048, idPV, s > 0 ? 1u : acc0);
+      for (int k = 0; k < BN / 16; ++k) mma_ts_one(t_o, t_p + k * 8, vst, k * 2048, idPV, k > 0 ? 1u : acc0);
     };
-    auto wait_k = [&](int tile) { return mbar_wait_warp(&bar_k_full[tile % NS], (tile / NS) & 1, status); };
-    // V of a tile: rows that are no real key become zeros (P is 0 there, but 0 times NaN is
-    // not). j: the tile's number in its item.
-    auto wait_v = [&](int x, int tile, int j) -> bool {
-      const int st = tile % NS;
-      if (!mbar_wait_warp(&bar_v_full[st], (tile / NS) & 1, status)) return false;
-      const int real = j < cur[x].n_pre ? cur[x].p_left - j * BN : cur[x].o_left - (j - cur[x].n_pre) * BN;
-      if (real < BN) {
-        for (int z = real * 8 + lane; z < BN * 8; z += 32)
-          for (int c = 0; c < S::kChunks; ++c)
-            st_shared_v4(sV + st * S::kKVBytes + c * BN * 128 + z * 16, 0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      return true;
+    auto issue_s = [&](int x, int tile) {
+      const SmemDesc qx{dq.lo + ((x * S::kQBytes) >> 4), dq.hi};
+      const SmemDesc kst{dk.lo + (((tile % NS) * S::kKVBytes) >> 4), dk.hi};
+      const uint32_t t_s = tmem + S::col_s(x);
+      __syncwarp();
+      if (elect_one())
+#pragma unroll
+      for (int k = 0; k < kD / 16; ++k)
+        mma_ss_one(t_s, qx, (k >> 2) * 16384 + (k & 3) * 32, kst, (k >> 2) * (BN * 128) + (k & 3) * 32, idS, k > 0 ? 1u : 0u);
+      mma_commit(&bar_s_full[x]);
     };
-    // P of stream x is ready, and for an item's first product the last item's O is read
-    auto wait_p = [&](int x, bool first) -> bool {
-      if (!mbar_wait_warp(&bar_p_ready[x], np[x] & 1, status)) return false;
-      ++np[x];
-      return !(first && no[x] > 0) || mbar_wait_warp(&bar_o_empty[x], (no[x] - 1) & 1, status);
-    };
-    // One step of stream x: the product of its last tile, then the scores of its next one.
-    auto step = [&](auto x_tag) -> bool {
-      constexpr int x = decltype(x_tag)::value;
-      auto& c = cur[x];
-      if (c.pend >= 0) {
-        const bool first_tile = c.j == 1, last_tile = c.j == c.n;
-        if (!wait_p(x, first_tile) || !wait_v(x, c.pend, c.j - 1)) return false;
-        tc_fence_after();
-        issue_pv(x, c.pend, first_tile);
-        mma_commit(&bar_v_empty[c.pend % NS]);
-        c.pend = -1;
-        if (last_tile) {
-          mma_commit(&bar_o_full[x]);
-          ++no[x];
-        }
-      }
-      return true;
-    };
-    auto start = [&](auto x_tag) -> bool {
-      constexpr int x = decltype(x_tag)::value;
-      auto& c = cur[x];
-      if (c.j == 0 && !mbar_wait_warp(&bar_q_full[x], (gets[x] - 1) & 1, status)) return false;
-      if (!wait_k(it)) return false;
-      tc_fence_after();
-      issue_s(x, it);
-      mma_commit(&bar_k_empty[it % NS]);
-      if (++c.j == c.n) mma_commit(&bar_q_empty[x]);
-      c.pend = it++;
-      return true;
-    };
-    // An item's next hand-over to stream x (its fields wait in `next` until the stream's
-    // last product is issued).
-    struct Next {
-      int n, n_pre, p_left, o_left;
-    };
-    Next next[2] = {};
+    // An item on both streams: in round r both products of tile r - 1 and both scores of tile r.
     auto run_pair = [&]() -> bool {
-      const int n[2] = {next[0].n, next[NT - 1].n};
-      for (int x = 0; x < NT; ++x) {
-        cur[x].n_pre = next[x].n_pre;
-        cur[x].p_left = next[x].p_left;
-        cur[x].o_left = next[x].o_left;
-        if (!mbar_wait_warp(&bar_q_full[x], (gets[x] - 1) & 1, status)) return false;
-      }
-      int s_left[2] = {n[0], n[1]};
-      auto scores = [&](auto x_tag, int tile) {
-        constexpr int x = decltype(x_tag)::value;
-        issue_s(x, tile);
-        if (--s_left[x] == 0) mma_commit(&bar_q_empty[x]);
-      };
-      const int rounds = max(n[0], n[1]);
-      if (!wait_k(it)) return false;
-      tc_fence_after();
-      for (int x = 0; x < NT; ++x)
-        if (n[x] == 0) mma_commit(&bar_q_empty[x]);
-      if (n[0] > 0) scores(std::integral_constant<int, 0>{}, it);
-      if (n[1] > 0) scores(std::integral_constant<int, NT - 1>{}, it);
-      mma_commit(&bar_k_empty[it % NS]);
-      for (int j = 0; j < rounds; ++j) {
+      const int rounds = max(s0.n, s1.n);
+      if (!mbar_wait_warp(&bar_q_full[0], (s0.gets - 1) & 1, status) ||
+          !mbar_wait_warp(&bar_q_full[NT - 1], (s1.gets - 1) & 1, status))
+        return false;
+      if (s0.n == 0) mma_commit(&bar_q_empty[0]);
+      if (s1.n == 0) mma_commit(&bar_q_empty[NT - 1]);
+#pragma unroll 1
+      for (int r = 0; r <= rounds; ++r) {
         bool v_ready = false, k_ready = false;
-        auto turn = [&](auto x_tag) -> bool {
+        auto turn = [&](auto x_tag, Stream& c) -> bool {
           constexpr int x = decltype(x_tag)::value;
-          if (j >= n[x]) return true;
-          if (!wait_p(x, j == 0)) return false;
-          if (!v_ready && !wait_v(x, it + j, j)) return false;
-          v_ready = true;
-          tc_fence_after();
-          issue_pv(x, it + j, j == 0);
-          if (j + 1 < n[x]) {
-            if (!k_ready && !wait_k(it + j + 1)) return false;
+          if (r > 0 && r <= c.n) {
+            if (!wait_p(x, c, r == 1)) return false;
+            if (!v_ready) {
+              if (!wait_v(it + r - 1)) return false;
+              const int real = real_keys(c, r - 1);
+              if (real < BN) zero_v(it + r - 1, real);
+              v_ready = true;
+            }
+            tc_fence_after();
+            issue_pv(x, it + r - 1, r == 1);
+          }
+          if (r < c.n) {
+            if (!k_ready && !wait_k(it + r)) return false;
             k_ready = true;
             tc_fence_after();
-            scores(x_tag, it + j + 1);
-          } else {
+            issue_s(x, it + r);
+            if (r + 1 == c.n) mma_commit(&bar_q_empty[x]);
+          } else if (r == c.n && r > 0) {
             mma_commit(&bar_o_full[x]);
-            ++no[x];
+            ++c.no;
           }
           return true;
         };
-        if (!turn(std::integral_constant<int, 0>{})) return false;
-        if (NT == 2 && !turn(std::integral_constant<int, NT - 1>{})) return false;
-        mma_commit(&bar_v_empty[(it + j) % NS]);
-        if (j + 1 < rounds) mma_commit(&bar_k_empty[(it + j + 1) % NS]);
+        if (!turn(std::integral_constant<int, 0>{}, s0)) return false;
+        if (!turn(std::integral_constant<int, NT - 1>{}, s1)) return false;
+        if (r > 0) mma_commit(&bar_v_empty[(it + r - 1) % NS]);
+        if (r < rounds) mma_commit(&bar_k_empty[(it + r) % NS]);
       }
       it += rounds;
       return true;
     };
-    while (ok) {
-      const int w = order.wants(!held[0] && !ended[0], !held[1] && !ended[1]);
-#pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        if (x != w) continue;
-        const int sl = gets[x] & 1;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&rings[x].full[sl], (gets[x] >> 1) & 1, status)))) break;
-        ++gets[x];
-        const PrefixItem& I = rings[x].item[sl];
-        next[x] = {I.n, I.np, I.p_left, I.o_left};
+    for (;;) {
+      const int w = order.wants(!held0 && !ended0, !held1 && !ended1);
+      if (w >= 0) {
+        const int gets = w ? s1.gets : s0.gets, sl = gets & 1;
+        if (!mbar_wait_warp(&rings[w].full[sl], (gets >> 1) & 1, status)) break;
+        const PrefixItem& I = rings[w].item[sl];
+        const int n = I.n, n_pre = I.np, p_left = I.p_left, o_left = I.o_left;
         const bool pair = I.pair != 0;
         __syncwarp();
-        mbar_arrive(&rings[x].empty[sl]);
-        if (next[x].n < 0) ended[x] = true;
-        else if (pair) held[x] = true;
-        else order.set(x, next[x].n);
-      }
-      if (!ok) break;
-      // a stream acts while it has tiles to start or a product to finish
-      const bool act0 = order.left0 > 0 || cur[0].pend >= 0, act1 = order.left1 > 0 || cur[1].pend >= 0;
-      if (act0 || act1) {
-        const int x = (order.last == 1 ? act0 : act1) ? 1 - order.last : order.last;
-        order.last = x;
-        auto act_on = [&](auto x_tag) -> bool {
-          constexpr int y = decltype(x_tag)::value;
-          if (!step(x_tag)) return false;
-          if (order.left(y) == 0) return true;
-          if (order.left(y) == next[y].n) {  // a new item
-            cur[y].n = next[y].n;
-            cur[y].j = 0;
-            cur[y].n_pre = next[y].n_pre;
-            cur[y].p_left = next[y].p_left;
-            cur[y].o_left = next[y].o_left;
+        mbar_arrive(&rings[w].empty[sl]);
+        auto take = [&](Stream& c, bool& held, bool& ended) {
+          ++c.gets;
+          if (n < 0) {
+            ended = true;
+          } else {
+            c.n = n;
+            c.j = 0;
+            c.n_pre = n_pre;
+            c.p_left = p_left;
+            c.o_left = o_left;
+            if (pair) held = true;
           }
-          order.set(y, order.left(y) - 1);
-          return start(x_tag);
         };
-        ok = x == 0 ? act_on(std::integral_constant<int, 0>{}) : act_on(std::integral_constant<int, NT - 1>{});
-      } else if (held[0] && held[1]) {
-        ok = run_pair();
-        held[0] = held[1] = false;
-        order = TileOrder();
-      } else if (w < 0) {
-        break;
+        if (w) take(s1, held1, ended1);
+        else take(s0, held0, ended0);
+        if (n >= 0 && !pair) order.set(w, n);
       }
+      // a stream acts while it has tiles to score or a product to issue
+      const bool act0 = order.left0 > 0 || s0.pend >= 0, act1 = order.left1 > 0 || s1.pend >= 0;
+      if (!act0 && !act1) {
+        if (NT == 2 && held0 && held1) {
+          if (!run_pair()) break;
+          held0 = held1 = false;
+          order = TileOrder();
+        } else if (w < 0) {
+          break;
+        }
+        continue;
+      }
+      const int x = (order.last == 1 ? act0 : act1) ? 1 - order.last : order.last;
+      order.last = x;
+      Stream c = NT == 2 && x ? s1 : s0;
+      if (c.pend >= 0) {
+        if (!wait_p(x, c, c.first) || !wait_v(c.pend)) break;
+        if (c.real < BN) zero_v(c.pend, c.real);
+        tc_fence_after();
+        issue_pv(x, c.pend, c.first);
+        mma_commit(&bar_v_empty[c.pend % NS]);
+        if (c.last) {
+          mma_commit(&bar_o_full[x]);
+          ++c.no;
+        }
+        c.pend = -1;
+      }
+      if (order.left(x) > 0) {
+        order.set(x, order.left(x) - 1);
+        if (c.j == 0 && !mbar_wait_warp(&bar_q_full[x], (c.gets - 1) & 1, status)) break;
+        if (!wait_k(it)) break;
+        tc_fence_after();
+        issue_s(x, it);
+        mma_commit(&bar_k_empty[it % NS]);
+        c.first = c.j == 0;
+        c.real = real_keys(c, c.j);
+        c.last = ++c.j == c.n;
+        c.pend = it++;
+        if (c.last) mma_commit(&bar_q_empty[x]);
+      }
+      if (NT == 2 && x) s1 = c;
+      else s0 = c;
     }
   } else {
     // ------------------------------------------------------------- softmax
@@ -913,6 +889,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
     uint8_t* stage = sStage + warp * 2048;
     int ns = 0, no = 0;  // S hand-overs of this stream, and items with an output, so far
     bool ok = true;
+#pragma unroll 1
     for (int ii = 0; ok; ++ii) {
       const int sl = ii & 1;
       ok = __all_sync(0xffffffffu, mbar_wait(&rings[x].full[sl], (ii >> 1) & 1, status));
@@ -929,6 +906,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       const bool live = row >= 0;
       const bool alive = __any_sync(0xffffffffu, live);  // no row of this warp: only hand-overs
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int j = 0; j < n; ++j) {
         ok = __all_sync(0xffffffffu, mbar_wait(&bar_s_full[x], ns & 1, status));
         if (!ok) break;
@@ -984,7 +962,8 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         uint32_t pk[BN / 32][16];
         // a row that has seen no key yet: any finite offset makes its P zeros
         float neg = !live ? -INFINITY : m == -INFINITY ? 0.f : -m;
-        for (;;) {
+        bool again;
+        do {  // (tested at its end only: the compiler keeps one copy of the pass)
           const uint64_t sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(neg, neg);
 #pragma unroll
           for (int k = 0; k < 4; ++k) sp[k] = f2_pack(0.f, 0.f);
@@ -1004,19 +983,21 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           }
           // a row whose P sums to at most 2^8 has no entry above 2^8: nothing to raise
           const float2 s01 = f2_unpack(fadd2(fadd2(sp[0], sp[1]), fadd2(sp[2], sp[3])));
-          if (!__any_sync(0xffffffffu, s01.x + s01.y > 256.0f)) break;
-          const float mxs = max_of(BN);
-          const bool raise = live && nvalid > 0 && mxs > m + 8.0f;
-          if (!__any_sync(0xffffffffu, raise)) break;
-          if (raise) {
-            // a row without an earlier key has nothing to scale (and l is 0)
-            alpha = m == -INFINITY ? 0.f : ex2p(m - mxs);
-            m = mxs;
-            neg = -mxs;
+          again = __any_sync(0xffffffffu, s01.x + s01.y > 256.0f);
+          if (again) {
+            const float mxs = max_of(BN);
+            const bool raise = live && nvalid > 0 && mxs > m + 8.0f;
+            again = __any_sync(0xffffffffu, raise);
+            if (raise) {
+              // a row without an earlier key has nothing to scale (and l is 0)
+              alpha = m == -INFINITY ? 0.f : ex2p(m - mxs);
+              m = mxs;
+              neg = -mxs;
+            }
           }
           // S(j) was issued after P V(j-1): O is final for the tiles before this one. At the
           // item's first tile there is nothing to scale: the product will overwrite it.
-          if (j > 0) {
+          if (again && j > 0) {
 #pragma unroll 1
             for (int c0 = 0; c0 < kD; c0 += 32) {
               uint32_t o[32];
@@ -1028,7 +1009,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
               tmem_st16(t_o + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
             }
           }
-        }
+        } while (again);
 #pragma unroll
         for (int k = 0; k < BN / 32; ++k) tmem_st16(t_s + 16 * k, pk[k]);
         tmem_st_wait();
