@@ -1046,7 +1046,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           __syncwarp();
         };
         if (direct) {
-          const float inv = l > 0.f ? 1.0f / l : 0.f;
+          const float inv = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll 1
           for (int c0 = 0; c0 < p.d; c0 += 32) {
             uint32_t o[32], w[16];
@@ -1057,7 +1057,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
             // a row without a key: zeros, whatever TMEM holds
 #pragma unroll
             for (int c = 0; c < 16; ++c)
-              w[c] = n > 0 && l > 0.f
+              w[c] = n > 0 && l != 0.f
                          ? pack2<kBF16>(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv)
                          : 0u;
             store64(w, [&](int rr, int c, const uint4& v) {
@@ -1066,7 +1066,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
                 *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + static_cast<size_t>(at) * p.d + c0 + 8 * c) = v;
             });
           }
-          if (live) p.lse[row] = l > 0.f ? m * 0.69314718055994531f + logf(l) : -INFINITY;
+          if (live) p.lse[row] = l == 0.f ? -INFINITY : m * 0.69314718055994531f + logf(l);
         } else {
           if (live && bounds_ok(part + lane < static_cast<size_t>(p.cap_rows), status))
             p.part_ml[part + lane] = make_float2(m, l);
@@ -1211,7 +1211,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     float M = -INFINITY;
     for (int k = lane; k < n; k += 32) {
       const float2 ml = p.part_ml[at(k)];
-      if (ml.y > 0.f) M = fmaxf(M, ml.x);
+      if (ml.y != 0.f) M = fmaxf(M, ml.x);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -1222,7 +1222,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
       if (k0 + lane < n) {
         const float2 ml = p.part_ml[at(k0 + lane)];
         // a part without a visible key left no output
-        wgt = ml.y > 0.f ? ex2p(ml.x - M) : 0.f;
+        wgt = ml.y != 0.f ? ex2p(ml.x - M) : 0.f;
         L += wgt * ml.y;
       }
       uint32_t todo = __ballot_sync(0xffffffffu, wgt != 0.f && (k0 + lane) % kWarps == sub);
@@ -1267,7 +1267,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
         for (int c = 0; c < 8; ++c) acc[c] += s_acc[warp + o][(c >> 2) * 128 + 4 * lane + (c & 3)];
     }
     if (!write) continue;
-    const float inv = L > 0.f ? 1.0f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.0f / L;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int col = 128 * c + 4 * lane;
@@ -1278,7 +1278,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
         *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + row * p.d + col) = v;
       }
     }
-    if (lane == 0) p.lse[row] = !real ? 0.f : L > 0.f ? M * 0.69314718055994531f + logf(L) : -INFINITY;
+    if (lane == 0) p.lse[row] = !real ? 0.f : L == 0.f ? -INFINITY : M * 0.69314718055994531f + logf(L);
   }
 }
 

@@ -320,6 +320,8 @@ int te_attn_rope_sbhd(const void* q, const void* k, void* q_out, void* k_out,
  * their padded slots, with TE_MASK_PADDING_CAUSAL_BOTTOM_RIGHT. Masks place queries and
  * own keys of one sequence against each other; the prefix lies before both. A real query
  * that sees no key at all gets out = 0, lse = -inf, dq = 0. total_q * hq < 2^31.
+ * The forward takes any bits in rows that hold no token (a cache's free slots, the rows
+ * behind the prefix's real length): none reaches a result. A NaN that a row sees does.
  * An inconsistent prefix_len counts as 0 and raises TE_STATUS_BAD_SEQLENS.
  * The workspaces' sizes are the *_workspace_size functions'; te_attn_read_status() works
  * on them.

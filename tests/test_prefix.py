@@ -206,6 +206,21 @@ def test_single_tokens(d, hq, hkv, batch, prefix):
 
 
 @gpu
+@pytest.mark.parametrize("d,hq,hkv,batch,longest", [(128, 8, 2, 84, 2600), (64, 4, 4, 150, 1500), (256, 16, 2, 40, 1900),
+                                                    (80, 18, 2, 64, 1100)])
+def test_many_long_caches(d, hq, hkv, batch, longest):
+    """Decoding where every block goes through many items of many key tiles, on one stream and
+    on both: groups of 1 to 8 heads and of 9; the same bits every time."""
+    lk = [longest - (91 * i * i + 13 * i) % (longest // 2) for i in range(batch)]
+    c = Case(batch, [1] * batch, lk, 700, hq, hkv, d, torch.bfloat16, BR, slot_q=1, slot_k=64, spread=0.4)
+    out, lse = c.fwd()
+    for _ in range(10):
+        again = c.fwd()
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    c.check(backward=False)
+
+
+@gpu
 def test_long_cache_of_one_sequence():
     """A single query over a long axis, which is split and joined; scores that grow along it
     move the running maximum in every part."""
@@ -248,6 +263,139 @@ def test_bad_lengths_are_reported():
     wsb = torch.empty(ta.prefix_bwd_workspace_size(3, c.q.shape[0], c.k.shape[0], 64, 4, 2, 64), dtype=torch.uint8, device="cuda")
     c.bwd(out, lse, workspace=wsb)
     assert ta.read_status(wsb) == 1
+
+
+@gpu
+@pytest.mark.parametrize("d,hq,hkv,dtype", [(128, 8, 2, torch.bfloat16), (64, 3, 3, torch.float16), (256, 8, 1, torch.bfloat16)])
+@pytest.mark.parametrize("mask", [BR, TL, PAD])
+def test_forward_takes_any_bits_in_the_pads(d, hq, hkv, dtype, mask):
+    """NaN and infinities in every row that holds no token, in a cache's free slots, behind the
+    last sequence and behind the prefix's real length: the same bits as with zeros there."""
+    c = Case(23, [1, 0, 37, 70, 1, 5], [9, 4, 37, 150, 0, 301], 133, hq, hkv, d, dtype, mask, prefix_rows=200, slot_k=64, tail=9).dev()
+    spans = (c.spans_q, c.spans_k, c.spans_k, [(0, 133)], [(0, 133)])
+    free = []
+    for x, at in zip(c.on, spans):
+        keep = torch.zeros(x.shape[0], dtype=torch.bool)
+        for o, n in at:
+            keep[o:o + n] = True
+        free.append(~keep)
+        x[free[-1].cuda()] = 0.0
+    ref = c.fwd()
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for x, rows in zip(c.on, free):
+            x[rows.cuda()] = bad
+        assert _same(ref, c.fwd())
+
+
+@gpu
+def test_a_nan_is_not_hidden():
+    """NaN in a key or value that a row sees comes out as NaN in that row, and only there."""
+    c = Case(24, [1, 1, 40, 1], [30, 300, 40, 600], 200, 4, 2, 64, torch.bfloat16, BR).dev()
+    (oq, _), (ok, _) = c.spans_q[1], c.spans_k[1]
+    ref, _ = c.fwd()
+    for x in (c.on[1], c.on[2]):
+        x[ok + 270, 0, 5] = float("nan")
+        out, lse = c.fwd()
+        bad = torch.isnan(out).any(-1)
+        assert bad[oq, :2].all() and not bad[oq, 2:].any() and int(bad.sum()) == 2
+        assert torch.equal(out[oq + 1:].view(torch.int16), ref[oq + 1:].view(torch.int16))
+    c.on[4][17, 1, 3] = float("nan")
+    out, _ = c.fwd()
+    rows = torch.zeros(out.shape[0], dtype=torch.bool)
+    for o, n in c.spans_q:
+        rows[o:o + n] = True
+    assert torch.isnan(out[rows][:, 2:, 3]).all() and not torch.isnan(out[~rows]).any()
+
+
+@gpu
+@pytest.mark.parametrize("batch", [1100, 2100])
+def test_many_sequences(batch):
+    """More sequences than the scheduler has threads, and than offsets fit in shared memory."""
+    lk = [(7 * i) % 40 for i in range(batch)]
+    lq = [1 if i % 5 else i % 3 for i in range(batch)]
+    Case(batch, lq, lk, 60, 2, 1, 64, torch.bfloat16, BR, slot_q=1, slot_k=4).check()
+
+
+@gpu
+def test_nothing_to_read_or_to_answer():
+    """No own keys at all, no prefix either, no queries: zeros, -infinity, and gradients of zero."""
+    for lq, lk, prefix, tail in (([1, 3], [0, 0], 50, 0), ([1, 3], [0, 0], 0, 0), ([0, 0], [4, 5], 30, 0), ([0, 0], [4, 5], 30, 3)):
+        c = Case(25, lq, lk, prefix, 4, 2, 64, torch.float16, BR, slot_q=1, slot_k=1, tail=tail)
+        if tail == 0 and sum(lk) == 0:
+            assert c.k.shape[0] == 0
+        out, lse = c.fwd()
+        grads = c.bwd(out, lse)
+        names = (FWD if c.q.shape[0] else ()) + ALL
+        prefix_check({"out": out, "lse": lse, **dict(zip(ALL, grads))}, c.plain(), names, c.dtype)
+
+
+@gpu
+def test_overlapping_sequences_are_reported():
+    """Offsets that fall back put two sequences on the same rows; with more tokens than rows
+    nothing is computed, and the status says so."""
+    c = Case(26, [40, 1, 40], [40, 8, 40], 50, 4, 2, 64, torch.bfloat16, BR, slot_q=1, slot_k=1, tail=0).dev()
+    sizes = (3, c.q.shape[0], c.k.shape[0], 50, 4, 2, 64)
+    ws = torch.empty(ta.prefix_fwd_workspace_size(*sizes), dtype=torch.uint8, device="cuda")
+    c.cu_on[0] = prefix_sums([60, 0, 60]).cuda()
+    c.cu_on[1] = prefix_sums([60, 0, 60]).cuda()
+    c.cu_on[2] = torch.tensor([0, 81, 0, 81], dtype=torch.int32).cuda()
+    c.cu_on[3] = torch.tensor([0, 88, 0, 88], dtype=torch.int32).cuda()
+    c.fwd(workspace=ws)
+    assert ta.read_status(ws) == 1
+
+
+@gpu
+def test_two_streams_at_once():
+    """Calls in flight on two streams, each with its own workspace, do not touch each other."""
+    cs = [Case(s, [1] * 30, [(s + 41 * i) % 700 for i in range(30)], 900, 8, 2, 128, torch.bfloat16, BR).dev() for s in (27, 28)]
+    refs = [[x.clone() for x in c.fwd()] for c in cs]
+    grads = [[x.clone() for x in c.bwd(*r)] for c, r in zip(cs, refs)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, (c, st) in enumerate(zip(cs, streams)):
+            with torch.cuda.stream(st):
+                out, lse = c.fwd()
+                got[i].append([out, lse, *c.bwd(out, lse)])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert _same(refs[i] + grads[i], g)
+
+
+@gpu
+def test_arguments_that_do_not_fit_are_refused():
+    """Shapes, types, strides and devices that do not go together, before any launch."""
+    c = Case(29, [3, 1], [3, 9], 20, 4, 2, 64, torch.bfloat16, BR).dev()
+    q, k, v, kp, vp = c.on
+    cu = c.cu_on
+
+    def call(tensors=c.on, lens=cu, **kw):
+        with pytest.raises(ValueError):
+            ta.prefix_fwd(*tensors, *lens, 0.1, **kw)
+    call((q.float(), k, v, kp, vp))
+    call((q, k.half(), v, kp, vp))
+    call((q, k, v[:-1], kp, vp))
+    call((q, k, v, kp[:, :1], vp[:, :1]))
+    call((q, k, v, kp, vp[:-1]))
+    call((q[..., :32], k, v, kp, vp))
+    call((q.transpose(0, 1), k, v, kp, vp))
+    call((q, k, v, kp.cpu(), vp))
+    call(lens=(cu[0].long(), *cu[1:]))
+    call(lens=(cu[0], cu[1][:-1], *cu[2:]))
+    call(lens=(cu[0].cpu(), *cu[1:]))
+    call(out=torch.empty_like(q)[:-1])
+    call(lse=torch.empty(q.shape[:2], dtype=torch.float64, device="cuda"))
+    call(prefix_len=torch.tensor([3, 4], dtype=torch.int32).cuda())
+    call(mask_type="no_mask")
+    with pytest.raises(RuntimeError):
+        ta.prefix_fwd(*c.on, *cu, 0.1, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    out, lse = c.fwd()
+    with pytest.raises(ValueError):
+        ta.prefix_bwd(*c.on, out, c.dout_on.transpose(0, 1), lse, *cu, 0.1)
+    with pytest.raises(ValueError):
+        ta.prefix_bwd(*c.on, out, c.dout_on, lse.double(), *cu, 0.1)
 
 
 @gpu

@@ -232,3 +232,45 @@ def test_captured_replay_and_side_stream():
     torch.cuda.synchronize()
     for a, b, c in zip(outs, ref, other):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16)) and torch.equal(b.view(torch.int16), c.view(torch.int16))
+
+
+@gpu
+def test_arguments_that_do_not_fit_are_refused():
+    """Shapes, types and devices that do not go together, before any launch."""
+    x = torch.zeros(8, 2, 64, dtype=torch.bfloat16, device="cuda")
+    w, _ = ta.rope_frequencies(64)
+    cu = prefix_sums([8]).cuda()
+
+    def call(q=x, k=None, w=w, cu=cu, pad=cu, **kw):
+        with pytest.raises((ValueError, RuntimeError)):
+            ta.rope(q, k, w, cu, pad, **kw)
+    call(q=x.float())
+    call(k=x.half())
+    call(k=x[:-1])
+    call(k=x[..., :32])
+    call(q=x.transpose(1, 2))
+    call(q=x[0])
+    call(w=w.float())
+    call(w=w.cpu())
+    call(w=torch.cat((w, w)))
+    call(cu=cu.long())
+    call(pad=cu[:-1])
+    call(start_positions=cu)
+    call(q_out=x[:-1])
+    call(k_out=x)
+    call(mscale=float("nan"))
+    call(q=torch.zeros(1, 4097, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        ta.rope_sbhd(x.view(4, 2, 2, 64), None, w, prefix_sums([4]).cuda())
+
+
+@gpu
+def test_nothing_to_turn():
+    """No rows, and rows without a sequence of any length."""
+    w, _ = ta.rope_frequencies(64)
+    cu = prefix_sums([0, 0]).cuda()
+    out, _ = ta.rope(torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda"), None, w, cu, cu)
+    assert out.shape == (0, 2, 64)
+    x = torch.full((5, 2, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out, k = ta.rope(x, x, w, cu, cu)
+    assert torch.equal(out, torch.zeros_like(x)) and torch.equal(k, torch.zeros_like(x))
