@@ -1153,11 +1153,13 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
   __shared__ float s_acc[kWarps > 1 ? 8 : 1][kWarps > 1 ? 256 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = warp % kWarps;  // this warp's share of a row's parts
-  const long long w = static_cast<long long>(blockIdx.x) * (8 / kWarps) + warp / kWarps;
-  const bool any = w < static_cast<long long>(p.total_q) * slices;
-  const int t = any ? static_cast<int>(w / slices) : 0, slice = any ? static_cast<int>(w % slices) : 0;
-  const int h0 = static_cast<int>(static_cast<long long>(p.hq) * slice / slices);
-  const int h1 = any ? static_cast<int>(static_cast<long long>(p.hq) * (slice + 1) / slices) : h0;
+  // (total_q * hq, and with it every count of rows here, is below 2^31)
+  const uint32_t w = blockIdx.x * (8 / kWarps) + warp / kWarps;
+  const bool any = w < static_cast<uint32_t>(p.total_q) * slices;
+  const int t = any ? w / slices : 0, slice = any ? w % slices : 0;
+  // several warps per row: one head each
+  const int h0 = kWarps > 1 ? slice : static_cast<int>(static_cast<long long>(p.hq) * slice / slices);
+  const int h1 = !any ? h0 : kWarps > 1 ? h0 + 1 : static_cast<int>(static_cast<long long>(p.hq) * (slice + 1) / slices);
   __shared__ int s_pad[kCachedOffsets];
   const int rt = prefix_row_tile(p.d);
   int i = 0;
@@ -1183,28 +1185,28 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     // the row's parts: na of row tile a (partial rows a0 + k astep), then nb of its own keys
     bool write = h < h1;
     int na = 0, nb = 0;
-    size_t a0 = 0, astep = 0, b0 = 0, bstep = 0;
+    int a0 = 0, astep = 0, b0 = 0, bstep = 0;  // (cap_rows is below 2^31)
+    const int tile_shift = rt == 256 ? 8 : 7;
     if (real && info.x < 0) {
       const int rr = i * p.group + j;
-      const int4 tile = p.longs[info.w + rr / rt];
+      const int4 tile = p.longs[info.w + (rr >> tile_shift)];
       write = write && (tile.x >= 0 || tile.y == 0);  // else the main kernel wrote it
       na = tile.y;
-      a0 = static_cast<size_t>(tile.x) + partial_offset(p, tile.z, 0, g) + rr % rt;
-      astep = partial_offset(p, tile.z, 1, 0);
+      a0 = tile.x + g * tile.z + (rr & (rt - 1));
+      astep = p.hkv * tile.z;
     } else if (real) {
       if (pre_chunks > 0) {
-        const int rr = (info.x + i) * p.group + j, u = rr / rt;
+        const int rr = (info.x + i) * p.group + j, u = rr >> tile_shift;
         const int rows = min(rt, pre_rows - u * rt);
         na = pre_chunks;
-        a0 = static_cast<size_t>(pre_slot) + static_cast<size_t>(u) * rt * pre_chunks * p.hkv +
-             partial_offset(p, rows, 0, g) + rr % rt;
-        astep = partial_offset(p, rows, 1, 0);
+        a0 = pre_slot + u * rt * pre_chunks * p.hkv + g * rows + (rr & (rt - 1));
+        astep = p.hkv * rows;
       }
       write = write && info.z >= 0;
       nb = max(info.z, 0);
       const int rows = s.len_q * p.group;
-      b0 = static_cast<size_t>(info.y) + partial_offset(p, rows, 0, g) + i * p.group + j;
-      bstep = partial_offset(p, rows, 1, 0);
+      b0 = info.y + (g * s.len_q + i) * p.group + j;
+      bstep = p.hkv * rows;
     }
     const int n = write ? na + nb : 0;
     auto at = [&](int k) { return k < na ? a0 + k * astep : b0 + (k - na) * bstep; };
@@ -1234,7 +1236,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
           const int k = todo ? __ffs(todo) - 1 : 0;
           const float ww = __shfl_sync(0xffffffffu, wgt, k);
           wk[u] = todo ? ww : 0.f;
-          const float* src = p.part_o + at(k0 + k) * p.d;
+          const float* src = p.part_o + static_cast<size_t>(at(k0 + k)) * p.d;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int col = 128 * c + 4 * lane;
