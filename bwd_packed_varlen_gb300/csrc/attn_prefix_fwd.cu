@@ -15,6 +15,8 @@
 // scores and stores overlap the other's products (a decoding step's items are a few tiles
 // long, and the chain S -> P -> O of a tile is about 2700 cycles against 1000 of tensor
 // work). An item of more rows takes both streams, row tile A and B, over the same key tiles.
+// Above head_dim 128 O takes half of TMEM and there is one stream; its scores run a tile ahead
+// of the products (batch 24, head_dim 256, prefix 20000: 42.2 -> 37.8 us).
 // S = Q K^T into TMEM, P = exp2(S scale log2e - m) over it as 16-bit values, O += P V in
 // TMEM. The offset m is raised only when a row's maximum exceeds it by more than 2^8.
 // P is rounded to 16 bits for the tensor cores (relative to the row's largest value, half a
@@ -386,7 +388,9 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
 
   __shared__ uint64_t bar_q_full[NT], bar_q_empty[NT];
   __shared__ uint64_t bar_k_full[NS], bar_k_empty[NS], bar_v_full[NS], bar_v_empty[NS];
-  __shared__ uint64_t bar_s_full[NT], bar_p_ready[NT], bar_o_full[NT], bar_o_empty[NT];
+  // S and P: of stream x, or with one stream of its two S tiles, which take turns
+  __shared__ uint64_t bar_s_full[2], bar_p_ready[2], bar_o_full[NT], bar_o_empty[NT];
+  __shared__ uint64_t bar_pv;  // one stream: a product is done
   __shared__ ItemRing rings[NT];
   __shared__ int tiles_loaded;  // by the K/V warp, for the item warp to keep pace with
   __shared__ uint32_t tmem_slot;
@@ -402,11 +406,14 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       mbar_init(&bar_v_full[i], 1);
       mbar_init(&bar_v_empty[i], 1);
     }
+    mbar_init(&bar_pv, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_s_full[i], 1);
+      mbar_init(&bar_p_ready[i], 128);
+    }
     for (int x = 0; x < NT; ++x) {
       mbar_init(&bar_q_full[x], 1);
       mbar_init(&bar_q_empty[x], 1);
-      mbar_init(&bar_s_full[x], 1);
-      mbar_init(&bar_p_ready[x], 128);
       mbar_init(&bar_o_full[x], 1);
       mbar_init(&bar_o_empty[x], 128);
       for (int i = 0; i < 2; ++i) {
@@ -742,24 +749,25 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
     auto real_keys = [&](const Stream& c, int j) {
       return j < c.n_pre ? c.p_left - j * BN : c.o_left - (j - c.n_pre) * BN;
     };
-    auto issue_pv = [&](int x, int tile, bool first) {
+    // (s: the stream, or with one stream the S tile)
+    auto issue_pv = [&](int x, int s, int tile, bool first) {
       const SmemDesc vst{dv.lo + (((tile % NS) * S::kKVBytes) >> 4), dv.hi};
-      const uint32_t t_o = tmem + S::col_o(x), t_p = tmem + S::col_s(x), acc0 = first ? 0u : 1u;
+      const uint32_t t_o = tmem + S::col_o(x), t_p = tmem + S::col_s(s), acc0 = first ? 0u : 1u;
       __syncwarp();  // elect.sync in the MMA wrappers needs a converged warp
       if (elect_one())
 #pragma unroll
       for (int k = 0; k < BN / 16; ++k) mma_ts_one(t_o, t_p + k * 8, vst, k * 2048, idPV, k > 0 ? 1u : acc0);
     };
-    auto issue_s = [&](int x, int tile) {
+    auto issue_s = [&](int x, int s, int tile) {
       const SmemDesc qx{dq.lo + ((x * S::kQBytes) >> 4), dq.hi};
       const SmemDesc kst{dk.lo + (((tile % NS) * S::kKVBytes) >> 4), dk.hi};
-      const uint32_t t_s = tmem + S::col_s(x);
+      const uint32_t t_s = tmem + S::col_s(s);
       __syncwarp();
       if (elect_one())
 #pragma unroll
       for (int k = 0; k < kD / 16; ++k)
         mma_ss_one(t_s, qx, (k >> 2) * 16384 + (k & 3) * 32, kst, (k >> 2) * (BN * 128) + (k & 3) * 32, idS, k > 0 ? 1u : 0u);
-      mma_commit(&bar_s_full[x]);
+      mma_commit(&bar_s_full[s]);
     };
     // An item on both streams: in round r both products of tile r - 1 and both scores of tile r.
     auto run_pair = [&]() -> bool {
@@ -783,13 +791,13 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
               v_ready = true;
             }
             tc_fence_after();
-            issue_pv(x, it + r - 1, r == 1);
+            issue_pv(x, x, it + r - 1, r == 1);
           }
           if (r < c.n) {
             if (!k_ready && !wait_k(it + r)) return false;
             k_ready = true;
             tc_fence_after();
-            issue_s(x, it + r);
+            issue_s(x, x, it + r);
             if (r + 1 == c.n) mma_commit(&bar_q_empty[x]);
           } else if (r == c.n && r > 0) {
             mma_commit(&bar_o_full[x]);
@@ -805,6 +813,52 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       it += rounds;
       return true;
     };
+    // One stream (head_dim above 128, O takes half of TMEM): within an item the scores run a
+    // tile ahead of the products, into the other S tile.
+    auto run_single = [&]() {
+      for (int ii = 0;; ++ii) {
+        const int sl = ii & 1;
+        if (!mbar_wait_warp(&rings[0].full[sl], (ii >> 1) & 1, status)) return;
+        const PrefixItem& I = rings[0].item[sl];
+        Stream c{};
+        c.n = I.n;
+        c.n_pre = I.np;
+        c.p_left = I.p_left;
+        c.o_left = I.o_left;
+        __syncwarp();
+        mbar_arrive(&rings[0].empty[sl]);
+        if (c.n < 0 || !mbar_wait_warp(&bar_q_full[0], ii & 1, status)) return;
+        if (c.n == 0) mma_commit(&bar_q_empty[0]);
+#pragma unroll 1
+        for (int r = 0; r <= c.n; ++r) {
+          if (r < c.n) {
+            if (!wait_k(it + r)) return;
+            tc_fence_after();
+            issue_s(0, (it + r) & 1, it + r);
+            mma_commit(&bar_k_empty[(it + r) % NS]);
+            if (r + 1 == c.n) mma_commit(&bar_q_empty[0]);
+          }
+          if (r == 0) continue;
+          const int t = it + r - 1;
+          if (!mbar_wait_warp(&bar_p_ready[t & 1], (t >> 1) & 1, status)) return;
+          if (r == 1 && s0.no > 0 && !mbar_wait_warp(&bar_o_empty[0], (s0.no - 1) & 1, status)) return;
+          if (!wait_v(t)) return;
+          const int real = real_keys(c, r - 1);
+          if (real < BN) zero_v(t, real);
+          tc_fence_after();
+          issue_pv(0, t & 1, t, r == 1);
+          mma_commit(&bar_v_empty[t % NS]);
+          mma_commit(&bar_pv);
+          if (r == c.n) {
+            mma_commit(&bar_o_full[0]);
+            ++s0.no;
+          }
+        }
+        it += c.n;
+      }
+    };
+    if constexpr (NT == 1) run_single();
+    else
     for (;;) {
       const int w = order.wants(!held0 && !ended0, !held1 && !ended1);
       if (w >= 0) {
@@ -851,7 +905,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         if (!wait_p(x, c, c.first) || !wait_v(c.pend)) break;
         if (c.real < BN) zero_v(c.pend, c.real);
         tc_fence_after();
-        issue_pv(x, c.pend, c.first);
+        issue_pv(x, x, c.pend, c.first);
         mma_commit(&bar_v_empty[c.pend % NS]);
         if (c.last) {
           mma_commit(&bar_o_full[x]);
@@ -864,7 +918,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         if (c.j == 0 && !mbar_wait_warp(&bar_q_full[x], (c.gets - 1) & 1, status)) break;
         if (!wait_k(it)) break;
         tc_fence_after();
-        issue_s(x, it);
+        issue_s(x, x, it);
         mma_commit(&bar_k_empty[it % NS]);
         c.first = c.j == 0;
         c.real = real_keys(c, c.j);
@@ -879,7 +933,6 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
     // ------------------------------------------------------------- softmax
     const int x = warp >> 2, quarter = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_s = tmem + S::col_s(x) + lane_base;
     const uint32_t t_o = tmem + S::col_o(x) + lane_base;
     using T = typename std::conditional<kBF16, __nv_bfloat16, __half>::type;
     // A scale of 0 becomes the smallest positive one, which gives the same P (2^(S 1e-38) =
@@ -908,11 +961,13 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar_s_full[x], ns & 1, status));
+        const int sb = NT == 1 ? ns & 1 : x;
+        const uint32_t t_s = tmem + S::col_s(sb) + lane_base;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar_s_full[sb], (NT == 1 ? ns >> 1 : ns) & 1, status));
         if (!ok) break;
         ++ns;
         if (!alive) {
-          mbar_arrive(&bar_p_ready[x]);
+          mbar_arrive(&bar_p_ready[sb]);
           continue;
         }
         tc_fence_after();
@@ -995,8 +1050,14 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
               neg = -mxs;
             }
           }
-          // S(j) was issued after P V(j-1): O is final for the tiles before this one. At the
-          // item's first tile there is nothing to scale: the product will overwrite it.
+          // O has to be final for the tiles before this one. With two streams S(j) was issued
+          // after P V(j-1), with one it may not be through. At the item's first tile there is
+          // nothing to scale: the product will overwrite it.
+          if (NT == 1 && again && j > 0) {
+            ok = mbar_wait_warp(&bar_pv, ns & 1, status);  // product ns - 2 of all
+            if (!ok) break;
+            tc_fence_after();
+          }
           if (again && j > 0) {
 #pragma unroll 1
             for (int c0 = 0; c0 < kD; c0 += 32) {
@@ -1010,11 +1071,12 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
             }
           }
         } while (again);
+        if (!ok) break;
 #pragma unroll
         for (int k = 0; k < BN / 32; ++k) tmem_st16(t_s + 16 * k, pk[k]);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bar_p_ready[x]);
+        mbar_arrive(&bar_p_ready[sb]);
         const float2 s01 = f2_unpack(fadd2(fadd2(sp[0], sp[1]), fadd2(sp[2], sp[3])));
         l = l * alpha + (s01.x + s01.y);
       }

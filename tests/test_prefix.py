@@ -231,6 +231,19 @@ def test_long_cache_of_one_sequence():
 
 
 @gpu
+@pytest.mark.parametrize("d", [128, 256])
+def test_scores_that_grow(d):
+    """The running maximum moves in most key tiles, of the prefix and of the own keys, so that
+    what is summed so far is scaled down again and again, while other rows' maxima stay."""
+    c = Case(31, [1, 90], [700, 800], 1500, 4, 1, d, torch.float16, BR, slot_q=1)
+    for x, n, b in ((c.kp, 1500, 0), (c.k[:700], 700, 0), (c.k[-802:-2], 800, 1)):
+        o = c.spans_q[b][0]
+        ramp = torch.linspace(0, 40.0 * n / 1500, n)[:, None, None]
+        x += (ramp * torch.sign(c.q[o:o + 1, :1].float()) / math.sqrt(d)).to(c.dtype)
+    c.check(backward=False)
+
+
+@gpu
 def test_large_scores_and_equal_scores():
     """Peaked softmaxes (scores of hundreds) and constant ones (every key alike)."""
     c = Case(13, [1, 40, 3], [30, 40, 300], 400, 4, 2, 128, torch.bfloat16, BR)
