@@ -8,8 +8,8 @@
 // cores against the prefix, and K/V tiles are read once for all of them. Roles:
 //   warps 0-3   softmax of stream 0 (one thread per row / TMEM lane),
 //   warps 4-7   softmax of stream 1 (head_dim <= 128 only),
-//   then        an item warp (decodes items ahead and starts the loads of their Q rows), a
-//               K/V warp (TMA) and an MMA warp.
+//   then        an item warp (takes items from the common list and decodes them), a K/V warp
+//               and a Q warp (TMA) and an MMA warp.
 // An item of at most 128 rows runs on one stream; the streams work on different items and
 // their key tiles alternate in the shared K/V ring, so one item's exponentials, first
 // scores and stores overlap the other's products (a decoding step's items are a few tiles
@@ -312,7 +312,7 @@ struct PrefixShape {
   static constexpr int kStages = kD == 64 ? 4 : 2;
   static constexpr int kStageBytes = kNT * 4 * 2048;       // per softmax warp, for its stores
   static constexpr int kSmemBytes = kNT * kQBytes + 2 * kStages * kKVBytes + kStageBytes + 1024;
-  static constexpr int kThreads = kNT * 128 + 96;
+  static constexpr int kThreads = kNT * 128 + 128;
   // TMEM columns of O and S of stream x: O_0 O_1 S_0 S_1
   __device__ static constexpr uint32_t col_o(int x) { return static_cast<uint32_t>(x) * 128u; }
   __device__ static constexpr uint32_t col_s(int x) { return 256u + static_cast<uint32_t>(x) * 128u; }
@@ -342,7 +342,8 @@ struct PrefixItem {
 };
 struct ItemRing {
   PrefixItem item[2];
-  // kv: all but the rows is there (the K/V warp starts on that); full: the rows too
+  // kv: all but the rows is there (the K/V warp starts on that); full: the rows too; empty: the
+  // K/V, Q and MMA warps and the stream are through with it
   uint64_t kv[2], full[2], empty[2];
 };
 
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
     attn_prefix_fwd_kernel(const __grid_constant__ PrefixParams p, const __grid_constant__ PrefixMaps tm) {
   using S = PrefixShape<kD>;
   constexpr int NT = S::kNT, NS = S::kStages, BN = S::kBN;
-  constexpr int kWarpItem = NT * 4, kWarpKv = NT * 4 + 1, kWarpMma = NT * 4 + 2;
+  constexpr int kWarpItem = NT * 4, kWarpKv = NT * 4 + 1, kWarpMma = NT * 4 + 2, kWarpQ = NT * 4 + 3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       for (int i = 0; i < 2; ++i) {
         mbar_init(&rings[x].kv[i], 1);
         mbar_init(&rings[x].full[i], 1);
-        mbar_init(&rings[x].empty[i], 1 + 32 + 128);  // K/V warp's lane 0, MMA warp, softmax
+        mbar_init(&rings[x].empty[i], 1 + 32 + 32 + 128);  // K/V warp's lane 0, MMA and Q warps, softmax
       }
     }
     fence_barrier_init();
@@ -440,14 +441,14 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
   pdl_wait();  // the scheduler's lists
 
   if (warp == kWarpItem) {
-    // ------------------------------------------------------------- items and Q rows
+    // ------------------------------------------------------------- items
     // the first entry is read along with the number of entries (the grid is no larger than
     // the entries' capacity)
     const PrefixEntry first = load_entry(p, blockIdx.x / p.hkv);
     const int n_items = p.header[kHdrPrefixEntries] * p.hkv;
     const int np_keys = prefix_keys(p);
     int nxt = blockIdx.x;
-    int puts0 = 0, puts1 = 0;  // hand-overs so far, per stream: each also uses its Q tile once
+    int puts0 = 0, puts1 = 0;  // hand-overs so far, per stream
     auto puts = [&](int x) { return x ? puts1 : puts0; };
     TileOrder order;
     bool ok = true;
@@ -455,11 +456,11 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       const int n = puts(x);
       return n < 2 || __all_sync(0xffffffffu, mbar_wait(&rings[x].empty[n & 1], ((n >> 1) - 1) & 1, status));
     };
-    // With few items per block an item is taken from the common list only when the tiles
-    // before it are loaded but for four: enough to hide its decoding, and no more, since a
-    // block that takes items early may sit on them while others have run out (decoding steps:
-    // 10 % slower). With many the hand-over slots alone bound it: there taking late cost 4 %.
-    const int ahead = n_items > 4 * static_cast<int>(gridDim.x) ? INT32_MAX : 4;
+    // An item is taken from the common list only when the tiles before it are loaded but for
+    // four: enough to hide its decoding, and no more, since a block that takes items early may
+    // sit on them while others have run out (8: usual decoding step 47.5 -> 48.7 us; as many
+    // as the slots hold: prompts 695 -> 760 us).
+    constexpr int ahead = 4;
     int emitted = 0;  // tiles in the order so far
     auto keep_pace = [&]() -> bool {
       const volatile int* loaded = &tiles_loaded;
@@ -515,8 +516,6 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         emitted += n0;
       }
       const int parts = pair ? 2 : 1;  // row tile k of the item goes to stream x0 + k
-      // Both streams' hand-overs of an item come before any wait for a Q tile: the MMA warp
-      // may need the second one to go on with the item that still uses that tile.
 #pragma unroll 1
       for (int k = 0; k < parts; ++k) {
         const int x = x0 + k, r0 = k * 128, rows = min(128, e.rows - r0);
@@ -524,6 +523,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         int tok[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
+          if (u * 32 >= rows) break;
           const int r = u * 32 + lane, i = (e.row0 + r0 + r) / p.group;
           tok[u] = r >= rows ? -1 : e.seq < 0 ? p.short_tok[i] : e.off_q + i;
         }
@@ -557,38 +557,6 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&rings[x].full[sl]);
-      }
-      if (!ok) break;
-      // Q rows by TMA: one box of 128 rows where tokens lie side by side and a tile holds
-      // whole ones, else token by token (all heads of the group in one box, one lane each),
-      // and row by row where a token's heads do not all lie in this tile. A box may start at
-      // any 128-byte row of the tile: the swizzle goes by shared-memory address.
-#pragma unroll 1
-      for (int k = 0; k < parts; ++k) {
-        const int x = x0 + k, n = puts(x);
-        if (n > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bar_q_empty[x], (n - 1) & 1, status)))) break;
-        uint8_t* q_tile = sQ + x * S::kQBytes;
-        const PrefixItem& I = rings[x].item[n & 1];
-        const int rows = min(128, e.rows - k * 128), h0 = h * p.group;
-        const int row_a = I.row[0], row_z = I.row[rows - 1];
-        const int tok_a = row_a / p.hq, tok_z = row_z / p.hq;
-        const bool whole = tm.q_tokens > 0 && min(row_a, row_z) >= 0 && row_a - tok_a * p.hq == h0 &&
-                           (tok_z - tok_a) * p.group + row_z - tok_z * p.hq - h0 == rows - 1;
-        if (lane == 0) mbar_arrive_expect_tx(&bar_q_full[x], (whole ? 128 : rows) * 128 * S::kChunks);
-        __syncwarp();
-#pragma unroll 1
-        for (int r = lane; r < rows; r += 32) {
-          // (a row without a place, after an error: zeros, from behind the last token)
-          const int row = I.row[r], t = row < 0 ? p.total_q : row / p.hq, head = row < 0 ? h0 : row - t * p.hq;
-          const int j = head - h0;  // the token's rows in the tile: from r - j on
-          const bool box = row >= 0 && p.group <= 128 && r >= j && r - j + p.group <= rows;
-          if (whole ? r > 0 : box && j > 0) continue;
-          const CUtensorMap* map = whole ? &tm.q_tile : box ? &tm.q_token : &tm.q_row;
-#pragma unroll 1
-          for (int c = 0; c < S::kChunks; ++c)
-            tma_load_4d(q_tile + c * 16384 + r * 128, map, &bar_q_full[x], c * 64, head, 0, t);
-        }
-        __syncwarp();
         if (x) ++puts1;
         else ++puts0;
       }
@@ -603,6 +571,75 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         mbar_arrive(&rings[x].kv[puts(x) & 1]);
         mbar_arrive(&rings[x].full[puts(x) & 1]);
       }
+    }
+  } else if (warp == kWarpQ) {
+    // ------------------------------------------------------------- Q rows
+    // In the order in which the streams take items, so that it never waits for a tile whose
+    // last scores wait for rows behind it. Beside the item warp, not in it: one warp needed
+    // 5500 cycles for both, and short items came no faster (192 caches of 515 keys: 104 -> 98
+    // us; 256 long ones 412 -> 406).
+    TileOrder order;
+    bool held0 = false, held1 = false, ended0 = false, ended1 = NT == 1;
+    int gets0 = 0, gets1 = 0, loads0 = 0, loads1 = 0;
+    for (;;) {
+      const int x = order.wants(!held0 && !ended0, !held1 && !ended1);
+      if (x < 0) {
+        if (held0 && held1) {
+          held0 = held1 = false;
+          order = TileOrder();
+        } else if (order.left0 > 0 || order.left1 > 0) {
+          order.take(order.next());
+        } else {
+          break;
+        }
+        continue;
+      }
+      const int gets = x ? gets1 : gets0, loads = x ? loads1 : loads0, sl = gets & 1;
+      if (!mbar_wait_warp(&rings[x].full[sl], (gets >> 1) & 1, status)) break;
+      if (x) ++gets1;
+      else ++gets0;
+      const PrefixItem& I = rings[x].item[sl];
+      const int n = I.n;
+      if (n < 0) {
+        if (x) ended1 = true;
+        else ended0 = true;
+        continue;
+      }
+      if (I.pair != 0) {
+        if (x) held1 = true;
+        else held0 = true;
+      } else {
+        order.set(x, n);
+      }
+      // by TMA: one box of 128 rows where tokens lie side by side and a tile holds whole ones,
+      // else token by token (all heads of the group in one box, one lane each), and row by row
+      // where a token's heads do not all lie in this tile. A box may start at any 128-byte
+      // row of the tile: the swizzle goes by shared-memory address.
+      const int rows = I.rows, h0 = I.head * p.group;
+      const int row_a = I.row[0], row_z = I.row[rows - 1];
+      const int tok_a = row_a / p.hq, tok_z = row_z / p.hq;
+      const bool whole = tm.q_tokens > 0 && min(row_a, row_z) >= 0 && row_a - tok_a * p.hq == h0 &&
+                         (tok_z - tok_a) * p.group + row_z - tok_z * p.hq - h0 == rows - 1;
+      if (loads > 0 && !mbar_wait_warp(&bar_q_empty[x], (loads - 1) & 1, status)) break;
+      uint8_t* q_tile = sQ + x * S::kQBytes;
+      if (lane == 0) mbar_arrive_expect_tx(&bar_q_full[x], (whole ? 128 : rows) * 128 * S::kChunks);
+      __syncwarp();
+#pragma unroll 1
+      for (int r = lane; r < rows; r += 32) {
+        // (a row without a place, after an error: zeros, from behind the last token)
+        const int row = I.row[r], t = row < 0 ? p.total_q : row / p.hq, head = row < 0 ? h0 : row - t * p.hq;
+        const int j = head - h0;  // the token's rows in the tile: from r - j on
+        const bool box = row >= 0 && p.group <= 128 && r >= j && r - j + p.group <= rows;
+        if (whole ? r > 0 : box && j > 0) continue;
+        const CUtensorMap* map = whole ? &tm.q_tile : box ? &tm.q_token : &tm.q_row;
+#pragma unroll 1
+        for (int c = 0; c < S::kChunks; ++c)
+          tma_load_4d(q_tile + c * 16384 + r * 128, map, &bar_q_full[x], c * 64, head, 0, t);
+      }
+      __syncwarp();
+      mbar_arrive(&rings[x].empty[sl]);
+      if (x) ++loads1;
+      else ++loads0;
     }
   } else if (warp == kWarpKv) {
     // ------------------------------------------------------------- K and V tiles
