@@ -773,10 +773,11 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       ++c.np;
       return !first || c.no == 0 || mbar_wait_warp(&bar_o_empty[x], (c.no - 1) & 1, status);
     };
-    // V rows that are no real key become zeros (P is 0 there, but 0 times NaN is not)
+    // The product takes a tile's keys by 16, as far as it has real ones; V rows behind the last
+    // one become zeros there (P is 0, but 0 times NaN is not).
     auto zero_v = [&](int tile, int real) {
 #pragma unroll 1
-      for (int z = real * 8 + lane; z < BN * 8; z += 32)
+      for (int z = real * 8 + lane; z < (real + 15) / 16 * 128; z += 32)
 #pragma unroll 1
         for (int k = 0; k < S::kChunks; ++k)
           st_shared_v4(sV + (tile % NS) * S::kKVBytes + k * BN * 128 + z * 16, 0, 0, 0, 0);
@@ -787,13 +788,14 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
       return j < c.n_pre ? c.p_left - j * BN : c.o_left - (j - c.n_pre) * BN;
     };
     // (s: the stream, or with one stream the S tile)
-    auto issue_pv = [&](int x, int s, int tile, bool first) {
+    auto issue_pv = [&](int x, int s, int tile, bool first, int real) {
       const SmemDesc vst{dv.lo + (((tile % NS) * S::kKVBytes) >> 4), dv.hi};
       const uint32_t t_o = tmem + S::col_o(x), t_p = tmem + S::col_s(s), acc0 = first ? 0u : 1u;
       __syncwarp();  // elect.sync in the MMA wrappers needs a converged warp
       if (elect_one())
 #pragma unroll
-      for (int k = 0; k < BN / 16; ++k) mma_ts_one(t_o, t_p + k * 8, vst, k * 2048, idPV, k > 0 ? 1u : acc0);
+      for (int k = 0; k < BN / 16; ++k)
+        if (16 * k < real) mma_ts_one(t_o, t_p + k * 8, vst, k * 2048, idPV, k > 0 ? 1u : acc0);
     };
     auto issue_s = [&](int x, int s, int tile) {
       const SmemDesc qx{dq.lo + ((x * S::kQBytes) >> 4), dq.hi};
@@ -821,14 +823,14 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           constexpr int x = decltype(x_tag)::value;
           if (r > 0 && r <= c.n) {
             if (!wait_p(x, c, r == 1)) return false;
+            const int real = real_keys(c, r - 1);
             if (!v_ready) {
               if (!wait_v(it + r - 1)) return false;
-              const int real = real_keys(c, r - 1);
               if (real < BN) zero_v(it + r - 1, real);
               v_ready = true;
             }
             tc_fence_after();
-            issue_pv(x, x, it + r - 1, r == 1);
+            issue_pv(x, x, it + r - 1, r == 1, real);
           }
           if (r < c.n) {
             if (!k_ready && !wait_k(it + r)) return false;
@@ -883,7 +885,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
           const int real = real_keys(c, r - 1);
           if (real < BN) zero_v(t, real);
           tc_fence_after();
-          issue_pv(0, t & 1, t, r == 1);
+          issue_pv(0, t & 1, t, r == 1, real);
           mma_commit(&bar_v_empty[t % NS]);
           mma_commit(&bar_pv);
           if (r == c.n) {
@@ -942,7 +944,7 @@ __global__ void __launch_bounds__(PrefixShape<kD>::kThreads, 1)
         if (!wait_p(x, c, c.first) || !wait_v(c.pend)) break;
         if (c.real < BN) zero_v(c.pend, c.real);
         tc_fence_after();
-        issue_pv(x, x, c.pend, c.first);
+        issue_pv(x, x, c.pend, c.first, c.real);
         mma_commit(&bar_v_empty[c.pend % NS]);
         if (c.last) {
           mma_commit(&bar_o_full[x]);
