@@ -1,4 +1,5 @@
-"""ctypes binding of libteattn.so: argument marshalling only.
+"""Binding of libteattn.so: argument marshalling only, by ctypes or, for the calls of a
+decoding step, by a small extension module (``csrc/host_calls.cpp``).
 
 Names mirror the C ABI (``te_attn_fwd_thd`` -> :func:`fwd`, ``te_attn_bwd_thd`` ->
 :func:`bwd`). Tensors are passed by ``data_ptr()``; the current torch CUDA stream
@@ -10,7 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
+import importlib.util
 import os
 
 import torch
@@ -345,101 +346,35 @@ def bwd_sbhd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, attn_scale,
     return dq, dk, dv
 
 
-# The rotary and shared-prefix entry points serve single decoding steps, where the kernels
-# take less time than the checks used to: these helpers, and the straight lines of conditions
-# below, keep a call's host side short.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_I32, _F32, _F64 = torch.int32, torch.float32, torch.float64
+# The rotary and shared-prefix entry points serve single decoding steps, whose kernels take less
+# time than checks, allocations and ctypes would: they go through a small extension module.
+_HOST_PATH = os.path.join(_HERE, "lib", "_teattn_host.so")
+_host = None
+_entries = {}  # addresses of the entry points, per build
 
 
-def _lib():
-    return _libs.get(_use_debug) or library()
+def _entry_points():
+    """(rope_thd, rope_sbhd, prefix_fwd, its size, prefix_bwd, its size) of the selected build."""
+    global _host
+    L = library()
+    if _host is None:
+        if not os.path.exists(_HOST_PATH):
+            raise RuntimeError(f"{_HOST_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; "
+                               "g.build()'` (or python bwd_packed_varlen_gb300/build.py)")
+        spec = importlib.util.spec_from_file_location("_teattn_host", _HOST_PATH)
+        _host = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_host)
+    names = ("rope_thd", "rope_sbhd", "prefix_fwd_thd", "prefix_fwd_workspace_size", "prefix_bwd_thd",
+             "prefix_bwd_workspace_size")
+    _entries[_use_debug] = tuple(ctypes.cast(getattr(L, "te_attn_" + n), ctypes.c_void_p).value for n in names)
+    return _entries[_use_debug]
 
 
-def _one_device(index):
-    if index < 0:
-        return "all tensors must be CUDA tensors (there is no CPU path)"
-    return "all tensors must be CUDA tensors on one device (there is no CPU path)"
-
-
-def _call(fn, index, stream, args):
-    """fn(*args, stream) with device ``index`` current, on its current stream by default."""
-    if stream is None:
-        stream = _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, stream)
-    if rc != 0:
-        _check(rc)
-
-
-def _cu_vector(t, n, index):
-    """t's address, as an int32 vector of n values on the device."""
-    if t.dtype != _I32 or t.dim() != 1 or t.numel() != n or t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"cu_seqlens and start_positions must be contiguous int32 vectors on q's device, of "
-                         f"batch + 1 and batch values (here {n})")
-    return t.data_ptr()
-
-
-def _rope_output(x, y, index):
-    """Output of a rotation: a new contiguous tensor, or the caller's after a check."""
-    if y is None:
-        return torch.empty_like(x, memory_format=torch.contiguous_format)
-    if y.shape != x.shape or y.dtype != x.dtype or y.get_device() != index or not y.is_contiguous():
-        raise ValueError("outputs must be contiguous, with the shape, dtype and device of their input")
-    return y
-
-
-def _rope(q, k, inv_freq, cu, cu_pad, start, interleaved, mscale, inverse, q_out, k_out, stream):
-    """Both layouts: ``cu_pad`` None is the sequence-major one."""
-    index = q.get_device()
-    if index < 0 or inv_freq.get_device() != index or (k is not None and k.get_device() != index):
-        raise ValueError(_one_device(index))
-    dtype, q_shape, qs = q.dtype, q.shape, q.stride()
-    code = _DTYPES.get(dtype)
-    if code is None or (k is not None and k.dtype != dtype):
-        raise ValueError("q and k must share one dtype, float16 or bfloat16")
-    dims = 4 if cu_pad is None else 3
-    if len(q_shape) != dims or (qs[-1] != 1 and q.numel()):
-        raise ValueError(f"q and k must have {dims} dimensions and adjacent elements in a head")
-    if inv_freq.dtype != _F64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous float64 vector")
-    n = cu.numel()
-    if n < 2:
-        raise ValueError("cu_seqlens must hold batch + 1 values")
-    at_cu = _cu_vector(cu, n, index)
-    at_start = None if start is None else _cu_vector(start, n - 1, index)
-    y = _rope_output(q, q_out, index)
-    if k is None:
-        if k_out is not None:
-            raise ValueError("k_out without k")
-        z, hkv, ks, at_k, at_z = None, 0, qs, None, None
-    else:
-        k_shape, ks = k.shape, k.stride()
-        if len(k_shape) != dims or (ks[-1] != 1 and k.numel()):
-            raise ValueError(f"q and k must have {dims} dimensions and adjacent elements in a head")
-        if k_shape[0] != q_shape[0] or k_shape[-1] != q_shape[-1] or (dims == 4 and k_shape[1] != q_shape[1]):
-            raise ValueError("q and k must share tokens and head dim")
-        z = _rope_output(k, k_out, index)
-        hkv, at_k, at_z = k_shape[-2], k.data_ptr(), z.data_ptr()
-    tail = (qs[-3], qs[-2], ks[-3], ks[-2], 1 if interleaved else 0, float(mscale), 1 if inverse else 0, code)
-    if cu_pad is None:
-        S, B, hq, d = q_shape
-        if B != n - 1:
-            raise ValueError("cu_seqlens must hold batch + 1 values")
-        if S > 1 and (qs[0] != B * qs[1] or ks[0] != B * ks[1]):
-            raise ValueError("rows i * batch + b must be evenly spaced")
-        _call(_lib().te_attn_rope_sbhd, index, stream,
-              (q.data_ptr(), at_k, y.data_ptr(), at_z, inv_freq.data_ptr(), inv_freq.numel(), at_cu, at_start, B, S,
-               hq, hkv, d) + tail)
-    else:
-        T, hq, d = q_shape
-        _call(_lib().te_attn_rope_thd, index, stream,
-              (q.data_ptr(), at_k, y.data_ptr(), at_z, inv_freq.data_ptr(), inv_freq.numel(), at_cu,
-               _cu_vector(cu_pad, n, index), at_start, n - 1, T, hq, hkv, d) + tail)
-    return y, z
+def _result(r):
+    """What a call of the extension returned: its outputs, or the library's code."""
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def rope(q, k, inv_freq, cu_seqlens, cu_seqlens_padded, start_positions=None, interleaved=False,
@@ -448,79 +383,28 @@ def rope(q, k, inv_freq, cu_seqlens, cu_seqlens_padded, start_positions=None, in
     (or ``k=None``); returns ``(q_out, k_out)``, contiguous. Inputs may be strided slices of a
     fused projection. ``inv_freq`` float64 ``[rot / 2]`` (see :func:`rope_frequencies`);
     ``inverse=True`` is the backward pass."""
-    return _rope(q, k, inv_freq, cu_seqlens, cu_seqlens_padded, start_positions, interleaved, mscale, inverse,
-                 q_out, k_out, stream)
+    if cu_seqlens_padded is None:
+        raise ValueError("packed tokens need cu_seqlens_padded")
+    e = _entries.get(_use_debug) or _entry_points()
+    return _result(_host.rope(e[0], q, k, inv_freq, cu_seqlens, cu_seqlens_padded, start_positions, interleaved,
+                              mscale, inverse, q_out, k_out, stream))
 
 
 def rope_sbhd(q, k, inv_freq, cu_seqlens, start_positions=None, interleaved=False, mscale=1.0,
               inverse=False, q_out=None, k_out=None, stream=None):
     """``te_attn_rope_sbhd``: the same on ``q [S, B, hq, d]`` and ``k [S, B, hkv, d]``, real
     lengths from ``cu_seqlens``."""
-    return _rope(q, k, inv_freq, cu_seqlens, None, start_positions, interleaved, mscale, inverse, q_out, k_out,
-                 stream)
+    e = _entries.get(_use_debug) or _entry_points()
+    return _result(_host.rope(e[1], q, k, inv_freq, cu_seqlens, None, start_positions, interleaved, mscale, inverse,
+                              q_out, k_out, stream))
 
 
-@functools.lru_cache(maxsize=512)
 def prefix_fwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d) -> int:
     return int(library().te_attn_prefix_fwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d))
 
 
-@functools.lru_cache(maxsize=512)
 def prefix_bwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d) -> int:
     return int(library().te_attn_prefix_bwd_workspace_size(batch, total_q, total_kv, prefix_rows, hq, hkv, d))
-
-
-def _prefix_args(q, k, v, kp, vp, cu_q, cu_kv, cu_q_pad, cu_kv_pad, prefix_len):
-    """Checks what forward and backward share: (device index, dtype code, sizes, the lengths'
-    addresses)."""
-    index, dtype = q.get_device(), q.dtype
-    if (index < 0 or k.get_device() != index or v.get_device() != index or kp.get_device() != index
-            or vp.get_device() != index):
-        raise ValueError(_one_device(index))
-    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and kp.is_contiguous()
-            and vp.is_contiguous()):
-        raise ValueError("all tensors must be contiguous")
-    code = _DTYPES.get(dtype)
-    if code is None or k.dtype != dtype or v.dtype != dtype or kp.dtype != dtype or vp.dtype != dtype:
-        raise ValueError("q, k, v, k_prefix, v_prefix must share one dtype, float16 or bfloat16")
-    q_shape, k_shape, p_shape = q.shape, k.shape, kp.shape
-    if len(q_shape) != 3 or len(k_shape) != 3 or len(p_shape) != 3:
-        raise ValueError("q, k, v, k_prefix, v_prefix must be [rows, heads, d]")
-    tq, hq, d = q_shape
-    tk, hkv, dk = k_shape
-    rows, hp, dp = p_shape
-    if v.shape != k_shape or vp.shape != p_shape or hp != hkv or dk != d or dp != d:
-        raise ValueError("k, v and k_prefix, v_prefix must share heads and head dim, and d with q")
-    n = cu_q.numel()
-    lens = (_cu_vector(cu_q, n, index), _cu_vector(cu_kv, n, index), _cu_vector(cu_q_pad, n, index),
-            _cu_vector(cu_kv_pad, n, index), None if prefix_len is None else _cu_vector(prefix_len, 1, index))
-    return index, code, (n - 1, tq, tk, rows, hq, hkv, d), lens
-
-
-def _like(x, y, name):
-    """A new tensor like x, or the caller's after a check."""
-    if y is None:
-        return torch.empty_like(x)
-    if y.shape != x.shape or y.dtype != x.dtype or y.get_device() != x.get_device() or not y.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, with the shape, dtype and device of its counterpart")
-    return y
-
-
-def _prefix_lse(q, lse):
-    """A new lse [T_q, hq], or the caller's after a check."""
-    if lse is None:
-        return torch.empty(q.shape[:2], dtype=_F32, device=q.device)
-    if lse.dtype != _F32 or lse.shape != q.shape[:2] or lse.get_device() != q.get_device() or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous float32 [T_q, hq] on q's device")
-    return lse
-
-
-def _prefix_workspace(q, ws, size):
-    if ws is None:
-        return torch.empty(size if size > 0 else 1, dtype=torch.uint8, device=q.device)
-    if ws.get_device() != q.get_device() or not ws.is_contiguous():
-        raise ValueError("workspace must be contiguous, on q's device")
-    return ws
 
 
 def prefix_fwd(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
@@ -529,15 +413,10 @@ def prefix_fwd(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seql
     """``te_attn_prefix_fwd_thd``: attention over a prefix ``k_prefix, v_prefix [P, hkv, d]``
     that every sequence shares, then each sequence's own keys; returns ``(out [T_q, hq, d],
     lse [T_q, hq])``."""
-    index, code, sizes, lens = _prefix_args(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv,
-                                            cu_seqlens_q_padded, cu_seqlens_kv_padded, prefix_len)
-    out = _like(q, out, "out")
-    lse = _prefix_lse(q, lse)
-    ws = _prefix_workspace(q, workspace, prefix_fwd_workspace_size(*sizes))
-    _call(_lib().te_attn_prefix_fwd_thd, index, stream,
-          (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), out.data_ptr(),
-           lse.data_ptr(), *lens, *sizes, float(attn_scale), _mask(mask_type), code, ws.data_ptr(), ws.numel()))
-    return out, lse
+    e = _entries.get(_use_debug) or _entry_points()
+    return _result(_host.prefix_fwd(
+        e[2], e[3], q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
+        cu_seqlens_kv_padded, prefix_len, attn_scale, _mask(mask_type), out, lse, workspace, stream))
 
 
 def prefix_bwd(q, k, v, k_prefix, v_prefix, out, dout, lse, cu_seqlens_q, cu_seqlens_kv,
@@ -545,21 +424,11 @@ def prefix_bwd(q, k, v, k_prefix, v_prefix, out, dout, lse, cu_seqlens_q, cu_seq
                mask_type="padding_causal_bottom_right", prefix_len=None, dq=None, dk=None, dv=None,
                dk_prefix=None, dv_prefix=None, workspace=None, stream=None):
     """``te_attn_prefix_bwd_thd``: returns ``(dq, dk, dv, dk_prefix, dv_prefix)``."""
-    index, code, sizes, lens = _prefix_args(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv,
-                                            cu_seqlens_q_padded, cu_seqlens_kv_padded, prefix_len)
-    if out is None or dout is None or lse is None:
-        raise ValueError("the backward needs out, dout and lse")
-    _like(q, out, "out")
-    _like(q, dout, "dout")
-    _prefix_lse(q, lse)
-    dq, dk, dv = _like(q, dq, "dq"), _like(k, dk, "dk"), _like(v, dv, "dv")
-    dkp, dvp = _like(k_prefix, dk_prefix, "dk_prefix"), _like(v_prefix, dv_prefix, "dv_prefix")
-    ws = _prefix_workspace(q, workspace, prefix_bwd_workspace_size(*sizes))
-    _call(_lib().te_attn_prefix_bwd_thd, index, stream,
-          (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), out.data_ptr(),
-           dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dkp.data_ptr(),
-           dvp.data_ptr(), *lens, *sizes, float(attn_scale), _mask(mask_type), code, ws.data_ptr(), ws.numel()))
-    return dq, dk, dv, dkp, dvp
+    e = _entries.get(_use_debug) or _entry_points()
+    return _result(_host.prefix_bwd(
+        e[4], e[5], q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
+        cu_seqlens_kv_padded, prefix_len, attn_scale, _mask(mask_type), out, dout, lse, dq, dk, dv, dk_prefix,
+        dv_prefix, workspace, stream))
 
 
 def read_status(workspace, stream=None) -> int:

@@ -378,6 +378,30 @@ def test_two_streams_at_once():
 
 
 @gpu
+def test_given_outputs_and_streams():
+    """Outputs that the caller gives come back as the same objects; a stream given by its handle
+    is used for the launches and for what is allocated; keyword and positional forms agree."""
+    c = Case(30, [1, 5, 1], [40, 5, 300], 200, 4, 2, 64, torch.bfloat16, BR).dev()
+    out, lse = c.fwd()
+    grads = c.bwd(out, lse)
+    o, l = torch.full_like(out, float("nan")), torch.full_like(lse, float("nan"))
+    got = ta.prefix_fwd(*c.on, *c.cu_on, c.scale, BR, None, o, l)
+    assert got[0] is o and got[1] is l and _same((out, lse), got)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        a = c.fwd(stream=side.cuda_stream)
+        b = c.bwd(*a, stream=side.cuda_stream)
+        torch.empty(1 << 20, device="cuda").fill_(float("nan"))  # of the current stream's memory
+        side.synchronize()
+        assert _same((out, lse, *grads), (*a, *b))
+    d = [torch.empty_like(x) for x in grads]
+    got = ta.prefix_bwd(*c.on, out, c.dout_on, lse, *c.cu_on, c.scale, BR, None, *d)
+    assert all(x is y for x, y in zip(got, d)) and _same(grads, got)
+    assert not any(x.requires_grad for x in ta.prefix_fwd(c.on[0].clone().requires_grad_(), *c.on[1:], *c.cu_on, c.scale, BR))
+
+
+@gpu
 def test_arguments_that_do_not_fit_are_refused():
     """Shapes, types, strides and devices that do not go together, before any launch."""
     c = Case(29, [3, 1], [3, 9], 20, 4, 2, 64, torch.bfloat16, BR).dev()

@@ -274,3 +274,24 @@ def test_nothing_to_turn():
     x = torch.full((5, 2, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
     out, k = ta.rope(x, x, w, cu, cu)
     assert torch.equal(out, torch.zeros_like(x)) and torch.equal(k, torch.zeros_like(x))
+
+
+@gpu
+def test_given_outputs_and_streams():
+    """Outputs that the caller gives come back as the same objects, also on another stream."""
+    gen = torch.Generator().manual_seed(12)
+    q, k = (torch.randn(20, h, 64, generator=gen).to(torch.float16).cuda() for h in (4, 2))
+    w, _ = ta.rope_frequencies(64)
+    cu = prefix_sums([20]).cuda()
+    ref = ta.rope(q, k, w, cu, cu)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    got = ta.rope(q, k, w, cu, cu, None, False, 1.0, False, qo, ko)
+    assert got[0] is qo and got[1] is ko
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    other = ta.rope(q, k, w, cu, cu, stream=side.cuda_stream)
+    side.synchronize()
+    for a, b, c in zip(ref, got, other):
+        assert torch.equal(a, b) and torch.equal(a, c)
+    with pytest.raises(ValueError):
+        ta.rope(q, None, w, cu, None)
