@@ -1311,8 +1311,25 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     }
     const int n = write ? na + nb : 0;
     auto at = [&](int k) { return k < na ? a0 + k * astep : b0 + (k - na) * bstep; };
-    float M = -INFINITY;
-    for (int k = lane; k < n; k += 32) {
+    // this warp's parts k, k + kWarps, ..., four at a time; the first four are on their way
+    // before their weights are known (what a part without a visible key left is not used)
+    float4 v[4][2];
+    auto load = [&](int k) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool some = k + u * kWarps < n;
+        const float* src = p.part_o + static_cast<size_t>(some ? at(k + u * kWarps) : 0) * p.d;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = 128 * c + 4 * lane;
+          v[u][c] = some && col < p.d ? *reinterpret_cast<const float4*>(src + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+    };
+    load(sub);
+    const float2 ml0 = lane < n ? p.part_ml[at(lane)] : make_float2(-INFINITY, 0.f);
+    float M = ml0.y != 0.f ? ml0.x : -INFINITY;
+    for (int k = lane + 32; k < n; k += 32) {
       const float2 ml = p.part_ml[at(k)];
       if (ml.y != 0.f) M = fmaxf(M, ml.x);
     }
@@ -1321,38 +1338,21 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     float L = 0.f;
     float acc[8] = {};
     for (int k0 = 0; k0 < n; k0 += 32) {
-      float wgt = 0.f;
-      if (k0 + lane < n) {
-        const float2 ml = p.part_ml[at(k0 + lane)];
-        // a part without a visible key left no output
-        wgt = ml.y != 0.f ? ex2p(ml.x - M) : 0.f;
-        L += wgt * ml.y;
-      }
-      uint32_t todo = __ballot_sync(0xffffffffu, wgt != 0.f && (k0 + lane) % kWarps == sub);
-      while (todo) {
-        float wk[4];
-        float4 v[4][2];
+      const float2 ml = k0 == 0 ? ml0 : k0 + lane < n ? p.part_ml[at(k0 + lane)] : make_float2(-INFINITY, 0.f);
+      const float wgt = ml.y != 0.f ? ex2p(ml.x - M) : 0.f;
+      L += wgt * ml.y;
+      for (int k = sub; k < min(32, n - k0); k += 4 * kWarps) {
+        if (k0 + k > sub) load(k0 + k);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int k = todo ? __ffs(todo) - 1 : 0;
-          const float ww = __shfl_sync(0xffffffffu, wgt, k);
-          wk[u] = todo ? ww : 0.f;
-          const float* src = p.part_o + static_cast<size_t>(at(k0 + k)) * p.d;
+          const float wk = __shfl_sync(0xffffffffu, wgt, (k + u * kWarps) & 31);
+          if (wk == 0.f || k + u * kWarps >= 32) continue;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int col = 128 * c + 4 * lane;
-            v[u][c] = todo && col < p.d ? *reinterpret_cast<const float4*>(src + col) : make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-          todo &= todo - 1;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            acc[4 * c] = fmaf(wk[u], v[u][c].x, acc[4 * c]);
-            acc[4 * c + 1] = fmaf(wk[u], v[u][c].y, acc[4 * c + 1]);
-            acc[4 * c + 2] = fmaf(wk[u], v[u][c].z, acc[4 * c + 2]);
-            acc[4 * c + 3] = fmaf(wk[u], v[u][c].w, acc[4 * c + 3]);
+            acc[4 * c] = fmaf(wk, v[u][c].x, acc[4 * c]);
+            acc[4 * c + 1] = fmaf(wk, v[u][c].y, acc[4 * c + 1]);
+            acc[4 * c + 2] = fmaf(wk, v[u][c].z, acc[4 * c + 2]);
+            acc[4 * c + 3] = fmaf(wk, v[u][c].w, acc[4 * c + 3]);
           }
         }
       }
