@@ -74,6 +74,7 @@ __device__ __forceinline__ Scan3 block_scan3(int x, int y, int z, int (*buf)[32]
 constexpr int kCachedOffsets = 2048;
 __device__ __forceinline__ const int* cache_offsets(const int* cu_pad, int batch, int* shared) {
   if (batch >= kCachedOffsets) return cu_pad;
+#pragma unroll 1
   for (int k = threadIdx.x; k <= batch; k += blockDim.x) shared[k] = cu_pad[k];
   __syncthreads();
   return shared;

@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
   // sequences: compact tokens, long row tiles; an upper bound of the key tiles
   SeqInfo s{};
   int n_tok = 0, n_long = 0, first_tok = 0, first_long = 0;
+#pragma unroll 1
   for (int base = 0; base < p.batch; base += blockDim.x) {
     const int b = base + tid;
     int tok = 0, nl = 0;
@@ -88,10 +89,10 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
       s = load_seq(p, b);
       if (!s.ok) bad = 1;
       const int tiles = div_up(s.len_k, bn);
-      const long long rows = static_cast<long long>(s.len_q) * p.group;
+      const int rows = s.len_q * p.group;  // (total_q * hq is below 2^31)
       q = s.len_q;
       if (rows > kShortRows) {
-        nl = static_cast<int>((rows + rt - 1) / rt);
+        nl = ((rows - 1) >> (rt == 256 ? 8 : 7)) + 1;
         w = static_cast<unsigned long long>(nl) * (np + tiles);
       } else if (rows > 0) {
         tok = s.len_q;
@@ -112,6 +113,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
     first_long = n_long + at.y;
     if (b < p.batch) {
       p.seqs[b] = make_int4(first_tok, -1, 0, first_long);
+#pragma unroll 1
       for (int i = 0; i < tok; ++i)
         if (first_tok + i < p.total_q) p.short_tok[first_tok + i] = s.off_q + i;
     }
@@ -135,7 +137,9 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
   // Chunk length in key tiles: all heads' chunks together about one per SM when there is
   // little to do (an item costs about four tiles before its first), two when there is much.
   const int parts = all >= 8ull * p.parts_target ? p.parts_target : (p.parts_target + 1) / 2;
-  const int len = static_cast<int>(max(1ull, (all + parts - 1) / parts));
+  // (a 64-bit division would be 500 cycles on the way of every call)
+  const int len = all >> 31 ? static_cast<int>((all + parts - 1) / parts)
+                            : max(1, static_cast<int>((static_cast<uint32_t>(all) + parts - 1) / parts));
   int n_entries = 0, n_rows = 0;  // running totals
   // Chunk c of a row tile with n key tiles in `chunks` chunks (they differ by one tile at
   // most), as entry `at`; e.slot: the row tile's first partial row.
@@ -189,6 +193,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
       if (e.rows > 0 && g < p.cap_longs) {
         e.slot = slots > 0 ? n_rows + at.y : -1;
         p.longs[g] = make_int4(e.slot, ch, e.rows, 0);
+#pragma unroll 1
         for (int c = 0; c < ch; ++c) put_chunk(e, n, ch, c, n_entries + at.x + c);
       }
       n_entries += at.tx;
@@ -201,6 +206,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
       n_rows += short_rows * pre_chunks * p.hkv;
     }
     const int u0 = wide || rt == 128 ? 0 : wide_pre, u1 = wide ? wide_pre : n_pre;
+#pragma unroll 1
     for (int k = tid; k < (u1 - u0) * pre_chunks; k += blockDim.x) {
       const int c = k / (u1 - u0), u = u0 + k - c * (u1 - u0);
       PrefixEntry e{};
@@ -234,6 +240,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
     s_order[place] = tid;
     __syncthreads();
   }
+#pragma unroll 1
   for (int base = 0; base < p.batch; base += blockDim.x) {
     const int at_b = base + tid;
     const int b = at_b < p.batch ? (sorted ? s_order[tid] : at_b) : p.batch;
@@ -269,6 +276,7 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
     if (ch > 0) {
       e.slot = slots > 0 ? n_rows + at.y : -1;
       p.seqs[b] = make_int4(first, e.slot, slots > 0 ? ch : -1, 0);
+#pragma unroll 1
       for (int c = 0; c < ch; ++c) put_chunk(e, n, ch, c, n_entries + at.x + c);
     }
     n_entries += at.tx;
@@ -1248,10 +1256,10 @@ cudaError_t launch_prefix_fwd(const PrefixParams& p, bool bf16, int num_sms, cud
 // then kWarps warps share a row's parts, four loads in flight each, and add up in shared
 // memory; with many, one warp takes a row alone, or several heads of a token.
 // ---------------------------------------------------------------------------
-template <bool kBF16, int kWarps>
+template <bool kBF16, int kWarps, int kCols>  // kCols: 128 or 256, at least d
 __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ PrefixParams p, int slices) {
   using T = typename std::conditional<kBF16, __nv_bfloat16, __half>::type;
-  __shared__ float s_acc[kWarps > 1 ? 8 : 1][kWarps > 1 ? 256 : 1];
+  __shared__ float s_acc[kWarps > 1 ? 8 : 1][kWarps > 1 ? kCols : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = warp % kWarps;  // this warp's share of a row's parts
   // (total_q * hq, and with it every count of rows here, is below 2^31)
@@ -1262,7 +1270,8 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
   const int h0 = kWarps > 1 ? slice : static_cast<int>(static_cast<long long>(p.hq) * slice / slices);
   const int h1 = !any ? h0 : kWarps > 1 ? h0 + 1 : static_cast<int>(static_cast<long long>(p.hq) * (slice + 1) / slices);
   __shared__ int s_pad[kCachedOffsets];
-  const int rt = prefix_row_tile(p.d);
+  constexpr int kC = kCols / 128;
+  constexpr int rt = prefix_row_tile(kCols), tile_shift = rt == 256 ? 8 : 7;
   int i = 0;
   const int b = locate_row(p, cache_offsets(p.cu_q_pad, p.batch, s_pad), t, &i);
   SeqInfo s{};
@@ -1280,6 +1289,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     if (p.group <= rt && first.x < 0 && first.y == 1 && last.x < 0 && last.y == 1) return;
   }
   // several warps per row: slices == hq, one head each, so the loop runs once for all
+#pragma unroll 1
   for (int h = h0; h < (kWarps > 1 ? h0 + 1 : h1); ++h) {
     const size_t row = static_cast<size_t>(t) * p.hq + h;
     const int g = h / p.group, j = h - g * p.group;
@@ -1287,7 +1297,6 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     bool write = h < h1;
     int na = 0, nb = 0;
     int a0 = 0, astep = 0, b0 = 0, bstep = 0;  // (cap_rows is below 2^31)
-    const int tile_shift = rt == 256 ? 8 : 7;
     if (real && info.x < 0) {
       const int rr = i * p.group + j;
       const int4 tile = p.longs[info.w + (rr >> tile_shift)];
@@ -1313,14 +1322,14 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     auto at = [&](int k) { return k < na ? a0 + k * astep : b0 + (k - na) * bstep; };
     // this warp's parts k, k + kWarps, ..., four at a time; the first four are on their way
     // before their weights are known (what a part without a visible key left is not used)
-    float4 v[4][2];
+    float4 v[4][kC];
     auto load = [&](int k) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const bool some = k + u * kWarps < n;
         const float* src = p.part_o + static_cast<size_t>(some ? at(k + u * kWarps) : 0) * p.d;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < kC; ++c) {
           const int col = 128 * c + 4 * lane;
           v[u][c] = some && col < p.d ? *reinterpret_cast<const float4*>(src + col) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -1329,6 +1338,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     load(sub);
     const float2 ml0 = lane < n ? p.part_ml[at(lane)] : make_float2(-INFINITY, 0.f);
     float M = ml0.y != 0.f ? ml0.x : -INFINITY;
+#pragma unroll 1
     for (int k = lane + 32; k < n; k += 32) {
       const float2 ml = p.part_ml[at(k)];
       if (ml.y != 0.f) M = fmaxf(M, ml.x);
@@ -1336,11 +1346,13 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float L = 0.f;
-    float acc[8] = {};
+    float acc[4 * kC] = {};
+#pragma unroll 1
     for (int k0 = 0; k0 < n; k0 += 32) {
       const float2 ml = k0 == 0 ? ml0 : k0 + lane < n ? p.part_ml[at(k0 + lane)] : make_float2(-INFINITY, 0.f);
       const float wgt = ml.y != 0.f ? ex2p(ml.x - M) : 0.f;
       L += wgt * ml.y;
+#pragma unroll 1
       for (int k = sub; k < min(32, n - k0); k += 4 * kWarps) {
         if (k0 + k > sub) load(k0 + k);
 #pragma unroll
@@ -1348,7 +1360,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
           const float wk = __shfl_sync(0xffffffffu, wgt, (k + u * kWarps) & 31);
           if (wk == 0.f || k + u * kWarps >= 32) continue;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < kC; ++c) {
             acc[4 * c] = fmaf(wk, v[u][c].x, acc[4 * c]);
             acc[4 * c + 1] = fmaf(wk, v[u][c].y, acc[4 * c + 1]);
             acc[4 * c + 2] = fmaf(wk, v[u][c].z, acc[4 * c + 2]);
@@ -1361,18 +1373,18 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if constexpr (kWarps > 1) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) s_acc[warp][(c >> 2) * 128 + 4 * lane + (c & 3)] = acc[c];
+      for (int c = 0; c < 4 * kC; ++c) s_acc[warp][(c >> 2) * 128 + 4 * lane + (c & 3)] = acc[c];
       __syncthreads();
       if (sub != 0) return;
 #pragma unroll
       for (int o = 1; o < kWarps; ++o)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] += s_acc[warp + o][(c >> 2) * 128 + 4 * lane + (c & 3)];
+        for (int c = 0; c < 4 * kC; ++c) acc[c] += s_acc[warp + o][(c >> 2) * 128 + 4 * lane + (c & 3)];
     }
     if (!write) continue;
     const float inv = L == 0.f ? 0.f : 1.0f / L;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < kC; ++c) {
       const int col = 128 * c + 4 * lane;
       if (col < p.d) {
         uint2 v;
@@ -1385,25 +1397,26 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
   }
 }
 
-template <bool kBF16>
+template <bool kBF16, int kCols>
 static cudaError_t launch_join_impl(const PrefixParams& p, int num_sms, cudaStream_t st) {
   const long long rows = static_cast<long long>(p.total_q) * p.hq, few = static_cast<long long>(num_sms) * 16;
   auto blocks = [](long long warps) { return static_cast<unsigned>((warps + 7) / 8); };
   if (rows * 4 <= few) {
-    return launch_dependent(prefix_join_kernel<kBF16, 8>, blocks(rows * 8), 256, 0, st, p, p.hq);
+    return launch_dependent(prefix_join_kernel<kBF16, 8, kCols>, blocks(rows * 8), 256, 0, st, p, p.hq);
   } else if (rows <= few) {
-    return launch_dependent(prefix_join_kernel<kBF16, 4>, blocks(rows * 4), 256, 0, st, p, p.hq);
+    return launch_dependent(prefix_join_kernel<kBF16, 4, kCols>, blocks(rows * 4), 256, 0, st, p, p.hq);
   } else {
     // one warp per row while that fills the GPU about twice over, several heads beyond it
     const long long want = (4 * few + p.total_q - 1) / p.total_q;
     const int slices = static_cast<int>(want < p.hq ? want : p.hq);
-    return launch_dependent(prefix_join_kernel<kBF16, 1>, blocks(static_cast<long long>(p.total_q) * slices), 256, 0,
+    return launch_dependent(prefix_join_kernel<kBF16, 1, kCols>, blocks(static_cast<long long>(p.total_q) * slices), 256, 0,
                             st, p, slices);
   }
 }
 
 cudaError_t launch_prefix_join(const PrefixParams& p, bool bf16, int num_sms, cudaStream_t st) {
-  return bf16 ? launch_join_impl<true>(p, num_sms, st) : launch_join_impl<false>(p, num_sms, st);
+  if (p.d <= 128) return bf16 ? launch_join_impl<true, 128>(p, num_sms, st) : launch_join_impl<false, 128>(p, num_sms, st);
+  return bf16 ? launch_join_impl<true, 256>(p, num_sms, st) : launch_join_impl<false, 256>(p, num_sms, st);
 }
 
 }  // namespace teattn
