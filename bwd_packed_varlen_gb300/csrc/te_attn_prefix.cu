@@ -130,12 +130,32 @@ bool bwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, i
   const int halves = d > 128 ? 2 : 1;
   const long long steps = (group >> sh) * (L->rows_lin / (d > 128 ? 64 : 128));
   const long long items = (static_cast<long long>(prefix_rows) + kBlockN - 1) / kBlockN * hkv * halves;
-  // parts of a sweep: as many as give the shortest run of whole rounds over the SMs, a part
-  // costing about three steps more than its sweep (starting it, storing its fp32 sums)
-  long long best = 0;
+  // Parts of a sweep: the number that ends the dK/dV launch soonest by this estimate, in
+  // microseconds. A step (a row tile against a key tile) takes 0.8, 2 and 0.8 of them at head
+  // dims to 64, 128 and 256, an item 8 more. The sequences' own items, here all of mean
+  // length, come after the prefix's and fill what those leave idle. The tail is 0.4 of the
+  // longest item, or of an own one if those are many and the prefix's fill the SMs without
+  // being cut. Summing parts costs 3, and their bytes at 2.5 MB a microsecond. The rates were
+  // fitted to 58 problems: the chosen number came within 1.7 % of the best one's backward pass
+  // on average, with counting whole rounds of the prefix's items alone within 6.6 % (16
+  // sequences of 38 to 192 tokens, 8 heads of 80, prefix 615: 85 -> 67 us).
+  const double step = d <= 64 ? 0.8 : d <= 128 ? 2.0 : 0.8;
+  const long long row_tile = d > 128 ? 64 : 128;
+  const long long seq_steps = (rows / batch + row_tile - 1) / row_tile, seq_tiles = (total_kv / batch + kBlockN - 1) / kBlockN;
+  const double own = total_kv > 0 ? static_cast<double>(hkv) * halves * batch * (seq_tiles > 1 ? seq_tiles : 1) : 0;
+  const double own_us = (group >> sh) * (seq_steps > 1 ? seq_steps : 1) * step + 8;
+  const double part_mb = static_cast<double>(prefix_rows) * hkv * d * 2 * sizeof(float) / 1e6;
+  double best = 0;
   L->splits = 1;
-  for (long long n = 1; items > 0 && n <= 64 && n <= (steps / 4 > 1 ? steps / 4 : 1); ++n) {
-    const long long cost = (items * n + kSMs - 1) / kSMs * ((steps + n - 1) / n + (n > 1 ? 3 : 1));
+  for (long long n = 1; items > 0 && n <= 64 && n <= (steps > 3 ? steps / 2 : 1); ++n) {
+    const double part_us = static_cast<double>((steps + n - 1) / n) * step + 8;
+    const double own_share = own * own_us / kSMs;
+    const double tail = items >= kSMs && own_share >= 0.5 * part_us ? own_us : part_us > own_us ? part_us : own_us;
+    const double area = items * n * part_us / kSMs + own_share + 0.4 * tail;
+    const double rounds = static_cast<double>((items * n + kSMs - 1) / kSMs) * part_us;
+    double cost = area > rounds ? area : rounds;
+    if (cost < own_us) cost = own_us;
+    if (n > 1) cost += 3 + n * part_mb / 2.5;
     if (best == 0 || cost < best) {
       best = cost;
       L->splits = static_cast<int>(n);
