@@ -106,9 +106,9 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(const __grid_constant_
   constexpr float kLog2e = 1.4426950408889634f;
   const int cpr = p.d / 8;  // 16-byte chunks per head
   pdl_trigger();
-  pdl_wait();  // pref_q and the header
-  // more tiles than the lists hold (overlapping sequences): no row is a token
-  const bool none = p.header[kHdrNumQPairs] != p.pref_q[p.batch];
+  // The first rows' sums are formed while the scheduler runs; what comes of them needs its
+  // result (small training steps 2 us shorter).
+  bool waited = false, none = false;
   // blocks of rows, up to the linear rows past the tensor's last one
   const long long rows_end = p.rows_lin >> sh;
   for (long long r0 = static_cast<long long>(blockIdx.x) * kPrepRows; r0 < rows_end;
@@ -116,14 +116,11 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(const __grid_constant_
     const long long r = r0 + warp;
     const size_t row = static_cast<size_t>(r);
     int i = 0;
-    const int b = none || r >= p.total_q ? -1 : locate_row(p, q_pad, static_cast<int>(r), &i);
+    const int b = r >= p.total_q ? -1 : locate_row(p, q_pad, static_cast<int>(r), &i);
     SeqInfo s{};
     if (b >= 0) s = load_seq(p, b);
     const bool real = b >= 0 && i < s.len_q;
-    // rows that see no key: their tiles leave dq to this kernel
-    if (r < p.total_q && (!real || (!prefix && row_keys(s, i, causal) == 0))) zero_rows(p.dq, row, p.hq * p.d * 2);
     const bool read = real && (prefix || s.len_k > 0);  // some tile reads this row
-    if (lane == 0) s_tile[warp] = read ? static_cast<long long>(packed_index(p, b, i << sh, 0)) : -1;
     for (int h0 = 0; h0 < p.hq; h0 += kPrepHeads) {
       const int nh = min(kPrepHeads, p.hq - h0);
       for (int h = lane; h < nh; h += 32) {
@@ -164,13 +161,25 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(const __grid_constant_
           }
         }
       }
+      if (!waited) {
+        pdl_wait();  // pref_q and the header
+        waited = true;
+        // more tiles than the lists hold (overlapping sequences): no row is a token
+        none = p.header[kHdrNumQPairs] != p.pref_q[p.batch];
+      }
+      if (h0 == 0) {
+        // rows that see no key: their tiles leave dq to this kernel
+        if (r < p.total_q && (none || !real || (!prefix && row_keys(s, i, causal) == 0)))
+          zero_rows(p.dq, row, p.hq * p.d * 2);
+        if (lane == 0) s_tile[warp] = read && !none ? static_cast<long long>(packed_index(p, b, i << sh, 0)) : -1;
+      }
       __syncthreads();
       // The rows' values leave in runs: of a virtual head, eight rows times its packed heads
       // lie side by side by tensor row, and a row's packed heads by tile.
       for (int z = threadIdx.x; z < nh * kPrepRows; z += 256) {
         const int w = (z >> sh) % kPrepRows, vh = (z >> sh) / kPrepRows, j = z & ((1 << sh) - 1);
         const int h = (vh << sh) + j;
-        const float lse = s_lse[h][w], delta = s_delta[h][w];
+        const float lse = none ? -INFINITY : s_lse[h][w], delta = none ? 0.f : s_delta[h][w];
         const size_t vhead = static_cast<size_t>((h0 >> sh) + vh);
         if (r0 + w < rows_end) {
           const size_t lin = vhead * p.rows_lin + (static_cast<size_t>(r0 + w) << sh) + j;
@@ -187,6 +196,10 @@ __global__ void __launch_bounds__(256) prefix_prep_kernel(const __grid_constant_
       }
       __syncthreads();
     }
+  }
+  if (!waited) {
+    pdl_wait();
+    none = p.header[kHdrNumQPairs] != p.pref_q[p.batch];
   }
   const long long warps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
   for (long long r = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < p.total_kv; r += warps) {
