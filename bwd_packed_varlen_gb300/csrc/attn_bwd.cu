@@ -630,14 +630,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* status = p.header + kHdrStatus;
-  if constexpr (is_prefix<P>) {
-    pdl_wait();
-    pdl_trigger();
-  }
-  const int n_pairs = p.header[kHdrNumQPairs];
-  const int n_items = n_pairs * virtual_heads(p);
-  const bool causal = p.causal != 0;
   constexpr bool kPrefix = is_prefix<P>;
+  int n_pairs = 0, n_items = 0;
+  auto read_lists = [&]() {
+    n_pairs = p.header[kHdrNumQPairs];
+    n_items = n_pairs * virtual_heads(p);
+  };
+  if constexpr (!kPrefix) read_lists();
+  const bool causal = p.causal != 0;
   const int sh = pack_shift(p), vgroup = virtual_group(p);
   const int pre_keys = prefix_keys_of(p);
   const int np = (pre_keys + kBN - 1) / kBN;  // prefix key tiles, ahead of the own ones
@@ -670,6 +670,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  if constexpr (kPrefix) {  // set up while the rows are prepared
+    pdl_wait();
+    pdl_trigger();
+    read_lists();
+  }
 
   if (warp == kWarpProducer) {
     if (lane == 0) {
