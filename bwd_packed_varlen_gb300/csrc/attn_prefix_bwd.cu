@@ -38,12 +38,16 @@ __global__ void __launch_bounds__(1024) prefix_bwd_schedule_kernel(const __grid_
     const Scan3 at = block_scan3(cq, ck, 0, buf);
     if (b < p.batch) pref_q[b] = n_q + at.x;
     // a warp writes its 32 sequences' tiles together
-    for (int l = 0; l < 32; ++l) {
+#pragma unroll 1
+    for (uint32_t some = __ballot_sync(0xffffffffu, cq > 0 || ck > 0); some; some &= some - 1) {
+      const int l = __ffs(some) - 1;
       const int seq = __shfl_sync(0xffffffffu, b, l);
       const int q0 = n_q + __shfl_sync(0xffffffffu, at.x, l), nq = __shfl_sync(0xffffffffu, cq, l);
       const int k0 = n_k + __shfl_sync(0xffffffffu, at.y, l), nk = __shfl_sync(0xffffffffu, ck, l);
+#pragma unroll 1
       for (int t = lane; t < nq; t += 32)
         if (q0 + t < p.pair_cap_q) p.q_pairs[q0 + t] = make_int2(seq, t);
+#pragma unroll 1
       for (int t = lane; t < nk; t += 32)
         if (k0 + t < p.pair_cap_k) p.k_pairs[k0 + t] = make_int2(seq, t);
     }
