@@ -19,21 +19,37 @@ __global__ void __launch_bounds__(1024) prefix_bwd_schedule_kernel(const __grid_
   pdl_trigger();
   __shared__ int buf[3][32];
   __shared__ int bad;
+  __shared__ unsigned long long tokens[2];  // of queries and of own keys
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) bad = p.prefix_len && (*p.prefix_len < 0 || *p.prefix_len > p.prefix_rows) ? 1 : 0;
+  if (threadIdx.x == 0) {
+    bad = p.prefix_len && (*p.prefix_len < 0 || *p.prefix_len > p.prefix_rows) ? 1 : 0;
+    tokens[0] = tokens[1] = 0;
+  }
   const bool prefix = prefix_keys(p) > 0;
   __syncthreads();
   int n_q = 0, n_k = 0;
   for (int base = 0; base < p.batch; base += blockDim.x) {
     const int b = base + threadIdx.x;
     int cq = 0, ck = 0;
+    unsigned long long both = 0;  // tokens of this sequence: queries, and keys in the upper half
     if (b < p.batch) {
       const SeqInfo s = load_seq(p, b);
       if (!s.ok) bad = 1;
+      both = static_cast<unsigned long long>(s.len_k) << 32 | static_cast<uint32_t>(s.len_q);
       if (s.len_q > 0) {
         if (prefix || s.len_k > 0) cq = ((s.len_q << p.pack_shift) + kBlockM - 1) / kBlockM;
         ck = (seen_keys(s, p.causal != 0) + kBlockN - 1) / kBlockN;
       }
+    }
+    unsigned long long q = both & 0xffffffffull, k = both >> 32;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+      k += __shfl_xor_sync(0xffffffffu, k, o);
+    }
+    if (lane == 0) {
+      atomicAdd(&tokens[0], q);
+      atomicAdd(&tokens[1], k);
     }
     const Scan3 at = block_scan3(cq, ck, 0, buf);
     if (b < p.batch) pref_q[b] = n_q + at.x;
@@ -46,18 +62,20 @@ __global__ void __launch_bounds__(1024) prefix_bwd_schedule_kernel(const __grid_
       const int k0 = n_k + __shfl_sync(0xffffffffu, at.y, l), nk = __shfl_sync(0xffffffffu, ck, l);
 #pragma unroll 1
       for (int t = lane; t < nq; t += 32)
-        if (q0 + t < p.pair_cap_q) p.q_pairs[q0 + t] = make_int2(seq, t);
+        if (static_cast<uint32_t>(q0 + t) < static_cast<uint32_t>(p.pair_cap_q)) p.q_pairs[q0 + t] = make_int2(seq, t);
 #pragma unroll 1
       for (int t = lane; t < nk; t += 32)
-        if (k0 + t < p.pair_cap_k) p.k_pairs[k0 + t] = make_int2(seq, t);
+        if (static_cast<uint32_t>(k0 + t) < static_cast<uint32_t>(p.pair_cap_k)) p.k_pairs[k0 + t] = make_int2(seq, t);
     }
     n_q += at.tx;
     n_k += at.ty;
   }
   if (threadIdx.x == 0) {
-    // overlapping sequences can have more tiles than the lists hold: none is computed
-    const bool over = n_q > p.pair_cap_q || n_k > p.pair_cap_k;
-    pref_q[p.batch] = n_q;
+    // overlapping sequences, which have more tokens than there are rows, can have more tiles
+    // than the lists hold: none is computed (the scans' barriers order the sums before this)
+    const bool over = tokens[0] > static_cast<unsigned long long>(p.total_q) ||
+                      tokens[1] > static_cast<unsigned long long>(p.total_kv) || n_q > p.pair_cap_q || n_k > p.pair_cap_k;
+    pref_q[p.batch] = over ? -1 : n_q;
     p.header[kHdrStatus] = bad || over ? kStatusBadSeqlens : 0;
     p.header[kHdrNumQPairs] = over ? 0 : n_q;
     p.header[kHdrNumKPairs] = over ? 0 : n_k;

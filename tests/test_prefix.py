@@ -353,8 +353,13 @@ def test_overlapping_sequences_are_reported():
     c.cu_on[1] = prefix_sums([60, 0, 60]).cuda()
     c.cu_on[2] = torch.tensor([0, 81, 0, 81], dtype=torch.int32).cuda()
     c.cu_on[3] = torch.tensor([0, 88, 0, 88], dtype=torch.int32).cuda()
-    c.fwd(workspace=ws)
+    out, lse = c.fwd(workspace=ws)
     assert ta.read_status(ws) == 1
+    wsb = torch.empty(ta.prefix_bwd_workspace_size(*sizes), dtype=torch.uint8, device="cuda")
+    out.zero_()
+    lse.zero_()
+    grads = c.bwd(out, lse, workspace=wsb)
+    assert ta.read_status(wsb) == 1 and all(torch.equal(g, torch.zeros_like(g)) for g in grads)
 
 
 @gpu
