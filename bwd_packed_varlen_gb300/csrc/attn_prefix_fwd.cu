@@ -120,7 +120,10 @@ __global__ void __launch_bounds__(kPrefixSchedThreads) prefix_schedule_kernel(co
     n_tok += at.tx;
     n_long += at.ty;
   }
-  // (the scans' barriers order the sums and the records above before what follows)
+  // The scans' barriers order the sums before what follows, but not the records: those are
+  // written behind the last scan, and the search below reads other threads'. (n_long is the
+  // same in every thread; steps of short sequences read only their own thread's record.)
+  if (n_long > 0) __syncthreads();
   if (tokens > static_cast<unsigned long long>(p.total_q)) {
     // sequences overlap: more tokens than rows, for which the lists have no room
     if (tid == 0) {
