@@ -390,7 +390,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // query columns i of this warp with a nonzero P^T for this key row: [lo, hi)
         const int q_base = qt * kBM + col0;
         int hi = kv_valid ? min(kG, (I.s.len_q << sh) - q_base) : 0;
-        int lo = causal ? max(0, (kv_row - I.s.diag) * (1 << sh) - q_base) : 0;
+        int first = kv_row - I.s.diag;  // query that sees the key first
+        // (in heads of tokens of the sequence: a key may lie 2^31 / 64 places before the triangle)
+        if constexpr (kPrefix) first = min(max(first, 0), I.s.len_q) << sh;
+        int lo = causal ? max(0, first - q_base) : 0;
         uint32_t tokens = 0xffffffffu;  // columns that are tokens (prefix items: among all rows)
         if constexpr (kPrefix) {
           if (I.pre) {

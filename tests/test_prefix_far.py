@@ -1,0 +1,51 @@
+"""Shared-prefix attention at sizes where index arithmetic runs out of bits."""
+
+import math
+
+import pytest
+import torch
+
+import bwd_packed_varlen_gb300 as ta
+from prefix_common import ROUNDOFF, TINY, prefix_sums
+
+gpu = pytest.mark.gpu
+
+
+@gpu
+def test_gradients_of_a_cache_of_many_keys():
+    """64 heads on one kv head and 34 million own keys behind the lower-right triangle: a key's
+    distance from the first query, times the 64 packed heads, is past 2^31. lse and out are
+    inputs of the backward, so dk and dv of some keys follow from the formula at any values of
+    theirs: P = exp(scale q k - lse), dS = P (dO v - rowsum(dO out)).
+
+    The bound: P and dS are rounded once to 16 bits (u of each term) and the result once (u), u
+    for fp32 (2^-20 of the terms of scores of at most a few units, of dO v and of rowsum)."""
+    hq, d, n, m, prefix = 64, 8, 4, 34_000_000, 10
+    dtype, scale = torch.bfloat16, 1.0 / math.sqrt(8)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=gen, device="cuda", dtype=torch.float32).to(dtype)
+    q, out, dout = rand(n, hq, d), rand(n, hq, d), rand(n, hq, d)
+    k, v, kp, vp = rand(m, 1, d), rand(m, 1, d), rand(prefix, 1, d), rand(prefix, 1, d)
+    lse = torch.randn((n, hq), generator=gen, device="cuda") * 0.5
+    cu_q, cu_k = prefix_sums([n]).cuda(), prefix_sums([m]).cuda()
+    ws = torch.empty(ta.prefix_bwd_workspace_size(1, n, m, prefix, hq, 1, d), dtype=torch.uint8, device="cuda")
+    dq, dk, dv, dkp, dvp = ta.prefix_bwd(q, k, v, kp, vp, out, dout, lse, cu_q, cu_k, cu_q, cu_k, scale,
+                                         "padding_causal_bottom_right", workspace=ws)
+    assert ta.read_status(ws) == 0
+    edge = m - n - 2 ** 31 // 64
+    keys = torch.cat([torch.arange(a, a + 300) for a in (0, edge - 150, m // 2, m - 300)]).cuda()
+    Q, G, O = (x.double().flatten(0, 1) for x in (q, dout, out))
+    token = torch.arange(n, device="cuda").repeat_interleave(hq)
+    for K, V, gk, gv, see in ((k[keys, 0], v[keys, 0], dk[keys, 0], dv[keys, 0], keys[None] <= token[:, None] + m - n),
+                              (kp[:, 0], vp[:, 0], dkp[:, 0], dvp[:, 0], torch.ones(n * hq, prefix, dtype=torch.bool, device="cuda"))):
+        K, V = K.double(), V.double()
+        P = torch.where(see, torch.exp(scale * Q @ K.T - lse.double().flatten()[:, None]), 0.0)
+        D = (G * O).sum(1, keepdim=True)
+        dS = P * (G @ V.T - D)
+        far = 2.0 ** -20 * P * (G.abs() @ V.abs().T + (G * O).abs().sum(1, keepdim=True))
+        u = ROUNDOFF[dtype]
+        for got, ref, size in ((gv, P.T @ G, P.T @ G.abs()), (gk, scale * dS.T @ Q, scale * (dS.abs() + far / u).T @ Q.abs())):
+            over = ((got.double() - ref).abs() - 2 * u * (size + ref.abs()) - TINY[dtype]).max().item()
+            assert over <= 0, over
