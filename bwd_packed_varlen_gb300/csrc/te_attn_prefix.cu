@@ -161,7 +161,9 @@ bool bwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, i
       L->splits = static_cast<int>(n);
     }
   }
-  if (steps / L->splits >= (1 << 24) - 1 || L->cap_q * hq > INT32_MAX || L->cap_k * hkv * halves > INT32_MAX) return false;
+  // (an item's steps have 24 bits; those of own keys are not cut into parts, and come to
+  // all of them where one sequence holds all queries)
+  if (steps >= (1 << 24) - 1 || L->cap_q * hq > INT32_MAX || L->cap_k * hkv * halves > INT32_MAX) return false;
   size_t off = kHdrWords * sizeof(int);
   auto take = [&off](size_t bytes) {
     const size_t at = off;

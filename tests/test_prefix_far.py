@@ -1,5 +1,6 @@
 """Shared-prefix attention at sizes where index arithmetic runs out of bits."""
 
+import ctypes
 import math
 
 import pytest
@@ -49,3 +50,20 @@ def test_gradients_of_a_cache_of_many_keys():
         for got, ref, size in ((gv, P.T @ G, P.T @ G.abs()), (gk, scale * dS.T @ Q, scale * (dS.abs() + far / u).T @ Q.abs())):
             over = ((got.double() - ref).abs() - 2 * u * (size + ref.abs()) - TINY[dtype]).max().item()
             assert over <= 0, over
+
+
+def _bwd_code(batch, total_q, total_kv, rows, hq, hkv, d):
+    """What the backward answers, with placeholder pointers and no launch, for a size."""
+    P, cu = ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 21)
+    return ta.library().te_attn_prefix_bwd_thd(*[P] * 13, cu, cu, cu, cu, None, batch, total_q, total_kv, rows, hq, hkv, d,
+                                               0.1, 1, 1, P, ctypes.c_size_t(1 << 60), None)
+
+
+def test_more_steps_than_an_item_can_tell():
+    """A dK/dV item hands its number of steps over in 24 bits. Cutting the prefix's sweep does
+    not shorten the items of a sequence's own keys, which take as many steps if it holds all
+    queries: 16,000,001 heads (an odd group, a head at a time) of two row tiles are refused."""
+    size = (2, 129, 64, 32, 16_000_001, 1, 8)
+    assert ta.prefix_bwd_workspace_size(*size) == 0
+    assert _bwd_code(*size) == -2
+    assert ta.prefix_bwd_workspace_size(2, 129, 64, 32, 8_000_001, 1, 8) > 0
