@@ -297,7 +297,8 @@ static int rope_impl(const void* q, const void* k, void* q_out, void* k_out, con
                      float mscale, int inverse, int dtype, void* stream, bool sbhd) {
   if (!cu || !cu_pad) return api_fail(TE_ERR_INVALID_ARG, "cu_seqlens pointers must not be NULL");
   if (batch < 1) return api_fail(TE_ERR_INVALID_ARG, "batch must be >= 1");
-  if (rows < 0 || rows > INT32_MAX) return api_fail(TE_ERR_INVALID_ARG, "rows must lie in [0, 2^31)");
+  // (rounded up to whole blocks of tokens in 32 bits)
+  if (rows < 0 || rows > INT32_MAX - 256) return api_fail(TE_ERR_INVALID_ARG, "rows must lie in [0, 2^31 - 256)");
   if (hq < 1 || hkv < 0) return api_fail(TE_ERR_INVALID_ARG, "hq must be >= 1 and hkv >= 0");
   if (hq > 4096 || hkv > 4096) return api_fail(TE_ERR_UNSUPPORTED, "at most 4096 heads");
   if (d < 8 || d > 256 || d % 8 != 0)

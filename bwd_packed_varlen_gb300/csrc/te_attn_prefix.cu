@@ -14,6 +14,12 @@ namespace {
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Lengths are rounded up to whole tiles (of at most 256 rows) in 32 bits.
+bool too_long(int total_q, int total_kv, int prefix_rows, int hq) {
+  constexpr int kMost = INT32_MAX - 256;
+  return static_cast<long long>(total_q) * hq > kMost || total_kv > kMost || prefix_rows > kMost;
+}
+
 int check_prefix(const void* const* tensors, int n_tensors, const int32_t* prefix_len, int batch,
                  int total_q, int total_kv, int prefix_rows, int hq, int hkv, int d, float attn_scale,
                  int mask_type, int dtype, const int32_t* cu_q, const int32_t* cu_kv,
@@ -22,8 +28,7 @@ int check_prefix(const void* const* tensors, int n_tensors, const int32_t* prefi
                                   cu_q, cu_kv, cu_q_pad, cu_kv_pad);
   if (rc != TE_OK) return rc;
   if (prefix_rows < 0) return api_fail(TE_ERR_INVALID_ARG, "prefix_rows must be >= 0");
-  if (static_cast<long long>(prefix_rows) * hkv * d >= (1ll << 40) ||
-      static_cast<long long>(total_q) * hq > INT32_MAX)
+  if (static_cast<long long>(prefix_rows) * hkv * d >= (1ll << 40) || too_long(total_q, total_kv, prefix_rows, hq))
     return api_fail(TE_ERR_UNSUPPORTED, "tensor too large");
   for (int i = 0; i < n_tensors; ++i)
     if (!aligned(tensors[i], 16)) return api_fail(TE_ERR_INVALID_ARG, "tensors must be 16-byte aligned");
@@ -81,7 +86,7 @@ struct FwdLayout {
 
 bool fwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, int hkv, int d, FwdLayout* L) {
   if (batch < 1 || total_q < 0 || total_kv < 0 || prefix_rows < 0 || hq < 1 || hkv < 1 || hq % hkv != 0 ||
-      d < 8 || d > 256 || d % 8 != 0 || static_cast<long long>(total_q) * hq > INT32_MAX)
+      d < 8 || d > 256 || d % 8 != 0 || too_long(total_q, total_kv, prefix_rows, hq))
     return false;
   const long long rows = static_cast<long long>(total_q) * (hq / hkv), rt = prefix_row_tile(d);
   L->parts_target = (kPartsTarget + hkv - 1) / hkv;
@@ -117,7 +122,7 @@ struct BwdLayout {
 
 bool bwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, int hkv, int d, BwdLayout* L) {
   if (batch < 1 || total_q < 0 || total_kv < 0 || prefix_rows < 0 || hq < 1 || hkv < 1 || hq % hkv != 0 ||
-      d < 8 || d > 256 || d % 8 != 0 || static_cast<long long>(total_q) * hq > INT32_MAX)
+      d < 8 || d > 256 || d % 8 != 0 || too_long(total_q, total_kv, prefix_rows, hq))
     return false;
   const int group = hq / hkv;
   int sh = 0;  // a 64-row tile holds whole tokens

@@ -283,7 +283,7 @@ int te_attn_fwd_thd_e4m3(const void* q, const void* k, const void* v, void* out,
  *   inv_freq: double [n_freq] on the device, finite, radians per position, already scaled
  *   for long contexts where wanted; angles are reduced exactly (a 64-bit fraction of a
  *   turn), so far positions lose nothing. start_positions: int32 [batch] or NULL (zeros).
- * d as for attention, 1 <= n_freq <= d / 2, at most 4096 heads. Fastest when pointers are 16-byte aligned and
+ * d as for attention, 1 <= n_freq <= d / 2, at most 4096 heads, fewer than 2^31 - 256 rows. Fastest when pointers are 16-byte aligned and
  * strides (and rot / 2, with interleaved = 0, or rot) are multiples of 8 elements.
  * No workspace; deterministic; capturable. The sbhd form takes row i * batch + b for
  * token i of sequence b, strides between those rows.
@@ -319,7 +319,8 @@ int te_attn_rope_sbhd(const void* q, const void* k, void* q_out, void* k_out,
  * errors are te_attn_fwd_thd's; k, v of one decoding step are the sequences' caches in
  * their padded slots, with TE_MASK_PADDING_CAUSAL_BOTTOM_RIGHT. Masks place queries and
  * own keys of one sequence against each other; the prefix lies before both. A real query
- * that sees no key at all gets out = 0, lse = -inf, dq = 0. total_q * hq < 2^31.
+ * that sees no key at all gets out = 0, lse = -inf, dq = 0. total_q * hq, total_kv and
+ * prefix_rows lie below 2^31 - 256 (TE_ERR_UNSUPPORTED otherwise).
  * The forward takes any bits in rows that hold no token (a cache's free slots, the rows
  * behind the prefix's real length): none reaches a result. A NaN that a row sees does.
  * An inconsistent prefix_len counts as 0 and raises TE_STATUS_BAD_SEQLENS.

@@ -67,3 +67,21 @@ def test_more_steps_than_an_item_can_tell():
     assert ta.prefix_bwd_workspace_size(*size) == 0
     assert _bwd_code(*size) == -2
     assert ta.prefix_bwd_workspace_size(2, 129, 64, 32, 8_000_001, 1, 8) > 0
+
+
+def test_sizes_within_a_tile_of_2_to_the_31():
+    """Rounding a length up to whole tiles must not pass 2^31: sizes that close are refused, by
+    the sizes' functions and by the calls; those a tile below are not."""
+    top = 2 ** 31 - 1
+    for size in ((1, 64, top, 32, 1, 1, 8), (1, 64, top - 255, 32, 1, 1, 8), (1, 64, 64, top, 1, 1, 8),
+                 (1, top, 64, 32, 1, 1, 8), (1, top // 3, 64, 32, 3, 1, 8)):
+        assert ta.prefix_fwd_workspace_size(*size) == 0 and ta.prefix_bwd_workspace_size(*size) == 0, size
+        assert _bwd_code(*size) == -2, size
+        P, cu = ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 21)
+        assert ta.library().te_attn_prefix_fwd_thd(*[P] * 7, cu, cu, cu, cu, None, *size, 0.1, 1, 1, P,
+                                                   ctypes.c_size_t(1 << 60), None) == -2, size
+    assert ta.prefix_fwd_workspace_size(1, 64, top - 256, top - 256, 1, 1, 8) > 0
+    assert ta.prefix_bwd_workspace_size(1, 64, top - 256, top - 256, 1, 1, 8) > 0
+    P = ctypes.c_void_p(1 << 20)
+    for rows in (top, top - 255):  # a rotation's blocks take up to four tokens
+        assert ta.library().te_attn_rope_thd(P, P, P, P, P, 4, P, P, None, 1, rows, 1, 1, 8, 8, 8, 8, 8, 0, 1.0, 0, 1, None) == -1
