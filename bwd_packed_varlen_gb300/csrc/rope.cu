@@ -303,7 +303,7 @@ static int rope_impl(const void* q, const void* k, void* q_out, void* k_out, con
   if (hq > 4096 || hkv > 4096) return api_fail(TE_ERR_UNSUPPORTED, "at most 4096 heads");
   if (d < 8 || d > 256 || d % 8 != 0)
     return api_fail(TE_ERR_UNSUPPORTED, "head dim must be a multiple of 8 in [8, 256]");
-  if (n_freq < 1 || 2 * n_freq > d)
+  if (n_freq < 1 || n_freq > d / 2)
     return api_fail(TE_ERR_INVALID_ARG, "n_freq must lie in [1, d / 2]");
   if (dtype != TE_DTYPE_FP16 && dtype != TE_DTYPE_BF16)
     return api_fail(TE_ERR_UNSUPPORTED, "dtype must be TE_DTYPE_FP16 or TE_DTYPE_BF16");

@@ -1,4 +1,4 @@
-"""Shared-prefix attention at sizes where index arithmetic runs out of bits."""
+"""Shared-prefix attention and rotations at sizes where index arithmetic runs out of bits."""
 
 import ctypes
 import math
@@ -85,3 +85,10 @@ def test_sizes_within_a_tile_of_2_to_the_31():
     P = ctypes.c_void_p(1 << 20)
     for rows in (top, top - 255):  # a rotation's blocks take up to four tokens
         assert ta.library().te_attn_rope_thd(P, P, P, P, P, 4, P, P, None, 1, rows, 1, 1, 8, 8, 8, 8, 8, 0, 1.0, 0, 1, None) == -1
+
+
+def test_more_frequencies_than_a_head_has_pairs():
+    """Any number of frequencies above d / 2 is refused, those whose double passes 2^31 too."""
+    P = ctypes.c_void_p(1 << 20)
+    for n in (33, 1 << 30, (1 << 31) - 1):
+        assert ta.library().te_attn_rope_thd(P, P, P, P, P, n, P, P, None, 1, 4, 1, 1, 64, 64, 64, 64, 64, 0, 1.0, 0, 1, None) == -1
