@@ -281,11 +281,15 @@ PyObject* rope(PyObject* const* a) {
   const int hq = as_int(q.size(dims - 2)), hkv = with_k ? as_int(k.size(dims - 2)) : 0, d = as_int(q.size(dims - 1));
   const int rows = as_int(q.size(0)), batch = as_int(n - 1), freqs = as_int(w.numel());
   const int32_t* pad = packed ? lengths(a[5], n, index) : nullptr;
-  if (!packed) {
-    need(q.size(1) == n - 1, "cu_seqlens must hold batch + 1 values");
-    need(rows <= 1 || (q.stride(0) == q.size(1) * q.stride(1) && k.stride(0) == k.size(1) * k.stride(1)),
-         "rows i * batch + b must be evenly spaced");
-  }
+  if (!packed) need(q.size(1) == n - 1, "cu_seqlens must hold batch + 1 values");
+  // strides (an axis of one element has none: torch lets it be anything)
+  auto stride = [](const at::Tensor& x, int64_t dim) { return x.size(dim) > 1 ? x.stride(dim) : 0; };
+  auto token_stride = [&](const at::Tensor& x) {
+    if (packed || batch == 1) return stride(x, 0);
+    need(rows <= 1 || x.stride(0) == batch * x.stride(1), "rows i * batch + b must be evenly spaced");
+    return stride(x, 1);
+  };
+  const int64_t qt = token_stride(q), qh = stride(q, dims - 2), kt = token_stride(k), kh = stride(k, dims - 2);
   const Place place(index, a[12]);
   const Output qo(a[10], q.sizes(), q, q.scalar_type(), "outputs must be contiguous, with the shape, dtype and device of their input");
   std::optional<Output> ko;
@@ -293,7 +297,6 @@ PyObject* rope(PyObject* const* a) {
     ko.emplace(a[11], k.sizes(), k, k.scalar_type(), "outputs must be contiguous, with the shape, dtype and device of their input");
   const void* k_at = with_k ? k.const_data_ptr() : nullptr;
   void* ko_at = with_k ? ko->at() : nullptr;
-  const int64_t qt = q.stride(dims - 3), qh = q.stride(dims - 2), kt = k.stride(dims - 3), kh = k.stride(dims - 2);
   int rc;
   void* fn = address(a[0]);
   Py_BEGIN_ALLOW_THREADS;
