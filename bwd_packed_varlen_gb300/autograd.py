@@ -100,14 +100,15 @@ class SBHDAttentionFunction(torch.autograd.Function):
 
 
 class RotaryFunction(torch.autograd.Function):
-    """``(q', k') = rotary positions of (q, k)``; the backward turns by the negative angle.
-    ``cu_pad`` None: the sequence-major layout ``[S, B, h, d]``, else packed ``[T, h, d]``."""
+    """``(q', k') = rotary positions of (q, k)``; the backward turns by the negative angle
+    (``inverse``), and its backward by the angle again. ``cu_pad`` None: the sequence-major
+    layout ``[S, B, h, d]``, else packed ``[T, h, d]``."""
 
     @staticmethod
-    def forward(ctx, q, k, inv_freq, cu, cu_pad, start, interleaved, mscale):
+    def forward(ctx, q, k, inv_freq, cu, cu_pad, start, interleaved, mscale, inverse=False):
         ctx.save_for_backward(inv_freq, cu, cu_pad, start)
-        ctx.args = (interleaved, mscale)
-        return RotaryFunction._turn(q, k, inv_freq, cu, cu_pad, start, interleaved, mscale, False)
+        ctx.args = (interleaved, mscale, not inverse)
+        return RotaryFunction._turn(q, k, inv_freq, cu, cu_pad, start, interleaved, mscale, inverse)
 
     @staticmethod
     def _turn(q, k, inv_freq, cu, cu_pad, start, *args):
@@ -122,14 +123,16 @@ class RotaryFunction(torch.autograd.Function):
         # and sequence-major rows evenly spaced
         dq, dk = (g if g is None or (g.stride(-1) == 1 and tables[2] is not None) else g.contiguous()
                   for g in (dq, dk))
-        dq, dk = RotaryFunction._turn(dq, dk, *tables, *ctx.args, True)
-        return (dq, dk) + (None,) * 6
+        # with a graph wanted (create_graph), the rotation of the gradients is part of it
+        turn = RotaryFunction.apply if torch.is_grad_enabled() else RotaryFunction._turn
+        dq, dk = turn(dq, dk, *tables, *ctx.args)
+        return (dq, dk) + (None,) * 7
 
 
 class PrefixAttentionFunction(torch.autograd.Function):
     """``out = attention(q, [k_prefix; k], [v_prefix; v])`` over packed sequences that share
     the prefix; returns ``(out, lse)``. The backward returns the gradients of all five, the
-    prefix's summed over the sequences."""
+    prefix's summed over the sequences; these have no gradients of their own."""
 
     @staticmethod
     def forward(ctx, q, k, v, kp, vp, cu_q, cu_kv, cu_q_pad, cu_kv_pad, scale, mask, prefix_len):
@@ -142,10 +145,22 @@ class PrefixAttentionFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout, _dlse):
         q, k, v, kp, vp, out, lse, cu_q, cu_kv, cu_q_pad, cu_kv_pad, prefix_len = ctx.saved_tensors
-        scale, mask = ctx.args
-        grads = _b.prefix_bwd(q, k, v, kp, vp, out, dout.contiguous(), lse, cu_q, cu_kv, cu_q_pad, cu_kv_pad,
-                              scale, mask, prefix_len)
+        args = (q, k, v, kp, vp, out, dout.contiguous(), lse, cu_q, cu_kv, cu_q_pad, cu_kv_pad, *ctx.args, prefix_len)
+        grads = _PrefixGradients.apply(*args) if torch.is_grad_enabled() else _b.prefix_bwd(*args)
         return tuple(grads) + (None,) * 7
+
+
+class _PrefixGradients(torch.autograd.Function):
+    """The backward of :class:`PrefixAttentionFunction` where a graph of it is wanted: going
+    through that graph raises, where leaving it out would drop a term of a loss unseen."""
+
+    @staticmethod
+    def forward(ctx, *args):
+        return _b.prefix_bwd(*args)
+
+    @staticmethod
+    def backward(ctx, *_grads):
+        raise RuntimeError("shared-prefix attention has no second derivatives")
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_length=4096,
