@@ -145,7 +145,10 @@ class PrefixAttentionFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout, _dlse):
         q, k, v, kp, vp, out, lse, cu_q, cu_kv, cu_q_pad, cu_kv_pad, prefix_len = ctx.saved_tensors
-        args = (q, k, v, kp, vp, out, dout.contiguous(), lse, cu_q, cu_kv, cu_q_pad, cu_kv_pad, *ctx.args, prefix_len)
+        dout = dout.contiguous()
+        if dout.data_ptr() % 16:  # e.g. a slice of a joined tensor's gradient
+            dout = dout.clone()
+        args = (q, k, v, kp, vp, out, dout, lse, cu_q, cu_kv, cu_q_pad, cu_kv_pad, *ctx.args, prefix_len)
         grads = _PrefixGradients.apply(*args) if torch.is_grad_enabled() else _b.prefix_bwd(*args)
         return tuple(grads) + (None,) * 7
 
