@@ -247,6 +247,8 @@ def shared_prefix_attention(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlen
 
 
 def _full_lengths(B, S, device):
+    if S == 0:
+        return torch.zeros(B + 1, dtype=torch.int32, device=device)
     return torch.arange(0, (B + 1) * S, S, dtype=torch.int32, device=device)
 
 

@@ -49,3 +49,15 @@ def test_strides_of_axes_of_one():
     for strides in ((1 << 40, d, 1), (d, 1 << 40, 1), (3, 5, 1)):
         got, k = ta.rope(x.as_strided((1, 1, d), strides), x.as_strided((1, 1, d), strides), w, cu, cu, start)
         assert torch.equal(_bits(got), _bits(ref)) and torch.equal(_bits(k), _bits(ref))
+
+
+@gpu
+@pytest.mark.parametrize("fmt,shape", [("bshd", (2, 0, 4, 64)), ("sbhd", (0, 2, 4, 64))])
+def test_layouts_without_a_token(fmt, shape):
+    """No token in any sequence: empty results and gradients, with lengths given or not."""
+    w, _ = ta.rope_frequencies(64)
+    x = torch.zeros(shape, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    for cu in (None, prefix_sums([0, 0]).cuda()):
+        q, k = ta.rotary_positions(x, x, w, cu, qkv_format=fmt)
+        assert q.shape == k.shape == shape
+        assert torch.autograd.grad(q, x, torch.zeros_like(q))[0].shape == shape
