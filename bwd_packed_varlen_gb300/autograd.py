@@ -175,12 +175,16 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_l
     ``"ntk"`` raises the base so that the slowest pair is stretched by ``factor`` and the
     fastest not at all; ``"yarn"`` divides the pairs that make less than ``beta_slow`` turns
     over ``original_length``, keeps those that make more than ``beta_fast`` and blends
-    between, with ``mscale = 0.1 ln(factor) + 1``."""
+    between, linearly in the number of turns, with ``mscale = 0.1 ln(factor) + 1``. (Some
+    programs blend linearly in the pair's index between the two bounds instead; a model
+    trained with those needs its own ``inv_freq``.)"""
     rot_dim = int(rot_dim)
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be even and positive")
-    if not (base > 0 and factor >= 1):
-        raise ValueError("base must be positive and factor at least 1")
+    if not (0 < base < math.inf and 1 <= factor < math.inf):
+        raise ValueError("base must be positive and factor at least 1, both finite")
+    if scaling == "yarn" and not (original_length > 0 and beta_fast > beta_slow):
+        raise ValueError("original_length must be positive and beta_fast above beta_slow")
     c = torch.arange(rot_dim // 2, dtype=torch.float64)
     mscale = 1.0
     if scaling == "ntk" and rot_dim > 2:
