@@ -182,8 +182,8 @@ def gpu_uuid(dev):
 
 # Sources each kernel's code comes from (its file and the headers it includes).
 _HEADERS = ["common.cuh", "sm103_ptx.cuh", "row_store.cuh", "work_queue.cuh", "tmap.h"]
-KERNEL_SOURCES = {"fwd": ["attn_fwd_pair.cu"] + _HEADERS, "dkdv": ["attn_bwd.cu"] + _HEADERS,
-                  "dq": ["attn_bwd.cu"] + _HEADERS, "bwd_fused": ["attn_bwd_fused.cu"] + _HEADERS}
+_BWD = ["attn_bwd.cu", "attn_prefix.cuh", "pdl.cuh"] + _HEADERS
+KERNEL_SOURCES = {"fwd": ["attn_fwd_pair.cu"] + _HEADERS, "dkdv": _BWD, "dq": _BWD, "bwd_fused": ["attn_bwd_fused.cu"] + _HEADERS}
 
 
 def code_only(text):
