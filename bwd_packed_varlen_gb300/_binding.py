@@ -412,7 +412,8 @@ def prefix_fwd(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seql
                prefix_len=None, out=None, lse=None, workspace=None, stream=None):
     """``te_attn_prefix_fwd_thd``: attention over a prefix ``k_prefix, v_prefix [P, hkv, d]``
     that every sequence shares, then each sequence's own keys; returns ``(out [T_q, hq, d],
-    lse [T_q, hq])``."""
+    lse [T_q, hq])``. The default mask is a decoding step's, unlike that of
+    :func:`shared_prefix_attention`."""
     e = _entries.get(_use_debug) or _entry_points()
     return _result(_host.prefix_fwd(
         e[2], e[3], q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,

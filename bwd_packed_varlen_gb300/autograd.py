@@ -239,7 +239,8 @@ def shared_prefix_attention(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlen
     ``q [T_q, hq, d]``, ``k, v [T_kv, hkv, d]``, ``k_prefix, v_prefix [P, hkv, d]``; lengths,
     mask names and the shape of the result as in :func:`dot_product_attention`. The prefix is
     read once for the batch. ``prefix_len`` (one int32 on the device) gives its real length.
-    For a decoding step pass the caches as ``k, v`` with ``"padding_causal_bottom_right"``."""
+    For a decoding step pass the caches as ``k, v`` with ``"padding_causal_bottom_right"``: the
+    default, of training, puts a single query at its sequence's first own key and no other."""
     scale = 1.0 / math.sqrt(q.shape[-1]) if softmax_scale is None else float(softmax_scale)
     out, lse = PrefixAttentionFunction.apply(
         q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv,

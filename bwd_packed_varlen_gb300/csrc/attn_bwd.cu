@@ -26,6 +26,10 @@
 //   dP = dO V^T, dS = P (dP - D) into one of two 16-bit TMEM buffers, dQ += dS K
 //   with dQ in TMEM.
 //
+// P and dS are rounded to the inputs' 16-bit type because the tensor cores multiply it with
+// Q, K and dO of that type (half a step, relative to each entry); S, dP, exp, D, the
+// subtraction and every sum stay in fp32.
+//
 // Both scale by attn_scale in the epilogue and store only rows that belong to
 // real tokens (and, for dK/dV, that some real query sees); every other row is
 // written as exact zero by the zero-fill kernel.
@@ -131,7 +135,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   int* status = p.header + kHdrStatus;
   const int per_pair = p.hkv * S::kSplit;
   // With a prefix this kernel is launched once every dQ block runs, i.e. has seen the lists
-  // and rows complete: it needs nothing of dQ, and takes SMs as dQ's blocks leave them.
+  // and rows complete: it needs nothing of dQ, and takes SMs as dQ's blocks leave them. It
+  // reads those lists without a wait of its own, so it must follow dQ and nothing else, and dQ
+  // must trigger behind its wait.
   if constexpr (is_prefix<P>) pdl_trigger();
   const int n_pairs = p.header[kHdrNumKPairs];
   // Items of the prefix come first: they are the longest.
@@ -673,7 +679,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  if constexpr (kPrefix) {  // set up while the rows are prepared
+  if constexpr (kPrefix) {
+    // set up while the rows are prepared; the trigger comes behind the wait, because dK/dV
+    // starts on it and takes lists and rows to be complete
     pdl_wait();
     pdl_trigger();
     read_lists();

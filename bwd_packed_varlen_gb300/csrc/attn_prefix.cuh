@@ -128,7 +128,7 @@ __device__ __forceinline__ size_t partial_offset(const PrefixParams& p, int rows
 // ---------------------------------------------------------------------------
 // Backward: the dQ and dK/dV kernels of the packed problem, with the prefix's keys as
 // further key tiles. `pack` = 2^pack_shift heads of a group (the largest power of two that
-// divides the group, at most 128) go token by token into one row tile: packed row r of a
+// divides the group, at most 64) go token by token into one row tile: packed row r of a
 // sequence is (token r >> pack_shift, head vh * pack + r % pack) of virtual head vh. A tile
 // then covers 128 / pack tokens, so short sequences waste little of it and the heads of a
 // group share the key tiles' loads; one TMA box still fetches it.

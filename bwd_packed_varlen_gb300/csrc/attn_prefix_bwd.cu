@@ -94,7 +94,9 @@ cudaError_t launch_prefix_bwd_schedule(const PrefixBwd& p, int* pref_q, cudaStre
 // Every query row: -lse log2(e) and -D = -rowsum(dO O) for the tiles that read it, both by
 // (sequence, row tile) and by tensor row (rows that are no token: -infinity, which makes
 // their P zero); dq of rows no tile writes. Every own key row that no query sees: zeros.
-// One warp per row, 16-byte loads, four groups in flight; memory-bound.
+// One warp per row, 16-byte loads. Where d / 8 divides 32 neighbouring lanes read
+// neighbouring pieces, four groups in flight, and memory bounds it; at other head dims (48,
+// 80, 96, ...) a lane goes through a head by itself, which is slower.
 // ---------------------------------------------------------------------------
 template <bool kBF16>
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {

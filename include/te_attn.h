@@ -323,6 +323,11 @@ int te_attn_rope_sbhd(const void* q, const void* k, void* q_out, void* k_out,
  * prefix_rows lie below 2^31 - 256 (TE_ERR_UNSUPPORTED otherwise).
  * The forward takes any bits in rows that hold no token (a cache's free slots, the rows
  * behind the prefix's real length): none reaches a result. A NaN that a row sees does.
+ * The backward takes any finite values there, as te_attn_bwd_thd does, and no others: it
+ * multiplies the rows of q and dout that hold no token by zeros, so a NaN or an infinity in
+ * one makes its column of dk_prefix or dv_prefix NaN for every prefix key of its kv head; one
+ * in a key behind the prefix's real length, or in the tile of a sequence's last key, its
+ * column of dq.
  * An inconsistent prefix_len counts as 0 and raises TE_STATUS_BAD_SEQLENS.
  * The workspaces' sizes are the *_workspace_size functions'; te_attn_read_status() works
  * on them.
