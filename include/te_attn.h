@@ -283,8 +283,9 @@ int te_attn_fwd_thd_e4m3(const void* q, const void* k, const void* v, void* out,
  *   inv_freq: double [n_freq] on the device, finite, radians per position, already scaled
  *   for long contexts where wanted; angles are reduced exactly (a 64-bit fraction of a
  *   turn), so far positions lose nothing. start_positions: int32 [batch] or NULL (zeros).
- * d as for attention, 1 <= n_freq <= d / 2, at most 4096 heads, fewer than 2^31 - 256 rows. Fastest when pointers are 16-byte aligned and
- * strides (and rot / 2, with interleaved = 0, or rot) are multiples of 8 elements.
+ * d as for attention, 1 <= n_freq <= d / 2, at most 4096 heads, fewer than 2^31 - 256 rows.
+ * Fastest when pointers are 16-byte aligned and strides (and rot / 2, with interleaved = 0,
+ * or rot) are multiples of 8 elements.
  * No workspace; deterministic; capturable. The sbhd form takes row i * batch + b for
  * token i of sequence b, strides between those rows.
  */
