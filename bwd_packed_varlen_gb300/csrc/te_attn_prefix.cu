@@ -140,11 +140,12 @@ bool bwd_layout(int batch, int total_q, int total_kv, int prefix_rows, int hq, i
   // of a step: a step (a row tile against a key tile) counts 0.8, 2 and 0.8 at head dims to 64,
   // 128 and 256 (where 64-row steps take longer than that), an item 8 more. The sequences'
   // own items, here all of mean length, come after the prefix's and fill what those leave
-  // idle. The tail is 0.4 of the longest item, or of an own one if those are many and the prefix's fill the SMs without
-  // being cut. Summing parts costs 3, and their bytes at 2.5 MB a microsecond. The rates were
-  // fitted to 58 problems: the chosen number came within 1.7 % of the best one's backward pass
-  // on average, with counting whole rounds of the prefix's items alone within 6.6 % (16
-  // sequences of 38 to 192 tokens, 8 heads of 80, prefix 615: 85 -> 67 us).
+  // idle. The tail is 0.4 of the longest item, or of an own one if those are many and the
+  // prefix's fill the SMs without being cut. Summing parts costs 3, and their bytes at 2.5 MB
+  // a microsecond. The rates were fitted to 58 problems: the chosen number came within 1.7 %
+  // of the best one's backward pass on average, with counting whole rounds of the prefix's
+  // items alone within 6.6 % (16 sequences of 38 to 192 tokens, 8 heads of 80, prefix 615: 85
+  // -> 67 us).
   const double step = d <= 64 ? 0.8 : d <= 128 ? 2.0 : 0.8;
   const long long row_tile = d > 128 ? 64 : 128;
   const long long seq_steps = (rows / batch + row_tile - 1) / row_tile, seq_tiles = (total_kv / batch + kBlockN - 1) / kBlockN;
