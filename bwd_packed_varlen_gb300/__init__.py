@@ -10,7 +10,8 @@ Entry points: ``fwd`` / ``bwd`` (packed THD layout, real and padded cu_seqlens),
 inputs with per-tensor descale factors, forward only), ``bwd_noalloc`` (backward
 without a workspace), ``rope`` / ``rope_sbhd`` (rotary positions on q and k, and their
 inverse for the backward pass), ``prefix_fwd`` / ``prefix_bwd`` (attention of a packed batch
-that shares a prefix of keys, one query token per sequence or many); ``read_status`` / ``read_status_noalloc`` read a call's device
+that shares a prefix of keys, one query token per sequence or many), ``window_fwd`` /
+``window_bwd`` and their ``_sbhd`` forms (a sliding window with sinks); ``read_status`` / ``read_status_noalloc`` read a call's device
 status word, ``selftest_wait_timeout`` runs the bounded-wait unwind path on purpose and
 ``debug_build()`` routes calls to the bounds-checking build; masks ``padding``, ``padding_causal`` (upper-left) and
 ``padding_causal_bottom_right``. ``dot_product_attention`` / ``DotProductAttention``
@@ -49,6 +50,10 @@ from ._binding import (  # noqa: F401
     rope_sbhd,
     selftest_wait_timeout,
     version,
+    window_bwd,
+    window_bwd_sbhd,
+    window_fwd,
+    window_fwd_sbhd,
 )
 from .autograd import (  # noqa: F401
     DotProductAttention,
@@ -56,6 +61,7 @@ from .autograd import (  # noqa: F401
     RotaryFunction,
     SBHDAttentionFunction,
     THDAttentionFunction,
+    WindowAttentionFunction,
     dot_product_attention,
     rope_frequencies,
     rotary_positions,

@@ -95,6 +95,14 @@ def library(debug: bool = None) -> ctypes.CDLL:
     L.te_attn_fwd_thd_e4m3.restype = i32
     L.te_attn_fwd_thd_e4m3.argtypes = ([vp] * 5 + [vp] * 4 + [i32] * 8 + [f32] * 4 +
                                         [i32, vp, sz, vp])
+    L.te_attn_window_fwd_thd.restype = i32
+    L.te_attn_window_fwd_thd.argtypes = [vp] * 9 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
+    L.te_attn_window_bwd_thd.restype = i32
+    L.te_attn_window_bwd_thd.argtypes = [vp] * 13 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
+    L.te_attn_window_fwd_sbhd.restype = i32
+    L.te_attn_window_fwd_sbhd.argtypes = [vp] * 7 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
+    L.te_attn_window_bwd_sbhd.restype = i32
+    L.te_attn_window_bwd_sbhd.argtypes = [vp] * 11 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
     L.te_attn_read_status.restype = i32
     L.te_attn_read_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int), vp]
     L.te_attn_last_error.restype = ctypes.c_char_p
@@ -344,6 +352,112 @@ def bwd_sbhd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, attn_scale,
             _ptr(cu_seqlens_q), _ptr(cu_seqlens_kv), B, Sq, Sk, hq, hkv, d, float(attn_scale),
             _mask(mask_type), _DTYPES[q.dtype], _ptr(workspace), workspace.numel(), ctypes.c_void_p(st)))
     return dq, dk, dv
+
+
+def _int32(n):
+    """n as a C int: what does not fit becomes the nearest that does."""
+    return max(-2 ** 31, min(int(n), 2 ** 31 - 1))
+
+
+def _window_operands(q, k, v, cus, like_q=(), like_k=(), lse=None, workspace=None):
+    """The batch size, after the checks that the windowed calls share; the tensors that have to
+    look like q, or like k, may be None."""
+    if any(t is None for t in (q, k, v) + tuple(cus)):
+        raise ValueError("q, k, v and the cu_seqlens must be given")
+    every = (q, k, v) + tuple(cus) + tuple(like_q) + tuple(like_k) + (lse, workspace)
+    _need_cuda(*every)
+    if any(t is not None and t.device != q.device for t in every):
+        raise ValueError("all tensors must be on one device")
+    _cu(*cus)
+    packed = len(cus) == 4
+    if q.dim() != (3 if packed else 4) or k.dim() != q.dim() or k.shape != v.shape or k.shape[-1] != q.shape[-1]:
+        raise ValueError("q, k and v must be [rows, heads, d]" if packed else "q, k and v must be [S, B, heads, d]")
+    if q.dtype not in _DTYPES or any(t is not None and t.dtype != q.dtype for t in (k, v) + tuple(like_q) + tuple(like_k)):
+        raise ValueError("q, k, v, outputs and gradients must share one dtype, float16 or bfloat16")
+    for ref, ts in ((q, like_q), (k, like_k)):
+        if any(t is not None and t.shape != ref.shape for t in ts):
+            raise ValueError("outputs and gradients must have the shapes of their counterparts")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:-1]):
+        raise ValueError("lse must be float32, one value per row and head of q")
+    batch = cus[0].numel() - 1
+    if batch < 1 or any(c.numel() != batch + 1 for c in cus):
+        raise ValueError("cu_seqlens must hold batch + 1 values each")
+    if not packed and not q.shape[1] == k.shape[1] == batch:
+        raise ValueError("q, k and v must have one batch entry per sequence")
+    return batch
+
+
+def _window_sizes(q, k, batch):
+    if q.dim() == 3:
+        return (batch, q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2])
+    return (batch, q.shape[0], k.shape[0], q.shape[2], k.shape[2], q.shape[3])
+
+
+def _window_fwd(entry, q, k, v, cus, attn_scale, window, sinks, mask_type, out, lse, workspace, stream):
+    batch = _window_operands(q, k, v, cus, (out,), (), lse, workspace)
+    sizes = _window_sizes(q, k, batch)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if lse is None else lse
+    rows = (sizes[1], sizes[2]) if q.dim() == 3 else (sizes[1] * batch, sizes[2] * batch)
+    if workspace is None:
+        workspace = torch.empty(max(fwd_workspace_size(batch, *rows, *sizes[3:]), 1), dtype=torch.uint8, device=q.device)
+    st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
+    with _on(q):
+        _check(entry(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), *(_ptr(c) for c in cus), *sizes, float(attn_scale),
+                     _mask(mask_type), _int32(window), _int32(sinks), _DTYPES[q.dtype], _ptr(workspace),
+                     workspace.numel() * workspace.element_size(), ctypes.c_void_p(st)))
+    return out, lse
+
+
+def _window_bwd(entry, q, k, v, out, dout, lse, cus, attn_scale, window, sinks, mask_type, dq, dk, dv, workspace, stream):
+    if out is None or dout is None or lse is None:
+        raise ValueError("the backward needs out, dout and lse")
+    batch = _window_operands(q, k, v, cus, (out, dout, dq), (dk, dv), lse, workspace)
+    sizes = _window_sizes(q, k, batch)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    rows = (sizes[1], sizes[2]) if q.dim() == 3 else (sizes[1] * batch, sizes[2] * batch)
+    if workspace is None:
+        workspace = torch.empty(max(bwd_workspace_size(batch, *rows, *sizes[3:]), 1), dtype=torch.uint8, device=q.device)
+    st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
+    with _on(q):
+        _check(entry(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+                     *(_ptr(c) for c in cus), *sizes, float(attn_scale), _mask(mask_type), int(window), int(sinks),
+                     _DTYPES[q.dtype], _ptr(workspace), workspace.numel() * workspace.element_size(), ctypes.c_void_p(st)))
+    return dq, dk, dv
+
+
+def window_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, attn_scale, window,
+               sinks=0, mask_type="padding_causal", out=None, lse=None, workspace=None, stream=None):
+    """``te_attn_window_fwd_thd``: :func:`fwd` of queries that see the last ``window`` keys up to
+    their own position and the first ``sinks`` keys of the sequence; returns ``(out, lse)``. The
+    workspace is :func:`fwd`'s."""
+    cus = (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded)
+    return _window_fwd(library().te_attn_window_fwd_thd, q, k, v, cus, attn_scale, window, sinks, mask_type, out, lse,
+                       workspace, stream)
+
+
+def window_bwd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, attn_scale,
+               window, sinks=0, mask_type="padding_causal", dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """``te_attn_window_bwd_thd``: returns ``(dq, dk, dv)``; the workspace is :func:`bwd`'s."""
+    cus = (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded)
+    return _window_bwd(library().te_attn_window_bwd_thd, q, k, v, out, dout, lse, cus, attn_scale, window, sinks, mask_type,
+                       dq, dk, dv, workspace, stream)
+
+
+def window_fwd_sbhd(q, k, v, cu_seqlens_q, cu_seqlens_kv, attn_scale, window, sinks=0, mask_type="padding_causal", out=None,
+                    lse=None, workspace=None, stream=None):
+    """``te_attn_window_fwd_sbhd``: the same on ``[S, B, h, d]`` tensors, as :func:`fwd_sbhd`."""
+    return _window_fwd(library().te_attn_window_fwd_sbhd, q, k, v, (cu_seqlens_q, cu_seqlens_kv), attn_scale, window, sinks,
+                       mask_type, out, lse, workspace, stream)
+
+
+def window_bwd_sbhd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, attn_scale, window, sinks=0,
+                    mask_type="padding_causal", dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """``te_attn_window_bwd_sbhd``: returns ``(dq, dk, dv)``."""
+    return _window_bwd(library().te_attn_window_bwd_sbhd, q, k, v, out, dout, lse, (cu_seqlens_q, cu_seqlens_kv), attn_scale,
+                       window, sinks, mask_type, dq, dk, dv, workspace, stream)
 
 
 # The rotary and shared-prefix entry points serve single decoding steps, whose kernels take less

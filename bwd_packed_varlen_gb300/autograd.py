@@ -99,6 +99,43 @@ class SBHDAttentionFunction(torch.autograd.Function):
         return dq, dk, dv, None, None, None, None
 
 
+class WindowAttentionFunction(torch.autograd.Function):
+    """Both of the above with a sliding window and sinks: ``cus`` of four are the packed layout's,
+    of two the sequence-major one's. Its gradients have no gradients of their own."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, scale, mask, window, sinks, *cus):
+        fwd = _b.window_fwd if len(cus) == 4 else _b.window_fwd_sbhd
+        out, lse = fwd(q, k, v, *cus, scale, window, sinks, mask)
+        ctx.save_for_backward(q, k, v, out, lse, *cus)
+        ctx.args = (scale, window, sinks, mask)
+        ctx.mark_non_differentiable(lse)
+        return out, lse
+
+    @staticmethod
+    def backward(ctx, dout, _dlse):
+        q, k, v, out, lse, *cus = ctx.saved_tensors
+        dout = dout.contiguous()
+        if dout.data_ptr() % 16:  # e.g. a slice of a joined tensor's gradient
+            dout = dout.clone()
+        args = (q, k, v, out, dout, lse, *cus, *ctx.args)
+        grads = _WindowGradients.apply(*args) if torch.is_grad_enabled() else _WindowGradients.forward(None, *args)
+        return tuple(grads) + (None,) * (4 + len(cus))
+
+
+class _WindowGradients(torch.autograd.Function):
+    """The backward of :class:`WindowAttentionFunction` where a graph of it is wanted: going
+    through that graph raises, where leaving it out would drop a term of a loss unseen."""
+
+    @staticmethod
+    def forward(ctx, *args):
+        return (_b.window_bwd if len(args) == 14 else _b.window_bwd_sbhd)(*args)
+
+    @staticmethod
+    def backward(ctx, *_grads):
+        raise RuntimeError("sliding-window attention has no second derivatives")
+
+
 class RotaryFunction(torch.autograd.Function):
     """``(q', k') = rotary positions of (q, k)``; the backward turns by the negative angle
     (``inverse``), and its backward by the angle again. ``cu_pad`` None: the sequence-major
@@ -269,7 +306,8 @@ def _bshd_to_thd(x, cu_real, S):
 def dot_product_attention(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None,
                           cu_seqlens_q_padded=None, cu_seqlens_kv_padded=None,
                           max_seqlen_q=0, max_seqlen_kv=0, attn_mask_type="padding_causal",
-                          softmax_scale=None, qkv_format="thd", return_lse=False):
+                          softmax_scale=None, qkv_format="thd", return_lse=False, window=None,
+                          sinks=0):
     """Differentiable attention over packed sequences; see the module docstring.
 
     ``thd``: ``q [T_q, hq, d]``, ``k, v [T_kv, hkv, d]``; ``cu_seqlens_q/kv`` (int32
@@ -279,8 +317,11 @@ def dot_product_attention(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None,
     (default: full). ``softmax_scale`` defaults to ``1 / sqrt(d)``. Returns ``[T_q,
     hq * d]`` (``[B, S_q, hq * d]`` for bshd, ``[S_q, B, hq * d]`` for sbhd), plus
     the fp32 lse (``[T_q, hq]``, ``[B * S_q, hq]``, ``[S_q, B, hq]``) when
-    ``return_lse``."""
+    ``return_lse``. With ``window`` (causal masks only) a query sees the last ``window`` keys up
+    to its own position and the first ``sinks`` keys of its sequence."""
     mask = _mask_name(attn_mask_type)
+    if window is None and sinks:
+        raise ValueError("sinks go with a window")
     if qkv_format == "bshd":
         if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
             raise ValueError("bshd tensors must be [B, S, h, d]")
@@ -303,7 +344,10 @@ def dot_product_attention(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None,
         cu_q = _full_lengths(B, Sq, q.device) if cu_seqlens_q is None else cu_seqlens_q
         cu_kv = _full_lengths(B, k.shape[0], q.device) if cu_seqlens_kv is None else cu_seqlens_kv
         scale = 1.0 / math.sqrt(q.shape[-1]) if softmax_scale is None else float(softmax_scale)
-        out, lse = SBHDAttentionFunction.apply(q, k, v, cu_q, cu_kv, scale, mask)
+        if window is None:
+            out, lse = SBHDAttentionFunction.apply(q, k, v, cu_q, cu_kv, scale, mask)
+        else:
+            out, lse = WindowAttentionFunction.apply(q, k, v, scale, mask, window, sinks, cu_q, cu_kv)
         out = out.view(Sq, B, q.shape[2] * q.shape[3])
         return (out, lse) if return_lse else out
     elif qkv_format == "thd":
@@ -317,19 +361,24 @@ def dot_product_attention(q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None,
     else:
         raise NotImplementedError(f"qkv_format {qkv_format!r}: 'thd', 'bshd' or 'sbhd'")
     scale = 1.0 / math.sqrt(q.shape[-1]) if softmax_scale is None else float(softmax_scale)
-    out, lse = THDAttentionFunction.apply(q3, k3, v3, cu_q, cu_kv, cu_q_pad, cu_kv_pad, scale,
-                                          mask, int(max_seqlen_q or 0), int(max_seqlen_kv or 0))
+    if window is None:
+        out, lse = THDAttentionFunction.apply(q3, k3, v3, cu_q, cu_kv, cu_q_pad, cu_kv_pad, scale,
+                                              mask, int(max_seqlen_q or 0), int(max_seqlen_kv or 0))
+    else:
+        out, lse = WindowAttentionFunction.apply(q3, k3, v3, scale, mask, window, sinks, cu_q, cu_kv,
+                                                 cu_q_pad, cu_kv_pad)
     out = out.view(shape)
     return (out, lse) if return_lse else out
 
 
 class DotProductAttention(torch.nn.Module):
     """Module form of :func:`dot_product_attention` with TransformerEngine's
-    constructor arguments ([2448] minimal repro); no parameters, no state."""
+    constructor arguments ([2448] minimal repro) and a sliding ``window`` with ``sinks``; no
+    parameters, no state."""
 
     def __init__(self, num_attention_heads, kv_channels, num_gqa_groups=None,
                  attn_mask_type="padding_causal", softmax_scale=None, qkv_format="thd",
-                 attention_dropout=0.0):
+                 attention_dropout=0.0, window=None, sinks=0):
         super().__init__()
         if attention_dropout != 0.0:
             raise NotImplementedError("attention dropout is not supported")
@@ -340,6 +389,9 @@ class DotProductAttention(torch.nn.Module):
             raise ValueError("num_attention_heads must be a multiple of num_gqa_groups")
         self.attn_mask_type = _mask_name(attn_mask_type)
         self.softmax_scale = softmax_scale
+        if window is None and sinks:
+            raise ValueError("sinks go with a window")
+        self.window, self.sinks = window, sinks
         self.qkv_format = qkv_format
 
     def forward(self, q, k, v, cu_seqlens_q=None, cu_seqlens_kv=None, cu_seqlens_q_padded=None,
@@ -353,4 +405,4 @@ class DotProductAttention(torch.nn.Module):
         return dot_product_attention(
             q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded,
             max_seqlen_q or 0, max_seqlen_kv or 0, attn_mask_type or self.attn_mask_type,
-            self.softmax_scale, fmt)
+            self.softmax_scale, fmt, window=self.window, sinks=self.sinks)

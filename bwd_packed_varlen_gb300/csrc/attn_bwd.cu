@@ -46,6 +46,7 @@
 #include "row_store.cuh"
 #include "sm103_ptx.cuh"
 #include "tmap.h"
+#include "window.cuh"
 #include "work_queue.cuh"
 
 namespace teattn {
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     it.b = pr.x;
     it.s = load_seq(p, pr.x);
     it.qt0 = (first_query(it.s, it.kt * kBlockN, causal) << sh) / kBM;
-    it.nq = ((it.s.len_q << sh) + kBM - 1) / kBM;
+    it.nq = ((tile_last_query(p, it.s, it.kt) << sh) + kBM - 1) / kBM;
     it.steps = vgroup * (it.nq - it.qt0);
     return it;
   };
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!ok) break;
         // query columns i of this warp with a nonzero P^T for this key row: [lo, hi)
         const int q_base = qt * kBM + col0;
-        int hi = kv_valid ? min(kG, (I.s.len_q << sh) - q_base) : 0;
+        int hi = kv_valid ? min(kG, (last_query(p, I.s, kv_row) << sh) - q_base) : 0;
         int first = kv_row - I.s.diag;  // query that sees the key first
         // (in heads of tokens of the sequence: a key may lie 2^31 / 64 places before the triangle)
         if constexpr (kPrefix) first = min(max(first, 0), I.s.len_q) << sh;
@@ -700,6 +701,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         int item = nxt < n_items ? nxt : -1;
         int2 pr;
         SeqInfo s;
+        TileRun run{0, 0, 0};
         int n = 0;
         // Query tiles that see no key (rows before a lower-right causal triangle)
         // are left to the zero fill and never reach the ring.
@@ -708,7 +710,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           ph = item_pair_head(item, n_pairs, vgroup);
           pr = p.q_pairs[ph.pair];
           s = load_seq(p, pr.x);
-          n = np + (tile_keys(p, s, pr.y, causal) + kBN - 1) / kBN;
+          run = tile_run(p, s, pr.y * kBlockM, tile_keys(p, s, pr.y, causal), kBN);
+          n = np + run.n;
           if (n > 0) break;
           nxt = next_item(p.header + kHdrNextDq);
           item = nxt < n_items ? nxt : -1;
@@ -730,7 +733,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int j = 0; j < n; ++j, ++it) {
           const int sk = it % KS, sv = it % VS;
           const CUtensorMap *mk = &tmK, *mv = &tmV;
-          int key = s.off_k + (j - np) * kBN;
+          int key = s.off_k + run.tile(j - np) * kBN;
           if constexpr (kPrefix) {
             if (j < np) {
               mk = &p.tm_kp;
@@ -846,19 +849,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       size_t gi;
       float nlse2, ndlt;  // -lse * log2(e) and -D of this row
       int pre;  // prefix keys the row sees
+      TileRun run;    // its tile's key tiles
+      RowWindow win;  // and, with a window, which of their keys it sees
     };
     auto decode = [&](int item) {
-      RowItem r{item, 0, 0, false, 0, 0.f, 0.f, 0};
+      RowItem r{item, 0, 0, false, 0, 0.f, 0.f, 0, {0, 0, 0}, {0, 0}};
       if (item < 0) return r;
       const PairHead ph = item_pair_head(item, n_pairs, vgroup);
       const int2 pr = p.q_pairs[ph.pair];
       const int h = ph.head;
       const SeqInfo s = load_seq(p, pr.x);
-      r.n = np + (tile_keys(p, s, pr.y, causal) + kBN - 1) / kBN;
+      r.run = tile_run(p, s, pr.y * kBlockM, tile_keys(p, s, pr.y, causal), kBN);
+      r.n = np + r.run.n;
       const int row = pr.y * kBlockM + quarter * 32 + lane;
       const int tok = row >> sh;
       // rows that see no key (before a lower-right triangle) are the zero fill's
       r.lim = tok < s.len_q ? row_keys(s, tok, causal) : 0;
+      r.win = row_window(p, s, tok);
       r.pre = tok < s.len_q ? pre_keys : 0;
       r.gi = q_row(p, s, tok) * p.hq + (h << sh) + (row & ((1 << sh) - 1));
       const size_t ti = packed_index(p, pr.x, row, h);
@@ -878,6 +885,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float nlse2 = cur.nlse2, ndlt = cur.ndlt;
       for (int j = 0; j < n; ++j, ++it) {
         int nvalid = lim - ((j - np) * kBN + col0);
+        // with a window: bit i, the row sees the key of column i
+        constexpr uint32_t kAll = kG == 32 ? ~0u : (1u << (kG % 32)) - 1u;
+        uint32_t seen = kAll;
+        if constexpr (is_window<P>) seen &= seen_bits(lim, cur.win, cur.run.tile(j) * kBN + col0);
+        auto all_seen = [&]() {
+          if constexpr (is_window<P>) return seen == kAll;
+          else return nvalid >= kG;
+        };
         if constexpr (kPrefix)
           if (j < np) nvalid = cur.pre - (j * kBN + col0);
         // ---- phase A: P = exp2(S * scale * log2e - nlse2) into registers, then free S
@@ -896,7 +911,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (!ok) break;
           tc_fence_before();
           mbar_arrive(&bar_s_free);
-          if (__all_sync(0xffffffffu, nvalid >= kG)) {
+          if (__all_sync(0xffffffffu, all_seen())) {
             // paired fma: one instruction for two entries, same rounding as fmaf
             const uint64_t sl2x2 = f2_pack(sl2, sl2), nl2 = f2_pack(nlse2, nlse2);
 #pragma unroll
@@ -910,7 +925,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
             for (int i = 0; i < kG; ++i) {
               const float x = ex2b(fmaf(__uint_as_float(sv[i]), sl2, nlse2));
-              pv[i] = i < nvalid ? x : 0.f;
+              if constexpr (is_window<P>) pv[i] = (seen >> i) & 1u ? x : 0.f;
+              else pv[i] = i < nvalid ? x : 0.f;
             }
           }
         }
@@ -996,8 +1012,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ===========================================================================
 // Launchers
 // ===========================================================================
-template <int kD, bool kBF16>
-static cudaError_t launch_dkdv_impl(const AttnParams& p, int num_sms, cudaStream_t st) {
+template <int kD, bool kBF16, class P = AttnParams>
+static cudaError_t launch_dkdv_impl(const P& p, int num_sms, cudaStream_t st) {
   using S = DkdvShape<kD>;
   CUtensorMap tq, tdo, tk, tv;
   const int nb = p.sbhd ? p.batch : 1;
@@ -1006,7 +1022,7 @@ static cudaError_t launch_dkdv_impl(const AttnParams& p, int num_sms, cudaStream
       !make_tmap_tokens(&tk, p.k, p.total_kv, nb, p.hkv, p.d, kBF16, 128) ||
       !make_tmap_tokens(&tv, p.v, p.total_kv, nb, p.hkv, p.d, kBF16, 128))
     return cudaErrorInvalidValue;
-  auto kern = attn_bwd_dkdv_kernel<kD, kBF16>;
+  auto kern = attn_bwd_dkdv_kernel<kD, kBF16, P>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const long long max_items = static_cast<long long>(p.pair_cap_k) * p.hkv * S::kSplit;
@@ -1015,8 +1031,8 @@ static cudaError_t launch_dkdv_impl(const AttnParams& p, int num_sms, cudaStream
   return cudaGetLastError();
 }
 
-template <int kD, bool kBF16>
-static cudaError_t launch_dq_impl(const AttnParams& p, int num_sms, cudaStream_t st) {
+template <int kD, bool kBF16, class P = AttnParams>
+static cudaError_t launch_dq_impl(const P& p, int num_sms, cudaStream_t st) {
   using S = DqShape<kD>;
   CUtensorMap tq, tdo, tk, tv;
   const int nb = p.sbhd ? p.batch : 1;
@@ -1025,7 +1041,7 @@ static cudaError_t launch_dq_impl(const AttnParams& p, int num_sms, cudaStream_t
       !make_tmap_tokens(&tk, p.k, p.total_kv, nb, p.hkv, p.d, kBF16, S::kBN) ||
       !make_tmap_tokens(&tv, p.v, p.total_kv, nb, p.hkv, p.d, kBF16, S::kBN))
     return cudaErrorInvalidValue;
-  auto kern = attn_bwd_dq_kernel<kD, kBF16>;
+  auto kern = attn_bwd_dq_kernel<kD, kBF16, P>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const long long max_items = static_cast<long long>(p.pair_cap_q) * p.hq;
@@ -1102,28 +1118,32 @@ cudaError_t launch_prefix_bwd_dq(const PrefixBwd& p, bool bf16, int num_sms, cud
   return launch_prefix_dq_impl<256, false>(p, num_sms, st);
 }
 
-cudaError_t launch_attn_bwd_dkdv(const AttnParams& p, bool bf16, int num_sms, cudaStream_t st) {
-  const int d = p.d;
-  if (bf16) {
-    if (d <= 64) return launch_dkdv_impl<64, true>(p, num_sms, st);
-    if (d <= 128) return launch_dkdv_impl<128, true>(p, num_sms, st);
-    return launch_dkdv_impl<256, true>(p, num_sms, st);
-  }
-  if (d <= 64) return launch_dkdv_impl<64, false>(p, num_sms, st);
-  if (d <= 128) return launch_dkdv_impl<128, false>(p, num_sms, st);
-  return launch_dkdv_impl<256, false>(p, num_sms, st);
+// The kernels of an ordinary or a windowed problem for its head dim.
+template <bool kBF16, class P>
+static cudaError_t launch_dkdv_d(const P& p, int num_sms, cudaStream_t st) {
+  if (p.d <= 64) return launch_dkdv_impl<64, kBF16>(p, num_sms, st);
+  if (p.d <= 128) return launch_dkdv_impl<128, kBF16>(p, num_sms, st);
+  return launch_dkdv_impl<256, kBF16>(p, num_sms, st);
 }
 
+template <bool kBF16, class P>
+static cudaError_t launch_dq_d(const P& p, int num_sms, cudaStream_t st) {
+  if (p.d <= 64) return launch_dq_impl<64, kBF16>(p, num_sms, st);
+  if (p.d <= 128) return launch_dq_impl<128, kBF16>(p, num_sms, st);
+  return launch_dq_impl<256, kBF16>(p, num_sms, st);
+}
+
+cudaError_t launch_attn_bwd_dkdv(const AttnParams& p, bool bf16, int num_sms, cudaStream_t st) {
+  return bf16 ? launch_dkdv_d<true>(p, num_sms, st) : launch_dkdv_d<false>(p, num_sms, st);
+}
 cudaError_t launch_attn_bwd_dq(const AttnParams& p, bool bf16, int num_sms, cudaStream_t st) {
-  const int d = p.d;
-  if (bf16) {
-    if (d <= 64) return launch_dq_impl<64, true>(p, num_sms, st);
-    if (d <= 128) return launch_dq_impl<128, true>(p, num_sms, st);
-    return launch_dq_impl<256, true>(p, num_sms, st);
-  }
-  if (d <= 64) return launch_dq_impl<64, false>(p, num_sms, st);
-  if (d <= 128) return launch_dq_impl<128, false>(p, num_sms, st);
-  return launch_dq_impl<256, false>(p, num_sms, st);
+  return bf16 ? launch_dq_d<true>(p, num_sms, st) : launch_dq_d<false>(p, num_sms, st);
+}
+cudaError_t launch_window_bwd_dkdv(const WindowParams& p, bool bf16, int num_sms, cudaStream_t st) {
+  return bf16 ? launch_dkdv_d<true>(p, num_sms, st) : launch_dkdv_d<false>(p, num_sms, st);
+}
+cudaError_t launch_window_bwd_dq(const WindowParams& p, bool bf16, int num_sms, cudaStream_t st) {
+  return bf16 ? launch_dq_d<true>(p, num_sms, st) : launch_dq_d<false>(p, num_sms, st);
 }
 
 }  // namespace teattn

@@ -29,6 +29,7 @@
 #include "launch.h"
 #include "sm103_ptx.cuh"
 #include "tmap.h"
+#include "window.cuh"
 
 namespace teattn {
 
@@ -51,9 +52,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-template <int kD, bool kBF16>
+template <int kD, bool kBF16, class P = AttnParams>
 __global__ void __launch_bounds__(192, 1)
-    attn_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap tmQ,
+    attn_fwd_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using S = FwdShape<kD>;
   constexpr int SK = S::kStagesK, SV = S::kStagesV;
@@ -118,7 +119,8 @@ __global__ void __launch_bounds__(192, 1)
         const int h = ph.head, g = h / p.group;
         const SeqInfo s = load_seq(p, pr.x);
         const int qt = pr.y;
-        const int n = (visible_keys(s, qt, causal) + kBlockN - 1) / kBlockN;
+        const TileRun run = tile_run(p, s, qt * kBlockM, visible_keys(s, qt, causal), kBlockN);
+        const int n = run.n;
         // a tile that sees no key (before a lower-right causal triangle) is the
         // zero fill's; every role skips it without touching a barrier
         if (n == 0) continue;
@@ -133,13 +135,13 @@ __global__ void __launch_bounds__(192, 1)
           mbar_arrive_expect_tx(&bar_k_full[sk], S::kTileBytes);
           for (int c = 0; c < S::kChunks; ++c)
             tma_load_4d(sK + sk * S::kTileBytes + c * 16384, &tmK, &bar_k_full[sk], c * 64, g, s.tb,
-                        s.off_k + j * kBlockN);
+                        s.off_k + run.tile(j) * kBlockN);
           const int sv = it % SV;
           if (it >= SV && !(ok = mbar_wait(&bar_v_empty[sv], ((it / SV) - 1) & 1, status))) break;
           mbar_arrive_expect_tx(&bar_v_full[sv], S::kTileBytes);
           for (int c = 0; c < S::kChunks; ++c)
             tma_load_4d(sV + sv * S::kTileBytes + c * 16384, &tmV, &bar_v_full[sv], c * 64, g, s.tb,
-                        s.off_k + j * kBlockN);
+                        s.off_k + run.tile(j) * kBlockN);
         }
       }
     }
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(192, 1)
       for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
         const int2 pr = p.q_pairs[item_pair_head(item, n_pairs, p.group).pair];
         const SeqInfo s = load_seq(p, pr.x);
-        const int n = (visible_keys(s, pr.y, causal) + kBlockN - 1) / kBlockN;
+        const int n = tile_run(p, s, pr.y * kBlockM, visible_keys(s, pr.y, causal), kBlockN).n;
         if (n == 0) continue;
         const int k = ii++;  // index of this item among the block's processed ones
         if (!(ok = mbar_wait_warp(&bar_q_full, k & 1, status))) break;
@@ -215,13 +217,15 @@ __global__ void __launch_bounds__(192, 1)
       const int h = ph.head;
       const SeqInfo s = load_seq(p, pr.x);
       const int qt = pr.y;
-      const int n = (visible_keys(s, qt, causal) + kBlockN - 1) / kBlockN;
+      const TileRun run = tile_run(p, s, qt * kBlockM, visible_keys(s, qt, causal), kBlockN);
+      const int n = run.n;
       if (n == 0) continue;
       const int row = qt * kBlockM + tid;
       // rows that see no key (before a lower-right triangle) are the zero fill's
       const int lim = row < s.len_q ? row_keys(s, row, causal) : 0;
       const bool row_valid = lim > 0 && bounds_ok(q_row(p, s, row) < static_cast<size_t>(p.total_q),
                                                   p.header + kHdrStatus);
+      const RowWindow win = row_window(p, s, row);
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
         const int cur = it + j;
@@ -236,10 +240,28 @@ __global__ void __launch_bounds__(192, 1)
         tmem_ld32(t_s + lane_base + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
         tmem_ld_wait();
         const int nvalid = min(max(lim - j * kBlockN, 0), kBlockN);
+        // with a window: bit c % 32 of word c / 32, the row sees the key of column c
+        [[maybe_unused]] uint32_t seen[kBlockN / 32];
+        bool some = nvalid > 0, all = nvalid >= kBlockN;
+        if constexpr (is_window<P>) {
+          uint32_t any = 0, every = ~0u;
+#pragma unroll
+          for (int k = 0; k < kBlockN / 32; ++k) {
+            seen[k] = seen_bits(lim, win, run.tile(j) * kBlockN + 32 * k);
+            any |= seen[k];
+            every &= seen[k];
+          }
+          some = any != 0;
+          all = every == ~0u;
+        }
+        auto valid = [&](int c) {
+          if constexpr (is_window<P>) return ((seen[c / 32] >> (c % 32)) & 1u) != 0;
+          else return c < nvalid;
+        };
         // Warp-uniform: only tiles on the causal diagonal or a length boundary pay
         // for per-element masking. Max and sum use 8 independent partials so the
         // dependent chains stay short.
-        const bool full = __all_sync(0xffffffffu, nvalid >= kBlockN);
+        const bool full = __all_sync(0xffffffffu, all);
         float mp[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) mp[k] = -INFINITY;
@@ -249,14 +271,14 @@ __global__ void __launch_bounds__(192, 1)
         } else {
 #pragma unroll
           for (int c = 0; c < kBlockN; ++c)
-            mp[c & 7] = fmaxf(mp[c & 7], c < nvalid ? __uint_as_float(sr[c]) : -INFINITY);
+            mp[c & 7] = fmaxf(mp[c & 7], valid(c) ? __uint_as_float(sr[c]) : -INFINITY);
         }
         const float mx = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
                                fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
         const float mxs = mx * sl2;
         float m_new = m;
         bool rescale = false;
-        if (nvalid > 0) {
+        if (some) {
           if (m == -INFINITY) {
             m_new = mxs;
           } else if (mxs > m + 8.0f) {
@@ -281,8 +303,8 @@ __global__ void __launch_bounds__(192, 1)
           for (int c = 0; c < kBlockN / 2; ++c) {
             const float x0 = ex2(fmaf(__uint_as_float(sr[2 * c]), sl2, -m_new));
             const float x1 = ex2(fmaf(__uint_as_float(sr[2 * c + 1]), sl2, -m_new));
-            const float p0 = 2 * c < nvalid ? x0 : 0.f;
-            const float p1 = 2 * c + 1 < nvalid ? x1 : 0.f;
+            const float p0 = valid(2 * c) ? x0 : 0.f;
+            const float p1 = valid(2 * c + 1) ? x1 : 0.f;
             sp[c & 7] += p0 + p1;
             pk[c] = pack2<kBF16>(p0, p1);
           }
@@ -364,8 +386,8 @@ __global__ void __launch_bounds__(192, 1)
   }
 }
 
-template <int kD, bool kBF16>
-static cudaError_t launch_fwd_impl(const AttnParams& p, int num_sms, cudaStream_t st) {
+template <int kD, bool kBF16, class P>
+static cudaError_t launch_fwd_impl(const P& p, int num_sms, cudaStream_t st) {
   using S = FwdShape<kD>;
   CUtensorMap tq, tk, tv;
   const bool bf16 = kBF16;
@@ -374,7 +396,7 @@ static cudaError_t launch_fwd_impl(const AttnParams& p, int num_sms, cudaStream_
       !make_tmap_tokens(&tk, p.k, p.total_kv, nb, p.hkv, p.d, bf16) ||
       !make_tmap_tokens(&tv, p.v, p.total_kv, nb, p.hkv, p.d, bf16))
     return cudaErrorInvalidValue;
-  auto kern = attn_fwd_kernel<kD, kBF16>;
+  auto kern = attn_fwd_kernel<kD, kBF16, P>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -394,6 +416,11 @@ cudaError_t launch_attn_fwd(const AttnParams& p, bool bf16, int num_sms, cudaStr
   if (d <= 64) return launch_fwd_impl<64, false>(p, num_sms, st);
   if (d <= 128) return launch_fwd_impl<128, false>(p, num_sms, st);
   return launch_fwd_impl<256, false>(p, num_sms, st);
+}
+
+// (a window at head dims up to 128 runs on the two-tile kernel)
+cudaError_t launch_window_fwd(const WindowParams& p, bool bf16, int num_sms, cudaStream_t st) {
+  return bf16 ? launch_fwd_impl<256, true>(p, num_sms, st) : launch_fwd_impl<256, false>(p, num_sms, st);
 }
 
 }  // namespace teattn

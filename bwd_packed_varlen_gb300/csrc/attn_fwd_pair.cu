@@ -30,6 +30,7 @@
 #include "row_store.cuh"
 #include "sm103_ptx.cuh"
 #include "tmap.h"
+#include "window.cuh"
 #include "work_queue.cuh"
 
 namespace teattn {
@@ -70,6 +71,7 @@ struct FwdItem {
   int h, g, u;
   int n[2];      // key tiles tile A / tile B visit (0: tile absent)
   int nmax;
+  TileRun run;   // the key tiles of both: tile A's window begins first, tile B's ends last
   bool whole[2];  // tile rows lie inside the sequence's padded rows (TMA store allowed)
 };
 
@@ -78,7 +80,8 @@ struct FwdItem {
 // shortest, so they finish together, and a pair's heads share one sequence's K/V
 // rows, which stay in L2 while they run. (The kernels with one query tile per item
 // keep the group-major order of item_pair_head, which measured faster for them.)
-__device__ __forceinline__ FwdItem fwd_item(const AttnParams& p, int item, bool causal) {
+template <class P>
+__device__ __forceinline__ FwdItem fwd_item(const P& p, int item, bool causal) {
   FwdItem I;
   const PairHead ph{item / p.hq, item % p.hq};
   const int2 pr = p.f_pairs[ph.pair];
@@ -90,6 +93,14 @@ __device__ __forceinline__ FwdItem fwd_item(const AttnParams& p, int item, bool 
   I.n[0] = (visible_keys(I.s, ta, causal) + kBlockN - 1) / kBlockN;
   I.n[1] = tb * kBlockM < I.s.len_q ? (visible_keys(I.s, tb, causal) + kBlockN - 1) / kBlockN : 0;
   I.nmax = I.n[0] > I.n[1] ? I.n[0] : I.n[1];
+  I.run = TileRun{0, 0, I.nmax};
+  if constexpr (is_window<P>) {
+    const int hi = max(visible_keys(I.s, ta, causal), I.n[1] > 0 ? visible_keys(I.s, tb, causal) : 0);
+    I.run = tile_run(p, I.s, ta * kBlockM, hi, kBlockN);
+    for (int x = 0; x < 2; ++x)
+      I.n[x] = min(I.n[x], I.run.sink_tiles) + max(0, I.n[x] - max(I.run.first, I.run.sink_tiles));
+    I.nmax = I.n[0] > I.n[1] ? I.n[0] : I.n[1];
+  }
   // the store box may not reach into the next sequence's rows; sequence-major
   // tensors keep every sequence in its own batch entry (the box is clipped there)
   const int pad_q = p.sbhd ? p.total_q : p.cu_q_pad[pr.x + 1] - p.cu_q_pad[pr.x];
@@ -98,9 +109,9 @@ __device__ __forceinline__ FwdItem fwd_item(const AttnParams& p, int item, bool 
   return I;
 }
 
-template <int kD, bool kBF16, bool kFP8 = false>
+template <int kD, bool kBF16, bool kFP8 = false, class P = AttnParams>
 __global__ void __launch_bounds__(kFwdPairThreads, 1)
-    attn_fwd_pair_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap tmQ,
+    attn_fwd_pair_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ CUtensorMap tmO) {
   using S = FwdPairShape<kD, kFP8>;
@@ -197,12 +208,12 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
           mbar_arrive_expect_tx(&bar_k_full[st], S::kQKBytes);
           for (int c = 0; c < S::kQKChunks; ++c)
             tma_load_4d(sK + st * S::kQKBytes + c * 16384, &tmK, &bar_k_full[st], c * S::kQKColsPerChunk, I.g, I.s.tb,
-                        I.s.off_k + j * kBlockN);
+                        I.s.off_k + I.run.tile(j) * kBlockN);
           if (it >= NS && !(ok = mbar_wait(&bar_v_empty[st], ((it / NS) - 1) & 1, status))) break;
           mbar_arrive_expect_tx(&bar_v_full[st], S::kVBytes);
           for (int c = 0; c < S::kChunks; ++c)
             tma_load_4d(sV + st * S::kVBytes + c * 16384, &tmV, &bar_v_full[st], c * 64, I.g, I.s.tb,
-                        I.s.off_k + j * kBlockN);
+                        I.s.off_k + I.run.tile(j) * kBlockN);
         }
       }
     }
@@ -317,9 +328,11 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
       int stage_item;    // staging uses of this item (both tiles)
       bool tma;          // this tile's O leaves through the staged TMA store
       int h, tb, tok0;   // store coordinates of this tile
+      TileRun run;       // with a window: the item's key tiles,
+      RowWindow win;     // and which of their keys the row sees
     };
     auto decode = [&](int item) {
-      RowItem r{item, 0, 0, false, 0, 0, 0, false, 0, 0, 0};
+      RowItem r{item, 0, 0, false, 0, 0, 0, false, 0, 0, 0, {0, 0, 0}, {0, 0}};
       if (item < 0) return r;
       const FwdItem I = fwd_item(p, item, causal);
       r.n = I.n[x];
@@ -333,6 +346,8 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
       const int row = (2 * I.u + x) * kBlockM + quarter * 32 + lane;
       // rows that see no key (before a lower-right triangle) are the zero fill's
       r.lim = row < I.s.len_q ? row_keys(I.s, row, causal) : 0;
+      r.run = I.run;
+      r.win = row_window(p, I.s, row);
       r.out_row = q_row(p, I.s, row) * p.hq + I.h;
       r.row_valid = r.lim > 0 &&
                     bounds_ok(r.out_row < static_cast<size_t>(p.total_q) * p.hq, p.header + kHdrStatus);
@@ -355,7 +370,25 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
         ++ns;
         tc_fence_after();
         const int nvalid = min(max(lim - j * kBlockN, 0), kBlockN);
-        const bool full = __all_sync(0xffffffffu, nvalid >= kBlockN);
+        // with a window: bit c % 32 of word c / 32, the row sees the key of column c
+        [[maybe_unused]] uint32_t seen[kBlockN / 32];
+        bool some = nvalid > 0, all = nvalid >= kBlockN;
+        if constexpr (is_window<P>) {
+          uint32_t any = 0, every = ~0u;
+#pragma unroll
+          for (int k = 0; k < kBlockN / 32; ++k) {
+            seen[k] = seen_bits(lim, cur.win, cur.run.tile(j) * kBlockN + 32 * k);
+            any |= seen[k];
+            every &= seen[k];
+          }
+          some = any != 0;
+          all = every == ~0u;
+        }
+        auto valid = [&](int c) {
+          if constexpr (is_window<P>) return ((seen[c / 32] >> (c % 32)) & 1u) != 0;
+          else return c < nvalid;
+        };
+        const bool full = __all_sync(0xffffffffu, all);
         const float sl2 = p.scale_log2;
         // Row max of this tile's visible scores (log2 domain), from S in TMEM.
         auto tile_max = [&]() -> float {
@@ -367,15 +400,15 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int c = 0; c < 16; ++c)
-              mp[c & 3] = max3(mp[c & 3], 32 * k + 2 * c < nvalid ? __uint_as_float(sv[2 * c]) : -INFINITY,
-                               32 * k + 2 * c + 1 < nvalid ? __uint_as_float(sv[2 * c + 1]) : -INFINITY);
+              mp[c & 3] = max3(mp[c & 3], valid(32 * k + 2 * c) ? __uint_as_float(sv[2 * c]) : -INFINITY,
+                               valid(32 * k + 2 * c + 1) ? __uint_as_float(sv[2 * c + 1]) : -INFINITY);
           }
           return fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]) * sl2;
         };
         // A row's first tile with a visible key: its max, to start the offset m.
-        if (__any_sync(0xffffffffu, m == -INFINITY && nvalid > 0)) {
+        if (__any_sync(0xffffffffu, m == -INFINITY && some)) {
           const float mxs = tile_max();
-          if (m == -INFINITY && nvalid > 0) m = mxs;
+          if (m == -INFINITY && some) m = mxs;
         }
         // One pass over S: P = exp2(S * scale*log2e - m) and its row sum, P held in
         // registers until the pass is accepted. The offset is raised lazily: only
@@ -406,8 +439,8 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
                                                 sl2x2, negm2));
               float p0 = ex2f(xx.x), p1 = ex2f(xx.y);
               if constexpr (!kFull) {
-                p0 = 32 * k + 2 * c < nvalid ? p0 : 0.f;
-                p1 = 32 * k + 2 * c + 1 < nvalid ? p1 : 0.f;
+                p0 = valid(32 * k + 2 * c) ? p0 : 0.f;
+                p1 = valid(32 * k + 2 * c + 1) ? p1 : 0.f;
               }
               sp[c & 3] = fadd2(sp[c & 3], f2_pack(p0, p1));
               pk[k][c] = pack2<kBF16>(p0, p1);
@@ -422,7 +455,7 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
           const float2 s01 = f2_unpack(fadd2(fadd2(sp[0], sp[1]), fadd2(sp[2], sp[3])));
           if (!__any_sync(0xffffffffu, s01.x + s01.y > 256.0f)) break;
           const float mxs = tile_max();
-          const bool raise = nvalid > 0 && mxs > m + 8.0f;
+          const bool raise = some && mxs > m + 8.0f;
           if (!__any_sync(0xffffffffu, raise)) break;
           // rare: a row's max grew by more than 2^8
           if (raise) {
@@ -529,8 +562,8 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
   }
 }
 
-template <int kD, bool kBF16, bool kFP8 = false>
-static cudaError_t launch_fwd_pair_impl(const AttnParams& p, int num_sms, cudaStream_t st) {
+template <int kD, bool kBF16, bool kFP8 = false, class P = AttnParams>
+static cudaError_t launch_fwd_pair_impl(const P& p, int num_sms, cudaStream_t st) {
   using S = FwdPairShape<kD, kFP8>;
   CUtensorMap tq, tk, tv, to;
   const int nb = p.sbhd ? p.batch : 1;
@@ -541,7 +574,7 @@ static cudaError_t launch_fwd_pair_impl(const AttnParams& p, int num_sms, cudaSt
   if (!qk_ok || !make_tmap_tokens(&tv, p.v, p.total_kv, nb, p.hkv, p.d, kBF16) ||
       !make_tmap_tokens(&to, p.out, p.total_q, nb, p.hq, p.d, kBF16))
     return cudaErrorInvalidValue;
-  auto kern = attn_fwd_pair_kernel<kD, kBF16, kFP8>;
+  auto kern = attn_fwd_pair_kernel<kD, kBF16, kFP8, P>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -556,11 +589,19 @@ cudaError_t launch_attn_fwd_pair_e4m3(const AttnParams& p, int num_sms, cudaStre
   return launch_fwd_pair_impl<128, true, true>(p, num_sms, st);
 }
 
+template <class P>
+static cudaError_t launch_fwd_pair_d(const P& p, bool bf16, int num_sms, cudaStream_t st) {
+  if (bf16) return p.d <= 64 ? launch_fwd_pair_impl<64, true, false>(p, num_sms, st)
+                             : launch_fwd_pair_impl<128, true, false>(p, num_sms, st);
+  return p.d <= 64 ? launch_fwd_pair_impl<64, false, false>(p, num_sms, st)
+                   : launch_fwd_pair_impl<128, false, false>(p, num_sms, st);
+}
+
 cudaError_t launch_attn_fwd_pair(const AttnParams& p, bool bf16, int num_sms, cudaStream_t st) {
-  if (bf16) return p.d <= 64 ? launch_fwd_pair_impl<64, true>(p, num_sms, st)
-                             : launch_fwd_pair_impl<128, true>(p, num_sms, st);
-  return p.d <= 64 ? launch_fwd_pair_impl<64, false>(p, num_sms, st)
-                   : launch_fwd_pair_impl<128, false>(p, num_sms, st);
+  return launch_fwd_pair_d(p, bf16, num_sms, st);
+}
+cudaError_t launch_window_fwd_pair(const WindowParams& p, bool bf16, int num_sms, cudaStream_t st) {
+  return launch_fwd_pair_d(p, bf16, num_sms, st);
 }
 
 }  // namespace teattn

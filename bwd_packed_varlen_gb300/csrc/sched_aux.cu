@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "window.cuh"
 
 namespace teattn {
 
@@ -75,23 +76,27 @@ __device__ __forceinline__ int find_seq(const int* pref, int B, int i) {
   return lo;
 }
 
-__device__ int q_pair_cost(const AttnParams& p, int b, int t) {
+template <class P>
+__device__ int q_pair_cost(const P& p, int b, int t) {
   SeqInfo s = load_seq(p, b);
-  return (visible_keys(s, t, p.causal) + kBlockN - 1) / kBlockN;
+  return tile_run(p, s, t * kBlockM, visible_keys(s, t, p.causal), kBlockN).n;
 }
 
-__device__ int k_pair_cost(const AttnParams& p, int b, int t) {
+template <class P>
+__device__ int k_pair_cost(const P& p, int b, int t) {
   SeqInfo s = load_seq(p, b);
-  int nq = (s.len_q + kBlockM - 1) / kBlockM;
+  t = key_tiles(p, s).tile(t);
+  int nq = (tile_last_query(p, s, t) + kBlockM - 1) / kBlockM;
   return nq - first_query(s, t * kBlockN, p.causal) / kBlockM;
 }
 
 // Forward item of two query tiles: both tiles' key tiles (the second sees most).
-__device__ int f_pair_cost(const AttnParams& p, int b, int t) {
+template <class P>
+__device__ int f_pair_cost(const P& p, int b, int t) {
   SeqInfo s = load_seq(p, b);
-  const int a = (visible_keys(s, 2 * t, p.causal) + kBlockN - 1) / kBlockN;
+  const int a = tile_run(p, s, 2 * t * kBlockM, visible_keys(s, 2 * t, p.causal), kBlockN).n;
   const int c = 2 * t * kBlockM + kBlockM < s.len_q
-                    ? (visible_keys(s, 2 * t + 1, p.causal) + kBlockN - 1) / kBlockN
+                    ? tile_run(p, s, 2 * t * kBlockM + kBlockM, visible_keys(s, 2 * t + 1, p.causal), kBlockN).n
                     : 0;
   return a + c;
 }
@@ -148,8 +153,8 @@ __device__ void build_chain_list(const AttnParams& p, const int* pref, int n, in
 // a list of n <= kSortCap pairs runs in three phases, each over the threads
 // [t, t + nt): the keys (cost descending, then list position) padded to a power of
 // two m, the bitonic stages (k, j), and the sorted pairs written out.
-template <int kKind>
-__device__ void list_keys(const AttnParams& p, const int* pref, int n, int m, uint64_t* keys, int t,
+template <int kKind, class P>
+__device__ void list_keys(const P& p, const int* pref, int n, int m, uint64_t* keys, int t,
                           int nt) {
   for (int i = t; i < m; i += nt) {
     uint64_t key = ~0ull;
@@ -179,13 +184,21 @@ __device__ __forceinline__ void list_stage(uint64_t* keys, int m, int k, int j, 
   }
 }
 
-__device__ void list_out(const AttnParams& p, const int* pref, int n, int2* out, const uint64_t* keys,
+// Pair `src` of a list in natural order. With a window the key tiles that no query sees are
+// left out of their count.
+template <int kKind, class P>
+__device__ __forceinline__ int2 natural_pair(const P& p, const int* pref, int src) {
+  const int b = find_seq(pref, p.batch, src);
+  int t = src - pref[b];
+  if constexpr (is_window<P> && kKind == 1) t = key_tiles(p, load_seq(p, b)).tile(t);
+  return make_int2(b, t);
+}
+
+template <int kKind, class P>
+__device__ void list_out(const P& p, const int* pref, int n, int2* out, const uint64_t* keys,
                          int t, int nt) {
-  for (int i = t; i < n; i += nt) {
-    const int src = static_cast<int>(keys[i] & 0xffffffffu);
-    const int b = find_seq(pref, p.batch, src);
-    out[i] = make_int2(b, src - pref[b]);
-  }
+  for (int i = t; i < n; i += nt)
+    out[i] = natural_pair<kKind>(p, pref, static_cast<int>(keys[i] & 0xffffffffu));
 }
 
 __device__ __forceinline__ int pow2_at_least(int n) {
@@ -194,8 +207,8 @@ __device__ __forceinline__ int pow2_at_least(int n) {
   return m;
 }
 
-template <int kKind>
-__device__ void build_list(const AttnParams& p, const int* pref, int n, int2* out,
+template <int kKind, class P>
+__device__ void build_list(const P& p, const int* pref, int n, int2* out,
                            uint64_t* keys) {
   if (n <= kSortCap) {
     const int m = pow2_at_least(n);
@@ -207,20 +220,18 @@ __device__ void build_list(const AttnParams& p, const int* pref, int n, int2* ou
         __syncthreads();
       }
     }
-    list_out(p, pref, n, out, keys, threadIdx.x, blockDim.x);
+    list_out<kKind>(p, pref, n, out, keys, threadIdx.x, blockDim.x);
     __syncthreads();
   } else {
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      int b = find_seq(pref, p.batch, i);
-      out[i] = make_int2(b, i - pref[b]);
-    }
+    for (int i = threadIdx.x; i < n; i += blockDim.x) out[i] = natural_pair<kKind>(p, pref, i);
   }
 }
 
 // The backward's query-tile and key-tile lists, sorted side by side: half of the
 // threads each, one block-wide barrier per stage of the longer list (the shorter
 // list's stages are a prefix of it), so the two sorts cost about one.
-__device__ void build_q_k_lists(const AttnParams& p, const int* pref_q, int nq, const int* pref_k, int nk,
+template <class P>
+__device__ void build_q_k_lists(const P& p, const int* pref_q, int nq, const int* pref_k, int nk,
                                 uint64_t* keys) {
   const int half = blockDim.x / 2;
   const bool first = threadIdx.x < half;
@@ -245,13 +256,14 @@ __device__ void build_q_k_lists(const AttnParams& p, const int* pref_q, int nq, 
     }
   }
   if (first)
-    list_out(p, pref_q, nq, p.q_pairs, kq, t, half);
+    list_out<0>(p, pref_q, nq, p.q_pairs, kq, t, half);
   else
-    list_out(p, pref_k, nk, p.k_pairs, kk, t, half);
+    list_out<1>(p, pref_k, nk, p.k_pairs, kk, t, half);
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kSchedThreads) schedule_kernel(AttnParams p, int* pref_q,
+template <class P>
+__global__ void __launch_bounds__(kSchedThreads) schedule_kernel(P p, int* pref_q,
                                                                   int* pref_k, int* pref_f) {
   extern __shared__ uint64_t sort_keys[];
   __shared__ int warp_sums[32];
@@ -267,7 +279,7 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(AttnParams p, i
       if (!s.ok) bad = 1;
       if (s.len_q > 0 && s.len_k > 0) {
         cq = (s.len_q + kBlockM - 1) / kBlockM;
-        ck = (seen_keys(s, p.causal) + kBlockN - 1) / kBlockN;
+        ck = key_tiles(p, s).n;
         cf = (s.len_q + kBlockF - 1) / kBlockF;
       }
     }
@@ -335,15 +347,22 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(AttnParams p, i
   }
 }
 
-cudaError_t launch_schedule(const AttnParams& p, int* pref_q, int* pref_k, int* pref_f,
-                            cudaStream_t st) {
+template <class P>
+static cudaError_t launch_schedule_impl(const P& p, int* pref_q, int* pref_k, int* pref_f, cudaStream_t st) {
   const size_t smem = 2 * kSortCap * sizeof(uint64_t);  // two lists sorted side by side
-  cudaError_t e = cudaFuncSetAttribute(schedule_kernel,
+  cudaError_t e = cudaFuncSetAttribute(schedule_kernel<P>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  schedule_kernel<<<1, kSchedThreads, smem, st>>>(p, pref_q, pref_k, pref_f);
+  schedule_kernel<P><<<1, kSchedThreads, smem, st>>>(p, pref_q, pref_k, pref_f);
   return cudaGetLastError();
+}
+
+cudaError_t launch_schedule(const AttnParams& p, int* pref_q, int* pref_k, int* pref_f, cudaStream_t st) {
+  return launch_schedule_impl(p, pref_q, pref_k, pref_f, st);
+}
+cudaError_t launch_window_schedule(const WindowParams& p, int* pref_q, int* pref_k, int* pref_f, cudaStream_t st) {
+  return launch_schedule_impl(p, pref_q, pref_k, pref_f, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -363,7 +382,8 @@ __device__ __forceinline__ void zero_row(void* base, long long r, int row_bytes)
 }
 
 // mode 0: forward (out, lse); mode 1: backward (dq, dk, dv)
-__global__ void __launch_bounds__(256) zero_fill_kernel(AttnParams p, int mode) {
+template <class P>
+__global__ void __launch_bounds__(256) zero_fill_kernel(P p, int mode) {
   const int b = blockIdx.x;
   const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
   const int w0 = blockIdx.y * nw + (threadIdx.x >> 5), wstep = nw * gridDim.y;
@@ -391,16 +411,21 @@ __global__ void __launch_bounds__(256) zero_fill_kernel(AttnParams p, int mode) 
     const int qn = min(max(p.sbhd ? p.total_q / p.batch : p.cu_q_pad[b + 1] - p.cu_q_pad[b], 0), p.total_q);
     const int stride = p.sbhd ? p.batch : 1;
     const int dead = s.len_k == 0 ? s.len_q : (causal ? min(s.len_q, max(0, -s.diag)) : 0);
-    const int nq = dead + max(0, qn - s.len_q);
+    const int tail = max(dead, blind_tail(p, s));  // real queries from here on see no key either
+    const int nq = dead + max(0, qn - tail);
     for (int z = w0; z < nq; z += wstep) {
-      const int i = z < dead ? z : s.len_q + (z - dead);
-      clear_q(qbase + static_cast<long long>(i) * stride, z < dead ? -INFINITY : 0.0f);
+      const int i = z < dead ? z : tail + (z - dead);
+      clear_q(qbase + static_cast<long long>(i) * stride, i < s.len_q ? -INFINITY : 0.0f);
     }
     if (mode == 1) {
       const long long kbase = p.sbhd ? b : p.cu_kv_pad[b];
       const int kn = min(max(p.sbhd ? p.total_kv / p.batch : p.cu_kv_pad[b + 1] - p.cu_kv_pad[b], 0), p.total_kv);
       const int seen = seen_keys(s, causal);
       for (int j = seen + w0; j < kn; j += wstep) clear_k(kbase + static_cast<long long>(j) * stride);
+      if constexpr (is_window<P>) {
+        const KeyGap g = key_gap(p, s);
+        for (int j = g.from + w0; j < g.to; j += wstep) clear_k(kbase + static_cast<long long>(j) * stride);
+      }
     }
   } else if (!p.sbhd) {
     // packed rows before the first and after the last sequence: [0, lo) and [hi, total)
@@ -422,13 +447,21 @@ __global__ void __launch_bounds__(256) zero_fill_kernel(AttnParams p, int mode) 
   }
 }
 
-cudaError_t launch_zero_fill(const AttnParams& p, int mode, int num_sms, cudaStream_t st) {
+template <class P>
+static cudaError_t launch_zero_fill_impl(const P& p, int mode, int num_sms, cudaStream_t st) {
   // one block per sequence plus one for the rows outside them, repeated along y
   // so that about four blocks per SM share the rows of few long sequences
   const int nb = p.batch + 1;
   const int y = std::max(1, std::min(65535, (num_sms * 4 + nb - 1) / nb));
-  zero_fill_kernel<<<dim3(nb, y), 256, 0, st>>>(p, mode);
+  zero_fill_kernel<P><<<dim3(nb, y), 256, 0, st>>>(p, mode);
   return cudaGetLastError();
+}
+
+cudaError_t launch_zero_fill(const AttnParams& p, int mode, int num_sms, cudaStream_t st) {
+  return launch_zero_fill_impl(p, mode, num_sms, st);
+}
+cudaError_t launch_window_zero_fill(const WindowParams& p, int mode, int num_sms, cudaStream_t st) {
+  return launch_zero_fill_impl(p, mode, num_sms, st);
 }
 
 // ---------------------------------------------------------------------------

@@ -23,6 +23,7 @@
 #include "api_internal.h"
 #include "common.cuh"
 #include "launch.h"
+#include "window.cuh"
 
 namespace {
 
@@ -297,6 +298,32 @@ size_t widened_v_bytes(int total_kv, int hkv, int d) {
   return align_up(static_cast<size_t>(total_kv > 0 ? total_kv : 0) * hkv * d * 2, 256);
 }
 
+// A sliding window with sinks; `on` false for masks without.
+struct Window {
+  bool on;
+  int window, sinks;
+};
+
+static int check_window(const Window& w, int mask_type, int total_q, int total_kv) {
+  if (!w.on) return TE_OK;
+  if (w.window < 1) return fail(TE_ERR_INVALID_ARG, "window must be >= 1");
+  if (w.sinks < 0) return fail(TE_ERR_INVALID_ARG, "sinks must be >= 0");
+  if (mask_type == TE_MASK_PADDING)
+    return fail(TE_ERR_UNSUPPORTED, "a sliding window needs one of the causal masks");
+  if (total_q >= teattn::kWindowLimit || total_kv >= teattn::kWindowLimit)
+    return fail(TE_ERR_UNSUPPORTED, "a sliding window needs fewer than 2^30 rows");
+  return TE_OK;
+}
+
+static teattn::WindowParams window_params(const teattn::AttnParams& p, const Window& w) {
+  teattn::WindowParams q{};
+  static_cast<teattn::AttnParams&>(q) = p;
+  // a window, or sinks, of 2^30 leave every key that the mask does
+  q.window = w.window < teattn::kWindowLimit ? w.window : teattn::kWindowLimit;
+  q.sinks = w.sinks < teattn::kWindowLimit ? w.sinks : teattn::kWindowLimit;
+  return q;
+}
+
 // Forward of either layout: sbhd = false packs sequences by cu_seqlens_*_padded,
 // sbhd = true puts token i of sequence b at row i * batch + b.
 static int fwd_impl(const void* q, const void* k, const void* v, void* out, float* lse,
@@ -304,9 +331,10 @@ static int fwd_impl(const void* q, const void* k, const void* v, void* out, floa
                     const int32_t* cu_seqlens_q_padded, const int32_t* cu_seqlens_kv_padded, int batch,
                     int total_q, int total_kv, int hq, int hkv, int d, float attn_scale, int mask_type,
                     int dtype, void* workspace, size_t workspace_bytes, void* stream, bool sbhd,
-                    E4m3Scales e4m3 = E4m3Scales{false, 1.f, 1.f, 1.f}) {
+                    E4m3Scales e4m3 = E4m3Scales{false, 1.f, 1.f, 1.f}, Window win = Window{false, 0, 0}) {
   int rc = check_common(batch, total_q, total_kv, hq, hkv, d, attn_scale, mask_type, dtype,
                         cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded);
+  if (rc == TE_OK) rc = check_window(win, mask_type, total_q, total_kv);
   if (rc != TE_OK) return rc;
   if (!workspace) return fail(TE_ERR_INVALID_ARG, "workspace must not be NULL");
   if (total_q > 0 && (!q || !out || !lse))
@@ -349,7 +377,12 @@ static int fwd_impl(const void* q, const void* k, const void* v, void* out, floa
   int* pref_q = reinterpret_cast<int*>(ws + L.pref_q);
   int* pref_k = reinterpret_cast<int*>(ws + L.pref_k);
   const bool bf16 = dtype == TE_DTYPE_BF16;
-  cudaError_t e = timed(TE_KERNEL_SCHEDULE, st, [&] { return teattn::launch_schedule(p, pref_q, pref_k, reinterpret_cast<int*>(ws + L.pref_f), st); });
+  const teattn::WindowParams pw = window_params(p, win);
+  cudaError_t e = timed(TE_KERNEL_SCHEDULE, st, [&] {
+    int* pref_f = reinterpret_cast<int*>(ws + L.pref_f);
+    return win.on ? teattn::launch_window_schedule(pw, pref_q, pref_k, pref_f, st)
+                  : teattn::launch_schedule(p, pref_q, pref_k, pref_f, st);
+  });
   if (e != cudaSuccess) return cuda_fail(e, "schedule");
   if (e4m3.on && total_kv > 0) {
     // every row of V, pad slots included (they are finite e4m3 values)
@@ -362,13 +395,17 @@ static int fwd_impl(const void* q, const void* k, const void* v, void* out, floa
   if (total_q > 0 && total_kv > 0) {
     e = timed(TE_KERNEL_FWD, st, [&] {
       if (e4m3.on) return teattn::launch_attn_fwd_pair_e4m3(p, sms, st);
+      if (win.on)
+        return d <= 128 ? teattn::launch_window_fwd_pair(pw, bf16, sms, st) : teattn::launch_window_fwd(pw, bf16, sms, st);
       return d <= 128 ? teattn::launch_attn_fwd_pair(p, bf16, sms, st)
                       : teattn::launch_attn_fwd(p, bf16, sms, st);
     });
     if (e != cudaSuccess) return cuda_fail(e, "attention forward");
   }
   if (total_q > 0) {
-    e = timed(TE_KERNEL_ZERO_FILL, st, [&] { return teattn::launch_zero_fill(p, 0, sms, st); });
+    e = timed(TE_KERNEL_ZERO_FILL, st, [&] {
+      return win.on ? teattn::launch_window_zero_fill(pw, 0, sms, st) : teattn::launch_zero_fill(p, 0, sms, st);
+    });
     if (e != cudaSuccess) return cuda_fail(e, "zero fill");
   }
   return ok_status();
@@ -464,10 +501,11 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* out
                     const int32_t* cu_seqlens_kv_padded, int batch, int total_q, int total_kv,
                     int hq, int hkv, int d, float attn_scale, int mask_type, int dtype,
                     void* workspace, size_t workspace_bytes, void* stream, cudaEvent_t dq_done,
-                    bool sbhd, bool fused = false) {
+                    bool sbhd, bool fused = false, Window win = Window{false, 0, 0}) {
   int rc = teattn::bwd_check_args(q, k, v, out, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_kv,
                                   cu_seqlens_q_padded, cu_seqlens_kv_padded, batch, total_q,
                                   total_kv, hq, hkv, d, attn_scale, mask_type, dtype);
+  if (rc == TE_OK) rc = check_window(win, mask_type, total_q, total_kv);
   if (rc != TE_OK) return rc;
   if (!workspace) return fail(TE_ERR_INVALID_ARG, "workspace must not be NULL");
   const int cols = fused ? fused_cols(d) : 0;
@@ -512,11 +550,18 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* out
   p.pref_q = pref_q;
   int* pref_k = reinterpret_cast<int*>(ws + L.pref_k);
   const bool bf16 = dtype == TE_DTYPE_BF16;
-  cudaError_t e = timed(TE_KERNEL_SCHEDULE, st, [&] { return teattn::launch_schedule(p, pref_q, pref_k, reinterpret_cast<int*>(ws + L.pref_f), st); });
+  const teattn::WindowParams pw = window_params(p, win);
+  cudaError_t e = timed(TE_KERNEL_SCHEDULE, st, [&] {
+    int* pref_f = reinterpret_cast<int*>(ws + L.pref_f);
+    return win.on ? teattn::launch_window_schedule(pw, pref_q, pref_k, pref_f, st)
+                  : teattn::launch_schedule(p, pref_q, pref_k, pref_f, st);
+  });
   if (e != cudaSuccess) return cuda_fail(e, "schedule");
   // Rows no tile writes are zeroed first (they depend on the lengths only), so dq
   // is final as soon as the dQ kernel ends and dk/dv when the dK/dV kernel does.
-  e = timed(TE_KERNEL_ZERO_FILL, st, [&] { return teattn::launch_zero_fill(p, 1, sms, st); });
+  e = timed(TE_KERNEL_ZERO_FILL, st, [&] {
+    return win.on ? teattn::launch_window_zero_fill(pw, 1, sms, st) : teattn::launch_zero_fill(p, 1, sms, st);
+  });
   if (e != cudaSuccess) return cuda_fail(e, "zero fill");
   if (total_q > 0) {
     e = timed(TE_KERNEL_DELTA, st, [&] { return teattn::launch_delta(p, bf16, sms, st); });
@@ -536,7 +581,9 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* out
     return ok_status();
   }
   if (total_q > 0 && total_kv > 0) {
-    e = timed(TE_KERNEL_DQ, st, [&] { return teattn::launch_attn_bwd_dq(p, bf16, sms, st); });
+    e = timed(TE_KERNEL_DQ, st, [&] {
+      return win.on ? teattn::launch_window_bwd_dq(pw, bf16, sms, st) : teattn::launch_attn_bwd_dq(p, bf16, sms, st);
+    });
     if (e != cudaSuccess) return cuda_fail(e, "dQ");
   }
   if (dq_done) {
@@ -544,7 +591,10 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* out
     if (e != cudaSuccess) return cuda_fail(e, "dq event record");
   }
   if (total_q > 0 && total_kv > 0) {
-    e = timed(TE_KERNEL_DKDV, st, [&] { return teattn::launch_attn_bwd_dkdv(p, bf16, sms, st); });
+    e = timed(TE_KERNEL_DKDV, st, [&] {
+      return win.on ? teattn::launch_window_bwd_dkdv(pw, bf16, sms, st)
+                    : teattn::launch_attn_bwd_dkdv(p, bf16, sms, st);
+    });
     if (e != cudaSuccess) return cuda_fail(e, "dK/dV");
   }
   return ok_status();
@@ -601,6 +651,51 @@ int te_attn_bwd_sbhd(const void* q, const void* k, const void* v, const void* ou
   return bwd_impl(q, k, v, out, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q,
                   cu_seqlens_kv, batch, tq, tk, hq, hkv, d, attn_scale, mask_type, dtype, workspace,
                   workspace_bytes, stream, nullptr, true);
+}
+
+int te_attn_window_fwd_thd(const void* q, const void* k, const void* v, void* out, float* lse,
+                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                           const int32_t* cu_seqlens_q_padded, const int32_t* cu_seqlens_kv_padded, int batch,
+                           int total_q, int total_kv, int hq, int hkv, int d, float attn_scale, int mask_type,
+                           int window, int sinks, int dtype, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  return fwd_impl(q, k, v, out, lse, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded,
+                  batch, total_q, total_kv, hq, hkv, d, attn_scale, mask_type, dtype, workspace, workspace_bytes,
+                  stream, false, E4m3Scales{false, 1.f, 1.f, 1.f}, Window{true, window, sinks});
+}
+
+int te_attn_window_bwd_thd(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                           const float* lse, void* dq, void* dk, void* dv, const int32_t* cu_seqlens_q,
+                           const int32_t* cu_seqlens_kv, const int32_t* cu_seqlens_q_padded,
+                           const int32_t* cu_seqlens_kv_padded, int batch, int total_q, int total_kv, int hq,
+                           int hkv, int d, float attn_scale, int mask_type, int window, int sinks, int dtype,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  return bwd_impl(q, k, v, out, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
+                  cu_seqlens_kv_padded, batch, total_q, total_kv, hq, hkv, d, attn_scale, mask_type, dtype,
+                  workspace, workspace_bytes, stream, nullptr, false, false, Window{true, window, sinks});
+}
+
+int te_attn_window_fwd_sbhd(const void* q, const void* k, const void* v, void* out, float* lse,
+                            const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv, int batch, int seq_q,
+                            int seq_kv, int hq, int hkv, int d, float attn_scale, int mask_type, int window,
+                            int sinks, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const int tq = sbhd_rows(batch, seq_q), tk = sbhd_rows(batch, seq_kv);
+  if (tq < 0 || tk < 0) return fail(TE_ERR_INVALID_ARG, "batch >= 1, seq_q/seq_kv >= 0, rows < 2^31");
+  return fwd_impl(q, k, v, out, lse, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q, cu_seqlens_kv, batch, tq, tk, hq,
+                  hkv, d, attn_scale, mask_type, dtype, workspace, workspace_bytes, stream, true,
+                  E4m3Scales{false, 1.f, 1.f, 1.f}, Window{true, window, sinks});
+}
+
+int te_attn_window_bwd_sbhd(const void* q, const void* k, const void* v, const void* out, const void* dout,
+                            const float* lse, void* dq, void* dk, void* dv, const int32_t* cu_seqlens_q,
+                            const int32_t* cu_seqlens_kv, int batch, int seq_q, int seq_kv, int hq, int hkv,
+                            int d, float attn_scale, int mask_type, int window, int sinks, int dtype,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  const int tq = sbhd_rows(batch, seq_q), tk = sbhd_rows(batch, seq_kv);
+  if (tq < 0 || tk < 0) return fail(TE_ERR_INVALID_ARG, "batch >= 1, seq_q/seq_kv >= 0, rows < 2^31");
+  return bwd_impl(q, k, v, out, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q, cu_seqlens_kv,
+                  batch, tq, tk, hq, hkv, d, attn_scale, mask_type, dtype, workspace, workspace_bytes, stream,
+                  nullptr, true, false, Window{true, window, sinks});
 }
 
 int te_attn_read_status(const void* workspace, int* status, void* stream) {

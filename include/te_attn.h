@@ -267,6 +267,43 @@ int te_attn_fwd_thd_e4m3(const void* q, const void* k, const void* v, void* out,
                          void* stream);
 
 /*
+ * Sliding windows with sinks (no counterpart in the pages): te_attn_fwd_thd / _bwd_thd and the
+ * sequence-major forms, of queries that see the last `window` keys up to their own position
+ * and the first `sinks` keys of the sequence. Query i, at key position p = i (upper-left mask)
+ * or p = i + Lk - Lq (lower-right), sees key j <= p iff p - j < window or j < sinks.
+ * window >= 1, sinks >= 0 (TE_ERR_INVALID_ARG otherwise); mask_type one of the causal ones and
+ * fewer than 2^30 rows (TE_ERR_UNSUPPORTED otherwise). Key tiles that no query of a tile sees
+ * are not visited, so the time is that of the window, not of the sequence.
+ * Everything else, the workspaces' sizes among it, is as for those entry points. A real query
+ * that sees no key (upper-left, a window or more behind the last key, without sinks) gets
+ * out = 0, lse = -inf, dq = 0; keys that no query sees get exact zeros in dk and dv.
+ */
+int te_attn_window_fwd_thd(const void* q, const void* k, const void* v, void* out, float* lse,
+                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                           const int32_t* cu_seqlens_q_padded, const int32_t* cu_seqlens_kv_padded,
+                           int batch, int total_q, int total_kv, int hq, int hkv, int d,
+                           float attn_scale, int mask_type, int window, int sinks, int dtype,
+                           void* workspace, size_t workspace_bytes, void* stream);
+int te_attn_window_bwd_thd(const void* q, const void* k, const void* v, const void* out,
+                           const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                           const int32_t* cu_seqlens_q_padded, const int32_t* cu_seqlens_kv_padded,
+                           int batch, int total_q, int total_kv, int hq, int hkv, int d,
+                           float attn_scale, int mask_type, int window, int sinks, int dtype,
+                           void* workspace, size_t workspace_bytes, void* stream);
+int te_attn_window_fwd_sbhd(const void* q, const void* k, const void* v, void* out, float* lse,
+                            const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv, int batch,
+                            int seq_q, int seq_kv, int hq, int hkv, int d, float attn_scale,
+                            int mask_type, int window, int sinks, int dtype, void* workspace,
+                            size_t workspace_bytes, void* stream);
+int te_attn_window_bwd_sbhd(const void* q, const void* k, const void* v, const void* out,
+                            const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                            const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv, int batch,
+                            int seq_q, int seq_kv, int hq, int hkv, int d, float attn_scale,
+                            int mask_type, int window, int sinks, int dtype, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
  * Rotary positions (no counterpart in the pages; attention itself takes q and k as they
  * are). Each head's first rot = 2 * n_freq elements are n_freq pairs; pair c of token i
  * of sequence b is turned by the angle a = (start_positions[b] + i) * inv_freq[c]:
