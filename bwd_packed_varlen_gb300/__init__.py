@@ -40,6 +40,9 @@ from ._binding import (  # noqa: F401
     bwd_fused_workspace_size,
     library,
     library_path,
+    paged_append,
+    paged_cache,
+    paged_gather,
     prefix_bwd,
     prefix_bwd_workspace_size,
     prefix_fwd,

@@ -103,6 +103,8 @@ def library(debug: bool = None) -> ctypes.CDLL:
     L.te_attn_window_fwd_sbhd.argtypes = [vp] * 7 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
     L.te_attn_window_bwd_sbhd.restype = i32
     L.te_attn_window_bwd_sbhd.argtypes = [vp] * 11 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
+    for name in ("te_attn_paged_append", "te_attn_paged_gather"):  # (called through the extension module)
+        getattr(L, name).restype = i32
     L.te_attn_read_status.restype = i32
     L.te_attn_read_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int), vp]
     L.te_attn_last_error.restype = ctypes.c_char_p
@@ -468,7 +470,8 @@ _entries = {}  # addresses of the entry points, per build
 
 
 def _entry_points():
-    """(rope_thd, rope_sbhd, prefix_fwd, its size, prefix_bwd, its size) of the selected build."""
+    """(rope_thd, rope_sbhd, prefix_fwd, its size, prefix_bwd, its size, paged_append, paged_gather) of the
+    selected build."""
     global _host
     L = library()
     if _host is None:
@@ -479,7 +482,7 @@ def _entry_points():
         _host = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(_host)
     names = ("rope_thd", "rope_sbhd", "prefix_fwd_thd", "prefix_fwd_workspace_size", "prefix_bwd_thd",
-             "prefix_bwd_workspace_size")
+             "prefix_bwd_workspace_size", "paged_append", "paged_gather")
     _entries[_use_debug] = tuple(ctypes.cast(getattr(L, "te_attn_" + n), ctypes.c_void_p).value for n in names)
     return _entries[_use_debug]
 
@@ -544,6 +547,44 @@ def prefix_bwd(q, k, v, k_prefix, v_prefix, out, dout, lse, cu_seqlens_q, cu_seq
         e[4], e[5], q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
         cu_seqlens_kv_padded, prefix_len, attn_scale, _mask(mask_type), out, dout, lse, dq, dk, dv, dk_prefix,
         dv_prefix, workspace, stream))
+
+
+def paged_cache(num_pages, page_size, hkv, d, dtype=torch.bfloat16, bits=16, device="cuda"):
+    """An empty paged cache, ``(k_cache, v_cache)``, as the ``paged_`` calls take it. 16 bits: tensors
+    ``[num_pages, hkv, page_size, d]``. 4 bits: each a pair of codes, uint8 ``[num_pages, hkv, page_size,
+    d / 2]``, and steps and least values, ``[num_pages, hkv, page_size, d / 32, 2]`` of ``dtype``."""
+    if bits not in (4, 16):
+        raise ValueError("bits must be 4 or 16")
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float16 or bfloat16")
+    lead = (int(num_pages), int(hkv), int(page_size))
+    if bits == 16:
+        return tuple(torch.zeros(*lead, int(d), dtype=dtype, device=device) for _ in range(2))
+    if d % 32:
+        raise ValueError("a cache of 4 bits needs a head dim that is a multiple of 32")
+    return tuple((torch.zeros(*lead, d // 2, dtype=torch.uint8, device=device),
+                  torch.zeros(*lead, d // 32, 2, dtype=dtype, device=device)) for _ in range(2))
+
+
+def paged_append(q, k, v, k_cache, v_cache, page_table, past, cu_seqlens, cu_seqlens_padded, inv_freq=None, interleaved=False,
+                 mscale=1.0, q_out=None, status=None, stream=None):
+    """``te_attn_paged_append``: writes the new keys and values ``k, v [T, hkv, d]`` of packed sequences
+    behind the ``past`` tokens (int32 ``[B]``) that the paged cache holds of each, and turns ``q [T, hq, d]``
+    (or None) and the keys by their positions on the way, as :func:`rope` does (``inv_freq=None``: not at
+    all). The caches are written in place; returns the turned queries (None without ``q``). ``page_table``:
+    int32 ``[B, pages of a sequence]``. ``status``: None, or an int32 on the device for the call's status bits."""
+    e = _entries.get(_use_debug) or _entry_points()
+    return _result(_host.paged_append(e[6], k_cache, v_cache, page_table, q, k, v, past, cu_seqlens, cu_seqlens_padded,
+                                      inv_freq, interleaved, mscale, q_out, status, stream))
+
+
+def paged_gather(k_cache, v_cache, page_table, start, cu_seqlens, cu_seqlens_padded, total, k=None, v=None, status=None,
+                 stream=None):
+    """``te_attn_paged_gather``: the cached keys and values of positions ``start_b .. start_b + n_b - 1`` as
+    packed tensors ``(k, v) [total, hkv, d]``, of 4 bits the values that the codes stand for."""
+    e = _entries.get(_use_debug) or _entry_points()
+    return _result(_host.paged_gather(e[7], k_cache, v_cache, page_table, start, cu_seqlens, cu_seqlens_padded, total, k, v,
+                                      status, stream))
 
 
 def read_status(workspace, stream=None) -> int:

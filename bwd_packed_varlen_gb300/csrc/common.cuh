@@ -43,6 +43,8 @@ constexpr int kStatusTimeout = 2;
 constexpr int kStatusOutOfBounds = 4;
 constexpr int kStatusInternal = 8;  // a kernel found its launch unusable (e.g. misaligned shared memory)
 
+constexpr int kStatusBadPages = 16;  // a page outside the cache, or a position behind the page table
+
 // Bounds checks of computed global offsets. In the debug build of the library
 // (TEATTN_DEBUG_BOUNDS defined) a failed check records kStatusOutOfBounds in the
 // call's status word and the caller skips the access; in the release build the

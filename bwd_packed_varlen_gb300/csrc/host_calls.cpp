@@ -1,4 +1,4 @@
-// Host side of the rotary and shared-prefix calls, as a Python extension module.
+// Host side of the rotary, shared-prefix and paged calls, as a Python extension module.
 //
 // A decoding step's kernels take 6 to 20 microseconds, and checking the arguments, allocating
 // the outputs and marshalling thirty values from Python took 15 to 30 of them before each.
@@ -313,6 +313,168 @@ PyObject* rope(PyObject* const* a) {
   return with_k ? pack({&qo, &*ko}) : pack({&qo}, true);
 }
 
+constexpr const char* kCacheForm =
+    "k_cache and v_cache must be [pages, hkv, page_size, d] of float16 or bfloat16, or pairs of uint8 codes "
+    "[pages, hkv, page_size, d / 2] and steps and least values [pages, hkv, page_size, d / 32, 2], whole pages contiguous";
+
+// A paged cache from (k_cache, v_cache, page_table): tensors of 16 bits, or pairs of codes and
+// their steps and least values.
+struct Cache {
+  te_attn_paged_cache c{};
+  const at::Tensor* first;  // of the cache's dtype
+  int batch;
+
+  explicit Cache(PyObject* const* o) {
+    const bool four = PyTuple_Check(o[0]) || PyList_Check(o[0]);
+    const at::Tensor *data[2], *meta[2] = {nullptr, nullptr};
+    for (int i = 0; i < 2; ++i) {
+      if (four) {
+        need((PyTuple_Check(o[i]) || PyList_Check(o[i])) && PySequence_Size(o[i]) == 2, kCacheForm);
+        PyObject** two = PySequence_Fast_ITEMS(o[i]);
+        data[i] = &tensor(two[0]);
+        meta[i] = &tensor(two[1]);
+      } else {
+        data[i] = &tensor(o[i]);
+      }
+    }
+    first = four ? meta[0] : data[0];
+    need(first->is_cuda(), kOneDevice);
+    const auto index = first->device().index();
+    c.dtype = dtype_code(*first);
+    need(c.dtype >= 0 && data[0]->dim() == 4, kCacheForm);
+    const int64_t pages = data[0]->size(0), heads = data[0]->size(1), size = data[0]->size(2);
+    const int64_t d = four ? 2 * data[0]->size(3) : data[0]->size(3);
+    int64_t strides[4] = {0, 0, 0, 0};
+    for (int i = 0; i < 2; ++i) {
+      need(on_device(*data[i], index) && (!four || on_device(*meta[i], index)), kOneDevice);
+      need(data[i]->sizes() == data[0]->sizes() && data[i]->scalar_type() == (four ? at::kByte : first->scalar_type()) &&
+               whole(*data[i]),
+           kCacheForm);
+      strides[i] = page_bytes(*data[i]);
+      if (four) {
+        const int64_t want[] = {pages, heads, size, d / 32, 2};
+        need(d % 32 == 0 && meta[i]->sizes() == at::IntArrayRef(want, 5) && meta[i]->scalar_type() == first->scalar_type() &&
+                 whole(*meta[i]),
+             kCacheForm);
+        strides[2 + i] = page_bytes(*meta[i]);
+      }
+    }
+    const at::Tensor& table = tensor(o[2]);
+    need(table.scalar_type() == at::kInt && table.dim() == 2 && on_device(table, index) &&
+             (table.size(1) <= 1 || table.stride(1) == 1),
+         "page_table must be int32 [batch, pages of a sequence] on the cache's device, its rows contiguous");
+    c.k = data[0]->mutable_data_ptr();
+    c.v = data[1]->mutable_data_ptr();
+    c.k_meta = four ? meta[0]->mutable_data_ptr() : nullptr;
+    c.v_meta = four ? meta[1]->mutable_data_ptr() : nullptr;
+    c.k_stride = strides[0];
+    c.v_stride = strides[1];
+    c.k_meta_stride = strides[2];
+    c.v_meta_stride = strides[3];
+    c.page_table = table.const_data_ptr<int32_t>();
+    batch = as_int(table.size(0));
+    c.table_stride = batch > 1 ? table.stride(0) : 0;
+    c.num_pages = as_int(pages);
+    c.page_size = as_int(size);
+    c.max_pages = as_int(table.size(1));
+    c.hkv = as_int(heads);
+    c.d = as_int(d);
+  }
+
+ private:
+  // everything behind the first axis contiguous (axes of one element have no stride)
+  static bool whole(const at::Tensor& t) {
+    int64_t n = 1;
+    for (int64_t i = t.dim() - 1; i > 0; --i) {
+      if (t.size(i) > 1 && t.stride(i) != n) return false;
+      n *= t.size(i);
+    }
+    return true;
+  }
+  static int64_t page_bytes(const at::Tensor& t) {
+    int64_t n = t.element_size();
+    if (t.size(0) > 1) return t.stride(0) * n;
+    for (int64_t i = 1; i < t.dim(); ++i) n *= t.size(i);
+    return (n + 15) / 16 * 16;
+  }
+};
+
+// One int32 for the call's status bits, or None.
+int32_t* status_word(PyObject* o, c10::DeviceIndex index) {
+  if (!given(o)) return nullptr;
+  const at::Tensor& t = tensor(o);
+  need(t.scalar_type() == at::kInt && t.numel() == 1 && on_device(t, index), "status must be one int32 on the cache's device");
+  return t.mutable_data_ptr<int32_t>();
+}
+
+// (entry point, k_cache, v_cache, page_table, q or None, k, v, past, cu_seqlens, padded ones, inv_freq or None, interleaved,
+// mscale, q_out, status, stream)
+PyObject* paged_append(PyObject* const* a) {
+  const Cache cache(a + 1);
+  const auto index = cache.first->device().index();
+  const bool with_q = given(a[4]), turn = given(a[10]);
+  const at::Tensor &k = tensor(a[5]), &v = tensor(a[6]);
+  const at::Tensor& q = with_q ? tensor(a[4]) : k;
+  const auto type = cache.first->scalar_type();
+  need(on_device(q, index) && on_device(k, index) && on_device(v, index), kOneDevice);
+  for (const at::Tensor* x : {&q, &k, &v})
+    need(x->scalar_type() == type && x->dim() == 3 && x->size(0) == k.size(0) && x->size(2) == cache.c.d &&
+             (x->numel() == 0 || x->stride(2) == 1),
+         "q, k and v must be [T, heads, d] of the cache's dtype, with adjacent elements in a head");
+  need(k.size(1) == cache.c.hkv && v.size(1) == cache.c.hkv, "k and v must have the cache's heads");
+  need(with_q || !given(a[13]), "q_out without q");
+  const at::Tensor* w = turn ? &tensor(a[10]) : nullptr;
+  if (turn)
+    need(w->scalar_type() == at::kDouble && w->dim() == 1 && w->is_contiguous() && on_device(*w, index),
+         "inv_freq must be a contiguous float64 vector");
+  const int batch = cache.batch;
+  const int32_t* past = lengths(a[7], batch, index);
+  const int32_t *cu = lengths(a[8], batch + int64_t{1}, index), *pad = lengths(a[9], batch + int64_t{1}, index);
+  const int interleaved = PyObject_IsTrue(a[11]);
+  if (interleaved < 0) throw python_error();
+  const float mscale = static_cast<float>(number(a[12]));
+  int32_t* status = status_word(a[14], index);
+  auto stride = [](const at::Tensor& x, int64_t dim) { return x.size(dim) > 1 ? x.stride(dim) : 0; };
+  const int hq = with_q ? as_int(q.size(1)) : 0, total = as_int(k.size(0)), freqs = turn ? as_int(w->numel()) : 0;
+  const Place place(index, a[15]);
+  std::optional<Output> qo;
+  if (with_q) qo.emplace(a[13], q.sizes(), q, type, "q_out must be contiguous, with the shape, dtype and device of q");
+  const void* q_at = with_q ? q.const_data_ptr() : nullptr;
+  void* qo_at = with_q ? qo->at() : nullptr;
+  const auto fn = reinterpret_cast<decltype(&te_attn_paged_append)>(address(a[0]));
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = fn(&cache.c, q_at, k.const_data_ptr(), v.const_data_ptr(), qo_at, turn ? w->const_data_ptr<double>() : nullptr, freqs,
+          cu, pad, past, batch, total, hq, with_q ? stride(q, 0) : 0, with_q ? stride(q, 1) : 0, stride(k, 0), stride(k, 1),
+          stride(v, 0), stride(v, 1), interleaved, mscale, status, place.stream());
+  Py_END_ALLOW_THREADS;
+  if (rc != 0) return PyLong_FromLong(rc);
+  return with_q ? qo->result() : Py_NewRef(Py_None);
+}
+
+// (entry point, k_cache, v_cache, page_table, start, cu_seqlens, padded ones, total, k, v, status, stream)
+PyObject* paged_gather(PyObject* const* a) {
+  const Cache cache(a + 1);
+  const auto index = cache.first->device().index();
+  const int batch = cache.batch;
+  const int32_t* start = lengths(a[4], batch, index);
+  const int32_t *cu = lengths(a[5], batch + int64_t{1}, index), *pad = lengths(a[6], batch + int64_t{1}, index);
+  const long total = integer(a[7]);
+  need(total >= 0 && total <= INT_MAX, "total must lie in [0, 2^31)");
+  int32_t* status = status_word(a[10], index);
+  const Place place(index, a[11]);
+  const int64_t shape[] = {total, cache.c.hkv, cache.c.d};
+  constexpr const char* what = "k and v must be contiguous [total, hkv, d] of the cache's dtype, on its device";
+  const Output k(a[8], at::IntArrayRef(shape, 3), *cache.first, cache.first->scalar_type(), what);
+  const Output v(a[9], at::IntArrayRef(shape, 3), *cache.first, cache.first->scalar_type(), what);
+  const auto fn = reinterpret_cast<decltype(&te_attn_paged_gather)>(address(a[0]));
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = fn(&cache.c, k.at(), v.at(), cu, pad, start, batch, static_cast<int>(total), status, place.stream());
+  Py_END_ALLOW_THREADS;
+  return rc != 0 ? PyLong_FromLong(rc) : pack({&k, &v});
+}
+
 template <PyObject* (*kCall)(PyObject* const*), Py_ssize_t kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -333,6 +495,8 @@ PyMethodDef methods[] = {
     {"prefix_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<prefix_fwd, 18>)), METH_FASTCALL, nullptr},
     {"prefix_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<prefix_bwd, 24>)), METH_FASTCALL, nullptr},
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<rope, 13>)), METH_FASTCALL, nullptr},
+    {"paged_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<paged_append, 16>)), METH_FASTCALL, nullptr},
+    {"paged_gather", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<paged_gather, 12>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_teattn_host", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

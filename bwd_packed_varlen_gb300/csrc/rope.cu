@@ -27,7 +27,7 @@
 #include "../../include/te_attn.h"
 #include "api_internal.h"
 #include "common.cuh"
-#include "sm103_ptx.cuh"
+#include "rope.cuh"
 
 namespace teattn {
 
@@ -50,11 +50,6 @@ struct RopeParams {
 
 constexpr int kRopeThreads = 256, kRopeTokens = 4;
 constexpr int kRopeSMs = 152;  // of the GPU that work is cut for
-
-// n / d with inv = ceil(2^32 / d), exact for n d < 2^32.
-__device__ __forceinline__ int div_by(int n, uint32_t inv, int d) {
-  return d == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), inv));
-}
 
 // Position of row r, or *real = false for a row that holds no token. A whole warp works on
 // one row: the lanes count the sequences that start at or before it, one trip to memory
@@ -81,46 +76,6 @@ __device__ __forceinline__ long long rope_position(const RopeParams& p, int r, b
   if (i < 0 || i >= p.cu[b + 1] - p.cu[b]) return 0;
   *real = true;
   return static_cast<long long>(p.start ? p.start[b] : 0) + i;
-}
-
-// V consecutive 16-bit elements.
-template <int V>
-struct Vec;
-template <>
-struct Vec<8> { using type = uint4; };
-template <>
-struct Vec<4> { using type = uint2; };
-template <>
-struct Vec<2> { using type = uint32_t; };
-template <>
-struct Vec<1> { using type = uint16_t; };
-
-template <int V, bool kBF16>
-__device__ __forceinline__ void widen(typename Vec<V>::type v, float (&f)[V]) {
-  if constexpr (V == 1) {
-    f[0] = kBF16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
-  } else {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const float2 x = unpack2<kBF16>(w[i]);
-      f[2 * i] = x.x;
-      f[2 * i + 1] = x.y;
-    }
-  }
-}
-
-template <int V, bool kBF16>
-__device__ __forceinline__ typename Vec<V>::type narrow(const float (&f)[V]) {
-  typename Vec<V>::type v;
-  if constexpr (V == 1) {
-    v = kBF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f[0])) : __half_as_ushort(__float2half_rn(f[0]));
-  } else {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) w[i] = pack2<kBF16>(f[2 * i], f[2 * i + 1]);
-  }
-  return v;
 }
 
 // kHalf: pairs (c, c + rot/2), a rotated unit is V pairs in two accesses; otherwise pairs
@@ -182,14 +137,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   __syncthreads();
   const int per = half / units;  // pairs of a unit
   for (int c = tid; c < half; c += kRopeThreads) {
-    const double turns = p.inv_freq[c] * 0.15915494309189535;  // 1 / (2 pi)
-    const unsigned long long step =
-        static_cast<unsigned long long>((turns - floor(turns)) * 18446744073709551616.0);
+    const unsigned long long step = turn_per_position(p.inv_freq[c]);
     const int u = c / per, at = (c - u * per) * units + u;
     for (int t = 0; t < nt; ++t) {
-      const long long frac = static_cast<long long>(static_cast<unsigned long long>(s_pos[t]) * step);
       float sn, cs;
-      sincospif(static_cast<float>(frac) * 1.0842021724855044e-19f, &sn, &cs);  // 2^-63: half turns
+      sincos_at(s_pos[t], step, &sn, &cs);
       s_cs[t * half + at] = make_float2(cs * p.mscale, sn * p.mscale * p.sign);
     }
   }

@@ -123,6 +123,9 @@ extern "C" {
 /* A kernel found its launch unusable (shared memory not 1024-byte aligned); it
    returned without computing and the outputs of the call are undefined. */
 #define TE_STATUS_INTERNAL 8
+/* Paged calls: a page that the call needs lies outside the cache, or a position behind the
+   page table's last page; what is there is not read (its keys are not seen) or written. */
+#define TE_STATUS_BAD_PAGES 16
 
 /* Library version, major * 10000 + minor * 100 + patch. */
 int te_attn_version(void);
@@ -398,6 +401,67 @@ int te_attn_prefix_bwd_thd(const void* q, const void* k, const void* v, const vo
                            int batch, int total_q, int total_kv, int prefix_rows, int hq, int hkv,
                            int d, float attn_scale, int mask_type, int dtype, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/*
+ * Paged key/value caches (no counterpart in the pages). The keys and values of a batch's
+ * sequences lie in pages of page_size tokens, in any order: position t of sequence b is token
+ * t % page_size of page page_table[b * table_stride + t / page_size].
+ *   16 bits: k, v  [num_pages, hkv, page_size, d], the batch's dtype.
+ *   4 bits:  k, v  [num_pages, hkv, page_size, d / 2] bytes, two codes each (the earlier
+ *            element in the low half), and k_meta, v_meta [num_pages, hkv, page_size, d / 32, 2]
+ *            of the batch's dtype: step s and least value m of every 32 elements. An element's
+ *            value is s * code + m, rounded to the dtype. d a multiple of 32. Storing: m is
+ *            the least of the 32, s = (greatest - m) / 15 rounded towards zero to 16 bits,
+ *            code = (x - m) / s rounded to the nearest of 0..15, ties to even; 32 elements among
+ *            which is a NaN or an infinity read as NaN.
+ * A page is contiguous; strides from page to page, in bytes, are multiples of 16 (k_meta,
+ * v_meta: of 4) and pointers are aligned to 16 bytes, so that layers, or keys and values, may
+ * lie side by side. page_size is a power of two in [16, 4096], d a multiple of 8 in [8, 256].
+ * Entries of the page table beside those that a call needs are not looked at. No two live
+ * positions may share a place.
+ */
+typedef struct te_attn_paged_cache {
+  void* k;
+  void* v;
+  void* k_meta; /* NULL: 16 bits */
+  void* v_meta;
+  int64_t k_stride, v_stride, k_meta_stride, v_meta_stride;
+  const int32_t* page_table;
+  int64_t table_stride; /* entries from sequence to sequence */
+  int num_pages, page_size;
+  int max_pages; /* entries of a sequence */
+  int hkv, d, dtype;
+} te_attn_paged_cache;
+
+/*
+ * Appends new tokens to the cache, with their positions put in on the way: token i of
+ * sequence b stands at position past[b] + i (past: int32 [batch], the tokens that the cache
+ * holds before the call). q and k are turned as te_attn_rope_thd turns them (n_freq pairs;
+ * n_freq = 0 and inv_freq NULL: not at all); turned queries go to q_out [total, hq, d], turned
+ * keys, and v as it is, to the cache. Keys are rounded to 16 bits before they are stored in 4.
+ * q, k, v: [total, h, d] with any non-negative strides as there, slices of a fused projection
+ * among them; q_out may be q. hq = 0: no queries. Rows of q_out that are no token become zeros;
+ * places of the cache that are no new token's are left as they are. A sequence whose lengths are
+ * inconsistent or whose past is negative counts as empty.
+ * `status`: NULL, or one int32 on the device that is set to the call's TE_STATUS_* bits.
+ * No workspace; deterministic; capturable.
+ */
+int te_attn_paged_append(const te_attn_paged_cache* cache, const void* q, const void* k,
+                         const void* v, void* q_out, const double* inv_freq, int n_freq,
+                         const int32_t* cu_seqlens, const int32_t* cu_seqlens_padded,
+                         const int32_t* past, int batch, int total, int hq, int64_t q_stride_t,
+                         int64_t q_stride_h, int64_t k_stride_t, int64_t k_stride_h,
+                         int64_t v_stride_t, int64_t v_stride_h, int interleaved, float mscale,
+                         int32_t* status, void* stream);
+
+/*
+ * The cached keys and values of positions start[b] .. start[b] + n_b - 1 as packed tensors
+ * k, v [total, hkv, d], 16 bits (n_b and the rows from cu_seqlens and cu_seqlens_padded). Rows
+ * that are no token, or whose page is outside the cache, become zeros. `status` as above.
+ */
+int te_attn_paged_gather(const te_attn_paged_cache* cache, void* k, void* v,
+                         const int32_t* cu_seqlens, const int32_t* cu_seqlens_padded,
+                         const int32_t* start, int batch, int total, int32_t* status, void* stream);
 
 /*
  * Synchronises `stream`, then copies the device status word of the last call that
