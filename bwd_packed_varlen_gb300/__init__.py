@@ -42,6 +42,8 @@ from ._binding import (  # noqa: F401
     library_path,
     paged_append,
     paged_cache,
+    paged_fwd,
+    paged_fwd_workspace_size,
     paged_gather,
     prefix_bwd,
     prefix_bwd_workspace_size,

@@ -103,7 +103,9 @@ def library(debug: bool = None) -> ctypes.CDLL:
     L.te_attn_window_fwd_sbhd.argtypes = [vp] * 7 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
     L.te_attn_window_bwd_sbhd.restype = i32
     L.te_attn_window_bwd_sbhd.argtypes = [vp] * 11 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
-    for name in ("te_attn_paged_append", "te_attn_paged_gather"):  # (called through the extension module)
+    L.te_attn_paged_fwd_workspace_size.restype = sz
+    L.te_attn_paged_fwd_workspace_size.argtypes = [i32] * 6
+    for name in ("te_attn_paged_append", "te_attn_paged_gather", "te_attn_paged_fwd_thd"):  # (called through the extension module)
         getattr(L, name).restype = i32
     L.te_attn_read_status.restype = i32
     L.te_attn_read_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int), vp]
@@ -470,8 +472,8 @@ _entries = {}  # addresses of the entry points, per build
 
 
 def _entry_points():
-    """(rope_thd, rope_sbhd, prefix_fwd, its size, prefix_bwd, its size, paged_append, paged_gather) of the
-    selected build."""
+    """(rope_thd, rope_sbhd, prefix_fwd, its size, prefix_bwd, its size, paged_append, paged_gather, paged_fwd,
+    its size) of the selected build."""
     global _host
     L = library()
     if _host is None:
@@ -482,7 +484,7 @@ def _entry_points():
         _host = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(_host)
     names = ("rope_thd", "rope_sbhd", "prefix_fwd_thd", "prefix_fwd_workspace_size", "prefix_bwd_thd",
-             "prefix_bwd_workspace_size", "paged_append", "paged_gather")
+             "prefix_bwd_workspace_size", "paged_append", "paged_gather", "paged_fwd_thd", "paged_fwd_workspace_size")
     _entries[_use_debug] = tuple(ctypes.cast(getattr(L, "te_attn_" + n), ctypes.c_void_p).value for n in names)
     return _entries[_use_debug]
 
@@ -585,6 +587,20 @@ def paged_gather(k_cache, v_cache, page_table, start, cu_seqlens, cu_seqlens_pad
     e = _entries.get(_use_debug) or _entry_points()
     return _result(_host.paged_gather(e[7], k_cache, v_cache, page_table, start, cu_seqlens, cu_seqlens_padded, total, k, v,
                                       status, stream))
+
+
+def paged_fwd_workspace_size(batch, total_q, hq, hkv, d, bits=16) -> int:
+    return int(library().te_attn_paged_fwd_workspace_size(batch, total_q, hq, hkv, d, bits))
+
+
+def paged_fwd(q, k_cache, v_cache, page_table, past, cu_seqlens_q, cu_seqlens_q_padded, attn_scale, window=0, sinks=0, out=None,
+              lse=None, workspace=None, stream=None):
+    """``te_attn_paged_fwd_thd``: attention of packed queries ``q [T_q, hq, d]`` over a paged cache in 16 or 4
+    bits. Query i of sequence b stands at position ``past[b] + i`` and sees the keys up to it (append them
+    first), or with ``window`` the last ``window`` of them and the first ``sinks``; returns ``(out, lse)``."""
+    e = _entries.get(_use_debug) or _entry_points()
+    return _result(_host.paged_fwd(e[8], e[9], k_cache, v_cache, page_table, q, past, cu_seqlens_q, cu_seqlens_q_padded, attn_scale,
+                                   _int32(window), _int32(sinks), out, lse, workspace, stream))
 
 
 def read_status(workspace, stream=None) -> int:

@@ -1,0 +1,788 @@
+// Attention of few queries over a paged cache, in 16 or in 4 bits.
+//
+//   S = scale q K^T over the keys that a query sees,  O = softmax(S) V,  LSE = log sum exp S
+//
+// A decoding step reads every cached key and value once and does next to nothing with it, so
+// what counts is to keep loads in flight everywhere and all the time. The work is a line of
+// units (16 or 32 keys of one sequence, kv head and row tile), cut into equal slices, one for
+// each warp of the grid: no warp waits for another, and a long cache is spread over the GPU as
+// evenly as many short ones. A warp copies its units into a ring of its own in shared memory
+// (TMA; no role but its own, no barrier across warps) and multiplies them with the warp-wide
+// tensor instructions, keys as the rows of the tile:
+//   S^T = K Q^T  (16 keys x 8 rows a product), P^T = exp2(S^T scale log2e - m), O^T += V^T P^T,
+// since a kv head's group has 8 rows or a few more in one step: with queries as the 128 rows of
+// a tcgen05 tile 120 would be empty, with 16-row query tiles half. P^T comes out of the scores'
+// registers in the place where the second product wants it but transposed (movmatrix).
+// The offset m is raised only when a score exceeds it by more than 2^8; sums of P stay in each
+// lane until the end. P is rounded to 16 bits for the product, everything else is fp32.
+//
+// 4 bits: a lane takes a word of eight codes of a key, spreads it into pairs, takes the magic
+// number off and applies step and least value with one fused multiply-add a pair: exactly the
+// 16-bit values that the codes stand for, in registers, so that shared memory sees the 4 bits only.
+// Which element of a head goes to which place of a product is free as long as Q and K, or V and
+// O, agree; the places are chosen so that a lane's word feeds its own registers.
+//
+// Slices cut sequences anywhere. A warp that has a whole segment (sequence, row tile, head)
+// writes its rows; the others leave maximum, sum and unnormalised output in fp32, which a second
+// kernel joins in the order of the keys, and which also writes zeros to rows that hold no token.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+
+#include "attn_paged.cuh"
+#include "common.cuh"
+#include "pdl.cuh"
+#include "sm103_ptx.cuh"
+#include "tmap.h"
+
+namespace teattn {
+
+template <int kD, int kNT, bool k4>
+struct RowsShape {
+  static constexpr int kRows = 8 * kNT;
+  static constexpr int kBlocks = k4 || kD == 64 ? 2 : 1;  // 16-key blocks of a unit
+  static constexpr int kUnit = 16 * kBlocks;
+  static constexpr int kWarps = k4 ? (kD == 256 ? 6 : 12) : (kD == 256 ? 4 : 8);
+  // (a 4-bit ring is laid out for kD elements a row, whatever d is)
+  static constexpr int kDataBytes = kUnit * (k4 ? kD / 2 : 2 * kD);  // keys or values of a unit
+  static constexpr int kMetaBytes = k4 ? kUnit * kD / 8 : 0;
+  static constexpr int kStageBytes = 2 * (kDataBytes + kMetaBytes);
+  static constexpr int kStages = 3;
+  static constexpr int kSmem = kWarps * kStages * kStageBytes + 1024;
+  static_assert(kSmem <= 208 * 1024, "shared memory budget");
+};
+
+struct RowsMaps {
+  CUtensorMap k, v;  // boxes of 64 columns and a 16-key block's rows (16 bits only)
+};
+
+__device__ __forceinline__ float ex2r(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool kBF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (kBF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool kTrans>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  if constexpr (kTrans)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The four pairs (i, i + 4) of a word's codes as values.
+template <bool kBF16>
+__device__ __forceinline__ void pairs_of(uint32_t w, uint32_t step2, uint32_t least2, uint32_t (&r)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = value_pair<kBF16>(code_pair<kBF16>((w >> (4 * i)) & 0x000f000fu), step2, least2);
+}
+
+// One stretch of units of one segment, as the cursors of loads and of products go through them.
+struct Stretch {
+  int b, head, tile;   // sequence, kv head, row tile
+  int u0, n;           // units [u0, u0 + n) of the segment's `all`
+  int all;
+  PagedSeq s;
+  PagedRun run;
+};
+
+// Stretch that begins at place `at` of the line, ending at `end` at the latest.
+template <int kRows, int kUnit>
+__device__ __forceinline__ Stretch stretch_at(const PagedParams& p, const long long* pref, long long at, long long end) {
+  Stretch t;
+  int lo = 0, hi = p.batch - 1;  // the last sequence that begins at or before it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pref[mid] <= at) lo = mid; else hi = mid - 1;
+  }
+  t.b = lo;
+  t.s = load_paged_seq(p, lo);
+  t.run = paged_run(p, t.s, kUnit);
+  t.all = t.run.n;
+  const long long r = at - pref[lo];
+  const int seg = static_cast<int>(r / t.all);
+  t.u0 = static_cast<int>(r - static_cast<long long>(seg) * t.all);
+  t.tile = seg / p.hkv;
+  t.head = seg - t.tile * p.hkv;
+  const long long left = end - at;
+  t.n = left < t.all - t.u0 ? static_cast<int>(left) : t.all - t.u0;
+  return t;
+}
+
+// Prefix sums of the sequences' units in `pref` (shared memory, batch + 1 values), by the whole
+// block; returns the total.
+template <int kRows, int kUnit>
+__device__ long long sum_units(const PagedParams& p, long long* pref, int* status) {
+  __shared__ long long warp_sum[32];
+  __shared__ long long carry;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  if (tid == 0) carry = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int base = 0; base < p.batch; base += blockDim.x) {
+    const int b = base + tid;
+    long long w = 0;
+    if (b < p.batch) {
+      const PagedSeq s = load_paged_seq(p, b);
+      if (!s.ok) atomicOr(status, kStatusBadSeqlens);
+      const long long tiles = (static_cast<long long>(s.n) * p.group + kRows - 1) / kRows;
+      w = tiles * p.hkv * paged_run(p, s, kUnit).n;
+    }
+    long long x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    long long before = carry, all = 0;
+    for (int i = 0; i < nw; ++i) {
+      if (i < warp) before += warp_sum[i];
+      all += warp_sum[i];
+    }
+    if (b < p.batch) pref[b] = before + x - w;
+    __syncthreads();
+    if (tid == 0) carry += all;
+    __syncthreads();
+  }
+  const long long total = carry;
+  if (tid == 0) pref[p.batch] = total;
+  __syncthreads();
+  return total;
+}
+
+// Units of a slice: equal for all warps, four at least (a warp needs a microsecond before its
+// first product, and what it leaves has to be joined).
+constexpr int kLeastUnits = 4;
+__device__ __forceinline__ long long slice_units(long long total, int warps) {
+  const long long per = (total + warps - 1) / warps;
+  return per < kLeastUnits ? kLeastUnits : per;
+}
+
+template <int kD, int kNT, bool kBF16, bool k4>
+__global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
+    paged_rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ RowsMaps tm) {
+  using S = RowsShape<kD, kNT, k4>;
+  constexpr int kRows = S::kRows, kUnit = S::kUnit, kBlocks = S::kBlocks, NS = S::kStages, kSteps = kD / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  long long* pref = reinterpret_cast<long long*>(smem + S::kWarps * NS * S::kStageBytes);  // [batch + 1]
+  __shared__ uint64_t bar[S::kWarps][NS];
+  __shared__ uint32_t s_seen[S::kWarps][NS];  // bit k: block k of the unit was loaded
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int warps = gridDim.x * S::kWarps;
+  // neighbouring slices on different SMs, so that few of them still use all
+  const int mine = warp * gridDim.x + blockIdx.x;
+  // a word of its own for each warp's status, which the join collects: no launch ahead of this
+  // one has to clear a common one
+  int* status = p.warp_status + mine;
+  pdl_trigger();
+  if (lane == 0) {
+    *status = 0;
+    for (int i = 0; i < NS; ++i) mbar_init(&bar[warp][i], 1);
+    fence_barrier_init();
+  }
+  const long long total = sum_units<kRows, kUnit>(p, pref, status);
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= p.batch; b += blockDim.x) p.pref[b] = pref[b];
+  const long long per = slice_units(total, warps);
+  const long long begin = mine * per, end = begin + per < total ? begin + per : total;
+  if (begin >= end) return;
+
+  uint8_t* ring = smem + warp * NS * S::kStageBytes;
+  // ------------------------------------------------------------- loads
+  // Pages are looked up 32 blocks at a time, a batch ahead of its use.
+  constexpr int kBatch = 32 / kBlocks;  // units of a batch
+  struct Batch {
+    Stretch t;
+    int page;   // lane l: page of block l of the batch; -1: outside the cache
+    int first, n;  // units [first, first + n) of the segment
+  };
+  auto look_up = [&](Batch& x) {
+    const int u = x.first + lane / kBlocks;
+    x.page = -1;
+    if (lane / kBlocks < x.n) {
+      const int key = x.t.run.unit(u) * kUnit + lane % kBlocks * 16;
+      // (blocks of a unit that no query sees are not looked at)
+      if (key < x.t.s.past + x.t.s.n && (key + 16 > paged_first(p, x.t.s, 0) || key < p.sinks)) {
+        x.page = page_of(p.cache, x.t.b, key);
+        if (x.page < 0) atomicOr(status, kStatusBadPages);
+      }
+    }
+  };
+  auto batch_of = [&](const Stretch& t, int first) {
+    Batch x;
+    x.t = t;
+    x.first = first;
+    x.n = min(kBatch, t.u0 + t.n - first);
+    look_up(x);
+    return x;
+  };
+  const Stretch first_stretch = stretch_at<kRows, kUnit>(p, pref, begin, end);
+  Batch cur = batch_of(first_stretch, first_stretch.u0);
+  Batch nxt = cur;
+  long long looked = begin + cur.n;  // places looked up so far
+  auto prefetch = [&]() {
+    if (looked >= end) return;
+    if (cur.first + cur.n < cur.t.u0 + cur.t.n) {
+      nxt = batch_of(cur.t, cur.first + cur.n);
+    } else {
+      const Stretch t = stretch_at<kRows, kUnit>(p, pref, looked, end);
+      nxt = batch_of(t, t.u0);
+    }
+    looked += nxt.n;
+  };
+  prefetch();
+  int at = 0;  // unit of the current batch that is loaded next
+  int loaded = 0;
+  const long long units = end - begin;
+  const int slot_mask = (1 << p.cache.shift) - 1;
+  auto load_next = [&]() {
+    if (at == cur.n) {
+      cur = nxt;
+      at = 0;
+      prefetch();
+    }
+    const int st = loaded % NS;
+    uint8_t* dst = ring + st * S::kStageBytes;
+    const int key0 = cur.t.run.unit(cur.first + at) * kUnit;
+    uint32_t seen = 0;
+    int page[kBlocks];
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+      page[k] = __shfl_sync(0xffffffffu, cur.page, at * kBlocks + k);
+      if (page[k] >= 0) seen |= 1u << k;
+    }
+    if (lane == 0) {
+      s_seen[warp][st] = seen;
+      if constexpr (k4) {
+        const uint32_t row = p.cache.row_bytes, meta = p.d / 8;
+        mbar_arrive_expect_tx(&bar[warp][st], __popc(seen) * 2 * 16 * (row + meta));
+      } else {
+        mbar_arrive_expect_tx(&bar[warp][st], __popc(seen) * 2 * 16 * 2 * kD);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kBlocks; ++k) {
+      if (page[k] < 0) continue;
+      const int slot = (key0 + 16 * k) & slot_mask;
+      if constexpr (k4) {
+        if (lane < 4) {  // codes and steps of keys and of values
+          const int kv = lane & 1, is_meta = lane >> 1;
+          const long long row = page_row(p.cache, cur.t.head, slot);
+          const uint32_t bytes = is_meta ? p.d / 8 : p.cache.row_bytes;
+          const uint8_t* src = (is_meta ? p.cache.meta[kv] + page[k] * p.cache.meta_stride[kv]
+                                        : p.cache.data[kv] + page[k] * p.cache.stride[kv]) + row * bytes;
+          uint8_t* to = dst + (is_meta ? 2 * S::kDataBytes + kv * S::kMetaBytes : kv * S::kDataBytes) + k * 16 * bytes;
+          bulk_load(to, src, 16 * bytes, &bar[warp][st]);
+        }
+      } else {
+        constexpr int kChunks = kD / 64;
+        if (lane < 2 * kChunks) {
+          const int kv = lane / kChunks, c = lane % kChunks;
+          tma_load_4d(dst + kv * S::kDataBytes + c * kUnit * 128 + k * 16 * 128, kv ? &tm.v : &tm.k, &bar[warp][st], c * 64,
+                      slot, cur.t.head, page[k]);
+        }
+      }
+    }
+    ++at;
+    ++loaded;
+  };
+  while (loaded < NS && loaded < units) load_next();
+
+  // ------------------------------------------------------------- products
+  const float sl2 = p.scale_log2;
+  long long done = 0;
+  while (done < units) {
+    const Stretch t = stretch_at<kRows, kUnit>(p, pref, begin + done, end);
+    const int row0 = t.tile * kRows, rows = min(kRows, t.s.n * p.group - row0);
+    const int i0 = row0 / p.group, i1 = (row0 + rows - 1) / p.group;  // first and last query
+    const int sees_all = t.s.past + i0 + 1, sees = t.s.past + i1 + 1;  // keys below: of every row, of some
+    const int lo_some = paged_first(p, t.s, i0), lo_all = paged_first(p, t.s, i1);
+    const int sinks = p.window > 0 ? p.sinks : 0;
+    // this lane's rows of the scores: 8 nt + 2 t4, + 1
+    int hi[kNT][2], lo[kNT][2];
+    float m[kNT][2], l[kNT][2];
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * nt + 2 * t4 + e, i = (row0 + r) / p.group;
+        hi[nt][e] = r < rows ? t.s.past + i + 1 : 0;
+        lo[nt][e] = paged_first(p, t.s, i);
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+      }
+    // Q^T as the second operand: column g of n-tile nt is row 8 nt + g
+    uint32_t qf[kNT][kSteps][2];
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      const int r = 8 * nt + g, rr = row0 + min(r, rows - 1), i = rr / p.group, j = rr - i * p.group;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) +
+                          (static_cast<long long>(t.s.off + i) * p.hq + t.head * p.group + j) * p.d;
+      if constexpr (k4) {
+        // pairs (c, c + 4) of the eight elements that this lane's word of K holds
+#pragma unroll
+        for (int w = 0; w < kD / 32; ++w) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (w * 32 < p.d) v = *reinterpret_cast<const uint4*>(q + w * 32 + t4 * 8);
+          qf[nt][2 * w][0] = __byte_perm(v.x, v.z, 0x5410);
+          qf[nt][2 * w][1] = __byte_perm(v.x, v.z, 0x7632);
+          qf[nt][2 * w + 1][0] = __byte_perm(v.y, v.w, 0x5410);
+          qf[nt][2 * w + 1][1] = __byte_perm(v.y, v.w, 0x7632);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int c = 16 * s + 8 * e + 2 * t4;
+            qf[nt][s][e] = c < p.d ? *reinterpret_cast<const uint32_t*>(q + c) : 0u;
+          }
+      }
+    }
+    float o[kNT][kSteps][4];
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.f;
+
+#pragma unroll 1
+    for (int u = t.u0; u < t.u0 + t.n; ++u, ++done) {
+      const int it = static_cast<int>(done), st = it % NS;
+      if (!mbar_wait_warp(&bar[warp][st], (it / NS) & 1, status)) return;
+      const uint32_t stage = smem_u32(ring + st * S::kStageBytes);
+      const uint32_t loaded_blocks = s_seen[warp][st];
+      const int key0 = t.run.unit(u) * kUnit;
+      const bool some = loaded_blocks != 0 && key0 < sees && (key0 + kUnit > lo_some || key0 < sinks);
+      if (some) {
+        const bool full = loaded_blocks == (1u << kBlocks) - 1u && key0 + kUnit <= sees_all &&
+                          (key0 >= lo_all || key0 + kUnit <= sinks);
+        // ---- S^T
+        float sc[kBlocks][kNT][4];
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[k][nt][e] = 0.f;
+          if constexpr (k4) {
+            const uint32_t words = stage + (k * 16 + g) * p.cache.row_bytes + t4 * 4;
+            const uint32_t metas = stage + 2 * S::kDataBytes + (k * 16 + g) * (p.d / 8);
+#pragma unroll
+            for (int w = 0; w < kD / 32; ++w) {
+              if (w * 32 >= p.d) break;
+              uint32_t a[2][4];
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const uint32_t mt = lds32(metas + half * p.d + w * 4);
+                pairs_of<kBF16>(lds32(words + half * 8 * p.cache.row_bytes + w * 16), __byte_perm(mt, mt, 0x1010),
+                                __byte_perm(mt, mt, 0x3232), a[half]);
+              }
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t af[4] = {a[0][2 * x], a[1][2 * x], a[0][2 * x + 1], a[1][2 * x + 1]};
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(sc[k][nt], af, qf[nt][2 * w + x][0], qf[nt][2 * w + x][1]);
+              }
+            }
+          } else {
+            // lanes 0-7: keys 0-7, columns 0-7; 8-15: keys 8-15; 16-31: columns 8-15
+            const int row = k * 16 + (lane & 15), piece = lane >> 4;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+              uint32_t a[4];
+              ldmatrix4<false>(a, stage + (s >> 2) * (kUnit * 128) + row * 128 + ((((s & 3) * 2 + piece) ^ (row & 7)) << 4));
+#pragma unroll
+              for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(sc[k][nt], a, qf[nt][s][0], qf[nt][s][1]);
+            }
+          }
+        }
+        // ---- which of them are seen; bit 4 k + e of the lane's scores
+        uint32_t seen[kNT];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) seen[nt] = ~0u;
+        if (!full) {
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            seen[nt] = 0;
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = key0 + 16 * k + g + (e >> 1) * 8;
+                if (((loaded_blocks >> k) & 1u) && key < hi[nt][e & 1] && (key >= lo[nt][e & 1] || key < sinks))
+                  seen[nt] |= 1u << (4 * k + e);
+              }
+          }
+        }
+        // ---- the offset, raised where a score lies more than 2^8 above it
+        bool high = false;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              sc[k][nt][e] = sc[k][nt][e] * sl2;
+              high = high || (sc[k][nt][e] > m[nt][e & 1] + 8.f && ((seen[nt] >> (4 * k + e)) & 1u));
+            }
+        if (__any_sync(0xffffffffu, high)) {
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = -INFINITY;
+#pragma unroll
+              for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if ((seen[nt] >> (4 * k + e + 2 * h)) & 1u) x = fmaxf(x, sc[k][nt][e + 2 * h]);
+#pragma unroll
+              for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+              if (x > m[nt][e] + 8.f || (m[nt][e] == -INFINITY && x > -INFINITY)) {
+                const float alpha = ex2r(m[nt][e] - x);
+                m[nt][e] = x;
+                l[nt][e] *= alpha;
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                  o[nt][s][e] *= alpha;
+                  o[nt][s][e + 2] *= alpha;
+                }
+              }
+            }
+        }
+        // ---- P^T and O^T
+#pragma unroll
+        for (int k = 0; k < kBlocks; ++k) {
+          uint32_t pf[kNT][2];
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            float e4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = ex2r(sc[k][nt][e] - m[nt][e & 1]);
+              e4[e] = (seen[nt] >> (4 * k + e)) & 1u ? x : 0.f;
+              l[nt][e & 1] += e4[e];
+            }
+            pf[nt][0] = transpose8x8(pack2<kBF16>(e4[0], e4[1]));
+            pf[nt][1] = transpose8x8(pack2<kBF16>(e4[2], e4[3]));
+          }
+          // values of keys that no row sees count as zeros, whatever they hold
+          uint32_t keep[2] = {~0u, ~0u};
+          if (!full) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              keep[h] = 0;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int key = key0 + 16 * k + 8 * h + 2 * t4 + e;
+                if (((loaded_blocks >> k) & 1u) && key < sees && (key >= lo_some || key < sinks)) keep[h] |= 0xffffu << (16 * e);
+              }
+            }
+          }
+          if constexpr (k4) {
+            const uint32_t words = stage + S::kDataBytes + (k * 16 + 2 * t4) * p.cache.row_bytes + g * 4;
+            const uint32_t metas = stage + 2 * S::kDataBytes + S::kMetaBytes + (k * 16 + 2 * t4) * (p.d / 8) + (g >> 2) * 4;
+#pragma unroll
+            for (int c = 0; c < kD / 64; ++c) {
+              if (c * 64 >= p.d) break;
+              const bool in = c * 64 + g * 8 < p.d;  // (a last half of 32 elements is of half the lanes)
+              uint32_t lo4[2][4], hi4[2][4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t wa = 0, wb = 0, ma = 0, mb = 0;
+                if (in) {
+                  wa = lds32(words + 8 * h * p.cache.row_bytes + c * 32);
+                  wb = lds32(words + (8 * h + 1) * p.cache.row_bytes + c * 32);
+                  ma = lds32(metas + h * p.d + c * 8);
+                  mb = lds32(metas + h * p.d + p.d / 8 + c * 8);
+                }
+                const uint32_t step2 = __byte_perm(ma, mb, 0x5410) & keep[h], least2 = __byte_perm(ma, mb, 0x7632) & keep[h];
+                const uint32_t w0 = __byte_perm(wa, wb, 0x5410), w1 = __byte_perm(wa, wb, 0x7632);
+                pairs_of<kBF16>(w0, step2, least2, lo4[h]);
+                pairs_of<kBF16>(w1, step2, least2, hi4[h]);
+              }
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t af[4] = {lo4[0][x], hi4[0][x], lo4[1][x], hi4[1][x]};
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(o[nt][4 * c + x], af, pf[nt][0], pf[nt][1]);
+              }
+            }
+          } else {
+            // lanes 0-7: keys 0-7, columns 0-7; 8-15: columns 8-15; 16-31: keys 8-15
+            const int row = k * 16 + (lane & 7) + ((lane >> 4) << 3), piece = (lane >> 3) & 1;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+              uint32_t a[4];
+              ldmatrix4<true>(a, stage + S::kDataBytes + (s >> 2) * (kUnit * 128) + row * 128 +
+                                     ((((s & 3) * 2 + piece) ^ (row & 7)) << 4));
+              if (!full) {
+                a[0] &= keep[0];
+                a[1] &= keep[0];
+                a[2] &= keep[1];
+                a[3] &= keep[1];
+              }
+#pragma unroll
+              for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(o[nt][s], a, pf[nt][0], pf[nt][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (loaded < units) load_next();
+    }
+
+    // ---- the rows: sums over the lanes that hold other keys, then out or to a partial slot
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], w);
+    const bool whole = t.n == t.all;
+    const int slot = 2 * mine + (t.u0 == 0 ? 1 : 0);
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * nt + 2 * t4 + e;
+        if (r >= rows) continue;
+        const int rr = row0 + r, i = rr / p.group, j = rr - i * p.group;
+        const long long at_row = static_cast<long long>(t.s.off + i) * p.hq + t.head * p.group + j;
+        if (!bounds_ok(at_row < static_cast<long long>(p.total_q) * p.hq, status)) continue;
+        const float inv = whole ? (l[nt][e] > 0.f ? 1.f / l[nt][e] : l[nt][e] == 0.f ? 0.f : NAN) : 1.f;
+        if (g == 0) {
+          if (whole) p.lse[at_row] = m[nt][e] * 0.69314718055994531f + logf(l[nt][e]);
+          else p.part_ml[static_cast<long long>(slot) * kRows + r] = make_float2(m[nt][e], l[nt][e]);
+        }
+        uint16_t* out = static_cast<uint16_t*>(p.out) + at_row * p.d;
+        float* part = p.part_o + (static_cast<long long>(slot) * kRows + r) * p.d;
+        if constexpr (k4) {
+          // elements 64 c + 8 g + 0..7 are this lane's
+#pragma unroll
+          for (int c = 0; c < kD / 64; ++c) {
+            const int col = c * 64 + g * 8;
+            if (col >= p.d) break;
+            float f[8];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              f[x] = o[nt][4 * c + x][e] * inv;
+              f[x + 4] = o[nt][4 * c + x][e + 2] * inv;
+            }
+            if (whole) {
+              *reinterpret_cast<uint4*>(out + col) = make_uint4(pack2<kBF16>(f[0], f[1]), pack2<kBF16>(f[2], f[3]),
+                                                               pack2<kBF16>(f[4], f[5]), pack2<kBF16>(f[6], f[7]));
+            } else {
+              *reinterpret_cast<float4*>(part + col) = make_float4(f[0], f[1], f[2], f[3]);
+              *reinterpret_cast<float4*>(part + col + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int col = 16 * s + 8 * h + g;
+              if (col >= p.d) continue;
+              const float f = o[nt][s][e + 2 * h] * inv;
+              if (whole) out[col] = static_cast<uint16_t>(pack2<kBF16>(f, 0.f));
+              else part[col] = f;
+            }
+        }
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joining: a block of four warps per row of out. Rows that one warp has written whole are left;
+// rows that hold no token become zeros.
+// ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 128;
+
+template <int kRows, int kUnit, bool kBF16>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedParams p, int warps) {
+  __shared__ float2 s_ml[4];
+  __shared__ float s_o[4][256];
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) {  // (ahead of the rows: it takes longest) the call's status
+    int bits = 0;
+    for (int k = threadIdx.x; k < warps; k += kJoinThreads) bits |= p.warp_status[k];
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (lane == 0) s_ml[warp].x = __int_as_float(bits);
+    __syncthreads();
+    if (threadIdx.x == 0)
+      p.header[kHdrStatus] = __float_as_int(s_ml[0].x) | __float_as_int(s_ml[1].x) | __float_as_int(s_ml[2].x) | __float_as_int(s_ml[3].x);
+    return;
+  }
+  const int at_row = blockIdx.x - 1, tok = at_row / p.hq, hq = at_row - tok * p.hq;
+  const long long row = static_cast<long long>(tok) * p.hq + hq;
+  int before = 0;
+  for (int k = lane; k < p.batch; k += 32) before += p.cu_q_pad[k] <= tok ? 1 : 0;
+  const int b = __reduce_add_sync(0xffffffffu, before) - 1;
+  PagedSeq s{0, 0, 0, true};
+  if (b >= 0) s = load_paged_seq(p, b);
+  const int i = tok - s.off;
+  uint16_t* out = static_cast<uint16_t*>(p.out) + row * p.d;
+  if (b < 0 || i >= s.n) {
+    for (int c = threadIdx.x * 8; c < p.d; c += kJoinThreads * 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) p.lse[row] = 0.f;
+    return;
+  }
+  const int n = paged_run(p, s, kUnit).n;
+  const int h = hq / p.group, rr = i * p.group + hq - h * p.group, tile = rr / kRows, r = rr - tile * kRows;
+  const long long per = slice_units(p.pref[p.batch], warps);
+  const long long first = p.pref[b] + (static_cast<long long>(tile) * p.hkv + h) * n;
+  const int w0 = static_cast<int>(first / per), w1 = static_cast<int>((first + n - 1) / per);
+  if (w0 == w1) return;  // written whole
+  // piece w is in slot 1 of the warp that begins the segment, in slot 0 of the others
+  float m = -INFINITY, l = 0.f;
+  float acc[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) acc[x] = 0.f;
+  const int cols = p.d / 8;  // eight columns a lane
+  for (int w = w0 + warp; w <= w1; w += 4) {
+    // (a piece that ends with its slice's last unit but begins the segment)
+    const long long at = (2ll * w + (static_cast<long long>(w) * per <= first ? 1 : 0)) * kRows + r;
+    const float2 ml = p.part_ml[at];
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
+    if (lane < cols) {
+      a = *reinterpret_cast<const float4*>(p.part_o + at * p.d + lane * 8);
+      c = *reinterpret_cast<const float4*>(p.part_o + at * p.d + lane * 8 + 4);
+    }
+    const float top = fmaxf(m, ml.x);
+    const float x = m == -INFINITY ? 0.f : ex2r(m - top), y = ml.x == -INFINITY ? 0.f : ex2r(ml.x - top);
+    const float f[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = acc[e] * x + f[e] * y;
+    l = l * x + ml.y * y;
+    m = top;
+  }
+  if (lane == 0) s_ml[warp] = make_float2(m, l);
+  if (lane < cols) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s_o[warp][lane * 8 + e] = acc[e];
+  }
+  __syncthreads();
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w].x);
+  float f[4], sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    f[w] = s_ml[w].x == -INFINITY ? 0.f : ex2r(s_ml[w].x - top);
+    sum += s_ml[w].y * f[w];
+  }
+  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : NAN;
+  for (int c = threadIdx.x * 2; c < p.d; c += kJoinThreads * 2) {
+    float a = 0.f, d = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      a += s_o[w][c] * f[w];
+      d += s_o[w][c + 1] * f[w];
+    }
+    *reinterpret_cast<uint32_t*>(out + c) = pack2<kBF16>(a * inv, d * inv);
+  }
+  if (threadIdx.x == 0) p.lse[row] = top * 0.69314718055994531f + logf(sum);
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+// Map of a 16-bit cache: columns, slots of a page, heads, pages; a box of 64 columns and 16 slots.
+static bool make_tmap_pages(CUtensorMap* map, const PagedCache& c, int kv, bool bf16) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  const cuuint64_t page = 1ull << c.shift, row = 2ull * c.d;
+  cuuint64_t gdim[4] = {static_cast<cuuint64_t>(c.d), page, static_cast<cuuint64_t>(c.hkv), static_cast<cuuint64_t>(c.num_pages)};
+  cuuint64_t gstride[3] = {row, row * page, static_cast<cuuint64_t>(c.stride[kv])};
+  cuuint32_t box[4] = {64, 16, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, c.data[kv], gdim, gstride, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kD, int kNT, bool kBF16, bool k4>
+static cudaError_t launch_rows_impl(const PagedParams& p, int num_sms, cudaStream_t st) {
+  using S = RowsShape<kD, kNT, k4>;
+  RowsMaps tm{};
+  if (!k4 && (!make_tmap_pages(&tm.k, p.cache, 0, kBF16) || !make_tmap_pages(&tm.v, p.cache, 1, kBF16))) return cudaErrorInvalidValue;
+  const int smem = S::kSmem + (p.batch + 1) * static_cast<int>(sizeof(long long));
+  auto kern = paged_rows_kernel<kD, kNT, kBF16, k4>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + (kPagedMaxBatch + 1) * 8);
+  if (e != cudaSuccess) return e;
+  const int grid = num_sms < kPagedSMs ? num_sms : kPagedSMs;
+  kern<<<grid, S::kWarps * 32, smem, st>>>(p, tm);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_dependent(paged_join_kernel<S::kRows, S::kUnit, kBF16>, dim3(p.total_q * p.hq + 1), dim3(kJoinThreads), 0, st, p,
+                          grid * S::kWarps);
+}
+
+template <bool kBF16, bool k4>
+static cudaError_t launch_rows_d(const PagedParams& p, int rows, int num_sms, cudaStream_t st) {
+  if (p.d <= 64) return rows == 8 ? launch_rows_impl<64, 1, kBF16, k4>(p, num_sms, st) : launch_rows_impl<64, 2, kBF16, k4>(p, num_sms, st);
+  if (p.d <= 128) return rows == 8 ? launch_rows_impl<128, 1, kBF16, k4>(p, num_sms, st) : launch_rows_impl<128, 2, kBF16, k4>(p, num_sms, st);
+  return launch_rows_impl<256, 1, kBF16, k4>(p, num_sms, st);
+}
+
+cudaError_t launch_paged_rows(const PagedParams& p, bool bf16, bool four, int rows, int num_sms, cudaStream_t st) {
+  if (four) return bf16 ? launch_rows_d<true, true>(p, rows, num_sms, st) : launch_rows_d<false, true>(p, rows, num_sms, st);
+  return bf16 ? launch_rows_d<true, false>(p, rows, num_sms, st) : launch_rows_d<false, false>(p, rows, num_sms, st);
+}
+
+int paged_rows(int batch, int total_q, int group, int d) {
+  if (d > 128) return 8;  // (16 rows' output and queries would not fit the registers)
+  const long long each = (static_cast<long long>(total_q) + batch - 1) / batch * group;
+  return each <= 8 ? 8 : 16;
+}
+
+int paged_warps(int d, bool four) {
+  const int warps = d <= 64 ? (four ? RowsShape<64, 1, true>::kWarps : RowsShape<64, 1, false>::kWarps)
+                    : d <= 128 ? (four ? RowsShape<128, 1, true>::kWarps : RowsShape<128, 1, false>::kWarps)
+                               : (four ? RowsShape<256, 1, true>::kWarps : RowsShape<256, 1, false>::kWarps);
+  return warps * kPagedSMs;
+}
+
+}  // namespace teattn

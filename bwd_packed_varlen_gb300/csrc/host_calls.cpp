@@ -475,6 +475,35 @@ PyObject* paged_gather(PyObject* const* a) {
   return rc != 0 ? PyLong_FromLong(rc) : pack({&k, &v});
 }
 
+// (entry point, size function, k_cache, v_cache, page_table, q, past, cu_seqlens_q, padded ones, scale, window, sinks, out,
+// lse, workspace, stream)
+PyObject* paged_fwd(PyObject* const* a) {
+  const auto fn = reinterpret_cast<decltype(&te_attn_paged_fwd_thd)>(address(a[0]));
+  const auto size = reinterpret_cast<decltype(&te_attn_paged_fwd_workspace_size)>(address(a[1]));
+  const Cache cache(a + 2);
+  const auto index = cache.first->device().index();
+  const at::Tensor& q = tensor(a[5]);
+  need(on_device(q, index), kOneDevice);
+  need(q.scalar_type() == cache.first->scalar_type() && q.dim() == 3 && q.size(2) == cache.c.d && q.is_contiguous(),
+       "q must be contiguous [T_q, hq, d] of the cache's dtype");
+  const int batch = cache.batch;
+  const int32_t* past = lengths(a[6], batch, index);
+  const int32_t *cu = lengths(a[7], batch + int64_t{1}, index), *pad = lengths(a[8], batch + int64_t{1}, index);
+  const float scale = static_cast<float>(number(a[9]));
+  const int window = static_cast<int>(integer(a[10])), sinks = static_cast<int>(integer(a[11]));
+  const int total = as_int(q.size(0)), hq = as_int(q.size(1));
+  const Place place(index, a[15]);
+  const Output out(a[12], q.sizes(), q, q.scalar_type(), kOutput);
+  const Output lse(a[13], q.sizes().slice(0, 2), q, at::kFloat, kLse);
+  const Workspace ws(a[14], given(a[14]) ? 0 : size(batch, total, hq, cache.c.hkv, cache.c.d, cache.c.k_meta ? 4 : 16), q);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = fn(&cache.c, q.const_data_ptr(), out.at(), static_cast<float*>(lse.at()), cu, pad, past, batch, total, hq, scale, window,
+          sinks, ws.at(), ws.bytes(), place.stream());
+  Py_END_ALLOW_THREADS;
+  return rc != 0 ? PyLong_FromLong(rc) : pack({&out, &lse});
+}
+
 template <PyObject* (*kCall)(PyObject* const*), Py_ssize_t kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -497,6 +526,7 @@ PyMethodDef methods[] = {
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<rope, 13>)), METH_FASTCALL, nullptr},
     {"paged_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<paged_append, 16>)), METH_FASTCALL, nullptr},
     {"paged_gather", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<paged_gather, 12>)), METH_FASTCALL, nullptr},
+    {"paged_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<paged_fwd, 16>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_teattn_host", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -464,6 +464,33 @@ int te_attn_paged_gather(const te_attn_paged_cache* cache, void* k, void* v,
                          const int32_t* start, int batch, int total, int32_t* status, void* stream);
 
 /*
+ * Attention over a paged cache: query i of sequence b, at position past[b] + i, sees the cached
+ * keys of positions 0 .. past[b] + i (its own among them: append first), or with window > 0 the
+ * last `window` of them and the first `sinks` ones. From one query per sequence (decoding) to
+ * pieces of prompts; sequences of both kinds may share a batch.
+ *   S = attn_scale q K^T on those keys, O = softmax(S) V, LSE = log sum exp S (natural)
+ * q, out [total_q, hq, d] and lse [total_q, hq] as for te_attn_fwd_thd, hq a multiple of the
+ * cache's hkv; window = 0: every key, sinks = 0 then. Of a 4-bit cache the values that the codes
+ * stand for are taken. Pages before a window, and behind the last key, are not looked at; rows
+ * of a page that hold no key that a query sees may hold any bits. (A NaN or an infinity in a
+ * value that one query sees may reach the other queries of its sequence in the same call.)
+ * Keys whose page lies outside the cache are not seen, and TE_STATUS_BAD_PAGES is raised; a
+ * sequence whose lengths are inconsistent, or whose keys do not fit the page table, counts as
+ * empty, and TE_STATUS_BAD_SEQLENS is raised. Rows that are no token are written as zeros.
+ * A query that sees no key (all its pages outside the cache) gets out = 0, lse = -inf.
+ * At most 4096 sequences of at most 2^30 keys. Workspace, determinism, streams, graphs and
+ * errors as for te_attn_fwd_thd; the workspace's size depends on the shape of the batch and on
+ * the cache's bits (16 or 4), not on the lengths.
+ */
+size_t te_attn_paged_fwd_workspace_size(int batch, int total_q, int hq, int hkv, int d, int bits);
+
+int te_attn_paged_fwd_thd(const te_attn_paged_cache* cache, const void* q, void* out, float* lse,
+                          const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_q_padded,
+                          const int32_t* past, int batch, int total_q, int hq, float attn_scale,
+                          int window, int sinks, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
  * Synchronises `stream`, then copies the device status word of the last call that
  * used `workspace` into *status (0 = clean, else TE_STATUS_* bits). Returns TE_OK or
  * TE_ERR_CUDA. Intended for tests and debugging; it blocks the host.
