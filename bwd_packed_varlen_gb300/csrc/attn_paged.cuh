@@ -1,6 +1,8 @@
 // Attention over a paged cache: launch parameters and how the work is cut.
 #pragma once
 
+#include <cuda.h>
+
 #include "paged.cuh"
 
 namespace teattn {
@@ -22,9 +24,7 @@ struct PagedParams {
   float scale_log2;
   int* header;
   int* warp_status;  // status bits of each warp of the grid
-  long long* pref;   // [batch + 1]: units of work before each sequence
-  float2* part_ml;   // partial results, two slots a warp: maximum (log2 domain) and sum per row,
-  float* part_o;     // unnormalised output, d columns
+  int wide_rows;     // 0: the kernel of few rows takes every sequence
 };
 
 // Queries and keys of a sequence: token i sees the keys [lo(i), i + past + 1) and the sinks.
@@ -47,26 +47,171 @@ __device__ __forceinline__ int paged_first(const PagedParams& p, const PagedSeq&
   return p.window > 0 ? max(0, s.past + i + 1 - p.window) : 0;
 }
 
-// Blocks of `unit` keys that some query of the sequence sees: the sinks', then from the first
-// query's window on.
+// Blocks of `unit` keys that some query sees: the sinks', then from the first query's window on.
 struct PagedRun {
   int sink_units, first, n;
   __device__ __forceinline__ int unit(int u) const { return u < sink_units ? u : u - sink_units + first; }
 };
-__device__ __forceinline__ PagedRun paged_run(const PagedParams& p, const PagedSeq& s, int unit) {
-  const int keys = s.past + s.n;
+// Run of the queries i0 .. i1.
+__device__ __forceinline__ PagedRun paged_run(const PagedParams& p, const PagedSeq& s, int i0, int i1, int unit) {
+  const int keys = s.past + i1 + 1;
   PagedRun r;
-  r.first = paged_first(p, s, 0) / unit;
+  r.first = paged_first(p, s, i0) / unit;
   r.sink_units = p.window > 0 ? min((min(p.sinks, keys) + unit - 1) / unit, r.first) : 0;
-  r.n = s.n > 0 ? r.sink_units + (keys + unit - 1) / unit - r.first : 0;
+  r.n = r.sink_units + (keys + unit - 1) / unit - r.first;
   return r;
 }
 
-cudaError_t launch_paged_rows(const PagedParams& p, bool bf16, bool four, int rows, int num_sms, cudaStream_t st);
+// How a kernel cuts the work: into segments of (sequence, row tile, kv head), each a run of
+// blocks of `unit` keys, one behind the other on a line. The rows of a kv head are its group's
+// queries, token by token; a row tile holds `rows` of them. Two kernels share the sequences:
+// the `wide` one takes those with more than wide_rows rows a kv head, if it is launched at all.
+struct PagedCut {
+  int rows, unit;
+  bool wide;
+
+  __device__ __forceinline__ bool takes(const PagedParams& p, const PagedSeq& s) const {
+    const bool many = p.wide_rows > 0 && static_cast<long long>(s.n) * p.group > p.wide_rows;
+    return s.n > 0 && many == wide;
+  }
+  __device__ __forceinline__ int tiles(const PagedParams& p, const PagedSeq& s) const {
+    return static_cast<int>((static_cast<long long>(s.n) * p.group + rows - 1) / rows);
+  }
+  // Run of a row tile. Tiles of few rows take that of the whole sequence, so that a place on the
+  // line is found by division; their kernel passes over what the tile does not see.
+  __device__ __forceinline__ PagedRun run(const PagedParams& p, const PagedSeq& s, int tile) const {
+    if (!wide) return paged_run(p, s, 0, s.n - 1, unit);
+    const long long r0 = static_cast<long long>(tile) * rows;
+    const int i0 = static_cast<int>(r0 / p.group);
+    const long long i1 = (r0 + rows - 1) / p.group;
+    return paged_run(p, s, i0, i1 < s.n ? static_cast<int>(i1) : s.n - 1, unit);
+  }
+  // Units of the first `n` row tiles of a sequence.
+  __device__ __forceinline__ long long before(const PagedParams& p, const PagedSeq& s, int n) const {
+    if (!wide) return n > 0 ? static_cast<long long>(n) * p.hkv * run(p, s, 0).n : 0;
+    long long sum = 0;
+    for (int t = 0; t < n; ++t) sum += run(p, s, t).n;
+    return sum * p.hkv;
+  }
+};
+
+// A stretch of one segment, as a slice of the line goes through it.
+struct Stretch {
+  int b, head, tile;
+  int u0, n;  // units [u0, u0 + n) of the segment's run
+  PagedSeq s;
+  PagedRun run;
+};
+
+// Stretch that begins at place `at` of the line, ending at `end` at the latest.
+__device__ __forceinline__ Stretch stretch_at(const PagedParams& p, const PagedCut& cut, const long long* pref, long long at,
+                                              long long end) {
+  Stretch t;
+  int lo = 0, hi = p.batch - 1;  // the last sequence that begins at or before it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pref[mid] <= at) lo = mid; else hi = mid - 1;
+  }
+  t.b = lo;
+  t.s = load_paged_seq(p, lo);
+  long long r = at - pref[lo];
+  if (cut.wide) {
+    for (t.tile = 0;; ++t.tile) {
+      t.run = cut.run(p, t.s, t.tile);
+      const long long all = static_cast<long long>(p.hkv) * t.run.n;
+      if (r < all) break;
+      r -= all;
+    }
+    t.head = static_cast<int>(r / t.run.n);
+    t.u0 = static_cast<int>(r - static_cast<long long>(t.head) * t.run.n);
+  } else {
+    t.run = cut.run(p, t.s, 0);
+    const int seg = static_cast<int>(r / t.run.n);
+    t.u0 = static_cast<int>(r - static_cast<long long>(seg) * t.run.n);
+    t.tile = seg / p.hkv;
+    t.head = seg - t.tile * p.hkv;
+  }
+  const long long left = end - at;
+  t.n = left < t.run.n - t.u0 ? static_cast<int>(left) : t.run.n - t.u0;
+  return t;
+}
+
+// Prefix sums of the sequences' units in `pref` (shared memory, batch + 1 values), by the whole
+// block; returns the total. Lengths that do not fit are reported in *status.
+__device__ __forceinline__ long long sum_units(const PagedParams& p, const PagedCut& cut, long long* pref, int* status) {
+  __shared__ long long warp_sum[32];
+  __shared__ long long carry;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  if (tid == 0) carry = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int base = 0; base < p.batch; base += blockDim.x) {
+    const int b = base + tid;
+    long long w = 0;
+    if (b < p.batch) {
+      const PagedSeq s = load_paged_seq(p, b);
+      if (!s.ok) atomicOr(status, kStatusBadSeqlens);
+      if (cut.takes(p, s)) w = cut.before(p, s, cut.tiles(p, s));
+    }
+    long long x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    long long before = carry, all = 0;
+    for (int i = 0; i < nw; ++i) {
+      if (i < warp) before += warp_sum[i];
+      all += warp_sum[i];
+    }
+    if (b < p.batch) pref[b] = before + x - w;
+    __syncthreads();
+    if (tid == 0) carry += all;
+    __syncthreads();
+  }
+  const long long total = carry;
+  if (tid == 0) pref[p.batch] = total;
+  __syncthreads();
+  return total;
+}
+
+// Units of a slice, equal for all; `least` keeps what is left to join in bounds.
+__device__ __forceinline__ long long slice_units(long long total, int slices, int least) {
+  const long long per = (total + slices - 1) / slices;
+  return per < least ? least : per;
+}
+constexpr int kLeastUnits = 4;      // of a warp: it needs a microsecond before its first product
+constexpr int kLeastWideUnits = 2;  // of a block
+
+// Partial results of one kernel: two slots a slice (of the segment that it ends, of the one that
+// it begins), each of a row tile's rows; its prefix sums; slices in all.
+struct PagedParts {
+  long long* pref;
+  float2* ml;   // maximum (log2 domain) and sum per row
+  float* o;     // unnormalised output, d columns
+  int slices, least;
+};
+
+// The kernel of few rows, that of many, and the join of both (wide.slices 0: the second was not
+// launched). cut: set to how the first one cuts the work.
+cudaError_t launch_paged_rows(const PagedParams& p, const PagedParts& parts, bool bf16, bool four, int rows,
+                              PagedCut* cut, cudaStream_t st);
+cudaError_t launch_paged_tiles(const PagedParams& p, const PagedParts& parts, int first_status, bool bf16, bool four, cudaStream_t st);
+cudaError_t launch_paged_join(const PagedParams& p, const PagedCut& cut, const PagedParts& parts, const PagedParts& wide, bool bf16,
+                              cudaStream_t st);
+
+// Map of a 16-bit cache: columns, slots of a page, heads, pages; a box of 64 columns and `slots`.
+bool make_tmap_pages(CUtensorMap* map, const PagedCache& c, int kv, bool bf16, int slots);
+
+constexpr int kWideRows = 256, kWideKeys = 128;  // of a row tile and a unit of the second kernel
 
 // Rows that one pass over a sequence's keys takes, for a batch of this shape.
 int paged_rows(int batch, int total_q, int group, int d);
-// Warps of the whole grid, and with them the slots for partial results.
+// Warps of the first kernel's whole grid.
 int paged_warps(int d, bool four);
+// Rows a kv head from which a sequence goes to the second kernel; 0: it is not launched.
+int paged_wide_rows(int batch, int total_q, int group, int d);
 
 }  // namespace teattn

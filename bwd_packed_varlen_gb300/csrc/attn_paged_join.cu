@@ -1,0 +1,183 @@
+// Attention over a paged cache: joins what the slices left of segments that several of them
+// share, writes zeros to rows that hold no token, and collects the call's status.
+//
+// A block of four warps per row of out. Of a row's pieces O = sum 2^(m_k - M) O_k / L with
+// M = max m_k and L = sum 2^(m_k - M) l_k, in fp32, every fourth piece in order by a warp and the
+// four warps' sums in order, rounded once. Latency-bound: a decoding step's rows have a few pieces.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "attn_paged.cuh"
+#include "pdl.cuh"
+#include "sm103_ptx.cuh"
+#include "tmap.h"
+
+namespace teattn {
+
+constexpr int kJoinThreads = 128;
+
+__device__ __forceinline__ float ex2j(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr int kWideJoin = 8;  // blocks that share the rows of a segment of the kernel of many rows
+
+// A warp adds up the pieces w, w + step, ... <= w1 of row r of the segment that begins at `first`, eight
+// columns a lane: maximum, sum and output. Piece w is in slot 1 of the slice that begins the segment,
+// in slot 0 of the others.
+__device__ __forceinline__ void join_pieces(const PagedParams& p, const PagedParts& parts, int rows, int r, long long first,
+                                            long long per, int w, int w1, int step, float& m, float& l, float (&acc)[8]) {
+  const int lane = threadIdx.x & 31;
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int x = 0; x < 8; ++x) acc[x] = 0.f;
+  for (; w <= w1; w += step) {
+    const long long at = (2ll * w + (w * per <= first ? 1 : 0)) * rows + r;
+    const float2 ml = parts.ml[at];
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
+    if (lane < p.d / 8) {
+      a = *reinterpret_cast<const float4*>(parts.o + at * p.d + lane * 8);
+      c = *reinterpret_cast<const float4*>(parts.o + at * p.d + lane * 8 + 4);
+    }
+    const float top = fmaxf(m, ml.x);
+    // (a piece without a key has left a sum of 0, or a NaN that it saw)
+    const float x = m == -INFINITY ? (l == 0.f ? 0.f : NAN) : ex2j(m - top);
+    const float y = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : NAN) : ex2j(ml.x - top);
+    const float f[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = acc[e] * x + f[e] * y;
+    l = l * x + ml.y * y;
+    m = top;
+  }
+}
+
+// The segment that slice `w` goes on with, if it is the first slice to do so: a warp a row.
+template <bool kBF16>
+__device__ void join_wide(const PagedParams& p, const PagedParts& parts, int w, int part) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long total = parts.pref[p.batch], per = slice_units(total, parts.slices, parts.least), at = w * per;
+  if (at >= total) return;
+  constexpr PagedCut cut{kWideRows, kWideKeys, true};
+  const Stretch t = stretch_at(p, cut, parts.pref, at, total);
+  const long long first = at - t.u0;
+  if (t.u0 == 0 || first < at - per) return;  // begins it, or an earlier slice went on with it
+  const int w1 = static_cast<int>((first + t.run.n - 1) / per);
+  const int row0 = t.tile * kWideRows, rows = min(kWideRows, t.s.n * p.group - row0);
+  for (int r = part * 4 + warp; r < rows; r += kWideJoin * 4) {
+    float m, l, acc[8];
+    join_pieces(p, parts, kWideRows, r, first, per, w - 1, w1, 1, m, l, acc);
+    const int i = (row0 + r) / p.group, j = row0 + r - i * p.group;
+    const long long row = static_cast<long long>(t.s.off + i) * p.hq + t.head * p.group + j;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (lane < p.d / 8)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.d + lane * 8) =
+          make_uint4(pack2<kBF16>(acc[0] * inv, acc[1] * inv), pack2<kBF16>(acc[2] * inv, acc[3] * inv),
+                     pack2<kBF16>(acc[4] * inv, acc[5] * inv), pack2<kBF16>(acc[6] * inv, acc[7] * inv));
+    if (lane == 0) p.lse[row] = m * 0.69314718055994531f + logf(l);
+  }
+}
+
+template <bool kBF16>
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_join_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ PagedCut few, const __grid_constant__ PagedParts few_parts,
+                      const __grid_constant__ PagedParts wide_parts) {
+  __shared__ float2 s_ml[4];
+  __shared__ float s_o[4][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wide_blocks = wide_parts.slices * kWideJoin;  // ahead of the rows
+  const int at_row = blockIdx.x - 1 - wide_blocks, tok = at_row / p.hq, hq = at_row - tok * p.hq;
+  PagedSeq s{0, 0, 0, true};
+  int b = -1;
+  if (at_row >= 0) {
+    int before = 0;
+    for (int k = lane; k < p.batch; k += 32) before += p.cu_q_pad[k] <= tok ? 1 : 0;
+    b = __reduce_add_sync(0xffffffffu, before) - 1;
+    if (b >= 0) s = load_paged_seq(p, b);
+  }
+  pdl_wait();
+  if (blockIdx.x == 0) {  // the call's status
+    int bits = 0;
+    for (int k = threadIdx.x; k < few_parts.slices + wide_parts.slices; k += kJoinThreads) bits |= p.warp_status[k];
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (lane == 0) s_ml[warp].x = __int_as_float(bits);
+    __syncthreads();
+    if (threadIdx.x == 0)
+      p.header[kHdrStatus] = __float_as_int(s_ml[0].x) | __float_as_int(s_ml[1].x) | __float_as_int(s_ml[2].x) | __float_as_int(s_ml[3].x);
+    return;
+  }
+  if (at_row < 0) {
+    join_wide<kBF16>(p, wide_parts, (blockIdx.x - 1) / kWideJoin, (blockIdx.x - 1) % kWideJoin);
+    return;
+  }
+  const long long row = at_row;
+  const int i = tok - s.off;
+  uint16_t* out = static_cast<uint16_t*>(p.out) + row * p.d;
+  if (b < 0 || i >= s.n) {
+    for (int c = threadIdx.x * 8; c < p.d; c += kJoinThreads * 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) p.lse[row] = 0.f;
+    return;
+  }
+  if (!few.takes(p, s)) return;  // the other kernel's
+  const PagedParts& parts = few_parts;
+  const int h = hq / p.group;
+  const long long rr = static_cast<long long>(i) * p.group + hq - h * p.group;
+  const int tile = static_cast<int>(rr / few.rows), r = static_cast<int>(rr - static_cast<long long>(tile) * few.rows);
+  const int n = few.run(p, s, tile).n;
+  const long long per = slice_units(parts.pref[p.batch], parts.slices, parts.least);
+  const long long first = parts.pref[b] + few.before(p, s, tile) + static_cast<long long>(h) * n;
+  const int w0 = static_cast<int>(first / per), w1 = static_cast<int>((first + n - 1) / per);
+  if (w0 == w1) return;  // written whole
+  float m, l, acc[8];
+  const int cols = p.d / 8;  // eight columns a lane
+  join_pieces(p, parts, few.rows, r, first, per, w0 + warp, w1, 4, m, l, acc);
+  if (lane == 0) s_ml[warp] = make_float2(m, l);
+  if (lane < cols) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s_o[warp][lane * 8 + e] = acc[e];
+  }
+  __syncthreads();
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w].x);
+  float f[4], sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    f[w] = s_ml[w].x == -INFINITY ? (s_ml[w].y == 0.f ? 0.f : NAN) : ex2j(s_ml[w].x - top);
+    sum += s_ml[w].y * f[w];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  for (int c = threadIdx.x * 2; c < p.d; c += kJoinThreads * 2) {
+    float a = 0.f, d = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      a += s_o[w][c] * f[w];
+      d += s_o[w][c + 1] * f[w];
+    }
+    *reinterpret_cast<uint32_t*>(out + c) = pack2<kBF16>(a * inv, d * inv);
+  }
+  if (threadIdx.x == 0) p.lse[row] = top * 0.69314718055994531f + logf(sum);
+}
+
+bool make_tmap_pages(CUtensorMap* map, const PagedCache& c, int kv, bool bf16, int slots) {
+  auto enc = tmap_encoder();
+  if (!enc) return false;
+  const cuuint64_t page = 1ull << c.shift, row = 2ull * c.d;
+  cuuint64_t gdim[4] = {static_cast<cuuint64_t>(c.d), page, static_cast<cuuint64_t>(c.hkv), static_cast<cuuint64_t>(c.num_pages)};
+  cuuint64_t gstride[3] = {row, row * page, static_cast<cuuint64_t>(c.stride[kv])};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(slots), 1, 1}, estr[4] = {1, 1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, c.data[kv], gdim, gstride, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_paged_join(const PagedParams& p, const PagedCut& cut, const PagedParts& parts, const PagedParts& wide, bool bf16,
+                              cudaStream_t st) {
+  return launch_dependent(bf16 ? paged_join_kernel<true> : paged_join_kernel<false>, dim3(p.total_q * p.hq + wide.slices * kWideJoin + 1), dim3(kJoinThreads), 0, st,
+                          p, cut, parts, wide);
+}
+
+}  // namespace teattn

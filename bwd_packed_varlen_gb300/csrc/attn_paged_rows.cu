@@ -112,92 +112,10 @@ __device__ __forceinline__ void pairs_of(uint32_t w, uint32_t step2, uint32_t le
     r[i] = value_pair<kBF16>(code_pair<kBF16>((w >> (4 * i)) & 0x000f000fu), step2, least2);
 }
 
-// One stretch of units of one segment, as the cursors of loads and of products go through them.
-struct Stretch {
-  int b, head, tile;   // sequence, kv head, row tile
-  int u0, n;           // units [u0, u0 + n) of the segment's `all`
-  int all;
-  PagedSeq s;
-  PagedRun run;
-};
-
-// Stretch that begins at place `at` of the line, ending at `end` at the latest.
-template <int kRows, int kUnit>
-__device__ __forceinline__ Stretch stretch_at(const PagedParams& p, const long long* pref, long long at, long long end) {
-  Stretch t;
-  int lo = 0, hi = p.batch - 1;  // the last sequence that begins at or before it
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pref[mid] <= at) lo = mid; else hi = mid - 1;
-  }
-  t.b = lo;
-  t.s = load_paged_seq(p, lo);
-  t.run = paged_run(p, t.s, kUnit);
-  t.all = t.run.n;
-  const long long r = at - pref[lo];
-  const int seg = static_cast<int>(r / t.all);
-  t.u0 = static_cast<int>(r - static_cast<long long>(seg) * t.all);
-  t.tile = seg / p.hkv;
-  t.head = seg - t.tile * p.hkv;
-  const long long left = end - at;
-  t.n = left < t.all - t.u0 ? static_cast<int>(left) : t.all - t.u0;
-  return t;
-}
-
-// Prefix sums of the sequences' units in `pref` (shared memory, batch + 1 values), by the whole
-// block; returns the total.
-template <int kRows, int kUnit>
-__device__ long long sum_units(const PagedParams& p, long long* pref, int* status) {
-  __shared__ long long warp_sum[32];
-  __shared__ long long carry;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  if (tid == 0) carry = 0;
-  __syncthreads();
-#pragma unroll 1
-  for (int base = 0; base < p.batch; base += blockDim.x) {
-    const int b = base + tid;
-    long long w = 0;
-    if (b < p.batch) {
-      const PagedSeq s = load_paged_seq(p, b);
-      if (!s.ok) atomicOr(status, kStatusBadSeqlens);
-      const long long tiles = (static_cast<long long>(s.n) * p.group + kRows - 1) / kRows;
-      w = tiles * p.hkv * paged_run(p, s, kUnit).n;
-    }
-    long long x = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    long long before = carry, all = 0;
-    for (int i = 0; i < nw; ++i) {
-      if (i < warp) before += warp_sum[i];
-      all += warp_sum[i];
-    }
-    if (b < p.batch) pref[b] = before + x - w;
-    __syncthreads();
-    if (tid == 0) carry += all;
-    __syncthreads();
-  }
-  const long long total = carry;
-  if (tid == 0) pref[p.batch] = total;
-  __syncthreads();
-  return total;
-}
-
-// Units of a slice: equal for all warps, four at least (a warp needs a microsecond before its
-// first product, and what it leaves has to be joined).
-constexpr int kLeastUnits = 4;
-__device__ __forceinline__ long long slice_units(long long total, int warps) {
-  const long long per = (total + warps - 1) / warps;
-  return per < kLeastUnits ? kLeastUnits : per;
-}
-
 template <int kD, int kNT, bool kBF16, bool k4>
 __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
-    paged_rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ RowsMaps tm) {
+    paged_rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ PagedParts parts,
+                      const __grid_constant__ RowsMaps tm) {
   using S = RowsShape<kD, kNT, k4>;
   constexpr int kRows = S::kRows, kUnit = S::kUnit, kBlocks = S::kBlocks, NS = S::kStages, kSteps = kD / 16;
   extern __shared__ uint8_t smem_raw[];
@@ -218,10 +136,11 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
     for (int i = 0; i < NS; ++i) mbar_init(&bar[warp][i], 1);
     fence_barrier_init();
   }
-  const long long total = sum_units<kRows, kUnit>(p, pref, status);
+  constexpr PagedCut cut{kRows, kUnit, false};
+  const long long total = sum_units(p, cut, pref, status);
   if (blockIdx.x == 0)
-    for (int b = tid; b <= p.batch; b += blockDim.x) p.pref[b] = pref[b];
-  const long long per = slice_units(total, warps);
+    for (int b = tid; b <= p.batch; b += blockDim.x) parts.pref[b] = pref[b];
+  const long long per = slice_units(total, warps, kLeastUnits);
   const long long begin = mine * per, end = begin + per < total ? begin + per : total;
   if (begin >= end) return;
 
@@ -254,7 +173,7 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
     look_up(x);
     return x;
   };
-  const Stretch first_stretch = stretch_at<kRows, kUnit>(p, pref, begin, end);
+  const Stretch first_stretch = stretch_at(p, cut, pref, begin, end);
   Batch cur = batch_of(first_stretch, first_stretch.u0);
   Batch nxt = cur;
   long long looked = begin + cur.n;  // places looked up so far
@@ -263,7 +182,7 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
     if (cur.first + cur.n < cur.t.u0 + cur.t.n) {
       nxt = batch_of(cur.t, cur.first + cur.n);
     } else {
-      const Stretch t = stretch_at<kRows, kUnit>(p, pref, looked, end);
+      const Stretch t = stretch_at(p, cut, pref, looked, end);
       nxt = batch_of(t, t.u0);
     }
     looked += nxt.n;
@@ -331,7 +250,7 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
   const float sl2 = p.scale_log2;
   long long done = 0;
   while (done < units) {
-    const Stretch t = stretch_at<kRows, kUnit>(p, pref, begin + done, end);
+    const Stretch t = stretch_at(p, cut, pref, begin + done, end);
     const int row0 = t.tile * kRows, rows = min(kRows, t.s.n * p.group - row0);
     const int i0 = row0 / p.group, i1 = (row0 + rows - 1) / p.group;  // first and last query
     const int sees_all = t.s.past + i0 + 1, sees = t.s.past + i1 + 1;  // keys below: of every row, of some
@@ -580,7 +499,7 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], w);
-    const bool whole = t.n == t.all;
+    const bool whole = t.n == t.run.n;
     const int slot = 2 * mine + (t.u0 == 0 ? 1 : 0);
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt)
@@ -594,10 +513,10 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
         const float inv = whole ? (l[nt][e] > 0.f ? 1.f / l[nt][e] : l[nt][e] == 0.f ? 0.f : NAN) : 1.f;
         if (g == 0) {
           if (whole) p.lse[at_row] = m[nt][e] * 0.69314718055994531f + logf(l[nt][e]);
-          else p.part_ml[static_cast<long long>(slot) * kRows + r] = make_float2(m[nt][e], l[nt][e]);
+          else parts.ml[static_cast<long long>(slot) * kRows + r] = make_float2(m[nt][e], l[nt][e]);
         }
         uint16_t* out = static_cast<uint16_t*>(p.out) + at_row * p.d;
-        float* part = p.part_o + (static_cast<long long>(slot) * kRows + r) * p.d;
+        float* part = parts.o + (static_cast<long long>(slot) * kRows + r) * p.d;
         if constexpr (k4) {
           // elements 64 c + 8 g + 0..7 are this lane's
 #pragma unroll
@@ -634,142 +553,37 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
   }
 }
 
-// ---------------------------------------------------------------------------
-// Joining: a block of four warps per row of out. Rows that one warp has written whole are left;
-// rows that hold no token become zeros.
-// ---------------------------------------------------------------------------
-constexpr int kJoinThreads = 128;
-
-template <int kRows, int kUnit, bool kBF16>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedParams p, int warps) {
-  __shared__ float2 s_ml[4];
-  __shared__ float s_o[4][256];
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0) {  // (ahead of the rows: it takes longest) the call's status
-    int bits = 0;
-    for (int k = threadIdx.x; k < warps; k += kJoinThreads) bits |= p.warp_status[k];
-    bits = __reduce_or_sync(0xffffffffu, bits);
-    if (lane == 0) s_ml[warp].x = __int_as_float(bits);
-    __syncthreads();
-    if (threadIdx.x == 0)
-      p.header[kHdrStatus] = __float_as_int(s_ml[0].x) | __float_as_int(s_ml[1].x) | __float_as_int(s_ml[2].x) | __float_as_int(s_ml[3].x);
-    return;
-  }
-  const int at_row = blockIdx.x - 1, tok = at_row / p.hq, hq = at_row - tok * p.hq;
-  const long long row = static_cast<long long>(tok) * p.hq + hq;
-  int before = 0;
-  for (int k = lane; k < p.batch; k += 32) before += p.cu_q_pad[k] <= tok ? 1 : 0;
-  const int b = __reduce_add_sync(0xffffffffu, before) - 1;
-  PagedSeq s{0, 0, 0, true};
-  if (b >= 0) s = load_paged_seq(p, b);
-  const int i = tok - s.off;
-  uint16_t* out = static_cast<uint16_t*>(p.out) + row * p.d;
-  if (b < 0 || i >= s.n) {
-    for (int c = threadIdx.x * 8; c < p.d; c += kJoinThreads * 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
-    if (threadIdx.x == 0) p.lse[row] = 0.f;
-    return;
-  }
-  const int n = paged_run(p, s, kUnit).n;
-  const int h = hq / p.group, rr = i * p.group + hq - h * p.group, tile = rr / kRows, r = rr - tile * kRows;
-  const long long per = slice_units(p.pref[p.batch], warps);
-  const long long first = p.pref[b] + (static_cast<long long>(tile) * p.hkv + h) * n;
-  const int w0 = static_cast<int>(first / per), w1 = static_cast<int>((first + n - 1) / per);
-  if (w0 == w1) return;  // written whole
-  // piece w is in slot 1 of the warp that begins the segment, in slot 0 of the others
-  float m = -INFINITY, l = 0.f;
-  float acc[8];
-#pragma unroll
-  for (int x = 0; x < 8; ++x) acc[x] = 0.f;
-  const int cols = p.d / 8;  // eight columns a lane
-  for (int w = w0 + warp; w <= w1; w += 4) {
-    // (a piece that ends with its slice's last unit but begins the segment)
-    const long long at = (2ll * w + (static_cast<long long>(w) * per <= first ? 1 : 0)) * kRows + r;
-    const float2 ml = p.part_ml[at];
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
-    if (lane < cols) {
-      a = *reinterpret_cast<const float4*>(p.part_o + at * p.d + lane * 8);
-      c = *reinterpret_cast<const float4*>(p.part_o + at * p.d + lane * 8 + 4);
-    }
-    const float top = fmaxf(m, ml.x);
-    const float x = m == -INFINITY ? 0.f : ex2r(m - top), y = ml.x == -INFINITY ? 0.f : ex2r(ml.x - top);
-    const float f[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = acc[e] * x + f[e] * y;
-    l = l * x + ml.y * y;
-    m = top;
-  }
-  if (lane == 0) s_ml[warp] = make_float2(m, l);
-  if (lane < cols) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s_o[warp][lane * 8 + e] = acc[e];
-  }
-  __syncthreads();
-  float top = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w].x);
-  float f[4], sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    f[w] = s_ml[w].x == -INFINITY ? 0.f : ex2r(s_ml[w].x - top);
-    sum += s_ml[w].y * f[w];
-  }
-  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : NAN;
-  for (int c = threadIdx.x * 2; c < p.d; c += kJoinThreads * 2) {
-    float a = 0.f, d = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      a += s_o[w][c] * f[w];
-      d += s_o[w][c + 1] * f[w];
-    }
-    *reinterpret_cast<uint32_t*>(out + c) = pack2<kBF16>(a * inv, d * inv);
-  }
-  if (threadIdx.x == 0) p.lse[row] = top * 0.69314718055994531f + logf(sum);
-}
-
-// ---------------------------------------------------------------------------
-// Launches
-// ---------------------------------------------------------------------------
-// Map of a 16-bit cache: columns, slots of a page, heads, pages; a box of 64 columns and 16 slots.
-static bool make_tmap_pages(CUtensorMap* map, const PagedCache& c, int kv, bool bf16) {
-  auto enc = tmap_encoder();
-  if (!enc) return false;
-  const cuuint64_t page = 1ull << c.shift, row = 2ull * c.d;
-  cuuint64_t gdim[4] = {static_cast<cuuint64_t>(c.d), page, static_cast<cuuint64_t>(c.hkv), static_cast<cuuint64_t>(c.num_pages)};
-  cuuint64_t gstride[3] = {row, row * page, static_cast<cuuint64_t>(c.stride[kv])};
-  cuuint32_t box[4] = {64, 16, 1, 1}, estr[4] = {1, 1, 1, 1};
-  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, c.data[kv], gdim, gstride, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int kD, int kNT, bool kBF16, bool k4>
-static cudaError_t launch_rows_impl(const PagedParams& p, int num_sms, cudaStream_t st) {
+static cudaError_t launch_rows_impl(const PagedParams& p, const PagedParts& parts, PagedCut* cut, cudaStream_t st) {
   using S = RowsShape<kD, kNT, k4>;
+  *cut = PagedCut{S::kRows, S::kUnit, false};
   RowsMaps tm{};
-  if (!k4 && (!make_tmap_pages(&tm.k, p.cache, 0, kBF16) || !make_tmap_pages(&tm.v, p.cache, 1, kBF16))) return cudaErrorInvalidValue;
+  if (!k4 && (!make_tmap_pages(&tm.k, p.cache, 0, kBF16, 16) || !make_tmap_pages(&tm.v, p.cache, 1, kBF16, 16)))
+    return cudaErrorInvalidValue;
   const int smem = S::kSmem + (p.batch + 1) * static_cast<int>(sizeof(long long));
   auto kern = paged_rows_kernel<kD, kNT, kBF16, k4>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + (kPagedMaxBatch + 1) * 8);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + (kPagedMaxBatch + 1) * 8);
   if (e != cudaSuccess) return e;
-  const int grid = num_sms < kPagedSMs ? num_sms : kPagedSMs;
-  kern<<<grid, S::kWarps * 32, smem, st>>>(p, tm);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_dependent(paged_join_kernel<S::kRows, S::kUnit, kBF16>, dim3(p.total_q * p.hq + 1), dim3(kJoinThreads), 0, st, p,
-                          grid * S::kWarps);
+  kern<<<parts.slices / S::kWarps, S::kWarps * 32, smem, st>>>(p, parts, tm);
+  return cudaGetLastError();
 }
 
 template <bool kBF16, bool k4>
-static cudaError_t launch_rows_d(const PagedParams& p, int rows, int num_sms, cudaStream_t st) {
-  if (p.d <= 64) return rows == 8 ? launch_rows_impl<64, 1, kBF16, k4>(p, num_sms, st) : launch_rows_impl<64, 2, kBF16, k4>(p, num_sms, st);
-  if (p.d <= 128) return rows == 8 ? launch_rows_impl<128, 1, kBF16, k4>(p, num_sms, st) : launch_rows_impl<128, 2, kBF16, k4>(p, num_sms, st);
-  return launch_rows_impl<256, 1, kBF16, k4>(p, num_sms, st);
+static cudaError_t launch_rows_d(const PagedParams& p, const PagedParts& parts, int rows, PagedCut* cut, cudaStream_t st) {
+  if (p.d <= 64)
+    return rows == 8 ? launch_rows_impl<64, 1, kBF16, k4>(p, parts, cut, st)
+                     : launch_rows_impl<64, 2, kBF16, k4>(p, parts, cut, st);
+  if (p.d <= 128)
+    return rows == 8 ? launch_rows_impl<128, 1, kBF16, k4>(p, parts, cut, st)
+                     : launch_rows_impl<128, 2, kBF16, k4>(p, parts, cut, st);
+  return launch_rows_impl<256, 1, kBF16, k4>(p, parts, cut, st);
 }
 
-cudaError_t launch_paged_rows(const PagedParams& p, bool bf16, bool four, int rows, int num_sms, cudaStream_t st) {
-  if (four) return bf16 ? launch_rows_d<true, true>(p, rows, num_sms, st) : launch_rows_d<false, true>(p, rows, num_sms, st);
-  return bf16 ? launch_rows_d<true, false>(p, rows, num_sms, st) : launch_rows_d<false, false>(p, rows, num_sms, st);
+cudaError_t launch_paged_rows(const PagedParams& p, const PagedParts& parts, bool bf16, bool four, int rows,
+                              PagedCut* cut, cudaStream_t st) {
+  if (four)
+    return bf16 ? launch_rows_d<true, true>(p, parts, rows, cut, st) : launch_rows_d<false, true>(p, parts, rows, cut, st);
+  return bf16 ? launch_rows_d<true, false>(p, parts, rows, cut, st) : launch_rows_d<false, false>(p, parts, rows, cut, st);
 }
 
 int paged_rows(int batch, int total_q, int group, int d) {

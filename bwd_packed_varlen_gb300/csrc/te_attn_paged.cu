@@ -11,11 +11,12 @@
 namespace teattn {
 namespace {
 
-// Workspace, 256-byte aligned sections: header, a status word a warp, prefix sums of the sequences' work, partial rows
-// (maximum and sum; d fp32 columns), two slots of a row tile for every warp of the grid.
+// Workspace, 256-byte aligned sections: header, a status word a slice, and for each of the two
+// kernels prefix sums of the sequences' work and partial rows (maximum and sum; d fp32 columns),
+// two slots of a row tile for every slice.
 struct PagedLayout {
-  size_t warp_status, pref, part_ml, part_o, total;
-  int rows;
+  size_t warp_status, pref[2], ml[2], o[2], total;
+  int rows, slices[2], wide_rows;
 };
 
 bool paged_layout(int batch, int total_q, int hq, int hkv, int d, bool four, PagedLayout* L) {
@@ -23,17 +24,22 @@ bool paged_layout(int batch, int total_q, int hq, int hkv, int d, bool four, Pag
       static_cast<long long>(total_q) * hq > INT32_MAX - 256)
     return false;
   L->rows = paged_rows(batch, total_q, hq / hkv, d);
-  const size_t slots = 2 * static_cast<size_t>(paged_warps(d, four)) * L->rows;
+  L->wide_rows = paged_wide_rows(batch, total_q, hq / hkv, d);
+  L->slices[0] = paged_warps(d, four);
+  L->slices[1] = L->wide_rows > 0 ? kPagedSMs : 0;
   size_t off = kHdrWords * sizeof(int);
   auto take = [&off](size_t bytes) {
     const size_t at = off;
     off = (off + bytes + 255) / 256 * 256;
     return at;
   };
-  L->warp_status = take(paged_warps(d, four) * sizeof(int));
-  L->pref = take((static_cast<size_t>(batch) + 1) * sizeof(long long));
-  L->part_ml = take(slots * sizeof(float2));
-  L->part_o = take(slots * d * sizeof(float));
+  L->warp_status = take((L->slices[0] + L->slices[1]) * sizeof(int));
+  for (int k = 0; k < 2; ++k) {
+    const size_t rows = 2 * static_cast<size_t>(L->slices[k]) * (k ? kWideRows : L->rows);
+    L->pref[k] = take((static_cast<size_t>(batch) + 1) * sizeof(long long));
+    L->ml[k] = take(rows * sizeof(float2));
+    L->o[k] = take(rows * d * sizeof(float));
+  }
   L->total = off;
   return true;
 }
@@ -105,13 +111,23 @@ int te_attn_paged_fwd_thd(const te_attn_paged_cache* cache, const void* q, void*
   p.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
   p.scale_log2 = attn_scale * 1.4426950408889634f;
   p.warp_status = reinterpret_cast<int*>(ws + L.warp_status);
-  p.pref = reinterpret_cast<long long*>(ws + L.pref);
-  p.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
-  p.part_o = reinterpret_cast<float*>(ws + L.part_o);
-  const cudaError_t e = api_timed(TE_KERNEL_FWD, st, [&] {
-    return launch_paged_rows(p, cache->dtype == TE_DTYPE_BF16, four, L.rows, sms, st);
-  });
-  return e == cudaSuccess ? api_ok() : api_cuda_fail(e, "paged attention");
+  p.wide_rows = L.wide_rows;
+  // one slice for each warp, or block, of as many SMs as there are
+  const int use = sms < kPagedSMs ? sms : kPagedSMs;
+  PagedParts parts[2];
+  for (int k = 0; k < 2; ++k)
+    parts[k] = PagedParts{reinterpret_cast<long long*>(ws + L.pref[k]), reinterpret_cast<float2*>(ws + L.ml[k]),
+                          reinterpret_cast<float*>(ws + L.o[k]), L.slices[k] / kPagedSMs * use, k ? kLeastWideUnits : kLeastUnits};
+  const bool bf16 = cache->dtype == TE_DTYPE_BF16;
+  PagedCut cut{};
+  cudaError_t e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_paged_rows(p, parts[0], bf16, four, L.rows, &cut, st); });
+  if (e != cudaSuccess) return api_cuda_fail(e, "paged attention");
+  if (L.wide_rows > 0) {
+    e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_paged_tiles(p, parts[1], parts[0].slices, bf16, four, st); });
+    if (e != cudaSuccess) return api_cuda_fail(e, "paged attention of long pieces");
+  }
+  e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_paged_join(p, cut, parts[0], parts[1], bf16, st); });
+  return e == cudaSuccess ? api_ok() : api_cuda_fail(e, "paged join");
 }
 
 }  // extern "C"
