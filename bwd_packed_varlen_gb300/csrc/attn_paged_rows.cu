@@ -28,8 +28,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "attn_paged.cuh"
 #include "common.cuh"
@@ -104,15 +104,8 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return v;
 }
 
-// The four pairs (i, i + 4) of a word's codes as values.
-template <bool kBF16>
-__device__ __forceinline__ void pairs_of(uint32_t w, uint32_t step2, uint32_t least2, uint32_t (&r)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r[i] = value_pair<kBF16>(code_pair<kBF16>((w >> (4 * i)) & 0x000f000fu), step2, least2);
-}
-
-template <int kD, int kNT, bool kBF16, bool k4>
+// kExact: 4 bits, d is kD (offsets into a row are then constants).
+template <int kD, int kNT, bool kBF16, bool k4, bool kExact>
 __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
     paged_rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ PagedParts parts,
                       const __grid_constant__ RowsMaps tm) {
@@ -122,7 +115,7 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   long long* pref = reinterpret_cast<long long*>(smem + S::kWarps * NS * S::kStageBytes);  // [batch + 1]
   __shared__ uint64_t bar[S::kWarps][NS];
-  __shared__ uint32_t s_seen[S::kWarps][NS];  // bit k: block k of the unit was loaded
+  __shared__ uint32_t s_magic;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int warps = gridDim.x * S::kWarps;
   // neighbouring slices on different SMs, so that few of them still use all
@@ -131,6 +124,7 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
   // one has to clear a common one
   int* status = p.warp_status + mine;
   pdl_trigger();
+  if (tid == 0) s_magic = kCodeMagic<kBF16>;
   if (lane == 0) {
     *status = 0;
     for (int i = 0; i < NS; ++i) mbar_init(&bar[warp][i], 1);
@@ -145,110 +139,99 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
   if (begin >= end) return;
 
   uint8_t* ring = smem + warp * NS * S::kStageBytes;
+  const int row_bytes = kExact ? kD / 2 : p.cache.row_bytes, meta_bytes = kExact ? kD / 8 : p.d / 8;
   // ------------------------------------------------------------- loads
-  // Pages are looked up 32 blocks at a time, a batch ahead of its use.
+  // Pages are looked up 32 blocks of 16 keys at a time, a batch ahead of its use. A lane works out
+  // where its block lies once, and issues its copies when the block's unit comes: a unit then
+  // costs the warp a few instructions.
   constexpr int kBatch = 32 / kBlocks;  // units of a batch
-  struct Batch {
-    Stretch t;
-    int page;   // lane l: page of block l of the batch; -1: outside the cache
-    int first, n;  // units [first, first + n) of the segment
-  };
-  auto look_up = [&](Batch& x) {
-    const int u = x.first + lane / kBlocks;
-    x.page = -1;
-    if (lane / kBlocks < x.n) {
-      const int key = x.t.run.unit(u) * kUnit + lane % kBlocks * 16;
-      // (blocks of a unit that no query sees are not looked at)
-      if (key < x.t.s.past + x.t.s.n && (key + 16 > paged_first(p, x.t.s, 0) || key < p.sinks)) {
-        x.page = page_of(p.cache, x.t.b, key);
-        if (x.page < 0) atomicOr(status, kStatusBadPages);
-      }
-    }
-  };
-  auto batch_of = [&](const Stretch& t, int first) {
-    Batch x;
-    x.t = t;
-    x.first = first;
-    x.n = min(kBatch, t.u0 + t.n - first);
-    look_up(x);
-    return x;
-  };
-  const Stretch first_stretch = stretch_at(p, cut, pref, begin, end);
-  Batch cur = batch_of(first_stretch, first_stretch.u0);
-  Batch nxt = cur;
-  long long looked = begin + cur.n;  // places looked up so far
-  auto prefetch = [&]() {
+  Stretch lt = stretch_at(p, cut, pref, begin, end);
+  int lu = lt.u0;      // first unit of the batch that is looked up next
+  int ahead_n = 0;     // its units,
+  int ahead_page = -1, ahead_head = 0, ahead_slot = 0;  // and this lane's block of them
+  long long looked = begin;  // places looked up so far
+  auto look_up = [&]() {
+    ahead_n = 0;
     if (looked >= end) return;
-    if (cur.first + cur.n < cur.t.u0 + cur.t.n) {
-      nxt = batch_of(cur.t, cur.first + cur.n);
-    } else {
-      const Stretch t = stretch_at(p, cut, pref, looked, end);
-      nxt = batch_of(t, t.u0);
+    if (lu == lt.u0 + lt.n) {
+      lt = stretch_at(p, cut, pref, looked, end);
+      lu = lt.u0;
     }
-    looked += nxt.n;
+    ahead_n = min(kBatch, lt.u0 + lt.n - lu);
+    ahead_page = -1;
+    ahead_head = lt.head;
+    if (lane / kBlocks < ahead_n) {
+      const int key = lt.run.unit(lu + lane / kBlocks) * kUnit + lane % kBlocks * 16;
+      // (blocks of a unit that no query sees are not looked at)
+      if (key < lt.s.past + lt.s.n && (key + 16 > paged_first(p, lt.s, 0) || key < p.sinks)) {
+        ahead_page = page_of(p.cache, lt.b, key);
+        if (ahead_page < 0) atomicOr(status, kStatusBadPages);
+      }
+      ahead_slot = key & ((1 << p.cache.shift) - 1);
+    }
+    lu += ahead_n;
+    looked += ahead_n;
   };
-  prefetch();
-  int at = 0;  // unit of the current batch that is loaded next
-  int loaded = 0;
-  const long long units = end - begin;
-  const int slot_mask = (1 << p.cache.shift) - 1;
-  auto load_next = [&]() {
-    if (at == cur.n) {
-      cur = nxt;
-      at = 0;
-      prefetch();
-    }
-    const int st = loaded % NS;
-    uint8_t* dst = ring + st * S::kStageBytes;
-    const int key0 = cur.t.run.unit(cur.first + at) * kUnit;
-    uint32_t seen = 0;
-    int page[kBlocks];
+  int batch_n = 0, at = 0;        // units of the current batch, and those of them that are on their way
+  uint32_t batch_seen = 0;        // bit l: block l is loaded
+  const uint8_t* src[4];          // 4 bits: of this lane's block, codes and steps of keys and values
+  int page = -1, head = 0, slot = 0;  // 16 bits: its coordinates
+  auto next_batch = [&]() {
+    batch_n = ahead_n;
+    at = 0;
+    batch_seen = __ballot_sync(0xffffffffu, ahead_page >= 0);
+    page = ahead_page;
+    head = ahead_head;
+    slot = ahead_slot;
+    if constexpr (k4) {
+      const long long row = page_row(p.cache, head, slot);
 #pragma unroll
-    for (int k = 0; k < kBlocks; ++k) {
-      page[k] = __shfl_sync(0xffffffffu, cur.page, at * kBlocks + k);
-      if (page[k] >= 0) seen |= 1u << k;
-    }
-    if (lane == 0) {
-      s_seen[warp][st] = seen;
-      if constexpr (k4) {
-        const uint32_t row = p.cache.row_bytes, meta = p.d / 8;
-        mbar_arrive_expect_tx(&bar[warp][st], __popc(seen) * 2 * 16 * (row + meta));
-      } else {
-        mbar_arrive_expect_tx(&bar[warp][st], __popc(seen) * 2 * 16 * 2 * kD);
+      for (int kv = 0; kv < 2; ++kv) {
+        src[kv] = p.cache.data[kv] + page * p.cache.stride[kv] + row * row_bytes;
+        src[2 + kv] = p.cache.meta[kv] + page * p.cache.meta_stride[kv] + row * meta_bytes;
       }
     }
+    look_up();
+  };
+  look_up();
+  const int units = static_cast<int>(end - begin);
+  int loaded = 0, load_stage = 0;
+  uint32_t seen_fifo = 0;  // blocks of the units on their way, the oldest lowest
+  auto load_next = [&](int pending) {  // pending: units on their way before this one
+    if (at == batch_n) next_batch();
+    const uint32_t seen = (batch_seen >> (at * kBlocks)) & ((1u << kBlocks) - 1u);
+    seen_fifo |= seen << (pending * kBlocks);
+    uint8_t* dst = ring + load_stage * S::kStageBytes;
+    uint64_t* full = &bar[warp][load_stage];
+    const uint32_t block_bytes = k4 ? 2 * 16 * (row_bytes + meta_bytes) : 2 * 16 * 2 * kD;
+    if (lane == 0) mbar_arrive_expect_tx(full, __popc(seen) * block_bytes);
     __syncwarp();
-#pragma unroll
-    for (int k = 0; k < kBlocks; ++k) {
-      if (page[k] < 0) continue;
-      const int slot = (key0 + 16 * k) & slot_mask;
+    if (lane / kBlocks == at && page >= 0) {
+      const int k = lane % kBlocks;
       if constexpr (k4) {
-        if (lane < 4) {  // codes and steps of keys and of values
-          const int kv = lane & 1, is_meta = lane >> 1;
-          const long long row = page_row(p.cache, cur.t.head, slot);
-          const uint32_t bytes = is_meta ? p.d / 8 : p.cache.row_bytes;
-          const uint8_t* src = (is_meta ? p.cache.meta[kv] + page[k] * p.cache.meta_stride[kv]
-                                        : p.cache.data[kv] + page[k] * p.cache.stride[kv]) + row * bytes;
-          uint8_t* to = dst + (is_meta ? 2 * S::kDataBytes + kv * S::kMetaBytes : kv * S::kDataBytes) + k * 16 * bytes;
-          bulk_load(to, src, 16 * bytes, &bar[warp][st]);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          bulk_load(dst + kv * S::kDataBytes + k * 16 * row_bytes, src[kv], 16 * row_bytes, full);
+          bulk_load(dst + 2 * S::kDataBytes + kv * S::kMetaBytes + k * 16 * meta_bytes, src[2 + kv], 16 * meta_bytes, full);
         }
       } else {
-        constexpr int kChunks = kD / 64;
-        if (lane < 2 * kChunks) {
-          const int kv = lane / kChunks, c = lane % kChunks;
-          tma_load_4d(dst + kv * S::kDataBytes + c * kUnit * 128 + k * 16 * 128, kv ? &tm.v : &tm.k, &bar[warp][st], c * 64,
-                      slot, cur.t.head, page[k]);
-        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+          for (int c = 0; c < kD / 64; ++c)
+            tma_load_4d(dst + kv * S::kDataBytes + c * kUnit * 128 + k * 16 * 128, kv ? &tm.v : &tm.k, full, c * 64, slot, head, page);
       }
     }
     ++at;
     ++loaded;
+    load_stage = load_stage + 1 == NS ? 0 : load_stage + 1;
   };
-  while (loaded < NS && loaded < units) load_next();
+  while (loaded < NS && loaded < units) load_next(loaded);
 
   // ------------------------------------------------------------- products
   const float sl2 = p.scale_log2;
-  long long done = 0;
+  const uint32_t magic = lds32(smem_u32(&s_magic));
+  int done = 0, stage_at = 0, phase = 0;
   while (done < units) {
     const Stretch t = stretch_at(p, cut, pref, begin + done, end);
     const int row0 = t.tile * kRows, rows = min(kRows, t.s.n * p.group - row0);
@@ -306,190 +289,208 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
         for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.f;
 
 #pragma unroll 1
-    for (int u = t.u0; u < t.u0 + t.n; ++u, ++done) {
-      const int it = static_cast<int>(done), st = it % NS;
-      if (!mbar_wait_warp(&bar[warp][st], (it / NS) & 1, status)) return;
-      const uint32_t stage = smem_u32(ring + st * S::kStageBytes);
-      const uint32_t loaded_blocks = s_seen[warp][st];
+    for (int u = t.u0; u < t.u0 + t.n; ++u) {
+      if (!mbar_wait_warp(&bar[warp][stage_at], phase, status)) return;
+      const uint32_t stage = smem_u32(ring + stage_at * S::kStageBytes);
+      const uint32_t loaded_blocks = seen_fifo & ((1u << kBlocks) - 1u);
       const int key0 = t.run.unit(u) * kUnit;
-      const bool some = loaded_blocks != 0 && key0 < sees && (key0 + kUnit > lo_some || key0 < sinks);
-      if (some) {
-        const bool full = loaded_blocks == (1u << kBlocks) - 1u && key0 + kUnit <= sees_all &&
-                          (key0 >= lo_all || key0 + kUnit <= sinks);
-        // ---- S^T
-        float sc[kBlocks][kNT][4];
+      const bool full = loaded_blocks == (1u << kBlocks) - 1u && key0 + kUnit <= sees_all && (key0 >= lo_all || key0 + kUnit <= sinks);
+      if (full || (loaded_blocks != 0 && key0 < sees && (key0 + kUnit > lo_some || key0 < sinks))) {
+        // the unit, as code without masks for those that every row sees whole
+        auto unit = [&](auto full_tag) {
+          constexpr bool kFull = decltype(full_tag)::value;
+          // ---- S^T
+          float sc[kBlocks][kNT][4];
 #pragma unroll
-        for (int k = 0; k < kBlocks; ++k) {
+          for (int k = 0; k < kBlocks; ++k) {
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
+            for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[k][nt][e] = 0.f;
-          if constexpr (k4) {
-            const uint32_t words = stage + (k * 16 + g) * p.cache.row_bytes + t4 * 4;
-            const uint32_t metas = stage + 2 * S::kDataBytes + (k * 16 + g) * (p.d / 8);
+              for (int e = 0; e < 4; ++e) sc[k][nt][e] = 0.f;
+            if constexpr (k4) {
+              const uint32_t words = stage + (k * 16 + g) * row_bytes + t4 * 4;
+              const uint32_t metas = stage + 2 * S::kDataBytes + (k * 16 + g) * meta_bytes;
 #pragma unroll
-            for (int w = 0; w < kD / 32; ++w) {
-              if (w * 32 >= p.d) break;
-              uint32_t a[2][4];
+              for (int w = 0; w < kD / 32; ++w) {
+                if (!kExact && w * 32 >= p.d) break;
+                uint32_t a[2][4];
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const uint32_t mt = lds32(metas + half * p.d + w * 4);
-                pairs_of<kBF16>(lds32(words + half * 8 * p.cache.row_bytes + w * 16), __byte_perm(mt, mt, 0x1010),
-                                __byte_perm(mt, mt, 0x3232), a[half]);
+                for (int half = 0; half < 2; ++half) {
+                  const uint32_t mt = lds32(metas + half * 8 * meta_bytes + w * 4);
+                  value_pairs<kBF16>(lds32(words + half * 8 * row_bytes + w * 16), __byte_perm(mt, mt, 0x1010),
+                                  __byte_perm(mt, mt, 0x3232), magic, a[half]);
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const uint32_t af[4] = {a[0][2 * x], a[1][2 * x], a[0][2 * x + 1], a[1][2 * x + 1]};
+#pragma unroll
+                  for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(sc[k][nt], af, qf[nt][2 * w + x][0], qf[nt][2 * w + x][1]);
+                }
               }
+            } else {
+              // lanes 0-7: keys 0-7, columns 0-7; 8-15: keys 8-15; 16-31: columns 8-15
+              const int row = k * 16 + (lane & 15), piece = lane >> 4;
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t af[4] = {a[0][2 * x], a[1][2 * x], a[0][2 * x + 1], a[1][2 * x + 1]};
+              for (int s = 0; s < kSteps; ++s) {
+                uint32_t a[4];
+                ldmatrix4<false>(a, stage + (s >> 2) * (kUnit * 128) + row * 128 + ((((s & 3) * 2 + piece) ^ (row & 7)) << 4));
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(sc[k][nt], af, qf[nt][2 * w + x][0], qf[nt][2 * w + x][1]);
+                for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(sc[k][nt], a, qf[nt][s][0], qf[nt][s][1]);
               }
-            }
-          } else {
-            // lanes 0-7: keys 0-7, columns 0-7; 8-15: keys 8-15; 16-31: columns 8-15
-            const int row = k * 16 + (lane & 15), piece = lane >> 4;
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-              uint32_t a[4];
-              ldmatrix4<false>(a, stage + (s >> 2) * (kUnit * 128) + row * 128 + ((((s & 3) * 2 + piece) ^ (row & 7)) << 4));
-#pragma unroll
-              for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(sc[k][nt], a, qf[nt][s][0], qf[nt][s][1]);
             }
           }
-        }
-        // ---- which of them are seen; bit 4 k + e of the lane's scores
-        uint32_t seen[kNT];
+          // ---- which of them are seen; bit 4 k + e of the lane's scores
+          [[maybe_unused]] uint32_t seen[kNT];
+          if constexpr (!kFull) {
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) seen[nt] = ~0u;
-        if (!full) {
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            seen[nt] = 0;
-#pragma unroll
-            for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int key = key0 + 16 * k + g + (e >> 1) * 8;
-                if (((loaded_blocks >> k) & 1u) && key < hi[nt][e & 1] && (key >= lo[nt][e & 1] || key < sinks))
-                  seen[nt] |= 1u << (4 * k + e);
-              }
-          }
-        }
-        // ---- the offset, raised where a score lies more than 2^8 above it
-        bool high = false;
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int k = 0; k < kBlocks; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              sc[k][nt][e] = sc[k][nt][e] * sl2;
-              high = high || (sc[k][nt][e] > m[nt][e & 1] + 8.f && ((seen[nt] >> (4 * k + e)) & 1u));
-            }
-        if (__any_sync(0xffffffffu, high)) {
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = -INFINITY;
+            for (int nt = 0; nt < kNT; ++nt) {
+              seen[nt] = 0;
 #pragma unroll
               for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  if ((seen[nt] >> (4 * k + e + 2 * h)) & 1u) x = fmaxf(x, sc[k][nt][e + 2 * h]);
-#pragma unroll
-              for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
-              if (x > m[nt][e] + 8.f || (m[nt][e] == -INFINITY && x > -INFINITY)) {
-                const float alpha = ex2r(m[nt][e] - x);
-                m[nt][e] = x;
-                l[nt][e] *= alpha;
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                  o[nt][s][e] *= alpha;
-                  o[nt][s][e + 2] *= alpha;
+                for (int e = 0; e < 4; ++e) {
+                  const int key = key0 + 16 * k + g + (e >> 1) * 8;
+                  if (((loaded_blocks >> k) & 1u) && key < hi[nt][e & 1] && (key >= lo[nt][e & 1] || key < sinks))
+                    seen[nt] |= 1u << (4 * k + e);
                 }
-              }
             }
-        }
-        // ---- P^T and O^T
-#pragma unroll
-        for (int k = 0; k < kBlocks; ++k) {
-          uint32_t pf[kNT][2];
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            float e4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = ex2r(sc[k][nt][e] - m[nt][e & 1]);
-              e4[e] = (seen[nt] >> (4 * k + e)) & 1u ? x : 0.f;
-              l[nt][e & 1] += e4[e];
-            }
-            pf[nt][0] = transpose8x8(pack2<kBF16>(e4[0], e4[1]));
-            pf[nt][1] = transpose8x8(pack2<kBF16>(e4[2], e4[3]));
           }
-          // values of keys that no row sees count as zeros, whatever they hold
-          uint32_t keep[2] = {~0u, ~0u};
-          if (!full) {
+          auto is_seen = [&](int nt, int k, int e) {
+            if constexpr (kFull) return true;
+            else return ((seen[nt] >> (4 * k + e)) & 1u) != 0;
+          };
+          // ---- relative to the offset (log2 domain); raised where a score lies 8 above it
+          float x[kBlocks][kNT][4];
+          auto relative = [&]() {
+            float top = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              keep[h] = 0;
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+              for (int k = 0; k < kBlocks; ++k) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  x[k][nt][e] = fmaf(sc[k][nt][e], sl2, -m[nt][e & 1]);
+                  if constexpr (!kFull) x[k][nt][e] = is_seen(nt, k, e) ? x[k][nt][e] : -INFINITY;
+                }
+                top = max3(top, x[k][nt][0], x[k][nt][1]);
+                top = max3(top, x[k][nt][2], x[k][nt][3]);
+              }
+            return top;
+          };
+          if (__any_sync(0xffffffffu, relative() > 8.f)) {
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int key = key0 + 16 * k + 8 * h + 2 * t4 + e;
-                if (((loaded_blocks >> k) & 1u) && key < sees && (key >= lo_some || key < sinks)) keep[h] |= 0xffffu << (16 * e);
-              }
-            }
-          }
-          if constexpr (k4) {
-            const uint32_t words = stage + S::kDataBytes + (k * 16 + 2 * t4) * p.cache.row_bytes + g * 4;
-            const uint32_t metas = stage + 2 * S::kDataBytes + S::kMetaBytes + (k * 16 + 2 * t4) * (p.d / 8) + (g >> 2) * 4;
+                float y = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < kD / 64; ++c) {
-              if (c * 64 >= p.d) break;
-              const bool in = c * 64 + g * 8 < p.d;  // (a last half of 32 elements is of half the lanes)
-              uint32_t lo4[2][4], hi4[2][4];
+                for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    if (is_seen(nt, k, e + 2 * h)) y = fmaxf(y, sc[k][nt][e + 2 * h] * sl2);
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
+                if (y > m[nt][e] + 8.f || (m[nt][e] == -INFINITY && y > -INFINITY)) {
+                  const float alpha = ex2r(m[nt][e] - y);
+                  m[nt][e] = y;
+                  l[nt][e] *= alpha;
+#pragma unroll
+                  for (int s = 0; s < kSteps; ++s) {
+                    o[nt][s][e] *= alpha;
+                    o[nt][s][e + 2] *= alpha;
+                  }
+                }
+              }
+            relative();
+          }
+          // ---- P^T and O^T
+#pragma unroll
+          for (int k = 0; k < kBlocks; ++k) {
+            uint32_t pf[kNT][2];
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+              float e4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // (a row that has seen no key yet has an infinite offset)
+                e4[e] = ex2r(x[k][nt][e]);
+                if constexpr (!kFull) e4[e] = is_seen(nt, k, e) ? e4[e] : 0.f;
+                l[nt][e & 1] += e4[e];
+              }
+              pf[nt][0] = transpose8x8(pack2<kBF16>(e4[0], e4[1]));
+              pf[nt][1] = transpose8x8(pack2<kBF16>(e4[2], e4[3]));
+            }
+            // values of keys that no row sees count as zeros, whatever they hold
+            uint32_t keep[2] = {~0u, ~0u};
+            if constexpr (!kFull) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                uint32_t wa = 0, wb = 0, ma = 0, mb = 0;
-                if (in) {
-                  wa = lds32(words + 8 * h * p.cache.row_bytes + c * 32);
-                  wb = lds32(words + (8 * h + 1) * p.cache.row_bytes + c * 32);
-                  ma = lds32(metas + h * p.d + c * 8);
-                  mb = lds32(metas + h * p.d + p.d / 8 + c * 8);
+                keep[h] = 0;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int key = key0 + 16 * k + 8 * h + 2 * t4 + e;
+                  if (((loaded_blocks >> k) & 1u) && key < sees && (key >= lo_some || key < sinks)) keep[h] |= 0xffffu << (16 * e);
                 }
-                const uint32_t step2 = __byte_perm(ma, mb, 0x5410) & keep[h], least2 = __byte_perm(ma, mb, 0x7632) & keep[h];
-                const uint32_t w0 = __byte_perm(wa, wb, 0x5410), w1 = __byte_perm(wa, wb, 0x7632);
-                pairs_of<kBF16>(w0, step2, least2, lo4[h]);
-                pairs_of<kBF16>(w1, step2, least2, hi4[h]);
-              }
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const uint32_t af[4] = {lo4[0][x], hi4[0][x], lo4[1][x], hi4[1][x]};
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(o[nt][4 * c + x], af, pf[nt][0], pf[nt][1]);
               }
             }
-          } else {
-            // lanes 0-7: keys 0-7, columns 0-7; 8-15: columns 8-15; 16-31: keys 8-15
-            const int row = k * 16 + (lane & 7) + ((lane >> 4) << 3), piece = (lane >> 3) & 1;
+            if constexpr (k4) {
+              const uint32_t words = stage + S::kDataBytes + (k * 16 + 2 * t4) * row_bytes + g * 4;
+              const uint32_t metas = stage + 2 * S::kDataBytes + S::kMetaBytes + (k * 16 + 2 * t4) * meta_bytes + (g >> 2) * 4;
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-              uint32_t a[4];
-              ldmatrix4<true>(a, stage + S::kDataBytes + (s >> 2) * (kUnit * 128) + row * 128 +
-                                     ((((s & 3) * 2 + piece) ^ (row & 7)) << 4));
-              if (!full) {
-                a[0] &= keep[0];
-                a[1] &= keep[0];
-                a[2] &= keep[1];
-                a[3] &= keep[1];
+              for (int c = 0; c < kD / 64; ++c) {
+                if (!kExact && c * 64 >= p.d) break;
+                const bool in = kExact || c * 64 + g * 8 < p.d;  // (a last half of 32 elements is of half the lanes)
+                uint32_t lo4[2][4], hi4[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint32_t wa = 0, wb = 0, ma = 0, mb = 0;
+                  if (in) {
+                    wa = lds32(words + 8 * h * row_bytes + c * 32);
+                    wb = lds32(words + (8 * h + 1) * row_bytes + c * 32);
+                    ma = lds32(metas + 8 * h * meta_bytes + c * 8);
+                    mb = lds32(metas + (8 * h + 1) * meta_bytes + c * 8);
+                  }
+                  const uint32_t step2 = __byte_perm(ma, mb, 0x5410) & keep[h], least2 = __byte_perm(ma, mb, 0x7632) & keep[h];
+                  const uint32_t w0 = __byte_perm(wa, wb, 0x5410), w1 = __byte_perm(wa, wb, 0x7632);
+                  value_pairs<kBF16>(w0, step2, least2, magic, lo4[h]);
+                  value_pairs<kBF16>(w1, step2, least2, magic, hi4[h]);
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  const uint32_t af[4] = {lo4[0][y], hi4[0][y], lo4[1][y], hi4[1][y]};
+#pragma unroll
+                  for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(o[nt][4 * c + y], af, pf[nt][0], pf[nt][1]);
+                }
               }
+            } else {
+              // lanes 0-7: keys 0-7, columns 0-7; 8-15: columns 8-15; 16-31: keys 8-15
+              const int row = k * 16 + (lane & 7) + ((lane >> 4) << 3), piece = (lane >> 3) & 1;
 #pragma unroll
-              for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(o[nt][s], a, pf[nt][0], pf[nt][1]);
+              for (int s = 0; s < kSteps; ++s) {
+                uint32_t a[4];
+                ldmatrix4<true>(a, stage + S::kDataBytes + (s >> 2) * (kUnit * 128) + row * 128 +
+                                       ((((s & 3) * 2 + piece) ^ (row & 7)) << 4));
+                if constexpr (!kFull) {
+                  a[0] &= keep[0];
+                  a[1] &= keep[0];
+                  a[2] &= keep[1];
+                  a[3] &= keep[1];
+                }
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(o[nt][s], a, pf[nt][0], pf[nt][1]);
+              }
             }
           }
-        }
+        };
+        if (full) unit(std::true_type{});
+        else unit(std::false_type{});
       }
       __syncwarp();  // every lane has read the stage
-      if (loaded < units) load_next();
+      ++done;
+      seen_fifo >>= kBlocks;
+      stage_at = stage_at + 1 == NS ? 0 : stage_at + 1;
+      phase ^= stage_at == 0 ? 1 : 0;
+      if (loaded < units) load_next(loaded - done);
     }
 
     // ---- the rows: sums over the lanes that hold other keys, then out or to a partial slot
@@ -561,7 +562,7 @@ static cudaError_t launch_rows_impl(const PagedParams& p, const PagedParts& part
   if (!k4 && (!make_tmap_pages(&tm.k, p.cache, 0, kBF16, 16) || !make_tmap_pages(&tm.v, p.cache, 1, kBF16, 16)))
     return cudaErrorInvalidValue;
   const int smem = S::kSmem + (p.batch + 1) * static_cast<int>(sizeof(long long));
-  auto kern = paged_rows_kernel<kD, kNT, kBF16, k4>;
+  auto kern = k4 && p.d == kD ? paged_rows_kernel<kD, kNT, kBF16, k4, k4> : paged_rows_kernel<kD, kNT, kBF16, k4, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + (kPagedMaxBatch + 1) * 8);
   if (e != cudaSuccess) return e;
   kern<<<parts.slices / S::kWarps, S::kWarps * 32, smem, st>>>(p, parts, tm);

@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
   // until its product is issued, so five of them are alive at most.
   __shared__ union { uint32_t word; uint8_t part[4]; } s_blocks[8];
   constexpr uint32_t kAllBlocks = 0x03030303u;
+  __shared__ uint32_t s_magic;
   __shared__ uint32_t tmem_slot;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -97,6 +98,7 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
   pdl_trigger();
   if (tid == 0) {
     *status = 0;
+    s_magic = kCodeMagic<kBF16>;
     mbar_init(&bar_q_full, 1);
     mbar_init(&bar_q_empty, 1);
     for (int i = 0; i < NS; ++i) {
@@ -439,6 +441,7 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
     int it = 0;
     bool ok = true;
     constexpr int kG = kD / 32;
+    const uint32_t magic = *const_cast<volatile uint32_t*>(&s_magic);
     struct Raw {
       uint4 code[kG];
       uint32_t meta[kG];
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
           const uint32_t words[4] = {raw.code[g].x, raw.code[g].y, raw.code[g].z, raw.code[g].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 v = dequantize8<kBF16>(words[k], raw.meta[g]);
+            const uint4 v = dequantize8<kBF16>(words[k], raw.meta[g], magic);
             const int piece = (g & 1) * 4 + k;
             st_shared_v4(tile + (g >> 1) * 16384 + r * 128 + ((piece ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
           }

@@ -46,18 +46,24 @@ __device__ __forceinline__ uint32_t pack_meta(float step, float least) {
            static_cast<uint32_t>(__half_as_ushort(__float2half_rn(least))) << 16;
 }
 
-// Two neighbouring codes c0, c1 < 16, given as bits 0-3 and 16-19, as numbers: put into the
-// fraction of 128 (bf16) or 1024 (fp16), which is then taken off; both steps are exact.
+// Codes become numbers by a magic one: put into the fraction of 128 (bf16) or 1024 (fp16), which
+// is then taken off; both steps are exact.
 template <bool kBF16>
-__device__ __forceinline__ uint32_t code_pair(uint32_t bits) {
+constexpr uint32_t kCodeMagic = kBF16 ? 0x43004300u : 0x64006400u;
+
+// The two codes in bits 0-3 and 16-19 of w. `magic` is kCodeMagic from a place that the compiler
+// cannot see into: with mask and magic both constants it spends two instructions on the one
+// that does both.
+template <bool kBF16>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t magic) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(0x000f000fu), "r"(magic));  // (w & mask) | magic
   if constexpr (kBF16) {
-    const uint32_t w = bits | 0x43004300u;
-    const __nv_bfloat162 x = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(128.f));
-    return *reinterpret_cast<const uint32_t*>(&x);
+    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __float2bfloat162_rn(128.f));
+    return *reinterpret_cast<const uint32_t*>(&y);
   } else {
-    const uint32_t w = bits | 0x64006400u;
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(1024.f));
-    return *reinterpret_cast<const uint32_t*>(&x);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(1024.f));
+    return *reinterpret_cast<const uint32_t*>(&y);
   }
 }
 
@@ -72,17 +78,20 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t codes, uint32_t step2, u
   return r;
 }
 
+// The four pairs (i, i + 4) of a word's codes as values.
+template <bool kBF16>
+__device__ __forceinline__ void value_pairs(uint32_t w, uint32_t step2, uint32_t least2, uint32_t magic, uint32_t (&r)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = value_pair<kBF16>(code_pair<kBF16>(w >> (4 * i), magic), step2, least2);
+}
+
 // The eight elements of a word of codes, in order.
 template <bool kBF16>
-__device__ __forceinline__ uint4 dequantize8(uint32_t codes, uint32_t meta) {
-  const uint32_t step2 = __byte_perm(meta, meta, 0x1010), least2 = __byte_perm(meta, meta, 0x3232);
+__device__ __forceinline__ uint4 dequantize8(uint32_t codes, uint32_t meta, uint32_t magic) {
   uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t c = codes >> (8 * i), bits = (c & 15u) | (c & 0xf0u) << 12;
-    r[i] = value_pair<kBF16>(code_pair<kBF16>(bits), step2, least2);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+  value_pairs<kBF16>(codes, __byte_perm(meta, meta, 0x1010), __byte_perm(meta, meta, 0x3232), magic, r);
+  return make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410), __byte_perm(r[0], r[1], 0x7632),
+                    __byte_perm(r[2], r[3], 0x7632));
 }
 
 // Host: the device form of a cache after its checks: TE_OK or an error code.

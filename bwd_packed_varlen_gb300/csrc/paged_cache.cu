@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(const __gr
         const uint32_t codes = *reinterpret_cast<const uint32_t*>(base + word * 4);
         const uint32_t meta = *reinterpret_cast<const uint32_t*>(p.cache.meta[kv] + tk.page * p.cache.meta_stride[kv] +
                                                                  row * (p.cache.d / 8) + word / 4 * 4);
-        v = dequantize8<kBF16>(codes, meta);
+        v = dequantize8<kBF16>(codes, meta, kCodeMagic<kBF16>);
       } else {
         v = *reinterpret_cast<const uint4*>(base + word * 16);
       }
