@@ -95,18 +95,18 @@ def library(debug: bool = None) -> ctypes.CDLL:
     L.te_attn_fwd_thd_e4m3.restype = i32
     L.te_attn_fwd_thd_e4m3.argtypes = ([vp] * 5 + [vp] * 4 + [i32] * 8 + [f32] * 4 +
                                         [i32, vp, sz, vp])
-    L.te_attn_window_fwd_thd.restype = i32
-    L.te_attn_window_fwd_thd.argtypes = [vp] * 9 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
-    L.te_attn_window_bwd_thd.restype = i32
-    L.te_attn_window_bwd_thd.argtypes = [vp] * 13 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
-    L.te_attn_window_fwd_sbhd.restype = i32
-    L.te_attn_window_fwd_sbhd.argtypes = [vp] * 7 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
-    L.te_attn_window_bwd_sbhd.restype = i32
-    L.te_attn_window_bwd_sbhd.argtypes = [vp] * 11 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]
     L.te_attn_paged_fwd_workspace_size.restype = sz
     L.te_attn_paged_fwd_workspace_size.argtypes = [i32] * 6
-    for name in ("te_attn_paged_append", "te_attn_paged_gather", "te_attn_paged_fwd_thd"):  # (called through the extension module)
-        getattr(L, name).restype = i32
+    for name, args in (
+            ("window_fwd_thd", [vp] * 9 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]),
+            ("window_bwd_thd", [vp] * 13 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]),
+            ("window_fwd_sbhd", [vp] * 7 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]),
+            ("window_bwd_sbhd", [vp] * 11 + [i32] * 6 + [f32] + [i32] * 4 + [vp, sz, vp]),
+            ("paged_append", [vp] * 6 + [i32] + [vp] * 3 + [i32] * 3 + [ctypes.c_int64] * 6 + [i32, f32, vp, vp]),
+            ("paged_gather", [vp] * 6 + [i32] * 2 + [vp, vp]),
+            ("paged_fwd_thd", [vp] * 7 + [i32] * 3 + [f32] + [i32] * 2 + [vp, sz, vp])):
+        fn = getattr(L, "te_attn_" + name)
+        fn.restype, fn.argtypes = i32, args
     L.te_attn_read_status.restype = i32
     L.te_attn_read_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int), vp]
     L.te_attn_last_error.restype = ctypes.c_char_p
@@ -358,114 +358,9 @@ def bwd_sbhd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, attn_scale,
     return dq, dk, dv
 
 
-def _int32(n):
-    """n as a C int: what does not fit becomes the nearest that does."""
-    return max(-2 ** 31, min(int(n), 2 ** 31 - 1))
-
-
-def _window_operands(q, k, v, cus, like_q=(), like_k=(), lse=None, workspace=None):
-    """The batch size, after the checks that the windowed calls share; the tensors that have to
-    look like q, or like k, may be None."""
-    if any(t is None for t in (q, k, v) + tuple(cus)):
-        raise ValueError("q, k, v and the cu_seqlens must be given")
-    every = (q, k, v) + tuple(cus) + tuple(like_q) + tuple(like_k) + (lse, workspace)
-    _need_cuda(*every)
-    if any(t is not None and t.device != q.device for t in every):
-        raise ValueError("all tensors must be on one device")
-    _cu(*cus)
-    packed = len(cus) == 4
-    if q.dim() != (3 if packed else 4) or k.dim() != q.dim() or k.shape != v.shape or k.shape[-1] != q.shape[-1]:
-        raise ValueError("q, k and v must be [rows, heads, d]" if packed else "q, k and v must be [S, B, heads, d]")
-    if q.dtype not in _DTYPES or any(t is not None and t.dtype != q.dtype for t in (k, v) + tuple(like_q) + tuple(like_k)):
-        raise ValueError("q, k, v, outputs and gradients must share one dtype, float16 or bfloat16")
-    for ref, ts in ((q, like_q), (k, like_k)):
-        if any(t is not None and t.shape != ref.shape for t in ts):
-            raise ValueError("outputs and gradients must have the shapes of their counterparts")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:-1]):
-        raise ValueError("lse must be float32, one value per row and head of q")
-    batch = cus[0].numel() - 1
-    if batch < 1 or any(c.numel() != batch + 1 for c in cus):
-        raise ValueError("cu_seqlens must hold batch + 1 values each")
-    if not packed and not q.shape[1] == k.shape[1] == batch:
-        raise ValueError("q, k and v must have one batch entry per sequence")
-    return batch
-
-
-def _window_sizes(q, k, batch):
-    if q.dim() == 3:
-        return (batch, q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2])
-    return (batch, q.shape[0], k.shape[0], q.shape[2], k.shape[2], q.shape[3])
-
-
-def _window_fwd(entry, q, k, v, cus, attn_scale, window, sinks, mask_type, out, lse, workspace, stream):
-    batch = _window_operands(q, k, v, cus, (out,), (), lse, workspace)
-    sizes = _window_sizes(q, k, batch)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if lse is None else lse
-    rows = (sizes[1], sizes[2]) if q.dim() == 3 else (sizes[1] * batch, sizes[2] * batch)
-    if workspace is None:
-        workspace = torch.empty(max(fwd_workspace_size(batch, *rows, *sizes[3:]), 1), dtype=torch.uint8, device=q.device)
-    st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
-    with _on(q):
-        _check(entry(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), *(_ptr(c) for c in cus), *sizes, float(attn_scale),
-                     _mask(mask_type), _int32(window), _int32(sinks), _DTYPES[q.dtype], _ptr(workspace),
-                     workspace.numel() * workspace.element_size(), ctypes.c_void_p(st)))
-    return out, lse
-
-
-def _window_bwd(entry, q, k, v, out, dout, lse, cus, attn_scale, window, sinks, mask_type, dq, dk, dv, workspace, stream):
-    if out is None or dout is None or lse is None:
-        raise ValueError("the backward needs out, dout and lse")
-    batch = _window_operands(q, k, v, cus, (out, dout, dq), (dk, dv), lse, workspace)
-    sizes = _window_sizes(q, k, batch)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    rows = (sizes[1], sizes[2]) if q.dim() == 3 else (sizes[1] * batch, sizes[2] * batch)
-    if workspace is None:
-        workspace = torch.empty(max(bwd_workspace_size(batch, *rows, *sizes[3:]), 1), dtype=torch.uint8, device=q.device)
-    st = stream if stream is not None else torch.cuda.current_stream(q.device).cuda_stream
-    with _on(q):
-        _check(entry(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-                     *(_ptr(c) for c in cus), *sizes, float(attn_scale), _mask(mask_type), int(window), int(sinks),
-                     _DTYPES[q.dtype], _ptr(workspace), workspace.numel() * workspace.element_size(), ctypes.c_void_p(st)))
-    return dq, dk, dv
-
-
-def window_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, attn_scale, window,
-               sinks=0, mask_type="padding_causal", out=None, lse=None, workspace=None, stream=None):
-    """``te_attn_window_fwd_thd``: :func:`fwd` of queries that see the last ``window`` keys up to
-    their own position and the first ``sinks`` keys of the sequence; returns ``(out, lse)``. The
-    workspace is :func:`fwd`'s."""
-    cus = (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded)
-    return _window_fwd(library().te_attn_window_fwd_thd, q, k, v, cus, attn_scale, window, sinks, mask_type, out, lse,
-                       workspace, stream)
-
-
-def window_bwd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, attn_scale,
-               window, sinks=0, mask_type="padding_causal", dq=None, dk=None, dv=None, workspace=None, stream=None):
-    """``te_attn_window_bwd_thd``: returns ``(dq, dk, dv)``; the workspace is :func:`bwd`'s."""
-    cus = (cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded)
-    return _window_bwd(library().te_attn_window_bwd_thd, q, k, v, out, dout, lse, cus, attn_scale, window, sinks, mask_type,
-                       dq, dk, dv, workspace, stream)
-
-
-def window_fwd_sbhd(q, k, v, cu_seqlens_q, cu_seqlens_kv, attn_scale, window, sinks=0, mask_type="padding_causal", out=None,
-                    lse=None, workspace=None, stream=None):
-    """``te_attn_window_fwd_sbhd``: the same on ``[S, B, h, d]`` tensors, as :func:`fwd_sbhd`."""
-    return _window_fwd(library().te_attn_window_fwd_sbhd, q, k, v, (cu_seqlens_q, cu_seqlens_kv), attn_scale, window, sinks,
-                       mask_type, out, lse, workspace, stream)
-
-
-def window_bwd_sbhd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, attn_scale, window, sinks=0,
-                    mask_type="padding_causal", dq=None, dk=None, dv=None, workspace=None, stream=None):
-    """``te_attn_window_bwd_sbhd``: returns ``(dq, dk, dv)``."""
-    return _window_bwd(library().te_attn_window_bwd_sbhd, q, k, v, out, dout, lse, (cu_seqlens_q, cu_seqlens_kv), attn_scale,
-                       window, sinks, mask_type, dq, dk, dv, workspace, stream)
-
-
-# The rotary and shared-prefix entry points serve single decoding steps, whose kernels take less
-# time than checks, allocations and ctypes would: they go through a small extension module.
+# The rotary, shared-prefix, paged and windowed entry points serve single decoding steps and small
+# batches, whose kernels take less time than checks, allocations and ctypes would: they go through
+# a small extension module.
 _HOST_PATH = os.path.join(_HERE, "lib", "_teattn_host.so")
 _host = None
 _entries = {}  # addresses of the entry points, per build
@@ -473,7 +368,7 @@ _entries = {}  # addresses of the entry points, per build
 
 def _entry_points():
     """(rope_thd, rope_sbhd, prefix_fwd, its size, prefix_bwd, its size, paged_append, paged_gather, paged_fwd,
-    its size) of the selected build."""
+    its size, window_fwd, window_bwd, the same sequence-major, their sizes) of the selected build."""
     global _host
     L = library()
     if _host is None:
@@ -484,7 +379,8 @@ def _entry_points():
         _host = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(_host)
     names = ("rope_thd", "rope_sbhd", "prefix_fwd_thd", "prefix_fwd_workspace_size", "prefix_bwd_thd",
-             "prefix_bwd_workspace_size", "paged_append", "paged_gather", "paged_fwd_thd", "paged_fwd_workspace_size")
+             "prefix_bwd_workspace_size", "paged_append", "paged_gather", "paged_fwd_thd", "paged_fwd_workspace_size", "window_fwd_thd",
+             "window_bwd_thd", "window_fwd_sbhd", "window_bwd_sbhd", "fwd_workspace_size", "bwd_workspace_size")
     _entries[_use_debug] = tuple(ctypes.cast(getattr(L, "te_attn_" + n), ctypes.c_void_p).value for n in names)
     return _entries[_use_debug]
 
@@ -549,6 +445,51 @@ def prefix_bwd(q, k, v, k_prefix, v_prefix, out, dout, lse, cu_seqlens_q, cu_seq
         e[4], e[5], q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
         cu_seqlens_kv_padded, prefix_len, attn_scale, _mask(mask_type), out, dout, lse, dq, dk, dv, dk_prefix,
         dv_prefix, workspace, stream))
+
+
+def _int32(n):
+    """n as a C int: what does not fit becomes the nearest that does."""
+    return max(-2 ** 31, min(int(n), 2 ** 31 - 1))
+
+
+def window_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, attn_scale, window,
+               sinks=0, mask_type="padding_causal", out=None, lse=None, workspace=None, stream=None):
+    """``te_attn_window_fwd_thd``: :func:`fwd` of queries that see the last ``window`` keys up to
+    their own position and the first ``sinks`` keys of the sequence; returns ``(out, lse)``. The
+    workspace is :func:`fwd`'s."""
+    if cu_seqlens_q_padded is None:
+        raise ValueError("packed tokens need cu_seqlens_q_padded")
+    e = _entries.get(_use_debug) or _entry_points()
+    return _result(_host.window_fwd(e[10], e[14], q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
+                                    cu_seqlens_kv_padded, attn_scale, _mask(mask_type), _int32(window), _int32(sinks), out,
+                                    lse, workspace, stream))
+
+
+def window_bwd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, attn_scale,
+               window, sinks=0, mask_type="padding_causal", dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """``te_attn_window_bwd_thd``: returns ``(dq, dk, dv)``; the workspace is :func:`bwd`'s."""
+    if cu_seqlens_q_padded is None:
+        raise ValueError("packed tokens need cu_seqlens_q_padded")
+    e = _entries.get(_use_debug) or _entry_points()
+    return _result(_host.window_bwd(e[11], e[15], q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded,
+                                    cu_seqlens_kv_padded, attn_scale, _mask(mask_type), _int32(window), _int32(sinks), out, dout,
+                                    lse, dq, dk, dv, workspace, stream))
+
+
+def window_fwd_sbhd(q, k, v, cu_seqlens_q, cu_seqlens_kv, attn_scale, window, sinks=0, mask_type="padding_causal", out=None,
+                    lse=None, workspace=None, stream=None):
+    """``te_attn_window_fwd_sbhd``: the same on ``[S, B, h, d]`` tensors, as :func:`fwd_sbhd`."""
+    e = _entries.get(_use_debug) or _entry_points()
+    return _result(_host.window_fwd(e[12], e[14], q, k, v, cu_seqlens_q, cu_seqlens_kv, None, None, attn_scale,
+                                    _mask(mask_type), _int32(window), _int32(sinks), out, lse, workspace, stream))
+
+
+def window_bwd_sbhd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, attn_scale, window, sinks=0,
+                    mask_type="padding_causal", dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """``te_attn_window_bwd_sbhd``: returns ``(dq, dk, dv)``."""
+    e = _entries.get(_use_debug) or _entry_points()
+    return _result(_host.window_bwd(e[13], e[15], q, k, v, cu_seqlens_q, cu_seqlens_kv, None, None, attn_scale,
+                                    _mask(mask_type), _int32(window), _int32(sinks), out, dout, lse, dq, dk, dv, workspace, stream))
 
 
 def paged_cache(num_pages, page_size, hkv, d, dtype=torch.bfloat16, bits=16, device="cuda"):

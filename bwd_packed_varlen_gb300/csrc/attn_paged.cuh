@@ -210,7 +210,7 @@ constexpr int kWideRows = 256, kWideKeys = 128;  // of a row tile and a unit of 
 // Rows that one pass over a sequence's keys takes, for a batch of this shape.
 int paged_rows(int batch, int total_q, int group, int d);
 // Warps of the first kernel's whole grid.
-int paged_warps(int d, bool four);
+int paged_warps(int d, bool four, int rows);
 // Rows a kv head from which a sequence goes to the second kernel; 0: it is not launched.
 int paged_wide_rows(int batch, int total_q, int group, int d);
 

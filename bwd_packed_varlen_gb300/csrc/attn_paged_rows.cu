@@ -44,12 +44,12 @@ struct RowsShape {
   static constexpr int kRows = 8 * kNT;
   static constexpr int kBlocks = k4 || kD == 64 ? 2 : 1;  // 16-key blocks of a unit
   static constexpr int kUnit = 16 * kBlocks;
-  static constexpr int kWarps = k4 ? (kD == 256 ? 6 : 12) : (kD == 256 ? 4 : 8);
+  static constexpr int kWarps = k4 ? (kD == 256 ? 6 : kD == 64 && kNT == 1 ? 16 : 12) : (kD == 256 ? 4 : 8);
   // (a 4-bit ring is laid out for kD elements a row, whatever d is)
   static constexpr int kDataBytes = kUnit * (k4 ? kD / 2 : 2 * kD);  // keys or values of a unit
   static constexpr int kMetaBytes = k4 ? kUnit * kD / 8 : 0;
   static constexpr int kStageBytes = 2 * (kDataBytes + kMetaBytes);
-  static constexpr int kStages = 3;
+  static constexpr int kStages = k4 && kD == 64 && kNT == 1 ? 2 : 3;
   static constexpr int kSmem = kWarps * kStages * kStageBytes + 1024;
   static_assert(kSmem <= 208 * 1024, "shared memory budget");
 };
@@ -299,46 +299,57 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
         // the unit, as code without masks for those that every row sees whole
         auto unit = [&](auto full_tag) {
           constexpr bool kFull = decltype(full_tag)::value;
-          // ---- S^T
-          float sc[kBlocks][kNT][4];
+          // ---- S^T, every other product into a second sum: each waits for the one before it
+          float sc[kBlocks][kNT][4], odd[kBlocks][kNT][4];
 #pragma unroll
-          for (int k = 0; k < kBlocks; ++k) {
+          for (int k = 0; k < kBlocks; ++k)
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) sc[k][nt][e] = 0.f;
-            if constexpr (k4) {
-              const uint32_t words = stage + (k * 16 + g) * row_bytes + t4 * 4;
-              const uint32_t metas = stage + 2 * S::kDataBytes + (k * 16 + g) * meta_bytes;
+              for (int e = 0; e < 4; ++e) sc[k][nt][e] = odd[k][nt][e] = 0.f;
+          if constexpr (k4) {
+            const uint32_t words = stage + g * row_bytes + t4 * 4;
+            const uint32_t metas = stage + 2 * S::kDataBytes + g * meta_bytes;
 #pragma unroll
-              for (int w = 0; w < kD / 32; ++w) {
-                if (!kExact && w * 32 >= p.d) break;
+            for (int w = 0; w < kD / 32; ++w) {
+              if (!kExact && w * 32 >= p.d) break;
+#pragma unroll
+              for (int k = 0; k < kBlocks; ++k) {
                 uint32_t a[2][4];
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                  const uint32_t mt = lds32(metas + half * 8 * meta_bytes + w * 4);
-                  value_pairs<kBF16>(lds32(words + half * 8 * row_bytes + w * 16), __byte_perm(mt, mt, 0x1010),
-                                  __byte_perm(mt, mt, 0x3232), magic, a[half]);
+                  const int row = 16 * k + 8 * half;
+                  const uint32_t mt = lds32(metas + row * meta_bytes + w * 4);
+                  value_pairs<kBF16>(lds32(words + row * row_bytes + w * 16), __byte_perm(mt, mt, 0x1010),
+                                     __byte_perm(mt, mt, 0x3232), magic, a[half]);
                 }
+                const uint32_t a0[4] = {a[0][0], a[1][0], a[0][1], a[1][1]}, a1[4] = {a[0][2], a[1][2], a[0][3], a[1][3]};
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const uint32_t af[4] = {a[0][2 * x], a[1][2 * x], a[0][2 * x + 1], a[1][2 * x + 1]};
-#pragma unroll
-                  for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(sc[k][nt], af, qf[nt][2 * w + x][0], qf[nt][2 * w + x][1]);
+                for (int nt = 0; nt < kNT; ++nt) {
+                  mma16816<kBF16>(sc[k][nt], a0, qf[nt][2 * w][0], qf[nt][2 * w][1]);
+                  mma16816<kBF16>(odd[k][nt], a1, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
                 }
-              }
-            } else {
-              // lanes 0-7: keys 0-7, columns 0-7; 8-15: keys 8-15; 16-31: columns 8-15
-              const int row = k * 16 + (lane & 15), piece = lane >> 4;
-#pragma unroll
-              for (int s = 0; s < kSteps; ++s) {
-                uint32_t a[4];
-                ldmatrix4<false>(a, stage + (s >> 2) * (kUnit * 128) + row * 128 + ((((s & 3) * 2 + piece) ^ (row & 7)) << 4));
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(sc[k][nt], a, qf[nt][s][0], qf[nt][s][1]);
               }
             }
+          } else {
+            // lanes 0-7: keys 0-7, columns 0-7; 8-15: keys 8-15; 16-31: columns 8-15
+            const int row = lane & 15, piece = lane >> 4;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+              for (int k = 0; k < kBlocks; ++k) {
+                uint32_t a[4];
+                ldmatrix4<false>(a, stage + (s >> 2) * (kUnit * 128) + (k * 16 + row) * 128 + ((((s & 3) * 2 + piece) ^ (row & 7)) << 4));
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) mma16816<kBF16>(s & 1 ? odd[k][nt] : sc[k][nt], a, qf[nt][s][0], qf[nt][s][1]);
+              }
           }
+#pragma unroll
+          for (int k = 0; k < kBlocks; ++k)
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[k][nt][e] += odd[k][nt][e];
           // ---- which of them are seen; bit 4 k + e of the lane's scores
           [[maybe_unused]] uint32_t seen[kNT];
           if constexpr (!kFull) {
@@ -593,10 +604,15 @@ int paged_rows(int batch, int total_q, int group, int d) {
   return each <= 8 ? 8 : 16;
 }
 
-int paged_warps(int d, bool four) {
-  const int warps = d <= 64 ? (four ? RowsShape<64, 1, true>::kWarps : RowsShape<64, 1, false>::kWarps)
-                    : d <= 128 ? (four ? RowsShape<128, 1, true>::kWarps : RowsShape<128, 1, false>::kWarps)
-                               : (four ? RowsShape<256, 1, true>::kWarps : RowsShape<256, 1, false>::kWarps);
+int paged_warps(int d, bool four, int rows) {
+  auto pick = [&](auto shape_d) {
+    constexpr int kD = decltype(shape_d)::value;
+    constexpr int kTwo = kD <= 128 ? 2 : 1;
+    if (rows == 8) return four ? RowsShape<kD, 1, true>::kWarps : RowsShape<kD, 1, false>::kWarps;
+    return four ? RowsShape<kD, kTwo, true>::kWarps : RowsShape<kD, kTwo, false>::kWarps;
+  };
+  const int warps = d <= 64 ? pick(std::integral_constant<int, 64>{})
+                    : d <= 128 ? pick(std::integral_constant<int, 128>{}) : pick(std::integral_constant<int, 256>{});
   return warps * kPagedSMs;
 }
 

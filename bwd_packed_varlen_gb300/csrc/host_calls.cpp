@@ -1,4 +1,4 @@
-// Host side of the rotary, shared-prefix and paged calls, as a Python extension module.
+// Host side of the rotary, shared-prefix, paged and windowed calls, as a Python extension module.
 //
 // A decoding step's kernels take 6 to 20 microseconds, and checking the arguments, allocating
 // the outputs and marshalling thirty values from Python took 15 to 30 of them before each.
@@ -504,6 +504,105 @@ PyObject* paged_fwd(PyObject* const* a) {
   return rc != 0 ? PyLong_FromLong(rc) : pack({&out, &lse});
 }
 
+// What forward and backward with a sliding window have in common: packed tensors with four
+// cu_seqlens, or sequence-major ones with two (the padded ones None).
+struct Windowed {
+  const at::Tensor &q, &k, &v;
+  c10::DeviceIndex index;
+  int code, batch, hq, hkv, d;
+  bool packed;
+  int lq, lk;      // rows, or tokens of a batch entry
+  int tq, tk;      // rows
+  const int32_t* cu[4];
+
+  Windowed(PyObject* const* tensors, PyObject* const* lens) : q(tensor(tensors[0])), k(tensor(tensors[1])), v(tensor(tensors[2])) {
+    need(q.is_cuda(), kOneDevice);
+    index = q.device().index();
+    need(on_device(k, index) && on_device(v, index), kOneDevice);
+    need(q.is_contiguous() && k.is_contiguous() && v.is_contiguous(), "all tensors must be contiguous");
+    code = dtype_code(q);
+    need(code >= 0 && k.scalar_type() == q.scalar_type() && v.scalar_type() == q.scalar_type(),
+         "q, k, v must share one dtype, float16 or bfloat16");
+    packed = given(lens[2]);
+    const int64_t dims = packed ? 3 : 4;
+    need(q.dim() == dims && k.dim() == dims && v.sizes() == k.sizes() && k.size(dims - 1) == q.size(dims - 1),
+         packed ? "q, k and v must be [rows, heads, d], v shaped like k" : "q, k and v must be [S, B, heads, d], v shaped like k");
+    const int64_t n = tensor(lens[0]).numel();
+    need(n >= 2, "cu_seqlens must hold batch + 1 values");
+    batch = as_int(n - 1);
+    for (int i = 0; i < (packed ? 4 : 2); ++i) cu[i] = lengths(lens[i], n, index);
+    need(packed || (q.size(1) == batch && k.size(1) == batch), "q, k and v must have one batch entry per sequence");
+    hq = as_int(q.size(dims - 2));
+    hkv = as_int(k.size(dims - 2));
+    d = as_int(q.size(dims - 1));
+    lq = as_int(q.size(0));
+    lk = as_int(k.size(0));
+    tq = packed ? lq : as_int(static_cast<int64_t>(lq) * batch);
+    tk = packed ? lk : as_int(static_cast<int64_t>(lk) * batch);
+  }
+};
+
+constexpr const char* kWindowLse = "lse must be contiguous float32, one value per row and head of q, on q's device";
+using WindowSizeFn = size_t (*)(int, int, int, int, int, int);
+
+// (entry point, size function, q, k, v, cu_seqlens_q, cu_seqlens_kv, padded ones or None, scale, mask, window, sinks, out,
+// lse, workspace, stream)
+PyObject* window_fwd(PyObject* const* a) {
+  const auto size = reinterpret_cast<WindowSizeFn>(address(a[1]));
+  const Windowed p(a + 2, a + 5);
+  const float scale = static_cast<float>(number(a[9]));
+  const int mask = static_cast<int>(integer(a[10])), window = static_cast<int>(integer(a[11])), sinks = static_cast<int>(integer(a[12]));
+  const Place place(p.index, a[16]);
+  const Output out(a[13], p.q.sizes(), p.q, p.q.scalar_type(), kOutput);
+  const Output lse(a[14], p.q.sizes().slice(0, p.q.dim() - 1), p.q, at::kFloat, kWindowLse);
+  const Workspace ws(a[15], given(a[15]) ? 0 : size(p.batch, p.tq, p.tk, p.hq, p.hkv, p.d), p.q);
+  void* fn = address(a[0]);
+  const void *q = p.q.const_data_ptr(), *k = p.k.const_data_ptr(), *v = p.v.const_data_ptr();
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  if (p.packed)
+    rc = reinterpret_cast<decltype(&te_attn_window_fwd_thd)>(fn)(
+        q, k, v, out.at(), static_cast<float*>(lse.at()), p.cu[0], p.cu[1], p.cu[2], p.cu[3], p.batch, p.lq, p.lk, p.hq, p.hkv, p.d,
+        scale, mask, window, sinks, p.code, ws.at(), ws.bytes(), place.stream());
+  else
+    rc = reinterpret_cast<decltype(&te_attn_window_fwd_sbhd)>(fn)(
+        q, k, v, out.at(), static_cast<float*>(lse.at()), p.cu[0], p.cu[1], p.batch, p.lq, p.lk, p.hq, p.hkv, p.d, scale, mask, window,
+        sinks, p.code, ws.at(), ws.bytes(), place.stream());
+  Py_END_ALLOW_THREADS;
+  return rc != 0 ? PyLong_FromLong(rc) : pack({&out, &lse});
+}
+
+// (entry point, size function, q, k, v, cu_seqlens_q, cu_seqlens_kv, padded ones or None, scale, mask, window, sinks, out,
+// dout, lse, dq, dk, dv, workspace, stream)
+PyObject* window_bwd(PyObject* const* a) {
+  const auto size = reinterpret_cast<WindowSizeFn>(address(a[1]));
+  const Windowed p(a + 2, a + 5);
+  const float scale = static_cast<float>(number(a[9]));
+  const int mask = static_cast<int>(integer(a[10])), window = static_cast<int>(integer(a[11])), sinks = static_cast<int>(integer(a[12]));
+  need(given(a[13]) && given(a[14]) && given(a[15]), "the backward needs out, dout and lse");
+  const Place place(p.index, a[20]);
+  const auto type = p.q.scalar_type();
+  const Output out(a[13], p.q.sizes(), p.q, type, kOutput), dout(a[14], p.q.sizes(), p.q, type, kOutput);
+  const Output lse(a[15], p.q.sizes().slice(0, p.q.dim() - 1), p.q, at::kFloat, kWindowLse);
+  const Output dq(a[16], p.q.sizes(), p.q, type, kOutput), dk(a[17], p.k.sizes(), p.q, type, kOutput);
+  const Output dv(a[18], p.k.sizes(), p.q, type, kOutput);
+  const Workspace ws(a[19], given(a[19]) ? 0 : size(p.batch, p.tq, p.tk, p.hq, p.hkv, p.d), p.q);
+  void* fn = address(a[0]);
+  const void *q = p.q.const_data_ptr(), *k = p.k.const_data_ptr(), *v = p.v.const_data_ptr();
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  if (p.packed)
+    rc = reinterpret_cast<decltype(&te_attn_window_bwd_thd)>(fn)(
+        q, k, v, out.at(), dout.at(), static_cast<float*>(lse.at()), dq.at(), dk.at(), dv.at(), p.cu[0], p.cu[1], p.cu[2], p.cu[3],
+        p.batch, p.lq, p.lk, p.hq, p.hkv, p.d, scale, mask, window, sinks, p.code, ws.at(), ws.bytes(), place.stream());
+  else
+    rc = reinterpret_cast<decltype(&te_attn_window_bwd_sbhd)>(fn)(
+        q, k, v, out.at(), dout.at(), static_cast<float*>(lse.at()), dq.at(), dk.at(), dv.at(), p.cu[0], p.cu[1], p.batch, p.lq, p.lk,
+        p.hq, p.hkv, p.d, scale, mask, window, sinks, p.code, ws.at(), ws.bytes(), place.stream());
+  Py_END_ALLOW_THREADS;
+  return rc != 0 ? PyLong_FromLong(rc) : pack({&dq, &dk, &dv});
+}
+
 template <PyObject* (*kCall)(PyObject* const*), Py_ssize_t kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -527,6 +626,8 @@ PyMethodDef methods[] = {
     {"paged_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<paged_append, 16>)), METH_FASTCALL, nullptr},
     {"paged_gather", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<paged_gather, 12>)), METH_FASTCALL, nullptr},
     {"paged_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<paged_fwd, 16>)), METH_FASTCALL, nullptr},
+    {"window_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<window_fwd, 17>)), METH_FASTCALL, nullptr},
+    {"window_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<window_bwd, 21>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_teattn_host", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

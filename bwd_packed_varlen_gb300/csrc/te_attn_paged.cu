@@ -25,7 +25,7 @@ bool paged_layout(int batch, int total_q, int hq, int hkv, int d, bool four, Pag
     return false;
   L->rows = paged_rows(batch, total_q, hq / hkv, d);
   L->wide_rows = paged_wide_rows(batch, total_q, hq / hkv, d);
-  L->slices[0] = paged_warps(d, four);
+  L->slices[0] = paged_warps(d, four, L->rows);
   L->slices[1] = L->wide_rows > 0 ? kPagedSMs : 0;
   size_t off = kHdrWords * sizeof(int);
   auto take = [&off](size_t bytes) {

@@ -135,8 +135,10 @@ def test_refusals_in_python():
     q, cu = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.tensor([0, 4], dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
         ta.window_fwd(q, q, q, cu, cu, cu, cu, 0.1, 4)
-    with pytest.raises(ValueError, match="given"):
+    with pytest.raises(ValueError, match="tensor"):
         ta.window_fwd(q, None, q, cu, cu, cu, cu, 0.1, 4)
+    with pytest.raises(ValueError, match="padded"):
+        ta.window_fwd(q, q, q, cu, cu, None, cu, 0.1, 4)
     with pytest.raises(ValueError, match="window"):
         ta.dot_product_attention(q, q, q, cu, cu, sinks=3)
     with pytest.raises(ValueError, match="window"):
