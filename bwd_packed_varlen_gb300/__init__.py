@@ -57,6 +57,7 @@ from ._binding import (  # noqa: F401
     version,
     window_bwd,
     window_bwd_sbhd,
+    window_bwd_workspace_size,
     window_fwd,
     window_fwd_sbhd,
 )

@@ -95,6 +95,8 @@ def library(debug: bool = None) -> ctypes.CDLL:
     L.te_attn_fwd_thd_e4m3.restype = i32
     L.te_attn_fwd_thd_e4m3.argtypes = ([vp] * 5 + [vp] * 4 + [i32] * 8 + [f32] * 4 +
                                         [i32, vp, sz, vp])
+    L.te_attn_window_bwd_workspace_size.restype = sz
+    L.te_attn_window_bwd_workspace_size.argtypes = [i32] * 8
     L.te_attn_paged_fwd_workspace_size.restype = sz
     L.te_attn_paged_fwd_workspace_size.argtypes = [i32] * 6
     for name, args in (
@@ -380,7 +382,7 @@ def _entry_points():
         spec.loader.exec_module(_host)
     names = ("rope_thd", "rope_sbhd", "prefix_fwd_thd", "prefix_fwd_workspace_size", "prefix_bwd_thd",
              "prefix_bwd_workspace_size", "paged_append", "paged_gather", "paged_fwd_thd", "paged_fwd_workspace_size", "window_fwd_thd",
-             "window_bwd_thd", "window_fwd_sbhd", "window_bwd_sbhd", "fwd_workspace_size", "bwd_workspace_size")
+             "window_bwd_thd", "window_fwd_sbhd", "window_bwd_sbhd", "fwd_workspace_size", "window_bwd_workspace_size")
     _entries[_use_debug] = tuple(ctypes.cast(getattr(L, "te_attn_" + n), ctypes.c_void_p).value for n in names)
     return _entries[_use_debug]
 
@@ -465,9 +467,14 @@ def window_fwd(q, k, v, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seq
                                     lse, workspace, stream))
 
 
+def window_bwd_workspace_size(batch, total_q, total_kv, hq, hkv, d, window, sinks=0) -> int:
+    return int(library().te_attn_window_bwd_workspace_size(batch, total_q, total_kv, hq, hkv, d, _int32(window), _int32(sinks)))
+
+
 def window_bwd(q, k, v, out, dout, lse, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q_padded, cu_seqlens_kv_padded, attn_scale,
                window, sinks=0, mask_type="padding_causal", dq=None, dk=None, dv=None, workspace=None, stream=None):
-    """``te_attn_window_bwd_thd``: returns ``(dq, dk, dv)``; the workspace is :func:`bwd`'s."""
+    """``te_attn_window_bwd_thd``: returns ``(dq, dk, dv)``; the workspace is of
+    :func:`window_bwd_workspace_size` bytes."""
     if cu_seqlens_q_padded is None:
         raise ValueError("packed tokens need cu_seqlens_q_padded")
     e = _entries.get(_use_debug) or _entry_points()

@@ -109,6 +109,25 @@ struct DkdvShape {
   static_assert(kStages >= 1, "shared memory budget");
 };
 
+// fp32 sums of a cut sweep (dK not scaled yet) from TMEM: kCols columns of dK and dV of this
+// lane's row, of which the first `left` exist.
+template <int kCols>
+__device__ __forceinline__ void store_sums(uint32_t tmem, float* dk, float* dv, int left) {
+#pragma unroll
+  for (int c = 0; c < kCols; c += 16) {
+    uint32_t a[16], b[16];
+    tmem_ld16(tmem + c, a);        // dK's columns begin at 0, dV's at 128
+    tmem_ld16(tmem + 128 + c, b);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      if (c + e >= left) continue;
+      *reinterpret_cast<uint4*>(dk + c + e) = make_uint4(a[e], a[e + 1], a[e + 2], a[e + 3]);
+      *reinterpret_cast<uint4*>(dv + c + e) = make_uint4(b[e], b[e + 1], b[e + 2], b[e + 3]);
+    }
+  }
+}
+
 template <int kD, bool kBF16, class P = AttnParams>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_bwd_dkdv_kernel(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tmQ,
@@ -130,6 +149,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __shared__ uint64_t bar_q_full[NS], bar_q_empty[NS];
   __shared__ uint64_t bar_s_full, bar_dp_full, bar_p_ready, bar_ds_ready;
   __shared__ WorkRing ring;
+  // With a window, where the sums of a cut sweep go (-1: the sweep is whole), for the epilogue: in a
+  // register of the compute warps it would cost spills. Item ii + 4 is handed over behind item
+  // ii's epilogue.
+  __shared__ int s_slot[is_window<P> ? 4 : 1];
   __shared__ uint32_t tmem_slot;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -139,13 +162,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // and rows complete: it needs nothing of dQ, and takes SMs as dQ's blocks leave them. It
   // reads those lists without a wait of its own, so it must follow dQ and nothing else, and dQ
   // must trigger behind its wait.
-  if constexpr (is_prefix<P>) pdl_trigger();
+  // (A windowed backward is launched the same way.)
+  constexpr bool kDependent = is_prefix<P> || is_window<P>;
+  if constexpr (kDependent) pdl_trigger();
   const int n_pairs = p.header[kHdrNumKPairs];
   // Items of the prefix come first: they are the longest.
   constexpr bool kPrefix = is_prefix<P>;
   const int pre_keys = prefix_keys_of(p);
   int n_pre = 0;
   if constexpr (kPrefix) n_pre = (pre_keys + kBlockN - 1) / kBlockN * per_pair * p.splits;
+  // so do the parts of cut sweeps over sinks
+  constexpr bool kWindow = is_window<P>;
+  if constexpr (kWindow) n_pre = p.header[kHdrSinkSlots] * per_pair;
   const int n_items = n_pre + n_pairs * per_pair;
   const bool causal = p.causal != 0;
   const int sh = pack_shift(p), vgroup = virtual_group(p);
@@ -181,11 +209,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int b, kt, g, split, qt0, nq, steps;
     bool pre;  // prefix keys; the steps are [t0, t0 + steps) of the sweep over all rows
     int t0, part;
+    int slot;  // with a window: where the sums of a cut sweep go; -1: the sweep is whole
   };
   auto decode = [&](int item) {
     Item it;
     it.pre = false;
     it.t0 = it.part = 0;
+    it.slot = -1;
+    constexpr int kPerTile = kBlockM / kBM;
+    if constexpr (kWindow) {
+      if (item < n_pre) {
+        it.slot = item / per_pair;
+        const int4 e = p.slots[it.slot];
+        it.g = item % per_pair / S::kSplit;
+        it.split = item % S::kSplit;
+        it.b = e.x;
+        it.kt = e.y;
+        it.s = load_seq(p, e.x);
+        const int q0 = sweep_of(p, it.s, e.y).end + e.z * p.sweep_tiles;
+        it.qt0 = q0 * kPerTile;
+        it.nq = min((it.s.len_q + kBM - 1) / kBM, (q0 + p.sweep_tiles) * kPerTile);
+        // (the entry of the sweep's begin is no item here)
+        it.steps = e.z < 0 ? 0 : vgroup * (it.nq - it.qt0);
+        return it;
+      }
+      item -= n_pre;
+    }
     if constexpr (kPrefix) {
       if (item < n_pre) {
         // parts of one key tile and head side by side: they share its K and V
@@ -215,6 +264,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     it.s = load_seq(p, pr.x);
     it.qt0 = (first_query(it.s, it.kt * kBlockN, causal) << sh) / kBM;
     it.nq = ((tile_last_query(p, it.s, it.kt) << sh) + kBM - 1) / kBM;
+    if constexpr (kWindow) {
+      const Sweep w = sweep_of(p, it.s, it.kt);
+      if (w.parts > 0) {
+        it.nq = w.end * kPerTile;
+        it.slot = p.pref_s[pr.x] + slots_before(p, it.s, it.kt);
+      }
+    }
     it.steps = vgroup * (it.nq - it.qt0);
     return it;
   };
@@ -230,12 +286,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bool ok = true;
       int nxt = blockIdx.x;
       for (; ok; ++ii) {
-        const int item = nxt < n_items ? nxt : -1;
+        int item = nxt < n_items ? nxt : -1;
+        Item I;
+        while (item >= 0) {
+          I = decode(item);
+          if (!kWindow || I.steps > 0) break;
+          nxt = next_item(p.header + kHdrNextDkdv);
+          item = nxt < n_items ? nxt : -1;
+        }
         if (item < 0) {
           ok = ring_put(ring, ii, -1, status);
           break;
         }
-        const Item I = decode(item);
+        if constexpr (kWindow) *const_cast<volatile int*>(&s_slot[ii & 3]) = I.slot;
         // step count and column half travel with the item: the MMA thread then
         // needs no global loads (which would queue behind the dK/dV row stores)
         if (!(ok = ring_put(ring, ii, item, status, I.steps | (I.split << 24)))) break;
@@ -527,6 +590,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const size_t kv_off = (kv_tok * p.hkv + I.g) * p.d;
       const int col_out = I.split * S::kDo;
       constexpr int kOutCols = S::kDo / kColGroups;
+      if constexpr (kWindow) {
+        const int slot = *const_cast<volatile int*>(&s_slot[ii & 3]);
+        if (slot >= 0) {
+          const size_t at = ((static_cast<size_t>(slot) * p.hkv + I.g) * kBlockN + quarter * 32 + lane) * p.d + col_out + grp * kOutCols;
+          store_sums<kOutCols>(tmem + lane_base + grp * kOutCols, p.part_dk + at, p.part_dv + at, store ? p.d - col_out - grp * kOutCols : 0);
+          tc_fence_before();
+          mbar_arrive(&bar_acc_empty);
+          continue;
+        }
+      }
       if constexpr (kPrefix) {
         if (I.pre && p.splits > 1) {
           // fp32 partial sums (dK not scaled yet); the reduction rounds once
@@ -574,7 +647,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if constexpr (kPrefix) pdl_wait();  // complete only after dQ, for what follows in the stream
+  if constexpr (kDependent) pdl_wait();  // complete only after dQ, for what follows in the stream
 }
 
 // ===========================================================================
@@ -646,7 +719,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     n_pairs = p.header[kHdrNumQPairs];
     n_items = n_pairs * virtual_heads(p);
   };
-  if constexpr (!kPrefix) read_lists();
+  constexpr bool kDependent = kPrefix || is_window<P>;
+  if constexpr (!kDependent) read_lists();
   const bool causal = p.causal != 0;
   const int sh = pack_shift(p), vgroup = virtual_group(p);
   const int pre_keys = prefix_keys_of(p);
@@ -680,7 +754,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  if constexpr (kPrefix) {
+  if constexpr (kDependent) {
     // set up while the rows are prepared; the trigger comes behind the wait, because dK/dV
     // starts on it and takes lists and rows to be complete
     pdl_wait();
@@ -1010,6 +1084,51 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // ===========================================================================
+// Sums of cut sweeps
+// ===========================================================================
+// dK and dV of a sink tile: the parts of its sweep added in order, in fp32, rounded once. A block
+// takes a quarter of a tile's rows of one kv head; four columns a thread.
+template <bool kBF16>
+__global__ void __launch_bounds__(256) window_sum_kernel(const __grid_constant__ WindowParams p) {
+  pdl_wait();
+  if (static_cast<int>(blockIdx.x) >= p.header[kHdrSinkSlots]) return;
+  const int4 e = p.slots[blockIdx.x];
+  if (e.z >= 0) return;  // the entry of the sweep's begin stands for the tile
+  const SeqInfo s = load_seq(p, e.x);
+  const int g = blockIdx.y, cols = p.d / 4;
+  const int rows = min(kBlockN, seen_keys(s, true) - e.y * kBlockN);
+  const size_t step = static_cast<size_t>(p.hkv) * kBlockN * p.d;
+  for (int n = blockIdx.z * 256 + threadIdx.x; n < rows * cols; n += 256 * gridDim.z) {
+    const int r = n / cols, c = (n - r * cols) * 4;
+    const size_t at = (static_cast<size_t>(blockIdx.x) * p.hkv + g) * kBlockN * p.d + static_cast<size_t>(r) * p.d + c;
+    float k[4] = {}, v[4] = {};
+    // (keys that are no sinks have nothing from the later parts)
+    const int parts = e.y * kBlockN + r < p.sinks ? e.w + 1 : 1;
+    for (int i = 0; i < parts; ++i) {
+      const float4 a = *reinterpret_cast<const float4*>(p.part_dk + at + i * step), b = *reinterpret_cast<const float4*>(p.part_dv + at + i * step);
+      k[0] += a.x;
+      k[1] += a.y;
+      k[2] += a.z;
+      k[3] += a.w;
+      v[0] += b.x;
+      v[1] += b.y;
+      v[2] += b.z;
+      v[3] += b.w;
+    }
+    const size_t out = (k_row(p, s, e.y * kBlockN + r) * p.hkv + g) * p.d + c;
+    if (!bounds_ok(out < static_cast<size_t>(p.total_kv) * p.hkv * p.d, p.header + kHdrStatus)) continue;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dk) + out) =
+        make_uint2(pack2<kBF16>(k[0] * p.scale, k[1] * p.scale), pack2<kBF16>(k[2] * p.scale, k[3] * p.scale));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dv) + out) = make_uint2(pack2<kBF16>(v[0], v[1]), pack2<kBF16>(v[2], v[3]));
+  }
+}
+
+cudaError_t launch_window_sum(const WindowParams& p, bool bf16, cudaStream_t st) {
+  const dim3 grid(p.cap_slots, p.hkv, 4);
+  return launch_dependent(bf16 ? window_sum_kernel<true> : window_sum_kernel<false>, grid, dim3(256), 0, st, p);
+}
+
+// ===========================================================================
 // Launchers
 // ===========================================================================
 template <int kD, bool kBF16, class P = AttnParams>
@@ -1025,8 +1144,10 @@ static cudaError_t launch_dkdv_impl(const P& p, int num_sms, cudaStream_t st) {
   auto kern = attn_bwd_dkdv_kernel<kD, kBF16, P>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes);
   if (e != cudaSuccess) return e;
-  const long long max_items = static_cast<long long>(p.pair_cap_k) * p.hkv * S::kSplit;
+  long long max_items = static_cast<long long>(p.pair_cap_k) * p.hkv * S::kSplit;
+  if constexpr (is_window<P>) max_items += static_cast<long long>(p.cap_slots) * p.hkv * S::kSplit;
   const int grid = static_cast<int>(max_items < num_sms ? (max_items > 0 ? max_items : 1) : num_sms);
+  if constexpr (is_window<P>) return launch_dependent(kern, grid, kBwdThreads, S::kSmemBytes, st, p, tq, tdo, tk, tv);
   kern<<<grid, kBwdThreads, S::kSmemBytes, st>>>(p, tq, tdo, tk, tv);
   return cudaGetLastError();
 }
@@ -1046,6 +1167,7 @@ static cudaError_t launch_dq_impl(const P& p, int num_sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const long long max_items = static_cast<long long>(p.pair_cap_q) * p.hq;
   const int grid = static_cast<int>(max_items < num_sms ? (max_items > 0 ? max_items : 1) : num_sms);
+  if constexpr (is_window<P>) return launch_dependent(kern, grid, kBwdThreads, S::kSmemBytes, st, p, tq, tdo, tk, tv);
   kern<<<grid, kBwdThreads, S::kSmemBytes, st>>>(p, tq, tdo, tk, tv);
   return cudaGetLastError();
 }

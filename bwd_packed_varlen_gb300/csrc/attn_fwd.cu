@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 #include "sm103_ptx.cuh"
 #include "tmap.h"
 #include "window.cuh"
@@ -72,8 +73,10 @@ __global__ void __launch_bounds__(192, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* status = p.header + kHdrStatus;
-  const int n_pairs = p.header[kHdrNumQPairs];
-  const int n_items = n_pairs * p.hq;
+  // with a window the kernel is launched while the scheduler runs, and waits for its lists below
+  if constexpr (is_window<P>) pdl_trigger();
+  int n_pairs = is_window<P> ? 0 : p.header[kHdrNumQPairs];
+  int n_items = n_pairs * p.hq;
   const bool causal = p.causal != 0;
 
   if (tid == 0) {
@@ -104,6 +107,11 @@ __global__ void __launch_bounds__(192, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const uint32_t t_o = tmem;
+  if constexpr (is_window<P>) {
+    pdl_wait();
+    n_pairs = p.header[kHdrNumQPairs];
+    n_items = n_pairs * p.hq;
+  }
 
   if (warp == 4) {
     // ------------------------------------------------------------- TMA producer
@@ -402,6 +410,7 @@ static cudaError_t launch_fwd_impl(const P& p, int num_sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const long long max_items = static_cast<long long>(p.pair_cap_q) * p.hq;
   const int grid = static_cast<int>(max_items < num_sms ? (max_items > 0 ? max_items : 1) : num_sms);
+  if constexpr (is_window<P>) return launch_dependent(kern, grid, 192, S::kSmemBytes, st, p, tq, tk, tv);
   kern<<<grid, 192, S::kSmemBytes, st>>>(p, tq, tk, tv);
   return cudaGetLastError();
 }

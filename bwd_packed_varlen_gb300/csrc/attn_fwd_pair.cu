@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 #include "row_store.cuh"
 #include "sm103_ptx.cuh"
 #include "tmap.h"
@@ -72,6 +73,7 @@ struct FwdItem {
   int n[2];      // key tiles tile A / tile B visit (0: tile absent)
   int nmax;
   TileRun run;   // the key tiles of both: tile A's window begins first, tile B's ends last
+  int skip;      // step at which tile B sees no key (its window begins a tile later); -1: none
   bool whole[2];  // tile rows lie inside the sequence's padded rows (TMA store allowed)
 };
 
@@ -94,12 +96,17 @@ __device__ __forceinline__ FwdItem fwd_item(const P& p, int item, bool causal) {
   I.n[1] = tb * kBlockM < I.s.len_q ? (visible_keys(I.s, tb, causal) + kBlockN - 1) / kBlockN : 0;
   I.nmax = I.n[0] > I.n[1] ? I.n[0] : I.n[1];
   I.run = TileRun{0, 0, I.nmax};
+  I.skip = -1;
   if constexpr (is_window<P>) {
     const int hi = max(visible_keys(I.s, ta, causal), I.n[1] > 0 ? visible_keys(I.s, tb, causal) : 0);
     I.run = tile_run(p, I.s, ta * kBlockM, hi, kBlockN);
     for (int x = 0; x < 2; ++x)
       I.n[x] = min(I.n[x], I.run.sink_tiles) + max(0, I.n[x] - max(I.run.first, I.run.sink_tiles));
     I.nmax = I.n[0] > I.n[1] ? I.n[0] : I.n[1];
+    // (only where tile B has steps behind that one)
+    if (I.n[1] > I.run.sink_tiles + 1 && window_first(p, I.s, tb * kBlockM) >= (I.run.first + 1) * kBlockN &&
+        p.sinks <= I.run.first * kBlockN)
+      I.skip = I.run.sink_tiles;
   }
   // the store box may not reach into the next sequence's rows; sequence-major
   // tensors keep every sequence in its own batch entry (the box is clipped there)
@@ -134,7 +141,9 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* status = p.header + kHdrStatus;
-  const int n_items = p.header[kHdrNumFPairs] * p.hq;
+  // with a window the kernel is launched while the scheduler runs, and waits for its lists below
+  if constexpr (is_window<P>) pdl_trigger();
+  int n_items = is_window<P> ? 0 : p.header[kHdrNumFPairs] * p.hq;
   const bool causal = p.causal != 0;
 
   if (tid == 0) {
@@ -166,6 +175,10 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  if constexpr (is_window<P>) {
+    pdl_wait();
+    n_items = p.header[kHdrNumFPairs] * p.hq;
+  }
 
   if (warp == kFwdWarpProducer) {
     // ------------------------------------------------------------- TMA producer
@@ -193,7 +206,8 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
         }
         // both tiles' key-tile counts travel with the item: the MMA thread then
         // needs no global loads (which would queue behind the softmax warps' O stores)
-        if (!(ok = ring_put(ring, ii, item, status, I.n[0] | (I.n[1] << 16)))) break;
+        if (!(ok = ring_put(ring, ii, item, status, I.n[0] | (I.n[1] << 16),
+                            I.skip))) break;
         nxt = next_item(p.header + kHdrNextFwd);  // used at the next hand-over
         if (ii > 0 && !(ok = mbar_wait(&bar_q_empty, (ii - 1) & 1, status))) break;
         const int ntiles = I.n[1] > 0 ? 2 : 1;
@@ -231,6 +245,7 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
       int np[2] = {0, 0};  // P hand-overs consumed per tile
       int no[2] = {0, 0};  // items in which the tile was present
       bool ok = true;
+      int skip = -1;  // with a window: the step that tile B leaves out
       // S_x = Q_x K^T for the key tile in ring stage st.
       auto issue_s = [&](int x, int st) {
         const SmemDesc qx{dq.lo + ((x * S::kQKBytes) >> 4), dq.hi};
@@ -251,9 +266,11 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
         int n[2], nmax;
       } I;
       for (int ii = 0; ok; ++ii) {
-        int counts = 0;
-        const int item = ring_get_warp_once(ring, ii, status, &ok, &counts);
+        int counts = 0, more = 0;
+        const int item = ring_get_warp_once(ring, ii, status, &ok, &counts, is_window<P> ? &more : nullptr);
         if (!ok || item < 0) break;
+        if constexpr (is_window<P>) skip = more;
+        bool first[2] = {true, true};  // the next product is the tile's first of the item
         I.n[0] = counts & 0xffff;
         I.n[1] = counts >> 16;
         I.nmax = I.n[0] > I.n[1] ? I.n[0] : I.n[1];
@@ -261,7 +278,7 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
         if (!(ok = mbar_wait_warp(&bar_k_full[it % NS], (it / NS) & 1, status))) break;
         tc_fence_after();
         for (int x = 0; x < 2; ++x)
-          if (I.n[x] > 0) issue_s(x, it % NS);
+          if (I.n[x] > 0 && !(x == 1 && skip == 0)) issue_s(x, it % NS);
         mma_commit(&bar_k_empty[it % NS]);
         if (I.nmax == 1) mma_commit(&bar_q_empty);
         for (int j = 0; j < I.nmax && ok; ++j) {
@@ -269,22 +286,27 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
           bool v_ready = false, k_ready = false;
           for (int x = 0; x < 2 && ok; ++x) {
             if (j >= I.n[x]) continue;
-            if (!(ok = mbar_wait_warp(&bar_p_ready[x], np[x] & 1, status))) break;
-            ++np[x];
-            if (j == 0 && no[x] > 0 && !(ok = mbar_wait_warp(&bar_o_empty[x], (no[x] - 1) & 1, status))) break;
-            if (!v_ready) {
-              if (!(ok = mbar_wait_warp(&bar_v_full[st], (cur / NS) & 1, status))) break;
-              v_ready = true;
-            }
-            tc_fence_after();
-            const SmemDesc vst{dv.lo + ((st * S::kVBytes) >> 4), dv.hi};
-            const uint32_t acc0 = j > 0 ? 1u : 0u;
-            __syncwarp();  // elect.sync in the MMA wrappers needs a converged warp
+            const bool left_out = is_window<P> && x == 1 && j == skip;
+            if (!left_out) {
+              if (!(ok = mbar_wait_warp(&bar_p_ready[x], np[x] & 1, status))) break;
+              ++np[x];
+              if (first[x] && no[x] > 0 && !(ok = mbar_wait_warp(&bar_o_empty[x], (no[x] - 1) & 1, status))) break;
+              if (!v_ready) {
+                if (!(ok = mbar_wait_warp(&bar_v_full[st], (cur / NS) & 1, status))) break;
+                v_ready = true;
+              }
+              tc_fence_after();
+              const SmemDesc vst{dv.lo + ((st * S::kVBytes) >> 4), dv.hi};
+              const uint32_t acc0 = first[x] ? 0u : 1u;
+              first[x] = false;
+              __syncwarp();  // elect.sync in the MMA wrappers needs a converged warp
 #pragma unroll
-            for (int s = 0; s < kBlockN / 16; ++s)
-              mma_ts(tmem + S::col_o(x), tmem + S::col_s(x) + s * 8, vst, s * 2048, idPV,
-                     s > 0 ? 1u : acc0);
+              for (int s = 0; s < kBlockN / 16; ++s)
+                mma_ts(tmem + S::col_o(x), tmem + S::col_s(x) + s * 8, vst, s * 2048, idPV,
+                       s > 0 ? 1u : acc0);
+            }
             if (j + 1 < I.n[x]) {
+              if (is_window<P> && x == 1 && j + 1 == skip) continue;
               const int nx = cur + 1;
               if (!k_ready) {
                 if (!(ok = mbar_wait_warp(&bar_k_full[nx % NS], (nx / NS) & 1, status))) break;
@@ -329,10 +351,11 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
       bool tma;          // this tile's O leaves through the staged TMA store
       int h, tb, tok0;   // store coordinates of this tile
       TileRun run;       // with a window: the item's key tiles,
-      RowWindow win;     // and which of their keys the row sees
+      RowWindow win;     // which of their keys the row sees, and the step this tile leaves out
+      int skip;
     };
     auto decode = [&](int item) {
-      RowItem r{item, 0, 0, false, 0, 0, 0, false, 0, 0, 0, {0, 0, 0}, {0, 0}};
+      RowItem r{item, 0, 0, false, 0, 0, 0, false, 0, 0, 0, {0, 0, 0}, {0, 0}, -1};
       if (item < 0) return r;
       const FwdItem I = fwd_item(p, item, causal);
       r.n = I.n[x];
@@ -347,6 +370,7 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
       // rows that see no key (before a lower-right triangle) are the zero fill's
       r.lim = row < I.s.len_q ? row_keys(I.s, row, causal) : 0;
       r.run = I.run;
+      r.skip = x == 1 ? I.skip : -1;
       r.win = row_window(p, I.s, row);
       r.out_row = q_row(p, I.s, row) * p.hq + I.h;
       r.row_valid = r.lim > 0 &&
@@ -365,6 +389,7 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
       const bool row_valid = cur.row_valid;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
+        if (is_window<P> && j == cur.skip) continue;
         ok = __all_sync(0xffffffffu, mbar_wait(&bar_s_full[x], ns & 1, status));
         if (!ok) break;
         ++ns;
@@ -580,6 +605,7 @@ static cudaError_t launch_fwd_pair_impl(const P& p, int num_sms, cudaStream_t st
   if (e != cudaSuccess) return e;
   const long long max_items = static_cast<long long>(p.pair_cap_f) * p.hq;
   const int grid = static_cast<int>(max_items < num_sms ? (max_items > 0 ? max_items : 1) : num_sms);
+  if constexpr (is_window<P>) return launch_dependent(kern, grid, kFwdPairThreads, S::kSmemBytes, st, p, tq, tk, tv, to);
   kern<<<grid, kFwdPairThreads, S::kSmemBytes, st>>>(p, tq, tk, tv, to);
   return cudaGetLastError();
 }

@@ -29,6 +29,7 @@ enum HeaderWord : int {
   kHdrPrefixChunks = 13,  // prefix: chunks (0: none, -1: no row has a result), first partial
   kHdrPrefixSlot = 14,    // row, rows
   kHdrPrefixRows = 15,
+  kHdrSinkSlots = 16,  // windowed backward: partial results of sink tiles
   kHdrWords = 64     // header size in int32 words (256 bytes, keeps alignment)
 };
 

@@ -575,7 +575,7 @@ PyObject* window_fwd(PyObject* const* a) {
 // (entry point, size function, q, k, v, cu_seqlens_q, cu_seqlens_kv, padded ones or None, scale, mask, window, sinks, out,
 // dout, lse, dq, dk, dv, workspace, stream)
 PyObject* window_bwd(PyObject* const* a) {
-  const auto size = reinterpret_cast<WindowSizeFn>(address(a[1]));
+  const auto size = reinterpret_cast<decltype(&te_attn_window_bwd_workspace_size)>(address(a[1]));
   const Windowed p(a + 2, a + 5);
   const float scale = static_cast<float>(number(a[9]));
   const int mask = static_cast<int>(integer(a[10])), window = static_cast<int>(integer(a[11])), sinks = static_cast<int>(integer(a[12]));
@@ -586,7 +586,7 @@ PyObject* window_bwd(PyObject* const* a) {
   const Output lse(a[15], p.q.sizes().slice(0, p.q.dim() - 1), p.q, at::kFloat, kWindowLse);
   const Output dq(a[16], p.q.sizes(), p.q, type, kOutput), dk(a[17], p.k.sizes(), p.q, type, kOutput);
   const Output dv(a[18], p.k.sizes(), p.q, type, kOutput);
-  const Workspace ws(a[19], given(a[19]) ? 0 : size(p.batch, p.tq, p.tk, p.hq, p.hkv, p.d), p.q);
+  const Workspace ws(a[19], given(a[19]) ? 0 : size(p.batch, p.tq, p.tk, p.hq, p.hkv, p.d, window, sinks), p.q);
   void* fn = address(a[0]);
   const void *q = p.q.const_data_ptr(), *k = p.k.const_data_ptr(), *v = p.v.const_data_ptr();
   int rc;

@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "pdl.cuh"
 #include "window.cuh"
 
 namespace teattn {
@@ -86,7 +87,7 @@ template <class P>
 __device__ int k_pair_cost(const P& p, int b, int t) {
   SeqInfo s = load_seq(p, b);
   t = key_tiles(p, s).tile(t);
-  int nq = (tile_last_query(p, s, t) + kBlockM - 1) / kBlockM;
+  const int nq = sweep_of(p, s, t).end;
   return nq - first_query(s, t * kBlockN, p.causal) / kBlockM;
 }
 
@@ -266,6 +267,8 @@ template <class P>
 __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(P p, int* pref_q,
                                                                   int* pref_k, int* pref_f) {
   extern __shared__ uint64_t sort_keys[];
+  // (the later kernels of a windowed call are launched while the ones ahead of them run)
+  if constexpr (is_window<P>) pdl_trigger();
   __shared__ int warp_sums[32];
   __shared__ int bad;
   if (threadIdx.x == 0) bad = 0;
@@ -300,6 +303,34 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(P p, int* pref_
     pref_q[p.batch] = carry_q;
     pref_k[p.batch] = carry_k;
     pref_f[p.batch] = carry_f;
+  }
+  if constexpr (is_window<P>) {
+    if (p.sweep_tiles > 0) {
+      int carry = 0;
+      for (int base = 0; base < p.batch; base += blockDim.x) {
+        const int b = base + threadIdx.x;
+        SeqInfo s{};
+        int n = 0;
+        if (b < p.batch) {
+          s = load_seq(p, b);
+          if (s.len_q > 0 && s.len_k > 0) n = slots_before(p, s, kSplitSinkTiles);
+        }
+        int total;
+        int at = carry + block_excl_scan(n, warp_sums, &total);
+        if (b < p.batch) {
+          p.pref_s[b] = at;
+          for (int kt = 0; n > 0 && kt < kSplitSinkTiles && kt * kBlockN < p.sinks; ++kt) {
+            const Sweep w = sweep_of(p, s, kt);
+            for (int part = -1; w.parts > 0 && part < w.parts; ++part, ++at, --n)
+              if (at < p.cap_slots) p.slots[at] = make_int4(b, kt, part, w.parts);
+          }
+        }
+        carry += total;
+      }
+      if (threadIdx.x == 0) p.header[kHdrSinkSlots] = min(carry, p.cap_slots);
+    } else if (threadIdx.x == 0) {
+      p.header[kHdrSinkSlots] = 0;
+    }
   }
   __threadfence_block();
   __syncthreads();
@@ -384,6 +415,10 @@ __device__ __forceinline__ void zero_row(void* base, long long r, int row_bytes)
 // mode 0: forward (out, lse); mode 1: backward (dq, dk, dv)
 template <class P>
 __global__ void __launch_bounds__(256) zero_fill_kernel(P p, int mode) {
+  if constexpr (is_window<P>) {
+    pdl_trigger();
+    if (mode == 0) pdl_wait();  // the forward's tiles also write rows that are none
+  }
   const int b = blockIdx.x;
   const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
   const int w0 = blockIdx.y * nw + (threadIdx.x >> 5), wstep = nw * gridDim.y;
@@ -445,6 +480,8 @@ __global__ void __launch_bounds__(256) zero_fill_kernel(P p, int mode) {
     const size_t bid = static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x;
     for (size_t i = bid * blockDim.x + threadIdx.x; i < n; i += stride) p.dq_sem[i] = 0;
   }
+  if constexpr (is_window<P>)
+    if (mode == 1) pdl_wait();  // complete only after the scheduler
 }
 
 template <class P>
@@ -453,6 +490,7 @@ static cudaError_t launch_zero_fill_impl(const P& p, int mode, int num_sms, cuda
   // so that about four blocks per SM share the rows of few long sequences
   const int nb = p.batch + 1;
   const int y = std::max(1, std::min(65535, (num_sms * 4 + nb - 1) / nb));
+  if constexpr (is_window<P>) return launch_dependent(zero_fill_kernel<P>, dim3(nb, y), dim3(256), 0, st, p, mode);
   zero_fill_kernel<P><<<dim3(nb, y), 256, 0, st>>>(p, mode);
   return cudaGetLastError();
 }
@@ -483,8 +521,12 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   return s;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) delta_kernel(AttnParams p) {
+template <typename T, class P>
+__global__ void __launch_bounds__(256) delta_kernel(P p) {
+  if constexpr (is_window<P>) {
+    pdl_trigger();
+    pdl_wait();
+  }
   const int warps = (gridDim.x * blockDim.x) >> 5;
   const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
@@ -542,10 +584,14 @@ __global__ void __launch_bounds__(256) delta_kernel(AttnParams p) {
 
 cudaError_t launch_delta(const AttnParams& p, bool bf16, int num_sms, cudaStream_t st) {
   if (bf16)
-    delta_kernel<__nv_bfloat16><<<num_sms * 8, 256, 0, st>>>(p);
+    delta_kernel<__nv_bfloat16, AttnParams><<<num_sms * 8, 256, 0, st>>>(p);
   else
-    delta_kernel<__half><<<num_sms * 8, 256, 0, st>>>(p);
+    delta_kernel<__half, AttnParams><<<num_sms * 8, 256, 0, st>>>(p);
   return cudaGetLastError();
+}
+cudaError_t launch_window_delta(const WindowParams& p, bool bf16, int num_sms, cudaStream_t st) {
+  return launch_dependent(bf16 ? delta_kernel<__nv_bfloat16, WindowParams> : delta_kernel<__half, WindowParams>, dim3(num_sms * 8), dim3(256),
+                          0, st, p);
 }
 
 // ---------------------------------------------------------------------------

@@ -315,6 +315,35 @@ static int check_window(const Window& w, int mask_type, int total_q, int total_k
   return TE_OK;
 }
 
+// Sections that a windowed backward adds behind the layout, where sinks make it cut sweeps: a
+// sequence with a cut sweep has more than sweep_tiles query tiles, and of n query tiles at most
+// n / sweep_tiles + 1 parts and the begin.
+struct SinkLayout {
+  size_t pref, slots, dk, dv, total;
+  long long cap;
+};
+SinkLayout sink_layout(const Layout& L, int batch, int total_q, int hkv, int d, const Window& w) {
+  SinkLayout S{L.total, L.total, L.total, L.total, L.total, 0};
+  const int tiles = teattn::sweep_tiles_of(w.window);
+  const long long q_tiles = total_q / teattn::kBlockM;
+  if (!w.on || w.sinks < 1 || q_tiles < tiles) return S;
+  const long long sink_tiles = w.sinks > teattn::kBlockN ? teattn::kSplitSinkTiles : 1;
+  S.cap = sink_tiles * 3 * (q_tiles / tiles + 1);
+  size_t off = L.total;
+  auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  S.pref = take((static_cast<size_t>(batch) + 1) * sizeof(int));
+  S.slots = take(static_cast<size_t>(S.cap) * sizeof(int4));
+  const size_t part = static_cast<size_t>(S.cap) * hkv * teattn::kBlockN * d * sizeof(float);
+  S.dk = take(part);
+  S.dv = take(part);
+  S.total = off;
+  return S;
+}
+
 static teattn::WindowParams window_params(const teattn::AttnParams& p, const Window& w) {
   teattn::WindowParams q{};
   static_cast<teattn::AttnParams&>(q) = p;
@@ -513,9 +542,12 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* out
   Layout L;
   if (!make_layout(batch, total_q, total_kv, hq, true, &L, cols, hkv))
     return fail(TE_ERR_INVALID_ARG, "sizes out of range");
-  if (workspace_bytes < L.total)
+  // (a window, or sinks, of 2^30 leave every key that the mask does)
+  win.window = win.window < teattn::kWindowLimit ? win.window : teattn::kWindowLimit;
+  const SinkLayout K = sink_layout(L, batch, total_q, hkv, d, win);
+  if (workspace_bytes < K.total)
     return fail(TE_ERR_WORKSPACE_TOO_SMALL,
-                fused ? "workspace smaller than te_attn_bwd_fused_workspace_size()"
+                win.on ? "workspace smaller than te_attn_window_bwd_workspace_size()" : fused ? "workspace smaller than te_attn_bwd_fused_workspace_size()"
                       : "workspace smaller than te_attn_bwd_workspace_size()");
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return fail(TE_ERR_CUDA, "no CUDA device");
@@ -550,7 +582,15 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* out
   p.pref_q = pref_q;
   int* pref_k = reinterpret_cast<int*>(ws + L.pref_k);
   const bool bf16 = dtype == TE_DTYPE_BF16;
-  const teattn::WindowParams pw = window_params(p, win);
+  teattn::WindowParams pw = window_params(p, win);
+  if (K.cap > 0) {
+    pw.sweep_tiles = teattn::sweep_tiles_of(pw.window);
+    pw.pref_s = reinterpret_cast<int*>(ws + K.pref);
+    pw.slots = reinterpret_cast<int4*>(ws + K.slots);
+    pw.part_dk = reinterpret_cast<float*>(ws + K.dk);
+    pw.part_dv = reinterpret_cast<float*>(ws + K.dv);
+    pw.cap_slots = static_cast<int>(K.cap);
+  }
   cudaError_t e = timed(TE_KERNEL_SCHEDULE, st, [&] {
     int* pref_f = reinterpret_cast<int*>(ws + L.pref_f);
     return win.on ? teattn::launch_window_schedule(pw, pref_q, pref_k, pref_f, st)
@@ -564,7 +604,9 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* out
   });
   if (e != cudaSuccess) return cuda_fail(e, "zero fill");
   if (total_q > 0) {
-    e = timed(TE_KERNEL_DELTA, st, [&] { return teattn::launch_delta(p, bf16, sms, st); });
+    e = timed(TE_KERNEL_DELTA, st, [&] {
+      return win.on ? teattn::launch_window_delta(pw, bf16, sms, st) : teattn::launch_delta(p, bf16, sms, st);
+    });
     if (e != cudaSuccess) return cuda_fail(e, "delta");
   }
   if (fused) {
@@ -596,6 +638,10 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* out
                     : teattn::launch_attn_bwd_dkdv(p, bf16, sms, st);
     });
     if (e != cudaSuccess) return cuda_fail(e, "dK/dV");
+    if (K.cap > 0) {
+      e = timed(TE_KERNEL_DKDV, st, [&] { return teattn::launch_window_sum(pw, bf16, st); });
+      if (e != cudaSuccess) return cuda_fail(e, "sum of cut sweeps");
+    }
   }
   return ok_status();
 }
@@ -651,6 +697,12 @@ int te_attn_bwd_sbhd(const void* q, const void* k, const void* v, const void* ou
   return bwd_impl(q, k, v, out, dout, lse, dq, dk, dv, cu_seqlens_q, cu_seqlens_kv, cu_seqlens_q,
                   cu_seqlens_kv, batch, tq, tk, hq, hkv, d, attn_scale, mask_type, dtype, workspace,
                   workspace_bytes, stream, nullptr, true);
+}
+
+size_t te_attn_window_bwd_workspace_size(int batch, int total_q, int total_kv, int hq, int hkv, int d, int window, int sinks) {
+  Layout L;
+  if (window < 1 || sinks < 0 || hkv < 1 || d < 1 || !make_layout(batch, total_q, total_kv, hq, true, &L)) return 0;
+  return sink_layout(L, batch, total_q, hkv, d, Window{true, window < teattn::kWindowLimit ? window : teattn::kWindowLimit, sinks}).total;
 }
 
 int te_attn_window_fwd_thd(const void* q, const void* k, const void* v, void* out, float* lse,

@@ -19,7 +19,20 @@ constexpr int kWindowLimit = 1 << 30;
 struct WindowParams : AttnParams {
   int window;  // >= 1
   int sinks;   // >= 0
+  // Backward: a key tile with sinks is seen by every query behind it, while the others' sweeps end
+  // with the window. Sweeps of the first kSplitSinkTiles tiles are cut into parts of sweep_tiles query
+  // tiles, whose fp32 sums a last kernel adds up in order.
+  int sweep_tiles;   // 0: no sweep is cut
+  int* pref_s;       // [batch + 1]: slots for parts before each sequence
+  int4* slots;       // (sequence, key tile, part): part -1 is the sweep's begin, an ordinary item
+  float* part_dk;    // [slots][hkv][128][d]
+  float* part_dv;
+  int cap_slots;
 };
+
+constexpr int kSplitSinkTiles = 2;
+// As long as an ordinary sweep, but so long that few sequences have more than one part.
+__host__ __device__ constexpr int sweep_tiles_of(int window) { return (window + kBlockM - 1) / kBlockM + 1 > 16 ? (window + kBlockM - 1) / kBlockM + 1 : 16; }
 
 template <class P>
 constexpr bool is_window = std::is_base_of_v<WindowParams, P>;
@@ -119,6 +132,40 @@ __device__ __forceinline__ int tile_last_query(const P& p, const SeqInfo& s, int
   return s.len_q;
 }
 
+// Sweep over key tile kt: query tiles [first, end) of 128 in the ordinary item, and then parts of
+// sweep_tiles up to the sequence's last one.
+struct Sweep {
+  int end, parts;
+};
+template <class P>
+__device__ __forceinline__ Sweep sweep_of(const P& p, const SeqInfo& s, int kt) {
+  Sweep w{(tile_last_query(p, s, kt) + kBlockM - 1) / kBlockM, 0};
+  if constexpr (is_window<P>) {
+    if (p.sweep_tiles > 0 && kt < kSplitSinkTiles && kt * kBlockN < p.sinks) {
+      const int last = min(s.len_q, min(kt * kBlockN + kBlockN, s.len_k) - 1 - s.diag + p.window);
+      const int first = first_query(s, kt * kBlockN, true) / kBlockM;
+      const int end = max((max(last, 0) + kBlockM - 1) / kBlockM, first + p.sweep_tiles);
+      if (end < w.end) {
+        w.parts = (w.end - end + p.sweep_tiles - 1) / p.sweep_tiles;
+        w.end = end;
+      }
+    }
+  }
+  return w;
+}
+// Slots of a sequence's key tiles before kt.
+__device__ __forceinline__ int slots_before(const WindowParams& p, const SeqInfo& s, int kt) {
+  const int tiles = key_tiles(p, s).n > 0 ? (min(p.sinks, seen_keys(s, true)) + kBlockN - 1) / kBlockN : 0;
+  int n = 0;
+  for (int k = 0; k < min(min(kt, kSplitSinkTiles), tiles); ++k) {
+    const Sweep w = sweep_of(p, s, k);
+    n += w.parts > 0 ? w.parts + 1 : 0;
+  }
+  return n;
+}
+
+cudaError_t launch_window_delta(const WindowParams& p, bool bf16, int num_sms, cudaStream_t st);
+cudaError_t launch_window_sum(const WindowParams& p, bool bf16, cudaStream_t st);
 cudaError_t launch_window_schedule(const WindowParams& p, int* pref_q, int* pref_k, int* pref_f, cudaStream_t st);
 cudaError_t launch_window_zero_fill(const WindowParams& p, int mode, int num_sms, cudaStream_t st);
 cudaError_t launch_window_fwd(const WindowParams& p, bool bf16, int num_sms, cudaStream_t st);

@@ -15,7 +15,8 @@ namespace teattn {
 
 struct WorkRing {
   int item[2];
-  int aux[2];  // optional per-item value the producer hands over with the item
+  int aux[2];  // optional per-item values the producer hands over with the item
+  int more[2];
   uint64_t full[2];
   uint64_t empty[2];
 };
@@ -29,11 +30,12 @@ __device__ __forceinline__ void ring_init(WorkRing& r, uint32_t consumers) {
 }
 
 // Producer (one thread): publish hand-over number k (item < 0 means "no more work").
-__device__ __forceinline__ bool ring_put(WorkRing& r, int k, int item, int* status, int aux = 0) {
+__device__ __forceinline__ bool ring_put(WorkRing& r, int k, int item, int* status, int aux = 0, int more = 0) {
   const int s = k & 1;
   if (k >= 2 && !mbar_wait(&r.empty[s], ((k >> 1) - 1) & 1, status)) return false;
   *reinterpret_cast<volatile int*>(&r.item[s]) = item;
   *reinterpret_cast<volatile int*>(&r.aux[s]) = aux;
+  *reinterpret_cast<volatile int*>(&r.more[s]) = more;
   mbar_arrive(&r.full[s]);
   return true;
 }
@@ -66,7 +68,7 @@ __device__ __forceinline__ int ring_get_warp(WorkRing& r, int k, int* status, bo
 // Consumer (a whole warp, counted once in `consumers`): every lane waits and reads
 // the warp-uniform item; lane 0 alone arrives on the slot's empty barrier.
 __device__ __forceinline__ int ring_get_warp_once(WorkRing& r, int k, int* status, bool* ok,
-                                                  int* aux) {
+                                                  int* aux, int* more = nullptr) {
   const int s = k & 1;
   if (!__all_sync(0xffffffffu, mbar_wait(&r.full[s], (k >> 1) & 1, status))) {
     *ok = false;
@@ -74,6 +76,7 @@ __device__ __forceinline__ int ring_get_warp_once(WorkRing& r, int k, int* statu
   }
   const int item = *reinterpret_cast<volatile int*>(&r.item[s]);
   *aux = *reinterpret_cast<volatile int*>(&r.aux[s]);
+  if (more) *more = *reinterpret_cast<volatile int*>(&r.more[s]);
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[s]);
   __syncwarp();

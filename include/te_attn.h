@@ -277,10 +277,14 @@ int te_attn_fwd_thd_e4m3(const void* q, const void* k, const void* v, void* out,
  * window >= 1, sinks >= 0 (TE_ERR_INVALID_ARG otherwise); mask_type one of the causal ones and
  * fewer than 2^30 rows (TE_ERR_UNSUPPORTED otherwise). Key tiles that no query of a tile sees
  * are not visited, so the time is that of the window, not of the sequence.
- * Everything else, the workspaces' sizes among it, is as for those entry points. A real query
+ * Everything else is as for those entry points; the forward's workspace is theirs too, the
+ * backward's holds partial sums for sinks besides (te_attn_window_bwd_workspace_size(); rows of
+ * the sequence-major forms as there). A real query
  * that sees no key (upper-left, a window or more behind the last key, without sinks) gets
  * out = 0, lse = -inf, dq = 0; keys that no query sees get exact zeros in dk and dv.
  */
+size_t te_attn_window_bwd_workspace_size(int batch, int total_q, int total_kv, int hq, int hkv,
+                                         int d, int window, int sinks);
 int te_attn_window_fwd_thd(const void* q, const void* k, const void* v, void* out, float* lse,
                            const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
                            const int32_t* cu_seqlens_q_padded, const int32_t* cu_seqlens_kv_padded,

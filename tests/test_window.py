@@ -166,6 +166,13 @@ CASES = [
     ([500, 20], [30, 20], 17, 0, 1, 1, 192, torch.bfloat16, TL),
     ([500], None, 3, 0, 1, 1, 8, torch.float16, TL),
     ([1200], None, 385, 1, 2, 1, 128, torch.bfloat16, TL),
+    # sweeps over sinks that are cut into parts: more than 16 query tiles
+    ([5000, 300, 2500], None, 100, 4, 2, 1, 64, torch.bfloat16, TL),
+    ([2700], None, 300, 200, 2, 2, 128, torch.float16, TL),
+    ([2600], None, 64, 140, 1, 1, 256, torch.bfloat16, TL),
+    ([2500, 4300], [6000, 4400], 90, 3, 2, 1, 64, torch.float16, BR),   # the sinks lie before every window
+    ([4500], [60], 40, 20, 1, 1, 64, torch.bfloat16, TL),              # a single, short key tile
+    ([4500], [900], 2300, 300, 1, 1, 64, torch.float16, BR),
 ]
 
 
@@ -193,7 +200,7 @@ def test_random(seed):
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_long_windows_are_the_causal_masks(mask, d):
     """Window and sinks that leave everything: the entry points without them, bit for bit."""
-    for window, sinks in ((FAR, 0), (1500, 3), (1, FAR)):
+    for window, sinks in ((FAR, 0), (1500, 3), (1, FAR), (1, 1000)):
         c = Case(5, [700, 1, 300], [900, 40, 300], window, sinks, 4, 2, d, torch.bfloat16, mask).dev()
         out, lse = c.fwd()
         same = ta.fwd(*c.on, *c.cu_on, c.scale, mask)
@@ -208,7 +215,7 @@ def test_repeats_and_what_buffers_held():
     grads = c.bwd(*first)
     poison = lambda t: torch.full_like(t.view(torch.uint8), 255).view(t.dtype)  # noqa: E731
     B, tq, hq, d = len(c.cu[0]) - 1, c.q.shape[0], 4, 128
-    ws = torch.full((ta.bwd_workspace_size(B, tq, c.k.shape[0], hq, 2, d),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((ta.window_bwd_workspace_size(B, tq, c.k.shape[0], hq, 2, d, 60, 3),), 255, dtype=torch.uint8, device="cuda")
     again = c.fwd(out=poison(first[0]), lse=poison(first[1]), workspace=ws)
     assert _same(first, again) and ta.read_status(ws) == 0
     ws.fill_(255)
@@ -223,7 +230,7 @@ def test_debug_build_finds_nothing():
         out, lse = c.fwd()
         grads = c.bwd(out, lse)
         with ta.debug_build():
-            ws = torch.empty(ta.bwd_workspace_size(3, c.q.shape[0], c.k.shape[0], 2, 1, d), dtype=torch.uint8, device="cuda")
+            ws = torch.empty(ta.window_bwd_workspace_size(3, c.q.shape[0], c.k.shape[0], 2, 1, d, 77, 2), dtype=torch.uint8, device="cuda")
             assert _same((out, lse), c.fwd(workspace=ws)) and ta.read_status(ws) == 0
             assert _same(grads, c.bwd(out, lse, workspace=ws)) and ta.read_status(ws) == 0
 
