@@ -395,19 +395,25 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
         ++ns;
         tc_fence_after();
         const int nvalid = min(max(lim - j * kBlockN, 0), kBlockN);
+        bool some = nvalid > 0, all = nvalid >= kBlockN;
         // with a window: bit c % 32 of word c / 32, the row sees the key of column c
         [[maybe_unused]] uint32_t seen[kBlockN / 32];
-        bool some = nvalid > 0, all = nvalid >= kBlockN;
         if constexpr (is_window<P>) {
-          uint32_t any = 0, every = ~0u;
+          const int key = cur.run.tile(j) * kBlockN;
+          all = key + kBlockN <= lim && (key >= cur.win.lo || key + kBlockN <= cur.win.sinks);
+          some = true;
+          if (__all_sync(0xffffffffu, all)) {
 #pragma unroll
-          for (int k = 0; k < kBlockN / 32; ++k) {
-            seen[k] = seen_bits(lim, cur.win, cur.run.tile(j) * kBlockN + 32 * k);
-            any |= seen[k];
-            every &= seen[k];
+            for (int k = 0; k < kBlockN / 32; ++k) seen[k] = ~0u;
+          } else {
+            uint32_t any = 0;
+#pragma unroll
+            for (int k = 0; k < kBlockN / 32; ++k) {
+              seen[k] = seen_bits(lim, cur.win, key + 32 * k);
+              any |= seen[k];
+            }
+            some = any != 0;
           }
-          some = any != 0;
-          all = every == ~0u;
         }
         auto valid = [&](int c) {
           if constexpr (is_window<P>) return ((seen[c / 32] >> (c % 32)) & 1u) != 0;

@@ -55,10 +55,10 @@ __device__ __forceinline__ void join_pieces(const PagedParams& p, const PagedPar
   }
 }
 
-// The segment that slice `w` goes on with, if it is the first slice to do so: a warp a row.
+// The segment that slice `w` goes on with, if it is the first slice to do so: a thread a row, a
+// quarter of the columns a block (its pieces lie column by column).
 template <bool kBF16>
 __device__ void join_wide(const PagedParams& p, const PagedParts& parts, int w, int part) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long total = parts.pref[p.batch], per = slice_units(total, parts.slices, parts.least), at = w * per;
   if (at >= total) return;
   constexpr PagedCut cut{kWideRows, kWideKeys, true};
@@ -67,29 +67,46 @@ __device__ void join_wide(const PagedParams& p, const PagedParts& parts, int w, 
   if (t.u0 == 0 || first < at - per) return;  // begins it, or an earlier slice went on with it
   const int w1 = static_cast<int>((first + t.run.n - 1) / per);
   const int row0 = t.tile * kWideRows, rows = min(kWideRows, t.s.n * p.group - row0);
-  for (int r = part * 4 + warp; r < rows; r += kWideJoin * 4) {
-    float m, l, acc[8];
-    join_pieces(p, parts, kWideRows, r, first, per, w - 1, w1, 1, m, l, acc);
-    const int i = (row0 + r) / p.group, j = row0 + r - i * p.group;
-    const long long row = static_cast<long long>(t.s.off + i) * p.hq + t.head * p.group + j;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (lane < p.d / 8)
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.d + lane * 8) =
-          make_uint4(pack2<kBF16>(acc[0] * inv, acc[1] * inv), pack2<kBF16>(acc[2] * inv, acc[3] * inv),
-                     pack2<kBF16>(acc[4] * inv, acc[5] * inv), pack2<kBF16>(acc[6] * inv, acc[7] * inv));
-    if (lane == 0) p.lse[row] = m * 0.69314718055994531f + logf(l);
+  const int r = (part & 1) * kJoinThreads + threadIdx.x;
+  if (r >= rows) return;
+  // piece k is in slot 1 of the slice that begins the segment, in slot 0 of the others
+  auto slot = [&](int k) { return 2ll * k + (k == w - 1 ? 1 : 0); };
+  float M = -INFINITY, L = 0.f;
+  for (int k = w - 1; k <= w1; ++k) M = fmaxf(M, parts.ml[slot(k) * kWideRows + r].x);
+  // (a piece without a key has left a sum of 0, or a NaN that it saw)
+  auto weight = [&](float2 ml) { return ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : NAN) : ex2j(ml.x - M); };
+  for (int k = w - 1; k <= w1; ++k) {
+    const float2 ml = parts.ml[slot(k) * kWideRows + r];
+    L += weight(ml) * ml.y;
   }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int i = (row0 + r) / p.group, j = row0 + r - i * p.group;
+  const long long row = static_cast<long long>(t.s.off + i) * p.hq + t.head * p.group + j;
+  for (int c = part >> 1; c < p.d / 8; c += kWideJoin / 2) {
+    float acc[8] = {};
+    for (int k = w - 1; k <= w1; ++k) {
+      const float f = weight(parts.ml[slot(k) * kWideRows + r]);
+      const float* o = parts.o + (slot(k) * p.d + c * 8) * kWideRows + r;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(f, o[e * kWideRows], acc[e]);
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.d + c * 8) =
+        make_uint4(pack2<kBF16>(acc[0] * inv, acc[1] * inv), pack2<kBF16>(acc[2] * inv, acc[3] * inv),
+                   pack2<kBF16>(acc[4] * inv, acc[5] * inv), pack2<kBF16>(acc[6] * inv, acc[7] * inv));
+  }
+  if (part < 2) p.lse[row] = M * 0.69314718055994531f + logf(L);
 }
 
 template <bool kBF16>
 __global__ void __launch_bounds__(kJoinThreads)
     paged_join_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ PagedCut few, const __grid_constant__ PagedParts few_parts,
-                      const __grid_constant__ PagedParts wide_parts) {
+                      const __grid_constant__ PagedParts wide_parts, int heads) {
   __shared__ float2 s_ml[4];
   __shared__ float s_o[4][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wide_blocks = wide_parts.slices * kWideJoin;  // ahead of the rows
-  const int at_row = blockIdx.x - 1 - wide_blocks, tok = at_row / p.hq, hq = at_row - tok * p.hq;
+  const int per_token = p.hq / heads;  // blocks of a token, of `heads` heads each
+  const int at_row = blockIdx.x - 1 - wide_blocks, tok = at_row / per_token, hq0 = (at_row - tok * per_token) * heads;
   PagedSeq s{0, 0, 0, true};
   int b = -1;
   if (at_row >= 0) {
@@ -113,53 +130,59 @@ __global__ void __launch_bounds__(kJoinThreads)
     join_wide<kBF16>(p, wide_parts, (blockIdx.x - 1) / kWideJoin, (blockIdx.x - 1) % kWideJoin);
     return;
   }
-  const long long row = at_row;
   const int i = tok - s.off;
-  uint16_t* out = static_cast<uint16_t*>(p.out) + row * p.d;
   if (b < 0 || i >= s.n) {
-    for (int c = threadIdx.x * 8; c < p.d; c += kJoinThreads * 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
-    if (threadIdx.x == 0) p.lse[row] = 0.f;
+    const long long row = static_cast<long long>(tok) * p.hq + hq0;
+    for (int c = threadIdx.x * 8; c < p.d * heads; c += kJoinThreads * 8)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.d + c) = make_uint4(0, 0, 0, 0);
+    for (int h = threadIdx.x; h < heads; h += kJoinThreads) p.lse[row + h] = 0.f;
     return;
   }
   if (!few.takes(p, s)) return;  // the other kernel's
-  const PagedParts& parts = few_parts;
-  const int h = hq / p.group;
-  const long long rr = static_cast<long long>(i) * p.group + hq - h * p.group;
-  const int tile = static_cast<int>(rr / few.rows), r = static_cast<int>(rr - static_cast<long long>(tile) * few.rows);
-  const int n = few.run(p, s, tile).n;
-  const long long per = slice_units(parts.pref[p.batch], parts.slices, parts.least);
-  const long long first = parts.pref[b] + few.before(p, s, tile) + static_cast<long long>(h) * n;
-  const int w0 = static_cast<int>(first / per), w1 = static_cast<int>((first + n - 1) / per);
-  if (w0 == w1) return;  // written whole
-  float m, l, acc[8];
-  const int cols = p.d / 8;  // eight columns a lane
-  join_pieces(p, parts, few.rows, r, first, per, w0 + warp, w1, 4, m, l, acc);
-  if (lane == 0) s_ml[warp] = make_float2(m, l);
-  if (lane < cols) {
+#pragma unroll 1
+  for (int hq = hq0; hq < hq0 + heads; ++hq) {
+    const long long row = static_cast<long long>(tok) * p.hq + hq;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + row * p.d;
+    const PagedParts& parts = few_parts;
+    const int h = hq / p.group;
+    const long long rr = static_cast<long long>(i) * p.group + hq - h * p.group;
+    const int tile = static_cast<int>(rr / few.rows), r = static_cast<int>(rr - static_cast<long long>(tile) * few.rows);
+    const int n = few.run(p, s, tile).n;
+    const long long per = slice_units(parts.pref[p.batch], parts.slices, parts.least);
+    const long long first = parts.pref[b] + few.before(p, s, tile) + static_cast<long long>(h) * n;
+    const int w0 = static_cast<int>(first / per), w1 = static_cast<int>((first + n - 1) / per);
+    if (w0 == w1) continue;  // written whole
+    float m, l, acc[8];
+    const int cols = p.d / 8;  // eight columns a lane
+    join_pieces(p, parts, few.rows, r, first, per, w0 + warp, w1, 4, m, l, acc);
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    if (lane < cols) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s_o[warp][lane * 8 + e] = acc[e];
-  }
-  __syncthreads();
-  float top = -INFINITY;
+      for (int e = 0; e < 8; ++e) s_o[warp][lane * 8 + e] = acc[e];
+    }
+    __syncthreads();
+    float top = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w].x);
-  float f[4], sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    f[w] = s_ml[w].x == -INFINITY ? (s_ml[w].y == 0.f ? 0.f : NAN) : ex2j(s_ml[w].x - top);
-    sum += s_ml[w].y * f[w];
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int c = threadIdx.x * 2; c < p.d; c += kJoinThreads * 2) {
-    float a = 0.f, d = 0.f;
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w].x);
+    float f[4], sum = 0.f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      a += s_o[w][c] * f[w];
-      d += s_o[w][c + 1] * f[w];
+      f[w] = s_ml[w].x == -INFINITY ? (s_ml[w].y == 0.f ? 0.f : NAN) : ex2j(s_ml[w].x - top);
+      sum += s_ml[w].y * f[w];
     }
-    *reinterpret_cast<uint32_t*>(out + c) = pack2<kBF16>(a * inv, d * inv);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int c = threadIdx.x * 2; c < p.d; c += kJoinThreads * 2) {
+      float a = 0.f, d = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        a += s_o[w][c] * f[w];
+        d += s_o[w][c + 1] * f[w];
+      }
+      *reinterpret_cast<uint32_t*>(out + c) = pack2<kBF16>(a * inv, d * inv);
+    }
+    if (threadIdx.x == 0) p.lse[row] = top * 0.69314718055994531f + logf(sum);
+    __syncthreads();  // (the sums in shared memory are read)
   }
-  if (threadIdx.x == 0) p.lse[row] = top * 0.69314718055994531f + logf(sum);
 }
 
 bool make_tmap_pages(CUtensorMap* map, const PagedCache& c, int kv, bool bf16, int slots) {
@@ -176,8 +199,12 @@ bool make_tmap_pages(CUtensorMap* map, const PagedCache& c, int kv, bool bf16, i
 
 cudaError_t launch_paged_join(const PagedParams& p, const PagedCut& cut, const PagedParts& parts, const PagedParts& wide, bool bf16,
                               cudaStream_t st) {
-  return launch_dependent(bf16 ? paged_join_kernel<true> : paged_join_kernel<false>, dim3(p.total_q * p.hq + wide.slices * kWideJoin + 1), dim3(kJoinThreads), 0, st,
-                          p, cut, parts, wide);
+  // A block a row while that fills the GPU a few times over, then one a token.
+  const long long rows = static_cast<long long>(p.total_q) * p.hq;
+  const int heads = rows > 16 * 16 * kPagedSMs ? p.hq : 1;
+  return launch_dependent(bf16 ? paged_join_kernel<true> : paged_join_kernel<false>,
+                          dim3(static_cast<unsigned>(rows / heads + wide.slices * kWideJoin + 1)), dim3(kJoinThreads), 0, st, p, cut, parts,
+                          wide, heads);
 }
 
 }  // namespace teattn

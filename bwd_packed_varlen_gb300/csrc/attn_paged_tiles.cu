@@ -307,19 +307,25 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
         // bit c % 32 of word c / 32: the row sees the key of column c
         const uint32_t blocks = *const_cast<volatile uint32_t*>(&s_blocks[(ns + skipped) & 7].word);
         ++ns;
-        uint32_t seen[4], any = 0, every = ~0u;
+        uint32_t seen[4];
+        const bool full = __all_sync(0xffffffffu, key0 + kWideKeys <= hi && (key0 >= lo || key0 + kWideKeys <= w.sinks) &&
+                                                      blocks == kAllBlocks);
+        bool some = true;
+        if (full) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = key0 + 32 * k;
-          seen[k] = low_bits_of(hi - key) & (~low_bits_of(lo - key) | low_bits_of(w.sinks - key));
-          if (blocks != kAllBlocks) {
+          for (int k = 0; k < 4; ++k) seen[k] = ~0u;
+        } else {
+          uint32_t any = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int key = key0 + 32 * k;
+            seen[k] = low_bits_of(hi - key) & (~low_bits_of(lo - key) | low_bits_of(w.sinks - key));
             if (!((blocks >> (8 * k)) & 1u)) seen[k] &= 0xffff0000u;
             if (!((blocks >> (8 * k)) & 2u)) seen[k] &= 0x0000ffffu;
+            any |= seen[k];
           }
-          any |= seen[k];
-          every &= seen[k];
+          some = any != 0;
         }
-        const bool some = any != 0, full = __all_sync(0xffffffffu, every == ~0u);
         auto valid = [&](int c) { return ((seen[c / 32] >> (c % 32)) & 1u) != 0; };
         auto tile_max = [&]() -> float {
           float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -419,17 +425,18 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
         }
         if (store) p.lse[row] = m * 0.69314718055994531f + logf(l);
       } else {
-        const long long slot = (2ll * blockIdx.x + (t.u0 == 0 ? 1 : 0)) * kWideRows + r;
-        if (live) parts.ml[slot] = make_float2(m, l);
+        // column by column, so that a warp's 32 rows lie side by side
+        const long long slot = 2ll * blockIdx.x + (t.u0 == 0 ? 1 : 0);
+        parts.ml[slot * kWideRows + r] = make_float2(m, l);
+        float* part = parts.o + slot * p.d * kWideRows + r;
 #pragma unroll
         for (int c0 = 0; c0 < kD; c0 += 16) {
           uint32_t o[16];
           tmem_ld16(t_o + c0, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 16; c += 4)
-            if (live && c0 + c < p.d)
-              *reinterpret_cast<uint4*>(parts.o + slot * p.d + c0 + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+          for (int c = 0; c < 16; ++c)
+            if (c0 + c < p.d) part[(c0 + c) * kWideRows] = __uint_as_float(o[c]);
         }
       }
       tc_fence_before();
@@ -512,7 +519,6 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  pdl_wait();  // complete only after the kernel ahead, for the join behind
 }
 
 template <int kD, bool kBF16, bool k4>
@@ -528,8 +534,8 @@ static cudaError_t launch_tiles_impl(const PagedParams& p, const PagedParts& par
   auto kern = paged_tiles_kernel<kD, kBF16, k4>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + (kPagedMaxBatch + 1) * 8);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(parts.slices), dim3(S::kThreads), S::kSmem + (p.batch + 1) * sizeof(long long), st, p, parts, tm,
-                          first_status);
+  kern<<<parts.slices, S::kThreads, S::kSmem + (p.batch + 1) * sizeof(long long), st>>>(p, parts, tm, first_status);
+  return cudaGetLastError();
 }
 
 template <bool kBF16, bool k4>
