@@ -136,12 +136,7 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
     for (int b = tid; b <= p.batch; b += blockDim.x) parts.pref[b] = pref[b];
   const long long per = slice_units(total, warps, kLeastUnits);
   const long long begin = mine * per, end = begin + per < total ? begin + per : total;
-  // Behind the kernel of many rows it starts as that one's blocks end; it shares nothing with it but
-  // must not be complete before it, for the join behind both.
-  if (begin >= end) {
-    pdl_wait();
-    return;
-  }
+  if (begin >= end) return;
 
   uint8_t* ring = smem + warp * NS * S::kStageBytes;
   const int row_bytes = kExact ? kD / 2 : p.cache.row_bytes, meta_bytes = kExact ? kD / 8 : p.d / 8;
@@ -295,10 +290,7 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
 
 #pragma unroll 1
     for (int u = t.u0; u < t.u0 + t.n; ++u) {
-      if (!mbar_wait_warp(&bar[warp][stage_at], phase, status)) {
-        pdl_wait();
-        return;
-      }
+      if (!mbar_wait_warp(&bar[warp][stage_at], phase, status)) return;
       const uint32_t stage = smem_u32(ring + stage_at * S::kStageBytes);
       const uint32_t loaded_blocks = seen_fifo & ((1u << kBlocks) - 1u);
       const int key0 = t.run.unit(u) * kUnit;
@@ -571,12 +563,10 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
         }
       }
   }
-  pdl_wait();
 }
 
 template <int kD, int kNT, bool kBF16, bool k4>
 static cudaError_t launch_rows_impl(const PagedParams& p, const PagedParts& parts, PagedCut* cut, cudaStream_t st) {
-  // (a call's first kernel is launched as usual)
   using S = RowsShape<kD, kNT, k4>;
   *cut = PagedCut{S::kRows, S::kUnit, false};
   RowsMaps tm{};
@@ -586,7 +576,6 @@ static cudaError_t launch_rows_impl(const PagedParams& p, const PagedParts& part
   auto kern = k4 && p.d == kD ? paged_rows_kernel<kD, kNT, kBF16, k4, k4> : paged_rows_kernel<kD, kNT, kBF16, k4, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + (kPagedMaxBatch + 1) * 8);
   if (e != cudaSuccess) return e;
-  if (p.wide_rows > 0) return launch_dependent(kern, dim3(parts.slices / S::kWarps), dim3(S::kWarps * 32), smem, st, p, parts, tm);
   kern<<<parts.slices / S::kWarps, S::kWarps * 32, smem, st>>>(p, parts, tm);
   return cudaGetLastError();
 }

@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  pdl_wait();  // complete only after the kernel ahead, for the join behind both
 }
 
 template <int kD, bool kBF16, bool k4>
@@ -534,8 +535,8 @@ static cudaError_t launch_tiles_impl(const PagedParams& p, const PagedParts& par
   auto kern = paged_tiles_kernel<kD, kBF16, k4>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem + (kPagedMaxBatch + 1) * 8);
   if (e != cudaSuccess) return e;
-  kern<<<parts.slices, S::kThreads, S::kSmem + (p.batch + 1) * sizeof(long long), st>>>(p, parts, tm, first_status);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(parts.slices), dim3(S::kThreads), S::kSmem + (p.batch + 1) * sizeof(long long), st, p, parts, tm,
+                          first_status);
 }
 
 template <bool kBF16, bool k4>
@@ -550,11 +551,11 @@ cudaError_t launch_paged_tiles(const PagedParams& p, const PagedParts& parts, in
 }
 
 int paged_wide_rows(int batch, int total_q, int group, int d) {
-  // Launched where some sequence must have many queries: with 64 rows a kv head more than one
-  // query each comes to. Above head_dim 128 the kernel of few rows takes all.
+  // Launched where sequences must have many rows on average, or some sequence may have many enough
+  // to outweigh a launch for nothing (4 us). Above head_dim 128 the kernel of few rows takes all.
   if (d > 128) return 0;
-  const long long over = (static_cast<long long>(total_q) - batch) * group;
-  return over >= 64 ? 64 : 0;
+  const long long rows = static_cast<long long>(total_q) * group, over = rows - static_cast<long long>(batch) * group;
+  return rows > 32ll * batch || over >= 512 ? 64 : 0;
 }
 
 }  // namespace teattn

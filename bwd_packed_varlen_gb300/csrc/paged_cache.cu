@@ -41,7 +41,7 @@ struct AppendParams {
   float mscale;
   int tokens, heads_per; // tokens and heads (of q, k, then v) of a block
   int units[3];          // of a head: turned; copied beside them; copied of a head of v
-  uint32_t units_inv[3];
+  uint32_t units_inv[3], words_inv;
 };
 
 constexpr int kAppendThreads = 256, kAppendTokens = 4;
@@ -233,22 +233,31 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
     if (w.in) put(w, w.e, w.a);
   }
   if constexpr (!k4) {
-    const int n_v = nt * nv * p.units[2];
-    for (int n = tid; n < n_v; n += kAppendThreads) {
-      const int th = div_by(n, p.units_inv[2], p.units[2]), t = th / nv, h = v0 + th - t * nv;
-      const int e = (n - th * p.units[2]) * V;
-      const Token tk = s_tok[t];
-      if (tk.page >= 0)
-        *reinterpret_cast<T*>(cached(1, tk.page, tk.pos, h - p.heads[0] - p.heads[1], e)) =
-            *reinterpret_cast<const T*>(source(t, h, e));
+    // values, two accesses in flight: a place in a token's heads for all of the block's tokens
+    const int per = nv * p.units[2];
+    for (int n = tid; n < per; n += kAppendThreads) {
+      const int hh = div_by(n, p.units_inv[2], p.units[2]), h = v0 + hh, e = (n - hh * p.units[2]) * V;
+      for (int t = 0; t < nt; t += 2) {
+        T v[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (t + k < nt) v[k] = *reinterpret_cast<const T*>(source(t + k, h, e));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (t + k >= nt) continue;
+          const Token tk = s_tok[t + k];
+          if (tk.page >= 0) *reinterpret_cast<T*>(cached(1, tk.page, tk.pos, h - p.heads[0] - p.heads[1], e)) = v[k];
+        }
+      }
     }
   } else {
     __syncthreads();
     const int words = p.d / 8, n_w = nt * (nk + nv) * words;  // eight elements a lane
+    const uint32_t kv_inv = nk + nv > 0 ? 0xffffffffu / static_cast<uint32_t>(nk + nv) + 1u : 0u;  // ceil(2^32 / n), or 0 for 1
 #pragma unroll 1
     for (int base = 0; base < n_w; base += kAppendThreads) {
       const int n = min(base + tid, n_w - 1);  // (every lane takes part in the exchanges)
-      const int th = n / words, word = n - th * words, t = th / (nk + nv), hh = th - t * (nk + nv);
+      const int th = div_by(n, p.words_inv, words), word = n - th * words, t = div_by(th, kv_inv, nk + nv), hh = th - t * (nk + nv);
       const bool key = hh < nk;
       const uint16_t* x = key ? s_keys + (t * nk + hh) * p.d + word * 8 : source(t, v0 + hh - nk, word * 8);
       float f[8];
@@ -293,6 +302,7 @@ static cudaError_t launch_append_v(AppendParams p, bool bf16, cudaStream_t st) {
   p.heads_per = (heads + parts - 1) / parts;
   for (int i = 0; i < 3; ++i)
     p.units_inv[i] = p.units[i] > 0 ? static_cast<uint32_t>(((1ull << 32) + p.units[i] - 1) / p.units[i]) : 0u;
+  p.words_inv = static_cast<uint32_t>(((1ull << 32) + p.d / 8 - 1) / (p.d / 8));
   size_t smem = static_cast<size_t>(p.tokens) * (p.rot / 2) * sizeof(float2);
   if (k4) {
     smem = (smem + 15) / 16 * 16 + static_cast<size_t>(p.tokens) * min(p.heads_per, p.heads[1]) * p.d * 2;
@@ -339,6 +349,7 @@ struct GatherParams {
   int* status;
   int batch, total;
   int tokens;  // of a block
+  uint32_t words_inv, heads_inv;  // ceil(2^32 / n) of d / 8 and of hkv
 };
 
 constexpr int kGatherThreads = 256, kGatherTokens = 8;
@@ -360,7 +371,8 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(const __gr
   __syncthreads();
   const int words = p.cache.d / 8, per = p.cache.hkv * words;
   for (int n = tid; n < 2 * nt * per; n += kGatherThreads) {
-    const int kv = n / (nt * per), m = n - kv * nt * per, t = m / per, hw = m - t * per, h = hw / words, word = hw - h * words;
+    const int th = div_by(n, p.words_inv, words), word = n - th * words, tk2 = div_by(th, p.heads_inv, p.cache.hkv);
+    const int h = th - tk2 * p.cache.hkv, kv = tk2 >= nt ? 1 : 0, t = tk2 - kv * nt;
     const Token tk = s_tok[t];
     uint4 v = make_uint4(0, 0, 0, 0);
     if (tk.page >= 0) {
@@ -523,6 +535,9 @@ int te_attn_paged_gather(const te_attn_paged_cache* cache, void* k, void* v, con
   p.total = total;
   // enough blocks for the SMs first, then up to eight rows a block
   p.tokens = total >= 8 * 4 * kAppendSMs ? 8 : total >= 4 * kAppendSMs ? 2 : 1;
+  auto inverse = [](int n) { return static_cast<uint32_t>(((1ull << 32) + n - 1) / n); };
+  p.words_inv = inverse(cache->d / 8);
+  p.heads_inv = inverse(cache->hkv);
   const int blocks = (total + p.tokens - 1) / p.tokens;
   const bool bf16 = cache->dtype == TE_DTYPE_BF16;
   if (!cache->k_meta) paged_gather_kernel<true, false><<<blocks, kGatherThreads, 0, st>>>(p);

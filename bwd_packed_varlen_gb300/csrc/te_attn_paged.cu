@@ -120,13 +120,12 @@ int te_attn_paged_fwd_thd(const te_attn_paged_cache* cache, const void* q, void*
                           reinterpret_cast<float*>(ws + L.o[k]), L.slices[k] / kPagedSMs * use, k ? kLeastWideUnits : kLeastUnits};
   const bool bf16 = cache->dtype == TE_DTYPE_BF16;
   PagedCut cut{};
-  cudaError_t e = cudaSuccess;
-  if (L.wide_rows > 0) {  // the longer work first
+  cudaError_t e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_paged_rows(p, parts[0], bf16, four, L.rows, &cut, st); });
+  if (e != cudaSuccess) return api_cuda_fail(e, "paged attention");
+  if (L.wide_rows > 0) {
     e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_paged_tiles(p, parts[1], parts[0].slices, bf16, four, st); });
     if (e != cudaSuccess) return api_cuda_fail(e, "paged attention of long pieces");
   }
-  e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_paged_rows(p, parts[0], bf16, four, L.rows, &cut, st); });
-  if (e != cudaSuccess) return api_cuda_fail(e, "paged attention");
   e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_paged_join(p, cut, parts[0], parts[1], bf16, st); });
   return e == cudaSuccess ? api_ok() : api_cuda_fail(e, "paged join");
 }
