@@ -276,20 +276,22 @@ __global__ void __launch_bounds__(192, 1)
         // for per-element masking. Max and sum use 8 independent partials so the
         // dependent chains stay short.
         const bool full = __all_sync(0xffffffffu, all);
+        // (with a window each score is scaled before the maximum is taken: a negative scale may be given)
+        const float each = is_window<P> ? sl2 : 1.f;
         float mp[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) mp[k] = -INFINITY;
         if (full) {
 #pragma unroll
-          for (int c = 0; c < kBlockN; ++c) mp[c & 7] = fmaxf(mp[c & 7], __uint_as_float(sr[c]));
+          for (int c = 0; c < kBlockN; ++c) mp[c & 7] = fmaxf(mp[c & 7], __uint_as_float(sr[c]) * each);
         } else {
 #pragma unroll
           for (int c = 0; c < kBlockN; ++c)
-            mp[c & 7] = fmaxf(mp[c & 7], valid(c) ? __uint_as_float(sr[c]) : -INFINITY);
+            mp[c & 7] = fmaxf(mp[c & 7], valid(c) ? __uint_as_float(sr[c]) * each : -INFINITY);
         }
         const float mx = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
                                fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
-        const float mxs = mx * sl2;
+        const float mxs = is_window<P> ? mx : mx * sl2;
         float m_new = m;
         bool rescale = false;
         if (some) {

@@ -421,8 +421,10 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
         };
         const bool full = __all_sync(0xffffffffu, all);
         const float sl2 = p.scale_log2;
-        // Row max of this tile's visible scores (log2 domain), from S in TMEM.
+        // Row max of this tile's visible scores (log2 domain), from S in TMEM. (With a window each
+        // score is scaled before the maximum is taken, so that a negative scale may be given.)
         auto tile_max = [&]() -> float {
+          const float each = is_window<P> ? sl2 : 1.f;
           float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int k = 0; k < kBlockN / 32; ++k) {
@@ -431,10 +433,11 @@ __global__ void __launch_bounds__(kFwdPairThreads, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int c = 0; c < 16; ++c)
-              mp[c & 3] = max3(mp[c & 3], valid(32 * k + 2 * c) ? __uint_as_float(sv[2 * c]) : -INFINITY,
-                               valid(32 * k + 2 * c + 1) ? __uint_as_float(sv[2 * c + 1]) : -INFINITY);
+              mp[c & 3] = max3(mp[c & 3], valid(32 * k + 2 * c) ? __uint_as_float(sv[2 * c]) * each : -INFINITY,
+                               valid(32 * k + 2 * c + 1) ? __uint_as_float(sv[2 * c + 1]) * each : -INFINITY);
           }
-          return fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]) * sl2;
+          const float top = fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]);
+          return is_window<P> ? top : top * sl2;
         };
         // A row's first tile with a visible key: its max, to start the offset m.
         if (__any_sync(0xffffffffu, m == -INFINITY && some)) {

@@ -498,8 +498,10 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
         const int st = it % NS;
         const bool more = u + 1 < t.u0 + t.n;
         if (it >= NS && !(ok = mbar_wait_warp(&bar_k_empty[st], ((it / NS) - 1) & 1, status))) break;
-        const uint32_t there = __ballot_sync(0xffffffffu, k.there);  // (a page holds 16 keys at least)
-        if (lane == 0) *const_cast<volatile uint8_t*>(&s_blocks[it & 7].part[warp - 10]) = (there & 1u) | ((there >> 15) & 2u);
+        // (a page holds 16 keys at least; a block of which some row sees a key counts as there)
+        const uint32_t there = __ballot_sync(0xffffffffu, k.there);
+        if (lane == 0)
+          *const_cast<volatile uint8_t*>(&s_blocks[it & 7].part[warp - 10]) = ((there & 0xffffu) != 0 ? 1 : 0) | (there >> 16 != 0 ? 2 : 0);
         put(sK + st * S::kTileBytes, k);
         mbar_arrive(&bar_k_full[st]);
         if (more) fetch(u + 1, 0, k);

@@ -178,6 +178,79 @@ def test_many_sequences_and_long_ones(bits):
     Case(43, [1, 2], [20000, 7], 64, 4, 2, 128, FP, bits, slot=1, tail=0).check()
 
 
+WIDE = [
+    # pieces of prompts: more than 64 rows a kv head go to the kernel of many rows
+    ([200, 300], [0, 500], 16, 8, 2, 128, BF, 16),
+    ([200, 300], [0, 500], 32, 8, 2, 128, BF, 4),
+    ([129, 1, 64, 0, 700], [1000, 30, 5, 9, 0], 64, 4, 2, 64, FP, 16),
+    ([129, 1, 64, 0, 700], [1000, 30, 5, 9, 0], 16, 4, 2, 64, FP, 4),
+    ([90, 41], [400, 3000], 128, 3, 1, 96, BF, 16),             # groups that no tile holds whole
+    ([90, 41], [400, 3000], 64, 10, 2, 96, BF, 4),
+    ([30, 7], [700, 100], 256, 48, 1, 80, FP, 16),
+    ([5, 3], [900, 100], 32, 300, 1, 64, BF, 16),               # more heads than a row tile
+    ([300, 90], [900, 100], 16, 4, 1, 128, FP, 16, 100, 4),
+    ([300, 90], [900, 100], 16, 4, 1, 128, FP, 4, 100, 4),
+    ([300, 90], [900, 4000], 64, 4, 2, 64, BF, 16, 33, 0),
+    ([300, 90], [900, 4000], 32, 4, 2, 64, BF, 4, 500, 300),
+    ([140, 200], [2000, 30], 16, 6, 1, 256, BF, 16, 90, 2),     # (head_dim 256: the kernel of few rows takes them)
+    ([140], [200], 16, 2, 1, 256, FP, 4),
+    ([1500], [700], 64, 2, 1, 128, BF, 16),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", WIDE, ids=[str(i) for i in range(len(WIDE))])
+def test_pieces_of_prompts(case):
+    Case(61, *case).check()
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+def test_both_kernels_in_one_call(bits):
+    """A piece of a prompt among decoding sequences gives what each gives alone, within what their
+    tensors' type leaves, and repeats give the same bits."""
+    c = Case(62, [1, 200, 1, 2, 1], [700, 300, 40, 5, 90], 16, 4, 2, 128, BF, bits)
+    first = c.check()
+    assert _same(first, c.fwd())
+    with ta.debug_build():
+        ws = c.workspace()
+        assert _same(first, c.fwd(workspace=ws)) and ta.read_status(ws) == 0
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+def test_pages_outside_the_cache_for_pieces(bits):
+    """Their keys are seen by no query, and the call says so (the last token's keys alone differ)."""
+    c = Case(63, [100], [300], 16, 2, 1, 64, FP, bits, slot=1, tail=0)
+    table = c.table.clone()
+    table[0, 3], table[0, 9] = -1, c.pages
+    c.dev().on[3].copy_(table)
+    ws = c.workspace()
+    out, lse = c.fwd(workspace=ws)
+    assert ta.read_status(ws) == 16
+    # the same queries over a cache in which those pages hold keys that nothing sees: positions 48-63
+    # and 144-159 lie before all queries, so leaving them out shifts no query's limit but by 32
+    keep = torch.ones(400, dtype=torch.bool)
+    keep[48:64] = keep[144:160] = False
+    ref = window_plain(c.q, c.kv[0][keep], c.kv[1][keep], None, [(0, 100)], [(0, 368)], c.scale, BR, 0, 0)
+    prefix_check({"out": out, "lse": lse}, ref, ("out", "lse"), FP)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("scale", [-0.9, 0.0])
+def test_other_scales(bits, scale):
+    """Negative ones, with scores far apart, and none at all, for both kernels."""
+    c = Case(64, [1, 90], [300, 200], 16, 2, 1, 64, BF, bits)
+    c.scale = scale
+    c.check()
+
+
+@gpu
+def test_as_many_sequences_as_are_taken():
+    Case(65, [1] * 4096, [i % 20 for i in range(4096)], 16, 1, 1, 8, FP, 16, slot=1, tail=0).check()
+
+
 @gpu
 @pytest.mark.parametrize("bits", [16, 4])
 @pytest.mark.parametrize("growth", [4.0, -4.0])

@@ -196,6 +196,17 @@ def test_random(seed):
 
 
 @gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("scale", [-0.9, 0.0])
+def test_other_scales(d, scale):
+    """Negative ones, with scores far apart, and none at all. (Scores of a few tens: fp32's 2^-24 of
+    them, and of the products in them, stays below the lse's 1e-4.)"""
+    c = Case(12, [300, 40], [300, 60], 90, 3, 2, 1, d, torch.bfloat16, BR)
+    c.scale = scale
+    c.check()
+
+
+@gpu
 @pytest.mark.parametrize("mask", [TL, BR])
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_long_windows_are_the_causal_masks(mask, d):
