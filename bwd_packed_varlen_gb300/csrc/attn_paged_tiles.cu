@@ -19,6 +19,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -296,7 +297,8 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
       }
       const int r = x * 128 + quarter * 32 + lane, rr = w.row0 + min(r, w.rows - 1), i = rr / p.group;
       const bool live = r < w.rows;
-      const int hi = live ? t.s.past + i + 1 : 0, lo = paged_first(p, t.s, i);
+      // (rows behind the last one see everything: their warp then takes the way without masks)
+      const int hi = live ? t.s.past + i + 1 : INT_MAX, lo = live ? paged_first(p, t.s, i) : 0;
       float m = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int u = t.u0; u < t.u0 + t.n; ++u) {

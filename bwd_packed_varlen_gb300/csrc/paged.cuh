@@ -51,18 +51,20 @@ __device__ __forceinline__ uint32_t pack_meta(float step, float least) {
 template <bool kBF16>
 constexpr uint32_t kCodeMagic = kBF16 ? 0x43004300u : 0x64006400u;
 
-// The two codes in bits 0-3 and 16-19 of w. `magic` is kCodeMagic from a place that the compiler
-// cannot see into: with mask and magic both constants it spends two instructions on the one
-// that does both.
-template <bool kBF16>
+// The two codes in bits 0-3 and 16-19 of w (kHigh, fp16 alone, whose fraction has room for them:
+// bits 4-7 and 20-23). `magic` is kCodeMagic from a place that the compiler cannot see into: with
+// mask and magic both constants it spends two instructions on the one that does both.
+template <bool kBF16, bool kHigh = false>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t magic) {
   uint32_t x;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(0x000f000fu), "r"(magic));  // (w & mask) | magic
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(kHigh ? 0x00f000f0u : 0x000f000fu), "r"(magic));  // (w & mask) | magic
   if constexpr (kBF16) {
+    static_assert(!kHigh, "bf16 keeps seven bits of a fraction");
     const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __float2bfloat162_rn(128.f));
     return *reinterpret_cast<const uint32_t*>(&y);
   } else {
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(1024.f));
+    const __half2 h = *reinterpret_cast<const __half2*>(&x);
+    const __half2 y = kHigh ? __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-64.f)) : __hsub2(h, __float2half2_rn(1024.f));
     return *reinterpret_cast<const uint32_t*>(&y);
   }
 }
@@ -81,8 +83,16 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t codes, uint32_t step2, u
 // The four pairs (i, i + 4) of a word's codes as values.
 template <bool kBF16>
 __device__ __forceinline__ void value_pairs(uint32_t w, uint32_t step2, uint32_t least2, uint32_t magic, uint32_t (&r)[4]) {
+  if constexpr (kBF16) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = value_pair<kBF16>(code_pair<kBF16>(w >> (4 * i), magic), step2, least2);
+    for (int i = 0; i < 4; ++i) r[i] = value_pair<true>(code_pair<true>(w >> (4 * i), magic), step2, least2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      r[i] = value_pair<false>(code_pair<false>(w >> (4 * i), magic), step2, least2);
+      r[i + 1] = value_pair<false>(code_pair<false, true>(w >> (4 * i), magic), step2, least2);
+    }
+  }
 }
 
 // The eight elements of a word of codes, in order.

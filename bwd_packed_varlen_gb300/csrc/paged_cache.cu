@@ -112,7 +112,7 @@ __device__ __forceinline__ uint32_t quantize8(const float (&f)[8], uint32_t* met
 
 // V elements per access; kHalf: pairs (c, c + rot/2), otherwise (2c, 2c + 1), as in rope.cu.
 template <int V, bool kHalf, bool kBF16, bool k4>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 8) paged_append_kernel(const __grid_constant__ AppendParams p) {
   // (cos, sin) of pair i of unit u at [token][i][u]; behind them, with 4 bits, turned keys
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Token s_tok[kAppendTokens];
