@@ -81,17 +81,12 @@ struct PagedCut {
   // line is found by division; their kernel passes over what the tile does not see.
   __device__ __forceinline__ PagedRun run(const PagedParams& p, const PagedSeq& s, int tile) const {
     if (!wide) return paged_run(p, s, 0, s.n - 1, unit);
-    const long long r0 = static_cast<long long>(tile) * rows;
-    const int i0 = static_cast<int>(r0 / p.group);
-    const long long i1 = (r0 + rows - 1) / p.group;
-    return paged_run(p, s, i0, i1 < s.n ? static_cast<int>(i1) : s.n - 1, unit);
+    const int r0 = tile * rows;  // (a call's rows are below 2^31 - 256)
+    return paged_run(p, s, r0 / p.group, min((r0 + rows - 1) / p.group, s.n - 1), unit);
   }
-  // Units of the first `n` row tiles of a sequence.
+  // Units of the first `n` row tiles of a sequence, for tiles of few rows.
   __device__ __forceinline__ long long before(const PagedParams& p, const PagedSeq& s, int n) const {
-    if (!wide) return n > 0 ? static_cast<long long>(n) * p.hkv * run(p, s, 0).n : 0;
-    long long sum = 0;
-    for (int t = 0; t < n; ++t) sum += run(p, s, t).n;
-    return sum * p.hkv;
+    return n > 0 ? static_cast<long long>(n) * p.hkv * run(p, s, 0).n : 0;
   }
 };
 
@@ -116,12 +111,25 @@ __device__ __forceinline__ Stretch stretch_at(const PagedParams& p, const PagedC
   t.s = load_paged_seq(p, lo);
   long long r = at - pref[lo];
   if (cut.wide) {
-    for (t.tile = 0;; ++t.tile) {
-      t.run = cut.run(p, t.s, t.tile);
-      const long long all = static_cast<long long>(p.hkv) * t.run.n;
-      if (r < all) break;
-      r -= all;
+    // the whole warp looks through the row tiles, 32 at a time
+    const int lane = threadIdx.x & 31, tiles = cut.tiles(p, t.s);
+    for (t.tile = 0; t.tile < tiles; t.tile += 32) {
+      const int mine = t.tile + lane < tiles ? cut.run(p, t.s, t.tile + lane).n : 0;
+      long long upto = static_cast<long long>(mine) * p.hkv;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const uint32_t behind = __ballot_sync(0xffffffffu, upto > r);
+      const int k = behind ? __ffs(behind) - 1 : 32;  // the tile in which the place lies
+      if (k > 0) r -= __shfl_sync(0xffffffffu, upto, k - 1);
+      if (k < 32) {
+        t.tile += k;
+        break;
+      }
     }
+    t.run = cut.run(p, t.s, t.tile);
     t.head = static_cast<int>(r / t.run.n);
     t.u0 = static_cast<int>(r - static_cast<long long>(t.head) * t.run.n);
   } else {
@@ -136,6 +144,22 @@ __device__ __forceinline__ Stretch stretch_at(const PagedParams& p, const PagedC
   return t;
 }
 
+// The stretch of many rows that follows `t`, which ends at place `at`; with `first` the one there.
+__device__ __forceinline__ void next_stretch(const PagedParams& p, const PagedCut& cut, const long long* pref, long long at, long long end,
+                                             bool first, Stretch& t) {
+  if (!first && ++t.head == p.hkv) {
+    t.head = 0;
+    if (++t.tile < cut.tiles(p, t.s)) t.run = cut.run(p, t.s, t.tile);
+    else first = true;  // the next sequence
+  }
+  if (first) {
+    t = stretch_at(p, cut, pref, at, end);
+    return;
+  }
+  t.u0 = 0;
+  t.n = end - at < t.run.n ? static_cast<int>(end - at) : t.run.n;
+}
+
 // Prefix sums of the sequences' units in `pref` (shared memory, batch + 1 values), by the whole
 // block; returns the total. Lengths that do not fit are reported in *status.
 __device__ __forceinline__ long long sum_units(const PagedParams& p, const PagedCut& cut, long long* pref, int* status) {
@@ -148,10 +172,25 @@ __device__ __forceinline__ long long sum_units(const PagedParams& p, const Paged
   for (int base = 0; base < p.batch; base += blockDim.x) {
     const int b = base + tid;
     long long w = 0;
+    int tiles = 0;
     if (b < p.batch) {
       const PagedSeq s = load_paged_seq(p, b);
       if (!s.ok) atomicOr(status, kStatusBadSeqlens);
-      if (cut.takes(p, s)) w = cut.before(p, s, cut.tiles(p, s));
+      if (cut.takes(p, s)) {
+        tiles = cut.tiles(p, s);
+        if (!cut.wide) w = cut.before(p, s, tiles);
+      }
+    }
+    if (cut.wide) {  // the warp adds up its sequences' row tiles, one sequence after the other
+      for (uint32_t some = __ballot_sync(0xffffffffu, tiles > 0); some; some &= some - 1) {
+        const int k = __ffs(some) - 1, n = __shfl_sync(0xffffffffu, tiles, k);
+        const PagedSeq s = load_paged_seq(p, b - lane + k);
+        long long sum = 0;
+        for (int t = lane; t < n; t += 32) sum += cut.run(p, s, t).n;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == k) w = sum * p.hkv;
+      }
     }
     long long x = w;
 #pragma unroll

@@ -290,7 +290,14 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
 
 #pragma unroll 1
     for (int u = t.u0; u < t.u0 + t.n; ++u) {
-      if (!mbar_wait_warp(&bar[warp][stage_at], phase, status)) return;
+      if (!mbar_wait_warp(&bar[warp][stage_at], phase, status)) {
+        for (int i = done; i < loaded; ++i) {
+          mbar_drain(&bar[warp][stage_at], phase);
+          stage_at = stage_at + 1 == NS ? 0 : stage_at + 1;
+          phase ^= stage_at == 0 ? 1 : 0;
+        }
+        return;
+      }
       const uint32_t stage = smem_u32(ring + stage_at * S::kStageBytes);
       const uint32_t loaded_blocks = seen_fifo & ((1u << kBlocks) - 1u);
       const int key0 = t.run.unit(u) * kUnit;

@@ -135,9 +135,10 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
     int it = 0;
     bool ok = true;
     int ii = 0;
+    Stretch t;
 #pragma unroll 1
     for (long long at = begin; at < end && ok; ++ii) {
-      const Stretch t = stretch_at(p, cut, pref, at, end);
+      next_stretch(p, cut, pref, at, end, at == begin, t);
       const TileView w = tile_view(p, t);
       if (ii > 0 && !(ok = mbar_wait_warp(&bar_q_empty, (ii - 1) & 1, status))) break;
       const bool boxes = tm.q_tokens > 0;
@@ -189,6 +190,15 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
       }
       at += t.n;
     }
+    if (!ok) {  // given up: the copies on their way land before the block ends
+      mbar_drain(&bar_q_full, ii & 1);
+      if constexpr (!k4) {
+        for (int i = it > NS ? it - NS : 0; i <= it; ++i) {
+          mbar_drain(&bar_k_full[i % NS], (i / NS) & 1);
+          mbar_drain(&bar_v_full[i % NS], (i / NS) & 1);
+        }
+      }
+    }
   } else if (warp == 9) {
     // ------------------------------------------------------------- products
     constexpr uint32_t idS = make_idesc_f16(kBF16, false, false, 128, 128);
@@ -209,9 +219,10 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
       }
       mma_commit(&bar_s_full[x]);
     };
+    Stretch t;
 #pragma unroll 1
     for (long long at = begin; at < end && ok; ++ii) {
-      const Stretch t = stretch_at(p, cut, pref, at, end);
+      next_stretch(p, cut, pref, at, end, at == begin, t);
       const TileView w = tile_view(p, t);
       const int nx = w.rows > 128 ? 2 : 1;
       if (!(ok = mbar_wait_warp(&bar_q_full, ii & 1, status))) break;
@@ -286,9 +297,10 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
     int ns = 0, no = 0;  // tiles and stretches of this side so far
     int skipped = 0;     // tiles that the other side had alone
     bool ok = true;
+    Stretch t;
 #pragma unroll 1
     for (long long at = begin; at < end && ok;) {
-      const Stretch t = stretch_at(p, cut, pref, at, end);
+      next_stretch(p, cut, pref, at, end, at == begin, t);
       const TileView w = tile_view(p, t);
       at += t.n;
       if (x == 1 && w.rows <= 128) {
@@ -456,9 +468,10 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
       uint32_t meta[kG];
       bool there;
     };
+    Stretch t;
 #pragma unroll 1
     for (long long at = begin; at < end && ok;) {
-      const Stretch t = stretch_at(p, cut, pref, at, end);
+      next_stretch(p, cut, pref, at, end, at == begin, t);
       const TileView w = tile_view(p, t);
       // keys or values of a unit, into registers; a key that no row sees stands for zeros
       auto fetch = [&](int u, int kv, Raw& raw) {

@@ -63,6 +63,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // about kWaitLimitNs, records kErrTimeout in *status and returns false. A wait
 // also gives up early once another thread has recorded a timeout.
 constexpr unsigned long long kWaitLimitNs = 4000000000ull;
+constexpr unsigned long long kDrainLimitNs = 100000000ull;
 constexpr int kErrTimeout = 2;
 
 __device__ __forceinline__ unsigned long long global_ns() {
@@ -96,6 +97,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* s
 // result is warp-uniform and the warp is converged afterwards.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, int* status) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+}
+
+// Bounded wait for a copy that is still on its way, by a kernel that is giving up: its shared
+// memory must not be another block's when the copy lands.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, parity) && global_ns() - t0 < kDrainLimitNs) {
+  }
 }
 
 // ---------------------------------------------------------------------------

@@ -410,3 +410,106 @@ def test_decoding_in_a_graph(bits):
     if bits == 16:
         same = ta.window_fwd(qr, kr, v, cu, cu, cu, cu, 0.125, 24, 2)
         prefix_check({"out": same[0], "lse": same[1]}, ref, ("out", "lse"), BF)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("window", [0, 100])
+def test_prompts_of_many_row_tiles(bits, window):
+    """More row tiles than a warp looks through at once, in sequences on both sides of one of few rows."""
+    Case(66, [700, 1, 560], [40, 90, 0], 64, 17, 1, 64, BF, bits, window, 3 if window else 0).check()
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("n", [1, 60])
+def test_pages_that_sequences_share(bits, n):
+    """Two sequences over the same pages, the same page twice in one of them, and a table whose rows are
+    slices of wider ones, against a cache in which every sequence has copies of its own."""
+    c = Case(67, [n] * 2, [64 * 5 - n] * 2, 64, 8, 2, 128, BF, bits, slot=1, tail=0).dev()
+    table = torch.full((2, 40), -9, dtype=torch.int32, device="cuda")
+    table[0, 3:8] = c.on[3][0, :5]
+    table[1, 3:8] = c.on[3][0, :5]
+    table[1, 5] = table[1, 3]
+    shared = ta.paged_fwd(*c.on[:3], table[:, 3:8], *c.on[4:], c.scale)
+    own = torch.arange(10, dtype=torch.int32, device="cuda").view(2, 5)
+    pages = table[:, 3:8].flatten().long()
+    copies = [tuple(t[pages].clone() for t in x) if bits == 4 else x[pages].clone() for x in c.on[1:3]]
+    assert _same(shared, ta.paged_fwd(c.on[0], *copies, own, *c.on[4:], c.scale))
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("n", [1, 60])
+def test_offsets_past_32_bits(bits, n):
+    """Pages that begin more than 4 GiB, and 2^31 elements, into the cache."""
+    c = Case(68, [n, 1], [300, 5], 64, 32, 8, 128, BF, bits).dev()
+    first = c.fwd()
+    far = 40000 * (4 if bits == 4 else 1)
+    large = ta.paged_cache(far + c.pages, 64, 8, 128, BF, bits)
+    for big, x in zip(large, c.on[1:3]):
+        for a, b in zip(big, x) if bits == 4 else ((big, x),):
+            a[far:].copy_(b)
+    table = torch.where(c.on[3] >= 0, c.on[3] + far, c.on[3])
+    assert _same(first, ta.paged_fwd(c.on[0], *large, table, *c.on[4:], c.scale))
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+def test_two_streams_at_once(bits):
+    """Calls in flight on two streams, each with its own workspace, do not touch each other."""
+    cs = [Case(s, [1] * 20 + [90, 130], [(s + 41 * i) % 700 for i in range(20)] + [500, 30], 32, 8, 2, 128, BF, bits).dev() for s in (69, 70)]
+    refs = [[x.clone() for x in c.fwd()] for c in cs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, (c, st) in enumerate(zip(cs, streams)):
+            with torch.cuda.stream(st):
+                got[i].append(c.fwd())
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert _same(refs[i], g)
+
+
+@gpu
+def test_given_outputs_and_streams():
+    c = Case(71, [1, 90, 3], [300, 20, 64], 16, 4, 2, 64, BF, 16).dev()
+    want = c.fwd()
+    o, l = torch.full_like(want[0], float("nan")), torch.full_like(want[1], float("nan"))
+    got = c.fwd(out=o, lse=l)
+    assert got[0] is o and got[1] is l and _same(want, got)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        a = c.fwd(stream=side.cuda_stream)
+        torch.empty(1 << 20, device="cuda").fill_(float("nan"))  # of the current stream's memory
+        side.synchronize()
+        assert _same(want, a)
+    assert not any(x.requires_grad for x in ta.paged_fwd(c.on[0].clone().requires_grad_(), *c.on[1:], c.scale))
+    for bad in (dict(out=o[:-1]), dict(lse=l.double()), dict(out=o.half()), dict(lse=l[:, :1])):
+        with pytest.raises(ValueError):
+            c.fwd(**bad)
+    with pytest.raises(ta.TeAttnError, match="workspace"):
+        c.fwd(workspace=c.workspace()[:-256])
+    assert _same(want, c.fwd())
+
+
+@gpu
+def test_captured_calls_that_share_a_workspace():
+    """Two captured calls of different shapes, one workspace, replayed in turn on one stream."""
+    a, b = (Case(s, n, p, 16, 4, 2, 128, BF, 16).dev() for s, n, p in ((72, [1, 70], [400, 60], ), (73, [90, 2, 1], [30, 0, 800])))
+    want = [a.fwd(), b.fwd()]
+    ws = max((c.workspace() for c in (a, b)), key=lambda t: t.numel())
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for graph, c in zip(graphs, (a, b)):
+        with torch.cuda.graph(graph):
+            outs.append(c.fwd(workspace=ws))
+    for _ in range(3):
+        for i in range(2):
+            outs[i][0].fill_(float("nan"))
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert _same(want[i], outs[i]) and ta.read_status(ws) == 0
