@@ -402,6 +402,8 @@ int api_paged_cache(const te_attn_paged_cache* c, PagedCache* out) {
   if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)))
     return api_fail(TE_ERR_UNSUPPORTED, "page_size must be a power of two in [16, 4096]");
   if (c->num_pages < 1 || c->max_pages < 1) return api_fail(TE_ERR_INVALID_ARG, "num_pages and max_pages must be >= 1");
+  if (static_cast<long long>(c->max_pages) * c->page_size > (1 << 30))
+    return api_fail(TE_ERR_UNSUPPORTED, "a sequence's pages hold at most 2^30 tokens");
   if (c->hkv < 1) return api_fail(TE_ERR_INVALID_ARG, "hkv must be >= 1");
   if (c->hkv > 4096) return api_fail(TE_ERR_UNSUPPORTED, "at most 4096 heads");
   if (c->d < 8 || c->d > 256 || c->d % 8 != 0)

@@ -76,8 +76,6 @@ int te_attn_paged_fwd_thd(const te_attn_paged_cache* cache, const void* q, void*
                         static_cast<const void*>(past), static_cast<const void*>(lse)})
     if (!aligned(x, 4)) return api_fail(TE_ERR_INVALID_ARG, "int32 arrays and lse need their natural alignment");
   if (batch > kPagedMaxBatch) return api_fail(TE_ERR_UNSUPPORTED, "at most 4096 sequences");
-  if (static_cast<long long>(cache->max_pages) * cache->page_size > (1 << 30))
-    return api_fail(TE_ERR_UNSUPPORTED, "a sequence's pages hold at most 2^30 tokens");
   if (!workspace) return api_fail(TE_ERR_INVALID_ARG, "workspace must not be NULL");
   if (total_q > 0 && (!q || !out || !lse)) return api_fail(TE_ERR_INVALID_ARG, "q, out and lse must not be NULL");
   PagedLayout L;

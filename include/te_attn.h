@@ -418,11 +418,12 @@ int te_attn_prefix_bwd_thd(const void* q, const void* k, const void* v, const vo
  *            the least of the 32, s = (greatest - m) / 15 rounded towards zero to 16 bits,
  *            code = (x - m) / s rounded to the nearest of 0..15, ties to even; 32 elements among
  *            which is a NaN or an infinity read as NaN.
- * A page is contiguous; strides from page to page, in bytes, are multiples of 16 (k_meta,
- * v_meta: of 4) and pointers are aligned to 16 bytes, so that layers, or keys and values, may
- * lie side by side. page_size is a power of two in [16, 4096], d a multiple of 8 in [8, 256].
- * Entries of the page table beside those that a call needs are not looked at. No two live
- * positions may share a place.
+ * A page is contiguous; strides from page to page, in bytes, and pointers are multiples of 16, so
+ * that layers, or keys and values, may lie side by side. page_size is a power of two in
+ * [16, 4096], d a multiple of 8 in [8, 256]; a sequence's pages hold at most 2^30 tokens.
+ * Entries of the page table beside those that a call needs are not looked at. Sequences may read
+ * the same pages (of a common beginning, say); an append that writes a place twice leaves any
+ * mixture of both there.
  */
 typedef struct te_attn_paged_cache {
   void* k;

@@ -332,3 +332,77 @@ def test_graph_and_streams(bits):
     other = c.append(want, stream=side.cuda_stream)
     side.synchronize()
     assert torch.equal(other, ref)
+
+
+def test_tables_of_too_many_pages_are_refused():
+    """Positions stay below 2^30 for every call on a cache."""
+    L, one, null = ta.library(), ctypes.c_void_p(4096), None
+    for pages, page, code in ((2 ** 26, 16, 0), (2 ** 26 + 1, 16, -2), (2 ** 31 - 1, 16, -2), (2 ** 18, 4096, 0), (2 ** 18 + 1, 4096, -2)):
+        c = sound_struct(page=page)
+        c.max_pages = pages
+        assert L.te_attn_paged_gather(ctypes.byref(c), one, one, one, one, one, 1, 0, null, null) == code, (pages, page)
+        assert L.te_attn_paged_append(ctypes.byref(c), null, null, null, null, null, 0, one, one, one, 1, 0, 0, *[ctypes.c_int64(0)] * 6, 0,
+                                      ctypes.c_float(1.0), null, null) == code, (pages, page)
+        if code:
+            assert "2^30" in _last()
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+def test_offsets_past_32_bits(bits):
+    """Pages whose bytes begin more than 4 GiB, and whose elements more than 2^31, into the cache."""
+    c = Case(37, [70, 1], [30, 200], 64, 4, 8, 128, BF, bits, 64).dev()
+    small, far = c.fresh(), 40000 * (4 if bits == 4 else 1)
+    large = ta.paged_cache(far + c.pages, 64, 8, 128, BF, bits)
+    q = c.append(small)
+    first = c.gather(small)
+    c.table_on = torch.where(c.table_on >= 0, c.table_on + far, c.table_on)
+    assert torch.equal(q, c.append(large))
+    assert all(torch.equal(a, b) for a, b in zip(first, c.gather(large)))
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+def test_queries_turned_in_place(bits):
+    c = Case(38, [40, 3], [0, 20], 16, 3, 1, 96, FP, bits, 64, fused=False).dev()
+    a, b = c.fresh(), c.fresh()
+    want = c.append(a)
+    got = c.append(b, q_out=c.on[0])
+    assert got is c.on[0] and torch.equal(want, got)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+def test_two_appends_at_once(bits):
+    """On two streams, into caches of their own."""
+    cs = [Case(s, [300, 1, 70], [5, 90, 0], 32, 8, 2, 128, BF, bits, 128).dev() for s in (39, 40)]
+    want = [c.fresh() for c in cs]
+    qs = [c.append(w) for c, w in zip(cs, want)]
+    refs = [c.gather(w) for c, w in zip(cs, want)]
+    fresh, streams = [c.fresh() for c in cs], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append((cs[i].append(fresh[i]), *cs[i].gather(fresh[i])))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip((qs[i], *refs[i]), g))
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+def test_pages_read_by_several(bits):
+    """Sequences that share the pages of a common beginning, out of a table with rows wider than it."""
+    c = Case(41, [100, 20], [0, 90], 16, 2, 2, 64, BF, bits, 0).dev()
+    caches = c.fresh()
+    c.append(caches)
+    wide = torch.full((4, 20), 2 ** 30, dtype=torch.int32, device="cuda")
+    wide[0, :7], wide[3, :7] = c.table_on[0, :7], c.table_on[0, :7]
+    cu = torch.tensor([0, 100, 200], dtype=torch.int32, device="cuda")
+    start = torch.zeros(2, dtype=torch.int32, device="cuda")
+    k, v = ta.paged_gather(*caches, wide[::3, :7], start, cu, cu, 200)
+    want = four_bits(c.v[:100])[2] if bits == 4 else c.v[:100]
+    assert torch.equal(v[:100].cpu(), want) and torch.equal(v[:100], v[100:]) and torch.equal(k[:100], k[100:])

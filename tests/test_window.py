@@ -305,3 +305,80 @@ def test_graph_replays_follow_their_buffers():
     graph.replay()
     torch.cuda.synchronize()
     assert _same((out, lse, *grads), want)
+
+
+@gpu
+def test_two_streams_at_once():
+    """Calls in flight on two streams, each with its own workspace, do not touch each other."""
+    cs = [Case(s, [2600, 90, 300], [2600, 400, 300], 100, 3, 4, 2, 64, torch.bfloat16, BR).dev() for s in (31, 32)]
+    refs = [[x.clone() for x in c.fwd()] for c in cs]
+    grads = [[x.clone() for x in c.bwd(*r)] for c, r in zip(cs, refs)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for i, (c, st) in enumerate(zip(cs, streams)):
+            with torch.cuda.stream(st):
+                out, lse = c.fwd()
+                got[i].append([out, lse, *c.bwd(out, lse)])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert _same(refs[i] + grads[i], g)
+
+
+@gpu
+def test_given_outputs_streams_and_workspaces():
+    c = Case(33, [5, 300, 1], [40, 300, 90], 50, 2, 4, 2, 128, torch.float16, BR).dev()
+    out, lse = c.fwd()
+    grads = c.bwd(out, lse)
+    o, l = torch.full_like(out, float("nan")), torch.full_like(lse, float("nan"))
+    got = c.fwd(out=o, lse=l)
+    assert got[0] is o and got[1] is l and _same((out, lse), got)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        a = c.fwd(stream=side.cuda_stream)
+        b = c.bwd(*a, stream=side.cuda_stream)
+        torch.empty(1 << 20, device="cuda").fill_(float("nan"))  # of the current stream's memory
+        side.synchronize()
+        assert _same((out, lse, *grads), (*a, *b))
+    for call, bad in ((c.fwd, dict(out=o[:-1])), (c.fwd, dict(lse=l.half())), (lambda **kw: c.bwd(out, lse, **kw), dict(dq=o.float())),
+                      (lambda **kw: c.bwd(out, lse, **kw), dict(dk=o))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ta.TeAttnError, match="workspace"):
+        c.fwd(workspace=small)
+    with pytest.raises(ta.TeAttnError, match="workspace"):
+        c.bwd(out, lse, workspace=small)
+    with pytest.raises(ValueError):
+        ta.window_fwd(c.on[0].transpose(0, 1), *c.on[1:], *c.cu_on, c.scale, 50, 2)
+
+
+@gpu
+def test_a_captured_backward_of_its_own_leaves():
+    """Forward and backward through autograd, captured into a graph, follow their leaves."""
+    gen = torch.Generator().manual_seed(34)
+    x = [torch.randn(260, h, 64, generator=gen).to(torch.bfloat16).cuda() for h in (4, 2, 2, 4)]
+    cu = prefix_sums([200, 60]).cuda()
+
+    def run(leaves):
+        out = ta.dot_product_attention(*leaves, cu, cu, cu, cu, window=40, sinks=1)
+        return (out.detach(), *torch.autograd.grad(out, leaves, x[3].view(260, -1)))
+    want = run([t.clone().requires_grad_() for t in x[:3]])
+    leaves = [torch.zeros_like(t).requires_grad_() for t in x[:3]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(leaves)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(leaves)
+    with torch.no_grad():
+        for a, b in zip(leaves, x):
+            a.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert _same(want, got)
