@@ -160,6 +160,8 @@ __device__ __forceinline__ void next_stretch(const PagedParams& p, const PagedCu
   t.n = end - at < t.run.n ? static_cast<int>(end - at) : t.run.n;
 }
 
+constexpr int kTilesOfThread = 8;  // row tiles that a thread adds up by itself
+
 // Prefix sums of the sequences' units in `pref` (shared memory, batch + 1 values), by the whole
 // block; returns the total. Lengths that do not fit are reported in *status.
 __device__ __forceinline__ long long sum_units(const PagedParams& p, const PagedCut& cut, long long* pref, int* status) {
@@ -173,18 +175,25 @@ __device__ __forceinline__ long long sum_units(const PagedParams& p, const Paged
     const int b = base + tid;
     long long w = 0;
     int tiles = 0;
+    PagedSeq s{0, 0, 0, true};
     if (b < p.batch) {
-      const PagedSeq s = load_paged_seq(p, b);
+      s = load_paged_seq(p, b);
       if (!s.ok) atomicOr(status, kStatusBadSeqlens);
       if (cut.takes(p, s)) {
         tiles = cut.tiles(p, s);
         if (!cut.wide) w = cut.before(p, s, tiles);
       }
     }
-    if (cut.wide) {  // the warp adds up its sequences' row tiles, one sequence after the other
-      for (uint32_t some = __ballot_sync(0xffffffffu, tiles > 0); some; some &= some - 1) {
+    if (cut.wide) {
+      // a thread adds up a sequence of few row tiles, a warp one of many
+      const bool many = tiles > kTilesOfThread;
+      if (!many) {
+        for (int t = 0; t < tiles; ++t) w += cut.run(p, s, t).n;
+        w *= p.hkv;
+      }
+      for (uint32_t some = __ballot_sync(0xffffffffu, many); some; some &= some - 1) {
         const int k = __ffs(some) - 1, n = __shfl_sync(0xffffffffu, tiles, k);
-        const PagedSeq s = load_paged_seq(p, b - lane + k);
+        s = load_paged_seq(p, b - lane + k);
         long long sum = 0;
         for (int t = lane; t < n; t += 32) sum += cut.run(p, s, t).n;
 #pragma unroll

@@ -16,6 +16,7 @@
 namespace teattn {
 
 constexpr int kJoinThreads = 128;
+constexpr int kJoinBlocks = 16 * kPagedSMs;
 
 __device__ __forceinline__ float ex2j(float x) {
   float y;
@@ -97,23 +98,68 @@ __device__ void join_wide(const PagedParams& p, const PagedParts& parts, int w, 
   if (part < 2) p.lse[row] = M * 0.69314718055994531f + logf(L);
 }
 
+// How blocks share the rows of the kernel of few rows. Without the other kernel: `heads` heads of a
+// token each. With it most tokens may be the other's, and blocks that find nothing to do take a
+// nanosecond each: a block a head of a sequence (parts of its queries), behind `scans` blocks that
+// look for rows that are no token.
+struct JoinGrid {
+  int heads, scans, parts;
+};
+constexpr int kScanTokens = 32;
+
 template <bool kBF16>
 __global__ void __launch_bounds__(kJoinThreads)
     paged_join_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ PagedCut few, const __grid_constant__ PagedParts few_parts,
-                      const __grid_constant__ PagedParts wide_parts, int heads) {
+                      const __grid_constant__ PagedParts wide_parts, JoinGrid grid) {
   __shared__ float2 s_ml[4];
   __shared__ float s_o[4][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wide_blocks = wide_parts.slices * kWideJoin;  // ahead of the rows
-  const int per_token = p.hq / heads;  // blocks of a token, of `heads` heads each
-  const int at_row = blockIdx.x - 1 - wide_blocks, tok = at_row / per_token, hq0 = (at_row - tok * per_token) * heads;
+  const int at_row = blockIdx.x - 1 - wide_blocks;
   PagedSeq s{0, 0, 0, true};
-  int b = -1;
-  if (at_row >= 0) {
+  int b = -1, i0 = 0, i1 = 0, step = 1, hq0 = 0, hq1 = 0;  // queries i0, i0 + step, ... of sequence b; their heads
+  auto sequence_of = [&](int tok) {  // by a whole warp
     int before = 0;
     for (int k = lane; k < p.batch; k += 32) before += p.cu_q_pad[k] <= tok ? 1 : 0;
     b = __reduce_add_sync(0xffffffffu, before) - 1;
     if (b >= 0) s = load_paged_seq(p, b);
+    return b >= 0 && tok - s.off < s.n;
+  };
+  auto no_token = [&](int tok, int h0, int h1, int at, int threads) {
+    const long long row = static_cast<long long>(tok) * p.hq + h0;
+    for (int c = at * 8; c < p.d * (h1 - h0); c += threads * 8)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.d + c) = make_uint4(0, 0, 0, 0);
+    for (int h = at; h < h1 - h0; h += threads) p.lse[row + h] = 0.f;
+  };
+  if (at_row < 0) {
+  } else if (grid.parts == 0) {  // a token, or a head of it
+    const int per_token = p.hq / grid.heads, tok = at_row / per_token;
+    hq0 = (at_row - tok * per_token) * grid.heads;
+    hq1 = hq0 + grid.heads;
+    if (sequence_of(tok)) {
+      i0 = tok - s.off;
+      i1 = i0 + 1;
+    } else {
+      pdl_wait();
+      no_token(tok, hq0, hq1, threadIdx.x, kJoinThreads);
+      return;
+    }
+  } else if (at_row < grid.scans) {  // rows that are no token, of kScanTokens rows
+    pdl_wait();
+    for (int k = warp; k < kScanTokens; k += kJoinThreads / 32) {
+      const int tok = at_row * kScanTokens + k;
+      if (tok < p.total_q && !sequence_of(tok)) no_token(tok, 0, p.hq, lane, 32);
+    }
+    return;
+  } else {  // a head of a sequence, or of every grid.parts-th query
+    const int n = at_row - grid.scans, seg = n / grid.parts;
+    b = seg / p.hq;
+    hq0 = seg - b * p.hq;
+    hq1 = hq0 + 1;
+    i0 = n - seg * grid.parts;
+    step = grid.parts;
+    s = load_paged_seq(p, b);
+    i1 = s.n;
   }
   pdl_wait();
   if (blockIdx.x == 0) {  // the call's status
@@ -130,27 +176,20 @@ __global__ void __launch_bounds__(kJoinThreads)
     join_wide<kBF16>(p, wide_parts, (blockIdx.x - 1) / kWideJoin, (blockIdx.x - 1) % kWideJoin);
     return;
   }
-  const int i = tok - s.off;
-  if (b < 0 || i >= s.n) {
-    const long long row = static_cast<long long>(tok) * p.hq + hq0;
-    for (int c = threadIdx.x * 8; c < p.d * heads; c += kJoinThreads * 8)
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.d + c) = make_uint4(0, 0, 0, 0);
-    for (int h = threadIdx.x; h < heads; h += kJoinThreads) p.lse[row + h] = 0.f;
-    return;
-  }
   if (!few.takes(p, s)) return;  // the other kernel's
 #pragma unroll 1
-  for (int hq = hq0; hq < hq0 + heads; ++hq) {
-    const long long row = static_cast<long long>(tok) * p.hq + hq;
+  for (int n = 0; i0 + n / (hq1 - hq0) * step < i1; ++n) {
+    const int i = i0 + n / (hq1 - hq0) * step, hq = hq0 + n % (hq1 - hq0);
+    const long long row = static_cast<long long>(s.off + i) * p.hq + hq;
     uint16_t* out = static_cast<uint16_t*>(p.out) + row * p.d;
     const PagedParts& parts = few_parts;
     const int h = hq / p.group;
     const long long rr = static_cast<long long>(i) * p.group + hq - h * p.group;
     const int tile = static_cast<int>(rr / few.rows), r = static_cast<int>(rr - static_cast<long long>(tile) * few.rows);
-    const int n = few.run(p, s, tile).n;
+    const int units = few.run(p, s, tile).n;
     const long long per = slice_units(parts.pref[p.batch], parts.slices, parts.least);
-    const long long first = parts.pref[b] + few.before(p, s, tile) + static_cast<long long>(h) * n;
-    const int w0 = static_cast<int>(first / per), w1 = static_cast<int>((first + n - 1) / per);
+    const long long first = parts.pref[b] + few.before(p, s, tile) + static_cast<long long>(h) * units;
+    const int w0 = static_cast<int>(first / per), w1 = static_cast<int>((first + units - 1) / per);
     if (w0 == w1) continue;  // written whole
     float m, l, acc[8];
     const int cols = p.d / 8;  // eight columns a lane
@@ -199,12 +238,21 @@ bool make_tmap_pages(CUtensorMap* map, const PagedCache& c, int kv, bool bf16, i
 
 cudaError_t launch_paged_join(const PagedParams& p, const PagedCut& cut, const PagedParts& parts, const PagedParts& wide, bool bf16,
                               cudaStream_t st) {
-  // A block a row while that fills the GPU a few times over, then one a token.
-  const long long rows = static_cast<long long>(p.total_q) * p.hq;
-  const int heads = rows > 16 * 16 * kPagedSMs ? p.hq : 1;
+  const long long rows = static_cast<long long>(p.total_q) * p.hq, heads = static_cast<long long>(p.batch) * p.hq;
+  JoinGrid g{1, 0, 0};
+  long long blocks;
+  if (wide.slices > 0) {
+    const long long most = p.wide_rows / p.group, want = kJoinBlocks / heads;  // queries that a sequence may have here
+    g.parts = static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? want : most);
+    g.scans = (p.total_q + kScanTokens - 1) / kScanTokens;
+    blocks = g.scans + heads * g.parts;
+  } else {
+    // a block a row while that fills the GPU a few times over, then one a token
+    if (rows > 16 * 16 * kPagedSMs) g.heads = p.hq;
+    blocks = rows / g.heads;
+  }
   return launch_dependent(bf16 ? paged_join_kernel<true> : paged_join_kernel<false>,
-                          dim3(static_cast<unsigned>(rows / heads + wide.slices * kWideJoin + 1)), dim3(kJoinThreads), 0, st, p, cut, parts,
-                          wide, heads);
+                          dim3(static_cast<unsigned>(blocks + wide.slices * kWideJoin + 1)), dim3(kJoinThreads), 0, st, p, cut, parts, wide, g);
 }
 
 }  // namespace teattn

@@ -219,10 +219,11 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
       }
       mma_commit(&bar_s_full[x]);
     };
-    Stretch t;
+    Stretch t, ahead;
+    if (begin < end) next_stretch(p, cut, pref, begin, end, true, ahead);
 #pragma unroll 1
     for (long long at = begin; at < end && ok; ++ii) {
-      next_stretch(p, cut, pref, at, end, at == begin, t);
+      t = ahead;
       const TileView w = tile_view(p, t);
       const int nx = w.rows > 128 ? 2 : 1;
       if (!(ok = mbar_wait_warp(&bar_q_full, ii & 1, status))) break;
@@ -235,6 +236,8 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
       for (int j = 0; j < t.n && ok; ++j) {
         const int cur = it + j, st = cur % NS;
         bool v_ready = false, k_ready = false;
+        // (worked out while this stretch's last P are awaited)
+        if (j + 1 == t.n && at + t.n < end) next_stretch(p, cut, pref, at + t.n, end, false, ahead);
         for (int x = 0; x < nx && ok; ++x) {
           if (!(ok = mbar_wait_warp(&bar_p_ready[x], np[x] & 1, status))) break;
           ++np[x];
@@ -298,13 +301,14 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
     int skipped = 0;     // tiles that the other side had alone
     bool ok = true;
     Stretch t;
+    if (begin < end) next_stretch(p, cut, pref, begin, end, true, t);
 #pragma unroll 1
     for (long long at = begin; at < end && ok;) {
-      next_stretch(p, cut, pref, at, end, at == begin, t);
       const TileView w = tile_view(p, t);
       at += t.n;
       if (x == 1 && w.rows <= 128) {
         skipped += t.n;
+        if (at < end) next_stretch(p, cut, pref, at, end, false, t);
         continue;
       }
       const int r = x * 128 + quarter * 32 + lane, rr = w.row0 + min(r, w.rows - 1), i = rr / p.group;
@@ -420,14 +424,16 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
         l = l * alpha + (s01.x + s01.y);
       }
       if (!ok) break;
+      const int j = rr - i * p.group;
+      const long long row = static_cast<long long>(t.s.off + i) * p.hq + t.head * p.group + j;
+      const bool store = live && bounds_ok(row < static_cast<long long>(p.total_q) * p.hq, status);
+      const bool whole = t.n == t.run.n, begins = t.u0 == 0;
+      if (at < end) next_stretch(p, cut, pref, at, end, false, t);  // (while the last products run)
       ok = __all_sync(0xffffffffu, mbar_wait(&bar_o_full[x], no & 1, status));
       if (!ok) break;
       ++no;
       tc_fence_after();
-      const int j = rr - i * p.group;
-      const long long row = static_cast<long long>(t.s.off + i) * p.hq + t.head * p.group + j;
-      const bool store = live && bounds_ok(row < static_cast<long long>(p.total_q) * p.hq, status);
-      if (t.n == t.run.n) {
+      if (whole) {
         const float inv = l == 0.f ? 0.f : 1.0f / l;
         const auto rows = make_row_pair(static_cast<T*>(p.out) + row * p.d, store);
 #pragma unroll
@@ -440,7 +446,7 @@ __global__ void __launch_bounds__(TilesShape<kD, k4>::kThreads, 1)
         if (store) p.lse[row] = m * 0.69314718055994531f + logf(l);
       } else {
         // column by column, so that a warp's 32 rows lie side by side
-        const long long slot = 2ll * blockIdx.x + (t.u0 == 0 ? 1 : 0);
+        const long long slot = 2ll * blockIdx.x + (begins ? 1 : 0);
         parts.ml[slot * kWideRows + r] = make_float2(m, l);
         float* part = parts.o + slot * p.d * kWideRows + r;
 #pragma unroll
