@@ -11,7 +11,9 @@ inputs with per-tensor descale factors, forward only), ``bwd_noalloc`` (backward
 without a workspace), ``rope`` / ``rope_sbhd`` (rotary positions on q and k, and their
 inverse for the backward pass), ``prefix_fwd`` / ``prefix_bwd`` (attention of a packed batch
 that shares a prefix of keys, one query token per sequence or many), ``window_fwd`` /
-``window_bwd`` and their ``_sbhd`` forms (a sliding window with sinks); ``read_status`` / ``read_status_noalloc`` read a call's device
+``window_bwd`` and their ``_sbhd`` forms (a sliding window with sinks), ``paged_cache`` / ``paged_append`` /
+``paged_gather`` / ``paged_fwd`` (a paged key/value cache in 16 or 4 bits and attention over it); ``read_status`` /
+``read_status_noalloc`` read a call's device
 status word, ``selftest_wait_timeout`` runs the bounded-wait unwind path on purpose and
 ``debug_build()`` routes calls to the bounds-checking build; masks ``padding``, ``padding_causal`` (upper-left) and
 ``padding_causal_bottom_right``. ``dot_product_attention`` / ``DotProductAttention``

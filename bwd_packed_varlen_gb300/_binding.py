@@ -553,7 +553,7 @@ def paged_fwd(q, k_cache, v_cache, page_table, past, cu_seqlens_q, cu_seqlens_q_
 
 def read_status(workspace, stream=None) -> int:
     """Synchronise and return the device status word of the last call that used
-    ``workspace`` (0 clean; bit 1 inconsistent cu_seqlens; bit 2 wait timeout)."""
+    ``workspace`` (0 clean; 1 inconsistent cu_seqlens; 2 wait timeout; 16 pages outside a cache)."""
     L = library()
     st = stream if stream is not None else torch.cuda.current_stream(workspace.device).cuda_stream
     val = ctypes.c_int(0)

@@ -160,7 +160,9 @@ __device__ __forceinline__ void next_stretch(const PagedParams& p, const PagedCu
   t.n = end - at < t.run.n ? static_cast<int>(end - at) : t.run.n;
 }
 
-constexpr int kTilesOfThread = 8;  // row tiles that a thread adds up by itself
+// Row tiles that a thread adds up by itself: a warp of its own for each of 152 short sequences
+// took 25 us, a thread alone for one of 1024 tiles a tenth of a millisecond.
+constexpr int kTilesOfThread = 8;
 
 // Prefix sums of the sequences' units in `pref` (shared memory, batch + 1 values), by the whole
 // block; returns the total. Lengths that do not fit are reported in *status.
@@ -230,8 +232,11 @@ __device__ __forceinline__ long long slice_units(long long total, int slices, in
   const long long per = (total + slices - 1) / slices;
   return per < least ? least : per;
 }
-constexpr int kLeastUnits = 4;      // of a warp: it needs a microsecond before its first product
-constexpr int kLeastWideUnits = 2;  // of a block
+// Keys of a warp at least: it needs a microsecond before its first product, and more pieces to join
+// cost too. 3 sequences of 20-200 keys, d 64: 9.2 us with 32, 11.3 with 64, 12.5 with 128, 26 with 512;
+// 3 of 500 in 16 bits, d 128: 17.8 us with 16, 15.6 with 32, 15.3 with 64.
+constexpr int kLeastKeys = 32;
+constexpr int kLeastWideUnits = 2;  // key tiles of a block
 
 // Partial results of one kernel: two slots a slice (of the segment that it ends, of the one that
 // it begins), each of a row tile's rows; its prefix sums; slices in all.
@@ -256,10 +261,10 @@ bool make_tmap_pages(CUtensorMap* map, const PagedCache& c, int kv, bool bf16, i
 constexpr int kWideRows = 256, kWideKeys = 128;  // of a row tile and a unit of the second kernel
 
 // Rows that one pass over a sequence's keys takes, for a batch of this shape.
-int paged_rows(int batch, int total_q, int group, int d);
+int paged_rows(int batch, int total_q, int group, int d, bool four);
 // Warps of the first kernel's whole grid.
 int paged_warps(int d, bool four, int rows);
 // Rows a kv head from which a sequence goes to the second kernel; 0: it is not launched.
-int paged_wide_rows(int batch, int total_q, int group, int d);
+int paged_wide_rows(int batch, int total_q, int hq, int hkv, int d, bool four);
 
 }  // namespace teattn

@@ -3,7 +3,8 @@
 //
 // A block of four warps per row of out. Of a row's pieces O = sum 2^(m_k - M) O_k / L with
 // M = max m_k and L = sum 2^(m_k - M) l_k, in fp32, every fourth piece in order by a warp and the
-// four warps' sums in order, rounded once. Latency-bound: a decoding step's rows have a few pieces.
+// four warps' sums in order, rounded once. Latency-bound: a decoding step's rows have a few pieces
+// (3-5 us of the call). Rows of the other kernel are joined by a thread each, column by column.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -100,8 +101,9 @@ __device__ void join_wide(const PagedParams& p, const PagedParts& parts, int w, 
 
 // How blocks share the rows of the kernel of few rows. Without the other kernel: `heads` heads of a
 // token each. With it most tokens may be the other's, and blocks that find nothing to do take a
-// nanosecond each: a block a head of a sequence (parts of its queries), behind `scans` blocks that
-// look for rows that are no token.
+// nanosecond each: a block `heads` heads of a sequence (parts of its queries), behind `scans` blocks
+// that look for rows that are no token. 64 single queries beside four prompts of 512: 19 us, a call 211
+// (a block a token with all its heads: a call 271); 19 prompts of 64: 7 us, a block a row 34.
 struct JoinGrid {
   int heads, scans, parts;
 };
@@ -151,11 +153,11 @@ __global__ void __launch_bounds__(kJoinThreads)
       if (tok < p.total_q && !sequence_of(tok)) no_token(tok, 0, p.hq, lane, 32);
     }
     return;
-  } else {  // a head of a sequence, or of every grid.parts-th query
-    const int n = at_row - grid.scans, seg = n / grid.parts;
-    b = seg / p.hq;
-    hq0 = seg - b * p.hq;
-    hq1 = hq0 + 1;
+  } else {  // heads of a sequence, or of every grid.parts-th query
+    const int n = at_row - grid.scans, seg = n / grid.parts, per_seq = p.hq / grid.heads;
+    b = seg / per_seq;
+    hq0 = (seg - b * per_seq) * grid.heads;
+    hq1 = hq0 + grid.heads;
     i0 = n - seg * grid.parts;
     step = grid.parts;
     s = load_paged_seq(p, b);
@@ -238,18 +240,18 @@ bool make_tmap_pages(CUtensorMap* map, const PagedCache& c, int kv, bool bf16, i
 
 cudaError_t launch_paged_join(const PagedParams& p, const PagedCut& cut, const PagedParts& parts, const PagedParts& wide, bool bf16,
                               cudaStream_t st) {
-  const long long rows = static_cast<long long>(p.total_q) * p.hq, heads = static_cast<long long>(p.batch) * p.hq;
+  // A block a row (a head of a sequence) while that fills the GPU a few times over, then one a token (a sequence).
   JoinGrid g{1, 0, 0};
-  long long blocks;
+  long long blocks = static_cast<long long>(wide.slices > 0 ? p.batch : p.total_q) * p.hq;
+  if (blocks > 16 * 16 * kPagedSMs) {
+    g.heads = p.hq;
+    blocks /= p.hq;
+  }
   if (wide.slices > 0) {
-    const long long most = p.wide_rows / p.group, want = kJoinBlocks / heads;  // queries that a sequence may have here
+    const long long most = p.wide_rows / p.group, want = kJoinBlocks / blocks;  // queries that a sequence may have here
     g.parts = static_cast<int>(want < 1 || most < 1 ? 1 : want < most ? want : most);
     g.scans = (p.total_q + kScanTokens - 1) / kScanTokens;
-    blocks = g.scans + heads * g.parts;
-  } else {
-    // a block a row while that fills the GPU a few times over, then one a token
-    if (rows > 16 * 16 * kPagedSMs) g.heads = p.hq;
-    blocks = rows / g.heads;
+    blocks = g.scans + blocks * g.parts;
   }
   return launch_dependent(bf16 ? paged_join_kernel<true> : paged_join_kernel<false>,
                           dim3(static_cast<unsigned>(blocks + wide.slices * kWideJoin + 1)), dim3(kJoinThreads), 0, st, p, cut, parts, wide, g);

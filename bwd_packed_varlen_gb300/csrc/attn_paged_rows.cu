@@ -25,6 +25,11 @@
 // Slices cut sequences anywhere. A warp that has a whole segment (sequence, row tile, head)
 // writes its rows; the others leave maximum, sum and unnormalised output in fp32, which a second
 // kernel joins in the order of the keys, and which also writes zeros to rows that hold no token.
+//
+// Measured, bf16, hq 32, hkv 8, d 128, one query a sequence. 16 bits: 64 sequences of 200-4000 keys
+// 102 us a call (94 of them here, at 6.04 TB/s; the copy rate is 6.7), 32 with a window of 4096
+// 92 us: bounded by HBM. 4 bits: 128 sequences of 1000-16000 keys 328 us for 210 us of bytes:
+// bounded by instructions, 450 a 16-key block, most of them unpacking (the ALU pipe is 60 % busy).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -44,12 +49,15 @@ struct RowsShape {
   static constexpr int kRows = 8 * kNT;
   static constexpr int kBlocks = k4 || kD == 64 ? 2 : 1;  // 16-key blocks of a unit
   static constexpr int kUnit = 16 * kBlocks;
-  static constexpr int kWarps = k4 ? (kD == 256 ? 6 : kD == 64 && kNT == 1 ? 16 : 12) : (kD == 256 ? 4 : 8);
+  // As many warps as registers (168 a thread of 12 warps) and rings leave: at d 128 in 4 bits 8, 10,
+  // 14 and 16 were slower; at d 64 16 warps of two stages faster than 12 of three.
+  static constexpr int kWarps = k4 ? (kD == 256 ? 6 : kD == 64 ? 16 : 12) : (kD == 256 ? 4 : 8);
   // (a 4-bit ring is laid out for kD elements a row, whatever d is)
   static constexpr int kDataBytes = kUnit * (k4 ? kD / 2 : 2 * kD);  // keys or values of a unit
   static constexpr int kMetaBytes = k4 ? kUnit * kD / 8 : 0;
   static constexpr int kStageBytes = 2 * (kDataBytes + kMetaBytes);
-  static constexpr int kStages = k4 && kD == 64 && kNT == 1 ? 2 : 3;
+  static constexpr int kStages = k4 && kD == 64 ? 2 : 3;
+  static constexpr int kLeast = kLeastKeys / kUnit;
   static constexpr int kSmem = kWarps * kStages * kStageBytes + 1024;
   static_assert(kSmem <= 208 * 1024, "shared memory budget");
 };
@@ -134,7 +142,7 @@ __global__ void __launch_bounds__(RowsShape<kD, kNT, k4>::kWarps * 32, 1)
   const long long total = sum_units(p, cut, pref, status);
   if (blockIdx.x == 0)
     for (int b = tid; b <= p.batch; b += blockDim.x) parts.pref[b] = pref[b];
-  const long long per = slice_units(total, warps, kLeastUnits);
+  const long long per = slice_units(total, warps, S::kLeast);
   const long long begin = mine * per, end = begin + per < total ? begin + per : total;
   if (begin >= end) return;
 
@@ -587,15 +595,19 @@ static cudaError_t launch_rows_impl(const PagedParams& p, const PagedParts& part
   return cudaGetLastError();
 }
 
+template <int kD, bool kBF16, bool k4>
+static cudaError_t launch_rows_nt(const PagedParams& p, const PagedParts& parts, int rows, PagedCut* cut, cudaStream_t st) {
+  if constexpr (!k4 && kD <= 128) {
+    if (rows == 16) return launch_rows_impl<kD, 2, kBF16, k4>(p, parts, cut, st);
+  }
+  return launch_rows_impl<kD, 1, kBF16, k4>(p, parts, cut, st);
+}
+
 template <bool kBF16, bool k4>
 static cudaError_t launch_rows_d(const PagedParams& p, const PagedParts& parts, int rows, PagedCut* cut, cudaStream_t st) {
-  if (p.d <= 64)
-    return rows == 8 ? launch_rows_impl<64, 1, kBF16, k4>(p, parts, cut, st)
-                     : launch_rows_impl<64, 2, kBF16, k4>(p, parts, cut, st);
-  if (p.d <= 128)
-    return rows == 8 ? launch_rows_impl<128, 1, kBF16, k4>(p, parts, cut, st)
-                     : launch_rows_impl<128, 2, kBF16, k4>(p, parts, cut, st);
-  return launch_rows_impl<256, 1, kBF16, k4>(p, parts, cut, st);
+  return p.d <= 64    ? launch_rows_nt<64, kBF16, k4>(p, parts, rows, cut, st)
+         : p.d <= 128 ? launch_rows_nt<128, kBF16, k4>(p, parts, rows, cut, st)
+                      : launch_rows_nt<256, kBF16, k4>(p, parts, rows, cut, st);
 }
 
 cudaError_t launch_paged_rows(const PagedParams& p, const PagedParts& parts, bool bf16, bool four, int rows,
@@ -605,8 +617,12 @@ cudaError_t launch_paged_rows(const PagedParams& p, const PagedParts& parts, boo
   return bf16 ? launch_rows_d<true, false>(p, parts, rows, cut, st) : launch_rows_d<false, false>(p, parts, rows, cut, st);
 }
 
-int paged_rows(int batch, int total_q, int group, int d) {
-  if (d > 128) return 8;  // (16 rows' output and queries would not fit the registers)
+int paged_rows(int batch, int total_q, int group, int d, bool four) {
+  // In 16 bits a pass of 16 rows takes hardly longer than one of 8: 64 sequences of 2000 keys with 12 rows
+  // 113 us in one pass, 187 in two; with 8 rows 104 and 105. In 4 bits it takes twice as long, for the products and
+  // scores of a second n-tile: with 12 rows 115 us in one pass and 106 in two, so eight are taken always.
+  // (Above head_dim 128 16 rows' output and queries would not fit the registers.)
+  if (four || d > 128) return 8;
   const long long each = (static_cast<long long>(total_q) + batch - 1) / batch * group;
   return each <= 8 ? 8 : 16;
 }
@@ -614,9 +630,8 @@ int paged_rows(int batch, int total_q, int group, int d) {
 int paged_warps(int d, bool four, int rows) {
   auto pick = [&](auto shape_d) {
     constexpr int kD = decltype(shape_d)::value;
-    constexpr int kTwo = kD <= 128 ? 2 : 1;
-    if (rows == 8) return four ? RowsShape<kD, 1, true>::kWarps : RowsShape<kD, 1, false>::kWarps;
-    return four ? RowsShape<kD, kTwo, true>::kWarps : RowsShape<kD, kTwo, false>::kWarps;
+    if (four) return RowsShape<kD, 1, true>::kWarps;
+    return rows == 16 ? RowsShape<kD, kD <= 128 ? 2 : 1, false>::kWarps : RowsShape<kD, 1, false>::kWarps;
   };
   const int warps = d <= 64 ? pick(std::integral_constant<int, 64>{})
                     : d <= 128 ? pick(std::integral_constant<int, 128>{}) : pick(std::integral_constant<int, 256>{});

@@ -15,7 +15,12 @@
 // TMEM: O_A, O_B, S_A, S_B of 128 columns. The issue order is S_A0, S_B0 | PV_A0, S_A1 | PV_B0,
 // S_B1 | ...: while one tile's scores become P, the tensor cores work on the other tile.
 // The softmax is attn_fwd_pair.cu's: offset raised only past 2^8, P over S as 16 bits, sums and
-// outputs in fp32. Bounded by the tensor cores and the exponentials.
+// outputs in fp32. Bounded by the chain S, softmax, P V of either tile, 1.7-2.0 us a key tile of
+// both at d 128: the tensor cores are 50 % busy, the exponentials' pipe 26 %.
+//
+// Measured, bf16, hq 32, hkv 8, d 128: four pieces of 100-512 queries behind 2000-12000 keys 208
+// us a call (0.93 PFLOP/s); 16384 queries 2380 us, with a window of 1024 635 us. A segment costs 6
+// to 8 us beside its key tiles (first scores, their maximum, the rows' end).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -573,12 +578,19 @@ cudaError_t launch_paged_tiles(const PagedParams& p, const PagedParts& parts, in
   return bf16 ? launch_tiles_d<true, false>(p, parts, first_status, st) : launch_tiles_d<false, false>(p, parts, first_status, st);
 }
 
-int paged_wide_rows(int batch, int total_q, int group, int d) {
-  // Launched where sequences must have many rows on average, or some sequence may have many enough
-  // to outweigh a launch for nothing (4 us). Above head_dim 128 the kernel of few rows takes all.
+int paged_wide_rows(int batch, int total_q, int hq, int hkv, int d, bool four) {
+  // Above head_dim 128 the kernel of few rows takes all.
   if (d > 128) return 0;
+  // Rows a kv head from which a sequence is faster here. With a segment for every SM, at d 128, 64
+  // sequences of 2000 keys: 20 rows 160 us here, 202 there, which reads keys once for every 16 rows; in 4
+  // bits 20 rows 197 and 189, 48 rows 199 and 317; at d 64 20 rows 138 and 120, 32 rows 138 and 137. With
+  // fewer segments blocks wait for one another's key tiles: 8 sequences, 32 rows 50 and 32 us.
+  const int least = static_cast<long long>(batch) * hkv < kPagedSMs ? 64 : four || d <= 64 ? 32 : 16;
+  // Launched where sequences must have many rows on average, or some sequence may have many enough
+  // to outweigh a launch for nothing (4 us).
+  const int group = hq / hkv;
   const long long rows = static_cast<long long>(total_q) * group, over = rows - static_cast<long long>(batch) * group;
-  return rows > 32ll * batch || over >= 512 ? 64 : 0;
+  return rows > static_cast<long long>(least) * batch || over >= 512 ? least : 0;
 }
 
 }  // namespace teattn

@@ -4,7 +4,8 @@
 // One pass: queries and keys are turned as in rope.cu (the angle of a token as a 64-bit
 // fraction of a turn, pairs in fp32, one rounding), queries go to their output, keys and values
 // to the place of their position. Memory-bound: each element is read once and written once,
-// 16 bytes per access where sizes and alignment allow it.
+// 16 bytes per access where sizes and alignment allow it. Prompts of 1500-8000 tokens, 32 + 2 * 8
+// heads of 128: 105 us, 90 % of the measured copy rate; 48 single tokens: 4.3 us, a launch.
 //
 // Into 4 bits a block's turned keys go to shared memory first, rounded to 16 bits as a 16-bit
 // cache would hold them (pairs that are turned together lie in different groups of 32); then
@@ -12,7 +13,9 @@
 // and write 16 bytes of codes and 4 of step and least value. The step is rounded towards zero,
 // so that no code stands for more than the greatest element, which may be the type's last.
 // Both quotients are true divisions: a product with a reciprocal would put elements on a border
-// between two codes, which 16-bit numbers often are, on either side.
+// between two codes, which 16-bit numbers often are, on either side. 12 prompts of 30-900 tokens,
+// 16 + 2 * 8 heads of 64, into 4 bits and gathered again: 29 us for 8.1 us of bytes; 6000 rows
+// are too few to hide a chain of lengths, table, loads, angles and two exchanges.
 #include <cuda_runtime.h>
 
 #include <climits>

@@ -23,8 +23,8 @@ bool paged_layout(int batch, int total_q, int hq, int hkv, int d, bool four, Pag
   if (batch < 1 || batch > kPagedMaxBatch || total_q < 0 || hq < 1 || hkv < 1 || hq % hkv != 0 || d < 8 || d > 256 || d % 8 != 0 ||
       static_cast<long long>(total_q) * hq > INT32_MAX - 256)
     return false;
-  L->rows = paged_rows(batch, total_q, hq / hkv, d);
-  L->wide_rows = paged_wide_rows(batch, total_q, hq / hkv, d);
+  L->rows = paged_rows(batch, total_q, hq / hkv, d, four);
+  L->wide_rows = paged_wide_rows(batch, total_q, hq, hkv, d, four);
   L->slices[0] = paged_warps(d, four, L->rows);
   L->slices[1] = L->wide_rows > 0 ? kPagedSMs : 0;
   size_t off = kHdrWords * sizeof(int);
@@ -115,11 +115,12 @@ int te_attn_paged_fwd_thd(const te_attn_paged_cache* cache, const void* q, void*
   PagedParts parts[2];
   for (int k = 0; k < 2; ++k)
     parts[k] = PagedParts{reinterpret_cast<long long*>(ws + L.pref[k]), reinterpret_cast<float2*>(ws + L.ml[k]),
-                          reinterpret_cast<float*>(ws + L.o[k]), L.slices[k] / kPagedSMs * use, k ? kLeastWideUnits : kLeastUnits};
+                          reinterpret_cast<float*>(ws + L.o[k]), L.slices[k] / kPagedSMs * use, kLeastWideUnits};
   const bool bf16 = cache->dtype == TE_DTYPE_BF16;
   PagedCut cut{};
   cudaError_t e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_paged_rows(p, parts[0], bf16, four, L.rows, &cut, st); });
   if (e != cudaSuccess) return api_cuda_fail(e, "paged attention");
+  parts[0].least = kLeastKeys / cut.unit;
   if (L.wide_rows > 0) {
     e = api_timed(TE_KERNEL_FWD, st, [&] { return launch_paged_tiles(p, parts[1], parts[0].slices, bf16, four, st); });
     if (e != cudaSuccess) return api_cuda_fail(e, "paged attention of long pieces");

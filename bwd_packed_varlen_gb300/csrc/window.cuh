@@ -5,6 +5,11 @@
 // its first row's window on, and a key tile's queries end a window behind its last key unless
 // it holds a sink: tiles between are not visited, and the work is that of the window, not of
 // the sequence.
+//
+// Measured, bf16, hq 32, hkv 8, d 128, four sequences of 1500-6000 tokens, window 1024, 4 sinks:
+// forward 465 us, delta 59, dQ 319, dK/dV 458, lists 29, zero fill 13 (events around each); forward and backward
+// in a call 1288 us, 5 products for each visible pair in 429 us at the measured bf16 rate. Bounded as
+// the kernels without a window are, and by an item's begin and end, 6 to 8 us beside ten tiles of 2.
 #pragma once
 
 #include <type_traits>
@@ -31,8 +36,11 @@ struct WindowParams : AttnParams {
 };
 
 constexpr int kSplitSinkTiles = 2;
-// As long as an ordinary sweep, but so long that few sequences have more than one part.
-__host__ __device__ constexpr int sweep_tiles_of(int window) { return (window + kBlockM - 1) / kBlockM + 1 > 16 ? (window + kBlockM - 1) / kBlockM + 1 : 16; }
+// As long as an ordinary sweep, but so long that few sequences have more than one part. (dK/dV of the
+// four sequences above: 694 us with whole sweeps, 452 with cut ones@SWEEP@.)
+__host__ __device__ constexpr int sweep_tiles_of(int window) {
+  return (window + kBlockM - 1) / kBlockM + 1 > 16 ? (window + kBlockM - 1) / kBlockM + 1 : 16;
+}
 
 template <class P>
 constexpr bool is_window = std::is_base_of_v<WindowParams, P>;

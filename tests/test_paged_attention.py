@@ -513,3 +513,12 @@ def test_captured_calls_that_share_a_workspace():
             graphs[i].replay()
             torch.cuda.synchronize()
             assert _same(want[i], outs[i]) and ta.read_status(ws) == 0
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+def test_prompts_among_many_sequences(bits):
+    """So many sequences that one block of the join takes all heads of one; drafts, whose queries several share; rows
+    between them that are no token."""
+    Case(74, [1] * 1300 + [70], [7 * i % 90 for i in range(1300)] + [20], 16, 32, 2, 32, BF, bits).check()
+    Case(75, [4, 3, 0, 64, 2], [3000, 700, 9, 40, 1200], 32, 8, 8, 64, FP, bits, tail=40).check()
