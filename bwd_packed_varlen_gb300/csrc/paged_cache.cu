@@ -5,7 +5,8 @@
 // fraction of a turn, pairs in fp32, one rounding), queries go to their output, keys and values
 // to the place of their position. Memory-bound: each element is read once and written once,
 // 16 bytes per access where sizes and alignment allow it. Prompts of 1500-8000 tokens, 32 + 2 * 8
-// heads of 128: 105 us, 90 % of the measured copy rate; 48 single tokens: 4.3 us, a launch.
+// heads of 128: 99 us, 95 % of the measured copy rate (eight blocks an SM, so 32 registers a thread:
+// left to the compiler, with four tokens a block, 122 instead of 105); 48 single tokens: 4.2 us, a launch.
 //
 // Into 4 bits a block's turned keys go to shared memory first, rounded to 16 bits as a 16-bit
 // cache would hold them (pairs that are turned together lie in different groups of 32); then
@@ -14,8 +15,8 @@
 // so that no code stands for more than the greatest element, which may be the type's last.
 // Both quotients are true divisions: a product with a reciprocal would put elements on a border
 // between two codes, which 16-bit numbers often are, on either side. 12 prompts of 30-900 tokens,
-// 16 + 2 * 8 heads of 64, into 4 bits and gathered again: 29 us for 8.1 us of bytes; 6000 rows
-// are too few to hide a chain of lengths, table, loads, angles and two exchanges.
+// 16 + 2 * 8 heads of 64, into 4 bits and gathered again: 29 us for 8.1 us of bytes; bounded
+// by instructions, some 45 an element of keys and values, in two issue slots of three.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -47,7 +48,7 @@ struct AppendParams {
   uint32_t units_inv[3], words_inv;
 };
 
-constexpr int kAppendThreads = 256, kAppendTokens = 4;
+constexpr int kAppendThreads = 256, kAppendTokens = 2;
 constexpr int kAppendSMs = 152;  // of the GPU that work is cut for
 
 struct Token {
@@ -289,8 +290,8 @@ static cudaError_t launch_append_v(AppendParams p, bool bf16, cudaStream_t st) {
   p.units[0] = kHalf ? p.rot / 2 / V : p.rot / (V == 1 ? 2 : V);
   p.units[1] = (p.d - p.rot) / V;
   p.units[2] = p.d / V;
-  // Tokens and heads of a block as in rope.cu: up to four tokens share the frequencies; with
-  // few tokens a block takes a part of a token's heads.
+  // Tokens and heads of a block much as in rope.cu: two tokens share the frequencies (four: 105 instead of
+  // 99 us for the prompts above); with few tokens a block takes a part of a token's heads.
   const int heads = p.heads[0] + p.heads[1] + p.heads[2], all = heads * (p.units[0] + p.units[1]);
   const int share = 5 * kAppendThreads / all;
   p.tokens = p.total < 16 * kAppendSMs || share < 1 ? 1 : share < kAppendTokens ? share : kAppendTokens;

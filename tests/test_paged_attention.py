@@ -522,3 +522,12 @@ def test_prompts_among_many_sequences(bits):
     between them that are no token."""
     Case(74, [1] * 1300 + [70], [7 * i % 90 for i in range(1300)] + [20], 16, 32, 2, 32, BF, bits).check()
     Case(75, [4, 3, 0, 64, 2], [3000, 700, 9, 40, 1200], 32, 8, 8, 64, FP, bits, tail=40).check()
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("d", [64, 128])
+def test_drafts_of_many_sequences(d, bits):
+    """With segments for every SM, sequences of 16, or 32, rows go to the tensor cores and those of fewer do not."""
+    Case(76, [5, 3, 9, 20, 0, 4, 8] * 24, [13 * i % 400 for i in range(168)], 32, 4, 1, d, FP, bits, slot=1).check()
+    Case(77, [5, 3, 9, 20, 0, 4, 8] * 24, [13 * i % 400 for i in range(168)], 16, 4, 1, d, BF, bits, 60, 2, slot=1).check()
