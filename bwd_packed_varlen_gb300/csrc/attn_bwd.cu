@@ -1087,20 +1087,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // Sums of cut sweeps
 // ===========================================================================
 // dK and dV of a sink tile: the parts of its sweep added in order, in fp32, rounded once. A block
-// takes a quarter of a tile's rows of one kv head; four columns a thread.
+// takes a quarter of a tile's rows of one kv head; four columns a thread. 10 us cold for the four
+// sequences of window.cuh (4 MB): a launch and two dependent reads.
 template <bool kBF16>
 __global__ void __launch_bounds__(256) window_sum_kernel(const __grid_constant__ WindowParams p) {
   pdl_wait();
-  if (static_cast<int>(blockIdx.x) >= p.header[kHdrSinkSlots]) return;
-  const int4 e = p.slots[blockIdx.x];
+  const int slot = blockIdx.x / p.hkv, g = blockIdx.x - slot * p.hkv;
+  if (slot >= p.header[kHdrSinkSlots]) return;
+  const int4 e = p.slots[slot];
   if (e.z >= 0) return;  // the entry of the sweep's begin stands for the tile
   const SeqInfo s = load_seq(p, e.x);
-  const int g = blockIdx.y, cols = p.d / 4;
+  const int cols = p.d / 4;
   const int rows = min(kBlockN, seen_keys(s, true) - e.y * kBlockN);
   const size_t step = static_cast<size_t>(p.hkv) * kBlockN * p.d;
-  for (int n = blockIdx.z * 256 + threadIdx.x; n < rows * cols; n += 256 * gridDim.z) {
+  for (int n = blockIdx.y * 256 + threadIdx.x; n < rows * cols; n += 256 * gridDim.y) {
     const int r = n / cols, c = (n - r * cols) * 4;
-    const size_t at = (static_cast<size_t>(blockIdx.x) * p.hkv + g) * kBlockN * p.d + static_cast<size_t>(r) * p.d + c;
+    const size_t at = (static_cast<size_t>(slot) * p.hkv + g) * kBlockN * p.d + static_cast<size_t>(r) * p.d + c;
     float k[4] = {}, v[4] = {};
     // (keys that are no sinks have nothing from the later parts)
     const int parts = e.y * kBlockN + r < p.sinks ? e.w + 1 : 1;
@@ -1124,7 +1126,7 @@ __global__ void __launch_bounds__(256) window_sum_kernel(const __grid_constant__
 }
 
 cudaError_t launch_window_sum(const WindowParams& p, bool bf16, cudaStream_t st) {
-  const dim3 grid(p.cap_slots, p.hkv, 4);
+  const dim3 grid(p.cap_slots * p.hkv, 4);
   return launch_dependent(bf16 ? window_sum_kernel<true> : window_sum_kernel<false>, grid, dim3(256), 0, st, p);
 }
 
