@@ -587,8 +587,8 @@ int paged_wide_rows(int batch, int total_q, int hq, int hkv, int d, bool four) {
   // fewer segments blocks wait for one another's key tiles: 8 sequences, 32 rows 50 and 32 us.
   const int least = static_cast<long long>(batch) * hkv < kPagedSMs ? 64 : four || d <= 64 ? 32 : 16;
   // Launched where sequences must have many rows on average, or some sequence may have many enough
-  // to outweigh a launch for nothing (4 us): 512 rows of one sequence take 37 us here and 36 there behind
-  // 500 keys, 50 and 50 behind 2000, 94 and 210 behind 20000 (in 4 bits 97 and 379).
+  // to outweigh a launch for nothing (4 us): 512 rows of one sequence take 34 us here and 36 there behind
+  // 500 keys, 43 and 50 behind 2000, 86 and 210 behind 20000 (in 4 bits 88 and 379).
   const int group = hq / hkv;
   const long long rows = static_cast<long long>(total_q) * group, over = rows - static_cast<long long>(batch) * group;
   return rows > static_cast<long long>(least) * batch || over >= 512 ? least : 0;
