@@ -60,8 +60,8 @@ __device__ __forceinline__ void join_pieces(const PagedParams& p, const PagedPar
   }
 }
 
-// The segment that slice `w` goes on with, if it is the first slice to do so: a thread a row, a
-// quarter of the columns a block (its pieces lie column by column).
+// The segment that slice `w` goes on with, if it is the first slice to do so: a thread a row, an
+// eighth of the columns a block (its pieces lie column by column).
 template <bool kBF16>
 __device__ void join_wide(const PagedParams& p, const PagedParts& parts, int w, int part) {
   const long long total = parts.pref[p.batch], per = slice_units(total, parts.slices, parts.least), at = w * per;

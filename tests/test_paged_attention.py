@@ -531,3 +531,24 @@ def test_drafts_of_many_sequences(d, bits):
     """With segments for every SM, sequences of 16, or 32, rows go to the tensor cores and those of fewer do not."""
     Case(76, [5, 3, 9, 20, 0, 4, 8] * 24, [13 * i % 400 for i in range(168)], 32, 4, 1, d, FP, bits, slot=1).check()
     Case(77, [5, 3, 9, 20, 0, 4, 8] * 24, [13 * i % 400 for i in range(168)], 16, 4, 1, d, BF, bits, 60, 2, slot=1).check()
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+def test_lengths_that_do_not_fit_among_prompts(bits):
+    """The same where the kernel of many rows is launched: rows of such a sequence are zeros, the others' are theirs."""
+    c = Case(78, [300, 2, 150], [60, 20, 5], 16, 4, 2, 64, BF, bits, slot=4, tail=3).dev()
+    whole = c.fwd()
+    for value in ([-1, 20, 5], [60, 20000, 5], [60, 20, 2 ** 31 - 1]):
+        kept = c.on[4].clone()
+        c.on[4].copy_(torch.tensor(value, dtype=torch.int32))
+        ws = c.workspace()
+        out, lse = c.fwd(workspace=ws)
+        assert ta.read_status(ws) == 1
+        for b in range(3):
+            rows = slice(c.off[b], c.off[b + 1])
+            good = value[b] == c.past[b]
+            assert torch.equal(out[rows], whole[0][rows] if good else torch.zeros_like(out[rows])), (value, b)
+            assert torch.equal(lse[rows], whole[1][rows] if good else torch.zeros_like(lse[rows])), (value, b)
+        assert not out[c.off[3]:].any() and not lse[c.off[3]:].any()
+        c.on[4].copy_(kept)
