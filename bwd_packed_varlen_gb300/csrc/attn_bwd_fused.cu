@@ -618,6 +618,7 @@ __global__ void __launch_bounds__(256) dq_convert_kernel(AttnParams p) {
   const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const bool causal = p.causal != 0;
+  if (p.header[kHdrOver]) return;  // (no tile was computed, and the places of tiles lie past the accumulator)
   // tile: two halves of 128 rows x dq_cols/2 fp32 columns (dq_cols = 64 or 128)
   const int half_units = p.dq_cols / 8;  // 16-byte units per row of a half
   const size_t half_bytes = static_cast<size_t>(kBlockM) * half_units * 16;

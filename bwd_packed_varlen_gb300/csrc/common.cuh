@@ -30,6 +30,7 @@ enum HeaderWord : int {
   kHdrPrefixSlot = 14,    // row, rows
   kHdrPrefixRows = 15,
   kHdrSinkSlots = 16,  // windowed backward: partial results of sink tiles
+  kHdrOver = 17,       // 1: overlapping sequences have more tiles than the workspace holds; nothing is computed
   kHdrWords = 64     // header size in int32 words (256 bytes, keeps alignment)
 };
 

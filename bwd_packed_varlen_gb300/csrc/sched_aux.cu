@@ -7,6 +7,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "common.cuh"
@@ -32,6 +33,9 @@ namespace teattn {
 // first, ties by natural order, so a persistent grid takes the long items first.
 // Up to kSortCap pairs are sorted in shared memory; a longer list keeps its
 // natural order. The result depends only on the cu_seqlens values.
+// Lists and per-tile buffers hold the tiles of sequences that lie side by side. Padded offsets
+// that fall back put sequences on the same rows, which can then have more tiles than that: all
+// lists are left empty, kHdrOver says so, and every row of the outputs becomes zero.
 // For the fused backward the key-tile list is built in chain order instead
 // (kListKChain): sequences with more key tiles first (ties: lower index), and
 // inside a sequence its key tiles in DESCENDING order -- the order in which that
@@ -271,7 +275,11 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(P p, int* pref_
   if constexpr (is_window<P>) pdl_trigger();
   __shared__ int warp_sums[32];
   __shared__ int bad;
-  if (threadIdx.x == 0) bad = 0;
+  __shared__ unsigned long long tiles;  // of all lists: the int sums below wrap only if this passes 2^31
+  if (threadIdx.x == 0) {
+    bad = 0;
+    tiles = 0;
+  }
   __syncthreads();
   int carry_q = 0, carry_k = 0, carry_f = 0;
   for (int base = 0; base < p.batch; base += blockDim.x) {
@@ -286,6 +294,10 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(P p, int* pref_
         cf = (s.len_q + kBlockF - 1) / kBlockF;
       }
     }
+    // (a thread's three counts are below 2^26 together)
+    const unsigned low = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(cq + ck + cf) & 0xffffu);
+    const unsigned high = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(cq + ck + cf) >> 16);
+    if ((threadIdx.x & 31) == 0 && (low | high)) atomicAdd(&tiles, (static_cast<unsigned long long>(high) << 16) + low);
     int tq, tk, tf;
     int eq = block_excl_scan(cq, warp_sums, &tq);
     int ek = block_excl_scan(ck, warp_sums, &tk);
@@ -304,8 +316,11 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(P p, int* pref_
     pref_k[p.batch] = carry_k;
     pref_f[p.batch] = carry_f;
   }
+  // (the scans' barriers order the sum before this)
+  const bool over = tiles > static_cast<unsigned long long>(INT_MAX) || carry_q > p.pair_cap_q || carry_k > p.pair_cap_k ||
+                    carry_f > p.pair_cap_f;
   if constexpr (is_window<P>) {
-    if (p.sweep_tiles > 0) {
+    if (p.sweep_tiles > 0 && !over) {
       int carry = 0;
       for (int base = 0; base < p.batch; base += blockDim.x) {
         const int b = base + threadIdx.x;
@@ -334,9 +349,7 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(P p, int* pref_
   }
   __threadfence_block();
   __syncthreads();
-  const int nq = min(carry_q, p.pair_cap_q);
-  const int nk = min(carry_k, p.pair_cap_k);
-  const int nf = min(carry_f, p.pair_cap_f);
+  const int nq = over ? 0 : carry_q, nk = over ? 0 : carry_k, nf = over ? 0 : carry_f;
   const bool both = (p.sched_lists & kListQ) && (p.sched_lists & kListK) && nq <= kSortCap &&
                     nk <= kSortCap;
   if (both) {
@@ -364,10 +377,8 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(P p, int* pref_
   }
   if (p.sched_lists & kListF) build_list<2>(p, pref_f, nf, p.f_pairs, sort_keys);
   if (threadIdx.x == 0) {
-    int status = bad ? kStatusBadSeqlens : 0;
-    if (carry_q > p.pair_cap_q || carry_k > p.pair_cap_k || carry_f > p.pair_cap_f)
-      status |= kStatusBadSeqlens;
-    p.header[kHdrStatus] = status;
+    p.header[kHdrStatus] = bad || over ? kStatusBadSeqlens : 0;
+    p.header[kHdrOver] = over ? 1 : 0;
     p.header[kHdrNumQPairs] = nq;
     p.header[kHdrNumKPairs] = nk;
     p.header[kHdrNumFPairs] = nf;
@@ -403,7 +414,9 @@ cudaError_t launch_window_schedule(const WindowParams& p, int* pref_q, int* pref
 // rows, those no real query sees and the pad rows. Block (b, y) clears a share of
 // sequence b's rows, one warp per row with 16-byte stores; block b = batch clears
 // the packed rows outside every sequence. Rows are kept inside the tensors even
-// when the lengths are inconsistent (the scheduler reports those).
+// when the lengths are inconsistent (the scheduler reports those). Where the scheduler left
+// its lists empty (kHdrOver) the forward's fill clears every row, and delta_kernel the backward's:
+// it is behind the scheduler, which a windowed backward's fill is not.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void zero_row(void* base, long long r, int row_bytes) {
   uint4* dst = reinterpret_cast<uint4*>(static_cast<char*>(base) +
@@ -439,6 +452,10 @@ __global__ void __launch_bounds__(256) zero_fill_kernel(P p, int mode) {
     zero_row(p.dk, r, kbytes);
     zero_row(p.dv, r, kbytes);
   };
+  if (mode == 0 && p.header[kHdrOver]) {
+    for (long long r = static_cast<long long>(b) * wstep + w0; r < p.total_q; r += static_cast<long long>(gridDim.x) * wstep) clear_q(r, 0.0f);
+    return;
+  }
   if (b < p.batch) {
     const SeqInfo s = load_seq(p, b);
     // rows of sequence b: base + i * stride for i in [0, n)
@@ -532,6 +549,14 @@ __global__ void __launch_bounds__(256) delta_kernel(P p) {
   const int lane = threadIdx.x & 31;
   const int cpr = p.d / 8;  // 16-byte chunks per head
   const int chunks = p.hq * cpr;
+  if (p.header[kHdrOver]) {
+    for (long long r = gw; r < p.total_q; r += warps) zero_row(p.dq, r, p.hq * p.d * 2);
+    for (long long r = gw; r < p.total_kv; r += warps) {
+      zero_row(p.dk, r, p.hkv * p.d * 2);
+      zero_row(p.dv, r, p.hkv * p.d * 2);
+    }
+    return;
+  }
   constexpr float kLog2e = 1.4426950408889634f;
   for (int r = gw; r < p.total_q; r += warps) {
     int i = 0;

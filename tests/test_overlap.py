@@ -1,0 +1,117 @@
+"""Padded offsets that fall back put sequences on the same rows. They can then have more tiles than
+a workspace of the call's sizes has room for: such a call computes nothing, says so in its status
+and leaves zeros, and no byte outside its workspace is touched."""
+
+import numpy as np
+import pytest
+import torch
+
+import bwd_packed_varlen_gb300 as ta
+from prefix_common import prefix_sums
+
+gpu = pytest.mark.gpu
+BEHIND = 4096  # bytes behind a workspace that a call may not touch
+
+
+def room_for_tiles(batch, rows, kv_rows, hkv=1, d=64):
+    """Query tiles that a backward's workspace holds: two fp32 rows of 128 for each, per head."""
+    one, two = (ta.bwd_workspace_size(batch, rows, kv_rows, hq, hkv, d) for hq in (1, 2))
+    return (two - one) // (2 * 128 * 4)
+
+
+def falling(batch, rows):
+    """Offsets 0, rows, 0, rows, ...: every other sequence has all rows, those between have none left."""
+    return torch.tensor([rows * (i % 2) for i in range(batch + 1)], dtype=torch.int32)
+
+
+class Overlap:
+    def __init__(self, batch=19, rows=1300, kv_rows=260, hq=4, hkv=2, d=64, dtype=torch.bfloat16):
+        gen = torch.Generator().manual_seed(51)
+        self.sizes = (batch, rows, kv_rows, hq, hkv, d)
+        self.q, self.dout, self.out = (torch.randn(rows, hq, d, generator=gen).to(dtype).cuda() for _ in range(3))
+        self.k, self.v = (torch.randn(kv_rows, hkv, d, generator=gen).to(dtype).cuda() for _ in range(2))
+        self.lse = torch.randn(rows, hq, generator=gen).cuda()
+        lens = [[n * ((i + 1) % 2) for i in range(batch)] for n in (rows, kv_rows)]
+        self.cu = [prefix_sums(n).cuda() for n in lens] + [falling(batch, n).cuda() for n in (rows, kv_rows)]
+        self.sound = [prefix_sums(x).cuda() for x in ([rows] + [0] * (batch - 1), [kv_rows] + [0] * (batch - 1))] * 2
+
+    def nans(self):
+        return [torch.full_like(x, float("nan")) for x in (self.q, self.k, self.v)]
+
+    def run(self, call, need):
+        """call(workspace): its outputs are zeros and its status is 1; then what lies behind."""
+        held = torch.full((need + BEHIND,), 0xA5, dtype=torch.uint8, device="cuda")
+        outputs = call(held[:need])
+        assert ta.read_status(held[:need]) == 1
+        assert not any(x.count_nonzero() for x in outputs)
+        assert (held[need:] == 0xA5).all()
+
+
+# ------------------------------------------------------------------ on the CPU
+def test_tiles_of_sequences_side_by_side_fit():
+    rng = np.random.default_rng(52)
+    for _ in range(200):
+        batch = int(rng.integers(1, 40))
+        lens = [int(x) for x in 2 ** rng.uniform(0, 12, batch)]
+        rows = sum(lens)
+        assert sum((n + 127) // 128 for n in lens) <= room_for_tiles(batch, rows, rows)
+
+
+def test_tiles_of_overlapping_sequences_need_not():
+    """The offsets of the calls below."""
+    assert falling(5, 9).tolist() == [0, 9, 0, 9, 0, 9]
+    batch, rows = 19, 1300
+    assert 10 * ((rows + 127) // 128) > room_for_tiles(batch, rows, 260)
+
+
+# ------------------------------------------------------------------ on the GPU
+@gpu
+@pytest.mark.parametrize("mask", ["padding", "padding_causal", "padding_causal_bottom_right"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_packed_calls(d, mask):
+    c = Overlap(d=d)
+
+    def fwd(ws):
+        out, lse = (torch.full_like(x, float("nan")) for x in (c.q, c.lse))
+        return ta.fwd(c.q, c.k, c.v, *c.cu, 0.1, mask, out=out, lse=lse, workspace=ws)
+
+    def bwd(ws, **kw):
+        dq, dk, dv = c.nans()
+        return ta.bwd(c.q, c.k, c.v, c.out, c.dout, c.lse, *c.cu, 0.1, mask, dq=dq, dk=dk, dv=dv, workspace=ws, **kw)
+    c.run(fwd, ta.fwd_workspace_size(*c.sizes))
+    c.run(bwd, ta.bwd_workspace_size(*c.sizes))
+    if d <= 128:
+        c.run(lambda ws: bwd(ws, fused=True), ta.bwd_fused_workspace_size(*c.sizes))
+    # and the next call with the same workspace is none the worse
+    ws = torch.empty(ta.bwd_workspace_size(*c.sizes), dtype=torch.uint8, device="cuda")
+    bwd(ws)
+    out, lse = ta.fwd(c.q, c.k, c.v, *c.sound, 0.1, mask)
+    args = (c.q, c.k, c.v, out, c.dout, lse, *c.sound, 0.1, mask)
+    again, want = ta.bwd(*args, workspace=ws), ta.bwd(*args)
+    assert ta.read_status(ws) == 0 and all(torch.equal(a, b) for a, b in zip(again, want))
+
+
+@gpu
+def test_built_in_scratch():
+    c = Overlap()
+    dq, dk, dv = c.nans()
+    got = ta.bwd_noalloc(c.q, c.k, c.v, c.out, c.dout, c.lse, *c.cu, 0.1, "padding", dq=dq, dk=dk, dv=dv)
+    assert ta.read_status_noalloc() == 1 and not any(x.count_nonzero() for x in got)
+
+
+@gpu
+@pytest.mark.parametrize("window,sinks", [(64, 0), (64, 4), (300, 140)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_windowed_calls(d, window, sinks):
+    """Sequences of 4096 queries over 128 keys: sweeps over sinks are cut, and have no room either."""
+    c = Overlap(batch=21, rows=4096, kv_rows=128, d=d)
+
+    def fwd(ws):
+        out, lse = (torch.full_like(x, float("nan")) for x in (c.q, c.lse))
+        return ta.window_fwd(c.q, c.k, c.v, *c.cu, 0.1, window, sinks, out=out, lse=lse, workspace=ws)
+
+    def bwd(ws):
+        dq, dk, dv = c.nans()
+        return ta.window_bwd(c.q, c.k, c.v, c.out, c.dout, c.lse, *c.cu, 0.1, window, sinks, dq=dq, dk=dk, dv=dv, workspace=ws)
+    c.run(fwd, ta.fwd_workspace_size(*c.sizes))
+    c.run(bwd, ta.window_bwd_workspace_size(*c.sizes, window, sinks))
