@@ -594,7 +594,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int slot = *const_cast<volatile int*>(&s_slot[ii & 3]);
         if (slot >= 0) {
           const size_t at = ((static_cast<size_t>(slot) * p.hkv + I.g) * kBlockN + quarter * 32 + lane) * p.d + col_out + grp * kOutCols;
-          store_sums<kOutCols>(tmem + lane_base + grp * kOutCols, p.part_dk + at, p.part_dv + at, store ? p.d - col_out - grp * kOutCols : 0);
+          store_sums<kOutCols>(tmem + lane_base + grp * kOutCols, p.part_dk + at, p.part_dv + at,
+                               store && bounds_ok(slot < p.cap_slots, status) ? p.d - col_out - grp * kOutCols : 0);
           tc_fence_before();
           mbar_arrive(&bar_acc_empty);
           continue;

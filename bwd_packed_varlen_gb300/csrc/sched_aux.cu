@@ -34,8 +34,9 @@ namespace teattn {
 // Up to kSortCap pairs are sorted in shared memory; a longer list keeps its
 // natural order. The result depends only on the cu_seqlens values.
 // Lists and per-tile buffers hold the tiles of sequences that lie side by side. Padded offsets
-// that fall back put sequences on the same rows, which can then have more tiles than that: all
-// lists are left empty, kHdrOver says so, and every row of the outputs becomes zero.
+// that fall back put sequences on the same rows, which can then have more tiles than that, or
+// more parts of cut sweeps over sinks: all lists are left empty, kHdrOver says so, and every row
+// of the outputs becomes zero.
 // For the fused backward the key-tile list is built in chain order instead
 // (kListKChain): sequences with more key tiles first (ties: lower index), and
 // inside a sequence its key tiles in DESCENDING order -- the order in which that
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(P p, int* pref_
     pref_f[p.batch] = carry_f;
   }
   // (the scans' barriers order the sum before this)
-  const bool over = tiles > static_cast<unsigned long long>(INT_MAX) || carry_q > p.pair_cap_q || carry_k > p.pair_cap_k ||
+  bool over = tiles > static_cast<unsigned long long>(INT_MAX) || carry_q > p.pair_cap_q || carry_k > p.pair_cap_k ||
                     carry_f > p.pair_cap_f;
   if constexpr (is_window<P>) {
     if (p.sweep_tiles > 0 && !over) {
@@ -342,7 +343,9 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(P p, int* pref_
         }
         carry += total;
       }
-      if (threadIdx.x == 0) p.header[kHdrSinkSlots] = min(carry, p.cap_slots);
+      // (sequences side by side have room for their parts; overlapping ones need not)
+      over = carry > p.cap_slots;
+      if (threadIdx.x == 0) p.header[kHdrSinkSlots] = over ? 0 : carry;
     } else if (threadIdx.x == 0) {
       p.header[kHdrSinkSlots] = 0;
     }

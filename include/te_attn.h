@@ -109,9 +109,10 @@ extern "C" {
  *                           length above its padded one, offsets past the tensor);
  *                           the offending sequences are treated as empty. Padded
  *                           offsets that fall back put sequences on the same rows;
- *                           where those have more 128-row tiles than the workspace
- *                           has room for, nothing is computed and every row of the
- *                           outputs (lse too) becomes zero.
+ *                           where those have more 128-row tiles, or parts of
+ *                           sweeps over sinks, than the workspace has room for,
+ *                           nothing is computed and every row of the outputs (lse
+ *                           too) becomes zero.
  *   TE_STATUS_TIMEOUT       a pipeline wait inside a kernel ran past its limit (4 s);
  *                           every other wait of that kernel then gave up too, the
  *                           kernel freed its tensor memory and returned, and the

@@ -19,20 +19,47 @@ def room_for_tiles(batch, rows, kv_rows, hkv=1, d=64):
     return (two - one) // (2 * 128 * 4)
 
 
-def falling(batch, rows):
-    """Offsets 0, rows, 0, rows, ...: every other sequence has all rows, those between have none left."""
-    return torch.tensor([rows * (i % 2) for i in range(batch + 1)], dtype=torch.int32)
+def falling(batch, rows, times=1 << 30):
+    """Offsets 0, rows, 0, rows, ...: every other sequence has all rows, those between have none left, up
+    to the last of `times` sequences; those behind it are empty."""
+    return torch.tensor([rows * (i % 2 if i < 2 * times else 1) for i in range(batch + 1)], dtype=torch.int32)
+
+
+SWEEP = 16  # query tiles of a part of a cut sweep, for windows below 15 tiles
+
+
+def parts_of(n, m, window, sinks, low):
+    """Partial sums that a windowed backward keeps of a sequence of n queries and m keys: for each of the
+    first two key tiles with a sink whose sweep ends more than a part behind its beginning, that beginning
+    and the parts behind it (low: the lower-right mask)."""
+    diag, total = m - n if low else 0, 0
+    seen = min(m, max(0, n + diag)) if n else 0
+    for kt in range(min(2, (min(sinks, seen) + 127) // 128)):
+        first = max(0, kt * 128 - diag) // 128
+        last = min(n, min(kt * 128 + 128, m) - 1 - diag + window)
+        end = max((max(last, 0) + 127) // 128, first + SWEEP)
+        left = (n + 127) // 128 - end
+        total += (left + SWEEP - 1) // SWEEP + 1 if left > 0 else 0
+    return total
+
+
+def room_for_parts(batch, rows, kv_rows, window, sinks):
+    """Partial sums that the workspace holds: at one head of 8 columns, 8 KB each and their entry."""
+    sizes = (batch, rows, kv_rows, 1, 1, 8, window)
+    extra = ta.window_bwd_workspace_size(*sizes, sinks) - ta.window_bwd_workspace_size(*sizes, 0)
+    return max(0, extra - 4 * (batch + 1) - 3 * 256) // (8192 + 16)
 
 
 class Overlap:
-    def __init__(self, batch=19, rows=1300, kv_rows=260, hq=4, hkv=2, d=64, dtype=torch.bfloat16):
+    def __init__(self, batch=19, rows=1300, kv_rows=260, hq=4, hkv=2, d=64, dtype=torch.bfloat16, times=None):
         gen = torch.Generator().manual_seed(51)
         self.sizes = (batch, rows, kv_rows, hq, hkv, d)
+        times = (batch + 1) // 2 if times is None else times
         self.q, self.dout, self.out = (torch.randn(rows, hq, d, generator=gen).to(dtype).cuda() for _ in range(3))
         self.k, self.v = (torch.randn(kv_rows, hkv, d, generator=gen).to(dtype).cuda() for _ in range(2))
         self.lse = torch.randn(rows, hq, generator=gen).cuda()
-        lens = [[n * ((i + 1) % 2) for i in range(batch)] for n in (rows, kv_rows)]
-        self.cu = [prefix_sums(n).cuda() for n in lens] + [falling(batch, n).cuda() for n in (rows, kv_rows)]
+        lens = [[n * ((i + 1) % 2) * (i < 2 * times) for i in range(batch)] for n in (rows, kv_rows)]
+        self.cu = [prefix_sums(n).cuda() for n in lens] + [falling(batch, n, times).cuda() for n in (rows, kv_rows)]
         self.sound = [prefix_sums(x).cuda() for x in ([rows] + [0] * (batch - 1), [kv_rows] + [0] * (batch - 1))] * 2
 
     def nans(self):
@@ -62,6 +89,29 @@ def test_tiles_of_overlapping_sequences_need_not():
     assert falling(5, 9).tolist() == [0, 9, 0, 9, 0, 9]
     batch, rows = 19, 1300
     assert 10 * ((rows + 127) // 128) > room_for_tiles(batch, rows, 260)
+
+
+def test_parts_of_sequences_side_by_side_fit():
+    rng, cut = np.random.default_rng(53), 0
+    for _ in range(400):
+        batch, window, sinks = int(rng.integers(1, 12)), int(2 ** rng.uniform(0, 10)), int(rng.choice([1, 100, 129, 300, 5000]))
+        lens = [int(x) for x in 2 ** rng.uniform(5, 15, batch)]
+        edge = [2049, 2048 + 128, 4097, 6145]  # just past one, two, three parts
+        lens = [edge[int(rng.integers(4))] if rng.random() < 0.5 else n for n in lens]
+        keys = [max(1, n + int(rng.integers(-400, 400))) for n in lens]
+        parts = sum(parts_of(n, m, window, sinks, low) for low in [bool(rng.integers(2))] for n, m in zip(lens, keys))
+        cut += parts > 0
+        assert parts <= room_for_parts(batch, sum(lens), sum(keys), window, sinks) or parts == 0
+    assert cut > 200
+
+
+FEW = dict(batch=60, rows=2200, kv_rows=128, times=4)  # whose tiles have room, and parts have not
+
+
+def test_parts_of_overlapping_sequences_need_not():
+    batch, rows, keys = FEW["batch"], FEW["rows"], FEW["kv_rows"]
+    assert FEW["times"] * ((rows + 127) // 128) <= room_for_tiles(batch, rows, keys)
+    assert FEW["times"] * parts_of(rows, keys, 64, 4, False) > room_for_parts(batch, rows, keys, 64, 4) > 0
 
 
 # ------------------------------------------------------------------ on the GPU
@@ -115,3 +165,18 @@ def test_windowed_calls(d, window, sinks):
         return ta.window_bwd(c.q, c.k, c.v, c.out, c.dout, c.lse, *c.cu, 0.1, window, sinks, dq=dq, dk=dk, dv=dv, workspace=ws)
     c.run(fwd, ta.fwd_workspace_size(*c.sizes))
     c.run(bwd, ta.window_bwd_workspace_size(*c.sizes, window, sinks))
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_parts_of_cut_sweeps(d):
+    """Offsets whose tiles have room, and whose parts of sweeps over sinks have not."""
+    c = Overlap(d=d, **FEW)
+
+    def bwd(ws):
+        dq, dk, dv = c.nans()
+        return ta.window_bwd(c.q, c.k, c.v, c.out, c.dout, c.lse, *c.cu, 0.1, 64, 4, dq=dq, dk=dk, dv=dv, workspace=ws)
+    need = ta.window_bwd_workspace_size(*c.sizes, 64, 4)
+    c.run(bwd, need)
+    with ta.debug_build():
+        c.run(bwd, need)
