@@ -459,11 +459,13 @@ __global__ void __launch_bounds__(256) zero_fill_kernel(P p, int mode) {
     for (long long r = static_cast<long long>(b) * wstep + w0; r < p.total_q; r += static_cast<long long>(gridDim.x) * wstep) clear_q(r, 0.0f);
     return;
   }
+  // packed rows of a span [a, c), inconsistent ones too, that lie in the tensor
+  auto rows_of = [](int a, int c, int total) { return max(0, min(max(c, 0), total) - min(max(a, 0), total)); };
   if (b < p.batch) {
     const SeqInfo s = load_seq(p, b);
     // rows of sequence b: base + i * stride for i in [0, n)
-    const long long qbase = p.sbhd ? b : p.cu_q_pad[b];
-    const int qn = min(max(p.sbhd ? p.total_q / p.batch : p.cu_q_pad[b + 1] - p.cu_q_pad[b], 0), p.total_q);
+    const long long qbase = p.sbhd ? b : max(p.cu_q_pad[b], 0);
+    const int qn = p.sbhd ? p.total_q / p.batch : rows_of(p.cu_q_pad[b], p.cu_q_pad[b + 1], p.total_q);
     const int stride = p.sbhd ? p.batch : 1;
     const int dead = s.len_k == 0 ? s.len_q : (causal ? min(s.len_q, max(0, -s.diag)) : 0);
     const int tail = max(dead, blind_tail(p, s));  // real queries from here on see no key either
@@ -473,8 +475,8 @@ __global__ void __launch_bounds__(256) zero_fill_kernel(P p, int mode) {
       clear_q(qbase + static_cast<long long>(i) * stride, i < s.len_q ? -INFINITY : 0.0f);
     }
     if (mode == 1) {
-      const long long kbase = p.sbhd ? b : p.cu_kv_pad[b];
-      const int kn = min(max(p.sbhd ? p.total_kv / p.batch : p.cu_kv_pad[b + 1] - p.cu_kv_pad[b], 0), p.total_kv);
+      const long long kbase = p.sbhd ? b : max(p.cu_kv_pad[b], 0);
+      const int kn = p.sbhd ? p.total_kv / p.batch : rows_of(p.cu_kv_pad[b], p.cu_kv_pad[b + 1], p.total_kv);
       const int seen = seen_keys(s, causal);
       for (int j = seen + w0; j < kn; j += wstep) clear_k(kbase + static_cast<long long>(j) * stride);
       if constexpr (is_window<P>) {

@@ -180,3 +180,48 @@ def test_parts_of_cut_sweeps(d):
     c.run(bwd, need)
     with ta.debug_build():
         c.run(bwd, need)
+
+
+LOW = -2 ** 31
+
+
+def _far_below(rows, kv_rows):
+    """Three sequences of 20, none and 30 tokens. The offset between the first and the third lies so far
+    below zero that the first one's span, as a 32-bit difference, looks long."""
+    sound = [prefix_sums([0, 0, 30])] * 2 + [torch.tensor([0, 30, 30, n], dtype=torch.int32) for n in (rows, kv_rows)]
+    bad = [prefix_sums([20, 0, 30])] * 2 + [torch.tensor([5, LOW, 30, n], dtype=torch.int32) for n in (rows, kv_rows)]
+    return [[x.cuda() for x in cu] for cu in (sound, bad)]
+
+
+def test_a_difference_that_wraps():
+    """What the third test below relies on: in 32 bits the span from 5 to -2^31 is long."""
+    assert np.subtract(np.int32(LOW), np.int32(5), dtype=np.int32) == 2 ** 31 - 5
+
+
+@gpu
+@pytest.mark.parametrize("window", [0, 12])
+@pytest.mark.parametrize("d", [64, 256])
+def test_offsets_far_below_zero(d, window):
+    """They leave the sequence beside them empty and the others as they are."""
+    c = Overlap(rows=70, kv_rows=66, d=d)
+    sound, bad = _far_below(70, 66)
+    head = (c.q, c.k, c.v)
+    size = (3, 70, 66, 4, 2, d)
+
+    def both(cu):
+        wf = torch.empty(ta.fwd_workspace_size(*size), dtype=torch.uint8, device="cuda")
+        out, lse = torch.full_like(c.q, float("nan")), torch.full_like(c.lse, float("nan"))
+        g = dict(zip(("dq", "dk", "dv"), c.nans()))
+        if window:
+            wb = torch.empty(ta.window_bwd_workspace_size(*size, window, 2), dtype=torch.uint8, device="cuda")
+            ta.window_fwd(*head, *cu, 0.1, window, 2, out=out, lse=lse, workspace=wf)
+            ta.window_bwd(*head, out, c.dout, lse, *cu, 0.1, window, 2, workspace=wb, **g)
+        else:
+            wb = torch.empty(ta.bwd_workspace_size(*size), dtype=torch.uint8, device="cuda")
+            ta.fwd(*head, *cu, 0.1, "padding_causal", out=out, lse=lse, workspace=wf)
+            ta.bwd(*head, out, c.dout, lse, *cu, 0.1, "padding_causal", workspace=wb, **g)
+        return (out, lse, *g.values()), ta.read_status(wf), ta.read_status(wb)
+    want, *clean = both(sound)
+    got, *status = both(bad)
+    assert clean == [0, 0] and status == [1, 1]
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
