@@ -124,9 +124,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   PagedSeq s{0, 0, 0, true};
   int b = -1, i0 = 0, i1 = 0, step = 1, hq0 = 0, hq1 = 0;  // queries i0, i0 + step, ... of sequence b; their heads
   auto sequence_of = [&](int tok) {  // by a whole warp
-    int before = 0;
-    for (int k = lane; k < p.batch; k += 32) before += p.cu_q_pad[k] <= tok ? 1 : 0;
-    b = __reduce_add_sync(0xffffffffu, before) - 1;
+    b = sequence_at(p.cu_q_pad, p.batch, tok);
     if (b >= 0) s = load_paged_seq(p, b);
     return b >= 0 && tok - s.off < s.n;
   };

@@ -30,6 +30,15 @@ __device__ __forceinline__ int page_of(const PagedCache& c, int b, int pos) {
   return page >= 0 && page < c.num_pages ? page : -1;
 }
 
+// Sequence whose rows [cu_pad[b], cu_pad[b + 1]) hold row r (the last one, should offsets that fall back
+// give it several); -1: none. A whole warp works on one row: one trip to memory for up to 32 sequences.
+__device__ __forceinline__ int sequence_at(const int* cu_pad, int batch, int r) {
+  int b = -1;
+  for (int k = threadIdx.x & 31; k < batch; k += 32)
+    if (cu_pad[k] <= r && r < cu_pad[k + 1]) b = k;
+  return __reduce_max_sync(0xffffffffu, b);
+}
+
 // Token row of (page, head, slot) within a page, in units of rows.
 __device__ __forceinline__ long long page_row(const PagedCache& c, int head, int slot) {
   return (static_cast<long long>(head) << c.shift) + slot;

@@ -60,9 +60,7 @@ struct Token {
 // status raised for lengths that are inconsistent. A whole warp works on one row.
 __device__ __forceinline__ int token_of(const int* cu, const int* cu_pad, const int* past, int batch, int total, int r,
                                         int* status, int* pos) {
-  int before = 0;
-  for (int k = threadIdx.x & 31; k < batch; k += 32) before += cu_pad[k] <= r ? 1 : 0;
-  const int b = __reduce_add_sync(0xffffffffu, before) - 1;
+  const int b = sequence_at(cu_pad, batch, r);
   if (b < 0) return -1;
   const int i = r - cu_pad[b], n = cu[b + 1] - cu[b], slot = cu_pad[b + 1] - cu_pad[b];
   const int first = past[b];
