@@ -194,7 +194,7 @@ def _far_below(rows, kv_rows):
 
 
 def test_a_difference_that_wraps():
-    """What the third test below relies on: in 32 bits the span from 5 to -2^31 is long."""
+    """What the tests of such offsets relies on: in 32 bits the span from 5 to -2^31 is long."""
     assert np.subtract(np.int32(LOW), np.int32(5), dtype=np.int32) == 2 ** 31 - 5
 
 

@@ -59,3 +59,19 @@ def test_append_and_gather(bits):
         rows, _, _ = places(d.table, 16, d.past, d.lengths, OFF)
         want[[r for r in range(TOTAL) if r not in rows.tolist()]] = 0
         assert torch.equal(x, want)
+
+
+@gpu
+@pytest.mark.parametrize("hq", [4, 160])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_an_offset_far_below_zero(bits, hq):
+    """The span from 5 to -2^31 is long as a 32-bit difference, and holds nothing."""
+    c = Attention(63, [20, 0, 30], [3, 0, 9], 16, hq, 2, 64, BF, bits, slot=1, tail=20).dev()
+    ws = c.workspace()
+    bad = torch.tensor([5, -2 ** 31, 20, 70], dtype=torch.int32, device="cuda")
+    kw = dict(out=torch.full_like(c.on[0], float("nan")), lse=torch.full((70, hq), float("nan"), device="cuda"), workspace=ws)
+    out, lse = ta.paged_fwd(*c.on[:6], bad, c.scale, **kw)
+    assert ta.read_status(ws) == 1
+    spans = [(0, 0), (0, 0), (20, 30)]
+    ref = window_plain(c.q, *c.kv, None, spans, list(zip(c.offk, c.keys)), c.scale, BR, 0, 0)
+    prefix_check({"out": out, "lse": lse}, ref, ("out", "lse"), BF)
