@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   auto sequence_of = [&](int tok) {  // by a whole warp
     b = sequence_at(p.cu_q_pad, p.batch, tok);
     if (b >= 0) s = load_paged_seq(p, b);
-    return b >= 0 && tok - s.off < s.n;
+    return b >= 0 && s.ok && tok - s.off < s.n;
   };
   auto no_token = [&](int tok, int h0, int h1, int at, int threads) {
     const long long row = static_cast<long long>(tok) * p.hq + h0;
