@@ -37,8 +37,8 @@ __device__ __forceinline__ PagedSeq load_paged_seq(const PagedParams& p, int b) 
   PagedSeq s{p.cu_q_pad[b], p.cu_q[b + 1] - p.cu_q[b], p.past[b], true};
   const int end = p.cu_q_pad[b + 1];
   const long long cap = static_cast<long long>(p.cache.max_pages) << p.cache.shift;
-  // (with no offset below zero the span does not wrap)
-  s.ok = s.n >= 0 && (s.off | end) >= 0 && s.n <= end - s.off && end <= p.total_q && s.past >= 0 &&
+  // (unsigned: with no offset below zero the span does not wrap)
+  s.ok = s.n >= 0 && s.off >= 0 && s.n <= end - s.off && static_cast<unsigned>(end) <= static_cast<unsigned>(p.total_q) && s.past >= 0 &&
          (s.n == 0 || s.past + static_cast<long long>(s.n) <= cap);
   if (!s.ok) s.n = 0;
   return s;

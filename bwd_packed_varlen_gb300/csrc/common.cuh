@@ -150,9 +150,10 @@ __device__ __forceinline__ SeqInfo load_seq(const AttnParams& p, int b) {
     s.off_q = pq0;
     s.off_k = pk0;
     s.tb = 0;
-    // (with no offset below zero the spans do not wrap)
-    s.ok = s.len_q >= 0 && s.len_k >= 0 && (pq0 | pq1 | pk0 | pk1) >= 0 && s.len_q <= pq1 - pq0 &&
-           s.len_k <= pk1 - pk0 && pq1 <= p.total_q && pk1 <= p.total_kv;
+    // (unsigned: with no offset below zero the spans do not wrap)
+    s.ok = s.len_q >= 0 && s.len_k >= 0 && pq0 >= 0 && pk0 >= 0 && s.len_q <= pq1 - pq0 &&
+           s.len_k <= pk1 - pk0 && static_cast<unsigned>(pq1) <= static_cast<unsigned>(p.total_q) &&
+           static_cast<unsigned>(pk1) <= static_cast<unsigned>(p.total_kv);
   }
   if (!s.ok) {
     s.len_q = 0;

@@ -30,10 +30,17 @@ __device__ __forceinline__ int page_of(const PagedCache& c, int b, int pos) {
   return page >= 0 && page < c.num_pages ? page : -1;
 }
 
-// Sequence whose rows [cu_pad[b], cu_pad[b + 1]) hold row r (the last one, should offsets that fall back
-// give it several); -1: none. A whole warp works on one row: one trip to memory for up to 32 sequences.
+// Sequence whose rows [cu_pad[b], cu_pad[b + 1]) hold row r; -1: none. A whole warp works on one row:
+// one trip to memory for up to 32 sequences, of which the last that begins at or before the row is
+// it. Only where that one does not hold the row are all spans looked at: none does, or offsets that fall
+// back have their own order (and may give the row several sequences: the last one then).
 __device__ __forceinline__ int sequence_at(const int* cu_pad, int batch, int r) {
-  int b = -1;
+  int before = 0;
+  for (int k = threadIdx.x & 31; k < batch; k += 32) before += cu_pad[k] <= r ? 1 : 0;
+  int b = __reduce_add_sync(0xffffffffu, before) - 1;
+  if (b >= 0 && cu_pad[b] <= r && r < cu_pad[b + 1]) return b;
+  b = -1;
+#pragma unroll 1
   for (int k = threadIdx.x & 31; k < batch; k += 32)
     if (cu_pad[k] <= r && r < cu_pad[k + 1]) b = k;
   return __reduce_max_sync(0xffffffffu, b);

@@ -455,14 +455,17 @@ __global__ void __launch_bounds__(256) zero_fill_kernel(P p, int mode) {
     zero_row(p.dk, r, kbytes);
     zero_row(p.dv, r, kbytes);
   };
-  if (mode == 0 && p.header[kHdrOver]) {
+  // (beside the loads of the lengths, so that it costs no trip to memory of its own)
+  const int over = mode == 0 ? p.header[kHdrOver] : 0;
+  SeqInfo s{};
+  if (b < p.batch) s = load_seq(p, b);
+  if (over) {
     for (long long r = static_cast<long long>(b) * wstep + w0; r < p.total_q; r += static_cast<long long>(gridDim.x) * wstep) clear_q(r, 0.0f);
     return;
   }
   // packed rows of a span [a, c), inconsistent ones too, that lie in the tensor
   auto rows_of = [](int a, int c, int total) { return max(0, min(max(c, 0), total) - min(max(a, 0), total)); };
   if (b < p.batch) {
-    const SeqInfo s = load_seq(p, b);
     // rows of sequence b: base + i * stride for i in [0, n)
     const long long qbase = p.sbhd ? b : max(p.cu_q_pad[b], 0);
     const int qn = p.sbhd ? p.total_q / p.batch : rows_of(p.cu_q_pad[b], p.cu_q_pad[b + 1], p.total_q);
@@ -555,11 +558,14 @@ __global__ void __launch_bounds__(256) delta_kernel(P p) {
   const int cpr = p.d / 8;  // 16-byte chunks per head
   const int chunks = p.hq * cpr;
   if (p.header[kHdrOver]) {
-    for (long long r = gw; r < p.total_q; r += warps) zero_row(p.dq, r, p.hq * p.d * 2);
-    for (long long r = gw; r < p.total_kv; r += warps) {
-      zero_row(p.dk, r, p.hkv * p.d * 2);
-      zero_row(p.dv, r, p.hkv * p.d * 2);
-    }
+    auto clear = [&](void* x, size_t rows, int heads) {
+      const size_t n = rows * heads * cpr, step = static_cast<size_t>(warps) * 32;
+#pragma unroll 1
+      for (size_t e = static_cast<size_t>(gw) * 32 + lane; e < n; e += step) static_cast<uint4*>(x)[e] = make_uint4(0, 0, 0, 0);
+    };
+    clear(p.dq, p.total_q, p.hq);
+    clear(p.dk, p.total_kv, p.hkv);
+    clear(p.dv, p.total_kv, p.hkv);
     return;
   }
   constexpr float kLog2e = 1.4426950408889634f;
