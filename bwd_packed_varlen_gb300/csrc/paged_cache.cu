@@ -56,19 +56,29 @@ struct Token {
   int page;  // -1: its place is outside the cache
 };
 
-// The sequence of packed row r and its token there; -1 for a row that holds no token, with the
-// status raised for lengths that are inconsistent. A whole warp works on one row.
-__device__ __forceinline__ int token_of(const int* cu, const int* cu_pad, const int* past, int batch, int total, int r,
-                                        int* status, int* pos) {
+// Tokens of sequence b; -1: its lengths, or its past, are inconsistent.
+__device__ __forceinline__ int tokens_of(const int* cu, const int* cu_pad, const int* past, int total, int b) {
+  const int n = cu[b + 1] - cu[b], off = cu_pad[b], end = cu_pad[b + 1];
+  // (with no offset below zero the span does not wrap)
+  return n < 0 || (off | end | past[b]) < 0 || n > end - off || end > total ? -1 : n;
+}
+
+// The status that a call begins with: whether some sequence is inconsistent. (The kernels go by rows,
+// and one without rows has none to be found by.)
+__global__ void __launch_bounds__(1024) paged_status_kernel(const int* cu, const int* cu_pad, const int* past, int batch, int total, int* status) {
+  int bad = 0;
+  for (int b = threadIdx.x; b < batch; b += blockDim.x) bad |= tokens_of(cu, cu_pad, past, total, b) < 0 ? 1 : 0;
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *status = bad ? kStatusBadSeqlens : 0;
+}
+
+// The sequence of packed row r and its token's position; -1 for a row that holds no token. A whole
+// warp works on one row.
+__device__ __forceinline__ int token_of(const int* cu, const int* cu_pad, const int* past, int batch, int total, int r, int* pos) {
   const int b = sequence_at(cu_pad, batch, r);
   if (b < 0) return -1;
-  const int i = r - cu_pad[b], n = cu[b + 1] - cu[b], slot = cu_pad[b + 1] - cu_pad[b];
-  const int first = past[b];
-  if (n < 0 || n > slot || cu_pad[b] < 0 || cu_pad[b + 1] > total || first < 0) {
-    if (status && (threadIdx.x & 31) == 0) atomicOr(status, kStatusBadSeqlens);
-    return -1;
-  }
-  if (i < 0 || i >= n) return -1;
+  const int n = tokens_of(cu, cu_pad, past, total, b), i = r - cu_pad[b], first = past[b];
+  if (n < 0 || i >= n) return -1;
   const long long at = static_cast<long long>(first) + i;
   *pos = at < INT_MAX ? static_cast<int>(at) : INT_MAX;
   return b;
@@ -166,7 +176,7 @@ __global__ void __launch_bounds__(kAppendThreads, 8) paged_append_kernel(const _
 
   if (warp < nt) {
     int pos = -1, page = -1;
-    const int b = token_of(p.cu, p.cu_pad, p.past, p.batch, p.total, r0 + warp, p.status, &pos);
+    const int b = token_of(p.cu, p.cu_pad, p.past, p.batch, p.total, r0 + warp, &pos);
     if (b >= 0) {
       page = page_of(p.cache, b, pos);
       if (page < 0 && p.status && (tid & 31) == 0) atomicOr(p.status, kStatusBadPages);
@@ -363,7 +373,7 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(const __gr
   const int r0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.total - r0);
   if (warp < nt) {
     int pos = -1, page = -1;
-    const int b = token_of(p.cu, p.cu_pad, p.start, p.batch, p.total, r0 + warp, p.status, &pos);
+    const int b = token_of(p.cu, p.cu_pad, p.start, p.batch, p.total, r0 + warp, &pos);
     if (b >= 0) {
       page = page_of(p.cache, b, pos);
       if (page < 0 && p.status && (tid & 31) == 0) atomicOr(p.status, kStatusBadPages);
@@ -444,7 +454,7 @@ int api_paged_cache(const te_attn_paged_cache* c, PagedCache* out) {
   return TE_OK;
 }
 
-// What append and gather check alike; sets *status to 0.
+// What append and gather check alike; sets *status to what the lengths say.
 static int begin(const int32_t* cu, const int32_t* cu_pad, const int32_t* past, int batch, int total, int32_t* status,
                  cudaStream_t st) {
   if (!cu || !cu_pad || !past) return api_fail(TE_ERR_INVALID_ARG, "cu_seqlens and positions must not be NULL");
@@ -454,7 +464,8 @@ static int begin(const int32_t* cu, const int32_t* cu_pad, const int32_t* past, 
                         static_cast<const void*>(status)})
     if (!aligned(x, 4)) return api_fail(TE_ERR_INVALID_ARG, "int32 arrays need their natural alignment");
   if (status) {
-    const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int32_t), st);
+    paged_status_kernel<<<1, batch < 1024 ? (batch + 31) / 32 * 32 : 1024, 0, st>>>(cu, cu_pad, past, batch, total, status);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return api_cuda_fail(e, "status");
   }
   return TE_OK;

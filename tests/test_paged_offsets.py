@@ -75,3 +75,22 @@ def test_an_offset_far_below_zero(bits, hq):
     spans = [(0, 0), (0, 0), (20, 30)]
     ref = window_plain(c.q, *c.kv, None, spans, list(zip(c.offk, c.keys)), c.scale, BR, 0, 0)
     prefix_check({"out": out, "lse": lse}, ref, ("out", "lse"), BF)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [16, 4])
+def test_sequences_without_rows_are_reported(bits):
+    """Inconsistent lengths, or a past below zero, of a sequence that has no row to be found by."""
+    c = Cache(64, [5, 0, 4], [20, 7, 40], 16, 3, 2, 64, FP, bits, 64, slot=1, tail=0).dev()
+    sound, status = c.fresh(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = c.append(sound, status=status)
+    kv = c.gather(sound, status=status)
+    assert status.item() == 0
+    flat = lambda cs: [t for x in cs for t in (x if bits == 4 else (x,))]  # noqa: E731
+    cu, past = c.cu_on[0], c.past_on
+    for bad in ((torch.tensor([0, 5, 8, 12], dtype=torch.int32).cuda(), past), (cu, torch.tensor([20, -1, 40], dtype=torch.int32).cuda())):
+        c.cu_on[0], c.past_on = bad
+        caches = c.fresh()
+        assert torch.equal(q, c.append(caches, status=status)) and status.item() == 1
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(flat(sound), flat(caches)))
+        assert all(torch.equal(a, b) for a, b in zip(kv, c.gather(caches, status=status))) and status.item() == 1
