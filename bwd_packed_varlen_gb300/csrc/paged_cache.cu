@@ -13,8 +13,8 @@
 // four lanes take a group, eight elements each, find its least and greatest by two exchanges
 // and write 16 bytes of codes and 4 of step and least value. The step is rounded towards zero,
 // so that no code stands for more than the greatest element, which may be the type's last.
-// Both quotients are true divisions: a product with a reciprocal would put elements on a border
-// between two codes, which 16-bit numbers often are, on either side. 12 prompts of 30-900 tokens,
+// Both quotients are true divisions: elements often lie on a border between two codes, and close
+// to one a product with a reciprocal could come out on the other side. 12 prompts of 30-900 tokens,
 // 16 + 2 * 8 heads of 64, into 4 bits and gathered again: 29 us for 8.1 us of bytes; bounded
 // by instructions, some 45 an element of keys and values, in two issue slots of three.
 #include <cuda_runtime.h>
@@ -86,8 +86,16 @@ __device__ __forceinline__ int token_of(const int* cu, const int* cu_pad, const 
 
 // Codes of one group's eight elements in this lane (the group's others in the lanes beside it:
 // four neighbouring lanes hold 32 elements); every lane of the warp takes part.
+//
+// Steps and codes are those of exact arithmetic, though 32 bits do not hold every difference of
+// 16-bit numbers (15 - 1e-7). The step's rounding is towards zero all along: 15 steps of 16 bits are
+// an fp32 number, so a difference cut off to fp32 has as many of them as the exact one. Borders
+// (c + 1/2) s between codes are fp32 numbers too, with zeros in the fraction's last bits: a difference
+// that is not exact takes its odd neighbour, which is no border and lies on the same side of each.
+// Dividing keeps that: a difference below a border b is at most b (1 - 2^-24), and its quotient is then
+// below c + 1/2 by more than half of the distance to the number before that; likewise above.
 template <bool kBF16>
-__device__ __forceinline__ uint32_t quantize8(const float (&f)[8], uint32_t* meta) {
+__device__ __forceinline__ uint32_t quantize8(float (&f)[8], uint32_t* meta) {
   float lo = f[0], hi = f[0];
   float sum = 0.f;  // NaN if any element is not finite
 #pragma unroll
@@ -102,21 +110,28 @@ __device__ __forceinline__ uint32_t quantize8(const float (&f)[8], uint32_t* met
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
-  const float range = hi - lo;
-  const float fifteenth = isinf(range) ? hi / 15.f - lo / 15.f : range / 15.f;
-  *meta = pack_meta<kBF16>(fifteenth, lo);
+  const float least = lo;
+  const bool far = isinf(hi - lo);
+  if (far) {  // past fp32's last number: everything halved, which is exact
+    lo *= 0.5f;
+    hi *= 0.5f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= 0.5f;
+  }
+  const float fifteenth = __fdiv_rz(__fsub_rz(hi, lo), 15.f);
+  *meta = pack_meta<kBF16>(far ? 2.f * fifteenth : fifteenth, least);
   if (sum != 0.f) {
     *meta = 0x7fff7fffu;  // NaN in either type
     return 0;
   }
-  const float step = unpack2<kBF16>(*meta).x;
+  const float step = unpack2<kBF16>(*meta).x * (far ? 0.5f : 1.f);
   uint32_t w = 0;
   if (step > 0.f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // (a difference past fp32's last number is of a group whose range is)
-      const float q = isinf(range) ? f[i] / step - lo / step : (f[i] - lo) / step;
-      w |= static_cast<uint32_t>(min(15, __float2int_rn(q))) << (4 * i);
+      const uint32_t down = __float_as_uint(__fsub_rz(f[i], lo)), up = __float_as_uint(__fsub_ru(f[i], lo));
+      const float d = __uint_as_float(down | ((down ^ up) & 1u));  // (neighbours differ in the last bit)
+      w |= static_cast<uint32_t>(min(15, __float2int_rn(d / step))) << (4 * i);
     }
   }
   return w;
