@@ -79,7 +79,9 @@ struct PagedCut {
     return static_cast<int>((static_cast<long long>(s.n) * p.group + rows - 1) / rows);
   }
   // Run of a row tile. Tiles of few rows take that of the whole sequence, so that a place on the
-  // line is found by division; their kernel passes over what the tile does not see.
+  // line is found by division; their kernel copies all of it and computes what the tile sees. That is next
+  // to nothing for the few tiles of a step or a draft; with many tiles, at d above 128, it is most of the time
+  // behind a window (rates beside paged_wide_rows).
   __device__ __forceinline__ PagedRun run(const PagedParams& p, const PagedSeq& s, int tile) const {
     if (!wide) return paged_run(p, s, 0, s.n - 1, unit);
     const int r0 = tile * rows;  // (a call's rows are below 2^31 - 256)

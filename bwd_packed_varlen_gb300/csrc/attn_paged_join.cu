@@ -1,7 +1,9 @@
 // Attention over a paged cache: joins what the slices left of segments that several of them
 // share, writes zeros to rows that hold no token, and collects the call's status.
 //
-// A block of four warps per row of out. Of a row's pieces O = sum 2^(m_k - M) O_k / L with
+// A block of four warps per row of out, per token or, beside long pieces, per head of a sequence (JoinGrid);
+// blocks ahead of them look for rows that are no token, or join the other kernel's segments. Of a row's
+// pieces O = sum 2^(m_k - M) O_k / L with
 // M = max m_k and L = sum 2^(m_k - M) l_k, in fp32, every fourth piece in order by a warp and the
 // four warps' sums in order, rounded once. Latency-bound: a decoding step's rows have a few pieces
 // (3-5 us of the call). Rows of the other kernel are joined by a thread each, column by column.

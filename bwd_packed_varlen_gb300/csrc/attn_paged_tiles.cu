@@ -19,8 +19,8 @@
 // both at d 128: the tensor cores are 50 % busy, the exponentials' pipe 26 %.
 //
 // Measured, bf16, hq 32, hkv 8, d 128: four pieces of 100-512 queries behind 2000-12000 keys 208
-// us a call (0.93 PFLOP/s); 16384 queries 2380 us, with a window of 1024 635 us. A segment costs 6
-// to 8 us beside its key tiles (first scores, their maximum, the rows' end).
+// us a call (0.93 PFLOP/s), in 4 bits 288; 16384 queries 2380 us, with a window of 1024 601 us. A segment
+// costs 6 to 8 us beside its key tiles (first scores, their maximum, the rows' end).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -579,7 +579,9 @@ cudaError_t launch_paged_tiles(const PagedParams& p, const PagedParts& parts, in
 }
 
 int paged_wide_rows(int batch, int total_q, int hq, int hkv, int d, bool four) {
-  // Above head_dim 128 the kernel of few rows takes all.
+  // Above head_dim 128 the kernel of few rows takes all, 8 rows a pass: four pieces of 100-512 queries behind
+  // 2000-12000 keys 4524 us (4 bits 4090), through a window of 1024 798 (844); 8192 queries from the first on
+  // 24283, through that window 15623. At d 128 these take 214 (288), 106 (109), 828 and 356 us here.
   if (d > 128) return 0;
   // Rows a kv head from which a sequence is faster here. With a segment for every SM, at d 128, 64
   // sequences of 2000 keys: 20 rows 160 us here, 202 there, which reads keys once for every 16 rows; in 4

@@ -62,8 +62,8 @@ __device__ __forceinline__ uint32_t pack_meta(float step, float least) {
            static_cast<uint32_t>(__half_as_ushort(__float2half_rn(least))) << 16;
 }
 
-// Codes become numbers by a magic one: put into the fraction of 128 (bf16) or 1024 (fp16), which
-// is then taken off; both steps are exact.
+// Codes become numbers by a magic one, the usual way for small integers: put into the fraction of 128
+// (bf16) or 1024 (fp16), which is then taken off; both steps are exact.
 template <bool kBF16>
 constexpr uint32_t kCodeMagic = kBF16 ? 0x43004300u : 0x64006400u;
 

@@ -4,12 +4,16 @@
 // p - j < window or j < sinks. So a query tile's key tiles are the sinks' and then those from
 // its first row's window on, and a key tile's queries end a window behind its last key unless
 // it holds a sink: tiles between are not visited, and the work is that of the window, not of
-// the sequence.
+// the sequence (but for the sweeps of sinks behind the 256th, see kSplitSinkTiles).
 //
 // Measured, bf16, hq 32, hkv 8, d 128, four sequences of 1500-6000 tokens, window 1024, 4 sinks:
-// forward 465 us, delta 59, dQ 319, dK/dV 458, lists 29, zero fill 13 (events around each); forward and backward
-// in a call 1288 us, 5 products for each visible pair in 429 us at the measured bf16 rate. Bounded as
-// the kernels without a window are, and by an item's begin and end, 6 to 8 us beside ten tiles of 2.
+// forward 465 us, delta 60, dQ 317, dK/dV 455, lists 29, zero fill 13 (events around each); forward and backward
+// in a call 1300 us, 5 products for each visible pair in 429 us at the measured bf16 rate. d 256: 658, 106,
+// 1098, 2310, 31, 17. Bounded as the kernels without a window are, by an item's begin and end, and in the
+// forward by second readings of scores: a row's offset starts as the maximum over the keys that it sees
+// of its first tile, and where those are few (a few sinks, a window's far edge) it lies so low that the
+// later tiles' P sum past 2^8, which has their maximum looked for. 1 sink 592 us, 4 465, 16 315, 64 to 128
+// 286-289 (instructions 150 million with 4, 110 with 64); none, windows of 1000 and 1024: 501 and 450.
 #pragma once
 
 #include <type_traits>
@@ -35,6 +39,8 @@ struct WindowParams : AttnParams {
   int cap_slots;
 };
 
+// Sweeps of sinks behind the 256th are not cut: one block takes all queries behind them. dK/dV of the four
+// sequences above with 256 sinks 483 us, 300 727, 1024 807; of one of 16384 tokens 533, 1291, 1809.
 constexpr int kSplitSinkTiles = 2;
 // As long as an ordinary sweep, but so long that few sequences have more than one part. (dK/dV of the
 // four sequences above: 694 us with whole sweeps, 452 with cut ones; of 8 tiles

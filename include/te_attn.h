@@ -281,7 +281,9 @@ int te_attn_fwd_thd_e4m3(const void* q, const void* k, const void* v, void* out,
  * or p = i + Lk - Lq (lower-right), sees key j <= p iff p - j < window or j < sinks.
  * window >= 1, sinks >= 0 (TE_ERR_INVALID_ARG otherwise); mask_type one of the causal ones and
  * fewer than 2^30 rows (TE_ERR_UNSUPPORTED otherwise). Key tiles that no query of a tile sees
- * are not visited, so the time is that of the window, not of the sequence.
+ * are not visited, so the time is that of the window, not of the sequence; dk and dv of sinks
+ * behind the 256th are gathered by one block a head and key tile over all queries behind them.
+ * (A NaN or an infinity in a token may reach queries of its sequence that do not see it.)
  * Everything else is as for those entry points; the forward's workspace is theirs too, the
  * backward's holds partial sums for sinks besides (te_attn_window_bwd_workspace_size(); rows of
  * the sequence-major forms as there). A real query
