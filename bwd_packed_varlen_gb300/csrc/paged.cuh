@@ -33,7 +33,7 @@ __device__ __forceinline__ int page_of(const PagedCache& c, int b, int pos) {
 // Sequence whose rows [cu_pad[b], cu_pad[b + 1]) hold row r; -1: none. A whole warp works on one row:
 // one trip to memory for up to 32 sequences, of which the last that begins at or before the row is
 // it. Only where that one does not hold the row are all spans looked at: none does, or offsets that fall
-// back have their own order (and may give the row several sequences: the last one then).
+// back have their own order (and may give the row several sequences: one of them then).
 __device__ __forceinline__ int sequence_at(const int* cu_pad, int batch, int r) {
   int before = 0;
   for (int k = threadIdx.x & 31; k < batch; k += 32) before += cu_pad[k] <= r ? 1 : 0;

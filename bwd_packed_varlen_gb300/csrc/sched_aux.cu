@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kSchedThreads) schedule_kernel(P p, int* pref_
   }
   // (the scans' barriers order the sum before this)
   bool over = tiles > static_cast<unsigned long long>(INT_MAX) || carry_q > p.pair_cap_q || carry_k > p.pair_cap_k ||
-                    carry_f > p.pair_cap_f;
+              carry_f > p.pair_cap_f;
   if constexpr (is_window<P>) {
     if (p.sweep_tiles > 0 && !over) {
       int carry = 0;

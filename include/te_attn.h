@@ -112,7 +112,9 @@ extern "C" {
  *                           where those have more 128-row tiles, or parts of
  *                           sweeps over sinks, than the workspace has room for,
  *                           nothing is computed and every row of the outputs (lse
- *                           too) becomes zero.
+ *                           too) becomes zero. With fewer, only that such a call
+ *                           stays inside its buffers is promised; the paged calls
+ *                           keep the consistent sequences' results.
  *   TE_STATUS_TIMEOUT       a pipeline wait inside a kernel ran past its limit (4 s);
  *                           every other wait of that kernel then gave up too, the
  *                           kernel freed its tensor memory and returned, and the
